@@ -1,0 +1,219 @@
+// C ABI of the cache calls (declared in include/gbattn.h): tree attention
+// over a cache, appending, accumulated key weights, eviction.  Validation is
+// on the host and touches no device memory; lengths, limits and indices that
+// live on the device are brought into range by the kernels.
+#include <cmath>
+
+#include "../../include/gbattn.h"
+#include "cache.h"
+#include "cache_kernel.cuh"
+#include "key_weight_kernel.cuh"
+#include "tree_kernel.cuh"
+
+namespace gbattn {
+namespace {
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+bool supported_d(int D) { return D == 64 || D == 96 || D == 128 || D == 256; }
+
+size_t round16(size_t x) { return (x + 15) & ~static_cast<size_t>(15); }
+
+// Sizes and type of a cache [B, Hkv, Lk (kv_pitch), D].
+attn_status_t check_cache(int B, int Hkv, int Lk, int D, int64_t kv_pitch, attn_dtype_t dtype) {
+  if (B < 1 || Hkv < 1 || Lk < 1) return ATTN_ERR_INVALID_ARG;
+  if (dtype != ATTN_DTYPE_FP16 && dtype != ATTN_DTYPE_BF16) return ATTN_ERR_INVALID_ARG;
+  if (kv_pitch < 0 || (kv_pitch != 0 && kv_pitch < Lk)) return ATTN_ERR_INVALID_ARG;
+  if (!supported_d(D)) return ATTN_ERR_UNSUPPORTED;
+  // the TMA stride limit between heads (2^40 bytes), head counts that a grid takes
+  if (kv_pitch > (int64_t{1} << 40) / (2 * D)) return ATTN_ERR_UNSUPPORTED;
+  if (static_cast<long long>(B) * Hkv > 65535) return ATTN_ERR_UNSUPPORTED;
+  return ATTN_OK;
+}
+
+attn_status_t check_scale(float scale) {
+  return std::isfinite(scale) && scale > 0.f ? ATTN_OK : ATTN_ERR_INVALID_ARG;
+}
+
+float scale_log2_of(float scale) { return static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074); }
+
+attn_status_t check_tree(int B, int Hq, int Hkv, int T, int Lk, int D) {
+  if (Hq < 1 || T < 1) return ATTN_ERR_INVALID_ARG;
+  const attn_status_t s = check_cache(B, Hkv, Lk, D, 0, ATTN_DTYPE_BF16);
+  if (s == ATTN_ERR_INVALID_ARG) return s;
+  if (Hq % Hkv != 0) return ATTN_ERR_INVALID_ARG;
+  if (s != ATTN_OK) return s;
+  if (T > kTreeMaxT || B > kTreeMaxB) return ATTN_ERR_UNSUPPORTED;
+  if (static_cast<long long>(B) * Hq * T > 0x7fffffffLL) return ATTN_ERR_UNSUPPORTED;
+  return ATTN_OK;
+}
+
+attn_status_t check_key_weight(int B, int Hq, int Hkv, int Lq, int Lk, int D) {
+  if (Hq < 1 || Lq < 1) return ATTN_ERR_INVALID_ARG;
+  const attn_status_t s = check_cache(B, Hkv, Lk, D, 0, ATTN_DTYPE_BF16);
+  if (s == ATTN_ERR_INVALID_ARG) return s;
+  if (Hq % Hkv != 0) return ATTN_ERR_INVALID_ARG;
+  if (s != ATTN_OK) return s;
+  if (static_cast<long long>(Hq / Hkv) * Lq > (1 << 30)) return ATTN_ERR_UNSUPPORTED;
+  return ATTN_OK;
+}
+
+attn_status_t launched() { return cudaPeekAtLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA; }
+
+template <int D, bool BF16>
+attn_status_t launch_tree(const TreeParams& p, cudaStream_t stream) {
+  attn_tree_kernel<D, BF16><<<p.B * p.Hq * p.T, kTreeThreads, 0, stream>>>(p);
+  return launched();
+}
+
+template <int D, bool BF16>
+attn_status_t launch_key_weight(const KeyWeightParams& p, cudaStream_t stream) {
+  constexpr int smem = D * kKeyWeightKeys * 4;
+  auto kern = attn_key_weight_kernel<D, BF16>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return ATTN_ERR_CUDA;
+  kern<<<dim3((p.Lk + kKeyWeightKeys - 1) / kKeyWeightKeys, p.B * p.Hkv), kKeyWeightKeys, smem, stream>>>(p);
+  return launched();
+}
+
+}  // namespace
+}  // namespace gbattn
+
+using namespace gbattn;
+
+extern "C" size_t attn_tree_workspace_bytes(int B, int Hq, int Hkv, int T, int Lk, int D) {
+  return check_tree(B, Hq, Hkv, T, Lk, D) == ATTN_OK ? 16 : 0;
+}
+
+extern "C" attn_status_t attn_fwd_tree(const void* q, const void* k, const void* v, const void* k_new,
+                                       const void* v_new, const uint8_t* tree_mask, const int32_t* cache_len,
+                                       const int32_t* tree_len, void* o, float* lse, void* workspace,
+                                       size_t workspace_bytes, int64_t kv_pitch, int B, int Hq, int Hkv, int T,
+                                       int Lk, int D, float scale, attn_dtype_t dtype, cudaStream_t stream) {
+  if (!q || !k || !v || !k_new || !v_new || !cache_len || !o || !lse || !workspace) return ATTN_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(k_new) || !aligned16(v_new) || !aligned16(o) ||
+      !aligned16(lse) || !aligned16(workspace) || !aligned4(cache_len) || !aligned4(tree_len))
+    return ATTN_ERR_INVALID_ARG;
+  attn_status_t s = check_scale(scale);
+  if (s != ATTN_OK) return s;
+  s = check_tree(B, Hq, Hkv, T, Lk, D);
+  if (s == ATTN_ERR_INVALID_ARG) return s;
+  const attn_status_t c = check_cache(B, Hkv, Lk, D, kv_pitch, dtype);
+  if (c != ATTN_OK) return c;
+  if (s != ATTN_OK) return s;
+  if (workspace_bytes < attn_tree_workspace_bytes(B, Hq, Hkv, T, Lk, D)) return ATTN_ERR_INVALID_ARG;
+  int dev, num_sms, *status;
+  EncodeTiledFn enc;
+  const attn_status_t ds = shared_device_state(&dev, &enc, &status, &num_sms);
+  if (ds != ATTN_OK) return ds;
+  TreeParams p{q, k, v, k_new, v_new, tree_mask, cache_len, tree_len, o, lse, kv_pitch ? kv_pitch : Lk,
+               B, Hq, Hkv, Hq / Hkv, T, Lk, scale_log2_of(scale), status, shared_wait_limit_ns()};
+  const bool bf = dtype == ATTN_DTYPE_BF16;
+  switch (D) {
+    case 64: return bf ? launch_tree<64, true>(p, stream) : launch_tree<64, false>(p, stream);
+    case 96: return bf ? launch_tree<96, true>(p, stream) : launch_tree<96, false>(p, stream);
+    case 128: return bf ? launch_tree<128, true>(p, stream) : launch_tree<128, false>(p, stream);
+    default: return bf ? launch_tree<256, true>(p, stream) : launch_tree<256, false>(p, stream);
+  }
+}
+
+extern "C" size_t attn_key_weight_workspace_bytes(int B, int Hq, int Hkv, int Lq, int Lk, int D) {
+  return check_key_weight(B, Hq, Hkv, Lq, Lk, D) == ATTN_OK ? 16 : 0;
+}
+
+extern "C" attn_status_t attn_key_weight(const void* q, const void* k, const float* lse, const int32_t* limit,
+                                         const float* weight, float* weight_out, void* workspace,
+                                         size_t workspace_bytes, int64_t kv_pitch, int B, int Hq, int Hkv, int Lq,
+                                         int Lk, int D, float scale, int causal, attn_dtype_t dtype,
+                                         cudaStream_t stream) {
+  if (!q || !k || !lse || !weight_out || !workspace) return ATTN_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(lse) || !aligned16(weight) || !aligned16(weight_out) ||
+      !aligned16(workspace) || !aligned4(limit))
+    return ATTN_ERR_INVALID_ARG;
+  attn_status_t s = check_scale(scale);
+  if (s != ATTN_OK) return s;
+  s = check_key_weight(B, Hq, Hkv, Lq, Lk, D);
+  if (s == ATTN_ERR_INVALID_ARG) return s;
+  const attn_status_t c = check_cache(B, Hkv, Lk, D, kv_pitch, dtype);
+  if (c == ATTN_ERR_INVALID_ARG) return c;
+  if (causal != 0 && causal != 1) return ATTN_ERR_INVALID_ARG;
+  if (causal && (limit || Lq > Lk)) return ATTN_ERR_INVALID_ARG;
+  if (c != ATTN_OK) return c;
+  if (s != ATTN_OK) return s;
+  if (limit && Lq > kTreeMaxT) return ATTN_ERR_UNSUPPORTED;
+  if (workspace_bytes < attn_key_weight_workspace_bytes(B, Hq, Hkv, Lq, Lk, D)) return ATTN_ERR_INVALID_ARG;
+  int dev, num_sms, *status;
+  EncodeTiledFn enc;
+  const attn_status_t ds = shared_device_state(&dev, &enc, &status, &num_sms);
+  if (ds != ATTN_OK) return ds;
+  KeyWeightParams p{q, k, lse, limit, weight, weight_out, kv_pitch ? kv_pitch : Lk, B, Hq, Hkv, Hq / Hkv, Lq, Lk,
+                    causal, scale_log2_of(scale), status, shared_wait_limit_ns()};
+  const bool bf = dtype == ATTN_DTYPE_BF16;
+  switch (D) {
+    case 64: return bf ? launch_key_weight<64, true>(p, stream) : launch_key_weight<64, false>(p, stream);
+    case 96: return bf ? launch_key_weight<96, true>(p, stream) : launch_key_weight<96, false>(p, stream);
+    case 128: return bf ? launch_key_weight<128, true>(p, stream) : launch_key_weight<128, false>(p, stream);
+    default: return bf ? launch_key_weight<256, true>(p, stream) : launch_key_weight<256, false>(p, stream);
+  }
+}
+
+extern "C" attn_status_t attn_cache_append(const void* k_new, const void* v_new, const int32_t* path,
+                                           const int32_t* accept_len, const int32_t* cache_len, const int32_t* seen,
+                                           void* k, void* v, int32_t* pos, int32_t* cache_len_out, int32_t* seen_out,
+                                           int32_t* limit, int64_t kv_pitch, int B, int Hkv, int T, int Lk, int D,
+                                           attn_dtype_t dtype, cudaStream_t stream) {
+  if (!k_new || !v_new || !cache_len || !k || !v || !cache_len_out) return ATTN_ERR_INVALID_ARG;
+  if (!aligned16(k_new) || !aligned16(v_new) || !aligned16(k) || !aligned16(v) || !aligned4(path) ||
+      !aligned4(accept_len) || !aligned4(cache_len) || !aligned4(seen) || !aligned4(pos) || !aligned4(cache_len_out) ||
+      !aligned4(seen_out) || !aligned4(limit))
+    return ATTN_ERR_INVALID_ARG;
+  if ((pos || seen_out) && !seen) return ATTN_ERR_INVALID_ARG;
+  // other blocks read the lengths while one writes the new ones
+  if (cache_len_out == cache_len || (seen_out && seen_out == seen)) return ATTN_ERR_INVALID_ARG;
+  if (T < 1) return ATTN_ERR_INVALID_ARG;
+  const attn_status_t s = check_cache(B, Hkv, Lk, D, kv_pitch, dtype);
+  if (s != ATTN_OK) return s;
+  int dev, num_sms, *status;
+  EncodeTiledFn enc;
+  const attn_status_t ds = shared_device_state(&dev, &enc, &status, &num_sms);
+  if (ds != ATTN_OK) return ds;
+  AppendParams p{k_new, v_new, path, accept_len, cache_len, seen, k, v, pos, cache_len_out, seen_out, limit,
+                 kv_pitch ? kv_pitch : Lk, B, Hkv, T, Lk, D / 8, status};
+  const long long pieces = (static_cast<long long>(T) * p.row16 + kAppendThreads - 1) / kAppendThreads;
+  const int gx = static_cast<int>(pieces < 64 ? pieces : 64);
+  attn_cache_append_kernel<<<dim3(gx, B * Hkv), kAppendThreads, 0, stream>>>(p);
+  return launched();
+}
+
+extern "C" size_t attn_cache_evict_workspace_bytes(int B, int Hkv, int Lk) {
+  if (B < 1 || Hkv < 1 || Lk < 1 || static_cast<long long>(B) * Hkv > 65535 || Lk > kEvictMaxLk) return 0;
+  return round16(static_cast<size_t>(B) * Hkv * (Lk / 2) * 2 * sizeof(int32_t) + 16);
+}
+
+extern "C" attn_status_t attn_cache_evict(void* k, void* v, const float* weight, const int32_t* pos,
+                                          const int32_t* cache_len, const int32_t* seen, float* weight_out,
+                                          int32_t* pos_out, int32_t* cache_len_out, void* workspace,
+                                          size_t workspace_bytes, int64_t kv_pitch, int B, int Hkv, int Lk, int D,
+                                          int keep, int recent, attn_dtype_t dtype, cudaStream_t stream) {
+  if (!k || !v || !weight || !pos || !cache_len || !seen || !weight_out || !pos_out || !cache_len_out || !workspace)
+    return ATTN_ERR_INVALID_ARG;
+  if (!aligned16(k) || !aligned16(v) || !aligned16(weight) || !aligned16(pos) || !aligned16(weight_out) ||
+      !aligned16(pos_out) || !aligned16(workspace) || !aligned4(cache_len) || !aligned4(seen) ||
+      !aligned4(cache_len_out))
+    return ATTN_ERR_INVALID_ARG;
+  if (weight_out == weight || pos_out == pos || cache_len_out == cache_len) return ATTN_ERR_INVALID_ARG;
+  const attn_status_t s = check_cache(B, Hkv, Lk, D, kv_pitch, dtype);
+  if (s == ATTN_ERR_INVALID_ARG) return s;
+  if (keep < 1 || keep > Lk || recent < 0 || recent > keep) return ATTN_ERR_INVALID_ARG;
+  if (s != ATTN_OK) return s;
+  if (Lk > kEvictMaxLk) return ATTN_ERR_UNSUPPORTED;
+  if (workspace_bytes < attn_cache_evict_workspace_bytes(B, Hkv, Lk)) return ATTN_ERR_INVALID_ARG;
+  int dev, num_sms, *status;
+  EncodeTiledFn enc;
+  const attn_status_t ds = shared_device_state(&dev, &enc, &status, &num_sms);
+  if (ds != ATTN_OK) return ds;
+  EvictParams p{k, v, weight, pos, cache_len, seen, weight_out, pos_out, cache_len_out,
+                static_cast<int32_t*>(workspace), kv_pitch ? kv_pitch : Lk, B, Hkv, Lk, D / 8, keep, recent, status};
+  attn_cache_evict_kernel<<<B * Hkv, kEvictThreads, 0, stream>>>(p);
+  return launched();
+}

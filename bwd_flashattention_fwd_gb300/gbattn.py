@@ -30,7 +30,9 @@ ATTN_DTYPE_BF16 = 1
 EXPORTED = ("attn_fwd", "attn_bwd_delta", "attn_bwd", "attn_bwd_dq", "attn_bwd_dkv", "attn_bwd_noalloc",
             "attn_fwd_masked", "attn_bwd_masked", "attn_fwd_ex", "attn_bwd_ex", "attn_decode_workspace_bytes",
             "attn_fwd_decode", "attn_bwd_decode", "attn_last_device_status", "attn_wait_probe", "attn_status_string",
-            "lce_workspace_bytes", "lce_fwd", "lce_bwd")
+            "lce_workspace_bytes", "lce_fwd", "lce_bwd", "attn_tree_workspace_bytes", "attn_fwd_tree",
+            "attn_cache_append", "attn_key_weight_workspace_bytes", "attn_key_weight",
+            "attn_cache_evict_workspace_bytes", "attn_cache_evict")
 
 _lib = None
 
@@ -90,6 +92,20 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
     lib.lce_fwd.restype = ci
     lib.lce_bwd.argtypes = [vp] * 8 + [sz, ci, ci, ci, ci, vp]
     lib.lce_bwd.restype = ci
+    lib.attn_tree_workspace_bytes.argtypes = [ci] * 6
+    lib.attn_tree_workspace_bytes.restype = sz
+    lib.attn_fwd_tree.argtypes = [vp] * 11 + [sz, i64] + [ci] * 6 + [cf, ci, vp]
+    lib.attn_fwd_tree.restype = ci
+    lib.attn_cache_append.argtypes = [vp] * 12 + [i64] + [ci] * 6 + [vp]
+    lib.attn_cache_append.restype = ci
+    lib.attn_key_weight_workspace_bytes.argtypes = [ci] * 6
+    lib.attn_key_weight_workspace_bytes.restype = sz
+    lib.attn_key_weight.argtypes = [vp] * 7 + [sz, i64] + [ci] * 6 + [cf, ci, ci, vp]
+    lib.attn_key_weight.restype = ci
+    lib.attn_cache_evict_workspace_bytes.argtypes = [ci] * 3
+    lib.attn_cache_evict_workspace_bytes.restype = sz
+    lib.attn_cache_evict.argtypes = [vp] * 10 + [sz, i64] + [ci] * 7 + [vp]
+    lib.attn_cache_evict.restype = ci
     lib.attn_last_device_status.argtypes = [vp]
     lib.attn_last_device_status.restype = ci
     lib.attn_wait_probe.argtypes = [vp]
@@ -360,6 +376,136 @@ def lce_bwd(hidden, weight, targets, lse, dloss, dhidden, dweight, workspace, st
                                 _ptr(dweight), _ptr(workspace), workspace.numel() * workspace.element_size(), N, Dm,
                                 weight.shape[0], _dtype_code(hidden), _stream_handle(stream))
     return _check(st, "lce_bwd", check)
+
+
+def _shape(call: str, t, want, name: str):
+    """Reject a tensor (or None) whose shape is not the one the call reads."""
+    if t is not None and tuple(t.shape) != tuple(want):
+        raise ValueError(f"{call}: {name} has shape {tuple(t.shape)}; expected {tuple(want)}")
+
+
+def attn_tree_workspace_bytes(B: int, Hq: int, Hkv: int, T: int, Lk: int, D: int) -> int:
+    """Bytes of device workspace attn_fwd_tree needs (0: shape not served)."""
+    return int(load_library().attn_tree_workspace_bytes(B, Hq, Hkv, T, Lk, D))
+
+
+def _workspace(n: int, call: str, device) -> torch.Tensor:
+    if n == 0:
+        raise AttnError(ATTN_ERR_UNSUPPORTED, call)
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def tree_workspace(q, k) -> torch.Tensor:
+    """A workspace tensor for attn_fwd_tree on drafts q [B,Hq,T,D] over a cache k [B,Hkv,Lk,D]."""
+    B, Hq, T, D = q.shape
+    return _workspace(attn_tree_workspace_bytes(B, Hq, k.shape[1], T, k.shape[2], D), "attn_tree_workspace_bytes",
+                      q.device)
+
+
+def attn_fwd_tree(q, k, v, k_new, v_new, cache_len, o, lse, workspace, scale: float, tree_mask=None, tree_len=None,
+                  kv_pitch=None, stream=None, check: bool = True) -> int:
+    """Attention of drafted tokens over a cache and each other (writes o, lse):
+    cache_len [B] int32 context lengths, tree_len [B] int32 draft counts (None:
+    all T), tree_mask uint8 [B,T,T] (None: a chain).  k and v may be slices of
+    a longer cache, as for attn_fwd_ex."""
+    _require("attn_fwd_tree", dense=(q, k_new, v_new, o), sliced=(k, v), f32=(lse,), u8=(tree_mask, workspace),
+             i32=(cache_len, tree_len))
+    B, Hq, T, D = q.shape
+    Hkv, Lk = k.shape[1], k.shape[2]
+    for t, want, name in ((k, (B, Hkv, Lk, D), "k"), (v, (B, Hkv, Lk, D), "v"), (k_new, (B, Hkv, T, D), "k_new"),
+                          (v_new, (B, Hkv, T, D), "v_new"), (o, q.shape, "o"), (lse, (B, Hq, T), "lse"),
+                          (cache_len, (B,), "cache_len"), (tree_len, (B,), "tree_len"),
+                          (tree_mask, (B, T, T), "tree_mask")):
+        _shape("attn_fwd_tree", t, want, name)
+    pitch = kv_row_pitch(k, v) if kv_pitch is None else int(kv_pitch)
+    st = load_library().attn_fwd_tree(_ptr(q), _ptr(k), _ptr(v), _ptr(k_new), _ptr(v_new), _ptr(tree_mask),
+                                      _ptr(cache_len), _ptr(tree_len), _ptr(o), _ptr(lse), _ptr(workspace),
+                                      workspace.numel(), pitch, B, Hq, Hkv, T, Lk, D, float(scale), _dtype_code(q),
+                                      _stream_handle(stream))
+    return _check(st, "attn_fwd_tree", check)
+
+
+def attn_cache_append(k_new, v_new, k, v, cache_len, accept_len, cache_len_out, path=None, pos=None, seen=None,
+                      seen_out=None, limit=None, kv_pitch=None, stream=None, check: bool = True) -> int:
+    """Accepted drafts into the cache (writes k, v, cache_len_out and, where
+    given, pos, seen_out, limit): rows path[b][:accept_len[b]] of k_new / v_new
+    (None: all T rows; the first ones) become cache rows cache_len[b] on."""
+    _require("attn_cache_append", dense=(k_new, v_new), sliced=(k, v),
+             i32=(cache_len, accept_len, cache_len_out, path, pos, seen, seen_out, limit))
+    B, Hkv, T, D = k_new.shape
+    Lk = k.shape[2]
+    for t, want, name in ((k, (B, Hkv, Lk, D), "k"), (v, (B, Hkv, Lk, D), "v"), (v_new, k_new.shape, "v_new"),
+                          (cache_len, (B,), "cache_len"), (accept_len, (B,), "accept_len"),
+                          (cache_len_out, (B,), "cache_len_out"), (path, (B, T), "path"), (pos, (B, Hkv, Lk), "pos"),
+                          (seen, (B,), "seen"), (seen_out, (B,), "seen_out"), (limit, (B, T), "limit")):
+        _shape("attn_cache_append", t, want, name)
+    pitch = kv_row_pitch(k, v) if kv_pitch is None else int(kv_pitch)
+    st = load_library().attn_cache_append(_ptr(k_new), _ptr(v_new), _ptr(path), _ptr(accept_len), _ptr(cache_len),
+                                          _ptr(seen), _ptr(k), _ptr(v), _ptr(pos), _ptr(cache_len_out),
+                                          _ptr(seen_out), _ptr(limit), pitch, B, Hkv, T, Lk, D, _dtype_code(k_new),
+                                          _stream_handle(stream))
+    return _check(st, "attn_cache_append", check)
+
+
+def attn_key_weight_workspace_bytes(B: int, Hq: int, Hkv: int, Lq: int, Lk: int, D: int) -> int:
+    """Bytes of device workspace attn_key_weight needs (0: shape not served)."""
+    return int(load_library().attn_key_weight_workspace_bytes(B, Hq, Hkv, Lq, Lk, D))
+
+
+def key_weight_workspace(q, k) -> torch.Tensor:
+    """A workspace tensor for attn_key_weight on q [B,Hq,Lq,D] and k [B,Hkv,Lk,D]."""
+    B, Hq, Lq, D = q.shape
+    return _workspace(attn_key_weight_workspace_bytes(B, Hq, k.shape[1], Lq, k.shape[2], D),
+                      "attn_key_weight_workspace_bytes", q.device)
+
+
+def attn_key_weight(q, k, lse, weight, weight_out, workspace, scale: float, causal: bool = False, limit=None,
+                    kv_pitch=None, stream=None, check: bool = True) -> int:
+    """weight_out = weight (None: zeros) + the attention weight each key of k
+    got from q's rows, whose base-2 log-sum-exps are lse; limit int32 [B,Lq]:
+    how many keys each row sees (0: the row adds nothing)."""
+    _require("attn_key_weight", dense=(q,), sliced=(k,), f32=(lse, weight, weight_out), u8=(workspace,), i32=(limit,))
+    B, Hq, Lq, D = q.shape
+    Hkv, Lk = k.shape[1], k.shape[2]
+    for t, want, name in ((k, (B, Hkv, Lk, D), "k"), (lse, (B, Hq, Lq), "lse"), (weight, (B, Hkv, Lk), "weight"),
+                          (weight_out, (B, Hkv, Lk), "weight_out"), (limit, (B, Lq), "limit")):
+        _shape("attn_key_weight", t, want, name)
+    pitch = kv_row_pitch(k, k) if kv_pitch is None else int(kv_pitch)
+    st = load_library().attn_key_weight(_ptr(q), _ptr(k), _ptr(lse), _ptr(limit), _ptr(weight), _ptr(weight_out),
+                                        _ptr(workspace), workspace.numel(), pitch, B, Hq, Hkv, Lq, Lk, D,
+                                        float(scale), int(bool(causal)), _dtype_code(q), _stream_handle(stream))
+    return _check(st, "attn_key_weight", check)
+
+
+def attn_cache_evict_workspace_bytes(B: int, Hkv: int, Lk: int) -> int:
+    """Bytes of device workspace attn_cache_evict needs (0: shape not served)."""
+    return int(load_library().attn_cache_evict_workspace_bytes(B, Hkv, Lk))
+
+
+def evict_workspace(k) -> torch.Tensor:
+    """A workspace tensor for attn_cache_evict on a cache k [B,Hkv,Lk,D]."""
+    return _workspace(attn_cache_evict_workspace_bytes(*k.shape[:3]), "attn_cache_evict_workspace_bytes", k.device)
+
+
+def attn_cache_evict(k, v, weight, pos, cache_len, seen, weight_out, pos_out, cache_len_out, workspace, keep: int,
+                     recent: int, kv_pitch=None, stream=None, check: bool = True) -> int:
+    """Keep, in every KV head, the `recent` newest tokens and the heaviest
+    others, `keep` in all (changes k and v in place, writes weight_out,
+    pos_out, cache_len_out)."""
+    _require("attn_cache_evict", sliced=(k, v), f32=(weight, weight_out), u8=(workspace,),
+             i32=(pos, cache_len, seen, pos_out, cache_len_out))
+    B, Hkv, Lk, D = k.shape
+    for t, want, name in ((v, k.shape, "v"), (weight, (B, Hkv, Lk), "weight"), (pos, (B, Hkv, Lk), "pos"),
+                          (weight_out, (B, Hkv, Lk), "weight_out"), (pos_out, (B, Hkv, Lk), "pos_out"),
+                          (cache_len, (B,), "cache_len"), (seen, (B,), "seen"),
+                          (cache_len_out, (B,), "cache_len_out")):
+        _shape("attn_cache_evict", t, want, name)
+    pitch = kv_row_pitch(k, v) if kv_pitch is None else int(kv_pitch)
+    st = load_library().attn_cache_evict(_ptr(k), _ptr(v), _ptr(weight), _ptr(pos), _ptr(cache_len), _ptr(seen),
+                                         _ptr(weight_out), _ptr(pos_out), _ptr(cache_len_out), _ptr(workspace),
+                                         workspace.numel(), pitch, B, Hkv, Lk, D, int(keep), int(recent),
+                                         _dtype_code(k), _stream_handle(stream))
+    return _check(st, "attn_cache_evict", check)
 
 
 def attn_last_device_status(stream=None) -> int:

@@ -209,6 +209,120 @@ attn_status_t attn_bwd_decode(const void* q, const void* k, const void* v, const
                               int causal, attn_dtype_t dtype, cudaStream_t stream);
 
 /*
+ * Drafted tokens over a key/value cache (tree attention).  Each sequence b
+ * has cache_len[b] tokens in the cache and up to T drafted tokens that are not
+ * in it yet: draft t attends to the whole context and, among the drafts, to
+ * those its mask row keeps (its ancestors and itself in a tree of drafts).
+ *   s_tj = scale * q_t . k_j        for cache rows j < cache_len[b],
+ *   s_tu = scale * q_t . k_new_u    for drafts u < tree_len[b] with
+ *                                   tree_mask[b][t][u] != 0 (NULL: u <= t),
+ *   O_t = softmax(s_t) [v; v_new],  lse_t = log2 sum exp2(s_t * log2(e)).
+ * T = 1 is an ordinary decode step over sequences of unequal lengths.
+ *   q [B,Hq,T,D], k_new and v_new [B,Hkv,T,D]: inputs (dtype), contiguous.
+ *   k, v: the cache, [B,Hkv,Lk,D] with kv_pitch rows between heads as in
+ *     attn_fwd_ex (0 = Lk); Lk is the capacity the call may read, not a length.
+ *   cache_len [B] int32, on the DEVICE: 0 <= cache_len[b] <= Lk (a value
+ *     outside is brought to the nearest end of that range).  Rows from
+ *     cache_len[b] on do not influence the result, whatever they hold.
+ *   tree_len [B] int32 on the device, or NULL (T for all): the drafts of
+ *     sequence b are t < tree_len[b] (values brought into 0..T); the others
+ *     are padding, whatever they hold.
+ *   tree_mask: uint8 [B,T,T] on the device, or NULL (a chain of drafts).
+ *   o [B,Hq,T,D] (dtype), lse float32 [B,Hq,T]: outputs, fully written; a
+ *     padding row and a row that sees nothing get O = 0 and lse = +inf.
+ *   A non-finite k_new row reaches only the rows that see it.  A non-finite
+ *     v_new (or v) row of a sequence reaches every row of that sequence,
+ *     as P = 0 times a non-finite value is not 0.
+ *   workspace: as for the decode calls (one per call in flight), at least
+ *     attn_tree_workspace_bytes(...) bytes; 0 there means the shape is rejected.
+ *   Limits: T <= 1024 and B <= 1024 (else ATTN_ERR_UNSUPPORTED).  G * T is not
+ *     limited.  int32 arrays are 4-byte aligned.  Other errors as for attn_fwd_ex.
+ */
+size_t attn_tree_workspace_bytes(int B, int Hq, int Hkv, int T, int Lk, int D);
+attn_status_t attn_fwd_tree(const void* q, const void* k, const void* v, const void* k_new, const void* v_new,
+                            const uint8_t* tree_mask, const int32_t* cache_len, const int32_t* tree_len, void* o,
+                            float* lse, void* workspace, size_t workspace_bytes, int64_t kv_pitch, int B, int Hq,
+                            int Hkv, int T, int Lk, int D, float scale, attn_dtype_t dtype, cudaStream_t stream);
+
+/*
+ * Accepted drafts into the cache.  Sequence b's n = accept_len[b] accepted
+ * drafts, path[b][0..n) (a root-to-leaf path of the draft tree, as draft
+ * indices), become its cache rows cache_len[b] .. cache_len[b] + n - 1, in
+ * every KV head: k[b,h,cache_len + i] = k_new[b,h,path[i]], v likewise.
+ *   k_new, v_new [B,Hkv,T,D]; k, v: the cache, as for attn_fwd_tree, written
+ *     at those rows only.
+ *   accept_len [B] or NULL (T for all); path [B,T] or NULL (0, 1, 2, ...: the
+ *     first n drafts, a prompt for instance).  n is cut at 0, at T, at the
+ *     cache's end, and at the first path entry outside 0..T-1.
+ *   cache_len_out [B]: cache_len[b] + n.  Not the same array as cache_len.
+ *   seen [B] or NULL: tokens sequence b has had so far, evicted ones included,
+ *     i.e. the next token's position.  seen_out [B] (with seen, not the same
+ *     array) gets seen[b] + n, and pos [B,Hkv,Lk] (with seen) gets the
+ *     position seen[b] + i of each new cache row.  Each may be NULL.
+ *   limit [B,T] or NULL: output for attn_key_weight: the number of cache rows
+ *     that draft t sees once the accepted ones are appended,
+ *     cache_len[b] + i + 1 for t = path[i] (the last such i), 0 for a draft
+ *     that was not accepted.
+ * All arrays but the 16-bit ones are int32; every pointer is a device pointer.
+ * Any T >= 1.  The inputs may not overlap the outputs.
+ */
+attn_status_t attn_cache_append(const void* k_new, const void* v_new, const int32_t* path, const int32_t* accept_len,
+                                const int32_t* cache_len, const int32_t* seen, void* k, void* v, int32_t* pos,
+                                int32_t* cache_len_out, int32_t* seen_out, int32_t* limit, int64_t kv_pitch, int B,
+                                int Hkv, int T, int Lk, int D, attn_dtype_t dtype, cudaStream_t stream);
+
+/*
+ * Accumulated attention weight of every cached key: to weight[b,hk,j] is
+ * added what the G query heads and all query rows that see key j gave it,
+ *   weight_out[b,hk,j] = weight[b,hk,j]
+ *                      + sum_{hq of hk} sum_i exp2(scale*log2(e) * q_i . k_j - lse_i),
+ * with the lse of attn_fwd, attn_fwd_tree or their variants over the same keys.
+ * It decides what attn_cache_evict keeps.
+ *   q [B,Hq,Lq,D], lse float32 [B,Hq,Lq]; k [B,Hkv,Lk,D] with kv_pitch.
+ *   Which keys row i sees: limit NULL: all, or with causal = 1 j <= i + (Lk - Lq)
+ *     as in attn_fwd; limit int32 [B,Lq] on the device (causal = 0): keys
+ *     j < limit[b][i], for every head (values outside 0..Lk are brought into
+ *     that range; 0: the row adds nothing).  limit needs Lq <= 1024.
+ *   A row whose lse is +inf adds nothing.
+ *   weight float32 [B,Hkv,Lk] contiguous, or NULL (zeros); weight_out
+ *     [B,Hkv,Lk] may be the same array.  Sums are in a fixed order: the same
+ *     call gives the same bits.
+ *   workspace: attn_key_weight_workspace_bytes(...) bytes, one per call in flight.
+ */
+size_t attn_key_weight_workspace_bytes(int B, int Hq, int Hkv, int Lq, int Lk, int D);
+attn_status_t attn_key_weight(const void* q, const void* k, const float* lse, const int32_t* limit,
+                              const float* weight, float* weight_out, void* workspace, size_t workspace_bytes,
+                              int64_t kv_pitch, int B, int Hq, int Hkv, int Lq, int Lk, int D, float scale, int causal,
+                              attn_dtype_t dtype, cudaStream_t stream);
+
+/*
+ * Eviction: every KV head of a sequence with more than `keep` tokens in the
+ * cache keeps `keep` of them.  Kept are the slots whose position is among the
+ * sequence's last `recent` ones (pos >= seen[b] - recent), then the ones with
+ * the largest weight; of equal ones the lower slot (NaN counts as the
+ * smallest weight; if more than `keep` slots are recent, the lower ones).
+ * A kept token in a slot below `keep` stays where it is; the i-th freed slot
+ * below `keep` takes the i-th kept token above, so only what has to move moves,
+ * sources and targets are different rows, and slots are in no order
+ * afterwards: pos says which token each holds (attention does not depend on
+ * the order of keys that all rows see).  Each KV head keeps its own choice.
+ *   k, v: the cache (as for attn_fwd_tree), changed in place: rows below
+ *     min(cache_len[b], keep) hold the kept tokens, the others are as before.
+ *   weight float32 and pos int32 [B,Hkv,Lk], cache_len and seen int32 [B]: inputs.
+ *   weight_out, pos_out [B,Hkv,Lk]: the kept slots' values; 0 and -1 in every
+ *     slot from the new length on.  cache_len_out [B]: min(cache_len[b], keep).
+ *     None of them is the same array as its input.
+ *   1 <= keep <= Lk, 0 <= recent <= keep (else ATTN_ERR_INVALID_ARG);
+ *   Lk <= 2^20 (else ATTN_ERR_UNSUPPORTED).
+ *   workspace: attn_cache_evict_workspace_bytes(...) bytes, one per call in flight.
+ */
+size_t attn_cache_evict_workspace_bytes(int B, int Hkv, int Lk);
+attn_status_t attn_cache_evict(void* k, void* v, const float* weight, const int32_t* pos, const int32_t* cache_len,
+                               const int32_t* seen, float* weight_out, int32_t* pos_out, int32_t* cache_len_out,
+                               void* workspace, size_t workspace_bytes, int64_t kv_pitch, int B, int Hkv, int Lk,
+                               int D, int keep, int recent, attn_dtype_t dtype, cudaStream_t stream);
+
+/*
  * attn_bwd for callers that cannot allocate device memory.  (The pages have no
  * counterpart: this is an entry point of this library only.)
  *
