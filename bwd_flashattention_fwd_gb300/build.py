@@ -1,7 +1,7 @@
 """Build libgbattn.so in-tree with nvcc for sm_103a.
 
 The kernel instantiations compile as one translation unit per head dimension
-(inst.cu with -DGBATTN_HEAD_DIM=<D>), in parallel, plus the C-ABI unit and
+(inst.cu and cache_inst.cu with -DGBATTN_HEAD_DIM=<D>), in parallel, plus the C-ABI unit and
 the linear cross-entropy unit (lce.cu) and the cache unit (cache.cu); the objects link into
 bwd_flashattention_fwd_gb300/libgbattn.so (no library besides the CUDA
 runtime).  checks.cu becomes libgbattn_checks.so, a test aid.
@@ -63,8 +63,9 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), debug: boo
     flags = [*FLAGS, *extra_flags] + (["-DGBATTN_DEBUG_CHECKS"] if debug else [])
     jobs = []
     for d in HEAD_DIMS:
-        obj = os.path.join(bdir, f"inst_d{d}.o")
-        jobs.append([nvcc, *ARCH, *flags, f"-DGBATTN_HEAD_DIM={d}", "-c", os.path.join(CSRC, "inst.cu"), "-o", obj])
+        for unit in ("inst", "cache_inst"):
+            obj = os.path.join(bdir, f"{unit}_d{d}.o")
+            jobs.append([nvcc, *ARCH, *flags, f"-DGBATTN_HEAD_DIM={d}", "-c", os.path.join(CSRC, unit + ".cu"), "-o", obj])
     for unit in ("api", "lce", "cache"):
         jobs.append([nvcc, *ARCH, *flags, "-c", os.path.join(CSRC, unit + ".cu"), "-o", os.path.join(bdir, unit + ".o")])
     checks_obj = os.path.join(bdir, "checks.o")

@@ -8,7 +8,6 @@
 #include "cache.h"
 #include "cache_kernel.cuh"
 #include "key_weight_kernel.cuh"
-#include "tree_kernel.cuh"
 
 namespace gbattn {
 namespace {
@@ -45,7 +44,10 @@ attn_status_t check_tree(int B, int Hq, int Hkv, int T, int Lk, int D) {
   if (Hq % Hkv != 0) return ATTN_ERR_INVALID_ARG;
   if (s != ATTN_OK) return s;
   if (T > kTreeMaxT || B > kTreeMaxB) return ATTN_ERR_UNSUPPORTED;
-  if (static_cast<long long>(B) * Hq * T > 0x7fffffffLL) return ATTN_ERR_UNSUPPORTED;
+  // stages of the whole call, and the combine kernel's rows per KV head, are ints that a grid takes
+  const long long stages = (Lk + kTreeStage - 1) / kTreeStage + (T + kTreeStage - 1) / kTreeStage;
+  if (stages * B * Hkv > 0x7fffffffLL) return ATTN_ERR_UNSUPPORTED;
+  if (static_cast<long long>(Hq / Hkv) * T > 65535) return ATTN_ERR_UNSUPPORTED;
   return ATTN_OK;
 }
 
@@ -61,10 +63,8 @@ attn_status_t check_key_weight(int B, int Hq, int Hkv, int Lq, int Lk, int D) {
 
 attn_status_t launched() { return cudaPeekAtLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA; }
 
-template <int D, bool BF16>
-attn_status_t launch_tree(const TreeParams& p, cudaStream_t stream) {
-  attn_tree_kernel<D, BF16><<<p.B * p.Hq * p.T, kTreeThreads, 0, stream>>>(p);
-  return launched();
+attn_status_t finish(int r) {
+  return r == kLaunchOk ? ATTN_OK : r == kLaunchBadMap ? ATTN_ERR_INVALID_ARG : ATTN_ERR_CUDA;
 }
 
 template <int D, bool BF16>
@@ -82,7 +82,9 @@ attn_status_t launch_key_weight(const KeyWeightParams& p, cudaStream_t stream) {
 using namespace gbattn;
 
 extern "C" size_t attn_tree_workspace_bytes(int B, int Hq, int Hkv, int T, int Lk, int D) {
-  return check_tree(B, Hq, Hkv, T, Lk, D) == ATTN_OK ? 16 : 0;
+  if (check_tree(B, Hq, Hkv, T, Lk, D) != ATTN_OK) return 0;
+  const TreePlan t = tree_plan(static_cast<long long>(Hq / Hkv) * T, D, kTreeMaxCtas);
+  return static_cast<size_t>(t.n_groups) * 2 * t.n_rb * t.rows * (D + 1) * sizeof(float);
 }
 
 extern "C" attn_status_t attn_fwd_tree(const void* q, const void* k, const void* v, const void* k_new,
@@ -106,14 +108,19 @@ extern "C" attn_status_t attn_fwd_tree(const void* q, const void* k, const void*
   EncodeTiledFn enc;
   const attn_status_t ds = shared_device_state(&dev, &enc, &status, &num_sms);
   if (ds != ATTN_OK) return ds;
-  TreeParams p{q, k, v, k_new, v_new, tree_mask, cache_len, tree_len, o, lse, kv_pitch ? kv_pitch : Lk,
-               B, Hq, Hkv, Hq / Hkv, T, Lk, scale_log2_of(scale), status, shared_wait_limit_ns()};
-  const bool bf = dtype == ATTN_DTYPE_BF16;
+  TreeParams p{};
+  p.q = q, p.k = k, p.v = v, p.k_new = k_new, p.v_new = v_new;
+  p.mask = tree_mask, p.cache_len = cache_len, p.tree_len = tree_len;
+  p.o = o, p.lse = lse, p.part = static_cast<float*>(workspace);
+  p.kv_pitch = kv_pitch ? kv_pitch : Lk;
+  p.B = B, p.Hq = Hq, p.Hkv = Hkv, p.G = Hq / Hkv, p.T = T, p.Lk = Lk;
+  p.scale_log2 = scale_log2_of(scale), p.status = status, p.limit_ns = shared_wait_limit_ns();
+  const bool bf16 = dtype == ATTN_DTYPE_BF16;
   switch (D) {
-    case 64: return bf ? launch_tree<64, true>(p, stream) : launch_tree<64, false>(p, stream);
-    case 96: return bf ? launch_tree<96, true>(p, stream) : launch_tree<96, false>(p, stream);
-    case 128: return bf ? launch_tree<128, true>(p, stream) : launch_tree<128, false>(p, stream);
-    default: return bf ? launch_tree<256, true>(p, stream) : launch_tree<256, false>(p, stream);
+    case 64: return finish(launch_tree_d64(p, bf16, num_sms, enc, stream));
+    case 96: return finish(launch_tree_d96(p, bf16, num_sms, enc, stream));
+    case 128: return finish(launch_tree_d128(p, bf16, num_sms, enc, stream));
+    default: return finish(launch_tree_d256(p, bf16, num_sms, enc, stream));
   }
 }
 

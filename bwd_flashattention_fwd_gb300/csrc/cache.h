@@ -8,6 +8,9 @@ namespace gbattn {
 
 constexpr int kTreeMaxT = 1024;   // drafts per sequence (the mask is T x T bytes per sequence)
 constexpr int kTreeMaxB = 1024;   // sequences (each CTA holds the lengths' prefix sums in shared memory)
+constexpr int kTreeStage = 64;    // keys per pipeline stage
+constexpr int kTreeMinStages = 2;  // least stages a CTA takes
+constexpr int kTreeMaxCtas = 152;  // one per SM of a GB300
 constexpr int kEvictMaxLk = 1 << 20;
 
 struct TreeParams {
@@ -22,7 +25,31 @@ struct TreeParams {
   float scale_log2;
   int* status;
   uint64_t limit_ns;
+  // division of the work (tree_plan) and the partials of KV heads that several CTAs share
+  int n_rb, n_groups;
+  float* part;      // [n_groups][2][n_rb][rows][D]
+  float* part_lse;  // [n_groups][2][n_rb][rows]
 };
+
+// How the packed rows of a KV head (R = G * T) are laid out over CTAs: rows
+// per CTA, row blocks, and groups of n_rb CTAs that share out the keys.
+struct TreePlan {
+  int qs, nt, rows, n_rb, n_groups;
+};
+
+// R <= 32 / 64: the rows sit in four / two lane quadrants that share the keys
+// out; up to 128: one full tile; above: 256 rows per CTA where two
+// accumulators fit tensor memory (D <= 128).
+inline TreePlan tree_plan(long long R, int D, int num_sms) {
+  TreePlan t;
+  t.qs = R <= 32 ? 4 : R <= 64 ? 2 : 1;
+  t.nt = R > 128 && D <= 128 ? 2 : 1;
+  t.rows = t.qs > 1 ? 128 / t.qs : 128 * t.nt;
+  t.n_rb = static_cast<int>((R + t.rows - 1) / t.rows);
+  const int ctas = num_sms < kTreeMaxCtas ? num_sms : kTreeMaxCtas;
+  t.n_groups = ctas / t.n_rb > 1 ? ctas / t.n_rb : 1;
+  return t;
+}
 
 struct KeyWeightParams {
   const void *q, *k;
@@ -59,5 +86,16 @@ struct EvictParams {
   int B, Hkv, Lk, row16, keep, recent;
   int* status;
 };
+
+// Launchers of one head dimension (cache_inst.cu); LaunchResult codes.
+#define GBATTN_DECLARE_CACHE_LAUNCHERS(DIM)                                                     \
+  int launch_tree_d##DIM(const TreeParams& p, bool bf16, int num_sms, EncodeTiledFn enc, cudaStream_t stream);
+
+GBATTN_DECLARE_CACHE_LAUNCHERS(64)
+GBATTN_DECLARE_CACHE_LAUNCHERS(96)
+GBATTN_DECLARE_CACHE_LAUNCHERS(128)
+GBATTN_DECLARE_CACHE_LAUNCHERS(256)
+
+#undef GBATTN_DECLARE_CACHE_LAUNCHERS
 
 }  // namespace gbattn

@@ -1,0 +1,100 @@
+// Instantiations and launchers of the cache kernels for one head dimension
+// (compiled once per supported D with -DGBATTN_HEAD_DIM=<D>, like inst.cu).
+#include "cache.h"
+#include "tree_kernel.cuh"
+
+#ifndef GBATTN_HEAD_DIM
+#error "compile with -DGBATTN_HEAD_DIM=<64|96|128|256>"
+#endif
+
+#define GBATTN_CAT2(a, b) a##b
+#define GBATTN_CAT(a, b) GBATTN_CAT2(a, b)
+
+namespace gbattn {
+namespace GBATTN_CAT(cache_d, GBATTN_HEAD_DIM) {
+
+constexpr int kD = GBATTN_HEAD_DIM;
+
+// Rank-3 view [heads, L, D] with `pitch` rows between heads; boxes of 64
+// columns x box_rows rows with the 128-byte swizzle.  Rows past L and columns
+// past D read as zeros.
+bool make_map(EncodeTiledFn enc, bool bf16, CUtensorMap* m, const void* base, long long L, long long heads,
+              int box_rows, long long pitch) {
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(kD), static_cast<cuuint64_t>(L),
+                              static_cast<cuuint64_t>(heads)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(kD) * 2,
+                                 static_cast<cuuint64_t>(kD) * 2 * static_cast<cuuint64_t>(pitch)};
+  const cuuint32_t box[3] = {64u, static_cast<cuuint32_t>(box_rows), 1u};
+  const cuuint32_t elem_strides[3] = {1u, 1u, 1u};
+  return enc(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+             const_cast<void*>(base), dims, strides, box, elem_strides, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Launch as a programmatic dependent of the kernel before it on the stream.
+template <typename Kern, typename... Args>
+int launch_dependent(Kern kern, dim3 grid, int threads, cudaStream_t stream, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kern, args...) != cudaSuccess) return kLaunchCudaError;
+  return cudaPeekAtLastError() == cudaSuccess ? kLaunchOk : kLaunchCudaError;
+}
+
+template <bool BF16, int QS, int NT>
+int tree_impl(const TreeParams& p, EncodeTiledFn enc, cudaStream_t stream) {
+  using Gm = TreeGeom<kD, QS, NT>;
+  const long long R = static_cast<long long>(p.G) * p.T, heads = static_cast<long long>(p.B) * p.Hkv;
+  CUtensorMap tq, tk, tv, tkn, tvn;
+  if (!make_map(enc, BF16, &tq, p.q, R, heads, Gm::QROWS, R) ||
+      !make_map(enc, BF16, &tk, p.k, p.Lk, heads, Gm::BK, p.kv_pitch) ||
+      !make_map(enc, BF16, &tv, p.v, p.Lk, heads, Gm::BK, p.kv_pitch) ||
+      !make_map(enc, BF16, &tkn, p.k_new, p.T, heads, Gm::BK, p.T) ||
+      !make_map(enc, BF16, &tvn, p.v_new, p.T, heads, Gm::BK, p.T))
+    return kLaunchBadMap;
+  auto kern = attn_tree_kernel<kD, BF16, QS, NT>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Gm::SMEM_BYTES) != cudaSuccess)
+    return kLaunchCudaError;
+  kern<<<p.n_groups * p.n_rb, Gm::NUM_THREADS, Gm::SMEM_BYTES, stream>>>(tq, tk, tv, tkn, tvn, p);
+  if (cudaPeekAtLastError() != cudaSuccess) return kLaunchCudaError;
+  if (p.n_groups == 1) return kLaunchOk;  // no KV head is shared
+  // warps per row by how many partials a head can have
+  const long long avg = p.n_groups / heads + 1;
+  if (avg > 8)
+    return launch_dependent(attn_tree_combine_kernel<kD, BF16, 8>, dim3(p.n_groups - 1, static_cast<unsigned>(R)), 256,
+                            stream, p, Gm::ROWS);
+  return launch_dependent(attn_tree_combine_kernel<kD, BF16, 2>,
+                          dim3(p.n_groups - 1, static_cast<unsigned>((R + 3) / 4)), 256, stream, p, Gm::ROWS);
+}
+
+template <bool BF16>
+int tree_dispatch(const TreeParams& p, const TreePlan& plan, EncodeTiledFn enc, cudaStream_t stream) {
+  if (plan.qs == 4) return tree_impl<BF16, 4, 1>(p, enc, stream);
+  if (plan.qs == 2) return tree_impl<BF16, 2, 1>(p, enc, stream);
+  if constexpr (kD <= 128) {
+    if (plan.nt == 2) return tree_impl<BF16, 1, 2>(p, enc, stream);
+  }
+  return tree_impl<BF16, 1, 1>(p, enc, stream);
+}
+
+}  // namespace GBATTN_CAT(cache_d, GBATTN_HEAD_DIM)
+
+using namespace GBATTN_CAT(cache_d, GBATTN_HEAD_DIM);
+
+int GBATTN_CAT(launch_tree_d, GBATTN_HEAD_DIM)(const TreeParams& p0, bool bf16, int num_sms, EncodeTiledFn enc,
+                                               cudaStream_t stream) {
+  const TreePlan plan = tree_plan(static_cast<long long>(p0.G) * p0.T, kD, num_sms);
+  TreeParams p = p0;
+  p.n_rb = plan.n_rb, p.n_groups = plan.n_groups;
+  p.part_lse = p.part + static_cast<size_t>(plan.n_groups) * 2 * plan.n_rb * plan.rows * kD;
+  return bf16 ? tree_dispatch<true>(p, plan, enc, stream) : tree_dispatch<false>(p, plan, enc, stream);
+}
+
+}  // namespace gbattn

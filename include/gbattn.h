@@ -235,8 +235,9 @@ attn_status_t attn_bwd_decode(const void* q, const void* k, const void* v, const
  *     as P = 0 times a non-finite value is not 0.
  *   workspace: as for the decode calls (one per call in flight), at least
  *     attn_tree_workspace_bytes(...) bytes; 0 there means the shape is rejected.
- *   Limits: T <= 1024 and B <= 1024 (else ATTN_ERR_UNSUPPORTED).  G * T is not
- *     limited.  int32 arrays are 4-byte aligned.  Other errors as for attn_fwd_ex.
+ *   Limits: T <= 1024, B <= 1024 and G * T <= 65535 (else
+ *     ATTN_ERR_UNSUPPORTED).  int32 arrays are 4-byte aligned.  Other errors as
+ *     for attn_fwd_ex.
  */
 size_t attn_tree_workspace_bytes(int B, int Hq, int Hkv, int T, int Lk, int D);
 attn_status_t attn_fwd_tree(const void* q, const void* k, const void* v, const void* k_new, const void* v_new,
