@@ -9,7 +9,7 @@ namespace gbattn {
 constexpr int kTreeMaxT = 1024;   // drafts per sequence (the mask is T x T bytes per sequence)
 constexpr int kTreeMaxB = 1024;   // sequences (each CTA holds the lengths' prefix sums in shared memory)
 constexpr int kTreeStage = 64;    // keys per pipeline stage
-constexpr int kTreeMinStages = 2;  // least stages a CTA takes
+constexpr int kTreeMinStages = 1;  // least stages a CTA takes
 constexpr int kTreeMaxCtas = 152;  // one per SM of a GB300
 constexpr int kEvictMaxLk = 1 << 20;
 

@@ -89,6 +89,19 @@ __device__ __forceinline__ void mbar_wait(uint32_t bar, uint32_t parity, const W
   mbar_wait_slow(bar, parity, g, code);
 }
 
+// Whether the phase is complete, without waiting.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+
 // Bounded wait until a shared-memory counter that another warp of the CTA
 // raises reaches v (the same limit and abort rules as mbar_wait).  A counter
 // that only grows cannot confuse one wait with a later one, which an

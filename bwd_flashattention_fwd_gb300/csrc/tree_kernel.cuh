@@ -46,6 +46,15 @@
 
 namespace gbattn {
 
+// What every block derives from the lengths: pre[b] = stages of one KV head
+// of the sequences before b (pre[B] the total), and the lengths themselves.
+struct TreeTable {
+  int pre[kTreeMaxB + 1];
+  int len[kTreeMaxB];
+  uint16_t tl[kTreeMaxB];
+};
+constexpr int kTreeStaticSmem = sizeof(TreeTable) + 4096;
+
 template <int D, int QS, int NT>
 struct TreeGeom {
   static constexpr int BK = kTreeStage;   // keys per stage
@@ -55,10 +64,11 @@ struct TreeGeom {
   static constexpr int NCH = n_chunks(D);
   static constexpr int Q_BYTES = NCH * 128 * 128;
   static constexpr int KV_BYTES = NCH * BK * 128;
-  static constexpr int XCH_BYTES = QS > 1 ? 128 * 33 * 4 : 0;  // merging the quadrants' O
-  static constexpr int AVAIL = kMaxDynSmem - 12288 - 1024 - NT * Q_BYTES - XCH_BYTES;
-  static constexpr int STAGES = AVAIL / (2 * KV_BYTES) > 8 ? 8 : AVAIL / (2 * KV_BYTES);  // K and V each
-  static constexpr int SMEM_BYTES = 1024 + NT * Q_BYTES + STAGES * 2 * KV_BYTES + XCH_BYTES;
+  static constexpr int XCH_PITCH = 36;  // floats: 16-byte pieces of eight neighbouring rows fall into different banks
+  static constexpr int XCH_BYTES = QS > 1 ? 128 * XCH_PITCH * 4 : 0;  // merging the quadrants' O
+  static constexpr int AVAIL = kMaxDynSmem - kTreeStaticSmem - 1024 - NT * Q_BYTES - XCH_BYTES;
+  static constexpr int SLOTS = AVAIL / KV_BYTES > 16 ? 16 : AVAIL / KV_BYTES;  // a K or a V tile each
+  static constexpr int SMEM_BYTES = 1024 + NT * Q_BYTES + SLOTS * KV_BYTES + XCH_BYTES;
   static constexpr int O_W = D <= 128 ? 128 : 256;
   static constexpr int TMEM_COLS = NT * (O_W + 2 * BK) <= 256 ? 256 : 512;
   static constexpr int SOFTMAX_WARPS = 4 * NT;
@@ -67,11 +77,11 @@ struct TreeGeom {
   __host__ __device__ static constexpr int o_col(int t) { return t * O_W; }
   __host__ __device__ static constexpr int s_col(int t, int b) { return NT * O_W + (2 * t + b) * BK; }
   static_assert(NT * (O_W + 2 * BK) <= 512, "tensor memory budget");
-  static_assert(STAGES >= 2, "shared memory budget");
+  static_assert(SLOTS >= 4, "shared memory budget");  // K of two stages ahead of the oldest V
   static_assert(QS == 1 || NT == 1, "only a full tile comes in pairs");
 };
 
-// Stages of sequence b (its drafts' first, then its context's).
+// Lengths of sequence b, and the stages of one of its KV heads (the drafts' first, then the context's).
 __device__ __forceinline__ void tree_lengths(const TreeParams& p, int b, int& len, int& tl) {
   len = min(max(p.cache_len[b], 0), p.Lk);
   tl = p.tree_len ? min(max(p.tree_len[b], 0), p.T) : p.T;
@@ -80,31 +90,45 @@ __device__ __forceinline__ int tree_stages(int len, int tl) {
   return tl == 0 ? 0 : (len + kTreeStage - 1) / kTreeStage + (tl + kTreeStage - 1) / kTreeStage;
 }
 
-// pre[b] = stages of one KV head of the sequences before b, pre[B] the total
-// (whole block; ends with a barrier).
-__device__ __forceinline__ void tree_prefix(const TreeParams& p, int* pre) {
-  for (int b = threadIdx.x; b < p.B; b += blockDim.x) {
-    int len, tl;
-    tree_lengths(p, b, len, tl);
-    pre[b + 1] = tree_stages(len, tl);
-  }
-  if (threadIdx.x == 0) pre[0] = 0;
-  __syncthreads();
-  if (threadIdx.x < 32) {
-    int run = 0;
-    for (int b0 = 0; b0 < p.B; b0 += 32) {
-      const int b = b0 + static_cast<int>(threadIdx.x);
-      int x = b < p.B ? pre[b + 1] : 0;
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, d);
-        if (static_cast<int>(threadIdx.x) >= d) x += y;
-      }
-      if (b < p.B) pre[b + 1] = run + x;
-      run += __shfl_sync(0xffffffffu, x, 31);
+// Fills the table (whole block; the caller's next barrier publishes it).  Up
+// to 32 sequences, one warp does it all; more, the block loads the lengths first.
+__device__ __forceinline__ void tree_table(const TreeParams& p, TreeTable& tab) {
+  if (p.B > 32) {
+    for (int b = threadIdx.x; b < p.B; b += blockDim.x) {
+      int len, tl;
+      tree_lengths(p, b, len, tl);
+      tab.pre[b + 1] = tree_stages(len, tl);
+      tab.len[b] = len;
+      tab.tl[b] = static_cast<uint16_t>(tl);
     }
+    __syncthreads();
   }
-  __syncthreads();
+  if (threadIdx.x >= 32) return;
+  const int lane = threadIdx.x;
+  if (lane == 0) tab.pre[0] = 0;
+  int run = 0;
+  for (int b0 = 0; b0 < p.B; b0 += 32) {
+    const int b = b0 + lane;
+    int x = 0;
+    if (b < p.B) {
+      if (p.B > 32) {
+        x = tab.pre[b + 1];
+      } else {
+        int len, tl;
+        tree_lengths(p, b, len, tl);
+        x = tree_stages(len, tl);
+        tab.len[b] = len;
+        tab.tl[b] = static_cast<uint16_t>(tl);
+      }
+    }
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, d);
+      if (lane >= d) x += y;
+    }
+    if (b < p.B) tab.pre[b + 1] = run + x;
+    run += __shfl_sync(0xffffffffu, x, 31);
+  }
 }
 
 // The sequence that stage x of the whole list belongs to: the largest b with pre[b] * Hkv <= x
@@ -181,14 +205,14 @@ __global__ void __launch_bounds__(TreeGeom<D, QS, NT>::NUM_THREADS, 1)
                      const __grid_constant__ CUtensorMap tmVn, const TreeParams p) {
   using Gm = TreeGeom<D, QS, NT>;
   using E = Elem<BF16>;
-  constexpr int BK = Gm::BK, NCH = Gm::NCH, ST = Gm::STAGES, KPW = Gm::KPW;
+  constexpr int BK = Gm::BK, NCH = Gm::NCH, SL = Gm::SLOTS, KPW = Gm::KPW;
   constexpr int PRODUCER = Gm::SOFTMAX_WARPS;
   constexpr int kWait = wait_code<94>();  // every bounded wait of this kernel
 
   extern __shared__ uint8_t smem_raw[];
-  __shared__ uint64_t bar_q, bar_qfree, bar_kvfull[ST], bar_kvempty[ST], bar_sfull[NT][2], bar_pready[NT][2],
+  __shared__ uint64_t bar_q, bar_qfree, bar_full[SL], bar_empty[SL], bar_sfull[NT][2], bar_pready[NT][2],
       bar_odone[NT][2], bar_mfin[NT];
-  __shared__ int pre[kTreeMaxB + 1];
+  __shared__ TreeTable tab;
   __shared__ float2 ml[128 * NT];
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int abort_flag;
@@ -198,18 +222,23 @@ __global__ void __launch_bounds__(TreeGeom<D, QS, NT>::NUM_THREADS, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t sbase = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const uint32_t sQ = sbase;                  // tile t at sQ + t * Q_BYTES
-  const uint32_t sK0 = sQ + NT * Gm::Q_BYTES;  // stage s: K at sK0 + 2 s KV_BYTES, V right after
-  float* xch = reinterpret_cast<float*>(smem_raw + (sK0 + ST * 2 * Gm::KV_BYTES - smem_u32(smem_raw)));
+  const uint32_t sKV = sQ + NT * Gm::Q_BYTES;  // slot s of the K / V ring at sKV + s * KV_BYTES
+  const uint32_t sX = sKV + SL * Gm::KV_BYTES;
   const int group = blockIdx.x / p.n_rb, rb = blockIdx.x - group * p.n_rb;
   const WaitGuard g{&abort_flag, p.status, p.limit_ns};
 
-  if (threadIdx.x == 0) {
+  if (threadIdx.x == 32 * PRODUCER) {
+    tma_prefetch_desc(&tmQ);
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+    tma_prefetch_desc(&tmKn);
+    tma_prefetch_desc(&tmVn);
     abort_flag = 0;
     mbar_init(smem_u32(&bar_q), 1);
     mbar_init(smem_u32(&bar_qfree), NT);
-    for (int s = 0; s < ST; ++s) {
-      mbar_init(smem_u32(&bar_kvfull[s]), 1);
-      mbar_init(smem_u32(&bar_kvempty[s]), NT);
+    for (int s = 0; s < SL; ++s) {
+      mbar_init(smem_u32(&bar_full[s]), 1);
+      mbar_init(smem_u32(&bar_empty[s]), NT);
     }
     for (int t = 0; t < NT; ++t) {
       for (int i = 0; i < 2; ++i) {
@@ -225,62 +254,81 @@ __global__ void __launch_bounds__(TreeGeom<D, QS, NT>::NUM_THREADS, 1)
     tmem_alloc(smem_u32(&tmem_slot), Gm::TMEM_COLS);
     tmem_relinquish();
   }
-  tree_prefix(p, pre);
+  tree_table(p, tab);
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem = tmem_slot;
-  TreeWalk w(p, pre, group);
+  TreeWalk w(p, tab.pre, group);
 
   if (warp == PRODUCER) {
     // ---------------- TMA producer (whole warp, one elected lane issues) ----------------
-    if (lane == 0) {
-      tma_prefetch_desc(&tmQ);
-      tma_prefetch_desc(&tmK);
-      tma_prefetch_desc(&tmV);
-      tma_prefetch_desc(&tmKn);
-      tma_prefetch_desc(&tmVn);
-    }
-    __syncwarp();
-    RingPos<ST> st;
+    // K and V tiles go into one ring in the order the MMA warps use them up:
+    // K0, K1, V0, K2, V1, ..., K(n-1), V(n-2), V(n-1).
+    RingPos<SL> st;
     int issued = 0, nq = 0;
-    for (; w.more() && !abort_flag; w.next()) {
-      const int z = w.b * p.Hkv + w.hk;
-      int len, tl;
-      tree_lengths(p, w.b, len, tl);
-      const int nd = (tl + BK - 1) / BK;  // draft stages
-      // the previous segment's S products, the only readers of Q, are complete
-      if (nq > 0) mbar_wait(smem_u32(&bar_qfree), (nq - 1) & 1, g, kWait);
-      __syncwarp();
-      if (abort_flag) break;
-      ++nq;
+    bool q_due = false;  // the segment's Q is still to be loaded (z, below)
+    int z = 0;
+    auto load_q = [&]() {
       mbar_arrive_expect_tx_w(smem_u32(&bar_q), NT * Gm::Q_BYTES);
       for (int t = 0; t < NT; ++t)
         for (int c = 0; c < NCH; ++c)
           for (int i = 0; i < QS; ++i)
             tma_load_3d_w(sQ + t * Gm::Q_BYTES + c * 128 * 128 + i * Gm::QROWS * 128, &tmQ, smem_u32(&bar_q), c * 64,
                           rb * Gm::ROWS + t * 128, z);
-      for (int j = w.j0; j < w.j1; ++j, st.next(), ++issued) {
-        const int s = st.slot;
-        if (issued >= ST) mbar_wait(smem_u32(&bar_kvempty[s]), st.phase ^ 1u, g, kWait);
-        __syncwarp();
-        if (abort_flag) break;
-        const uint32_t bar = smem_u32(&bar_kvfull[s]);
-        const uint32_t dK = sK0 + 2 * s * Gm::KV_BYTES;
-        mbar_arrive_expect_tx_w(bar, 2 * Gm::KV_BYTES);
-        const bool draft = j < nd;
-        const int row = draft ? j * BK : (j - nd) * BK;
-        for (int c = 0; c < NCH; ++c) {
-          tma_load_3d_w(dK + c * BK * 128, draft ? &tmKn : &tmK, bar, c * 64, row, z);
-          tma_load_3d_w(dK + Gm::KV_BYTES + c * BK * 128, draft ? &tmVn : &tmV, bar, c * 64, row, z);
-        }
+      ++nq;
+      q_due = false;
+    };
+    // Q's buffer is free once the previous segment's S products, its only
+    // readers, are complete.  The next segment's K and V do not wait for that:
+    // while a slot is awaited, Q is loaded as soon as it can be.
+    auto try_q = [&](bool block) {
+      if (!q_due) return;
+      if (nq > 0) {
+        if (block) mbar_wait(smem_u32(&bar_qfree), (nq - 1) & 1, g, kWait);
+        else if (!__all_sync(0xffffffffu, mbar_test(smem_u32(&bar_qfree), (nq - 1) & 1))) return;
       }
+      if (!__any_sync(0xffffffffu, abort_flag)) load_q();
+    };
+    auto load_tile = [&](const CUtensorMap* map, int row) {
+      const int s = st.slot;
+      if (issued >= SL) {
+        if (q_due) {  // whichever comes first; the limit is mbar_wait's, below
+          const uint64_t t0 = global_timer_ns();
+          while (q_due && !__any_sync(0xffffffffu, abort_flag || global_timer_ns() - t0 > p.limit_ns) &&
+                 !__all_sync(0xffffffffu, mbar_test(smem_u32(&bar_empty[s]), st.phase ^ 1u)))
+            try_q(false);
+        }
+        mbar_wait(smem_u32(&bar_empty[s]), st.phase ^ 1u, g, kWait);
+      }
+      if (__any_sync(0xffffffffu, abort_flag)) return;  // no further copy is issued
+      const uint32_t bar = smem_u32(&bar_full[s]);
+      mbar_arrive_expect_tx_w(bar, Gm::KV_BYTES);
+      for (int c = 0; c < NCH; ++c) tma_load_3d_w(sKV + s * Gm::KV_BYTES + c * BK * 128, map, bar, c * 64, row, z);
+      st.next();
+      ++issued;
+    };
+    for (; w.more() && !abort_flag; w.next()) {
+      z = w.b * p.Hkv + w.hk;
+      q_due = true;
+      try_q(false);
+      const int nd = (tab.tl[w.b] + BK - 1) / BK;  // draft stages
+      const int n = w.j1 - w.j0;
+      auto row_of = [&](int j) { return j < nd ? j * BK : (j - nd) * BK; };
+      load_tile(w.j0 < nd ? &tmKn : &tmK, row_of(w.j0));
+      for (int i = 1; i <= n && !abort_flag; ++i) {
+        const int jk = w.j0 + i, jv = jk - 1;
+        if (i < n) load_tile(jk < nd ? &tmKn : &tmK, row_of(jk));
+        load_tile(jv < nd ? &tmVn : &tmV, row_of(jv));
+        try_q(false);
+      }
+      try_q(true);
     }
-    // the last ST issued stages (each slot holds at most one copy in flight) and the last Q
-    for (int u = 0; u < ST && u < issued; ++u) {
+    // the last SL issued tiles (each slot holds at most one copy in flight) and the last Q
+    for (int u = 0; u < SL && u < issued; ++u) {
       if (st.slot == 0) st.phase ^= 1u;
-      st.slot = (st.slot == 0 ? ST : st.slot) - 1;
-      mbar_wait_drain(smem_u32(&bar_kvfull[st.slot]), st.phase);
+      st.slot = (st.slot == 0 ? SL : st.slot) - 1;
+      mbar_wait_drain(smem_u32(&bar_full[st.slot]), st.phase);
     }
     if (nq > 0) mbar_wait_drain(smem_u32(&bar_q), (nq - 1) & 1);
     __syncwarp();
@@ -290,24 +338,26 @@ __global__ void __launch_bounds__(TreeGeom<D, QS, NT>::NUM_THREADS, 1)
     constexpr uint32_t IDESC_QK = make_idesc_f16(128, BK, BF16, false, false);
     constexpr uint32_t IDESC_PV = make_idesc_f16(128, D, BF16, false, true);
     const uint64_t dQd = make_sdesc_sw128(sQ + t * Gm::Q_BYTES, 16, 1024);      // this tile's Q, K-major
-    const uint64_t dKk = make_sdesc_sw128(sK0, 16, 1024);                       // K stage 0, K-major
-    const uint64_t dVm = make_sdesc_sw128(sK0 + Gm::KV_BYTES, BK * 128, 1024);  // V stage 0, MN-major
-    RingPos<ST> st_s, st_pv;
+    const uint64_t dK = make_sdesc_sw128(sKV, 16, 1024);       // slot 0 as K, K-major
+    const uint64_t dV = make_sdesc_sw128(sKV, BK * 128, 1024);  // slot 0 as V, MN-major
+    RingPos<SL> st;
     int ts = 0, tp = 0;  // stages (all segments) of the next S and of the next P V
-    auto issue_s = [&]() {
-      const int s = st_s.slot, bb = ts & 1;
-      mbar_wait(smem_u32(&bar_kvfull[s]), st_s.phase, g, kWait);
-      st_s.next();
+    auto issue_s = [&](bool last) {
+      const int s = st.slot, bb = ts & 1;
+      mbar_wait(smem_u32(&bar_full[s]), st.phase, g, kWait);
+      st.next();
       ++ts;
       __syncwarp();
       tc_fence_after_sync();
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
         const uint32_t qo = (kk >> 2) * (128 * 128) + (kk & 3) * 32;
-        const uint32_t ko = 2 * s * Gm::KV_BYTES + (kk >> 2) * (BK * 128) + (kk & 3) * 32;
-        mma_ss_w(tmem + Gm::s_col(t, bb), sdesc_add(dQd, qo), sdesc_add(dKk, ko), IDESC_QK, kk > 0 ? 1u : 0u);
+        const uint32_t ko = s * Gm::KV_BYTES + (kk >> 2) * (BK * 128) + (kk & 3) * 32;
+        mma_ss_w(tmem + Gm::s_col(t, bb), sdesc_add(dQd, qo), sdesc_add(dK, ko), IDESC_QK, kk > 0 ? 1u : 0u);
       }
       mma_commit_w(smem_u32(&bar_sfull[t][bb]));
+      mma_commit_w(smem_u32(&bar_empty[s]));
+      if (last) mma_commit_w(smem_u32(&bar_qfree));  // last read of this segment's Q
     };
     int r = 0;
     for (; w.more(); w.next(), ++r) {
@@ -315,28 +365,24 @@ __global__ void __launch_bounds__(TreeGeom<D, QS, NT>::NUM_THREADS, 1)
       mbar_wait(smem_u32(&bar_q), r & 1, g, kWait);
       __syncwarp();
       tc_fence_after_sync();
-      for (int j = 0; j < 2 && j < n; ++j) {
-        issue_s();
-        if (j == n - 1) mma_commit_w(smem_u32(&bar_qfree));  // last read of this segment's Q
-      }
+      issue_s(n == 1);
+      if (n > 1) issue_s(n == 2);
       for (int j = 0; j < n; ++j) {
-        const int s = st_pv.slot, bb = tp & 1;
+        const int s = st.slot, bb = tp & 1;
+        mbar_wait(smem_u32(&bar_full[s]), st.phase, g, kWait);
         mbar_wait(smem_u32(&bar_pready[t][bb]), (tp >> 1) & 1, g, kWait);
-        st_pv.next();
+        st.next();
         ++tp;
         __syncwarp();
         tc_fence_after_sync();
 #pragma unroll
         for (int kk = 0; kk < BK / 16; ++kk)
           mma_ts_w(tmem + Gm::o_col(t), tmem + Gm::s_col(t, bb) + kk * 8,
-                   sdesc_add(dVm, 2 * s * Gm::KV_BYTES + kk * 2048), IDESC_PV, (j > 0 || kk > 0) ? 1u : 0u);
-        mma_commit_w(smem_u32(&bar_kvempty[s]));  // S and P V of this stage were its last reads
+                   sdesc_add(dV, s * Gm::KV_BYTES + kk * 2048), IDESC_PV, (j > 0 || kk > 0) ? 1u : 0u);
+        mma_commit_w(smem_u32(&bar_empty[s]));
         mma_commit_w(smem_u32(&bar_odone[t][bb]));
         // S of stage j + 2 goes over P of stage j, which the products above read (issue order)
-        if (j + 2 < n) {
-          issue_s();
-          if (j + 2 == n - 1) mma_commit_w(smem_u32(&bar_qfree));
-        }
+        if (j + 2 < n) issue_s(j + 3 == n);
       }
     }
     // every MMA this warp issued is complete before tensor memory is released
@@ -357,7 +403,7 @@ __global__ void __launch_bounds__(TreeGeom<D, QS, NT>::NUM_THREADS, 1)
     const float sl2 = p.scale_log2;
     // KV heads without a stage (no drafts): their rows see nothing
     for (int x = blockIdx.x; x < p.B * p.Hkv; x += gridDim.x) {
-      if (pre[x / p.Hkv + 1] != pre[x / p.Hkv]) continue;
+      if (tab.pre[x / p.Hkv + 1] != tab.pre[x / p.Hkv]) continue;
       uint4* o = reinterpret_cast<uint4*>(static_cast<typename E::T*>(p.o) + static_cast<size_t>(x) * R * D);
       for (long long i = threadIdx.x; i < static_cast<long long>(R) * (D / 8); i += 128 * NT) o[i] = make_uint4(0, 0, 0, 0);
       for (int i = threadIdx.x; i < R; i += 128 * NT) p.lse[static_cast<size_t>(x) * R + i] = INFINITY;
@@ -367,14 +413,13 @@ __global__ void __launch_bounds__(TreeGeom<D, QS, NT>::NUM_THREADS, 1)
     // may still run, and a single barrier's parity could not tell; k - 2 is
     // complete, S of stage k was issued behind it.)
     auto o_done = [&](int k) { mbar_wait(smem_u32(&bar_odone[t][k & 1]), (k >> 1) & 1, g, kWait); };
-    RingPos<ST> st;
     int ts = 0;  // stages (all segments) so far
     for (; w.more(); w.next()) {
-      int len, tl;
-      tree_lengths(p, w.b, len, tl);
+      const int len = tab.len[w.b], tl = tab.tl[w.b];
+      const int ts0 = ts, n = w.j1 - w.j0;
       const int nd = (tl + BK - 1) / BK;
       float m = -INFINITY, l = 0.f;
-      for (int j = w.j0; j < w.j1; ++j, ++ts, st.next()) {
+      for (int j = w.j0; j < w.j1; ++j, ++ts) {
         const bool draft = j < nd;
         const int k0 = draft ? j * BK : (j - nd) * BK;
         const int valid = min((draft ? tl : len) - k0, BK);  // keys of the stage that exist
@@ -382,12 +427,15 @@ __global__ void __launch_bounds__(TreeGeom<D, QS, NT>::NUM_THREADS, 1)
         uint64_t see = ~0ull;
         if (draft) {
           see = 0ull;
-          if (row < R) {
-            const uint8_t* mrow = p.mask ? p.mask + (static_cast<size_t>(w.b) * p.T + trow) * p.T + k0 + c0 : nullptr;
-#pragma unroll 8
-            for (int i = 0; i < KPW; ++i) {
-              if (c0 + i < valid && (mrow ? mrow[i] != 0 : k0 + c0 + i <= trow)) see |= 1ull << i;
-            }
+          const int most = min(valid - c0, KPW);
+          if (p.mask) {
+            const uint8_t* mrow = p.mask + (static_cast<size_t>(w.b) * p.T + trow) * p.T + k0 + c0;
+#pragma unroll 16
+            for (int i = 0; i < KPW; ++i)
+              if (i < most && mrow[i] != 0) see |= 1ull << i;
+          } else {
+            const int n_see = min(most, trow - (k0 + c0) + 1);
+            see = n_see <= 0 ? 0ull : n_see >= 64 ? ~0ull : (1ull << n_see) - 1ull;
           }
         } else if (valid < BK) {
           const int mine = valid - c0;
@@ -397,9 +445,13 @@ __global__ void __launch_bounds__(TreeGeom<D, QS, NT>::NUM_THREADS, 1)
         const uint32_t s_col = tmem + lanes + Gm::s_col(t, bb);
         mbar_wait(smem_u32(&bar_sfull[t][bb]), (ts >> 1) & 1, g, kWait);
         if (valid < BK) {
-          // V rows of no key: cleared, P = 0 does not hide a NaN there
-          mbar_wait(smem_u32(&bar_kvfull[st.slot]), st.phase, g, kWait);
-          const uint32_t sV = sK0 + 2 * st.slot * Gm::KV_BYTES + Gm::KV_BYTES;
+          // V rows of no key: cleared, P = 0 does not hide a NaN there.  V of
+          // the segment's stage i is tile 2 i + 2 of its ring order, the last one 2 n - 1.
+          const int i = j - w.j0;
+          const int tile = 2 * ts0 + (i == n - 1 ? 2 * n - 1 : 2 * i + 2);
+          const int s = tile % SL;
+          mbar_wait(smem_u32(&bar_full[s]), (tile / SL) & 1, g, kWait);
+          const uint32_t sV = sKV + s * Gm::KV_BYTES;
           const int pieces = (BK - valid) * 8;
           for (int x = threadIdx.x & 127; x < NCH * pieces; x += 128) {
             const int c = x / pieces, y = x - c * pieces;
@@ -548,18 +600,26 @@ __global__ void __launch_bounds__(TreeGeom<D, QS, NT>::NUM_THREADS, 1)
           }
         } else {
           constexpr int W = 32 / QS;  // columns per thread once merged
-          const int slotrow = kq * Gm::QROWS + lrow;
           const bool drop = empty || f == 0.f;
+          const uint32_t mine = sX + (kq * Gm::QROWS + lrow) * (Gm::XCH_PITCH * 4);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) xch[slotrow * 33 + i] = drop ? 0.f : __uint_as_float(rr[i]) * inv;
+          for (int i = 0; i < 32; ++i) rr[i] = drop ? 0u : __float_as_uint(__uint_as_float(rr[i]) * inv);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) st_shared_v4(mine + i * 16, rr[4 * i], rr[4 * i + 1], rr[4 * i + 2], rr[4 * i + 3]);
           named_bar_sync(1 + t, 128);
           float acc[W];
 #pragma unroll
-          for (int i = 0; i < W; ++i) {
-            acc[i] = 0.f;
+          for (int i = 0; i < W; ++i) acc[i] = 0.f;
 #pragma unroll
-            for (int k = 0; k < QS; ++k) acc[i] += xch[(k * Gm::QROWS + lrow) * 33 + kq * W + i];
-          }
+          for (int k = 0; k < QS; ++k)
+#pragma unroll
+            for (int i = 0; i < W / 4; ++i) {
+              const uint4 x = ld_shared_v4(sX + (k * Gm::QROWS + lrow) * (Gm::XCH_PITCH * 4) + kq * W * 4 + i * 16);
+              acc[4 * i] += __uint_as_float(x.x);
+              acc[4 * i + 1] += __uint_as_float(x.y);
+              acc[4 * i + 2] += __uint_as_float(x.z);
+              acc[4 * i + 3] += __uint_as_float(x.w);
+            }
           if (row < R) {
             if (whole) {
               uint4* d = reinterpret_cast<uint4*>(orow + c * 32 + kq * W);
@@ -589,75 +649,83 @@ __global__ void __launch_bounds__(TreeGeom<D, QS, NT>::NUM_THREADS, 1)
   }
 }
 
-// Merges the partials of the KV heads that more than one CTA worked on.  A
-// head is cut at the range boundaries inside it; block (x, y) takes the head
-// whose first cut is the start of group x + 1, rows 8 / WPR * y and on, WPR
-// warps per row.  With partial lse L_s and O_s: M = max L_s, w_s = 2^(L_s - M),
-// O = sum w_s O_s / sum w_s, lse = M + log2 sum w_s, partials in order.
+// Merges the partials of the KV heads that more than one CTA worked on.  With
+// partial lse L_s and O_s: M = max L_s, w_s = 2^(L_s - M), O = sum w_s O_s /
+// sum w_s, lse = M + log2 sum w_s, partials in order.  WPR warps per row share
+// its partials out.  One wave of blocks, launched as a programmatic dependent:
+// they derive the division while the attention kernel runs, then walk the
+// (head, 8 / WPR rows) tasks.
 template <int D, bool BF16, int WPR>
 __global__ void __launch_bounds__(256) attn_tree_combine_kernel(const TreeParams p, int rows) {
   using E = Elem<BF16>;
-  constexpr int PER = D / 32;
-  __shared__ int pre[kTreeMaxB + 1];
+  constexpr int PER = D / 32, RPB = 8 / WPR;  // columns per lane, rows per block
+  __shared__ TreeTable tab;
   __shared__ float sden[8], so[8][D];
-  tree_prefix(p, pre);
+  tree_table(p, tab);
+  __syncthreads();
+  const int* pre = tab.pre;
   const int total = pre[p.B] * p.Hkv, per = tree_per(total, p.n_groups);
-  const long long cut = (static_cast<long long>(blockIdx.x) + 1) * per;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int sub = warp % WPR;
-  const int row = static_cast<int>(blockIdx.y) * (8 / WPR) + warp / WPR;
-  bool mine = cut < total && row < p.G * p.T;
-  int s = 0, e = 0, b = 0, hk = 0;
-  if (cut < total) {
-    b = tree_find(pre, p.B, p.Hkv, static_cast<int>(cut));
-    const int n = pre[b + 1] - pre[b];
-    hk = (static_cast<int>(cut) - pre[b] * p.Hkv) / n;
-    s = pre[b] * p.Hkv + hk * n;
-    e = s + n;
-    // cut lies inside the head and is the first cut that does
-    mine = mine && s < cut && cut - per <= s;
-  }
+  const int R = p.G * p.T, chunks = (R + RPB - 1) / RPB;
+  const long long tasks = static_cast<long long>(p.B) * p.Hkv * chunks;
   grid_dependency_wait();  // the partials are written (and the whole call ends behind them)
-  float den = 0.f, M = -INFINITY, acc[PER];
-#pragma unroll
-  for (int c = 0; c < PER; ++c) acc[c] = 0.f;
-  const int g0 = s / per, ng = mine ? (e - 1) / per - g0 + 1 : 0;
-  const int rb = row / rows, lrow = row - rb * rows;
-  auto part_row = [&](int i) {
+  for (long long task = blockIdx.x; task < tasks; task += gridDim.x) {
+    const int head = static_cast<int>(task / chunks);
+    const int row = static_cast<int>(task - static_cast<long long>(head) * chunks) * RPB + warp / WPR;
+    const int b = head / p.Hkv, hk = head - b * p.Hkv;
+    const int n = pre[b + 1] - pre[b];
+    const int s = pre[b] * p.Hkv + hk * n;
+    const int g0 = s / per, ng = n > 0 ? (s + n - 1) / per - g0 + 1 : 0;
+    if (ng < 2) continue;  // written by its CTA (the same for the whole block)
+    const bool mine = row < R;
+    const int rb = row / rows, lrow = row - rb * rows;
     // the head's first partial is its group's second one, unless the head starts the group's range
-    return tree_slot_row(p, g0 + i, i == 0 && s != g0 * per ? 1 : 0, rb, rows) + lrow;
-  };
-  for (int i = lane; i < ng; i += 32) M = fmaxf(M, p.part_lse[part_row(i)]);
+    const int first = s != g0 * per ? 1 : 0;
+    auto part_row = [&](int i) { return tree_slot_row(p, g0 + i, i == 0 ? first : 0, rb, rows) + lrow; };
+    float den = 0.f, M = -INFINITY, acc[PER];
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+    for (int c = 0; c < PER; ++c) acc[c] = 0.f;
+    if (mine) {
+      for (int i = lane; i < ng; i += 32) M = fmaxf(M, p.part_lse[part_row(i)]);
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
 #pragma unroll 4
-  for (int i = sub; i < ng; i += WPR) {
-    const size_t r = part_row(i);
-    const float L = p.part_lse[r];
-    const float wgt = L == -INFINITY ? 0.f : exp2f(L - M);
-    den += wgt;
+      for (int i = sub; i < ng; i += WPR) {
+        const size_t r = part_row(i);
+        const float L = p.part_lse[r];
+        float x[PER];
 #pragma unroll
-    for (int c = 0; c < PER; ++c) acc[c] = fmaf(wgt, p.part[r * D + lane + 32 * c], acc[c]);
-  }
-  if constexpr (WPR > 1) {
-    if (lane == 0) sden[warp] = den;
+        for (int c = 0; c < PER; ++c) x[c] = p.part[r * D + lane + 32 * c];
+        const float wgt = L == -INFINITY ? 0.f : exp2f(L - M);
+        den += wgt;
 #pragma unroll
-    for (int c = 0; c < PER; ++c) so[warp][lane + 32 * c] = acc[c];
-    __syncthreads();
-    if (sub != 0) return;
-    for (int k = 1; k < WPR; ++k) {
-      den += sden[warp + k];
-#pragma unroll
-      for (int c = 0; c < PER; ++c) acc[c] += so[warp + k][lane + 32 * c];
+        for (int c = 0; c < PER; ++c) acc[c] = fmaf(wgt, x[c], acc[c]);
+      }
     }
-  }
-  if (!mine) return;
-  const size_t grow = (static_cast<size_t>(b) * p.Hkv + hk) * (p.G * p.T) + row;
-  const bool empty = den == 0.f;
-  typename E::T* o = static_cast<typename E::T*>(p.o) + grow * D;
+    if constexpr (WPR > 1) {
+      if (lane == 0) sden[warp] = den;
 #pragma unroll
-  for (int c = 0; c < PER; ++c) o[lane + 32 * c] = E::from_float(empty ? 0.f : acc[c] / den);
-  if (lane == 0) p.lse[grow] = empty ? INFINITY : M + log2f(den);
+      for (int c = 0; c < PER; ++c) so[warp][lane + 32 * c] = acc[c];
+      __syncthreads();
+      if (sub == 0) {
+        for (int k = 1; k < WPR; ++k) {
+          den += sden[warp + k];
+#pragma unroll
+          for (int c = 0; c < PER; ++c) acc[c] += so[warp + k][lane + 32 * c];
+        }
+      }
+    }
+    if (mine && sub == 0) {
+      const size_t grow = static_cast<size_t>(head) * R + row;
+      const bool empty = den == 0.f;
+      typename E::T* o = static_cast<typename E::T*>(p.o) + grow * D;
+#pragma unroll
+      for (int c = 0; c < PER; ++c) o[lane + 32 * c] = E::from_float(empty ? 0.f : acc[c] / den);
+      if (lane == 0) p.lse[grow] = empty ? INFINITY : M + log2f(den);
+    }
+    if constexpr (WPR > 1) __syncthreads();  // before the next task's partial sums
+  }
 }
 
 }  // namespace gbattn
