@@ -65,16 +65,16 @@ int tree_impl(const TreeParams& p, EncodeTiledFn enc, cudaStream_t stream) {
   kern<<<p.n_groups * p.n_rb, Gm::NUM_THREADS, Gm::SMEM_BYTES, stream>>>(tq, tk, tv, tkn, tvn, p);
   if (cudaPeekAtLastError() != cudaSuccess) return kLaunchCudaError;
   if (p.n_groups == 1) return kLaunchOk;  // no KV head is shared
-  // warps per row by how many partials a head has on average
+  // warps per 4 columns by how many partials a head has on average
   const long long avg = p.n_groups / heads + 1;
-  auto combine = [&](auto kern_c, int rows_per_block) {
-    const long long tasks = heads * ((R + rows_per_block - 1) / rows_per_block);
+  auto combine = [&](auto kern_c, int cols_per_block) {
+    const long long tasks = heads * ((R + 31) / 32) * (kD / cols_per_block);
     const long long most = 4LL * kTreeMaxCtas;  // resident beside the attention kernel's CTAs
     return launch_dependent(kern_c, dim3(static_cast<unsigned>(tasks < most ? tasks : most)), 256, stream, p, Gm::ROWS);
   };
-  if (avg > 8) return combine(attn_tree_combine_kernel<kD, BF16, 8>, 1);
-  if (avg > 3) return combine(attn_tree_combine_kernel<kD, BF16, 2>, 4);
-  return combine(attn_tree_combine_kernel<kD, BF16, 1>, 8);
+  if (avg > 8) return combine(attn_tree_combine_kernel<kD, BF16, 8>, 4);
+  if (avg > 3) return combine(attn_tree_combine_kernel<kD, BF16, 2>, 16);
+  return combine(attn_tree_combine_kernel<kD, BF16, 1>, 32);
 }
 
 template <bool BF16>

@@ -192,8 +192,10 @@ struct TreeWalk {
   __device__ __forceinline__ int slot() const { return x == lo ? 0 : 1; }
 };
 
-// First fp32 partial row of (group, slot, row block): slot 0 holds the segment
-// at the start of the group's range, slot 1 the one cut off by its end.
+// First partial row of (group, slot, row block): slot 0 holds the segment at
+// the start of the group's range, slot 1 the one cut off by its end.  Its lse
+// are consecutive; its O is kept for 32 rows at a time, as [D / 4][32 rows][4],
+// so a warp whose lanes are rows stores and loads 512 consecutive bytes.
 __device__ __forceinline__ size_t tree_slot_row(const TreeParams& p, int group, int slot, int rb, int rows) {
   return ((static_cast<size_t>(group) * 2 + slot) * p.n_rb + rb) * rows;
 }
@@ -429,10 +431,21 @@ __global__ void __launch_bounds__(TreeGeom<D, QS, NT>::NUM_THREADS, 1)
           see = 0ull;
           const int most = min(valid - c0, KPW);
           if (p.mask) {
-            const uint8_t* mrow = p.mask + (static_cast<size_t>(w.b) * p.T + trow) * p.T + k0 + c0;
+            // the warp reads 32 / KPW (at least one) mask rows at a time, a byte
+            // per lane, and every lane keeps the bits of its own row
+            const uint8_t* mb = p.mask + static_cast<size_t>(w.b) * p.T * p.T + k0 + c0;
+            constexpr int STEP = KPW < 32 ? KPW : 32, AT_ONCE = 32 / STEP;
 #pragma unroll 16
-            for (int i = 0; i < KPW; ++i)
-              if (i < most && mrow[i] != 0) see |= 1ull << i;
+            for (int i = 0; i < 32; i += AT_ONCE) {
+              const int mt = __shfl_sync(0xffffffffu, trow, i + lane / STEP);
+#pragma unroll
+              for (int h = 0; h < KPW; h += STEP) {
+                const int u = h + lane % STEP;
+                const uint32_t bits = __ballot_sync(0xffffffffu, u < most && mb[static_cast<size_t>(mt) * p.T + u] != 0);
+                if (lane / AT_ONCE == i / AT_ONCE)
+                  see |= static_cast<uint64_t>(STEP == 32 ? bits : (bits >> ((lane % AT_ONCE) * STEP)) & ((1u << (STEP & 31)) - 1u)) << h;
+              }
+            }
           } else {
             const int n_see = min(most, trow - (k0 + c0) + 1);
             see = n_see <= 0 ? 0ull : n_see >= 64 ? ~0ull : (1ull << n_see) - 1ull;
@@ -583,7 +596,7 @@ __global__ void __launch_bounds__(TreeGeom<D, QS, NT>::NUM_THREADS, 1)
         else p.part_lse[prow] = empty ? -INFINITY : lse;
       }
       typename E::T* orow = static_cast<typename E::T*>(p.o) + grow * D;
-      float* partrow = p.part + prow * D;
+      float* prt = p.part + (prow - lrow % 32) * D + (lrow % 32) * 4;  // 4 columns every 128 floats
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
         uint32_t rr[32];
@@ -595,8 +608,14 @@ __global__ void __launch_bounds__(TreeGeom<D, QS, NT>::NUM_THREADS, 1)
             for (int i = 0; i < 32; ++i) rr[i] = 0u;
           }
           if (row < R) {
-            if (whole) store_row32<BF16>(orow + c * 32, rr, empty ? 1.f : inv);
-            else store_row32_f32(partrow + c * 32, rr, empty ? 1.f : inv);
+            const float mul = empty ? 1.f : inv;
+            if (whole) store_row32<BF16>(orow + c * 32, rr, mul);
+            else
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                *reinterpret_cast<float4*>(prt + (c * 8 + i) * 128) =
+                    make_float4(__uint_as_float(rr[4 * i]) * mul, __uint_as_float(rr[4 * i + 1]) * mul,
+                                __uint_as_float(rr[4 * i + 2]) * mul, __uint_as_float(rr[4 * i + 3]) * mul);
           }
         } else {
           constexpr int W = 32 / QS;  // columns per thread once merged
@@ -628,9 +647,10 @@ __global__ void __launch_bounds__(TreeGeom<D, QS, NT>::NUM_THREADS, 1)
                 d[i] = make_uint4(E::pack(acc[8 * i], acc[8 * i + 1]), E::pack(acc[8 * i + 2], acc[8 * i + 3]),
                                   E::pack(acc[8 * i + 4], acc[8 * i + 5]), E::pack(acc[8 * i + 6], acc[8 * i + 7]));
             } else {
-              float4* d = reinterpret_cast<float4*>(partrow + c * 32 + kq * W);
 #pragma unroll
-              for (int i = 0; i < W / 4; ++i) d[i] = make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
+              for (int i = 0; i < W / 4; ++i)
+                *reinterpret_cast<float4*>(prt + (c * 8 + kq * (W / 4) + i) * 128) =
+                    make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
             }
           }
           named_bar_sync(1 + t, 128);
@@ -651,80 +671,80 @@ __global__ void __launch_bounds__(TreeGeom<D, QS, NT>::NUM_THREADS, 1)
 
 // Merges the partials of the KV heads that more than one CTA worked on.  With
 // partial lse L_s and O_s: M = max L_s, w_s = 2^(L_s - M), O = sum w_s O_s /
-// sum w_s, lse = M + log2 sum w_s, partials in order.  WPR warps per row share
-// its partials out.  One wave of blocks, launched as a programmatic dependent:
-// they derive the division while the attention kernel runs, then walk the
-// (head, 8 / WPR rows) tasks.
-template <int D, bool BF16, int WPR>
+// sum w_s, lse = M + log2 sum w_s.  Lane = row, 4 columns per thread; NS warps
+// share a head's partials out and are merged, in order, by the same rule.
+// One wave of blocks, launched as a programmatic dependent: they derive the
+// division while the attention kernel runs, then walk the (head, 32 rows,
+// 32 / NS columns) tasks.
+template <int D, bool BF16, int NS>
 __global__ void __launch_bounds__(256) attn_tree_combine_kernel(const TreeParams p, int rows) {
   using E = Elem<BF16>;
-  constexpr int PER = D / 32, RPB = 8 / WPR;  // columns per lane, rows per block
+  constexpr int QPB = 8 / NS, QB = D / 4 / QPB;  // column quads per block, blocks per row group
   __shared__ TreeTable tab;
-  __shared__ float sden[8], so[8][D];
+  __shared__ float sM[8][32], sden[8][32];
+  __shared__ float4 so[8][32];
   tree_table(p, tab);
   __syncthreads();
   const int* pre = tab.pre;
   const int total = pre[p.B] * p.Hkv, per = tree_per(total, p.n_groups);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int sub = warp % WPR;
-  const int R = p.G * p.T, chunks = (R + RPB - 1) / RPB;
-  const long long tasks = static_cast<long long>(p.B) * p.Hkv * chunks;
+  const int sub = warp % NS;
+  const int R = p.G * p.T, rgs = (R + 31) / 32;
+  const long long tasks = static_cast<long long>(p.B) * p.Hkv * rgs * QB;
   grid_dependency_wait();  // the partials are written (and the whole call ends behind them)
   for (long long task = blockIdx.x; task < tasks; task += gridDim.x) {
-    const int head = static_cast<int>(task / chunks);
-    const int row = static_cast<int>(task - static_cast<long long>(head) * chunks) * RPB + warp / WPR;
+    const int head = static_cast<int>(task / (rgs * QB)), rest = static_cast<int>(task % (rgs * QB));
+    const int rg = rest / QB, q = (rest - rg * QB) * QPB + warp / NS;
     const int b = head / p.Hkv, hk = head - b * p.Hkv;
     const int n = pre[b + 1] - pre[b];
     const int s = pre[b] * p.Hkv + hk * n;
     const int g0 = s / per, ng = n > 0 ? (s + n - 1) / per - g0 + 1 : 0;
     if (ng < 2) continue;  // written by its CTA (the same for the whole block)
-    const bool mine = row < R;
-    const int rb = row / rows, lrow = row - rb * rows;
+    const int row = rg * 32 + lane, rb = rg * 32 / rows, r0 = rg * 32 - rb * rows;
     // the head's first partial is its group's second one, unless the head starts the group's range
     const int first = s != g0 * per ? 1 : 0;
-    auto part_row = [&](int i) { return tree_slot_row(p, g0 + i, i == 0 ? first : 0, rb, rows) + lrow; };
-    float den = 0.f, M = -INFINITY, acc[PER];
-#pragma unroll
-    for (int c = 0; c < PER; ++c) acc[c] = 0.f;
-    if (mine) {
-      for (int i = lane; i < ng; i += 32) M = fmaxf(M, p.part_lse[part_row(i)]);
-#pragma unroll
-      for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+    auto part_row = [&](int i) { return tree_slot_row(p, g0 + i, i == 0 ? first : 0, rb, rows) + r0; };
+    float M = -INFINITY, den = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (row < R) {
 #pragma unroll 4
-      for (int i = sub; i < ng; i += WPR) {
+      for (int i = sub; i < ng; i += NS) M = fmaxf(M, p.part_lse[part_row(i) + lane]);
+#pragma unroll 4
+      for (int i = sub; i < ng; i += NS) {
         const size_t r = part_row(i);
-        const float L = p.part_lse[r];
-        float x[PER];
-#pragma unroll
-        for (int c = 0; c < PER; ++c) x[c] = p.part[r * D + lane + 32 * c];
+        const float L = p.part_lse[r + lane];
+        const float4 x = *reinterpret_cast<const float4*>(p.part + r * D + q * 128 + lane * 4);
         const float wgt = L == -INFINITY ? 0.f : exp2f(L - M);
         den += wgt;
-#pragma unroll
-        for (int c = 0; c < PER; ++c) acc[c] = fmaf(wgt, x[c], acc[c]);
+        acc.x = fmaf(wgt, x.x, acc.x), acc.y = fmaf(wgt, x.y, acc.y);
+        acc.z = fmaf(wgt, x.z, acc.z), acc.w = fmaf(wgt, x.w, acc.w);
       }
     }
-    if constexpr (WPR > 1) {
-      if (lane == 0) sden[warp] = den;
-#pragma unroll
-      for (int c = 0; c < PER; ++c) so[warp][lane + 32 * c] = acc[c];
+    if constexpr (NS > 1) {
+      sM[warp][lane] = M, sden[warp][lane] = den, so[warp][lane] = acc;
       __syncthreads();
       if (sub == 0) {
-        for (int k = 1; k < WPR; ++k) {
-          den += sden[warp + k];
-#pragma unroll
-          for (int c = 0; c < PER; ++c) acc[c] += so[warp + k][lane + 32 * c];
+        for (int k = 1; k < NS; ++k) M = fmaxf(M, sM[warp + k][lane]);
+        den = 0.f, acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k = 0; k < NS; ++k) {
+          const float d = sden[warp + k][lane];
+          const float wgt = d == 0.f ? 0.f : exp2f(sM[warp + k][lane] - M);
+          const float4 x = so[warp + k][lane];
+          den = fmaf(wgt, d, den);
+          acc.x = fmaf(wgt, x.x, acc.x), acc.y = fmaf(wgt, x.y, acc.y);
+          acc.z = fmaf(wgt, x.z, acc.z), acc.w = fmaf(wgt, x.w, acc.w);
         }
       }
     }
-    if (mine && sub == 0) {
+    if (row < R && sub == 0) {
       const size_t grow = static_cast<size_t>(head) * R + row;
-      const bool empty = den == 0.f;
-      typename E::T* o = static_cast<typename E::T*>(p.o) + grow * D;
-#pragma unroll
-      for (int c = 0; c < PER; ++c) o[lane + 32 * c] = E::from_float(empty ? 0.f : acc[c] / den);
-      if (lane == 0) p.lse[grow] = empty ? INFINITY : M + log2f(den);
+      const float inv = den == 0.f ? 0.f : 1.f / den;
+      uint2 o;
+      o.x = E::pack(acc.x * inv, acc.y * inv), o.y = E::pack(acc.z * inv, acc.w * inv);
+      *reinterpret_cast<uint2*>(static_cast<typename E::T*>(p.o) + grow * D + q * 4) = o;
+      if (q == 0) p.lse[grow] = den == 0.f ? INFINITY : M + log2f(den);
     }
-    if constexpr (WPR > 1) __syncthreads();  // before the next task's partial sums
+    if constexpr (NS > 1) __syncthreads();  // before the next task's values
   }
 }
 
