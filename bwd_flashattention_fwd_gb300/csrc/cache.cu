@@ -7,7 +7,6 @@
 #include "../../include/gbattn.h"
 #include "cache.h"
 #include "cache_kernel.cuh"
-#include "key_weight_kernel.cuh"
 
 namespace gbattn {
 namespace {
@@ -67,15 +66,6 @@ attn_status_t finish(int r) {
   return r == kLaunchOk ? ATTN_OK : r == kLaunchBadMap ? ATTN_ERR_INVALID_ARG : ATTN_ERR_CUDA;
 }
 
-template <int D, bool BF16>
-attn_status_t launch_key_weight(const KeyWeightParams& p, cudaStream_t stream) {
-  constexpr int smem = D * kKeyWeightKeys * 4;
-  auto kern = attn_key_weight_kernel<D, BF16>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return ATTN_ERR_CUDA;
-  kern<<<dim3((p.Lk + kKeyWeightKeys - 1) / kKeyWeightKeys, p.B * p.Hkv), kKeyWeightKeys, smem, stream>>>(p);
-  return launched();
-}
-
 }  // namespace
 }  // namespace gbattn
 
@@ -125,7 +115,10 @@ extern "C" attn_status_t attn_fwd_tree(const void* q, const void* k, const void*
 }
 
 extern "C" size_t attn_key_weight_workspace_bytes(int B, int Hq, int Hkv, int Lq, int Lk, int D) {
-  return check_key_weight(B, Hq, Hkv, Lq, Lk, D) == ATTN_OK ? 16 : 0;
+  if (check_key_weight(B, Hq, Hkv, Lq, Lk, D) != ATTN_OK) return 0;
+  // two sets of partial sums per CTA where the rows do not fit shared memory together
+  if (static_cast<long long>(Hq / Hkv) * Lq <= kKeyWeightFewRows) return 16;
+  return static_cast<size_t>(kTreeMaxCtas) * 2 * 256 * sizeof(float);
 }
 
 extern "C" attn_status_t attn_key_weight(const void* q, const void* k, const float* lse, const int32_t* limit,
@@ -147,20 +140,27 @@ extern "C" attn_status_t attn_key_weight(const void* q, const void* k, const flo
   if (causal && (limit || Lq > Lk)) return ATTN_ERR_INVALID_ARG;
   if (c != ATTN_OK) return c;
   if (s != ATTN_OK) return s;
-  if (limit && Lq > kTreeMaxT) return ATTN_ERR_UNSUPPORTED;
+  if (limit && (Lq > kTreeMaxT || B > kTreeMaxB)) return ATTN_ERR_UNSUPPORTED;
   if (workspace_bytes < attn_key_weight_workspace_bytes(B, Hq, Hkv, Lq, Lk, D)) return ATTN_ERR_INVALID_ARG;
   int dev, num_sms, *status;
   EncodeTiledFn enc;
   const attn_status_t ds = shared_device_state(&dev, &enc, &status, &num_sms);
   if (ds != ATTN_OK) return ds;
-  KeyWeightParams p{q, k, lse, limit, weight, weight_out, kv_pitch ? kv_pitch : Lk, B, Hq, Hkv, Hq / Hkv, Lq, Lk,
-                    causal, scale_log2_of(scale), status, shared_wait_limit_ns()};
-  const bool bf = dtype == ATTN_DTYPE_BF16;
+  KeyWeightParams p{};
+  p.q = q, p.k = k, p.lse = lse, p.limit = limit, p.weight = weight, p.weight_out = weight_out;
+  p.part = static_cast<float*>(workspace);
+  p.kv_pitch = kv_pitch ? kv_pitch : Lk;
+  p.B = B, p.Hq = Hq, p.Hkv = Hkv, p.G = Hq / Hkv, p.Lq = Lq, p.Lk = Lk, p.causal = causal;
+  // a list per query head lets causal calls leave out the row tiles above the
+  // diagonal; short or individually limited rows fill tiles better packed
+  p.packed = limit || Lq < 64;
+  p.scale_log2 = scale_log2_of(scale), p.status = status, p.limit_ns = shared_wait_limit_ns();
+  const bool bf16 = dtype == ATTN_DTYPE_BF16;
   switch (D) {
-    case 64: return bf ? launch_key_weight<64, true>(p, stream) : launch_key_weight<64, false>(p, stream);
-    case 96: return bf ? launch_key_weight<96, true>(p, stream) : launch_key_weight<96, false>(p, stream);
-    case 128: return bf ? launch_key_weight<128, true>(p, stream) : launch_key_weight<128, false>(p, stream);
-    default: return bf ? launch_key_weight<256, true>(p, stream) : launch_key_weight<256, false>(p, stream);
+    case 64: return finish(launch_key_weight_d64(p, bf16, num_sms, enc, stream));
+    case 96: return finish(launch_key_weight_d96(p, bf16, num_sms, enc, stream));
+    case 128: return finish(launch_key_weight_d128(p, bf16, num_sms, enc, stream));
+    default: return finish(launch_key_weight_d256(p, bf16, num_sms, enc, stream));
   }
 }
 

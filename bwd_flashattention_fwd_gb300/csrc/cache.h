@@ -63,7 +63,12 @@ struct KeyWeightParams {
   float scale_log2;
   int* status;
   uint64_t limit_ns;
+  int packed;   // many rows: the G x Lq rows of a KV head form one list (else a list per query head)
+  float* part;  // many rows: [CTAs][2][256] partial sums
 };
+
+// G * Lq rows up to which a KV head's rows stay in shared memory together.
+constexpr int kKeyWeightFewRows = 128;
 
 struct AppendParams {
   const void *k_new, *v_new;
@@ -88,8 +93,9 @@ struct EvictParams {
 };
 
 // Launchers of one head dimension (cache_inst.cu); LaunchResult codes.
-#define GBATTN_DECLARE_CACHE_LAUNCHERS(DIM)                                                     \
-  int launch_tree_d##DIM(const TreeParams& p, bool bf16, int num_sms, EncodeTiledFn enc, cudaStream_t stream);
+#define GBATTN_DECLARE_CACHE_LAUNCHERS(DIM)                                                                   \
+  int launch_tree_d##DIM(const TreeParams& p, bool bf16, int num_sms, EncodeTiledFn enc, cudaStream_t stream);      \
+  int launch_key_weight_d##DIM(const KeyWeightParams& p, bool bf16, int num_sms, EncodeTiledFn enc, cudaStream_t stream);
 
 GBATTN_DECLARE_CACHE_LAUNCHERS(64)
 GBATTN_DECLARE_CACHE_LAUNCHERS(96)

@@ -1,6 +1,7 @@
 // Instantiations and launchers of the cache kernels for one head dimension
 // (compiled once per supported D with -DGBATTN_HEAD_DIM=<D>, like inst.cu).
 #include "cache.h"
+#include "key_weight_kernel.cuh"
 #include "tree_kernel.cuh"
 
 #ifndef GBATTN_HEAD_DIM
@@ -87,6 +88,51 @@ int tree_dispatch(const TreeParams& p, const TreePlan& plan, EncodeTiledFn enc, 
   return tree_impl<BF16, 1, 1>(p, enc, stream);
 }
 
+template <bool BF16, int NQ>
+int key_weight_few(const KeyWeightParams& p, int num_sms, EncodeTiledFn enc, cudaStream_t stream) {
+  using Gm = KeyWeightFewGeom<kD, NQ>;
+  const long long R = static_cast<long long>(p.G) * p.Lq, heads = static_cast<long long>(p.B) * p.Hkv;
+  CUtensorMap tq, tk;
+  if (!make_map(enc, BF16, &tq, p.q, R, heads, NQ, R) || !make_map(enc, BF16, &tk, p.k, p.Lk, heads, Gm::BK, p.kv_pitch))
+    return kLaunchBadMap;
+  auto kern = attn_key_weight_few_kernel<kD, BF16, NQ>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Gm::SMEM_BYTES) != cudaSuccess)
+    return kLaunchCudaError;
+  const long long tiles = heads * ((p.Lk + Gm::BK - 1) / Gm::BK);
+  kern<<<static_cast<unsigned>(tiles < num_sms ? tiles : num_sms), Gm::NUM_THREADS, Gm::SMEM_BYTES, stream>>>(tq, tk, p);
+  return cudaPeekAtLastError() == cudaSuccess ? kLaunchOk : kLaunchCudaError;
+}
+
+template <bool BF16>
+int key_weight_many(const KeyWeightParams& p, int num_sms, EncodeTiledFn enc, cudaStream_t stream) {
+  using Gm = KeyWeightGeom<kD>;
+  const long long heads = static_cast<long long>(p.B) * p.Hkv;
+  const long long rows = p.packed ? static_cast<long long>(p.G) * p.Lq : p.Lq;
+  CUtensorMap tq, tk;
+  if (!make_map(enc, BF16, &tq, p.q, rows, p.packed ? heads : heads * p.G, Gm::NQ, rows) ||
+      !make_map(enc, BF16, &tk, p.k, p.Lk, heads, 128, p.kv_pitch))
+    return kLaunchBadMap;
+  auto kern = attn_key_weight_kernel<kD, BF16>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Gm::SMEM_BYTES) != cudaSuccess)
+    return kLaunchCudaError;
+  const int groups = num_sms < kTreeMaxCtas ? num_sms : kTreeMaxCtas;
+  kern<<<groups, Gm::NUM_THREADS, Gm::SMEM_BYTES, stream>>>(tq, tk, p);
+  if (cudaPeekAtLastError() != cudaSuccess) return kLaunchCudaError;
+  const long long tiles = heads * ((p.Lk + Gm::BK - 1) / Gm::BK), most = 4LL * kTreeMaxCtas;
+  return launch_dependent(attn_key_weight_join_kernel, dim3(static_cast<unsigned>(tiles < most ? tiles : most)), 256,
+                          stream, p, groups);
+}
+
+template <bool BF16>
+int key_weight_dispatch(const KeyWeightParams& p, int num_sms, EncodeTiledFn enc, cudaStream_t stream) {
+  const long long R = static_cast<long long>(p.G) * p.Lq;
+  if (R <= 16) return key_weight_few<BF16, 16>(p, num_sms, enc, stream);
+  if (R <= 32) return key_weight_few<BF16, 32>(p, num_sms, enc, stream);
+  if (R <= 64) return key_weight_few<BF16, 64>(p, num_sms, enc, stream);
+  if (R <= kKeyWeightFewRows) return key_weight_few<BF16, 128>(p, num_sms, enc, stream);
+  return key_weight_many<BF16>(p, num_sms, enc, stream);
+}
+
 }  // namespace GBATTN_CAT(cache_d, GBATTN_HEAD_DIM)
 
 using namespace GBATTN_CAT(cache_d, GBATTN_HEAD_DIM);
@@ -98,6 +144,11 @@ int GBATTN_CAT(launch_tree_d, GBATTN_HEAD_DIM)(const TreeParams& p0, bool bf16, 
   p.n_rb = plan.n_rb, p.n_groups = plan.n_groups;
   p.part_lse = p.part + static_cast<size_t>(plan.n_groups) * 2 * plan.n_rb * plan.rows * kD;
   return bf16 ? tree_dispatch<true>(p, plan, enc, stream) : tree_dispatch<false>(p, plan, enc, stream);
+}
+
+int GBATTN_CAT(launch_key_weight_d, GBATTN_HEAD_DIM)(const KeyWeightParams& p, bool bf16, int num_sms,
+                                                     EncodeTiledFn enc, cudaStream_t stream) {
+  return bf16 ? key_weight_dispatch<true>(p, num_sms, enc, stream) : key_weight_dispatch<false>(p, num_sms, enc, stream);
 }
 
 }  // namespace gbattn

@@ -130,7 +130,8 @@ def _dtype_code(t: torch.Tensor) -> int:
 
 def _stream_handle(stream) -> int:
     if stream is None:
-        stream = torch.cuda.current_stream()
+        # the current stream's handle without building a Stream object for it
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -146,26 +147,29 @@ def _require(call: str, dense=(), sliced=(), f32=(), u8=(), i32=()):
     float32 / uint8 / int32 tensors.  Every tensor must be on the current CUDA
     device.  None entries are skipped."""
     half = None
-    dev = None
+    dev = -1
     groups = ((dense, None, True), (sliced, None, False), (f32, torch.float32, True), (u8, torch.uint8, True),
               (i32, torch.int32, True))
     for ts, want, contig in groups:
         for t in ts:
             if t is None:
                 continue
-            if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
+            if not isinstance(t, torch.Tensor) or not t.is_cuda:
                 raise ValueError(f"{call}: every tensor must be a CUDA tensor; got {getattr(t, 'device', type(t))}")
-            dev = torch.cuda.current_device() if dev is None else dev
-            if t.device.index != dev:
+            if dev < 0:
+                dev = torch.cuda.current_device()
+            if t.get_device() != dev:
                 raise ValueError(f"{call}: every tensor must be on the current CUDA device (cuda:{dev}); got {t.device}")
             if contig and not t.is_contiguous():
                 raise ValueError(f"{call}: tensor of shape {tuple(t.shape)} strides {t.stride()} is not contiguous")
+            dt = t.dtype
             if want is None:
-                half = half or t.dtype
-                if t.dtype not in (torch.bfloat16, torch.float16) or t.dtype != half:
-                    raise TypeError(f"{call}: 16-bit tensors must all be bfloat16 or all float16; got {t.dtype}")
-            elif t.dtype != want:
-                raise TypeError(f"{call}: expected {want}, got {t.dtype}")
+                if half is None:
+                    half = dt
+                if dt is not half or (dt is not torch.bfloat16 and dt is not torch.float16):
+                    raise TypeError(f"{call}: 16-bit tensors must all be bfloat16 or all float16; got {dt}")
+            elif dt is not want:
+                raise TypeError(f"{call}: expected {want}, got {dt}")
 
 
 def _check(status: int, call: str, check: bool) -> int:
@@ -378,10 +382,11 @@ def lce_bwd(hidden, weight, targets, lse, dloss, dhidden, dweight, workspace, st
     return _check(st, "lce_bwd", check)
 
 
-def _shape(call: str, t, want, name: str):
-    """Reject a tensor (or None) whose shape is not the one the call reads."""
-    if t is not None and tuple(t.shape) != tuple(want):
-        raise ValueError(f"{call}: {name} has shape {tuple(t.shape)}; expected {tuple(want)}")
+def _shapes(call: str, *named) -> None:
+    """Reject (tensor or None, wanted shape, name) triples whose shapes differ from what the call reads."""
+    for t, want, name in named:
+        if t is not None and t.shape != want:
+            raise ValueError(f"{call}: {name} has shape {tuple(t.shape)}; expected {tuple(want)}")
 
 
 def attn_tree_workspace_bytes(B: int, Hq: int, Hkv: int, T: int, Lk: int, D: int) -> int:
@@ -412,11 +417,10 @@ def attn_fwd_tree(q, k, v, k_new, v_new, cache_len, o, lse, workspace, scale: fl
              i32=(cache_len, tree_len))
     B, Hq, T, D = q.shape
     Hkv, Lk = k.shape[1], k.shape[2]
-    for t, want, name in ((k, (B, Hkv, Lk, D), "k"), (v, (B, Hkv, Lk, D), "v"), (k_new, (B, Hkv, T, D), "k_new"),
-                          (v_new, (B, Hkv, T, D), "v_new"), (o, q.shape, "o"), (lse, (B, Hq, T), "lse"),
-                          (cache_len, (B,), "cache_len"), (tree_len, (B,), "tree_len"),
-                          (tree_mask, (B, T, T), "tree_mask")):
-        _shape("attn_fwd_tree", t, want, name)
+    _shapes("attn_fwd_tree", (k, (B, Hkv, Lk, D), "k"), (v, (B, Hkv, Lk, D), "v"), (k_new, (B, Hkv, T, D), "k_new"),
+            (v_new, (B, Hkv, T, D), "v_new"), (o, q.shape, "o"), (lse, (B, Hq, T), "lse"),
+            (cache_len, (B,), "cache_len"), (tree_len, (B,), "tree_len"),
+            (tree_mask, (B, T, T), "tree_mask"))
     pitch = kv_row_pitch(k, v) if kv_pitch is None else int(kv_pitch)
     st = load_library().attn_fwd_tree(_ptr(q), _ptr(k), _ptr(v), _ptr(k_new), _ptr(v_new), _ptr(tree_mask),
                                       _ptr(cache_len), _ptr(tree_len), _ptr(o), _ptr(lse), _ptr(workspace),
@@ -434,11 +438,10 @@ def attn_cache_append(k_new, v_new, k, v, cache_len, accept_len, cache_len_out, 
              i32=(cache_len, accept_len, cache_len_out, path, pos, seen, seen_out, limit))
     B, Hkv, T, D = k_new.shape
     Lk = k.shape[2]
-    for t, want, name in ((k, (B, Hkv, Lk, D), "k"), (v, (B, Hkv, Lk, D), "v"), (v_new, k_new.shape, "v_new"),
-                          (cache_len, (B,), "cache_len"), (accept_len, (B,), "accept_len"),
-                          (cache_len_out, (B,), "cache_len_out"), (path, (B, T), "path"), (pos, (B, Hkv, Lk), "pos"),
-                          (seen, (B,), "seen"), (seen_out, (B,), "seen_out"), (limit, (B, T), "limit")):
-        _shape("attn_cache_append", t, want, name)
+    _shapes("attn_cache_append", (k, (B, Hkv, Lk, D), "k"), (v, (B, Hkv, Lk, D), "v"), (v_new, k_new.shape, "v_new"),
+            (cache_len, (B,), "cache_len"), (accept_len, (B,), "accept_len"),
+            (cache_len_out, (B,), "cache_len_out"), (path, (B, T), "path"), (pos, (B, Hkv, Lk), "pos"),
+            (seen, (B,), "seen"), (seen_out, (B,), "seen_out"), (limit, (B, T), "limit"))
     pitch = kv_row_pitch(k, v) if kv_pitch is None else int(kv_pitch)
     st = load_library().attn_cache_append(_ptr(k_new), _ptr(v_new), _ptr(path), _ptr(accept_len), _ptr(cache_len),
                                           _ptr(seen), _ptr(k), _ptr(v), _ptr(pos), _ptr(cache_len_out),
@@ -467,9 +470,8 @@ def attn_key_weight(q, k, lse, weight, weight_out, workspace, scale: float, caus
     _require("attn_key_weight", dense=(q,), sliced=(k,), f32=(lse, weight, weight_out), u8=(workspace,), i32=(limit,))
     B, Hq, Lq, D = q.shape
     Hkv, Lk = k.shape[1], k.shape[2]
-    for t, want, name in ((k, (B, Hkv, Lk, D), "k"), (lse, (B, Hq, Lq), "lse"), (weight, (B, Hkv, Lk), "weight"),
-                          (weight_out, (B, Hkv, Lk), "weight_out"), (limit, (B, Lq), "limit")):
-        _shape("attn_key_weight", t, want, name)
+    _shapes("attn_key_weight", (k, (B, Hkv, Lk, D), "k"), (lse, (B, Hq, Lq), "lse"), (weight, (B, Hkv, Lk), "weight"),
+            (weight_out, (B, Hkv, Lk), "weight_out"), (limit, (B, Lq), "limit"))
     pitch = kv_row_pitch(k, k) if kv_pitch is None else int(kv_pitch)
     st = load_library().attn_key_weight(_ptr(q), _ptr(k), _ptr(lse), _ptr(limit), _ptr(weight), _ptr(weight_out),
                                         _ptr(workspace), workspace.numel(), pitch, B, Hq, Hkv, Lq, Lk, D,
@@ -495,11 +497,10 @@ def attn_cache_evict(k, v, weight, pos, cache_len, seen, weight_out, pos_out, ca
     _require("attn_cache_evict", sliced=(k, v), f32=(weight, weight_out), u8=(workspace,),
              i32=(pos, cache_len, seen, pos_out, cache_len_out))
     B, Hkv, Lk, D = k.shape
-    for t, want, name in ((v, k.shape, "v"), (weight, (B, Hkv, Lk), "weight"), (pos, (B, Hkv, Lk), "pos"),
-                          (weight_out, (B, Hkv, Lk), "weight_out"), (pos_out, (B, Hkv, Lk), "pos_out"),
-                          (cache_len, (B,), "cache_len"), (seen, (B,), "seen"),
-                          (cache_len_out, (B,), "cache_len_out")):
-        _shape("attn_cache_evict", t, want, name)
+    _shapes("attn_cache_evict", (v, k.shape, "v"), (weight, (B, Hkv, Lk), "weight"), (pos, (B, Hkv, Lk), "pos"),
+            (weight_out, (B, Hkv, Lk), "weight_out"), (pos_out, (B, Hkv, Lk), "pos_out"),
+            (cache_len, (B,), "cache_len"), (seen, (B,), "seen"),
+            (cache_len_out, (B,), "cache_len_out"))
     pitch = kv_row_pitch(k, v) if kv_pitch is None else int(kv_pitch)
     st = load_library().attn_cache_evict(_ptr(k), _ptr(v), _ptr(weight), _ptr(pos), _ptr(cache_len), _ptr(seen),
                                          _ptr(weight_out), _ptr(pos_out), _ptr(cache_len_out), _ptr(workspace),
