@@ -221,6 +221,36 @@ extern "C" attn_status_t attn_cache_evict(void* k, void* v, const float* weight,
   if (ds != ATTN_OK) return ds;
   EvictParams p{k, v, weight, pos, cache_len, seen, weight_out, pos_out, cache_len_out,
                 static_cast<int32_t*>(workspace), kv_pitch ? kv_pitch : Lk, B, Hkv, Lk, D / 8, keep, recent, status};
-  attn_cache_evict_kernel<<<B * Hkv, kEvictThreads, 0, stream>>>(p);
+  const int heads = B * Hkv;
+  if (Lk <= kEvictRowKeys) {
+    // about one CTA per SM, so that the moves run at the memory's rate
+    const int copies = heads < num_sms ? num_sms / heads : 1;
+    if (cudaFuncSetAttribute(attn_cache_evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(evict_smem(kEvictRowKeys, 1))) != cudaSuccess)
+      return ATTN_ERR_CUDA;
+    attn_cache_evict_kernel<<<heads * copies, kEvictThreads, evict_smem(Lk, copies), stream>>>(p, copies);
+    return launched();
+  }
+  // a CTA's part of the slots: every warp's share is a multiple of 32
+  constexpr int nc = kEvictCluster, warps = kEvictClusterThreads / 32;
+  const long long part = static_cast<long long>((((Lk + nc * warps - 1) / (nc * warps)) + 31) & ~31) * warps;
+  const bool cached = part <= kEvictKeys;
+  auto kern = cached ? attn_cache_evict_cluster_kernel<true> : attn_cache_evict_cluster_kernel<false>;
+  const size_t smem = cached ? static_cast<size_t>(part) * 4 : 0;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kEvictKeys * 4) != cudaSuccess)
+    return ATTN_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(heads) * nc);
+  cfg.blockDim = dim3(kEvictClusterThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = nc;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kern, p) != cudaSuccess) return ATTN_ERR_CUDA;
   return launched();
 }

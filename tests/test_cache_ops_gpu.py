@@ -366,6 +366,11 @@ EVICTS = [
     (1, 3, 9000, 128, [9000], 8192, 512, "random"),
     (1, 1, 20000, 64, [19999], 2500, 128, "heavy"),
     (1, 1, 700, 64, [700], 300, 300, "all recent"),
+    (1, 2, 32768, 64, [32768], 16384, 500, "heavy"),
+    (2, 1, 32769, 64, [32769, 17000], 16390, 77, "ties"),
+    (1, 1, 50001, 64, [50000], 4000, 100, "heavy"),
+    (1, 1, 33000, 64, [33000], 100, 0, "equal"),
+    (1, 1, 400000, 64, [399990], 200000, 1000, "ties"),
 ]
 
 
