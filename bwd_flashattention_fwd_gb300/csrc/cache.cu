@@ -231,13 +231,17 @@ extern "C" attn_status_t attn_cache_evict(void* k, void* v, const float* weight,
     attn_cache_evict_kernel<<<heads * copies, kEvictThreads, evict_smem(Lk, copies), stream>>>(p, copies);
     return launched();
   }
-  // a CTA's part of the slots: every warp's share is a multiple of 32
-  constexpr int nc = kEvictCluster, warps = kEvictClusterThreads / 32;
+  // sixteen CTAs per KV head where they still fit one wave; a CTA's part of
+  // the slots: every warp's share is a multiple of 32
+  const int nc = heads * 16 <= num_sms ? 16 : 8, warps = kEvictClusterThreads / 32;
   const long long part = static_cast<long long>((((Lk + nc * warps - 1) / (nc * warps)) + 31) & ~31) * warps;
   const bool cached = part <= kEvictKeys;
-  auto kern = cached ? attn_cache_evict_cluster_kernel<true> : attn_cache_evict_cluster_kernel<false>;
+  auto kern = nc == 16 ? (cached ? attn_cache_evict_cluster_kernel<true, 16> : attn_cache_evict_cluster_kernel<false, 16>)
+                       : (cached ? attn_cache_evict_cluster_kernel<true, 8> : attn_cache_evict_cluster_kernel<false, 8>);
   const size_t smem = cached ? static_cast<size_t>(part) * 4 : 0;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kEvictKeys * 4) != cudaSuccess)
+    return ATTN_ERR_CUDA;
+  if (nc == 16 && cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
     return ATTN_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(heads) * nc);

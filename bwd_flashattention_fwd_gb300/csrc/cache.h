@@ -12,8 +12,7 @@ constexpr int kTreeStage = 64;    // keys per pipeline stage
 constexpr int kTreeMinStages = 1;  // least stages a CTA takes
 constexpr int kTreeMaxCtas = 152;  // one per SM of a GB300
 constexpr int kEvictMaxLk = 1 << 20;
-constexpr int kEvictRowKeys = 32768;  // slots up to which one CTA holds a KV head's keys (and lists) in shared memory
-constexpr int kEvictCluster = 8;      // CTAs per KV head beyond that
+constexpr int kEvictRowKeys = 16384;  // slots up to which one CTA holds a KV head's keys in shared memory
 
 struct TreeParams {
   const void *q, *k, *v, *k_new, *v_new;

@@ -79,10 +79,9 @@ __global__ void __launch_bounds__(kAppendThreads) attn_cache_append_kernel(const
   }
 }
 
-constexpr int kEvictThreads = 1024;     // one CTA per copy of the search
+constexpr int kEvictThreads = 1024;  // one CTA per copy of the search
 constexpr int kEvictClusterThreads = 512;
-constexpr int kEvictBins = 1 << 11;  // digits of the radix search: 11, 11 and 10 bits
-constexpr int kEvictKeys = 40960;    // keys that a CTA of a cluster keeps in shared memory
+constexpr int kEvictKeys = 40960;  // keys that a CTA of a cluster keeps in shared memory
 
 // Order of the slots as an unsigned key, larger = kept first: recent slots
 // above all, then by weight (the usual monotone map of IEEE bits; -0 equals
@@ -94,24 +93,36 @@ __device__ __forceinline__ uint32_t evict_key(float w, int pos, long long recent
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// Digit d (0, 1, 2) of the radix search: its shift, its mask, and the bits of the digits before it.
-struct EvictDigit {
-  int shift;
-  uint32_t mask, above;
-};
-__device__ __forceinline__ EvictDigit evict_digit(int d) {
-  return d == 0 ? EvictDigit{21, 2047u, 0u} : d == 1 ? EvictDigit{10, 2047u, ~0u << 21} : EvictDigit{0, 1023u, ~0u << 10};
-}
-
-// One warp's 32 keys into a histogram.  Equal keys (fresh weights are all
-// zero, recent slots share one key) would hit one counter 32 times: counted at once.
-__device__ __forceinline__ void evict_count(int* hist, bool on, uint32_t key, const EvictDigit& dg) {
-  const int bin = on ? static_cast<int>((key >> dg.shift) & dg.mask) : -1;
+// One warp's 32 bins (-1: none) into a histogram.  Equal keys (fresh weights
+// are all zero, recent slots share one key) would hit one counter 32 times: counted at once.
+__device__ __forceinline__ void evict_count(int* hist, int bin) {
   if (__all_sync(0xffffffffu, bin == __shfl_sync(0xffffffffu, bin, 0))) {
-    if (on && (threadIdx.x & 31) == 0) atomicAdd(&hist[bin], 32);
-  } else if (on) {
+    if (bin >= 0 && (threadIdx.x & 31) == 0) atomicAdd(&hist[bin], 32);
+  } else if (bin >= 0) {
     atomicAdd(&hist[bin], 1);
   }
+}
+
+// Which slots a search keeps: those with key > threshold, and the first `need`
+// of the `equal` ones in slot order (ties: not all of them).
+struct EvictKept {
+  uint32_t threshold;
+  int need;
+  bool ties;
+  // The kept slots among the warp's 32 (bit per lane); in: the lane has a slot;
+  // eq: equal slots before these, counted on (ties only).
+  __device__ __forceinline__ uint32_t bits(bool in, uint32_t key, int& eq) const {
+    if (!ties) return __ballot_sync(0xffffffffu, in && key >= threshold);
+    const uint32_t e = __ballot_sync(0xffffffffu, in && key == threshold);
+    const int before = eq + __popc(e & ((1u << (threadIdx.x & 31)) - 1u));
+    eq += __popc(e);
+    return __ballot_sync(0xffffffffu, in && (key > threshold || (key == threshold && before < need)));
+  }
+};
+
+// Lanes of the strip of slots i .. i + 31 that lie below `keep`.
+__device__ __forceinline__ uint32_t evict_below(int i, int keep) {
+  return i + 32 <= keep ? ~0u : i >= keep ? 0u : (1u << (keep - i)) - 1u;
 }
 
 // The rows of the pairs (moving[i], freed[i]), i < n, and their weights and
@@ -120,11 +131,6 @@ template <class Index>
 __device__ __forceinline__ void evict_move(const EvictParams& p, int bh, const Index* moving, const Index* freed, int n,
                                            int all, int step) {
   const size_t row = static_cast<size_t>(bh) * p.Lk;
-  for (int i = all; i < n; i += step) {
-    const int to = freed[i], from = moving[i];
-    p.weight_out[row + to] = p.weight[row + from];
-    p.pos_out[row + to] = p.pos[row + from];
-  }
   uint4* k = static_cast<uint4*>(p.k) + static_cast<size_t>(bh) * p.kv_pitch * p.row16;
   uint4* v = static_cast<uint4*>(p.v) + static_cast<size_t>(bh) * p.kv_pitch * p.row16;
   const int pieces = n * p.row16;  // at most 2^19 x 32
@@ -147,6 +153,11 @@ __device__ __forceinline__ void evict_move(const EvictParams& p, int bh, const I
     for (int u = 0; u < U; ++u)
       if (x0 + u * step < pieces) k[to[u]] = a[u], v[to[u]] = e[u];
   }
+  for (int i = all; i < n; i += step) {
+    const int to = freed[i], from = moving[i];
+    p.weight_out[row + to] = p.weight[row + from];
+    p.pos_out[row + to] = p.pos[row + from];
+  }
 }
 
 // Slots from the new length on: weight 0, position -1.
@@ -158,6 +169,16 @@ __device__ __forceinline__ void evict_clear(const EvictParams& p, int bh, int fr
   }
 }
 
+// A KV head with at most `keep` tokens: nothing goes.
+__device__ __forceinline__ void evict_nothing(const EvictParams& p, int bh, int len, int all, int step) {
+  const size_t row = static_cast<size_t>(bh) * p.Lk;
+  for (int j = all; j < len; j += step) {
+    p.weight_out[row + j] = p.weight[row + j];
+    p.pos_out[row + j] = p.pos[row + j];
+  }
+  evict_clear(p, bh, len, all, step);
+}
+
 // Shared memory of the kernel below: keys, and its share of the two lists (16 bits per slot).
 __host__ __device__ inline int evict_share(int Lk, int copies) { return (Lk / 2 + copies - 1) / copies; }
 __host__ __device__ inline size_t evict_smem(int Lk, int copies) {
@@ -166,10 +187,12 @@ __host__ __device__ inline size_t evict_smem(int Lk, int copies) {
 
 // Eviction with rows of up to kEvictRowKeys slots.
 //   1. The keep-th largest key, by a radix search with digits of 11, 11 and 10
-//      bits over histograms in shared memory.
-//   2. Ranks in slot order (ballots within a warp's consecutive slots, prefix
-//      sums over the warps) give every freed slot below `keep` and every kept
-//      one above it its place in two lists; of equal keys the lower slots are kept.
+//      bits over histograms in shared memory (four, by lane, for the first
+//      digit: the weights' exponents meet in few bins).
+//   2. Kept tokens before each slot, in slot order (ballots within a warp's
+//      consecutive slots, prefix sums over the warps): the freed slot j below
+//      `keep` is number j - kept(j), the kept slot j above is number kept(j) -
+//      kept(keep).  Of equal keys the lower slots are kept.
 //   3. The i-th freed slot takes the i-th kept row from above.  Sources and
 //      targets are disjoint, so the rows move in place and in any order.
 // A single CTA's load/store unit would bound step 3, and a barrier between
@@ -177,52 +200,54 @@ __host__ __device__ inline size_t evict_smem(int Lk, int copies) {
 // and 2 (every one holds all keys, 4 bytes a slot) and share step 3 out, which
 // needs nothing from each other.
 __global__ void __launch_bounds__(kEvictThreads, 1) attn_cache_evict_kernel(const EvictParams p, int copies) {
+  constexpr int BINS = 2048, NH = 4;
   extern __shared__ uint32_t keys[];
-  __shared__ int hist[2][kEvictBins];  // counters for even and odd lanes
+  __shared__ int hist[NH][BINS];
   __shared__ int warp_sum[32];
   __shared__ int2 warp_pair[32];
-  __shared__ int s_digit, s_need;
+  __shared__ int s_digit, s_need, s_equal;
   const int bh = blockIdx.x / copies, rank = blockIdx.x - bh * copies, b = bh / p.Hkv;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int len = clamp_len(p.cache_len[b], p.Lk);
-  const int keep = p.keep, new_len = min(len, keep);
+  const int keep = p.keep;
+  const int all = rank * kEvictThreads + tid, step = copies * kEvictThreads;  // this thread among the head's
+  if (all == 0 && bh == b * p.Hkv) p.cache_len_out[b] = min(len, keep);
+  if (len <= keep) {
+    evict_nothing(p, bh, len, all, step);
+    return;
+  }
   const long long recent_from = static_cast<long long>(p.seen[b]) - p.recent;
   const size_t row = static_cast<size_t>(bh) * p.Lk;
   const float* w = p.weight + row;
   const int32_t* pos = p.pos + row;
-  float* wo = p.weight_out + row;
-  int32_t* po = p.pos_out + row;
-  const int all = rank * kEvictThreads + tid, step = copies * kEvictThreads;  // this thread among the head's
-  if (all == 0 && bh == b * p.Hkv) p.cache_len_out[b] = new_len;
-  if (len <= keep) {
-    for (int j = all; j < len; j += step) {
-      wo[j] = w[j];
-      po[j] = pos[j];
-    }
-    evict_clear(p, bh, new_len, all, step);
-    return;
-  }
   // every warp owns consecutive slots, a multiple of 32 of them
   const int per_warp = ((len + 31) / 32 + 31) & ~31;
   const int w0 = min(warp * per_warp, len), w1 = min(w0 + per_warp, len);
-  for (int i = tid; i < 2 * kEvictBins; i += kEvictThreads) (&hist[0][0])[i] = 0;
-#pragma unroll 8
-  for (int j = w0 + lane; j < w1; j += 32) keys[j] = evict_key(w[j], pos[j], recent_from);
+  for (int i = tid; i < NH * BINS; i += kEvictThreads) (&hist[0][0])[i] = 0;
+  __syncthreads();
+#pragma unroll 4
+  for (int i = w0; i < w1; i += 32) {
+    const bool in = i + lane < w1;
+    const uint32_t key = in ? evict_key(w[i + lane], pos[i + lane], recent_from) : 0u;
+    if (in) keys[i + lane] = key;
+    evict_count(hist[lane & (NH - 1)], in ? static_cast<int>(key >> 21) : -1);
+  }
   __syncthreads();
   uint32_t prefix = 0;
   int need = keep;  // how many of the slots that match the digits so far are kept
 #pragma unroll 1
   for (int d = 0; d < 3; ++d) {
-    const EvictDigit dg = evict_digit(d);
-    for (int i = w0; i < w1; i += 32) {
-      const uint32_t key = i + lane < w1 ? keys[i + lane] : 0u;
-      evict_count(hist[lane & 1], i + lane < w1 && (key & dg.above) == prefix, key, dg);
-    }
-    __syncthreads();
+    const int shift = d == 0 ? 21 : d == 1 ? 10 : 0;
     // two bins per thread, from the top: thread 0 has the last two
-    const int bin0 = kEvictBins - 2 - 2 * tid;
-    const int lo = hist[0][bin0] + hist[1][bin0], hi = hist[0][bin0 + 1] + hist[1][bin0 + 1], mine = lo + hi;
-    hist[0][bin0] = hist[1][bin0] = hist[0][bin0 + 1] = hist[1][bin0 + 1] = 0;
+    const int bin0 = BINS - 2 - 2 * tid;
+    int lo = 0, hi = 0;
+#pragma unroll
+    for (int h = 0; h < NH; ++h) {
+      int2* at = reinterpret_cast<int2*>(&hist[h][bin0]);
+      lo += at->x, hi += at->y;
+      *at = make_int2(0, 0);
+    }
+    const int mine = lo + hi;
     int incl = mine;
 #pragma unroll
     for (int k = 1; k < 32; k <<= 1) {
@@ -231,72 +256,82 @@ __global__ void __launch_bounds__(kEvictThreads, 1) attn_cache_evict_kernel(cons
     }
     if (lane == 31) warp_sum[warp] = incl;
     __syncthreads();
-    int before = lane < warp ? warp_sum[lane] : 0;
-    before = __reduce_add_sync(0xffffffffu, before) + incl - mine;  // keys in higher bins than this thread's
+    const int before = __reduce_add_sync(0xffffffffu, lane < warp ? warp_sum[lane] : 0) + incl - mine;
     if (before < need && need <= before + mine) {  // one thread
       const bool upper = need - before <= hi;
       s_digit = bin0 + upper;
       s_need = need - before - (upper ? 0 : hi);
+      s_equal = upper ? hi : lo;
     }
     __syncthreads();
-    prefix |= static_cast<uint32_t>(s_digit) << dg.shift;
+    prefix |= static_cast<uint32_t>(s_digit) << shift;
     need = s_need;
-  }
-  // ranks
-  const uint32_t lower = (1u << lane) - 1u;
-  int n_eq = 0;
-  for (int i = w0; i < w1; i += 32) n_eq += __popc(__ballot_sync(0xffffffffu, i + lane < w1 && keys[i + lane] == prefix));
-  if (lane == 0) warp_sum[warp] = n_eq;
-  __syncthreads();
-  const int eq_before = __reduce_add_sync(0xffffffffu, lane < warp ? warp_sum[lane] : 0);
-  // the slots of one strip of 32: which are kept
-  auto kept_of = [&](int i, int& eq) {
-    const uint32_t key = i + lane < w1 ? keys[i + lane] : 0u;
-    const uint32_t eqs = __ballot_sync(0xffffffffu, i + lane < w1 && key == prefix);
-    const bool k = i + lane < w1 && (key > prefix || (key == prefix && eq + __popc(eqs & lower) < need));
-    eq += __popc(eqs);
-    return k;
-  };
-  int holes = 0, movers = 0;
-  {
-    int eq = eq_before;
+    if (d == 2) break;
+    // the next digit of the slots that match so far (few)
+    const uint32_t above = ~0u << shift;
+    const int next = d == 0 ? 10 : 0;
+    const uint32_t mask = d == 0 ? 2047u : 1023u;
     for (int i = w0; i < w1; i += 32) {
-      const bool k = kept_of(i, eq);
-      holes += __popc(__ballot_sync(0xffffffffu, i + lane < w1 && !k && i + lane < keep));
-      movers += __popc(__ballot_sync(0xffffffffu, k && i + lane >= keep));
+      const uint32_t key = i + lane < w1 ? keys[i + lane] : ~prefix;
+      const bool on = (key & above) == prefix;
+      if (__any_sync(0xffffffffu, on)) evict_count(hist[0], on ? static_cast<int>((key >> next) & mask) : -1);
     }
+    __syncthreads();
   }
-  if (lane == 0) warp_pair[warp] = make_int2(holes, movers);
+  const EvictKept kept{prefix, need, need < s_equal};
+  // kept slots before each warp's: below `keep` and from there on
+  int eq0 = 0;
+  if (kept.ties) {
+    int n_eq = 0;
+    for (int i = w0; i < w1; i += 32)
+      n_eq += __popc(__ballot_sync(0xffffffffu, i + lane < w1 && keys[i + lane] == prefix));
+    if (lane == 0) warp_sum[warp] = n_eq;
+    __syncthreads();
+    eq0 = __reduce_add_sync(0xffffffffu, lane < warp ? warp_sum[lane] : 0);
+  }
+  int below = 0, above = 0, eq = eq0;
+  for (int i = w0; i < w1; i += 32) {
+    const uint32_t k = kept.bits(i + lane < w1, i + lane < w1 ? keys[i + lane] : 0u, eq);
+    const uint32_t m = evict_below(i, keep);
+    below += __popc(k & m), above += __popc(k & ~m);
+  }
+  if (lane == 0) warp_pair[warp] = make_int2(below, above);
   __syncthreads();
   const int2 of = warp_pair[lane];
-  const int n = __reduce_add_sync(0xffffffffu, of.x);  // freed slots, and as many moving ones
-  holes = __reduce_add_sync(0xffffffffu, lane < warp ? of.x : 0);
-  movers = __reduce_add_sync(0xffffffffu, lane < warp ? of.y : 0);
-  // this CTA's pairs m0 .. m1 - 1, listed in shared memory
-  const int share = evict_share(p.Lk, copies), mine_n = (n + copies - 1) / copies;
-  const int m0 = min(rank * mine_n, n), m1 = min(m0 + mine_n, n);
+  const int n = keep - __reduce_add_sync(0xffffffffu, of.x);  // freed slots, and as many moving ones
+  below = __reduce_add_sync(0xffffffffu, lane < warp ? of.x : 0);
+  above = __reduce_add_sync(0xffffffffu, lane < warp ? of.y : 0);
+  // this CTA's pairs m0 .. m1 - 1, listed in shared memory; strips of 32 kept slots' values are shared out, too
+  const int share = evict_share(p.Lk, copies), each = (n + copies - 1) / copies;
+  const int m0 = min(rank * each, n), m1 = min(m0 + each, n);
   uint16_t* freed = reinterpret_cast<uint16_t*>(keys + p.Lk);
   uint16_t* moving = freed + share;
-  {
-    int eq = eq_before;
-    for (int i = w0; i < w1; i += 32) {
-      const int j = i + lane;
-      const bool k = kept_of(i, eq);
-      const bool hole = j < w1 && !k && j < keep, mover = k && j >= keep;
-      const uint32_t hb = __ballot_sync(0xffffffffu, hole), mb = __ballot_sync(0xffffffffu, mover);
-      const int hi = holes + __popc(hb & lower), mi = movers + __popc(mb & lower);
-      if (hole && hi >= m0 && hi < m1) freed[hi - m0] = static_cast<uint16_t>(j);
-      if (mover && mi >= m0 && mi < m1) moving[mi - m0] = static_cast<uint16_t>(j);
-      if (k && j < keep && (i >> 5) % copies == rank) {  // strips are shared out, too
-        wo[j] = w[j];
-        po[j] = pos[j];
+  const uint32_t lower = (1u << lane) - 1u;
+  int turn = (w0 >> 5) % copies;
+  eq = eq0;
+  for (int i = w0; i < w1; i += 32) {
+    const int j = i + lane;
+    const uint32_t k = kept.bits(j < w1, j < w1 ? keys[j] : 0u, eq);
+    const uint32_t m = evict_below(i, keep);
+    const bool mine = (k >> lane) & 1u;
+    if (m != 0u) {
+      const int number = j - below - __popc(k & lower);
+      if (((m >> lane) & 1u) && !mine && number >= m0 && number < m1) freed[number - m0] = static_cast<uint16_t>(j);
+      if (turn == rank && mine && ((m >> lane) & 1u)) {
+        p.weight_out[row + j] = w[j];
+        p.pos_out[row + j] = pos[j];
       }
-      holes += __popc(hb), movers += __popc(mb);
     }
+    if (~m != 0u) {
+      const int number = above + __popc(k & ~m & lower);
+      if (mine && !((m >> lane) & 1u) && number >= m0 && number < m1) moving[number - m0] = static_cast<uint16_t>(j);
+    }
+    below += __popc(k & m), above += __popc(k & ~m);
+    if (++turn == copies) turn = 0;
   }
   __syncthreads();
   evict_move(p, bh, moving, freed, m1 - m0, tid, kEvictThreads);
-  evict_clear(p, bh, new_len, all, step);
+  evict_clear(p, bh, keep, all, step);
 }
 
 // Value of another CTA's shared memory (cluster address).
@@ -313,172 +348,182 @@ __device__ __forceinline__ int ld_cluster(uint32_t addr) {
   asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
   return v;
 }
-// The same for longer rows, one cluster of CTAs per KV head; each CTA owns a
-// consecutive part of the slots and keeps their keys in shared memory (CACHED;
-// parts that do not fit are read again in each pass).  Every CTA adds the
-// histograms up through distributed shared memory, one cluster barrier per
-// digit (a histogram per digit, so none is cleared while others read it);
-// prefix sums run over warps and CTAs, and the lists are in the workspace.
-template <bool CACHED>
+
+// The same for longer rows, one cluster of NC CTAs per KV head; each CTA owns
+// a consecutive part of the slots and keeps their keys in shared memory
+// (CACHED; parts that do not fit are read again in each pass).  Four digits of
+// 8 bits: what a digit costs is reading every CTA's histogram through
+// distributed shared memory (2048 bins: 2.3 us a digit, 256: 0.6) and a cluster
+// barrier.  Each digit has a histogram of its own, so none is cleared while
+// others read it.  Prefix sums run over warps and CTAs; the lists are in the workspace.
+template <bool CACHED, int NC>
 __global__ void __launch_bounds__(kEvictClusterThreads) attn_cache_evict_cluster_kernel(const EvictParams p) {
+  constexpr int NW = kEvictClusterThreads / 32, BINS = 256;
   extern __shared__ uint32_t keys[];
-  __shared__ __align__(16) int hist[3][kEvictBins];
-  __shared__ int warp_sum[16];
-  __shared__ int2 warp_pair[16];
-  __shared__ int s_digit, s_need;
+  __shared__ __align__(16) int hist[4][BINS];
+  __shared__ int first[4][BINS];  // the first digit's, by lane: the weights' exponents meet in few bins
+  __shared__ int warp_sum[NW];
+  __shared__ int2 warp_pair[NW];
+  __shared__ __align__(16) int4 quad_sum[NC][BINS / 4];
+  __shared__ int s_digit, s_need, s_equal;
   __shared__ int s_counts[2];
-  constexpr int NW = kEvictClusterThreads / 32;
-  constexpr int nc = kEvictCluster;  // constant, so that a thread's remote loads are all in flight at once
   const int rank = static_cast<int>(cluster_ctarank());
-  const int bh = blockIdx.x / nc, b = bh / p.Hkv, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int bh = blockIdx.x / NC, b = bh / p.Hkv, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int len = clamp_len(p.cache_len[b], p.Lk);
-  const int keep = p.keep, new_len = min(len, keep);
+  const int keep = p.keep;
+  const int all = rank * kEvictClusterThreads + tid, step = NC * kEvictClusterThreads;  // this thread among the cluster's
+  if (all == 0 && bh == b * p.Hkv) p.cache_len_out[b] = min(len, keep);
+  if (len <= keep) {  // the same for the whole cluster
+    evict_nothing(p, bh, len, all, step);
+    return;
+  }
   const long long recent_from = static_cast<long long>(p.seen[b]) - p.recent;
   const size_t row = static_cast<size_t>(bh) * p.Lk;
   const float* w = p.weight + row;
   const int32_t* pos = p.pos + row;
-  float* wo = p.weight_out + row;
-  int32_t* po = p.pos_out + row;
-  const int all = rank * kEvictClusterThreads + tid, step = nc * kEvictClusterThreads;  // this thread among the cluster's
-  if (all == 0 && bh == b * p.Hkv) p.cache_len_out[b] = new_len;
-  if (len <= keep) {  // the same for the whole cluster
-    for (int j = all; j < len; j += step) {
-      wo[j] = w[j];
-      po[j] = pos[j];
-    }
-    evict_clear(p, bh, new_len, all, step);
-    return;
-  }
   // this CTA's slots [j0, j1); every warp owns a consecutive multiple of 32 of them
-  const int per_warp = ((len + nc * NW - 1) / (nc * NW) + 31) & ~31;
+  const int per_warp = ((len + NC * NW - 1) / (NC * NW) + 31) & ~31;
   const int j0 = min(rank * NW * per_warp, len), j1 = min(j0 + NW * per_warp, len);
   const int w0 = min(j0 + warp * per_warp, j1), w1 = min(w0 + per_warp, j1);
   auto key_at = [&](int j) { return CACHED ? keys[j - j0] : evict_key(w[j], pos[j], recent_from); };
-  for (int i = tid; i < 3 * kEvictBins; i += kEvictClusterThreads) (&hist[0][0])[i] = 0;
-  if constexpr (CACHED) {
-#pragma unroll 4
-    for (int j = w0 + lane; j < w1; j += 32) keys[j - j0] = evict_key(w[j], pos[j], recent_from);
+  for (int i = tid; i < 4 * BINS; i += kEvictClusterThreads) (&hist[0][0])[i] = (&first[0][0])[i] = 0;
+  __syncthreads();
+#pragma unroll 8
+  for (int i = w0; i < w1; i += 32) {
+    const bool in = i + lane < w1;
+    const uint32_t key = in ? evict_key(w[i + lane], pos[i + lane], recent_from) : 0u;
+    if (CACHED && in) keys[i + lane - j0] = key;
+    evict_count(first[lane & 3], in ? static_cast<int>(key >> 24) : -1);
   }
   __syncthreads();
+  if (tid < BINS) hist[0][tid] = first[0][tid] + first[1][tid] + first[2][tid] + first[3][tid];
   uint32_t prefix = 0;
   int need = keep;
 #pragma unroll 1
-  for (int d = 0; d < 3; ++d) {
-    const EvictDigit dg = evict_digit(d);
-    for (int i = w0; i < w1; i += 32) {
-      const uint32_t key = i + lane < w1 ? key_at(i + lane) : 0u;
-      evict_count(hist[d], i + lane < w1 && (key & dg.above) == prefix, key, dg);
-    }
+  for (int d = 0; d < 4; ++d) {
+    const int shift = 24 - 8 * d;
     cluster_sync_all();
-    // the cluster's counts of this thread's four bins, from the top: thread 0 has the last four
-    const int bin0 = kEvictBins - 4 - 4 * tid;
-    int4 part[nc], c = make_int4(0, 0, 0, 0);
-#pragma unroll
-    for (int r = 0; r < nc; ++r) part[r] = ld_cluster_v4(cluster_map(smem_u32(&hist[d][bin0]), r));
-#pragma unroll
-    for (int r = 0; r < nc; ++r) c.x += part[r].x, c.y += part[r].y, c.z += part[r].z, c.w += part[r].w;
-    const int mine = c.x + c.y + c.z + c.w;
-    int incl = mine;
-#pragma unroll
-    for (int k = 1; k < 32; k <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, incl, k);
-      if (lane >= k) incl += y;
+    // every CTA's histogram, four bins a thread; then the sums, one warp, eight bins a lane from the top
+    for (int x = tid; x < NC * (BINS / 4); x += kEvictClusterThreads) {
+      const int r = x / (BINS / 4), q = x % (BINS / 4);
+      quad_sum[r][q] = ld_cluster_v4(cluster_map(smem_u32(&hist[d][4 * q]), r));
     }
-    if (lane == 31) warp_sum[warp] = incl;
     __syncthreads();
-    int before = incl - mine;  // keys in higher bins than this thread's
+    if (warp == 0) {
+      int c[8];
 #pragma unroll
-    for (int k = 0; k < NW; ++k)
-      if (k < warp) before += warp_sum[k];
-    if (before < need && need <= before + mine) {  // one thread
-      int left = need - before, bin = bin0 + 3;
-      if (left > c.w) {
-        left -= c.w, --bin;
-        if (left > c.z) {
-          left -= c.z, --bin;
-          if (left > c.y) left -= c.y, --bin;
+      for (int h = 0; h < 2; ++h) {
+        int4 t = make_int4(0, 0, 0, 0);
+#pragma unroll
+        for (int r = 0; r < NC; ++r) {
+          const int4 x = quad_sum[r][BINS / 4 - 1 - 2 * lane - h];
+          t.x += x.x, t.y += x.y, t.z += x.z, t.w += x.w;
         }
+        c[4 * h] = t.w, c[4 * h + 1] = t.z, c[4 * h + 2] = t.y, c[4 * h + 3] = t.x;  // from the top
       }
-      s_digit = bin;
-      s_need = left;
+      int mine = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) mine += c[i];
+      int incl = mine;
+#pragma unroll
+      for (int k = 1; k < 32; k <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, incl, k);
+        if (lane >= k) incl += y;
+      }
+      int left = need - (incl - mine);
+      if (left > 0 && left <= mine) {  // one lane
+        int i = 0;
+        bool found = false;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          if (!found) {
+            i = k;
+            if (left <= c[k]) found = true, s_equal = c[k];
+            else left -= c[k];
+          }
+        }
+        s_digit = BINS - 1 - 8 * lane - i;
+        s_need = left;
+      }
     }
     __syncthreads();
-    prefix |= static_cast<uint32_t>(s_digit) << dg.shift;
+    prefix |= static_cast<uint32_t>(s_digit) << shift;
     need = s_need;
-  }
-  // ranks.  Equal keys before this warp's slots:
-  const int eq_bin = static_cast<int>(prefix & 1023u);
-  int eq_before = 0, eq_of[nc];
-#pragma unroll
-  for (int r = 0; r < nc; ++r) eq_of[r] = ld_cluster(cluster_map(smem_u32(&hist[2][eq_bin]), r));
-#pragma unroll
-  for (int r = 0; r < nc; ++r) eq_before += r < rank ? eq_of[r] : 0;
-  int n_eq = 0;
-  for (int i = w0; i < w1; i += 32)
-    n_eq += __popc(__ballot_sync(0xffffffffu, i + lane < w1 && key_at(i + lane) == prefix));
-  if (lane == 0) warp_sum[warp] = n_eq;
-  __syncthreads();
-  for (int k = 0; k < warp; ++k) eq_before += warp_sum[k];
-  const uint32_t lower = (1u << lane) - 1u;
-  // the slots of one strip of 32: which are kept
-  auto kept_of = [&](int i, int& eq) {
-    const uint32_t key = i + lane < w1 ? key_at(i + lane) : 0u;
-    const uint32_t eqs = __ballot_sync(0xffffffffu, i + lane < w1 && key == prefix);
-    const bool k = i + lane < w1 && (key > prefix || (key == prefix && eq + __popc(eqs & lower) < need));
-    eq += __popc(eqs);
-    return k;
-  };
-  int holes = 0, movers = 0;
-  {
-    int eq = eq_before;
+    if (d == 3) break;
+    const uint32_t above = ~0u << shift;
     for (int i = w0; i < w1; i += 32) {
-      const bool k = kept_of(i, eq);
-      holes += __popc(__ballot_sync(0xffffffffu, i + lane < w1 && !k && i + lane < keep));
-      movers += __popc(__ballot_sync(0xffffffffu, k && i + lane >= keep));
+      const uint32_t key = i + lane < w1 ? key_at(i + lane) : ~prefix;
+      const bool on = (key & above) == prefix;
+      if (__any_sync(0xffffffffu, on)) evict_count(hist[d + 1], on ? static_cast<int>((key >> (shift - 8)) & 255u) : -1);
     }
   }
-  if (lane == 0) warp_pair[warp] = make_int2(holes, movers);
+  const EvictKept kept{prefix, need, need < s_equal};
+  int eq0 = 0;
+  if (kept.ties) {  // equal slots before this warp's
+    const int bin = static_cast<int>(prefix & 255u);
+    int of[NC];
+#pragma unroll
+    for (int r = 0; r < NC; ++r) of[r] = ld_cluster(cluster_map(smem_u32(&hist[3][bin]), r));
+#pragma unroll
+    for (int r = 0; r < NC; ++r) eq0 += r < rank ? of[r] : 0;
+    int n_eq = 0;
+    for (int i = w0; i < w1; i += 32)
+      n_eq += __popc(__ballot_sync(0xffffffffu, i + lane < w1 && key_at(i + lane) == prefix));
+    if (lane == 0) warp_sum[warp] = n_eq;
+    __syncthreads();
+    for (int k = 0; k < warp; ++k) eq0 += warp_sum[k];
+  }
+  int below = 0, above = 0, eq = eq0;
+  for (int i = w0; i < w1; i += 32) {
+    const uint32_t k = kept.bits(i + lane < w1, i + lane < w1 ? key_at(i + lane) : 0u, eq);
+    const uint32_t m = evict_below(i, keep);
+    below += __popc(k & m), above += __popc(k & ~m);
+  }
+  if (lane == 0) warp_pair[warp] = make_int2(below, above);
   __syncthreads();
-  int hole0 = 0, mover0 = 0;
-  for (int k = 0; k < NW; ++k) {
-    if (k == warp) holes = hole0, movers = mover0;
-    hole0 += warp_pair[k].x, mover0 += warp_pair[k].y;
+  const int2 of = lane < NW ? warp_pair[lane] : make_int2(0, 0);
+  if (warp == 0) {
+    const int x = __reduce_add_sync(0xffffffffu, of.x), y = __reduce_add_sync(0xffffffffu, of.y);
+    if (lane == 0) s_counts[0] = x, s_counts[1] = y;
   }
-  if (tid == 0) s_counts[0] = hole0, s_counts[1] = mover0;
+  below = __reduce_add_sync(0xffffffffu, lane < warp ? of.x : 0);
+  above = __reduce_add_sync(0xffffffffu, lane < warp ? of.y : 0);
   cluster_sync_all();
-  int n = 0, h_of[nc], m_of[nc];
+  int n = keep;
+  {
+    int bl[NC], ab[NC];
 #pragma unroll
-  for (int r = 0; r < nc; ++r) {
-    const uint32_t at = cluster_map(smem_u32(&s_counts[0]), r);
-    h_of[r] = ld_cluster(at), m_of[r] = ld_cluster(at + 4);
-  }
+    for (int r = 0; r < NC; ++r) {
+      const uint32_t at = cluster_map(smem_u32(&s_counts[0]), r);
+      bl[r] = ld_cluster(at), ab[r] = ld_cluster(at + 4);
+    }
 #pragma unroll
-  for (int r = 0; r < nc; ++r) {
-    if (r < rank) holes += h_of[r], movers += m_of[r];
-    n += h_of[r];
+    for (int r = 0; r < NC; ++r) {
+      n -= bl[r];
+      if (r < rank) below += bl[r], above += ab[r];
+    }
   }
   const int cap = p.Lk / 2;  // min(keep, len - keep) slots at most
   int32_t* freed = p.lists + static_cast<size_t>(bh) * 2 * cap;
   int32_t* moving = freed + cap;
-  {
-    int eq = eq_before;
-    for (int i = w0; i < w1; i += 32) {
-      const int j = i + lane;
-      const bool k = kept_of(i, eq);
-      const uint32_t hb = __ballot_sync(0xffffffffu, j < w1 && !k && j < keep);
-      const uint32_t mb = __ballot_sync(0xffffffffu, k && j >= keep);
-      if (j < w1 && !k && j < keep) freed[holes + __popc(hb & lower)] = j;
-      if (k && j >= keep) moving[movers + __popc(mb & lower)] = j;
-      if (k && j < keep) {
-        wo[j] = w[j];
-        po[j] = pos[j];
-      }
-      holes += __popc(hb), movers += __popc(mb);
+  const uint32_t lower = (1u << lane) - 1u;
+  eq = eq0;
+  for (int i = w0; i < w1; i += 32) {
+    const int j = i + lane;
+    const uint32_t k = kept.bits(j < w1, j < w1 ? key_at(j) : 0u, eq);
+    const uint32_t m = evict_below(i, keep);
+    const bool mine = (k >> lane) & 1u, low = (m >> lane) & 1u;
+    if (low && !mine) freed[j - below - __popc(k & lower)] = j;
+    if (!low && mine) moving[above + __popc(k & ~m & lower)] = j;
+    if (low && mine) {
+      p.weight_out[row + j] = w[j];
+      p.pos_out[row + j] = pos[j];
     }
+    below += __popc(k & m), above += __popc(k & ~m);
   }
   cluster_sync_all();  // the lists are written (and no CTA's shared memory is read any more)
   evict_move(p, bh, moving, freed, n, all, step);
-  evict_clear(p, bh, new_len, all, step);
+  evict_clear(p, bh, keep, all, step);
 }
 
 }  // namespace gbattn
