@@ -125,6 +125,45 @@ __device__ __forceinline__ uint32_t evict_below(int i, int keep) {
   return i + 32 <= keep ? ~0u : i >= keep ? 0u : (1u << (keep - i)) - 1u;
 }
 
+// The lists' entries of one strip of slots i .. i + 31 (k: kept, m: below
+// `keep`, in: existing), with `below` / `above` kept slots before it on either
+// side of `keep`; only pairs m0 .. m1 - 1 are listed.  The freed slot j is
+// number j - kept(j), the moving one number kept(j) - kept(keep).
+template <class Index>
+__device__ __forceinline__ void evict_list(int i, uint32_t k, uint32_t m, int below, int above, int m0, int m1,
+                                           Index* freed, Index* moving) {
+  uint32_t h = ~k & m, v = k & ~m;
+  int number = i - below;  // of the first freed slot
+  if (number < m1 && number + __popc(h) > m0)
+    for (; h; h &= h - 1, ++number)
+      if (number >= m0 && number < m1) freed[number - m0] = static_cast<Index>(i + __ffs(static_cast<int>(h)) - 1);
+  if (above < m1 && above + __popc(v) > m0)
+    for (; v; v &= v - 1, ++above)
+      if (above >= m0 && above < m1) moving[above - m0] = static_cast<Index>(i + __ffs(static_cast<int>(v)) - 1);
+}
+
+// Kept slots below `keep` keep their values: slots j0 + at, + by, ... below
+// j1; bits: their kept strips from slot j0 on.
+__device__ __forceinline__ void evict_stay(const EvictParams& p, int bh, const uint32_t* bits, int j0, int j1, int at,
+                                           int by) {
+  const size_t row = static_cast<size_t>(bh) * p.Lk;
+  const int end = min(j1, p.keep);
+  for (int j = j0 + at; j < end; j += 4 * by) {
+    float w[4];
+    int pos[4];
+    bool on[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int x = j + u * by;
+      on[u] = x < end && ((bits[(x - j0) >> 5] >> ((x - j0) & 31)) & 1u);
+      if (on[u]) w[u] = p.weight[row + x], pos[u] = p.pos[row + x];
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (on[u]) p.weight_out[row + j + u * by] = w[u], p.pos_out[row + j + u * by] = pos[u];
+  }
+}
+
 // The rows of the pairs (moving[i], freed[i]), i < n, and their weights and
 // positions: threads `all` of `step`, in 16-byte pieces.
 template <class Index>
@@ -179,6 +218,29 @@ __device__ __forceinline__ void evict_nothing(const EvictParams& p, int bh, int 
   evict_clear(p, bh, len, all, step);
 }
 
+// Keys of the warp's slots w0 .. w1 - 1 into `keys` (from slot j0 on; null:
+// not kept) and their first digit into the counters; four strips' loads at a time.
+__device__ __forceinline__ void evict_load(const EvictParams& p, int bh, int w0, int w1, int j0, uint32_t* keys,
+                                           long long recent_from, int* hist, int digit_shift) {
+  const int lane = threadIdx.x & 31;
+  const float* w = p.weight + static_cast<size_t>(bh) * p.Lk;
+  const int32_t* pos = p.pos + static_cast<size_t>(bh) * p.Lk;
+  for (int i = w0 + lane; i - lane < w1; i += 128) {
+    float x[4];
+    int y[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (i + 32 * u < w1) x[u] = w[i + 32 * u], y[u] = pos[i + 32 * u];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const bool in = i + 32 * u < w1;
+      const uint32_t key = in ? evict_key(x[u], y[u], recent_from) : 0u;
+      if (in && keys) keys[i + 32 * u - j0] = key;
+      evict_count(hist, in ? static_cast<int>(key >> digit_shift) : -1);
+    }
+  }
+}
+
 // Shared memory of the kernel below: keys, and its share of the two lists (16 bits per slot).
 __host__ __device__ inline int evict_share(int Lk, int copies) { return (Lk / 2 + copies - 1) / copies; }
 __host__ __device__ inline size_t evict_smem(int Lk, int copies) {
@@ -203,6 +265,7 @@ __global__ void __launch_bounds__(kEvictThreads, 1) attn_cache_evict_kernel(cons
   constexpr int BINS = 2048, NH = 4;
   extern __shared__ uint32_t keys[];
   __shared__ int hist[NH][BINS];
+  __shared__ uint32_t bits[kEvictRowKeys / 32];  // kept slots
   __shared__ int warp_sum[32];
   __shared__ int2 warp_pair[32];
   __shared__ int s_digit, s_need, s_equal;
@@ -217,21 +280,12 @@ __global__ void __launch_bounds__(kEvictThreads, 1) attn_cache_evict_kernel(cons
     return;
   }
   const long long recent_from = static_cast<long long>(p.seen[b]) - p.recent;
-  const size_t row = static_cast<size_t>(bh) * p.Lk;
-  const float* w = p.weight + row;
-  const int32_t* pos = p.pos + row;
   // every warp owns consecutive slots, a multiple of 32 of them
   const int per_warp = ((len + 31) / 32 + 31) & ~31;
   const int w0 = min(warp * per_warp, len), w1 = min(w0 + per_warp, len);
   for (int i = tid; i < NH * BINS; i += kEvictThreads) (&hist[0][0])[i] = 0;
   __syncthreads();
-#pragma unroll 4
-  for (int i = w0; i < w1; i += 32) {
-    const bool in = i + lane < w1;
-    const uint32_t key = in ? evict_key(w[i + lane], pos[i + lane], recent_from) : 0u;
-    if (in) keys[i + lane] = key;
-    evict_count(hist[lane & (NH - 1)], in ? static_cast<int>(key >> 21) : -1);
-  }
+  evict_load(p, bh, w0, w1, 0, keys, recent_from, hist[lane & (NH - 1)], 21);
   __syncthreads();
   uint32_t prefix = 0;
   int need = keep;  // how many of the slots that match the digits so far are kept
@@ -279,58 +333,47 @@ __global__ void __launch_bounds__(kEvictThreads, 1) attn_cache_evict_kernel(cons
     __syncthreads();
   }
   const EvictKept kept{prefix, need, need < s_equal};
-  // kept slots before each warp's: below `keep` and from there on
-  int eq0 = 0;
-  if (kept.ties) {
+  int eq = 0;
+  if (kept.ties) {  // equal slots before this warp's
     int n_eq = 0;
+#pragma unroll 4
     for (int i = w0; i < w1; i += 32)
       n_eq += __popc(__ballot_sync(0xffffffffu, i + lane < w1 && keys[i + lane] == prefix));
     if (lane == 0) warp_sum[warp] = n_eq;
     __syncthreads();
-    eq0 = __reduce_add_sync(0xffffffffu, lane < warp ? warp_sum[lane] : 0);
+    eq = __reduce_add_sync(0xffffffffu, lane < warp ? warp_sum[lane] : 0);
   }
-  int below = 0, above = 0, eq = eq0;
+#pragma unroll 4
   for (int i = w0; i < w1; i += 32) {
     const uint32_t k = kept.bits(i + lane < w1, i + lane < w1 ? keys[i + lane] : 0u, eq);
-    const uint32_t m = evict_below(i, keep);
-    below += __popc(k & m), above += __popc(k & ~m);
+    if (lane == 0) bits[i >> 5] = k;
   }
-  if (lane == 0) warp_pair[warp] = make_int2(below, above);
+  __syncthreads();
+  // a strip of 32 slots per thread: kept slots before it, below `keep` and from there on
+  const bool on = tid * 32 < len;
+  const uint32_t k = on ? bits[tid] : 0u, m = on ? evict_below(tid * 32, keep) : 0u;
+  int below = __popc(k & m), above = __popc(k & ~m);
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, below, d), y = __shfl_up_sync(0xffffffffu, above, d);
+    if (lane >= d) below += x, above += y;
+  }
+  if (lane == 31) warp_pair[warp] = make_int2(below, above);
+  below -= __popc(k & m), above -= __popc(k & ~m);
   __syncthreads();
   const int2 of = warp_pair[lane];
   const int n = keep - __reduce_add_sync(0xffffffffu, of.x);  // freed slots, and as many moving ones
-  below = __reduce_add_sync(0xffffffffu, lane < warp ? of.x : 0);
-  above = __reduce_add_sync(0xffffffffu, lane < warp ? of.y : 0);
-  // this CTA's pairs m0 .. m1 - 1, listed in shared memory; strips of 32 kept slots' values are shared out, too
+  below += __reduce_add_sync(0xffffffffu, lane < warp ? of.x : 0);
+  above += __reduce_add_sync(0xffffffffu, lane < warp ? of.y : 0);
+  // this CTA's pairs m0 .. m1 - 1, listed in shared memory
   const int share = evict_share(p.Lk, copies), each = (n + copies - 1) / copies;
   const int m0 = min(rank * each, n), m1 = min(m0 + each, n);
   uint16_t* freed = reinterpret_cast<uint16_t*>(keys + p.Lk);
   uint16_t* moving = freed + share;
-  const uint32_t lower = (1u << lane) - 1u;
-  int turn = (w0 >> 5) % copies;
-  eq = eq0;
-  for (int i = w0; i < w1; i += 32) {
-    const int j = i + lane;
-    const uint32_t k = kept.bits(j < w1, j < w1 ? keys[j] : 0u, eq);
-    const uint32_t m = evict_below(i, keep);
-    const bool mine = (k >> lane) & 1u;
-    if (m != 0u) {
-      const int number = j - below - __popc(k & lower);
-      if (((m >> lane) & 1u) && !mine && number >= m0 && number < m1) freed[number - m0] = static_cast<uint16_t>(j);
-      if (turn == rank && mine && ((m >> lane) & 1u)) {
-        p.weight_out[row + j] = w[j];
-        p.pos_out[row + j] = pos[j];
-      }
-    }
-    if (~m != 0u) {
-      const int number = above + __popc(k & ~m & lower);
-      if (mine && !((m >> lane) & 1u) && number >= m0 && number < m1) moving[number - m0] = static_cast<uint16_t>(j);
-    }
-    below += __popc(k & m), above += __popc(k & ~m);
-    if (++turn == copies) turn = 0;
-  }
+  if (on) evict_list(tid * 32, k, m, below, above, m0, m1, freed, moving);
   __syncthreads();
   evict_move(p, bh, moving, freed, m1 - m0, tid, kEvictThreads);
+  evict_stay(p, bh, bits, 0, len, all, step);
   evict_clear(p, bh, keep, all, step);
 }
 
@@ -362,6 +405,7 @@ __global__ void __launch_bounds__(kEvictClusterThreads) attn_cache_evict_cluster
   extern __shared__ uint32_t keys[];
   __shared__ __align__(16) int hist[4][BINS];
   __shared__ int first[4][BINS];  // the first digit's, by lane: the weights' exponents meet in few bins
+  __shared__ uint32_t bits[kEvictMaxLk / 8 / 32];  // kept slots
   __shared__ int warp_sum[NW];
   __shared__ int2 warp_pair[NW];
   __shared__ __align__(16) int4 quad_sum[NC][BINS / 4];
@@ -388,13 +432,7 @@ __global__ void __launch_bounds__(kEvictClusterThreads) attn_cache_evict_cluster
   auto key_at = [&](int j) { return CACHED ? keys[j - j0] : evict_key(w[j], pos[j], recent_from); };
   for (int i = tid; i < 4 * BINS; i += kEvictClusterThreads) (&hist[0][0])[i] = (&first[0][0])[i] = 0;
   __syncthreads();
-#pragma unroll 8
-  for (int i = w0; i < w1; i += 32) {
-    const bool in = i + lane < w1;
-    const uint32_t key = in ? evict_key(w[i + lane], pos[i + lane], recent_from) : 0u;
-    if (CACHED && in) keys[i + lane - j0] = key;
-    evict_count(first[lane & 3], in ? static_cast<int>(key >> 24) : -1);
-  }
+  evict_load(p, bh, w0, w1, j0, CACHED ? keys : nullptr, recent_from, first[lane & 3], 24);
   __syncthreads();
   if (tid < BINS) hist[0][tid] = first[0][tid] + first[1][tid] + first[2][tid] + first[3][tid];
   uint32_t prefix = 0;
@@ -458,25 +496,28 @@ __global__ void __launch_bounds__(kEvictClusterThreads) attn_cache_evict_cluster
     }
   }
   const EvictKept kept{prefix, need, need < s_equal};
-  int eq0 = 0;
+  int eq = 0;
   if (kept.ties) {  // equal slots before this warp's
     const int bin = static_cast<int>(prefix & 255u);
     int of[NC];
 #pragma unroll
     for (int r = 0; r < NC; ++r) of[r] = ld_cluster(cluster_map(smem_u32(&hist[3][bin]), r));
 #pragma unroll
-    for (int r = 0; r < NC; ++r) eq0 += r < rank ? of[r] : 0;
+    for (int r = 0; r < NC; ++r) eq += r < rank ? of[r] : 0;
     int n_eq = 0;
+#pragma unroll 4
     for (int i = w0; i < w1; i += 32)
       n_eq += __popc(__ballot_sync(0xffffffffu, i + lane < w1 && key_at(i + lane) == prefix));
     if (lane == 0) warp_sum[warp] = n_eq;
     __syncthreads();
-    for (int k = 0; k < warp; ++k) eq0 += warp_sum[k];
+    for (int k = 0; k < warp; ++k) eq += warp_sum[k];
   }
-  int below = 0, above = 0, eq = eq0;
+  int below = 0, above = 0;  // kept slots of the warp, on either side of `keep`
+#pragma unroll 4
   for (int i = w0; i < w1; i += 32) {
     const uint32_t k = kept.bits(i + lane < w1, i + lane < w1 ? key_at(i + lane) : 0u, eq);
     const uint32_t m = evict_below(i, keep);
+    if (lane == 0) bits[(i - j0) >> 5] = k;
     below += __popc(k & m), above += __popc(k & ~m);
   }
   if (lane == 0) warp_pair[warp] = make_int2(below, above);
@@ -489,7 +530,7 @@ __global__ void __launch_bounds__(kEvictClusterThreads) attn_cache_evict_cluster
   below = __reduce_add_sync(0xffffffffu, lane < warp ? of.x : 0);
   above = __reduce_add_sync(0xffffffffu, lane < warp ? of.y : 0);
   cluster_sync_all();
-  int n = keep;
+  int n = keep;  // freed slots, and as many moving ones
   {
     int bl[NC], ab[NC];
 #pragma unroll
@@ -506,23 +547,22 @@ __global__ void __launch_bounds__(kEvictClusterThreads) attn_cache_evict_cluster
   const int cap = p.Lk / 2;  // min(keep, len - keep) slots at most
   int32_t* freed = p.lists + static_cast<size_t>(bh) * 2 * cap;
   int32_t* moving = freed + cap;
-  const uint32_t lower = (1u << lane) - 1u;
-  eq = eq0;
-  for (int i = w0; i < w1; i += 32) {
-    const int j = i + lane;
-    const uint32_t k = kept.bits(j < w1, j < w1 ? key_at(j) : 0u, eq);
-    const uint32_t m = evict_below(i, keep);
-    const bool mine = (k >> lane) & 1u, low = (m >> lane) & 1u;
-    if (low && !mine) freed[j - below - __popc(k & lower)] = j;
-    if (!low && mine) moving[above + __popc(k & ~m & lower)] = j;
-    if (low && mine) {
-      p.weight_out[row + j] = w[j];
-      p.pos_out[row + j] = pos[j];
+  // a strip of 32 slots per lane
+  for (int i0 = w0; i0 < w1; i0 += 1024) {
+    const int i = i0 + 32 * lane;
+    const uint32_t k = i < w1 ? bits[(i - j0) >> 5] : 0u, m = i < w1 ? evict_below(i, keep) : 0u;
+    int b0 = __popc(k & m), a0 = __popc(k & ~m);
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, b0, d), y = __shfl_up_sync(0xffffffffu, a0, d);
+      if (lane >= d) b0 += x, a0 += y;
     }
-    below += __popc(k & m), above += __popc(k & ~m);
+    if (i < w1) evict_list(i, k, m, below + b0 - __popc(k & m), above + a0 - __popc(k & ~m), 0, n, freed, moving);
+    below += __shfl_sync(0xffffffffu, b0, 31), above += __shfl_sync(0xffffffffu, a0, 31);
   }
   cluster_sync_all();  // the lists are written (and no CTA's shared memory is read any more)
   evict_move(p, bh, moving, freed, n, all, step);
+  evict_stay(p, bh, bits, j0, j1, tid, kEvictClusterThreads);
   evict_clear(p, bh, keep, all, step);
 }
 
