@@ -56,7 +56,13 @@ attn_status_t check_key_weight(int B, int Hq, int Hkv, int Lq, int Lk, int D) {
   if (s == ATTN_ERR_INVALID_ARG) return s;
   if (Hq % Hkv != 0) return ATTN_ERR_INVALID_ARG;
   if (s != ATTN_OK) return s;
-  if (static_cast<long long>(Hq / Hkv) * Lq > (1 << 30)) return ATTN_ERR_UNSUPPORTED;
+  const long long rows = static_cast<long long>(Hq / Hkv) * Lq;
+  if (rows > (1 << 30)) return ATTN_ERR_UNSUPPORTED;
+  // the kernels count key tiles of 128, or steps of 256 keys x 64 rows (at
+  // most G partly filled row tiles more), in 32 bits
+  const long long heads = static_cast<long long>(B) * Hkv, row_tiles = rows / 64 + Hq / Hkv + 1;
+  if (heads * ((Lk + 127) / 128) > 0x7fff0000LL) return ATTN_ERR_UNSUPPORTED;
+  if (rows > kKeyWeightFewRows && heads * ((Lk + 255) / 256) > 0x7fff0000LL / row_tiles) return ATTN_ERR_UNSUPPORTED;
   return ATTN_OK;
 }
 
@@ -154,6 +160,7 @@ extern "C" attn_status_t attn_key_weight(const void* q, const void* k, const flo
   // a list per query head lets causal calls leave out the row tiles above the
   // diagonal; short or individually limited rows fill tiles better packed
   p.packed = limit || Lq < 64;
+  p.rows_per_step = key_weight_rows_per_step(D);
   p.scale_log2 = scale_log2_of(scale), p.status = status, p.limit_ns = shared_wait_limit_ns();
   const bool bf16 = dtype == ATTN_DTYPE_BF16;
   switch (D) {

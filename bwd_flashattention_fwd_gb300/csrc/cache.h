@@ -64,9 +64,13 @@ struct KeyWeightParams {
   float scale_log2;
   int* status;
   uint64_t limit_ns;
+  int rows_per_step;  // many rows: Q rows per step
   int packed;   // many rows: the G x Lq rows of a KV head form one list (else a list per query head)
   float* part;  // many rows: [CTAs][2][256] partial sums
 };
+
+// Q rows per step of the kernel for many rows: what tensor memory holds beside K of 256 keys.
+__host__ __device__ constexpr int key_weight_rows_per_step(int D) { return D <= 128 ? 128 : 64; }
 
 // G * Lq rows up to which a KV head's rows stay in shared memory together.
 constexpr int kKeyWeightFewRows = 128;
