@@ -44,7 +44,7 @@ attn_status_t check_tree(int B, int Hq, int Hkv, int T, int Lk, int D) {
   if (s != ATTN_OK) return s;
   if (T > kTreeMaxT || B > kTreeMaxB) return ATTN_ERR_UNSUPPORTED;
   // stages of the whole call, and the combine kernel's rows per KV head, are ints that a grid takes
-  const long long stages = (Lk + kTreeStage - 1) / kTreeStage + (T + kTreeStage - 1) / kTreeStage;
+  const long long stages = (Lk + kTreeStage - 1) / kTreeStage + (T + kTreeStage - 1) / kTreeStage + kTreeExtra;
   if (stages * B * Hkv > 0x7fffffffLL) return ATTN_ERR_UNSUPPORTED;
   if (static_cast<long long>(Hq / Hkv) * T > 65535) return ATTN_ERR_UNSUPPORTED;
   return ATTN_OK;
@@ -195,8 +195,7 @@ extern "C" attn_status_t attn_cache_append(const void* k_new, const void* v_new,
                  kv_pitch ? kv_pitch : Lk, B, Hkv, T, Lk, D / 8, status};
   const long long pieces = (static_cast<long long>(T) * p.row16 + kAppendThreads - 1) / kAppendThreads;
   const int gx = static_cast<int>(pieces < 64 ? pieces : 64);
-  attn_cache_append_kernel<<<dim3(gx, B * Hkv), kAppendThreads, 0, stream>>>(p);
-  return launched();
+  return finish(launch_dependent(attn_cache_append_kernel, dim3(gx, B * Hkv), kAppendThreads, 0, stream, p));
 }
 
 extern "C" size_t attn_cache_evict_workspace_bytes(int B, int Hkv, int Lk) {
@@ -232,11 +231,9 @@ extern "C" attn_status_t attn_cache_evict(void* k, void* v, const float* weight,
   if (Lk <= kEvictRowKeys) {
     // about one CTA per SM, so that the moves run at the memory's rate
     const int copies = heads < num_sms ? num_sms / heads : 1;
-    if (cudaFuncSetAttribute(attn_cache_evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(evict_smem(kEvictRowKeys, 1))) != cudaSuccess)
-      return ATTN_ERR_CUDA;
-    attn_cache_evict_kernel<<<heads * copies, kEvictThreads, evict_smem(Lk, copies), stream>>>(p, copies);
-    return launched();
+    if (!set_smem_limit(attn_cache_evict_kernel, evict_smem(kEvictRowKeys, 1))) return ATTN_ERR_CUDA;
+    return finish(launch_dependent(attn_cache_evict_kernel, dim3(heads * copies), kEvictThreads,
+                                   evict_smem(Lk, copies), stream, p, copies));
   }
   // sixteen CTAs per KV head where they still fit one wave; a CTA's part of
   // the slots: every warp's share is a multiple of 32
@@ -246,8 +243,7 @@ extern "C" attn_status_t attn_cache_evict(void* k, void* v, const float* weight,
   auto kern = nc == 16 ? (cached ? attn_cache_evict_cluster_kernel<true, 16> : attn_cache_evict_cluster_kernel<false, 16>)
                        : (cached ? attn_cache_evict_cluster_kernel<true, 8> : attn_cache_evict_cluster_kernel<false, 8>);
   const size_t smem = cached ? static_cast<size_t>(part) * 4 : 0;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kEvictKeys * 4) != cudaSuccess)
-    return ATTN_ERR_CUDA;
+  if (!set_smem_limit(kern, kEvictKeys * 4)) return ATTN_ERR_CUDA;
   if (nc == 16 && cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
     return ATTN_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};

@@ -9,7 +9,7 @@ namespace gbattn {
 constexpr int kTreeMaxT = 1024;   // drafts per sequence (the mask is T x T bytes per sequence)
 constexpr int kTreeMaxB = 1024;   // sequences (each CTA holds the lengths' prefix sums in shared memory)
 constexpr int kTreeStage = 64;    // keys per pipeline stage
-constexpr int kTreeMinStages = 1;  // least stages a CTA takes
+constexpr int kTreeExtra = 7;      // what a CTA spends on a KV head besides its stages, in stages
 constexpr int kTreeMaxCtas = 152;  // one per SM of a GB300
 constexpr int kEvictMaxLk = 1 << 20;
 constexpr int kEvictRowKeys = 16384;  // slots up to which one CTA holds a KV head's keys in shared memory
@@ -108,5 +108,32 @@ GBATTN_DECLARE_CACHE_LAUNCHERS(128)
 GBATTN_DECLARE_CACHE_LAUNCHERS(256)
 
 #undef GBATTN_DECLARE_CACHE_LAUNCHERS
+
+// Launch as a programmatic dependent of the kernel before it on the stream:
+// its CTAs may start (and set up) while that kernel finishes; every kernel of
+// the cache calls waits for it (griddepcontrol.wait) before it reads or writes
+// global memory, so stream order holds for the caller.  (A kernel whose shared
+// memory depends on the call has its limit set by set_smem_limit, to the same
+// value every time: callers on other threads may be about to launch it.)
+template <typename Kern>
+bool set_smem_limit(Kern kern, size_t smem) {
+  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) == cudaSuccess;
+}
+
+template <typename... Params, typename... Args>
+int launch_dependent(void (*kern)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t stream, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kern, args...) != cudaSuccess) return kLaunchCudaError;
+  return cudaPeekAtLastError() == cudaSuccess ? kLaunchOk : kLaunchCudaError;
+}
 
 }  // namespace gbattn

@@ -33,22 +33,6 @@ bool make_map(EncodeTiledFn enc, bool bf16, CUtensorMap* m, const void* base, lo
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Launch as a programmatic dependent of the kernel before it on the stream.
-template <typename Kern, typename... Args>
-int launch_dependent(Kern kern, dim3 grid, int threads, cudaStream_t stream, Args... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, kern, args...) != cudaSuccess) return kLaunchCudaError;
-  return cudaPeekAtLastError() == cudaSuccess ? kLaunchOk : kLaunchCudaError;
-}
-
 template <bool BF16, int QS, int NT>
 int tree_impl(const TreeParams& p, EncodeTiledFn enc, cudaStream_t stream) {
   using Gm = TreeGeom<kD, QS, NT>;
@@ -61,17 +45,18 @@ int tree_impl(const TreeParams& p, EncodeTiledFn enc, cudaStream_t stream) {
       !make_map(enc, BF16, &tvn, p.v_new, p.T, heads, Gm::BK, p.T))
     return kLaunchBadMap;
   auto kern = attn_tree_kernel<kD, BF16, QS, NT>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Gm::SMEM_BYTES) != cudaSuccess)
-    return kLaunchCudaError;
-  kern<<<p.n_groups * p.n_rb, Gm::NUM_THREADS, Gm::SMEM_BYTES, stream>>>(tq, tk, tv, tkn, tvn, p);
-  if (cudaPeekAtLastError() != cudaSuccess) return kLaunchCudaError;
+  if (!set_smem_limit(kern, Gm::SMEM_BYTES)) return kLaunchCudaError;
+  const int r = launch_dependent(kern, dim3(p.n_groups * p.n_rb), Gm::NUM_THREADS,
+                                 Gm::SMEM_BYTES, stream, tq, tk, tv, tkn, tvn, p);
+  if (r != kLaunchOk) return r;
   if (p.n_groups == 1) return kLaunchOk;  // no KV head is shared
   // warps per 4 columns by how many partials a head has on average
   const long long avg = p.n_groups / heads + 1;
   auto combine = [&](auto kern_c, int cols_per_block) {
     const long long tasks = heads * ((R + 31) / 32) * (kD / cols_per_block);
-    const long long most = 4LL * kTreeMaxCtas;  // resident beside the attention kernel's CTAs
-    return launch_dependent(kern_c, dim3(static_cast<unsigned>(tasks < most ? tasks : most)), 256, stream, p, Gm::ROWS);
+    const long long most = 8LL * kTreeMaxCtas;  // one wave
+    return launch_dependent(kern_c, dim3(static_cast<unsigned>(tasks < most ? tasks : most)), 256, 0, stream, p,
+                            static_cast<int>(Gm::ROWS));
   };
   if (avg > 8) return combine(attn_tree_combine_kernel<kD, BF16, 8>, 4);
   if (avg > 3) return combine(attn_tree_combine_kernel<kD, BF16, 2>, 16);
@@ -95,12 +80,11 @@ int key_weight_few(const KeyWeightParams& p, int num_sms, EncodeTiledFn enc, cud
   CUtensorMap tq, tk;
   if (!make_map(enc, BF16, &tq, p.q, R, heads, NQ, R) || !make_map(enc, BF16, &tk, p.k, p.Lk, heads, Gm::BK, p.kv_pitch))
     return kLaunchBadMap;
-  auto kern = attn_key_weight_few_kernel<kD, BF16, NQ>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Gm::SMEM_BYTES) != cudaSuccess)
-    return kLaunchCudaError;
   const long long tiles = heads * ((p.Lk + Gm::BK - 1) / Gm::BK);
-  kern<<<static_cast<unsigned>(tiles < num_sms ? tiles : num_sms), Gm::NUM_THREADS, Gm::SMEM_BYTES, stream>>>(tq, tk, p);
-  return cudaPeekAtLastError() == cudaSuccess ? kLaunchOk : kLaunchCudaError;
+  auto kern = attn_key_weight_few_kernel<kD, BF16, NQ>;
+  if (!set_smem_limit(kern, Gm::SMEM_BYTES)) return kLaunchCudaError;
+  return launch_dependent(kern, dim3(static_cast<unsigned>(tiles < num_sms ? tiles : num_sms)), Gm::NUM_THREADS,
+                          Gm::SMEM_BYTES, stream, tq, tk, p);
 }
 
 template <bool BF16>
@@ -112,14 +96,13 @@ int key_weight_many(const KeyWeightParams& p, int num_sms, EncodeTiledFn enc, cu
   if (!make_map(enc, BF16, &tq, p.q, rows, p.packed ? heads : heads * p.G, Gm::NQ, rows) ||
       !make_map(enc, BF16, &tk, p.k, p.Lk, heads, 128, p.kv_pitch))
     return kLaunchBadMap;
-  auto kern = attn_key_weight_kernel<kD, BF16>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Gm::SMEM_BYTES) != cudaSuccess)
-    return kLaunchCudaError;
   const int groups = num_sms < kTreeMaxCtas ? num_sms : kTreeMaxCtas;
-  kern<<<groups, Gm::NUM_THREADS, Gm::SMEM_BYTES, stream>>>(tq, tk, p);
-  if (cudaPeekAtLastError() != cudaSuccess) return kLaunchCudaError;
+  auto kern = attn_key_weight_kernel<kD, BF16>;
+  if (!set_smem_limit(kern, Gm::SMEM_BYTES)) return kLaunchCudaError;
+  const int r = launch_dependent(kern, dim3(groups), Gm::NUM_THREADS, Gm::SMEM_BYTES, stream, tq, tk, p);
+  if (r != kLaunchOk) return r;
   const long long tiles = heads * ((p.Lk + Gm::BK - 1) / Gm::BK), most = 4LL * kTreeMaxCtas;
-  return launch_dependent(attn_key_weight_join_kernel, dim3(static_cast<unsigned>(tiles < most ? tiles : most)), 256,
+  return launch_dependent(attn_key_weight_join_kernel, dim3(static_cast<unsigned>(tiles < most ? tiles : most)), 256, 0,
                           stream, p, groups);
 }
 

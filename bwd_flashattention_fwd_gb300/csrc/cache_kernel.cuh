@@ -21,6 +21,8 @@ constexpr int kAppendThreads = 256;
 // writes the sequence's lengths and key limits.
 __global__ void __launch_bounds__(kAppendThreads) attn_cache_append_kernel(const AppendParams p) {
   __shared__ int cut;
+  grid_dependency_wait();  // the kernels before this one are complete
+  if (threadIdx.x == 0) grid_launch_dependents();
   const int bh = blockIdx.y, b = bh / p.Hkv;
   const int len = clamp_len(p.cache_len[b], p.Lk);
   int n = clamp_len(p.accept_len ? p.accept_len[b] : p.T, p.T);
@@ -269,6 +271,8 @@ __global__ void __launch_bounds__(kEvictThreads, 1) attn_cache_evict_kernel(cons
   __shared__ int warp_sum[32];
   __shared__ int2 warp_pair[32];
   __shared__ int s_digit, s_need, s_equal;
+  grid_dependency_wait();  // the kernels before this one are complete
+  if (threadIdx.x == 0) grid_launch_dependents();
   const int bh = blockIdx.x / copies, rank = blockIdx.x - bh * copies, b = bh / p.Hkv;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int len = clamp_len(p.cache_len[b], p.Lk);

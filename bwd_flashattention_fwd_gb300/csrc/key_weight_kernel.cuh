@@ -221,6 +221,8 @@ __global__ void __launch_bounds__(320, 1)
     tmem_alloc(smem_u32(&tmem_slot), Gm::TMEM_COLS);
     tmem_relinquish();
   }
+  grid_dependency_wait();  // the kernels before this one are complete
+  if (threadIdx.x == 0) grid_launch_dependents();
   if (p.limit) key_weight_table<BK>(p, tab);
   tc_fence_before_sync();
   __syncthreads();
@@ -534,7 +536,6 @@ __global__ void __launch_bounds__(KeyWeightGeom<D>::NUM_THREADS, 1)
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int abort_flag;
 
-  if (threadIdx.x == 0) grid_launch_dependents();  // the join kernel waits for this grid before it reads
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t sbase = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const uint32_t sK = sbase, sQ = sK + Gm::K_BYTES;
@@ -566,6 +567,8 @@ __global__ void __launch_bounds__(KeyWeightGeom<D>::NUM_THREADS, 1)
     tmem_alloc(smem_u32(&tmem_slot), Gm::TMEM_COLS);
     tmem_relinquish();
   }
+  grid_dependency_wait();                          // the kernels before this one are complete
+  if (threadIdx.x == 0) grid_launch_dependents();  // the join kernel waits for this grid before it reads partials
   if (p.limit) {
     key_weight_table<256>(p, tab);
     __syncthreads();
@@ -802,6 +805,7 @@ static __global__ void __launch_bounds__(256) attn_key_weight_join_kernel(const 
   const int per = w.per(groups);
   const long long tiles = static_cast<long long>(p.B) * p.Hkv * w.n_kt;
   grid_dependency_wait();
+  if (threadIdx.x == 0) grid_launch_dependents();
   for (long long i = blockIdx.x; i < tiles; i += gridDim.x) {
     const int head = static_cast<int>(i / w.n_kt), kt = static_cast<int>(i - static_cast<long long>(head) * w.n_kt);
     const int b = head / p.Hkv, hk = head - b * p.Hkv;

@@ -46,9 +46,13 @@
 
 namespace gbattn {
 
-// What every block derives from the lengths: pre[b] = stages of one KV head
-// of the sequences before b (pre[B] the total), and the lengths themselves.
+// What every block derives from the lengths.  The list that the CTAs divide
+// counts units: a KV head's stages, and before them `extra` units for what a
+// CTA spends on a head besides its stages (loading Q, merging and writing O:
+// about three stages' time; fewer units where the ranges are short).
+// pre[b]: units of one KV head of the sequences before b (pre[B] the total).
 struct TreeTable {
+  int extra;
   int pre[kTreeMaxB + 1];
   int len[kTreeMaxB];
   uint16_t tl[kTreeMaxB];
@@ -93,34 +97,33 @@ __device__ __forceinline__ int tree_stages(int len, int tl) {
 // Fills the table (whole block; the caller's next barrier publishes it).  Up
 // to 32 sequences, one warp does it all; more, the block loads the lengths first.
 __device__ __forceinline__ void tree_table(const TreeParams& p, TreeTable& tab) {
+  auto load = [&](int b) {
+    int len, tl;
+    tree_lengths(p, b, len, tl);
+    tab.len[b] = len;
+    tab.tl[b] = static_cast<uint16_t>(tl);
+    return tree_stages(len, tl);
+  };
   if (p.B > 32) {
-    for (int b = threadIdx.x; b < p.B; b += blockDim.x) {
-      int len, tl;
-      tree_lengths(p, b, len, tl);
-      tab.pre[b + 1] = tree_stages(len, tl);
-      tab.len[b] = len;
-      tab.tl[b] = static_cast<uint16_t>(tl);
-    }
+    for (int b = threadIdx.x; b < p.B; b += blockDim.x) tab.pre[b + 1] = load(b);
     __syncthreads();
   }
   if (threadIdx.x >= 32) return;
   const int lane = threadIdx.x;
-  if (lane == 0) tab.pre[0] = 0;
+  int mine = 0, all = 0;  // this lane's sequence (up to 32 of them); all stages of a KV head
+  if (p.B > 32) {
+    for (int b = lane; b < p.B; b += 32) all += tab.pre[b + 1];
+  } else if (lane < p.B) {
+    all = mine = load(lane);
+  }
+  all = __reduce_add_sync(0xffffffffu, all);
+  const int extra = min(kTreeExtra, all * p.Hkv / (8 * p.n_groups));
+  if (lane == 0) tab.extra = extra, tab.pre[0] = 0;
   int run = 0;
   for (int b0 = 0; b0 < p.B; b0 += 32) {
     const int b = b0 + lane;
-    int x = 0;
-    if (b < p.B) {
-      if (p.B > 32) {
-        x = tab.pre[b + 1];
-      } else {
-        int len, tl;
-        tree_lengths(p, b, len, tl);
-        x = tree_stages(len, tl);
-        tab.len[b] = len;
-        tab.tl[b] = static_cast<uint16_t>(tl);
-      }
-    }
+    int x = b >= p.B ? 0 : p.B > 32 ? tab.pre[b + 1] : mine;
+    if (x > 0) x += extra;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const int y = __shfl_up_sync(0xffffffffu, x, d);
@@ -131,7 +134,7 @@ __device__ __forceinline__ void tree_table(const TreeParams& p, TreeTable& tab) 
   }
 }
 
-// The sequence that stage x of the whole list belongs to: the largest b with pre[b] * Hkv <= x
+// The sequence that unit x of the whole list belongs to: the largest b with pre[b] * Hkv <= x
 // (pre[b] < pre[b + 1] there, as x is below the total).
 __device__ __forceinline__ int tree_find(const int* pre, int B, int Hkv, int x) {
   int lo = 0, hi = B - 1;
@@ -143,53 +146,53 @@ __device__ __forceinline__ int tree_find(const int* pre, int B, int Hkv, int x) 
   return lo;
 }
 
-// Stages per CTA range.
-__device__ __forceinline__ int tree_per(int total, int n_groups) {
-  const int per = (total + n_groups - 1) / n_groups;
-  return per > kTreeMinStages ? per : kTreeMinStages;
-}
+// Units per CTA range.
+__device__ __forceinline__ int tree_per(int total, int n_groups) { return (total + n_groups - 1) / n_groups; }
 
-// Walks a CTA's range [x, xe) of the stage list, one KV head at a time: the
-// segment is stages j0 .. j1 - 1 of the n stages of head (b, hk).
+// Walks a CTA's range [lo, xe) of the list, one KV head at a time: the segment
+// is stages j0 .. j1 - 1 of the n of head (b, hk).  A range that ends among a
+// head's extra units leaves the head to the next one.
 struct TreeWalk {
-  const int* pre;
-  int Hkv, lo, x, xe;
+  const TreeTable& tab;
+  int Hkv, lo, xe, s;
   int b, hk, n, j0, j1;
-  __device__ __forceinline__ TreeWalk(const TreeParams& p, const int* pre_, int group)
-      : pre(pre_), Hkv(p.Hkv) {
-    const int total = pre[p.B] * p.Hkv, per = tree_per(total, p.n_groups);
+  bool more_;
+  __device__ __forceinline__ TreeWalk(const TreeParams& p, const TreeTable& tab_, int group) : tab(tab_), Hkv(p.Hkv) {
+    const int total = tab.pre[p.B] * p.Hkv, per = tree_per(total, p.n_groups);
     const long long from = static_cast<long long>(group) * per;
-    x = lo = from < total ? static_cast<int>(from) : total;
+    lo = from < total ? static_cast<int>(from) : total;
     xe = from + per < total ? static_cast<int>(from + per) : total;
-    if (x < xe) {
-      b = tree_find(pre, p.B, Hkv, x);
-      n = pre[b + 1] - pre[b];
-      hk = (x - pre[b] * Hkv) / n;
-      set();
+    more_ = lo < xe;
+    if (more_) {
+      b = tree_find(tab.pre, p.B, p.Hkv, lo);
+      hk = (lo - tab.pre[b] * Hkv) / (tab.pre[b + 1] - tab.pre[b]);
+      set(lo);
     }
   }
-  __device__ __forceinline__ bool more() const { return x < xe; }
-  __device__ __forceinline__ void set() {
-    const int s = pre[b] * Hkv + hk * n;
-    j0 = x - s;
-    j1 = min(xe - s, n);
+  __device__ __forceinline__ bool more() const { return more_; }
+  __device__ __forceinline__ void set(int x) {  // the segment that holds unit x
+    const int units = tab.pre[b + 1] - tab.pre[b];
+    s = tab.pre[b] * Hkv + hk * units;
+    n = units - tab.extra;
+    j0 = max(x - s - tab.extra, 0);
+    j1 = min(xe - s, units) - tab.extra;
+    more_ = j1 > j0;
   }
   __device__ __forceinline__ void next() {
-    x += j1 - j0;
-    if (x >= xe) return;
+    const int x = s + tab.extra + j1;
+    more_ = x < xe;
+    if (!more_) return;
     if (++hk == Hkv) {
       hk = 0;
-      do {
-        ++b;
-        n = pre[b + 1] - pre[b];
-      } while (n == 0);
+      do ++b;
+      while (tab.pre[b + 1] == tab.pre[b]);
     }
-    set();
+    set(x);
   }
   // the segment is the whole KV head
   __device__ __forceinline__ bool whole() const { return j0 == 0 && j1 == n; }
-  // where a partial segment goes: 0 at the start of the range, 1 behind it (cut off by its end)
-  __device__ __forceinline__ int slot() const { return x == lo ? 0 : 1; }
+  // where a partial segment goes: 0 if it is the range's first, 1 behind another (cut off by the range's end)
+  __device__ __forceinline__ int slot() const { return s > lo ? 1 : 0; }
 };
 
 // First partial row of (group, slot, row block): slot 0 holds the segment at
@@ -219,8 +222,6 @@ __global__ void __launch_bounds__(TreeGeom<D, QS, NT>::NUM_THREADS, 1)
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int abort_flag;
 
-  // the combine kernel may start; it waits for this grid before it reads
-  if (threadIdx.x == 0) grid_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t sbase = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const uint32_t sQ = sbase;                  // tile t at sQ + t * Q_BYTES
@@ -256,12 +257,15 @@ __global__ void __launch_bounds__(TreeGeom<D, QS, NT>::NUM_THREADS, 1)
     tmem_alloc(smem_u32(&tmem_slot), Gm::TMEM_COLS);
     tmem_relinquish();
   }
+  grid_dependency_wait();  // the kernels before this one are complete
+  // the combine kernel may start; it waits for this grid before it reads partials
+  if (threadIdx.x == 0) grid_launch_dependents();
   tree_table(p, tab);
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem = tmem_slot;
-  TreeWalk w(p, tab.pre, group);
+  TreeWalk w(p, tab, group);
 
   if (warp == PRODUCER) {
     // ---------------- TMA producer (whole warp, one elected lane issues) ----------------
@@ -686,38 +690,52 @@ __global__ void __launch_bounds__(256) attn_tree_combine_kernel(const TreeParams
   tree_table(p, tab);
   __syncthreads();
   const int* pre = tab.pre;
-  const int total = pre[p.B] * p.Hkv, per = tree_per(total, p.n_groups);
+  const int per = tree_per(pre[p.B] * p.Hkv, p.n_groups);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int sub = warp % NS;
   const int R = p.G * p.T, rgs = (R + 31) / 32;
   const long long tasks = static_cast<long long>(p.B) * p.Hkv * rgs * QB;
   grid_dependency_wait();  // the partials are written (and the whole call ends behind them)
+  if (threadIdx.x == 0) grid_launch_dependents();
   for (long long task = blockIdx.x; task < tasks; task += gridDim.x) {
     const int head = static_cast<int>(task / (rgs * QB)), rest = static_cast<int>(task % (rgs * QB));
     const int rg = rest / QB, q = (rest - rg * QB) * QPB + warp / NS;
     const int b = head / p.Hkv, hk = head - b * p.Hkv;
     const int n = pre[b + 1] - pre[b];
-    const int s = pre[b] * p.Hkv + hk * n;
-    const int g0 = s / per, ng = n > 0 ? (s + n - 1) / per - g0 + 1 : 0;
+    const int s = pre[b] * p.Hkv + hk * n;  // the head's units; its stages begin at s + extra
+    const int g0 = (s + tab.extra) / per, ng = n > 0 ? (s + n - 1) / per - g0 + 1 : 0;
     if (ng < 2) continue;  // written by its CTA (the same for the whole block)
     const int row = rg * 32 + lane, rb = rg * 32 / rows, r0 = rg * 32 - rb * rows;
-    // the head's first partial is its group's second one, unless the head starts the group's range
-    const int first = s != g0 * per ? 1 : 0;
+    const int first = s > g0 * per ? 1 : 0;  // slot of the head's first partial
     auto part_row = [&](int i) { return tree_slot_row(p, g0 + i, i == 0 ? first : 0, rb, rows) + r0; };
     float M = -INFINITY, den = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     if (row < R) {
-#pragma unroll 4
-      for (int i = sub; i < ng; i += NS) M = fmaxf(M, p.part_lse[part_row(i) + lane]);
-#pragma unroll 4
-      for (int i = sub; i < ng; i += NS) {
-        const size_t r = part_row(i);
-        const float L = p.part_lse[r + lane];
-        const float4 x = *reinterpret_cast<const float4*>(p.part + r * D + q * 128 + lane * 4);
-        const float wgt = L == -INFINITY ? 0.f : exp2f(L - M);
-        den += wgt;
-        acc.x = fmaf(wgt, x.x, acc.x), acc.y = fmaf(wgt, x.y, acc.y);
-        acc.z = fmaf(wgt, x.z, acc.z), acc.w = fmaf(wgt, x.w, acc.w);
+      // four partials at a time, all their loads in flight
+      for (int i = sub; i < ng; i += 4 * NS) {
+        float L[4];
+        float4 x[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          L[u] = -INFINITY;
+          if (i + u * NS < ng) {
+            const size_t r = part_row(i + u * NS);
+            L[u] = p.part_lse[r + lane];
+            x[u] = *reinterpret_cast<const float4*>(p.part + r * D + q * 128 + lane * 4);
+          }
+        }
+        const float Mn = fmaxf(M, fmaxf(fmaxf(L[0], L[1]), fmaxf(L[2], L[3])));
+        const float a = M == -INFINITY ? 0.f : exp2f(M - Mn);
+        den *= a, acc.x *= a, acc.y *= a, acc.z *= a, acc.w *= a;
+        M = Mn;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          if (L[u] == -INFINITY) continue;
+          const float wgt = exp2f(L[u] - M);
+          den += wgt;
+          acc.x = fmaf(wgt, x[u].x, acc.x), acc.y = fmaf(wgt, x[u].y, acc.y);
+          acc.z = fmaf(wgt, x[u].z, acc.z), acc.w = fmaf(wgt, x[u].w, acc.w);
+        }
       }
     }
     if constexpr (NS > 1) {

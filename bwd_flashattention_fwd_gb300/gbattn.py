@@ -120,10 +120,13 @@ def status_string(status: int) -> str:
     return load_library().attn_status_string(int(status)).decode()
 
 
+_F32, _U8, _I32, _BF16, _F16 = torch.float32, torch.uint8, torch.int32, torch.bfloat16, torch.float16
+
+
 def _dtype_code(t: torch.Tensor) -> int:
-    if t.dtype == torch.bfloat16:
+    if t.dtype is _BF16:
         return ATTN_DTYPE_BF16
-    if t.dtype == torch.float16:
+    if t.dtype is _F16:
         return ATTN_DTYPE_FP16
     raise TypeError(f"unsupported dtype {t.dtype}; expected bfloat16 or float16")
 
@@ -147,29 +150,30 @@ def _require(call: str, dense=(), sliced=(), f32=(), u8=(), i32=()):
     float32 / uint8 / int32 tensors.  Every tensor must be on the current CUDA
     device.  None entries are skipped."""
     half = None
-    dev = -1
-    groups = ((dense, None, True), (sliced, None, False), (f32, torch.float32, True), (u8, torch.uint8, True),
-              (i32, torch.int32, True))
-    for ts, want, contig in groups:
+    dev = None
+    for ts, want, contig in ((dense, None, True), (sliced, None, False), (f32, _F32, True), (u8, _U8, True),
+                             (i32, _I32, True)):
         for t in ts:
             if t is None:
                 continue
-            if not isinstance(t, torch.Tensor) or not t.is_cuda:
-                raise ValueError(f"{call}: every tensor must be a CUDA tensor; got {getattr(t, 'device', type(t))}")
-            if dev < 0:
+            d = t.get_device() if isinstance(t, torch.Tensor) else -1
+            if d != dev:
+                if d < 0 or not t.is_cuda:
+                    raise ValueError(f"{call}: every tensor must be a CUDA tensor; got {getattr(t, 'device', type(t))}")
                 dev = torch.cuda.current_device()
-            if t.get_device() != dev:
-                raise ValueError(f"{call}: every tensor must be on the current CUDA device (cuda:{dev}); got {t.device}")
+                if d != dev:
+                    raise ValueError(
+                        f"{call}: every tensor must be on the current CUDA device (cuda:{dev}); got {t.device}")
             if contig and not t.is_contiguous():
                 raise ValueError(f"{call}: tensor of shape {tuple(t.shape)} strides {t.stride()} is not contiguous")
             dt = t.dtype
-            if want is None:
-                if half is None:
-                    half = dt
-                if dt is not half or (dt is not torch.bfloat16 and dt is not torch.float16):
+            if want is not None:
+                if dt is not want:
+                    raise TypeError(f"{call}: expected {want}, got {dt}")
+            elif dt is not half:
+                if half is not None or (dt is not _BF16 and dt is not _F16):
                     raise TypeError(f"{call}: 16-bit tensors must all be bfloat16 or all float16; got {dt}")
-            elif dt is not want:
-                raise TypeError(f"{call}: expected {want}, got {dt}")
+                half = dt
 
 
 def _check(status: int, call: str, check: bool) -> int:
