@@ -66,8 +66,6 @@ attn_status_t check_key_weight(int B, int Hq, int Hkv, int Lq, int Lk, int D) {
   return ATTN_OK;
 }
 
-attn_status_t launched() { return cudaPeekAtLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA; }
-
 attn_status_t finish(int r) {
   return r == kLaunchOk ? ATTN_OK : r == kLaunchBadMap ? ATTN_ERR_INVALID_ARG : ATTN_ERR_CUDA;
 }
@@ -200,7 +198,8 @@ extern "C" attn_status_t attn_cache_append(const void* k_new, const void* v_new,
 
 extern "C" size_t attn_cache_evict_workspace_bytes(int B, int Hkv, int Lk) {
   if (B < 1 || Hkv < 1 || Lk < 1 || static_cast<long long>(B) * Hkv > 65535 || Lk > kEvictMaxLk) return 0;
-  return round16(static_cast<size_t>(B) * Hkv * (Lk / 2) * 2 * sizeof(int32_t) + 16);
+  // per KV head: two lists of at most Lk / 2 slots and their length
+  return round16(static_cast<size_t>(B) * Hkv * ((Lk / 2) * 2 + 1) * sizeof(int32_t));
 }
 
 extern "C" attn_status_t attn_cache_evict(void* k, void* v, const float* weight, const int32_t* pos,
@@ -226,7 +225,9 @@ extern "C" attn_status_t attn_cache_evict(void* k, void* v, const float* weight,
   const attn_status_t ds = shared_device_state(&dev, &enc, &status, &num_sms);
   if (ds != ATTN_OK) return ds;
   EvictParams p{k, v, weight, pos, cache_len, seen, weight_out, pos_out, cache_len_out,
-                static_cast<int32_t*>(workspace), kv_pitch ? kv_pitch : Lk, B, Hkv, Lk, D / 8, keep, recent, status};
+                static_cast<int32_t*>(workspace),
+                static_cast<int32_t*>(workspace) + static_cast<size_t>(B) * Hkv * (Lk / 2) * 2,
+                kv_pitch ? kv_pitch : Lk, B, Hkv, Lk, D / 8, keep, recent, status};
   const int heads = B * Hkv;
   if (Lk <= kEvictRowKeys) {
     // about one CTA per SM, so that the moves run at the memory's rate
@@ -235,17 +236,13 @@ extern "C" attn_status_t attn_cache_evict(void* k, void* v, const float* weight,
     return finish(launch_dependent(attn_cache_evict_kernel, dim3(heads * copies), kEvictThreads,
                                    evict_smem(Lk, copies), stream, p, copies));
   }
-  // sixteen CTAs per KV head where they still fit one wave; a CTA's part of
-  // the slots: every warp's share is a multiple of 32
-  const int nc = heads * 16 <= num_sms ? 16 : 8, warps = kEvictClusterThreads / 32;
+  // a CTA's part of the slots: every warp's share is a multiple of 32
+  constexpr int nc = kEvictCluster, warps = kEvictClusterThreads / 32;
   const long long part = static_cast<long long>((((Lk + nc * warps - 1) / (nc * warps)) + 31) & ~31) * warps;
   const bool cached = part <= kEvictKeys;
-  auto kern = nc == 16 ? (cached ? attn_cache_evict_cluster_kernel<true, 16> : attn_cache_evict_cluster_kernel<false, 16>)
-                       : (cached ? attn_cache_evict_cluster_kernel<true, 8> : attn_cache_evict_cluster_kernel<false, 8>);
+  auto kern = cached ? attn_cache_evict_cluster_kernel<true> : attn_cache_evict_cluster_kernel<false>;
   const size_t smem = cached ? static_cast<size_t>(part) * 4 : 0;
   if (!set_smem_limit(kern, kEvictKeys * 4)) return ATTN_ERR_CUDA;
-  if (nc == 16 && cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
-    return ATTN_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(heads) * nc);
   cfg.blockDim = dim3(kEvictClusterThreads);
@@ -259,5 +256,6 @@ extern "C" attn_status_t attn_cache_evict(void* k, void* v, const float* weight,
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   if (cudaLaunchKernelEx(&cfg, kern, p) != cudaSuccess) return ATTN_ERR_CUDA;
-  return launched();
+  const int blocks = 4 * num_sms / heads;
+  return finish(launch_dependent(attn_cache_move_kernel, dim3(blocks > 1 ? blocks : 1, heads), 256, 0, stream, p));
 }

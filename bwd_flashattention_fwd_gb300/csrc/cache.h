@@ -12,6 +12,7 @@ constexpr int kTreeStage = 64;    // keys per pipeline stage
 constexpr int kTreeExtra = 7;      // what a CTA spends on a KV head besides its stages, in stages
 constexpr int kTreeMaxCtas = 152;  // one per SM of a GB300
 constexpr int kEvictMaxLk = 1 << 20;
+constexpr int kEvictCluster = 8;      // CTAs per KV head beyond that
 constexpr int kEvictRowKeys = 16384;  // slots up to which one CTA holds a KV head's keys in shared memory
 
 struct TreeParams {
@@ -91,7 +92,8 @@ struct EvictParams {
   const int32_t *pos, *cache_len, *seen;
   float* weight_out;
   int32_t *pos_out, *cache_len_out;
-  int32_t* lists;  // [B * Hkv][2][Lk / 2]: freed slots, then the kept slots that move into them
+  int32_t* lists;   // [B * Hkv][2][Lk / 2]: freed slots, then the kept slots that move into them
+  int32_t* counts;  // [B * Hkv]: how many
   int64_t kv_pitch;
   int B, Hkv, Lk, row16, keep, recent;
   int* status;

@@ -396,15 +396,17 @@ __device__ __forceinline__ int ld_cluster(uint32_t addr) {
   return v;
 }
 
-// The same for longer rows, one cluster of NC CTAs per KV head; each CTA owns
+// The same for longer rows, one cluster of 8 CTAs per KV head (of 16: 28.8 us
+// for 32768 slots where 8 take 27.9); each CTA owns
 // a consecutive part of the slots and keeps their keys in shared memory
 // (CACHED; parts that do not fit are read again in each pass).  Four digits of
 // 8 bits: what a digit costs is reading every CTA's histogram through
 // distributed shared memory (2048 bins: 2.3 us a digit, 256: 0.6) and a cluster
 // barrier.  Each digit has a histogram of its own, so none is cleared while
 // others read it.  Prefix sums run over warps and CTAs; the lists are in the workspace.
-template <bool CACHED, int NC>
+template <bool CACHED>
 __global__ void __launch_bounds__(kEvictClusterThreads) attn_cache_evict_cluster_kernel(const EvictParams p) {
+  constexpr int NC = kEvictCluster;
   constexpr int NW = kEvictClusterThreads / 32, BINS = 256;
   extern __shared__ uint32_t keys[];
   __shared__ __align__(16) int hist[4][BINS];
@@ -415,6 +417,7 @@ __global__ void __launch_bounds__(kEvictClusterThreads) attn_cache_evict_cluster
   __shared__ __align__(16) int4 quad_sum[NC][BINS / 4];
   __shared__ int s_digit, s_need, s_equal;
   __shared__ int s_counts[2];
+  if (threadIdx.x == 0) grid_launch_dependents();  // the move kernel waits for this grid
   const int rank = static_cast<int>(cluster_ctarank());
   const int bh = blockIdx.x / NC, b = bh / p.Hkv, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int len = clamp_len(p.cache_len[b], p.Lk);
@@ -422,6 +425,7 @@ __global__ void __launch_bounds__(kEvictClusterThreads) attn_cache_evict_cluster
   const int all = rank * kEvictClusterThreads + tid, step = NC * kEvictClusterThreads;  // this thread among the cluster's
   if (all == 0 && bh == b * p.Hkv) p.cache_len_out[b] = min(len, keep);
   if (len <= keep) {  // the same for the whole cluster
+    if (all == 0) p.counts[bh] = 0;
     evict_nothing(p, bh, len, all, step);
     return;
   }
@@ -564,10 +568,20 @@ __global__ void __launch_bounds__(kEvictClusterThreads) attn_cache_evict_cluster
     if (i < w1) evict_list(i, k, m, below + b0 - __popc(k & m), above + a0 - __popc(k & ~m), 0, n, freed, moving);
     below += __shfl_sync(0xffffffffu, b0, 31), above += __shfl_sync(0xffffffffu, a0, 31);
   }
-  cluster_sync_all();  // the lists are written (and no CTA's shared memory is read any more)
-  evict_move(p, bh, moving, freed, n, all, step);
+  if (all == 0) p.counts[bh] = n;
   evict_stay(p, bh, bits, j0, j1, tid, kEvictClusterThreads);
   evict_clear(p, bh, keep, all, step);
+  cluster_sync_all();  // no CTA's shared memory is read any more
+}
+
+// The moves that the cluster kernel listed, over the whole GPU: block (x, bh).
+__global__ void __launch_bounds__(256) attn_cache_move_kernel(const EvictParams p) {
+  grid_dependency_wait();
+  if (threadIdx.x == 0) grid_launch_dependents();
+  const int bh = blockIdx.y, cap = p.Lk / 2;
+  const int32_t* freed = p.lists + static_cast<size_t>(bh) * 2 * cap;
+  evict_move(p, bh, freed + cap, freed, p.counts[bh], static_cast<int>(blockIdx.x * 256 + threadIdx.x),
+             static_cast<int>(gridDim.x * 256));
 }
 
 }  // namespace gbattn

@@ -94,30 +94,31 @@ __device__ __forceinline__ int tree_stages(int len, int tl) {
   return tl == 0 ? 0 : (len + kTreeStage - 1) / kTreeStage + (tl + kTreeStage - 1) / kTreeStage;
 }
 
-// Fills the table (whole block; the caller's next barrier publishes it).  Up
-// to 32 sequences, one warp does it all; more, the block loads the lengths first.
+// Fills the table: one warp for up to 32 sequences; for more, the whole block
+// loads the lengths first (tree_lengths_of_all and a barrier).  Whatever
+// follows needs a barrier, except in the calling warp.
+__device__ __forceinline__ int tree_load(const TreeParams& p, TreeTable& tab, int b) {
+  int len, tl;
+  tree_lengths(p, b, len, tl);
+  tab.len[b] = len;
+  tab.tl[b] = static_cast<uint16_t>(tl);
+  return tree_stages(len, tl);
+}
+__device__ __forceinline__ void tree_lengths_of_all(const TreeParams& p, TreeTable& tab) {
+  if (p.B <= 32) return;
+  for (int b = threadIdx.x; b < p.B; b += blockDim.x) tab.pre[b + 1] = tree_load(p, tab, b);
+  __syncthreads();
+}
 __device__ __forceinline__ void tree_table(const TreeParams& p, TreeTable& tab) {
-  auto load = [&](int b) {
-    int len, tl;
-    tree_lengths(p, b, len, tl);
-    tab.len[b] = len;
-    tab.tl[b] = static_cast<uint16_t>(tl);
-    return tree_stages(len, tl);
-  };
-  if (p.B > 32) {
-    for (int b = threadIdx.x; b < p.B; b += blockDim.x) tab.pre[b + 1] = load(b);
-    __syncthreads();
-  }
-  if (threadIdx.x >= 32) return;
-  const int lane = threadIdx.x;
+  const int lane = threadIdx.x & 31;
   int mine = 0, all = 0;  // this lane's sequence (up to 32 of them); all stages of a KV head
   if (p.B > 32) {
     for (int b = lane; b < p.B; b += 32) all += tab.pre[b + 1];
   } else if (lane < p.B) {
-    all = mine = load(lane);
+    all = mine = tree_load(p, tab, lane);
   }
   all = __reduce_add_sync(0xffffffffu, all);
-  const int extra = min(kTreeExtra, all * p.Hkv / (8 * p.n_groups));
+  const int extra = min(kTreeExtra, all * p.Hkv / (6 * p.n_groups));
   if (lane == 0) tab.extra = extra, tab.pre[0] = 0;
   int run = 0;
   for (int b0 = 0; b0 < p.B; b0 += 32) {
@@ -132,6 +133,7 @@ __device__ __forceinline__ void tree_table(const TreeParams& p, TreeTable& tab) 
     if (b < p.B) tab.pre[b + 1] = run + x;
     run += __shfl_sync(0xffffffffu, x, 31);
   }
+  __syncwarp();
 }
 
 // The sequence that unit x of the whole list belongs to: the largest b with pre[b] * Hkv <= x
@@ -203,6 +205,8 @@ __device__ __forceinline__ size_t tree_slot_row(const TreeParams& p, int group, 
   return ((static_cast<size_t>(group) * 2 + slot) * p.n_rb + rb) * rows;
 }
 
+constexpr int kTreeReady = 3;  // named barrier (1 and 2: the tiles' softmax warps)
+
 template <int D, bool BF16, int QS, int NT>
 __global__ void __launch_bounds__(TreeGeom<D, QS, NT>::NUM_THREADS, 1)
     attn_tree_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -230,41 +234,49 @@ __global__ void __launch_bounds__(TreeGeom<D, QS, NT>::NUM_THREADS, 1)
   const int group = blockIdx.x / p.n_rb, rb = blockIdx.x - group * p.n_rb;
   const WaitGuard g{&abort_flag, p.status, p.limit_ns};
 
-  if (threadIdx.x == 32 * PRODUCER) {
-    tma_prefetch_desc(&tmQ);
-    tma_prefetch_desc(&tmK);
-    tma_prefetch_desc(&tmV);
-    tma_prefetch_desc(&tmKn);
-    tma_prefetch_desc(&tmVn);
-    abort_flag = 0;
-    mbar_init(smem_u32(&bar_q), 1);
-    mbar_init(smem_u32(&bar_qfree), NT);
-    for (int s = 0; s < SL; ++s) {
-      mbar_init(smem_u32(&bar_full[s]), 1);
-      mbar_init(smem_u32(&bar_empty[s]), NT);
-    }
-    for (int t = 0; t < NT; ++t) {
-      for (int i = 0; i < 2; ++i) {
-        mbar_init(smem_u32(&bar_sfull[t][i]), 1);
-        mbar_init(smem_u32(&bar_pready[t][i]), 128);
-        mbar_init(smem_u32(&bar_odone[t][i]), 1);
+  // The producer warp sets up the barriers and the division and goes on to its
+  // loads at once; the others meet when that and tensor memory are ready.
+  if (warp == PRODUCER) {
+    if (lane == 0) {
+      tma_prefetch_desc(&tmQ);
+      tma_prefetch_desc(&tmK);
+      tma_prefetch_desc(&tmV);
+      tma_prefetch_desc(&tmKn);
+      tma_prefetch_desc(&tmVn);
+      abort_flag = 0;
+      mbar_init(smem_u32(&bar_q), 1);
+      mbar_init(smem_u32(&bar_qfree), NT);
+      for (int s = 0; s < SL; ++s) {
+        mbar_init(smem_u32(&bar_full[s]), 1);
+        mbar_init(smem_u32(&bar_empty[s]), NT);
       }
-      mbar_init(smem_u32(&bar_mfin[t]), 1);
+      for (int t = 0; t < NT; ++t) {
+        for (int i = 0; i < 2; ++i) {
+          mbar_init(smem_u32(&bar_sfull[t][i]), 1);
+          mbar_init(smem_u32(&bar_pready[t][i]), 128);
+          mbar_init(smem_u32(&bar_odone[t][i]), 1);
+        }
+        mbar_init(smem_u32(&bar_mfin[t]), 1);
+      }
+      fence_mbar_init();
     }
-    fence_mbar_init();
-  }
-  if (warp == PRODUCER + 1) {
+    __syncwarp();
+  } else if (warp == PRODUCER + 1) {
     tmem_alloc(smem_u32(&tmem_slot), Gm::TMEM_COLS);
     tmem_relinquish();
   }
   grid_dependency_wait();  // the kernels before this one are complete
   // the combine kernel may start; it waits for this grid before it reads partials
   if (threadIdx.x == 0) grid_launch_dependents();
-  tree_table(p, tab);
-  tc_fence_before_sync();
-  __syncthreads();
-  tc_fence_after_sync();
-  const uint32_t tmem = tmem_slot;
+  tree_lengths_of_all(p, tab);
+  if (warp == PRODUCER) {
+    tree_table(p, tab);
+    named_bar_arrive(kTreeReady, Gm::NUM_THREADS);
+  } else {
+    tc_fence_before_sync();
+    named_bar_sync(kTreeReady, Gm::NUM_THREADS);
+    tc_fence_after_sync();
+  }
   TreeWalk w(p, tab, group);
 
   if (warp == PRODUCER) {
@@ -339,6 +351,7 @@ __global__ void __launch_bounds__(TreeGeom<D, QS, NT>::NUM_THREADS, 1)
     if (nq > 0) mbar_wait_drain(smem_u32(&bar_q), (nq - 1) & 1);
     __syncwarp();
   } else if (warp > PRODUCER) {
+    const uint32_t tmem = tmem_slot;
     // ---------------- MMA issuer of tile t ----------------
     const int t = warp - PRODUCER - 1;
     constexpr uint32_t IDESC_QK = make_idesc_f16(128, BK, BF16, false, false);
@@ -396,6 +409,7 @@ __global__ void __launch_bounds__(TreeGeom<D, QS, NT>::NUM_THREADS, 1)
     mbar_wait_drain(smem_u32(&bar_mfin[t]), 0);
     __syncwarp();
   } else {
+    const uint32_t tmem = tmem_slot;
     // ---------------- softmax warps ----------------
     const int t = warp >> 2, quad = warp & 3;
     const int kq = QS == 4 ? quad : QS == 2 ? quad >> 1 : 0;  // which keys of a stage
@@ -669,7 +683,7 @@ __global__ void __launch_bounds__(TreeGeom<D, QS, NT>::NUM_THREADS, 1)
   __syncthreads();
   if (warp == PRODUCER + 1) {
     tc_fence_after_sync();
-    tmem_dealloc(tmem, Gm::TMEM_COLS);
+    tmem_dealloc(tmem_slot, Gm::TMEM_COLS);
   }
 }
 
@@ -687,7 +701,8 @@ __global__ void __launch_bounds__(256) attn_tree_combine_kernel(const TreeParams
   __shared__ TreeTable tab;
   __shared__ float sM[8][32], sden[8][32];
   __shared__ float4 so[8][32];
-  tree_table(p, tab);
+  tree_lengths_of_all(p, tab);
+  if (threadIdx.x < 32) tree_table(p, tab);
   __syncthreads();
   const int* pre = tab.pre;
   const int per = tree_per(pre[p.B] * p.Hkv, p.n_groups);
