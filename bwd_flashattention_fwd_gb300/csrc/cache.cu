@@ -27,6 +27,7 @@ attn_status_t check_cache(int B, int Hkv, int Lk, int D, int64_t kv_pitch, attn_
   // the TMA stride limit between heads (2^40 bytes), head counts that a grid takes
   if (kv_pitch > (int64_t{1} << 40) / (2 * D)) return ATTN_ERR_UNSUPPORTED;
   if (static_cast<long long>(B) * Hkv > 65535) return ATTN_ERR_UNSUPPORTED;
+  if (Lk > kCacheMaxLk) return ATTN_ERR_UNSUPPORTED;
   return ATTN_OK;
 }
 
@@ -45,7 +46,7 @@ attn_status_t check_tree(int B, int Hq, int Hkv, int T, int Lk, int D) {
   if (T > kTreeMaxT || B > kTreeMaxB) return ATTN_ERR_UNSUPPORTED;
   // stages of the whole call, and the combine kernel's rows per KV head, are ints that a grid takes
   const long long stages = (Lk + kTreeStage - 1) / kTreeStage + (T + kTreeStage - 1) / kTreeStage + kTreeExtra;
-  if (stages * B * Hkv > 0x7fffffffLL) return ATTN_ERR_UNSUPPORTED;
+  if (stages * B * Hkv > 0x7fff0000LL) return ATTN_ERR_UNSUPPORTED;
   if (static_cast<long long>(Hq / Hkv) * T > 65535) return ATTN_ERR_UNSUPPORTED;
   return ATTN_OK;
 }
@@ -90,6 +91,7 @@ extern "C" attn_status_t attn_fwd_tree(const void* q, const void* k, const void*
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(k_new) || !aligned16(v_new) || !aligned16(o) ||
       !aligned16(lse) || !aligned16(workspace) || !aligned4(cache_len) || !aligned4(tree_len))
     return ATTN_ERR_INVALID_ARG;
+  if (o == q) return ATTN_ERR_INVALID_ARG;  // several CTAs read a row of q
   attn_status_t s = check_scale(scale);
   if (s != ATTN_OK) return s;
   s = check_tree(B, Hq, Hkv, T, Lk, D);
@@ -185,6 +187,7 @@ extern "C" attn_status_t attn_cache_append(const void* k_new, const void* v_new,
   if (T < 1) return ATTN_ERR_INVALID_ARG;
   const attn_status_t s = check_cache(B, Hkv, Lk, D, kv_pitch, dtype);
   if (s != ATTN_OK) return s;
+  if (path && T > kTreeMaxT) return ATTN_ERR_UNSUPPORTED;
   int dev, num_sms, *status;
   EncodeTiledFn enc;
   const attn_status_t ds = shared_device_state(&dev, &enc, &status, &num_sms);

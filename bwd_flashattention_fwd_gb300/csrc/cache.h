@@ -11,6 +11,7 @@ constexpr int kTreeMaxB = 1024;   // sequences (each CTA holds the lengths' pref
 constexpr int kTreeStage = 64;    // keys per pipeline stage
 constexpr int kTreeExtra = 7;      // what a CTA spends on a KV head besides its stages, in stages
 constexpr int kTreeMaxCtas = 152;  // one per SM of a GB300
+constexpr int kCacheMaxLk = 1 << 30;  // rows of a KV head (row numbers are ints)
 constexpr int kEvictMaxLk = 1 << 20;
 constexpr int kEvictCluster = 8;      // CTAs per KV head beyond that
 constexpr int kEvictRowKeys = 16384;  // slots up to which one CTA holds a KV head's keys in shared memory

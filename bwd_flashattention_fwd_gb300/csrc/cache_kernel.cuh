@@ -57,8 +57,9 @@ __global__ void __launch_bounds__(kAppendThreads) attn_cache_append_kernel(const
     }
   }
   if (p.pos) {
-    int32_t* pos = p.pos + static_cast<size_t>(bh) * p.Lk + len;
-    for (int i = blockIdx.x * kAppendThreads + threadIdx.x; i < n; i += gridDim.x * kAppendThreads) pos[i] = seen + i;
+    const size_t at = static_cast<size_t>(bh) * p.Lk + len;
+    for (int i = blockIdx.x * kAppendThreads + threadIdx.x; i < n; i += gridDim.x * kAppendThreads)
+      if (dbg_in_range(at + i, 1, static_cast<size_t>(p.B) * p.Hkv * p.Lk, p.status, 68)) p.pos[at + i] = seen + i;
   }
   if (blockIdx.x == 0 && bh == b * p.Hkv) {
     if (threadIdx.x == 0) {
@@ -127,6 +128,11 @@ __device__ __forceinline__ uint32_t evict_below(int i, int keep) {
   return i + 32 <= keep ? ~0u : i >= keep ? 0u : (1u << (keep - i)) - 1u;
 }
 
+// Debug build: slot i of the weights and positions, piece i of a cache buffer.
+__device__ __forceinline__ bool evict_slot_ok(const EvictParams& p, size_t i, int site) {
+  return dbg_in_range(i, 1, static_cast<size_t>(p.B) * p.Hkv * p.Lk, p.status, site);
+}
+
 // The lists' entries of one strip of slots i .. i + 31 (k: kept, m: below
 // `keep`, in: existing), with `below` / `above` kept slots before it on either
 // side of `keep`; only pairs m0 .. m1 - 1 are listed.  The freed slot j is
@@ -157,7 +163,7 @@ __device__ __forceinline__ void evict_stay(const EvictParams& p, int bh, const u
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const int x = j + u * by;
-      on[u] = x < end && ((bits[(x - j0) >> 5] >> ((x - j0) & 31)) & 1u);
+      on[u] = x < end && ((bits[(x - j0) >> 5] >> ((x - j0) & 31)) & 1u) && evict_slot_ok(p, row + x, 80);
       if (on[u]) w[u] = p.weight[row + x], pos[u] = p.pos[row + x];
     }
 #pragma unroll
@@ -175,27 +181,32 @@ __device__ __forceinline__ void evict_move(const EvictParams& p, int bh, const I
   uint4* k = static_cast<uint4*>(p.k) + static_cast<size_t>(bh) * p.kv_pitch * p.row16;
   uint4* v = static_cast<uint4*>(p.v) + static_cast<size_t>(bh) * p.kv_pitch * p.row16;
   const int pieces = n * p.row16;  // at most 2^19 x 32
+  [[maybe_unused]] const size_t head = static_cast<size_t>(bh) * p.kv_pitch * p.row16;
+  [[maybe_unused]] const size_t n_pieces = cache_extent(p.B * p.Hkv, p.kv_pitch, p.Lk, p.row16);
   constexpr int U = 4;
   for (int x0 = all; x0 < pieces; x0 += U * step) {
     uint4 a[U], e[U];
     size_t to[U];
+    bool on[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int x = x0 + u * step;
-      if (x < pieces) {
+      on[u] = x < pieces;
+      if (on[u]) {
         const int i = x / p.row16, c = x - i * p.row16;
         const size_t from = static_cast<size_t>(moving[i]) * p.row16 + c;
         to[u] = static_cast<size_t>(freed[i]) * p.row16 + c;
-        a[u] = k[from];
-        e[u] = v[from];
+        on[u] = dbg_in_range(head + from, 1, n_pieces, p.status, 81) && dbg_in_range(head + to[u], 1, n_pieces, p.status, 82);
+        if (on[u]) a[u] = k[from], e[u] = v[from];
       }
     }
 #pragma unroll
     for (int u = 0; u < U; ++u)
-      if (x0 + u * step < pieces) k[to[u]] = a[u], v[to[u]] = e[u];
+      if (on[u]) k[to[u]] = a[u], v[to[u]] = e[u];
   }
   for (int i = all; i < n; i += step) {
     const int to = freed[i], from = moving[i];
+    if (!evict_slot_ok(p, row + to, 83) || !evict_slot_ok(p, row + from, 84)) continue;
     p.weight_out[row + to] = p.weight[row + from];
     p.pos_out[row + to] = p.pos[row + from];
   }
@@ -205,6 +216,7 @@ __device__ __forceinline__ void evict_move(const EvictParams& p, int bh, const I
 __device__ __forceinline__ void evict_clear(const EvictParams& p, int bh, int from, int all, int step) {
   const size_t row = static_cast<size_t>(bh) * p.Lk;
   for (int j = from + all; j < p.Lk; j += step) {
+    if (!evict_slot_ok(p, row + j, 85)) continue;
     p.weight_out[row + j] = 0.f;
     p.pos_out[row + j] = -1;
   }
@@ -214,6 +226,7 @@ __device__ __forceinline__ void evict_clear(const EvictParams& p, int bh, int fr
 __device__ __forceinline__ void evict_nothing(const EvictParams& p, int bh, int len, int all, int step) {
   const size_t row = static_cast<size_t>(bh) * p.Lk;
   for (int j = all; j < len; j += step) {
+    if (!evict_slot_ok(p, row + j, 86)) continue;
     p.weight_out[row + j] = p.weight[row + j];
     p.pos_out[row + j] = p.pos[row + j];
   }
@@ -232,7 +245,8 @@ __device__ __forceinline__ void evict_load(const EvictParams& p, int bh, int w0,
     int y[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u)
-      if (i + 32 * u < w1) x[u] = w[i + 32 * u], y[u] = pos[i + 32 * u];
+      if (i + 32 * u < w1 && evict_slot_ok(p, static_cast<size_t>(bh) * p.Lk + i + 32 * u, 87))
+        x[u] = w[i + 32 * u], y[u] = pos[i + 32 * u];
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const bool in = i + 32 * u < w1;

@@ -88,7 +88,9 @@ __device__ __forceinline__ void key_weight_table(const KeyWeightParams& p, int* 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   for (int b = warp; b < p.B; b += warps) {
     int most = 0;
-    for (int t = lane; t < p.Lq; t += 32) most = max(most, p.limit[static_cast<size_t>(b) * p.Lq + t]);
+    for (int t = lane; t < p.Lq; t += 32)
+      if (dbg_in_range(static_cast<size_t>(b) * p.Lq + t, 1, static_cast<size_t>(p.B) * p.Lq, p.status, 70))
+        most = max(most, p.limit[static_cast<size_t>(b) * p.Lq + t]);
     most = __reduce_max_sync(0xffffffffu, most);
     if (lane == 0) tab[b + 1] = (min(most, p.Lk) + BK - 1) / BK;
   }
@@ -251,7 +253,7 @@ __global__ void __launch_bounds__(320, 1)
         for (int r = lane; r < NQ; r += 32) {
           int lim = 0;
           float nl = -INFINITY;
-          if (r < R) {
+          if (r < R && dbg_in_range(static_cast<size_t>(z) * R + r, 1, static_cast<size_t>(p.B) * p.Hkv * R, p.status, 71)) {
             key_weight_row(p, w.b, r % p.Lq, p.lse[static_cast<size_t>(z) * R + r], lim, nl);
             least = min(least, lim);
           }
@@ -317,13 +319,14 @@ __global__ void __launch_bounds__(320, 1)
     // ---------------- epilogue: warpgroup h takes every other tile, thread = key ----------------
     const int h = warp >> 2, quad = warp & 3;
     const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
+    [[maybe_unused]] const size_t n_out = static_cast<size_t>(p.B) * p.Hkv * p.Lk;  // for the debug build's index checks
     // keys that no row reaches keep their weight
     for (int z = blockIdx.x; z < p.B * p.Hkv; z += gridDim.x) {
       const int b = z / p.Hkv;
       const int from = p.limit ? (tab[b + 1] - tab[b]) * BK : p.Lk;
       for (int j = from + threadIdx.x; j < p.Lk; j += 256) {
         const size_t o = static_cast<size_t>(z) * p.Lk + j;
-        p.weight_out[o] = p.weight ? p.weight[o] : 0.f;
+        if (dbg_in_range(o, 1, n_out, p.status, 72)) p.weight_out[o] = p.weight ? p.weight[o] : 0.f;
       }
     }
     RingPos<QB> sq;
@@ -338,7 +341,8 @@ __global__ void __launch_bounds__(320, 1)
         const int bb = i % NB;
         const int key = j * BK + quad * 32 + lane;
         const size_t o = (static_cast<size_t>(w.b) * p.Hkv + w.hk) * p.Lk + key;
-        const float w0 = p.weight && key < p.Lk ? p.weight[o] : 0.f;
+        const bool mine = key < p.Lk && dbg_in_range(o, 1, n_out, p.status, 73);
+        const float w0 = p.weight && mine ? p.weight[o] : 0.f;
         mbar_wait(smem_u32(&bar_sfull[bb]), (i / NB) & 1, g, kWait);
         __syncwarp();
         tc_fence_after_sync();
@@ -348,7 +352,7 @@ __global__ void __launch_bounds__(320, 1)
         tc_fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&bar_sempty[bb]));
-        if (key < p.Lk) p.weight_out[o] = w0 + sum;
+        if (mine) p.weight_out[o] = w0 + sum;
       }
       // every product with this Q that this warp waits for is complete; the
       // tables are read; (the other warpgroup's tiles are covered by its own arrival)
@@ -632,7 +636,9 @@ __global__ void __launch_bounds__(KeyWeightGeom<D>::NUM_THREADS, 1)
           for (int i = 0; i < RPL; ++i) {
             const int r = at.qt * NQ + i * 32 + lane, in = min(r, rows - 1);
             const int t = p.packed ? in % p.Lq : in;
-            x[u][i] = p.lse[(p.packed ? static_cast<size_t>(z) : static_cast<size_t>(z) * p.G + at.g) * rows + in];
+            const size_t row = (p.packed ? static_cast<size_t>(z) : static_cast<size_t>(z) * p.G + at.g) * rows + in;
+            const bool real = dbg_in_range(row, 1, static_cast<size_t>(p.B) * p.Hq * p.Lq, p.status, 74);
+            x[u][i] = real ? p.lse[row] : INFINITY;
             l[u][i] = p.limit ? p.limit[static_cast<size_t>(w.b) * p.Lq + t] : t;
             if (r >= rows) l[u][i] = -1;
           }
@@ -777,11 +783,12 @@ __global__ void __launch_bounds__(KeyWeightGeom<D>::NUM_THREADS, 1)
         if (half == 1) continue;
       }
       if (w.whole()) {
-        if (key < p.Lk) {
-          const size_t o = (static_cast<size_t>(w.b) * p.Hkv + w.hk) * p.Lk + key;
+        const size_t o = (static_cast<size_t>(w.b) * p.Hkv + w.hk) * p.Lk + key;
+        if (key < p.Lk && dbg_in_range(o, 1, static_cast<size_t>(p.B) * p.Hkv * p.Lk, p.status, 75)) {
           p.weight_out[o] = (p.weight ? p.weight[o] : 0.f) + total;
         }
-      } else {
+      } else if (dbg_in_range((static_cast<size_t>(blockIdx.x) * 2 + w.slot()) * 256 + mine, 1,
+                              static_cast<size_t>(kTreeMaxCtas) * 512, p.status, 76)) {
         p.part[(static_cast<size_t>(blockIdx.x) * 2 + w.slot()) * 256 + mine] = total;
       }
     }
@@ -817,10 +824,13 @@ static __global__ void __launch_bounds__(256) attn_key_weight_join_kernel(const 
       const int g0 = s / per, g1 = (s + w.st.steps(kt) - 1) / per;
       if (g0 == g1) continue;  // written by its CTA
 #pragma unroll 4
-      for (int g = g0; g <= g1; ++g)
-        sum += p.part[(g * 2 + (g == g0 && s != g0 * per ? 1 : 0)) * 256 + threadIdx.x];
+      for (int g = g0; g <= g1; ++g) {
+        const size_t at = (g * 2 + (g == g0 && s != g0 * per ? 1 : 0)) * 256 + threadIdx.x;
+        if (dbg_in_range(at, 1, static_cast<size_t>(kTreeMaxCtas) * 512, p.status, 77)) sum += p.part[at];
+      }
     }
-    if (key < p.Lk) p.weight_out[o] = (p.weight ? p.weight[o] : 0.f) + sum;
+    if (key < p.Lk && dbg_in_range(o, 1, static_cast<size_t>(p.B) * p.Hkv * p.Lk, p.status, 78))
+      p.weight_out[o] = (p.weight ? p.weight[o] : 0.f) + sum;
   }
 }
 

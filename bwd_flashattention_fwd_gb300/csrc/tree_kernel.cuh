@@ -421,9 +421,13 @@ __global__ void __launch_bounds__(TreeGeom<D, QS, NT>::NUM_THREADS, 1)
     const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
     const uint32_t o_col = tmem + lanes + Gm::o_col(t);
     const float sl2 = p.scale_log2;
+    // extents for the debug build's index checks: rows of o / lse, and of the partials
+    [[maybe_unused]] const size_t n_rows = static_cast<size_t>(p.B) * p.Hkv * R;
+    [[maybe_unused]] const size_t n_parts = static_cast<size_t>(p.n_groups) * 2 * p.n_rb * Gm::ROWS;
     // KV heads without a stage (no drafts): their rows see nothing
     for (int x = blockIdx.x; x < p.B * p.Hkv; x += gridDim.x) {
       if (tab.pre[x / p.Hkv + 1] != tab.pre[x / p.Hkv]) continue;
+      if (!dbg_in_range(static_cast<size_t>(x) * R, R, n_rows, p.status, 62)) continue;
       uint4* o = reinterpret_cast<uint4*>(static_cast<typename E::T*>(p.o) + static_cast<size_t>(x) * R * D);
       for (long long i = threadIdx.x; i < static_cast<long long>(R) * (D / 8); i += 128 * NT) o[i] = make_uint4(0, 0, 0, 0);
       for (int i = threadIdx.x; i < R; i += 128 * NT) p.lse[static_cast<size_t>(x) * R + i] = INFINITY;
@@ -459,7 +463,9 @@ __global__ void __launch_bounds__(TreeGeom<D, QS, NT>::NUM_THREADS, 1)
 #pragma unroll
               for (int h = 0; h < KPW; h += STEP) {
                 const int u = h + lane % STEP;
-                const uint32_t bits = __ballot_sync(0xffffffffu, u < most && mb[static_cast<size_t>(mt) * p.T + u] != 0);
+                const uint32_t bits = __ballot_sync(0xffffffffu, u < most && dbg_in_range(mb - p.mask + static_cast<size_t>(mt) * p.T + u, 1,
+                                                                 static_cast<size_t>(p.B) * p.T * p.T, p.status, 63) &&
+                                    mb[static_cast<size_t>(mt) * p.T + u] != 0);
                 if (lane / AT_ONCE == i / AT_ONCE)
                   see |= static_cast<uint64_t>(STEP == 32 ? bits : (bits >> ((lane % AT_ONCE) * STEP)) & ((1u << (STEP & 31)) - 1u)) << h;
               }
@@ -608,7 +614,9 @@ __global__ void __launch_bounds__(TreeGeom<D, QS, NT>::NUM_THREADS, 1)
       o_done(ts - 1);
       __syncwarp();
       tc_fence_after_sync();
-      if (kq == 0 && row < R) {
+      const bool mine = row < R && (whole ? dbg_in_range(grow, 1, n_rows, p.status, 64)
+                                          : dbg_in_range(prow, 1, n_parts, p.status, 65));
+      if (kq == 0 && mine) {
         const float lse = m + log2f(l);
         if (whole) p.lse[grow] = empty ? INFINITY : lse;
         else p.part_lse[prow] = empty ? -INFINITY : lse;
@@ -625,7 +633,7 @@ __global__ void __launch_bounds__(TreeGeom<D, QS, NT>::NUM_THREADS, 1)
 #pragma unroll
             for (int i = 0; i < 32; ++i) rr[i] = 0u;
           }
-          if (row < R) {
+          if (mine) {
             const float mul = empty ? 1.f : inv;
             if (whole) store_row32<BF16>(orow + c * 32, rr, mul);
             else
@@ -638,11 +646,11 @@ __global__ void __launch_bounds__(TreeGeom<D, QS, NT>::NUM_THREADS, 1)
         } else {
           constexpr int W = 32 / QS;  // columns per thread once merged
           const bool drop = empty || f == 0.f;
-          const uint32_t mine = sX + (kq * Gm::QROWS + lrow) * (Gm::XCH_PITCH * 4);
+          const uint32_t own = sX + (kq * Gm::QROWS + lrow) * (Gm::XCH_PITCH * 4);
 #pragma unroll
           for (int i = 0; i < 32; ++i) rr[i] = drop ? 0u : __float_as_uint(__uint_as_float(rr[i]) * inv);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) st_shared_v4(mine + i * 16, rr[4 * i], rr[4 * i + 1], rr[4 * i + 2], rr[4 * i + 3]);
+          for (int i = 0; i < 8; ++i) st_shared_v4(own + i * 16, rr[4 * i], rr[4 * i + 1], rr[4 * i + 2], rr[4 * i + 3]);
           named_bar_sync(1 + t, 128);
           float acc[W];
 #pragma unroll
@@ -657,7 +665,7 @@ __global__ void __launch_bounds__(TreeGeom<D, QS, NT>::NUM_THREADS, 1)
               acc[4 * i + 2] += __uint_as_float(x.z);
               acc[4 * i + 3] += __uint_as_float(x.w);
             }
-          if (row < R) {
+          if (mine) {
             if (whole) {
               uint4* d = reinterpret_cast<uint4*>(orow + c * 32 + kq * W);
 #pragma unroll
@@ -733,7 +741,8 @@ __global__ void __launch_bounds__(256) attn_tree_combine_kernel(const TreeParams
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           L[u] = -INFINITY;
-          if (i + u * NS < ng) {
+          if (i + u * NS < ng && dbg_in_range(part_row(i + u * NS), 32, static_cast<size_t>(p.n_groups) * 2 * p.n_rb * rows,
+                                              p.status, 66)) {
             const size_t r = part_row(i + u * NS);
             L[u] = p.part_lse[r + lane];
             x[u] = *reinterpret_cast<const float4*>(p.part + r * D + q * 128 + lane * 4);
@@ -769,8 +778,8 @@ __global__ void __launch_bounds__(256) attn_tree_combine_kernel(const TreeParams
         }
       }
     }
-    if (row < R && sub == 0) {
-      const size_t grow = static_cast<size_t>(head) * R + row;
+    const size_t grow = static_cast<size_t>(head) * R + row;
+    if (row < R && sub == 0 && dbg_in_range(grow, 1, static_cast<size_t>(p.B) * p.Hkv * R, p.status, 67)) {
       const float inv = den == 0.f ? 0.f : 1.f / den;
       uint2 o;
       o.x = E::pack(acc.x * inv, acc.y * inv), o.y = E::pack(acc.z * inv, acc.w * inv);

@@ -235,8 +235,9 @@ attn_status_t attn_bwd_decode(const void* q, const void* k, const void* v, const
  *     as P = 0 times a non-finite value is not 0.
  *   workspace: as for the decode calls (one per call in flight), at least
  *     attn_tree_workspace_bytes(...) bytes; 0 there means the shape is rejected.
- *   Limits: T <= 1024, B <= 1024 and G * T <= 65535 (else
- *     ATTN_ERR_UNSUPPORTED).  int32 arrays are 4-byte aligned.  Other errors as
+ *   Limits: T <= 1024, B <= 1024, G * T <= 65535 and Lk <= 2^30 (else
+ *     ATTN_ERR_UNSUPPORTED).  o is not q (ATTN_ERR_INVALID_ARG), and no output
+ *     overlaps an input.  int32 arrays are 4-byte aligned.  Other errors as
  *     for attn_fwd_ex.
  */
 size_t attn_tree_workspace_bytes(int B, int Hq, int Hkv, int T, int Lk, int D);
@@ -265,7 +266,8 @@ attn_status_t attn_fwd_tree(const void* q, const void* k, const void* v, const v
  *     cache_len[b] + i + 1 for t = path[i] (the last such i), 0 for a draft
  *     that was not accepted.
  * All arrays but the 16-bit ones are int32; every pointer is a device pointer.
- * Any T >= 1.  The inputs may not overlap the outputs.
+ * Any T >= 1, with a path T <= 1024 (else ATTN_ERR_UNSUPPORTED).  The inputs
+ * may not overlap the outputs.
  */
 attn_status_t attn_cache_append(const void* k_new, const void* v_new, const int32_t* path, const int32_t* accept_len,
                                 const int32_t* cache_len, const int32_t* seen, void* k, void* v, int32_t* pos,

@@ -22,18 +22,19 @@ def lib():
 
 def tree(lib, ptrs=None, mask=None, tree_len=None, nbytes=1 << 40, pitch=0, B=2, Hq=8, Hkv=2, T=8, Lk=100, D=128,
          scale=0.1, dtype=1, ws=FAKE):
-    q, k, v, kn, vn, cl, o, lse = ptrs or [FAKE] * 8
+    q, k, v, kn, vn, cl, o, lse = ptrs or [FAKE] * 6 + [FAKE2, FAKE]
     return lib.attn_fwd_tree(q, k, v, kn, vn, mask, cl, tree_len, o, lse, ws, nbytes, pitch, B, Hq, Hkv, T, Lk, D,
                              ctypes.c_float(scale), dtype, None)
 
 
 def test_tree_rejects(lib):
     for i in range(8):
-        ptrs = [FAKE] * 8
+        ptrs = [FAKE] * 6 + [FAKE2, FAKE]
         ptrs[i] = None
         assert tree(lib, ptrs) == INV
         ptrs[i] = FAKE + (2 if i == 5 else 8)
         assert tree(lib, ptrs) == INV
+    assert tree(lib, [FAKE] * 8) == INV  # o over q
     assert tree(lib, ws=None) == INV and tree(lib, ws=FAKE + 8) == INV
     assert tree(lib, tree_len=FAKE + 1) == INV
     need = lib.attn_tree_workspace_bytes(2, 8, 2, 8, 100, 128)
@@ -42,7 +43,8 @@ def test_tree_rejects(lib):
                dict(scale=-1.0), dict(scale=math.nan), dict(scale=math.inf), dict(dtype=3), dict(pitch=-1),
                dict(pitch=99)):
         assert tree(lib, **kw) == INV, kw
-    for kw in (dict(D=80), dict(D=512), dict(T=1025), dict(B=1025), dict(pitch=1 << 40), dict(Hkv=40000, Hq=40000)):
+    for kw in (dict(D=80), dict(D=512), dict(T=1025), dict(B=1025), dict(pitch=1 << 40), dict(Hkv=40000, Hq=40000),
+               dict(T=1024, Hq=128), dict(Lk=(1 << 30) + 1), dict(Lk=1 << 30, B=1024)):
         assert tree(lib, **kw) == UNS, kw
     ws = lib.attn_tree_workspace_bytes
     assert ws(0, 8, 2, 8, 100, 128) == 0 and ws(2, 8, 3, 8, 100, 128) == 0 and ws(2, 8, 2, 1025, 100, 128) == 0
@@ -69,7 +71,8 @@ def test_key_weight_rejects(lib):
     for kw in (dict(B=0), dict(Hq=0), dict(Lq=0), dict(Lk=0), dict(Hq=9), dict(scale=math.nan), dict(causal=2),
                dict(causal=1, Lq=101), dict(causal=1, limit=FAKE), dict(dtype=-1), dict(pitch=50)):
         assert weight(lib, **kw) == INV, kw
-    for kw in (dict(D=72), dict(limit=FAKE, Lq=1025), dict(pitch=1 << 40)):
+    for kw in (dict(D=72), dict(limit=FAKE, Lq=1025), dict(limit=FAKE, B=1025), dict(pitch=1 << 40),
+               dict(Lk=(1 << 30) + 1), dict(Lq=(1 << 28) + 1), dict(Lq=1 << 22, Lk=1 << 24, B=16)):
         assert weight(lib, **kw) == UNS, kw
     ws = lib.attn_key_weight_workspace_bytes
     assert ws(2, 8, 2, 8, 100, 90) == 0 and ws(2, 7, 2, 8, 100, 128) == 0 and ws(2, 8, 2, 0, 100, 128) == 0
@@ -98,6 +101,7 @@ def test_append_rejects(lib):
     for kw in (dict(B=0), dict(Hkv=0), dict(T=0), dict(Lk=0), dict(pitch=7), dict(dtype=9)):
         assert append(lib, **kw) == INV, kw
     assert append(lib, D=100) == UNS and append(lib, B=70000) == UNS
+    assert append(lib, path=FAKE, T=1025, Lk=4000) == UNS
 
 
 def evict(lib, ptrs=None, nbytes=1 << 40, ws=FAKE, pitch=0, B=2, Hkv=2, Lk=100, D=128, keep=50, recent=10, dtype=1):

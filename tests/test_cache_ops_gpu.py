@@ -135,6 +135,10 @@ TREES = [
     (1, 2, 1, 200, 64, 128, BF, [64], None, None),
     (4, 2, 2, 2, 4097, 128, BF, [4097, 1, 4096, 2050], None, None),
     (1, 2, 1, 1, 9000, 96, BF, [8999], None, None),
+    (40, 2, 1, 3, 150, 64, BF, [(37 * i) % 151 for i in range(40)], [i % 4 for i in range(40)], "tree"),
+    (1000, 1, 1, 1, 70, 64, HF, [(7 * i) % 71 for i in range(1000)], None, None),
+    (1, 40, 1, 1000, 60, 64, BF, [50], [990], None),  # more blocks of rows than SMs
+    (1, 1, 1, 1024, 10, 128, BF, [10], None, "tree"),
 ]
 
 
@@ -227,6 +231,12 @@ WEIGHTS = [
     (1, 4, 2, 200, 130, 128, BF, "dense"),
     (3, 3, 1, 7, 65, 96, BF, "dense"),
     (1, 16, 2, 1024, 1500, 128, BF, "limit"),
+    (2, 6, 2, 20, 300, 128, BF, "causal"),
+    (1, 4, 1, 40, 513, 96, HF, "causal"),
+    (40, 2, 1, 2, 300, 64, BF, "limit"),
+    (40, 4, 1, 40, 300, 64, BF, "limit"),
+    (2, 8, 1, 30, 400, 256, BF, "causal"),
+    (1, 4, 4, 1500, 1500, 128, BF, "dense"),
 ]
 
 
