@@ -235,7 +235,8 @@ extern "C" attn_status_t attn_cache_evict(void* k, void* v, const float* weight,
   if (Lk <= kEvictRowKeys) {
     // about one CTA per SM, so that the moves run at the memory's rate
     const int copies = heads < num_sms ? num_sms / heads : 1;
-    if (!set_smem_limit(attn_cache_evict_kernel, evict_smem(kEvictRowKeys, 1))) return ATTN_ERR_CUDA;
+    static std::atomic<uint64_t> done{0};
+    if (!set_smem_limit(attn_cache_evict_kernel, evict_smem(kEvictRowKeys, 1), done)) return ATTN_ERR_CUDA;
     return finish(launch_dependent(attn_cache_evict_kernel, dim3(heads * copies), kEvictThreads,
                                    evict_smem(Lk, copies), stream, p, copies));
   }
@@ -245,7 +246,8 @@ extern "C" attn_status_t attn_cache_evict(void* k, void* v, const float* weight,
   const bool cached = part <= kEvictKeys;
   auto kern = cached ? attn_cache_evict_cluster_kernel<true> : attn_cache_evict_cluster_kernel<false>;
   const size_t smem = cached ? static_cast<size_t>(part) * 4 : 0;
-  if (!set_smem_limit(kern, kEvictKeys * 4)) return ATTN_ERR_CUDA;
+  static std::atomic<uint64_t> done[2] = {};
+  if (!set_smem_limit(kern, kEvictKeys * 4, done[cached])) return ATTN_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(heads) * nc);
   cfg.blockDim = dim3(kEvictClusterThreads);

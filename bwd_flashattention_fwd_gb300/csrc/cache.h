@@ -2,6 +2,8 @@
 // their kernels.
 #pragma once
 
+#include <atomic>
+
 #include "launch.h"
 
 namespace gbattn {
@@ -112,17 +114,23 @@ GBATTN_DECLARE_CACHE_LAUNCHERS(256)
 
 #undef GBATTN_DECLARE_CACHE_LAUNCHERS
 
+// A kernel's shared-memory limit, once per device: `done` is that kernel's own record.
+template <typename Kern>
+bool set_smem_limit(Kern kern, size_t smem, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return false;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0ull;
+  if (done.load(std::memory_order_acquire) & bit) return true;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
+    return false;
+  done.fetch_or(bit, std::memory_order_release);
+  return true;
+}
+
 // Launch as a programmatic dependent of the kernel before it on the stream:
 // its CTAs may start (and set up) while that kernel finishes; every kernel of
 // the cache calls waits for it (griddepcontrol.wait) before it reads or writes
-// global memory, so stream order holds for the caller.  (A kernel whose shared
-// memory depends on the call has its limit set by set_smem_limit, to the same
-// value every time: callers on other threads may be about to launch it.)
-template <typename Kern>
-bool set_smem_limit(Kern kern, size_t smem) {
-  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) == cudaSuccess;
-}
-
+// global memory, so stream order holds for the caller.
 template <typename... Params, typename... Args>
 int launch_dependent(void (*kern)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t stream, Args... args) {
   cudaLaunchConfig_t cfg = {};

@@ -45,7 +45,8 @@ int tree_impl(const TreeParams& p, EncodeTiledFn enc, cudaStream_t stream) {
       !make_map(enc, BF16, &tvn, p.v_new, p.T, heads, Gm::BK, p.T))
     return kLaunchBadMap;
   auto kern = attn_tree_kernel<kD, BF16, QS, NT>;
-  if (!set_smem_limit(kern, Gm::SMEM_BYTES)) return kLaunchCudaError;
+  static std::atomic<uint64_t> done{0};
+  if (!set_smem_limit(kern, Gm::SMEM_BYTES, done)) return kLaunchCudaError;
   const int r = launch_dependent(kern, dim3(p.n_groups * p.n_rb), Gm::NUM_THREADS,
                                  Gm::SMEM_BYTES, stream, tq, tk, tv, tkn, tvn, p);
   if (r != kLaunchOk) return r;
@@ -82,7 +83,8 @@ int key_weight_few(const KeyWeightParams& p, int num_sms, EncodeTiledFn enc, cud
     return kLaunchBadMap;
   const long long tiles = heads * ((p.Lk + Gm::BK - 1) / Gm::BK);
   auto kern = attn_key_weight_few_kernel<kD, BF16, NQ>;
-  if (!set_smem_limit(kern, Gm::SMEM_BYTES)) return kLaunchCudaError;
+  static std::atomic<uint64_t> done{0};
+  if (!set_smem_limit(kern, Gm::SMEM_BYTES, done)) return kLaunchCudaError;
   return launch_dependent(kern, dim3(static_cast<unsigned>(tiles < num_sms ? tiles : num_sms)), Gm::NUM_THREADS,
                           Gm::SMEM_BYTES, stream, tq, tk, p);
 }
@@ -98,7 +100,8 @@ int key_weight_many(const KeyWeightParams& p, int num_sms, EncodeTiledFn enc, cu
     return kLaunchBadMap;
   const int groups = num_sms < kTreeMaxCtas ? num_sms : kTreeMaxCtas;
   auto kern = attn_key_weight_kernel<kD, BF16>;
-  if (!set_smem_limit(kern, Gm::SMEM_BYTES)) return kLaunchCudaError;
+  static std::atomic<uint64_t> done{0};
+  if (!set_smem_limit(kern, Gm::SMEM_BYTES, done)) return kLaunchCudaError;
   const int r = launch_dependent(kern, dim3(groups), Gm::NUM_THREADS, Gm::SMEM_BYTES, stream, tq, tk, p);
   if (r != kLaunchOk) return r;
   const long long tiles = heads * ((p.Lk + Gm::BK - 1) / Gm::BK), most = 4LL * kTreeMaxCtas;

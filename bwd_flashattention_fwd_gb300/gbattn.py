@@ -131,10 +131,15 @@ def _dtype_code(t: torch.Tensor) -> int:
     raise TypeError(f"unsupported dtype {t.dtype}; expected bfloat16 or float16")
 
 
+# torch.cuda.current_device() without its check that CUDA is initialised (a CUDA tensor exists by then)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+# the handle of a device's current stream, without a Stream object around it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
 def _stream_handle(stream) -> int:
     if stream is None:
-        # the current stream's handle without building a Stream object for it
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return _raw_stream(torch.cuda.current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -386,6 +391,16 @@ def lce_bwd(hidden, weight, targets, lse, dloss, dhidden, dweight, workspace, st
     return _check(st, "lce_bwd", check)
 
 
+# The serving calls below run every few tens of microseconds, so what their
+# checks cost counts: each tests all of its tensors in one expression (the
+# same conditions as _require and _shapes, which are called only when it does
+# not hold, to name what is wrong and raise).
+
+
+def _plain(t, dtype, dev: int, shape) -> bool:
+    return t.dtype is dtype and t.get_device() == dev and t.is_contiguous() and t.shape == shape
+
+
 def _shapes(call: str, *named) -> None:
     """Reject (tensor or None, wanted shape, name) triples whose shapes differ from what the call reads."""
     for t, want, name in named:
@@ -417,19 +432,31 @@ def attn_fwd_tree(q, k, v, k_new, v_new, cache_len, o, lse, workspace, scale: fl
     cache_len [B] int32 context lengths, tree_len [B] int32 draft counts (None:
     all T), tree_mask uint8 [B,T,T] (None: a chain).  k and v may be slices of
     a longer cache, as for attn_fwd_ex."""
-    _require("attn_fwd_tree", dense=(q, k_new, v_new, o), sliced=(k, v), f32=(lse,), u8=(tree_mask, workspace),
-             i32=(cache_len, tree_len))
     B, Hq, T, D = q.shape
     Hkv, Lk = k.shape[1], k.shape[2]
-    _shapes("attn_fwd_tree", (k, (B, Hkv, Lk, D), "k"), (v, (B, Hkv, Lk, D), "v"), (k_new, (B, Hkv, T, D), "k_new"),
-            (v_new, (B, Hkv, T, D), "v_new"), (o, q.shape, "o"), (lse, (B, Hq, T), "lse"),
-            (cache_len, (B,), "cache_len"), (tree_len, (B,), "tree_len"),
-            (tree_mask, (B, T, T), "tree_mask"))
+    dt, dev, lens, new = q.dtype, q.get_device(), (B,), (B, Hkv, T, D)
+    if not (dev >= 0 and dev == _current_device() and (dt is _BF16 or dt is _F16)
+            and dt is k.dtype is v.dtype is k_new.dtype is v_new.dtype is o.dtype
+            and lse.dtype is _F32 and cache_len.dtype is _I32 and workspace.dtype is _U8
+            and dev == k.get_device() == v.get_device() == k_new.get_device() == v_new.get_device() == o.get_device()
+            == lse.get_device() == cache_len.get_device() == workspace.get_device()
+            and q.is_contiguous() and k_new.is_contiguous() and v_new.is_contiguous() and o.is_contiguous()
+            and lse.is_contiguous() and cache_len.is_contiguous() and workspace.is_contiguous()
+            and (k.shape, v.shape, k_new.shape, v_new.shape, o.shape, lse.shape, cache_len.shape)
+            == ((B, Hkv, Lk, D), k.shape, new, new, q.shape, (B, Hq, T), lens)
+            and (tree_len is None or _plain(tree_len, _I32, dev, lens))
+            and (tree_mask is None or _plain(tree_mask, _U8, dev, (B, T, T)))):
+        _require("attn_fwd_tree", dense=(q, k_new, v_new, o), sliced=(k, v), f32=(lse,), u8=(tree_mask, workspace),
+                 i32=(cache_len, tree_len))
+        _shapes("attn_fwd_tree", (k, (B, Hkv, Lk, D), "k"), (v, (B, Hkv, Lk, D), "v"), (k_new, new, "k_new"),
+                (v_new, new, "v_new"), (o, q.shape, "o"), (lse, (B, Hq, T), "lse"), (cache_len, lens, "cache_len"),
+                (tree_len, lens, "tree_len"), (tree_mask, (B, T, T), "tree_mask"))
     pitch = kv_row_pitch(k, v) if kv_pitch is None else int(kv_pitch)
-    st = load_library().attn_fwd_tree(_ptr(q), _ptr(k), _ptr(v), _ptr(k_new), _ptr(v_new), _ptr(tree_mask),
-                                      _ptr(cache_len), _ptr(tree_len), _ptr(o), _ptr(lse), _ptr(workspace),
-                                      workspace.numel(), pitch, B, Hq, Hkv, T, Lk, D, float(scale), _dtype_code(q),
-                                      _stream_handle(stream))
+    st = load_library().attn_fwd_tree(q.data_ptr(), k.data_ptr(), v.data_ptr(), k_new.data_ptr(), v_new.data_ptr(),
+                                      _ptr(tree_mask), cache_len.data_ptr(), _ptr(tree_len), o.data_ptr(),
+                                      lse.data_ptr(), workspace.data_ptr(), workspace.numel(), pitch, B, Hq, Hkv, T,
+                                      Lk, D, float(scale), ATTN_DTYPE_BF16 if dt is _BF16 else ATTN_DTYPE_FP16,
+                                      _raw_stream(dev) if stream is None else _stream_handle(stream))
     return _check(st, "attn_fwd_tree", check)
 
 
@@ -438,19 +465,35 @@ def attn_cache_append(k_new, v_new, k, v, cache_len, accept_len, cache_len_out, 
     """Accepted drafts into the cache (writes k, v, cache_len_out and, where
     given, pos, seen_out, limit): rows path[b][:accept_len[b]] of k_new / v_new
     (None: all T rows; the first ones) become cache rows cache_len[b] on."""
-    _require("attn_cache_append", dense=(k_new, v_new), sliced=(k, v),
-             i32=(cache_len, accept_len, cache_len_out, path, pos, seen, seen_out, limit))
     B, Hkv, T, D = k_new.shape
     Lk = k.shape[2]
-    _shapes("attn_cache_append", (k, (B, Hkv, Lk, D), "k"), (v, (B, Hkv, Lk, D), "v"), (v_new, k_new.shape, "v_new"),
-            (cache_len, (B,), "cache_len"), (accept_len, (B,), "accept_len"),
-            (cache_len_out, (B,), "cache_len_out"), (path, (B, T), "path"), (pos, (B, Hkv, Lk), "pos"),
-            (seen, (B,), "seen"), (seen_out, (B,), "seen_out"), (limit, (B, T), "limit"))
+    dt, dev, lens = k_new.dtype, k_new.get_device(), (B,)
+    if not (dev >= 0 and dev == _current_device() and (dt is _BF16 or dt is _F16)
+            and dt is v_new.dtype is k.dtype is v.dtype and cache_len.dtype is _I32 and cache_len_out.dtype is _I32
+            and dev == v_new.get_device() == k.get_device() == v.get_device() == cache_len.get_device()
+            == cache_len_out.get_device()
+            and k_new.is_contiguous() and v_new.is_contiguous() and cache_len.is_contiguous()
+            and cache_len_out.is_contiguous()
+            and (v_new.shape, k.shape, v.shape, cache_len.shape, cache_len_out.shape)
+            == (k_new.shape, (B, Hkv, Lk, D), k.shape, lens, lens)
+            and (accept_len is None or _plain(accept_len, _I32, dev, lens))
+            and (path is None or _plain(path, _I32, dev, (B, T)))
+            and (pos is None or _plain(pos, _I32, dev, (B, Hkv, Lk)))
+            and (seen is None or _plain(seen, _I32, dev, lens))
+            and (seen_out is None or _plain(seen_out, _I32, dev, lens))
+            and (limit is None or _plain(limit, _I32, dev, (B, T)))):
+        _require("attn_cache_append", dense=(k_new, v_new), sliced=(k, v),
+                 i32=(cache_len, accept_len, cache_len_out, path, pos, seen, seen_out, limit))
+        _shapes("attn_cache_append", (k, (B, Hkv, Lk, D), "k"), (v, (B, Hkv, Lk, D), "v"),
+                (v_new, k_new.shape, "v_new"), (cache_len, lens, "cache_len"), (accept_len, lens, "accept_len"),
+                (cache_len_out, lens, "cache_len_out"), (path, (B, T), "path"), (pos, (B, Hkv, Lk), "pos"),
+                (seen, lens, "seen"), (seen_out, lens, "seen_out"), (limit, (B, T), "limit"))
     pitch = kv_row_pitch(k, v) if kv_pitch is None else int(kv_pitch)
-    st = load_library().attn_cache_append(_ptr(k_new), _ptr(v_new), _ptr(path), _ptr(accept_len), _ptr(cache_len),
-                                          _ptr(seen), _ptr(k), _ptr(v), _ptr(pos), _ptr(cache_len_out),
-                                          _ptr(seen_out), _ptr(limit), pitch, B, Hkv, T, Lk, D, _dtype_code(k_new),
-                                          _stream_handle(stream))
+    st = load_library().attn_cache_append(k_new.data_ptr(), v_new.data_ptr(), _ptr(path), _ptr(accept_len),
+                                          cache_len.data_ptr(), _ptr(seen), k.data_ptr(), v.data_ptr(), _ptr(pos),
+                                          cache_len_out.data_ptr(), _ptr(seen_out), _ptr(limit), pitch, B, Hkv, T, Lk,
+                                          D, ATTN_DTYPE_BF16 if dt is _BF16 else ATTN_DTYPE_FP16,
+                                          _raw_stream(dev) if stream is None else _stream_handle(stream))
     return _check(st, "attn_cache_append", check)
 
 
@@ -471,15 +514,26 @@ def attn_key_weight(q, k, lse, weight, weight_out, workspace, scale: float, caus
     """weight_out = weight (None: zeros) + the attention weight each key of k
     got from q's rows, whose base-2 log-sum-exps are lse; limit int32 [B,Lq]:
     how many keys each row sees (0: the row adds nothing)."""
-    _require("attn_key_weight", dense=(q,), sliced=(k,), f32=(lse, weight, weight_out), u8=(workspace,), i32=(limit,))
     B, Hq, Lq, D = q.shape
     Hkv, Lk = k.shape[1], k.shape[2]
-    _shapes("attn_key_weight", (k, (B, Hkv, Lk, D), "k"), (lse, (B, Hq, Lq), "lse"), (weight, (B, Hkv, Lk), "weight"),
-            (weight_out, (B, Hkv, Lk), "weight_out"), (limit, (B, Lq), "limit"))
+    dt, dev, slots = q.dtype, q.get_device(), (B, Hkv, Lk)
+    if not (dev >= 0 and dev == _current_device() and (dt is _BF16 or dt is _F16) and k.dtype is dt
+            and lse.dtype is _F32 and weight_out.dtype is _F32 and workspace.dtype is _U8
+            and dev == k.get_device() == lse.get_device() == weight_out.get_device() == workspace.get_device()
+            and q.is_contiguous() and lse.is_contiguous() and weight_out.is_contiguous() and workspace.is_contiguous()
+            and (k.shape, lse.shape, weight_out.shape) == ((B, Hkv, Lk, D), (B, Hq, Lq), slots)
+            and (weight is None or _plain(weight, _F32, dev, slots))
+            and (limit is None or _plain(limit, _I32, dev, (B, Lq)))):
+        _require("attn_key_weight", dense=(q,), sliced=(k,), f32=(lse, weight, weight_out), u8=(workspace,),
+                 i32=(limit,))
+        _shapes("attn_key_weight", (k, (B, Hkv, Lk, D), "k"), (lse, (B, Hq, Lq), "lse"), (weight, slots, "weight"),
+                (weight_out, slots, "weight_out"), (limit, (B, Lq), "limit"))
     pitch = kv_row_pitch(k, k) if kv_pitch is None else int(kv_pitch)
-    st = load_library().attn_key_weight(_ptr(q), _ptr(k), _ptr(lse), _ptr(limit), _ptr(weight), _ptr(weight_out),
-                                        _ptr(workspace), workspace.numel(), pitch, B, Hq, Hkv, Lq, Lk, D,
-                                        float(scale), int(bool(causal)), _dtype_code(q), _stream_handle(stream))
+    st = load_library().attn_key_weight(q.data_ptr(), k.data_ptr(), lse.data_ptr(), _ptr(limit), _ptr(weight),
+                                        weight_out.data_ptr(), workspace.data_ptr(), workspace.numel(), pitch, B, Hq,
+                                        Hkv, Lq, Lk, D, float(scale), int(bool(causal)),
+                                        ATTN_DTYPE_BF16 if dt is _BF16 else ATTN_DTYPE_FP16,
+                                        _raw_stream(dev) if stream is None else _stream_handle(stream))
     return _check(st, "attn_key_weight", check)
 
 
@@ -498,18 +552,31 @@ def attn_cache_evict(k, v, weight, pos, cache_len, seen, weight_out, pos_out, ca
     """Keep, in every KV head, the `recent` newest tokens and the heaviest
     others, `keep` in all (changes k and v in place, writes weight_out,
     pos_out, cache_len_out)."""
-    _require("attn_cache_evict", sliced=(k, v), f32=(weight, weight_out), u8=(workspace,),
-             i32=(pos, cache_len, seen, pos_out, cache_len_out))
     B, Hkv, Lk, D = k.shape
-    _shapes("attn_cache_evict", (v, k.shape, "v"), (weight, (B, Hkv, Lk), "weight"), (pos, (B, Hkv, Lk), "pos"),
-            (weight_out, (B, Hkv, Lk), "weight_out"), (pos_out, (B, Hkv, Lk), "pos_out"),
-            (cache_len, (B,), "cache_len"), (seen, (B,), "seen"),
-            (cache_len_out, (B,), "cache_len_out"))
+    dt, dev, lens, slots = k.dtype, k.get_device(), (B,), (B, Hkv, Lk)
+    if not (dev >= 0 and dev == _current_device() and (dt is _BF16 or dt is _F16) and v.dtype is dt
+            and weight.dtype is weight_out.dtype is _F32 and workspace.dtype is _U8
+            and pos.dtype is cache_len.dtype is seen.dtype is pos_out.dtype is cache_len_out.dtype is _I32
+            and dev == v.get_device() == weight.get_device() == pos.get_device() == cache_len.get_device()
+            == seen.get_device() == weight_out.get_device() == pos_out.get_device() == cache_len_out.get_device()
+            == workspace.get_device()
+            and weight.is_contiguous() and pos.is_contiguous() and cache_len.is_contiguous() and seen.is_contiguous()
+            and weight_out.is_contiguous() and pos_out.is_contiguous() and cache_len_out.is_contiguous()
+            and workspace.is_contiguous()
+            and (v.shape, weight.shape, pos.shape, weight_out.shape, pos_out.shape, cache_len.shape, seen.shape,
+                 cache_len_out.shape) == (k.shape, slots, slots, slots, slots, lens, lens, lens)):
+        _require("attn_cache_evict", sliced=(k, v), f32=(weight, weight_out), u8=(workspace,),
+                 i32=(pos, cache_len, seen, pos_out, cache_len_out))
+        _shapes("attn_cache_evict", (v, k.shape, "v"), (weight, slots, "weight"), (pos, slots, "pos"),
+                (weight_out, slots, "weight_out"), (pos_out, slots, "pos_out"), (cache_len, lens, "cache_len"),
+                (seen, lens, "seen"), (cache_len_out, lens, "cache_len_out"))
     pitch = kv_row_pitch(k, v) if kv_pitch is None else int(kv_pitch)
-    st = load_library().attn_cache_evict(_ptr(k), _ptr(v), _ptr(weight), _ptr(pos), _ptr(cache_len), _ptr(seen),
-                                         _ptr(weight_out), _ptr(pos_out), _ptr(cache_len_out), _ptr(workspace),
+    st = load_library().attn_cache_evict(k.data_ptr(), v.data_ptr(), weight.data_ptr(), pos.data_ptr(),
+                                         cache_len.data_ptr(), seen.data_ptr(), weight_out.data_ptr(),
+                                         pos_out.data_ptr(), cache_len_out.data_ptr(), workspace.data_ptr(),
                                          workspace.numel(), pitch, B, Hkv, Lk, D, int(keep), int(recent),
-                                         _dtype_code(k), _stream_handle(stream))
+                                         ATTN_DTYPE_BF16 if dt is _BF16 else ATTN_DTYPE_FP16,
+                                         _raw_stream(dev) if stream is None else _stream_handle(stream))
     return _check(st, "attn_cache_evict", check)
 
 

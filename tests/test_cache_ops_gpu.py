@@ -542,3 +542,38 @@ def test_calls_in_a_graph_on_another_stream_and_two_at_once():
         g.replay()
         ok()
         assert all(torch.equal(h[n], w) for n, w in zip(names, plain[0]))
+
+
+def test_binding_refuses_wrong_tensors():
+    """Each wrong dtype, shape or layout raises, and names its tensor or type."""
+    gen = torch.Generator().manual_seed(1)
+    B, Hq, Hkv, T, Lk, D = 2, 4, 2, 3, 40, 64
+    z = lambda *s: torch.zeros(s, dtype=torch.int32, device="cuda")  # noqa: E731
+    f = lambda *s: torch.zeros(s, device="cuda")  # noqa: E731
+    q, k, kn = rand(gen, (B, Hq, T, D), BF), rand(gen, (B, Hkv, Lk, D), BF), rand(gen, (B, Hkv, T, D), BF)
+    ws = torch.empty(1 << 24, dtype=torch.uint8, device="cuda")
+    tree = dict(q=q, k=k, v=k.clone(), k_new=kn, v_new=kn.clone(), cache_len=z(B), o=torch.empty_like(q), lse=f(B, Hq, T),
+                workspace=ws, scale=0.1, tree_mask=torch.ones(B, T, T, dtype=torch.uint8, device="cuda"), tree_len=z(B))
+    weight = dict(q=q, k=k, lse=f(B, Hq, T), weight=f(B, Hkv, Lk), weight_out=f(B, Hkv, Lk), workspace=ws, scale=0.1,
+                  limit=z(B, T))
+    append = dict(k_new=kn, v_new=kn.clone(), k=k, v=k.clone(), cache_len=z(B), accept_len=z(B), cache_len_out=z(B),
+                  path=z(B, T), pos=z(B, Hkv, Lk), seen=z(B), seen_out=z(B), limit=z(B, T))
+    evict = dict(k=k, v=k.clone(), weight=f(B, Hkv, Lk), pos=z(B, Hkv, Lk), cache_len=z(B), seen=z(B),
+                 weight_out=f(B, Hkv, Lk), pos_out=z(B, Hkv, Lk), cache_len_out=z(B), workspace=ws, keep=10, recent=2)
+    for call, good in ((gbattn.attn_fwd_tree, tree), (gbattn.attn_key_weight, weight), (gbattn.attn_cache_append, append),
+                       (gbattn.attn_cache_evict, evict)):
+        assert call(**good) == gbattn.ATTN_OK
+        for name, t in good.items():
+            if not isinstance(t, torch.Tensor):
+                continue
+            with pytest.raises((TypeError, ValueError)):
+                call(**dict(good, **{name: t.to(torch.float64)}))
+            with pytest.raises(ValueError):
+                call(**dict(good, **{name: t.cpu()}))
+            if name != "workspace":
+                with pytest.raises(ValueError):
+                    call(**dict(good, **{name: t[..., :-1].contiguous()}))
+                if t.dim() > 1:
+                    with pytest.raises(ValueError):  # right shape, other strides
+                        call(**dict(good, **{name: t.transpose(0, 1).contiguous().transpose(0, 1)}))
+    ok()
