@@ -224,11 +224,11 @@ __global__ void __launch_bounds__(320, 1)
     tmem_relinquish();
   }
   grid_dependency_wait();  // the kernels before this one are complete
-  if (threadIdx.x == 0) grid_launch_dependents();
   if (p.limit) key_weight_table<BK>(p, tab);
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
+  if (threadIdx.x == 0) grid_launch_dependents();  // after tensor memory is allocated
   const uint32_t tmem = tmem_slot;
   const int n_kt = (p.Lk + BK - 1) / BK;
   KeyTileWalk w(p.limit ? tab : nullptr, n_kt, p.B, p.Hkv);
@@ -571,8 +571,7 @@ __global__ void __launch_bounds__(KeyWeightGeom<D>::NUM_THREADS, 1)
     tmem_alloc(smem_u32(&tmem_slot), Gm::TMEM_COLS);
     tmem_relinquish();
   }
-  grid_dependency_wait();                          // the kernels before this one are complete
-  if (threadIdx.x == 0) grid_launch_dependents();  // the join kernel waits for this grid before it reads partials
+  grid_dependency_wait();  // the kernels before this one are complete
   if (p.limit) {
     key_weight_table<256>(p, tab);
     __syncthreads();
@@ -582,6 +581,8 @@ __global__ void __launch_bounds__(KeyWeightGeom<D>::NUM_THREADS, 1)
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
+  // the join kernel waits for this grid before it reads partials (after tensor memory is allocated)
+  if (threadIdx.x == 0) grid_launch_dependents();
   const uint32_t tmem = tmem_slot;
   w.begin(start);
 

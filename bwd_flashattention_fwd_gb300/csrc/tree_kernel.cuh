@@ -266,8 +266,6 @@ __global__ void __launch_bounds__(TreeGeom<D, QS, NT>::NUM_THREADS, 1)
     tmem_relinquish();
   }
   grid_dependency_wait();  // the kernels before this one are complete
-  // the combine kernel may start; it waits for this grid before it reads partials
-  if (threadIdx.x == 0) grid_launch_dependents();
   tree_lengths_of_all(p, tab);
   if (warp == PRODUCER) {
     tree_table(p, tab);
@@ -276,6 +274,10 @@ __global__ void __launch_bounds__(TreeGeom<D, QS, NT>::NUM_THREADS, 1)
     tc_fence_before_sync();
     named_bar_sync(kTreeReady, Gm::NUM_THREADS);
     tc_fence_after_sync();
+    // The combine kernel may start; it waits for this grid before it reads
+    // partials.  (After tensor memory is allocated: a dependent that wants
+    // some cannot get in front.)
+    if (threadIdx.x == 0) grid_launch_dependents();
   }
   TreeWalk w(p, tab, group);
 
