@@ -172,12 +172,10 @@ __device__ __forceinline__ void evict_stay(const EvictParams& p, int bh, const u
   }
 }
 
-// The rows of the pairs (moving[i], freed[i]), i < n, and their weights and
-// positions: threads `all` of `step`, in 16-byte pieces.
+// The rows of the pairs (moving[i], freed[i]), i < n: threads `all` of `step`, in 16-byte pieces.
 template <class Index>
 __device__ __forceinline__ void evict_move(const EvictParams& p, int bh, const Index* moving, const Index* freed, int n,
                                            int all, int step) {
-  const size_t row = static_cast<size_t>(bh) * p.Lk;
   uint4* k = static_cast<uint4*>(p.k) + static_cast<size_t>(bh) * p.kv_pitch * p.row16;
   uint4* v = static_cast<uint4*>(p.v) + static_cast<size_t>(bh) * p.kv_pitch * p.row16;
   const int pieces = n * p.row16;  // at most 2^19 x 32
@@ -204,6 +202,13 @@ __device__ __forceinline__ void evict_move(const EvictParams& p, int bh, const I
     for (int u = 0; u < U; ++u)
       if (on[u]) k[to[u]] = a[u], v[to[u]] = e[u];
   }
+}
+
+// Their weights and positions.
+template <class Index>
+__device__ __forceinline__ void evict_move_values(const EvictParams& p, int bh, const Index* moving, const Index* freed,
+                                                  int n, int all, int step) {
+  const size_t row = static_cast<size_t>(bh) * p.Lk;
   for (int i = all; i < n; i += step) {
     const int to = freed[i], from = moving[i];
     if (!evict_slot_ok(p, row + to, 83) || !evict_slot_ok(p, row + from, 84)) continue;
@@ -234,21 +239,22 @@ __device__ __forceinline__ void evict_nothing(const EvictParams& p, int bh, int 
 }
 
 // Keys of the warp's slots w0 .. w1 - 1 into `keys` (from slot j0 on; null:
-// not kept) and their first digit into the counters; four strips' loads at a time.
+// not kept) and their first digit into the counters; U strips' loads at a time.
+template <int U>
 __device__ __forceinline__ void evict_load(const EvictParams& p, int bh, int w0, int w1, int j0, uint32_t* keys,
                                            long long recent_from, int* hist, int digit_shift) {
   const int lane = threadIdx.x & 31;
   const float* w = p.weight + static_cast<size_t>(bh) * p.Lk;
   const int32_t* pos = p.pos + static_cast<size_t>(bh) * p.Lk;
-  for (int i = w0 + lane; i - lane < w1; i += 128) {
-    float x[4];
-    int y[4];
+  for (int i = w0 + lane; i - lane < w1; i += 32 * U) {
+    float x[U];
+    int y[U];
 #pragma unroll
-    for (int u = 0; u < 4; ++u)
+    for (int u = 0; u < U; ++u)
       if (i + 32 * u < w1 && evict_slot_ok(p, static_cast<size_t>(bh) * p.Lk + i + 32 * u, 87))
         x[u] = w[i + 32 * u], y[u] = pos[i + 32 * u];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
+    for (int u = 0; u < U; ++u) {
       const bool in = i + 32 * u < w1;
       const uint32_t key = in ? evict_key(x[u], y[u], recent_from) : 0u;
       if (in && keys) keys[i + 32 * u - j0] = key;
@@ -303,7 +309,7 @@ __global__ void __launch_bounds__(kEvictThreads, 1) attn_cache_evict_kernel(cons
   const int w0 = min(warp * per_warp, len), w1 = min(w0 + per_warp, len);
   for (int i = tid; i < NH * BINS; i += kEvictThreads) (&hist[0][0])[i] = 0;
   __syncthreads();
-  evict_load(p, bh, w0, w1, 0, keys, recent_from, hist[lane & (NH - 1)], 21);
+  evict_load<5>(p, bh, w0, w1, 0, keys, recent_from, hist[lane & (NH - 1)], 21);
   __syncthreads();
   uint32_t prefix = 0;
   int need = keep;  // how many of the slots that match the digits so far are kept
@@ -390,9 +396,16 @@ __global__ void __launch_bounds__(kEvictThreads, 1) attn_cache_evict_kernel(cons
   uint16_t* moving = freed + share;
   if (on) evict_list(tid * 32, k, m, below, above, m0, m1, freed, moving);
   __syncthreads();
-  evict_move(p, bh, moving, freed, m1 - m0, tid, kEvictThreads);
-  evict_stay(p, bh, bits, 0, len, all, step);
-  evict_clear(p, bh, keep, all, step);
+  // rows and values side by side: one's latency does not wait for the other's
+  constexpr int ROW_THREADS = kEvictThreads * 3 / 4, VALUE_THREADS = kEvictThreads - ROW_THREADS;
+  if (tid < ROW_THREADS) {
+    evict_move(p, bh, moving, freed, m1 - m0, tid, ROW_THREADS);
+  } else {
+    const int t = tid - ROW_THREADS;
+    evict_stay(p, bh, bits, 0, len, rank * VALUE_THREADS + t, copies * VALUE_THREADS);
+    evict_move_values(p, bh, moving, freed, m1 - m0, t, VALUE_THREADS);
+    evict_clear(p, bh, keep, rank * VALUE_THREADS + t, copies * VALUE_THREADS);
+  }
 }
 
 // Value of another CTA's shared memory (cluster address).
@@ -454,7 +467,7 @@ __global__ void __launch_bounds__(kEvictClusterThreads) attn_cache_evict_cluster
   auto key_at = [&](int j) { return CACHED ? keys[j - j0] : evict_key(w[j], pos[j], recent_from); };
   for (int i = tid; i < 4 * BINS; i += kEvictClusterThreads) (&hist[0][0])[i] = (&first[0][0])[i] = 0;
   __syncthreads();
-  evict_load(p, bh, w0, w1, j0, CACHED ? keys : nullptr, recent_from, first[lane & 3], 24);
+  evict_load<4>(p, bh, w0, w1, j0, CACHED ? keys : nullptr, recent_from, first[lane & 3], 24);
   __syncthreads();
   if (tid < BINS) hist[0][tid] = first[0][tid] + first[1][tid] + first[2][tid] + first[3][tid];
   uint32_t prefix = 0;
@@ -594,8 +607,9 @@ __global__ void __launch_bounds__(256) attn_cache_move_kernel(const EvictParams 
   if (threadIdx.x == 0) grid_launch_dependents();
   const int bh = blockIdx.y, cap = p.Lk / 2;
   const int32_t* freed = p.lists + static_cast<size_t>(bh) * 2 * cap;
-  evict_move(p, bh, freed + cap, freed, p.counts[bh], static_cast<int>(blockIdx.x * 256 + threadIdx.x),
-             static_cast<int>(gridDim.x * 256));
+  const int all = static_cast<int>(blockIdx.x * 256 + threadIdx.x), step = static_cast<int>(gridDim.x * 256);
+  evict_move(p, bh, freed + cap, freed, p.counts[bh], all, step);
+  evict_move_values(p, bh, freed + cap, freed, p.counts[bh], all, step);
 }
 
 }  // namespace gbattn
