@@ -45,7 +45,7 @@ attn_status_t check_tree(int B, int Hq, int Hkv, int T, int Lk, int D) {
   if (s != ATTN_OK) return s;
   if (T > kTreeMaxT || B > kTreeMaxB) return ATTN_ERR_UNSUPPORTED;
   // stages of the whole call, and the combine kernel's rows per KV head, are ints that a grid takes
-  const long long stages = (Lk + kTreeStage - 1) / kTreeStage + (T + kTreeStage - 1) / kTreeStage + kTreeExtra;
+  const long long stages = (Lk + 63) / 64 + (T + 63) / 64 + kTreeExtra;
   if (stages * B * Hkv > 0x7fff0000LL) return ATTN_ERR_UNSUPPORTED;
   if (static_cast<long long>(Hq / Hkv) * T > 65535) return ATTN_ERR_UNSUPPORTED;
   return ATTN_OK;

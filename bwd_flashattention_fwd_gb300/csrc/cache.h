@@ -10,7 +10,10 @@ namespace gbattn {
 
 constexpr int kTreeMaxT = 1024;   // drafts per sequence (the mask is T x T bytes per sequence)
 constexpr int kTreeMaxB = 1024;   // sequences (each CTA holds the lengths' prefix sums in shared memory)
-constexpr int kTreeStage = 64;    // keys per pipeline stage
+// Keys per pipeline stage.  64 keys of K and V at D = 64 arrive in 0.37 us, less
+// than a stage's chain of S, softmax and P V takes, so small heads take 128
+// (B8 T8 16384 keys D = 64: 49.5 us, with 64 keys 66.0, one full tile 70.5).
+constexpr int tree_stage_keys(int D, int qs) { return D <= 96 && qs > 1 ? 128 : 64; }
 constexpr int kTreeExtra = 7;      // what a CTA spends on a KV head besides its stages, in stages
 constexpr int kTreeMaxCtas = 152;  // one per SM of a GB300
 constexpr int kCacheMaxLk = 1 << 30;  // rows of a KV head (row numbers are ints)
@@ -31,7 +34,7 @@ struct TreeParams {
   int* status;
   uint64_t limit_ns;
   // division of the work (tree_plan) and the partials of KV heads that several CTAs share
-  int n_rb, n_groups;
+  int stage, n_rb, n_groups;
   float* part;      // [n_groups][2][n_rb][rows][D]
   float* part_lse;  // [n_groups][2][n_rb][rows]
 };
@@ -39,15 +42,19 @@ struct TreeParams {
 // How the packed rows of a KV head (R = G * T) are laid out over CTAs: rows
 // per CTA, row blocks, and groups of n_rb CTAs that share out the keys.
 struct TreePlan {
-  int qs, nt, rows, n_rb, n_groups;
+  int qs, nt, rows, stage, n_rb, n_groups;
 };
 
 // R <= 32 / 64: the rows sit in four / two lane quadrants that share the keys
-// out; up to 128: one full tile; above: 256 rows per CTA where two
-// accumulators fit tensor memory (D <= 128).
+// out, where that pays: B1 T8 1000 keys D = 128, 32 rows, 9.95 us against 10.15
+// with one full tile; 64 rows at D = 128, 31.9 against 31.3, and D = 256 (8
+// rows, 131072 keys) 86.2 against 85.6, so those take the full tile.
+// Above 128 rows: 256 rows per CTA where two accumulators fit tensor memory
+// (D <= 128): B16 T61 ragged 76.9 us, with 128 rows per CTA 87.5.
 inline TreePlan tree_plan(long long R, int D, int num_sms) {
   TreePlan t;
-  t.qs = R <= 32 ? 4 : R <= 64 ? 2 : 1;
+  t.qs = R <= 32 && D <= 128 ? 4 : R <= 64 && D <= 96 ? 2 : 1;
+  t.stage = tree_stage_keys(D, t.qs);
   t.nt = R > 128 && D <= 128 ? 2 : 1;
   t.rows = t.qs > 1 ? 128 / t.qs : 128 * t.nt;
   t.n_rb = static_cast<int>((R + t.rows - 1) / t.rows);

@@ -66,9 +66,11 @@ int tree_impl(const TreeParams& p, EncodeTiledFn enc, cudaStream_t stream) {
 
 template <bool BF16>
 int tree_dispatch(const TreeParams& p, const TreePlan& plan, EncodeTiledFn enc, cudaStream_t stream) {
-  if (plan.qs == 4) return tree_impl<BF16, 4, 1>(p, enc, stream);
-  if (plan.qs == 2) return tree_impl<BF16, 2, 1>(p, enc, stream);
+  if constexpr (kD <= 96) {
+    if (plan.qs == 2) return tree_impl<BF16, 2, 1>(p, enc, stream);
+  }
   if constexpr (kD <= 128) {
+    if (plan.qs == 4) return tree_impl<BF16, 4, 1>(p, enc, stream);
     if (plan.nt == 2) return tree_impl<BF16, 1, 2>(p, enc, stream);
   }
   return tree_impl<BF16, 1, 1>(p, enc, stream);
@@ -127,7 +129,7 @@ int GBATTN_CAT(launch_tree_d, GBATTN_HEAD_DIM)(const TreeParams& p0, bool bf16, 
                                                cudaStream_t stream) {
   const TreePlan plan = tree_plan(static_cast<long long>(p0.G) * p0.T, kD, num_sms);
   TreeParams p = p0;
-  p.n_rb = plan.n_rb, p.n_groups = plan.n_groups;
+  p.stage = plan.stage, p.n_rb = plan.n_rb, p.n_groups = plan.n_groups;
   p.part_lse = p.part + static_cast<size_t>(plan.n_groups) * 2 * plan.n_rb * plan.rows * kD;
   return bf16 ? tree_dispatch<true>(p, plan, enc, stream) : tree_dispatch<false>(p, plan, enc, stream);
 }

@@ -10,7 +10,7 @@
 //
 // * Work is split over keys, evenly, whatever the lengths.  The G query heads
 //   x T drafts of a KV head are consecutive rows of q and form one packed block
-//   of R = G T rows.  A KV head's keys are a list of 64-key stages, its drafts'
+//   of R = G T rows.  A KV head's keys are a list of stages (64 keys, or 128), its drafts'
 //   stages first; the lists of all KV heads form one list of N stages, which
 //   the CTAs (one per SM) divide into equal ranges.  A range that holds a
 //   whole KV head writes O and lse; a partial one writes (O / l, lse) in fp32
@@ -19,11 +19,10 @@
 //
 // * The tensor cores always compute 128 rows, so few rows leave lanes idle
 //   unless they share the keys out: with R <= 32 the rows are loaded into all
-//   four 32-lane quadrants (QS = 4) and quadrant w takes keys 16w .. 16w + 15 of
-//   each stage, with its own m, l and O; P is zero at the other quadrants'
+//   four 32-lane quadrants (QS = 4) and each quadrant takes a quarter of a
+//   stage's keys, with its own m, l and O; P is zero at the other quadrants'
 //   keys, so O += P V keeps them apart.  R <= 64: two (QS = 2).  The quadrants
-//   are merged when the range ends.  Per stage a softmax thread then handles
-//   64 / QS keys, and the exponentials stay far below the time of the loads.
+//   are merged when the range ends.  tree_plan has the rule and its figures.
 //
 // * More than 128 rows (NT = 2, D <= 128): a CTA takes 256 rows as two tiles
 //   that share every stage, with a softmax warpgroup and an MMA warp each.
@@ -31,7 +30,7 @@
 //   with different rows, so the keys come from memory once and then from L2.
 //
 // Warp roles: 4 NT softmax warps (thread = row of the tile = TMEM lane), one
-// TMA producer, NT MMA issuers.  S has two 64-column buffers per tile, P is
+// TMA producer, NT MMA issuers.  S has two buffers per tile, P is
 // written over the S it came from, a row keeps its reference m until a stage
 // raises its maximum by more than 8 (log2 units), so O is rescaled rarely;
 // O / l and m + log2 l use the same reference.
@@ -61,7 +60,7 @@ constexpr int kTreeStaticSmem = sizeof(TreeTable) + 4096;
 
 template <int D, int QS, int NT>
 struct TreeGeom {
-  static constexpr int BK = kTreeStage;   // keys per stage
+  static constexpr int BK = tree_stage_keys(D, QS);  // keys per stage
   static constexpr int KPW = BK / QS;     // keys per softmax thread and stage
   static constexpr int ROWS = QS > 1 ? 128 / QS : 128 * NT;  // packed rows per CTA
   static constexpr int QROWS = 128 / QS;  // rows of a Q load
@@ -90,8 +89,8 @@ __device__ __forceinline__ void tree_lengths(const TreeParams& p, int b, int& le
   len = min(max(p.cache_len[b], 0), p.Lk);
   tl = p.tree_len ? min(max(p.tree_len[b], 0), p.T) : p.T;
 }
-__device__ __forceinline__ int tree_stages(int len, int tl) {
-  return tl == 0 ? 0 : (len + kTreeStage - 1) / kTreeStage + (tl + kTreeStage - 1) / kTreeStage;
+__device__ __forceinline__ int tree_stages(int len, int tl, int stage) {
+  return tl == 0 ? 0 : (len + stage - 1) / stage + (tl + stage - 1) / stage;
 }
 
 // Fills the table: one warp for up to 32 sequences; for more, the whole block
@@ -102,7 +101,7 @@ __device__ __forceinline__ int tree_load(const TreeParams& p, TreeTable& tab, in
   tree_lengths(p, b, len, tl);
   tab.len[b] = len;
   tab.tl[b] = static_cast<uint16_t>(tl);
-  return tree_stages(len, tl);
+  return tree_stages(len, tl, p.stage);
 }
 __device__ __forceinline__ void tree_lengths_of_all(const TreeParams& p, TreeTable& tab) {
   if (p.B <= 32) return;
@@ -565,25 +564,23 @@ __global__ void __launch_bounds__(TreeGeom<D, QS, NT>::NUM_THREADS, 1)
           f2_unpack(f2_add(sum[0], sum[1]), s0, s1);
           l += s0 + s1;
         }
-        // P over the stage's S: pairs of keys in 32 columns, zeros at the other quadrants' keys
-        if constexpr (QS == 1) {
-          tmem_st16(s_col, pk[0]);
-          tmem_st16(s_col + 16, pk[1]);
-        } else {
-          uint32_t zero[NV / 2];
+        // P over the stage's S: pairs of keys, zeros at the other quadrants' keys
+        uint32_t zero[NV / 2];
 #pragma unroll
-          for (int i = 0; i < NV / 2; ++i) zero[i] = 0u;
+        for (int i = 0; i < NV / 2; ++i) zero[i] = 0u;
 #pragma unroll
-          for (int i = 0; i < QS; ++i) {
-            if constexpr (QS == 4) {
-              if (i == kq) tmem_st8(s_col + i * 8, pk[0]);
-              else tmem_st8(s_col + i * 8, zero);
+        for (int i = 0; i < QS; ++i)
+#pragma unroll
+          for (int h = 0; h < NB; ++h) {
+            const uint32_t col = s_col + i * (KPW / 2) + h * 16;
+            if constexpr (NV == 32) {
+              if (i == kq) tmem_st16(col, pk[h]);
+              else tmem_st16(col, zero);
             } else {
-              if (i == kq) tmem_st16(s_col + i * 16, pk[0]);
-              else tmem_st16(s_col + i * 16, zero);
+              if (i == kq) tmem_st8(col, pk[h]);
+              else tmem_st8(col, zero);
             }
           }
-        }
         tmem_st_wait();
         tc_fence_before_sync();
         mbar_arrive(smem_u32(&bar_pready[t][bb]));
