@@ -13,7 +13,7 @@ constexpr int kTreeMaxB = 1024;   // sequences (each CTA holds the lengths' pref
 // Keys per pipeline stage.  64 keys of K and V at D = 64 arrive in 0.37 us, less
 // than a stage's chain of S, softmax and P V takes, so small heads take 128
 // (B8 T8 16384 keys D = 64: 49.5 us, with 64 keys 66.0, one full tile 70.5).
-constexpr int tree_stage_keys(int D, int qs) { return D <= 96 && qs > 1 ? 128 : 64; }
+constexpr int tree_stage_keys(int D, int nt) { return D <= 96 && nt == 1 ? 128 : 64; }
 constexpr int kTreeExtra = 7;      // what a CTA spends on a KV head besides its stages, in stages
 constexpr int kTreeMaxCtas = 152;  // one per SM of a GB300
 constexpr int kCacheMaxLk = 1 << 30;  // rows of a KV head (row numbers are ints)
@@ -54,8 +54,8 @@ struct TreePlan {
 inline TreePlan tree_plan(long long R, int D, int num_sms) {
   TreePlan t;
   t.qs = R <= 32 && D <= 128 ? 4 : R <= 64 && D <= 96 ? 2 : 1;
-  t.stage = tree_stage_keys(D, t.qs);
   t.nt = R > 128 && D <= 128 ? 2 : 1;
+  t.stage = tree_stage_keys(D, t.nt);
   t.rows = t.qs > 1 ? 128 / t.qs : 128 * t.nt;
   t.n_rb = static_cast<int>((R + t.rows - 1) / t.rows);
   const int ctas = num_sms < kTreeMaxCtas ? num_sms : kTreeMaxCtas;

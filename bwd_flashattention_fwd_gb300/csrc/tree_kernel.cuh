@@ -60,8 +60,10 @@ constexpr int kTreeStaticSmem = sizeof(TreeTable) + 4096;
 
 template <int D, int QS, int NT>
 struct TreeGeom {
-  static constexpr int BK = tree_stage_keys(D, QS);  // keys per stage
-  static constexpr int KPW = BK / QS;     // keys per softmax thread and stage
+  static constexpr int BK = tree_stage_keys(D, NT);  // keys per stage
+  static constexpr int KPW = BK / QS;     // keys per softmax thread and stage,
+  static constexpr int NV = KPW > 32 ? 32 : KPW;  // in NB blocks of NV
+  static constexpr int NB = KPW / NV;
   static constexpr int ROWS = QS > 1 ? 128 / QS : 128 * NT;  // packed rows per CTA
   static constexpr int QROWS = 128 / QS;  // rows of a Q load
   static constexpr int NCH = n_chunks(D);
@@ -213,7 +215,7 @@ __global__ void __launch_bounds__(TreeGeom<D, QS, NT>::NUM_THREADS, 1)
                      const __grid_constant__ CUtensorMap tmVn, const TreeParams p) {
   using Gm = TreeGeom<D, QS, NT>;
   using E = Elem<BF16>;
-  constexpr int BK = Gm::BK, NCH = Gm::NCH, SL = Gm::SLOTS, KPW = Gm::KPW;
+  constexpr int BK = Gm::BK, NCH = Gm::NCH, SL = Gm::SLOTS, KPW = Gm::KPW, NV = Gm::NV, NB = Gm::NB;
   constexpr int PRODUCER = Gm::SOFTMAX_WARPS;
   constexpr int kWait = wait_code<94>();  // every bounded wait of this kernel
 
@@ -448,36 +450,37 @@ __global__ void __launch_bounds__(TreeGeom<D, QS, NT>::NUM_THREADS, 1)
         const bool draft = j < nd;
         const int k0 = draft ? j * BK : (j - nd) * BK;
         const int valid = min((draft ? tl : len) - k0, BK);  // keys of the stage that exist
-        // which of this thread's keys its row sees
-        uint64_t see = ~0ull;
-        if (draft) {
-          see = 0ull;
+        // which of this thread's keys its row sees, NV bits at a time
+        uint32_t see[NB];
+        auto first_n = [&](int n) {  // the first n of them
+#pragma unroll
+          for (int h = 0; h < NB; ++h) {
+            const int m = n - h * NV;
+            see[h] = m <= 0 ? 0u : m >= 32 ? ~0u : (1u << m) - 1u;
+          }
+        };
+        if (draft && p.mask) {
+          // the warp reads 32 / NV mask rows at a time, a byte per lane, and
+          // every lane keeps the bits of its own row
           const int most = min(valid - c0, KPW);
-          if (p.mask) {
-            // the warp reads 32 / KPW (at least one) mask rows at a time, a byte
-            // per lane, and every lane keeps the bits of its own row
-            const uint8_t* mb = p.mask + static_cast<size_t>(w.b) * p.T * p.T + k0 + c0;
-            constexpr int STEP = KPW < 32 ? KPW : 32, AT_ONCE = 32 / STEP;
+          const uint8_t* mb = p.mask + static_cast<size_t>(w.b) * p.T * p.T + k0 + c0;
+          constexpr int AT_ONCE = 32 / NV;
+#pragma unroll
+          for (int h = 0; h < NB; ++h) {
+            see[h] = 0u;
 #pragma unroll 16
             for (int i = 0; i < 32; i += AT_ONCE) {
-              const int mt = __shfl_sync(0xffffffffu, trow, i + lane / STEP);
-#pragma unroll
-              for (int h = 0; h < KPW; h += STEP) {
-                const int u = h + lane % STEP;
-                const uint32_t bits = __ballot_sync(0xffffffffu, u < most && dbg_in_range(mb - p.mask + static_cast<size_t>(mt) * p.T + u, 1,
-                                                                 static_cast<size_t>(p.B) * p.T * p.T, p.status, 63) &&
-                                    mb[static_cast<size_t>(mt) * p.T + u] != 0);
-                if (lane / AT_ONCE == i / AT_ONCE)
-                  see |= static_cast<uint64_t>(STEP == 32 ? bits : (bits >> ((lane % AT_ONCE) * STEP)) & ((1u << (STEP & 31)) - 1u)) << h;
-              }
+              const int mt = __shfl_sync(0xffffffffu, trow, i + lane / NV);
+              const int u = h * NV + lane % NV;
+              const uint32_t bits =
+                  __ballot_sync(0xffffffffu, u < most && dbg_in_range(mb - p.mask + static_cast<size_t>(mt) * p.T + u, 1,
+                                                                      static_cast<size_t>(p.B) * p.T * p.T, p.status, 63) &&
+                                                 mb[static_cast<size_t>(mt) * p.T + u] != 0);
+              if (lane / AT_ONCE == i / AT_ONCE) see[h] = NV == 32 ? bits : (bits >> ((lane % AT_ONCE) * NV)) & ((1u << (NV & 31)) - 1u);
             }
-          } else {
-            const int n_see = min(most, trow - (k0 + c0) + 1);
-            see = n_see <= 0 ? 0ull : n_see >= 64 ? ~0ull : (1ull << n_see) - 1ull;
           }
-        } else if (valid < BK) {
-          const int mine = valid - c0;
-          see = mine <= 0 ? 0ull : mine >= 64 ? ~0ull : (1ull << mine) - 1ull;
+        } else {
+          first_n(draft ? min(valid - c0, trow - (k0 + c0) + 1) : valid - c0);
         }
         const int bb = ts & 1;
         const uint32_t s_col = tmem + lanes + Gm::s_col(t, bb);
@@ -499,8 +502,6 @@ __global__ void __launch_bounds__(TreeGeom<D, QS, NT>::NUM_THREADS, 1)
         }
         __syncwarp();
         tc_fence_after_sync();
-        constexpr int NV = KPW > 32 ? 32 : KPW;  // values per register block
-        constexpr int NB = KPW / NV;
         uint32_t v[NB][NV];
 #pragma unroll
         for (int h = 0; h < NB; ++h) {
@@ -508,13 +509,14 @@ __global__ void __launch_bounds__(TreeGeom<D, QS, NT>::NUM_THREADS, 1)
           else tmem_ld16(s_col + c0, v[h]);
         }
         tmem_ld_wait(v[0]);
-        if constexpr (NB == 2) reg_fence(v[1]);
+#pragma unroll
+        for (int h = 1; h < NB; ++h) reg_fence(v[h]);
         if (draft || valid < BK) {
 #pragma unroll
           for (int h = 0; h < NB; ++h)
 #pragma unroll
             for (int i = 0; i < NV; ++i)
-              if (!((see >> (h * NV + i)) & 1ull)) v[h][i] = __float_as_uint(-INFINITY);
+              if (!((see[h] >> i) & 1u)) v[h][i] = __float_as_uint(-INFINITY);
         }
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll

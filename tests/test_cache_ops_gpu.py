@@ -139,6 +139,12 @@ TREES = [
     (1000, 1, 1, 1, 70, 64, HF, [(7 * i) % 71 for i in range(1000)], None, None),
     (1, 40, 1, 1000, 60, 64, BF, [50], [990], None),  # more blocks of rows than SMs
     (1, 1, 1, 1024, 10, 128, BF, [10], None, "tree"),
+    (2, 4, 1, 20, 333, 64, BF, [333, 128], [20, 7], "tree"),
+    (1, 2, 1, 60, 200, 96, HF, [129], None, "tree"),
+    (2, 2, 1, 30, 500, 64, BF, [500, 127], [30, 29], "tree"),
+    (1, 3, 1, 21, 450, 96, BF, [450], [20], None),
+    (1, 1, 1, 100, 260, 64, BF, [256], [97], "tree"),
+    (1, 1, 1, 128, 300, 96, BF, [299], None, "tree"),
 ]
 
 
