@@ -51,7 +51,8 @@ int tree_impl(const TreeParams& p, EncodeTiledFn enc, cudaStream_t stream) {
                                  Gm::SMEM_BYTES, stream, tq, tk, tv, tkn, tvn, p);
   if (r != kLaunchOk) return r;
   if (p.n_groups == 1) return kLaunchOk;  // no KV head is shared
-  // warps per 4 columns by how many partials a head has on average
+  // warps per 4 columns by how many partials a head has on average (131072 keys
+  // D = 256, 38 partials: 86.2 us with 8, 95.1 with one; B1 T8 1000 keys, 17: 10.1 and 14.0)
   const long long avg = p.n_groups / heads + 1;
   auto combine = [&](auto kern_c, int cols_per_block) {
     const long long tasks = heads * ((R + 31) / 32) * (kD / cols_per_block);
@@ -114,6 +115,8 @@ int key_weight_many(const KeyWeightParams& p, int num_sms, EncodeTiledFn enc, cu
 template <bool BF16>
 int key_weight_dispatch(const KeyWeightParams& p, int num_sms, EncodeTiledFn enc, cudaStream_t stream) {
   const long long R = static_cast<long long>(p.G) * p.Lq;
+  // the smallest tile that holds the rows: 32 rows over 4 x 8192 keys 15.9 us, in
+  // a 128-row tile 16.9; 128 rows 19.7, by the kernel for many rows 31.7
   if (R <= 16) return key_weight_few<BF16, 16>(p, num_sms, enc, stream);
   if (R <= 32) return key_weight_few<BF16, 32>(p, num_sms, enc, stream);
   if (R <= 64) return key_weight_few<BF16, 64>(p, num_sms, enc, stream);

@@ -1,5 +1,7 @@
 // The two cache calls that move rows: appending accepted drafts and evicting
-// the lightest keys.  Both are bound by memory traffic and latency.
+// the lightest keys.  Both are bound by memory traffic and latency: a prompt of
+// 2 x 2048 tokens, 8 heads, D = 128 is appended in 7.1 us (33.6 MB, 4.7 TB/s,
+// launch included), 8 drafts in 2.5.
 #pragma once
 
 #include "cache.h"
@@ -423,8 +425,8 @@ __device__ __forceinline__ int ld_cluster(uint32_t addr) {
   return v;
 }
 
-// The same for longer rows, one cluster of 8 CTAs per KV head (of 16: 28.8 us
-// for 32768 slots where 8 take 27.9); each CTA owns
+// The same for longer rows, one cluster of 8 CTAs per KV head (8 heads of
+// 32768 slots: 23 us; 28 with the moves in this kernel); each CTA owns
 // a consecutive part of the slots and keeps their keys in shared memory
 // (CACHED; parts that do not fit are read again in each pass).  Four digits of
 // 8 bits: what a digit costs is reading every CTA's histogram through
