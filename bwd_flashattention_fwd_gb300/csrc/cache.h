@@ -135,9 +135,11 @@ bool set_smem_limit(Kern kern, size_t smem, std::atomic<uint64_t>& done) {
 }
 
 // Launch as a programmatic dependent of the kernel before it on the stream:
-// its CTAs may start (and set up) while that kernel finishes; every kernel of
-// the cache calls waits for it (griddepcontrol.wait) before it reads or writes
-// global memory, so stream order holds for the caller.
+// its CTAs may start (and set up) while that kernel finishes.  A call's first
+// kernel waits for it (griddepcontrol.wait) before it reads or writes global
+// memory or allocates tensor memory, and lets its own dependents start behind
+// that; a second kernel reads nothing but lengths before its wait.  So stream
+// order holds for the caller.
 template <typename... Params, typename... Args>
 int launch_dependent(void (*kern)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t stream, Args... args) {
   cudaLaunchConfig_t cfg = {};

@@ -22,7 +22,7 @@ constexpr int kAppendThreads = 256;
 // x + gridDim.x, ... of the path, 16 bytes per thread; block (0, b * Hkv)
 // writes the sequence's lengths and key limits.
 __global__ void __launch_bounds__(kAppendThreads) attn_cache_append_kernel(const AppendParams p) {
-  __shared__ int cut;
+  __shared__ int cut, lims[kTreeMaxT];  // (a path has at most kTreeMaxT entries)
   grid_dependency_wait();  // the kernels before this one are complete
   if (threadIdx.x == 0) grid_launch_dependents();
   const int bh = blockIdx.y, b = bh / p.Hkv;
@@ -70,15 +70,15 @@ __global__ void __launch_bounds__(kAppendThreads) attn_cache_append_kernel(const
     }
     if (p.limit) {
       int32_t* limit = p.limit + static_cast<size_t>(b) * p.T;
-      for (int t = threadIdx.x; t < p.T; t += kAppendThreads) {
-        int lim = 0;
-        if (!path) {
-          lim = t < n ? len + t + 1 : 0;
-        } else {
-          for (int i = 0; i < n; ++i)
-            if (path[i] == t) lim = len + i + 1;
-        }
-        limit[t] = lim;
+      if (path) {
+        // the last of equal entries: the largest limit, whatever the order of the maxima
+        for (int t = threadIdx.x; t < p.T; t += kAppendThreads) lims[t] = 0;
+        __syncthreads();
+        for (int i = threadIdx.x; i < n; i += kAppendThreads) atomicMax(&lims[path[i]], len + i + 1);
+        __syncthreads();
+        for (int t = threadIdx.x; t < p.T; t += kAppendThreads) limit[t] = lims[t];
+      } else {
+        for (int t = threadIdx.x; t < p.T; t += kAppendThreads) limit[t] = t < n ? len + t + 1 : 0;
       }
     }
   }

@@ -223,11 +223,11 @@ __global__ void __launch_bounds__(320, 1)
     mbar_init(smem_u32(&bar_mfin), 1);
     fence_mbar_init();
   }
-  if (warp == Gm::MMA) {
+  grid_dependency_wait();  // the kernels before this one are complete
+  if (warp == Gm::MMA) {  // (behind that, so that those have had theirs)
     tmem_alloc(smem_u32(&tmem_slot), Gm::TMEM_COLS);
     tmem_relinquish();
   }
-  grid_dependency_wait();  // the kernels before this one are complete
   if (p.limit) key_weight_table<BK>(p, tab);
   tc_fence_before_sync();
   __syncthreads();
@@ -571,11 +571,11 @@ __global__ void __launch_bounds__(KeyWeightGeom<D>::NUM_THREADS, 1)
     mbar_init(smem_u32(&bar_mfin), 1);
     fence_mbar_init();
   }
-  if (warp == Gm::MMA) {
+  grid_dependency_wait();  // the kernels before this one are complete
+  if (warp == Gm::MMA) {  // (behind that, so that those have had theirs)
     tmem_alloc(smem_u32(&tmem_slot), Gm::TMEM_COLS);
     tmem_relinquish();
   }
-  grid_dependency_wait();  // the kernels before this one are complete
   if (p.limit) {
     key_weight_table<256>(p, tab);
     __syncthreads();

@@ -267,11 +267,14 @@ __global__ void __launch_bounds__(TreeGeom<D, QS, NT>::NUM_THREADS, 1)
       fence_mbar_init();
     }
     __syncwarp();
-  } else if (warp == PRODUCER + 1) {
+  }
+  grid_dependency_wait();  // the kernels before this one are complete
+  // (Tensor memory is allocated behind that: a kernel before this one whose
+  // CTA has not allocated its own yet cannot be left without.)
+  if (warp == PRODUCER + 1) {
     tmem_alloc(smem_u32(&tmem_slot), Gm::TMEM_COLS);
     tmem_relinquish();
   }
-  grid_dependency_wait();  // the kernels before this one are complete
   tree_lengths_of_all(p, tab);
   if (warp == PRODUCER) {
     tree_table(p, tab);
