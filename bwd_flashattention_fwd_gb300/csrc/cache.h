@@ -15,6 +15,13 @@ constexpr int kTreeMaxB = 1024;   // sequences (each CTA holds the lengths' pref
 // (B8 T8 16384 keys D = 64: 49.5 us, with 64 keys 66.0, one full tile 70.5).
 constexpr int tree_stage_keys(int D, int nt) { return D <= 96 && nt == 1 ? 128 : 64; }
 constexpr int kTreeExtra = 7;      // what a CTA spends on a KV head besides its stages, in stages
+// Small caches: KV heads are not divided, which saves the partials and the
+// second launch, where a CTA's stages are at most kTreeWholeMost and at most
+// kTreeWholeMore above an even share.  B2 T47 200 keys D = 64 (5 stages) 10.8
+// us, divided 15.7; B24 T4 400 keys D = 128 (2 heads of 8 stages) 18.1 and
+// 21.4; B1 T8 400 keys (8 stages) 10.0 and 9.6 on the device, with one launch
+// for the host instead of two; 700 keys (12 stages) 11.8 and 10.0.
+constexpr int kTreeWholeMost = 24, kTreeWholeMore = 8;
 constexpr int kTreeMaxCtas = 152;  // one per SM of a GB300
 constexpr int kCacheMaxLk = 1 << 30;  // rows of a KV head (row numbers are ints)
 constexpr int kEvictMaxLk = 1 << 20;
@@ -35,6 +42,7 @@ struct TreeParams {
   uint64_t limit_ns;
   // division of the work (tree_plan) and the partials of KV heads that several CTAs share
   int stage, n_rb, n_groups;
+  int whole;        // > 0: KV heads per group, undivided; no partials, no combine
   float* part;      // [n_groups][2][n_rb][rows][D]
   float* part_lse;  // [n_groups][2][n_rb][rows]
 };

@@ -50,7 +50,7 @@ int tree_impl(const TreeParams& p, EncodeTiledFn enc, cudaStream_t stream) {
   const int r = launch_dependent(kern, dim3(p.n_groups * p.n_rb), Gm::NUM_THREADS,
                                  Gm::SMEM_BYTES, stream, tq, tk, tv, tkn, tvn, p);
   if (r != kLaunchOk) return r;
-  if (p.n_groups == 1) return kLaunchOk;  // no KV head is shared
+  if (p.n_groups == 1 || p.whole) return kLaunchOk;  // no KV head is shared
   // warps per 4 columns by how many partials a head has on average (131072 keys
   // D = 256, 38 partials: 86.2 us with 8, 95.1 with one; B1 T8 1000 keys, 17: 10.1 and 14.0)
   const long long avg = p.n_groups / heads + 1;
@@ -134,6 +134,12 @@ int GBATTN_CAT(launch_tree_d, GBATTN_HEAD_DIM)(const TreeParams& p0, bool bf16, 
   TreeParams p = p0;
   p.stage = plan.stage, p.n_rb = plan.n_rb, p.n_groups = plan.n_groups;
   p.part_lse = p.part + static_cast<size_t>(plan.n_groups) * 2 * plan.n_rb * plan.rows * kD;
+  const long long heads = static_cast<long long>(p.B) * p.Hkv, each = (heads + p.n_groups - 1) / p.n_groups;
+  const long long stages = (p.Lk + p.stage - 1) / p.stage + (p.T + p.stage - 1) / p.stage;
+  if (each * stages <= kTreeWholeMost && (each * p.n_groups - heads) * stages <= kTreeWholeMore * p.n_groups) {
+    p.whole = static_cast<int>(each);
+    p.n_groups = static_cast<int>((heads + each - 1) / each);
+  }
   return bf16 ? tree_dispatch<true>(p, plan, enc, stream) : tree_dispatch<false>(p, plan, enc, stream);
 }
 

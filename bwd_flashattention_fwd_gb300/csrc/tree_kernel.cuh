@@ -167,9 +167,18 @@ struct TreeWalk {
   bool more_;
   __device__ __forceinline__ TreeWalk(const TreeParams& p, const TreeTable& tab_, int group) : tab(tab_), Hkv(p.Hkv) {
     const int total = tab.pre[p.B] * p.Hkv, per = tree_per(total, p.n_groups);
-    const long long from = static_cast<long long>(group) * per;
-    lo = from < total ? static_cast<int>(from) : total;
-    xe = from + per < total ? static_cast<int>(from + per) : total;
+    if (p.whole) {
+      auto first = [&](int head) {
+        const int i = head / Hkv;
+        return i < p.B ? tab.pre[i] * Hkv + (head - i * Hkv) * (tab.pre[i + 1] - tab.pre[i]) : total;
+      };
+      lo = first(min(group * p.whole, p.B * Hkv));
+      xe = first(min((group + 1) * p.whole, p.B * Hkv));
+    } else {
+      const long long from = static_cast<long long>(group) * per;
+      lo = from < total ? static_cast<int>(from) : total;
+      xe = from + per < total ? static_cast<int>(from + per) : total;
+    }
     more_ = lo < xe;
     if (more_) {
       b = tree_find(tab.pre, p.B, p.Hkv, lo);

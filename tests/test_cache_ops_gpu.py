@@ -170,6 +170,27 @@ def test_tree(case, stale):
     assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])
 
 
+# Small caches (whole KV heads, several of them per CTA, empty ones between)
+# and short contexts in large ones (divided into single stages).
+TREES_WHOLE_OR_DIVIDED = [
+    (64, 16, 8, 2, 200, 128, BF, [(53 * i) % 201 for i in range(64)], [i % 3 for i in range(64)], "tree"),
+    (20, 8, 8, 5, 380, 256, HF, [(91 * i) % 381 for i in range(20)], [(i + 1) % 6 for i in range(20)], None),
+    (40, 16, 2, 128, 70, 64, BF, [(19 * i) % 71 for i in range(40)], [(41 * i) % 129 for i in range(40)], "tree"),
+    (30, 12, 6, 31, 300, 96, HF, [(77 * i) % 301 for i in range(30)], None, "tree"),
+    (19, 8, 8, 1, 512, 128, BF, [512] * 18 + [0], [1] * 17 + [0, 1], None),
+    (6, 16, 4, 7, 4000, 128, BF, [0, 1, 64, 65, 130, 200], [7, 0, 1, 7, 3, 5], "tree"),
+    (6, 16, 4, 50, 3900, 64, HF, [0, 1, 64, 65, 130, 200], [50, 0, 1, 33, 3, 5], "tree"),
+    (3, 8, 2, 9, 2500, 256, BF, [5, 0, 129], None, "tree"),
+    (5, 4, 4, 20, 5000, 96, BF, [128, 5000, 0, 3, 129], [20, 1, 0, 17, 20], "tree"),
+]
+
+
+@pytest.mark.parametrize("case", TREES_WHOLE_OR_DIVIDED, ids=lambda c: f"b{c[0]}_h{c[1]}x{c[2]}_t{c[3]}_k{c[4]}_d{c[5]}")
+@pytest.mark.parametrize("stale", [None, float("nan")], ids=["dirty", "nan"])
+def test_tree_whole_or_divided_heads(case, stale):
+    test_tree(case, stale)
+
+
 def test_tree_rows_without_keys_and_lengths_out_of_range():
     gen = torch.Generator().manual_seed(5)
     B, Hq, Hkv, T, Lk, D = 4, 4, 2, 6, 150, 128
