@@ -222,6 +222,44 @@ __device__ __forceinline__ size_t tree_slot_row(const TreeParams& p, int group, 
   return ((static_cast<size_t>(group) * 2 + slot) * p.n_rb + rb) * rows;
 }
 
+// see &= which of the N bytes mask[at], mask[at + 1], ... are not zero, 32 bits
+// to a word; only the first `most` are needed, and the mask has n bytes.  The
+// words that cover them are loaded together, each aligned (a mask row begins at
+// any byte), so a stage waits for one latency.  (Rows read a byte per lane, 16
+// at a time, and balloted took 18,000 clocks of a CTA's 100,000 at B16 T61.)
+template <int N, int NB>
+__device__ __forceinline__ void tree_mask_bits(const uint8_t* mask, size_t at, size_t n, int most, uint32_t (&see)[NB]) {
+  constexpr int W = N / 4;
+  const int lead = static_cast<int>((reinterpret_cast<uintptr_t>(mask) + at) & 3u);
+  uint32_t x[W + 1];
+  if (at >= static_cast<size_t>(lead) && at - lead + 4 * (W + 1) <= n) {
+    const uint32_t* word = reinterpret_cast<const uint32_t*>(mask + at - lead);
+#pragma unroll
+    for (int i = 0; i <= W; ++i) x[i] = 4 * i - lead < most ? word[i] : 0u;
+#pragma unroll
+    for (int i = 0; i < W; ++i) x[i] = __funnelshift_r(x[i], x[i + 1], 8 * lead);
+  } else {  // at the mask's ends: byte by byte
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      x[i] = 0u;
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        if (4 * i + c < most) x[i] |= static_cast<uint32_t>(mask[at + 4 * i + c]) << (8 * c);
+    }
+  }
+#pragma unroll
+  for (int h = 0; h < NB; ++h) {
+    uint32_t bits = 0u;
+#pragma unroll
+    for (int i = 0; i < W / NB; ++i) {
+      uint32_t y = x[h * (W / NB) + i];
+      y |= y >> 4, y |= y >> 2, y |= y >> 1;            // bit 0 of a byte: any of its bits
+      bits |= (((y & 0x01010101u) * 0x10204080u) >> 28) << (4 * i);  // the four of them side by side
+    }
+    see[h] &= bits;
+  }
+}
+
 constexpr int kTreeReady = 3;  // named barrier (1 and 2: the tiles' softmax warps)
 
 template <int D, bool BF16, int QS, int NT>
@@ -443,6 +481,7 @@ __global__ void __launch_bounds__(TreeGeom<D, QS, NT>::NUM_THREADS, 1)
     const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
     const uint32_t o_col = tmem + lanes + Gm::o_col(t);
     const float sl2 = p.scale_log2;
+    const size_t n_mask = static_cast<size_t>(p.B) * p.T * p.T;
     // extents for the debug build's index checks: rows of o / lse, and of the partials
     [[maybe_unused]] const size_t n_rows = static_cast<size_t>(p.B) * p.Hkv * R;
     [[maybe_unused]] const size_t n_parts = static_cast<size_t>(p.n_groups) * 2 * p.n_rb * Gm::ROWS;
@@ -479,25 +518,11 @@ __global__ void __launch_bounds__(TreeGeom<D, QS, NT>::NUM_THREADS, 1)
           }
         };
         if (draft && p.mask) {
-          // the warp reads 32 / NV mask rows at a time, a byte per lane, and
-          // every lane keeps the bits of its own row
+          // bytes of the lane's own mask row from this stage's keys on (only the first `most` of them count)
           const int most = min(valid - c0, KPW);
-          const uint8_t* mb = p.mask + static_cast<size_t>(w.b) * p.T * p.T + k0 + c0;
-          constexpr int AT_ONCE = 32 / NV;
-#pragma unroll
-          for (int h = 0; h < NB; ++h) {
-            see[h] = 0u;
-#pragma unroll 16
-            for (int i = 0; i < 32; i += AT_ONCE) {
-              const int mt = __shfl_sync(0xffffffffu, trow, i + lane / NV);
-              const int u = h * NV + lane % NV;
-              const uint32_t bits =
-                  __ballot_sync(0xffffffffu, u < most && dbg_in_range(mb - p.mask + static_cast<size_t>(mt) * p.T + u, 1,
-                                                                      static_cast<size_t>(p.B) * p.T * p.T, p.status, 63) &&
-                                                 mb[static_cast<size_t>(mt) * p.T + u] != 0);
-              if (lane / AT_ONCE == i / AT_ONCE) see[h] = NV == 32 ? bits : (bits >> ((lane % AT_ONCE) * NV)) & ((1u << (NV & 31)) - 1u);
-            }
-          }
+          const size_t at = (static_cast<size_t>(w.b) * p.T + trow) * p.T + k0 + c0;
+          first_n(most);
+          if (most > 0 && dbg_in_range(at, most, n_mask, p.status, 63)) tree_mask_bits<KPW, NB>(p.mask, at, n_mask, most, see);
         } else {
           first_n(draft ? min(valid - c0, trow - (k0 + c0) + 1) : valid - c0);
         }

@@ -191,6 +191,26 @@ def test_tree_whole_or_divided_heads(case, stale):
     test_tree(case, stale)
 
 
+@pytest.mark.parametrize("D,G,T", [(128, 2, 3), (64, 1, 17), (96, 3, 21), (128, 4, 61), (256, 1, 67), (64, 4, 131)])
+def test_tree_mask_at_any_byte(D, G, T):
+    """A mask that begins at any byte of its buffer, whose neighbours are not zero."""
+    gen = torch.Generator().manual_seed(T)
+    B, Hkv, Lk = 2, 2, 40
+    q = rand(gen, (B, G * Hkv, T, D), BF)
+    kn, vn = rand(gen, (B, Hkv, T, D), BF), rand(gen, (B, Hkv, T, D), BF)
+    k, v = cache(gen, B, Hkv, Lk, D, BF), cache(gen, B, Hkv, Lk, D, BF)
+    bits = np.random.default_rng(T).random((B, T, T)) < 0.4
+    host = torch.from_numpy(bits.astype(np.uint8) * np.array([1, 2, 16, 128, 255], np.uint8)[np.arange(T) % 5])
+    for offset in range(4):
+        buf = torch.full((offset + host.numel() + 5,), 255, dtype=torch.uint8, device="cuda")
+        mask = buf[offset:offset + host.numel()].view(B, T, T)
+        mask.copy_(host)
+        args = (q, k, v, kn, vn, i32([Lk, 0]), i32([T, T - 1]), mask, 0.1)
+        got = run_tree(*args)
+        ok()
+        check_tree(*args, got)
+
+
 def test_tree_rows_without_keys_and_lengths_out_of_range():
     gen = torch.Generator().manual_seed(5)
     B, Hq, Hkv, T, Lk, D = 4, 4, 2, 6, 150, 128
