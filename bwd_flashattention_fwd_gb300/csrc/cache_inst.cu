@@ -51,18 +51,22 @@ int tree_impl(const TreeParams& p, EncodeTiledFn enc, cudaStream_t stream) {
                                  Gm::SMEM_BYTES, stream, tq, tk, tv, tkn, tvn, p);
   if (r != kLaunchOk) return r;
   if (p.n_groups == 1 || p.whole) return kLaunchOk;  // no KV head is shared
-  // warps per 4 columns by how many partials a head has on average (131072 keys
-  // D = 256, 38 partials: 86.2 us with 8, 95.1 with one; B1 T8 1000 keys, 17: 10.1 and 14.0)
+  // Warps that share a head's partials out by how many it has on average (131072
+  // keys D = 256, 38 partials: 86.2 us with 8, 95.1 with one; B1 T8 1000 keys, 17:
+  // 10.1 and 14.0), and column quads per thread, which are the loads in flight
+  // (B16 T61 ragged: 70.7 us with 2, 76.4 with one; B6 T26 ragged, 12 partials: 27.3
+  // with 4, 31.6 with one; B2 T27 1219 keys D = 96: 11.6 and 14.0)
   const long long avg = p.n_groups / heads + 1;
   auto combine = [&](auto kern_c, int cols_per_block) {
     const long long tasks = heads * ((R + 31) / 32) * (kD / cols_per_block);
-    const long long most = 8LL * kTreeMaxCtas;  // one wave
+    const long long most = 8LL * kTreeMaxCtas;  // blocks walk the tasks
     return launch_dependent(kern_c, dim3(static_cast<unsigned>(tasks < most ? tasks : most)), 256, 0, stream, p,
                             static_cast<int>(Gm::ROWS));
   };
-  if (avg > 8) return combine(attn_tree_combine_kernel<kD, BF16, 8>, 4);
-  if (avg > 3) return combine(attn_tree_combine_kernel<kD, BF16, 2>, 16);
-  return combine(attn_tree_combine_kernel<kD, BF16, 1>, 32);
+  constexpr int QT = kD == 96 ? 3 : 2;
+  if (avg > 8) return combine(attn_tree_combine_kernel<kD, BF16, 8, 4>, 16);
+  if (avg > 3) return combine(attn_tree_combine_kernel<kD, BF16, 2, 2>, 32);
+  return combine(attn_tree_combine_kernel<kD, BF16, 1, QT>, 32 * QT);
 }
 
 template <bool BF16>

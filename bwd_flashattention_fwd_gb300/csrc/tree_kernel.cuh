@@ -742,18 +742,20 @@ __global__ void __launch_bounds__(TreeGeom<D, QS, NT>::NUM_THREADS, 1)
 
 // Merges the partials of the KV heads that more than one CTA worked on.  With
 // partial lse L_s and O_s: M = max L_s, w_s = 2^(L_s - M), O = sum w_s O_s /
-// sum w_s, lse = M + log2 sum w_s.  Lane = row, 4 columns per thread; NS warps
+// sum w_s, lse = M + log2 sum w_s.  Lane = row, QT times 4 columns per thread; NS warps
 // share a head's partials out and are merged, in order, by the same rule.
-// One wave of blocks, launched as a programmatic dependent: they derive the
+// Launched as a programmatic dependent: the blocks derive the
 // division while the attention kernel runs, then walk the (head, 32 rows,
-// 32 / NS columns) tasks.
-template <int D, bool BF16, int NS>
+// 32 QT / NS columns) tasks.
+template <int D, bool BF16, int NS, int QT>
 __global__ void __launch_bounds__(256) attn_tree_combine_kernel(const TreeParams p, int rows) {
   using E = Elem<BF16>;
-  constexpr int QPB = 8 / NS, QB = D / 4 / QPB;  // column quads per block, blocks per row group
+  // QT column quads per thread, QPB quads at a time per block, QB blocks per row group
+  constexpr int QPB = 8 / NS, QB = D / 4 / (QPB * QT), U = NS == 1 ? 3 : 4;
+  static_assert(QB * QPB * QT * 4 == D, "whole blocks per row");
   __shared__ TreeTable tab;
   __shared__ float sM[8][32], sden[8][32];
-  __shared__ float4 so[8][32];
+  __shared__ float4 so[NS > 1 ? QT : 1][8][32];
   tree_lengths_of_all(p, tab);
   if (threadIdx.x < 32) tree_table(p, tab);
   __syncthreads();
@@ -767,7 +769,7 @@ __global__ void __launch_bounds__(256) attn_tree_combine_kernel(const TreeParams
   if (threadIdx.x == 0) grid_launch_dependents();
   for (long long task = blockIdx.x; task < tasks; task += gridDim.x) {
     const int head = static_cast<int>(task / (rgs * QB)), rest = static_cast<int>(task % (rgs * QB));
-    const int rg = rest / QB, q = (rest - rg * QB) * QPB + warp / NS;
+    const int rg = rest / QB, q = (rest - rg * QB) * QPB * QT + warp / NS;  // and q + QPB, ...
     const int b = head / p.Hkv, hk = head - b * p.Hkv;
     const int n = pre[b + 1] - pre[b];
     const int s = pre[b] * p.Hkv + hk * n;  // the head's units; its stages begin at s + extra
@@ -777,58 +779,76 @@ __global__ void __launch_bounds__(256) attn_tree_combine_kernel(const TreeParams
     const int first = s > g0 * per ? 1 : 0;  // slot of the head's first partial
     auto part_row = [&](int i) { return tree_slot_row(p, g0 + i, i == 0 ? first : 0, rb, rows) + r0; };
     float M = -INFINITY, den = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (row < R) {
-      // four partials at a time, all their loads in flight
-      for (int i = sub; i < ng; i += 4 * NS) {
-        float L[4];
-        float4 x[4];
+    float4 acc[QT];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
+    for (int c = 0; c < QT; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto scale = [](float4& y, float a) { y.x *= a, y.y *= a, y.z *= a, y.w *= a; };
+    auto add = [](float4& y, float a, const float4& x) {
+      y.x = fmaf(a, x.x, y.x), y.y = fmaf(a, x.y, y.y), y.z = fmaf(a, x.z, y.z), y.w = fmaf(a, x.w, y.w);
+    };
+    if (row < R) {
+      // U partials at a time, all their loads in flight
+      for (int i = sub; i < ng; i += U * NS) {
+        float L[U];
+        float4 x[U][QT];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
           L[u] = -INFINITY;
           if (i + u * NS < ng && dbg_in_range(part_row(i + u * NS), 32, static_cast<size_t>(p.n_groups) * 2 * p.n_rb * rows,
                                               p.status, 66)) {
             const size_t r = part_row(i + u * NS);
             L[u] = p.part_lse[r + lane];
-            x[u] = *reinterpret_cast<const float4*>(p.part + r * D + q * 128 + lane * 4);
+#pragma unroll
+            for (int c = 0; c < QT; ++c)
+              x[u][c] = *reinterpret_cast<const float4*>(p.part + r * D + (q + c * QPB) * 128 + lane * 4);
           }
         }
-        const float Mn = fmaxf(M, fmaxf(fmaxf(L[0], L[1]), fmaxf(L[2], L[3])));
+        float Mn = M;
+#pragma unroll
+        for (int u = 0; u < U; ++u) Mn = fmaxf(Mn, L[u]);
         const float a = M == -INFINITY ? 0.f : exp2f(M - Mn);
-        den *= a, acc.x *= a, acc.y *= a, acc.z *= a, acc.w *= a;
+        den *= a;
+#pragma unroll
+        for (int c = 0; c < QT; ++c) scale(acc[c], a);
         M = Mn;
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
+        for (int u = 0; u < U; ++u) {
           if (L[u] == -INFINITY) continue;
           const float wgt = exp2f(L[u] - M);
           den += wgt;
-          acc.x = fmaf(wgt, x[u].x, acc.x), acc.y = fmaf(wgt, x[u].y, acc.y);
-          acc.z = fmaf(wgt, x[u].z, acc.z), acc.w = fmaf(wgt, x[u].w, acc.w);
+#pragma unroll
+          for (int c = 0; c < QT; ++c) add(acc[c], wgt, x[u][c]);
         }
       }
     }
     if constexpr (NS > 1) {
-      sM[warp][lane] = M, sden[warp][lane] = den, so[warp][lane] = acc;
+      sM[warp][lane] = M, sden[warp][lane] = den;
+#pragma unroll
+      for (int c = 0; c < QT; ++c) so[c][warp][lane] = acc[c];
       __syncthreads();
       if (sub == 0) {
         for (int k = 1; k < NS; ++k) M = fmaxf(M, sM[warp + k][lane]);
-        den = 0.f, acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        den = 0.f;
+#pragma unroll
+        for (int c = 0; c < QT; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int k = 0; k < NS; ++k) {
           const float d = sden[warp + k][lane];
           const float wgt = d == 0.f ? 0.f : exp2f(sM[warp + k][lane] - M);
-          const float4 x = so[warp + k][lane];
           den = fmaf(wgt, d, den);
-          acc.x = fmaf(wgt, x.x, acc.x), acc.y = fmaf(wgt, x.y, acc.y);
-          acc.z = fmaf(wgt, x.z, acc.z), acc.w = fmaf(wgt, x.w, acc.w);
+#pragma unroll
+          for (int c = 0; c < QT; ++c) add(acc[c], wgt, so[c][warp + k][lane]);
         }
       }
     }
     const size_t grow = static_cast<size_t>(head) * R + row;
     if (row < R && sub == 0 && dbg_in_range(grow, 1, static_cast<size_t>(p.B) * p.Hkv * R, p.status, 67)) {
       const float inv = den == 0.f ? 0.f : 1.f / den;
-      uint2 o;
-      o.x = E::pack(acc.x * inv, acc.y * inv), o.y = E::pack(acc.z * inv, acc.w * inv);
-      *reinterpret_cast<uint2*>(static_cast<typename E::T*>(p.o) + grow * D + q * 4) = o;
+#pragma unroll
+      for (int c = 0; c < QT; ++c) {
+        uint2 o;
+        o.x = E::pack(acc[c].x * inv, acc[c].y * inv), o.y = E::pack(acc[c].z * inv, acc[c].w * inv);
+        *reinterpret_cast<uint2*>(static_cast<typename E::T*>(p.o) + grow * D + (q + c * QPB) * 4) = o;
+      }
       if (q == 0) p.lse[grow] = den == 0.f ? INFINITY : M + log2f(den);
     }
     if constexpr (NS > 1) __syncthreads();  // before the next task's values
