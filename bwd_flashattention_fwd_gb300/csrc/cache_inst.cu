@@ -57,16 +57,18 @@ int tree_impl(const TreeParams& p, EncodeTiledFn enc, cudaStream_t stream) {
   // (B16 T61 ragged: 70.7 us with 2, 76.4 with one; B6 T26 ragged, 12 partials: 27.3
   // with 4, 31.6 with one; B2 T27 1219 keys D = 96: 11.6 and 14.0)
   const long long avg = p.n_groups / heads + 1;
-  auto combine = [&](auto kern_c, int cols_per_block) {
+  // blocks walk the tasks: those that few warps share in more blocks (B16 T61 with
+  // 3 per SM 74.5 us), those with barriers in fewer (61 x 8 rows 60000 keys with 8 per SM 82.3, 80.8 with 3)
+  auto combine = [&](auto kern_c, int cols_per_block, int blocks_per_sm) {
     const long long tasks = heads * ((R + 31) / 32) * (kD / cols_per_block);
-    const long long most = 8LL * kTreeMaxCtas;  // blocks walk the tasks
+    const long long most = static_cast<long long>(blocks_per_sm) * kTreeMaxCtas;
     return launch_dependent(kern_c, dim3(static_cast<unsigned>(tasks < most ? tasks : most)), 256, 0, stream, p,
                             static_cast<int>(Gm::ROWS));
   };
   constexpr int QT = kD == 96 ? 3 : 2;
-  if (avg > 8) return combine(attn_tree_combine_kernel<kD, BF16, 8, 4>, 16);
-  if (avg > 3) return combine(attn_tree_combine_kernel<kD, BF16, 2, 2>, 32);
-  return combine(attn_tree_combine_kernel<kD, BF16, 1, QT>, 32 * QT);
+  if (avg > 8) return combine(attn_tree_combine_kernel<kD, BF16, 8, 4>, 16, 3);
+  if (avg > 3) return combine(attn_tree_combine_kernel<kD, BF16, 2, 2>, 32, 3);
+  return combine(attn_tree_combine_kernel<kD, BF16, 1, QT>, 32 * QT, 8);
 }
 
 template <bool BF16>
