@@ -12,7 +12,7 @@ constexpr int kTreeMaxT = 1024;   // drafts per sequence (the mask is T x T byte
 constexpr int kTreeMaxB = 1024;   // sequences (each CTA holds the lengths' prefix sums in shared memory)
 // Keys per pipeline stage.  64 keys of K and V at D = 64 arrive in 0.37 us, less
 // than a stage's chain of S, softmax and P V takes, so small heads take 128
-// (B8 T8 16384 keys D = 64: 49.5 us, with 64 keys 66.0, one full tile 70.5).
+// (16384 keys D = 64: B8 T8 50.7 us, with 64 keys 67.1; T30 58.9 and 72.4).
 constexpr int tree_stage_keys(int D, int nt) { return D <= 96 && nt == 1 ? 128 : 64; }
 constexpr int kTreeExtra = 7;      // what a CTA spends on a KV head besides its stages, in stages
 // Small caches: KV heads are not divided, which saves the partials and the
@@ -54,11 +54,12 @@ struct TreePlan {
 };
 
 // R <= 32 / 64: the rows sit in four / two lane quadrants that share the keys
-// out, where that pays: B1 T8 1000 keys D = 128, 32 rows, 9.95 us against 10.15
-// with one full tile; 64 rows at D = 128, 31.9 against 31.3, and D = 256 (8
-// rows, 131072 keys) 86.2 against 85.6, so those take the full tile.
+// out, where that pays: B8 T8 16384 keys D = 64, 32 rows, 50.7 us against 58.1
+// with one full tile; B4 T8 8192 keys D = 128 29.9 and 30.1; 64 rows at D = 128
+// 31.9 against 31.3, and D = 256 (8 rows, 131072 keys) 86.2 against 85.6, so
+// those take the full tile.
 // Above 128 rows: 256 rows per CTA where two accumulators fit tensor memory
-// (D <= 128): B16 T61 ragged 76.9 us, with 128 rows per CTA 87.5.
+// (D <= 128): B16 T61 ragged 70.3 us, with 128 rows per CTA 83.1.
 inline TreePlan tree_plan(long long R, int D, int num_sms) {
   TreePlan t;
   t.qs = R <= 32 && D <= 128 ? 4 : R <= 64 && D <= 96 ? 2 : 1;

@@ -52,8 +52,8 @@ int tree_impl(const TreeParams& p, EncodeTiledFn enc, cudaStream_t stream) {
   if (r != kLaunchOk) return r;
   if (p.n_groups == 1 || p.whole) return kLaunchOk;  // no KV head is shared
   // Warps that share a head's partials out by how many it has on average (131072
-  // keys D = 256, 38 partials: 86.2 us with 8, 95.1 with one; B1 T8 1000 keys, 17:
-  // 10.1 and 14.0), and column quads per thread, which are the loads in flight
+  // keys D = 256, 38 partials: 84.6 us with 8, 92.4 with one; B1 T8 1000 keys, 17:
+  // 9.8 and 16.0), and column quads per thread, which are the loads in flight
   // (B16 T61 ragged: 70.7 us with 2, 76.4 with one; B6 T26 ragged, 12 partials: 27.3
   // with 4, 31.6 with one; B2 T27 1219 keys D = 96: 11.6 and 14.0)
   const long long avg = p.n_groups / heads + 1;

@@ -14,7 +14,7 @@
 // lse is +inf and a row whose limit is 0 (both may hold anything) have limit 0,
 // which makes their tile a masked one.  (In the kernel for few rows, padding alone does not.)
 //
-// Measured (replayed): a prompt of 8192 tokens, 32/8 heads, D = 128 223 us (1230
+// Measured (replayed): a prompt of 8192 tokens, 32/8 heads, D = 128 225 us (1220
 // TFLOP/s; 145 at the matrix rate); B4 T8 8192 keys 15.9 us for 67 MB, B8 T8
 // 16384 keys D = 256 81 us (6.7 TB/s).
 //

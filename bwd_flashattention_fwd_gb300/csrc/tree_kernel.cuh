@@ -27,7 +27,8 @@
 // * More than 128 rows (NT = 2, D <= 128): a CTA takes 256 rows as two tiles
 //   that share every stage, with a softmax warpgroup and an MMA warp each.
 //   (With 128-key stages tensor memory holds one S buffer per tile, not two, and
-//   products and softmax take turns: B16 T61 ragged 98.5 us, this 79.0.)
+//   products and softmax take turns: B16 T61 ragged 98.5 us, against 79.0 before the
+//   mask and the combine kernel got faster.)
 //   More than one block of rows: n_rb neighbouring CTAs walk the same keys
 //   with different rows, so the keys come from memory once and then from L2.
 //
@@ -42,9 +43,9 @@
 // warps clear them in shared memory before O += P V reads the stage.
 //
 // Measured (call and combine kernel, replayed): B4 32/8 heads T8 8192 keys
-// D = 128 30.3 us for 134 MB (27 stages a CTA stream in 18.6 us, at the full copy
+// D = 128 29.9 us for 134 MB (27 stages a CTA stream in 18.6 us, at the full copy
 // rate; the rest is start, quadrant merge and combine); 131072 keys D = 256 85 us,
-// 6.3 TB/s; B16 T61 ragged 77 us, 0.65 us a stage of 256 rows.
+// 6.3 TB/s; B16 T61 ragged 70.3 us for 321 MB, which stream in 45 us, at the full rate too.
 #pragma once
 
 #include "cache.h"
