@@ -347,16 +347,21 @@ __global__ void __launch_bounds__(kEvictThreads, 1) attn_cache_evict_kernel(cons
     prefix |= static_cast<uint32_t>(s_digit) << shift;
     need = s_need;
     // every slot that matches so far is kept: the lower digits do not matter
-    // (the usual end, as two digits leave one slot: 11.7 us, with all three 12.7)
+    // (the usual end, as two digits leave one slot: 11.8 us, with all three 12.7)
     if (d == 2 || need == s_equal) break;
     // the next digit of the slots that match so far (few)
     const uint32_t above = ~0u << shift;
     const int next = d == 0 ? 10 : 0;
     const uint32_t mask = d == 0 ? 2047u : 1023u;
-    for (int i = w0; i < w1; i += 32) {
-      const uint32_t key = i + lane < w1 ? keys[i + lane] : ~prefix;
-      const bool on = (key & above) == prefix;
-      if (__any_sync(0xffffffffu, on)) evict_count(hist[0], on ? static_cast<int>((key >> next) & mask) : -1);
+    for (int i0 = w0; i0 < w1; i0 += 128) {
+      uint32_t key[4];  // four strips' loads before the first count
+#pragma unroll
+      for (int u = 0; u < 4; ++u) key[u] = i0 + 32 * u + lane < w1 ? keys[i0 + 32 * u + lane] : ~prefix;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const bool on = (key[u] & above) == prefix;
+        if (__any_sync(0xffffffffu, on)) evict_count(hist[0], on ? static_cast<int>((key[u] >> next) & mask) : -1);
+      }
     }
     __syncthreads();
   }
@@ -428,7 +433,7 @@ __device__ __forceinline__ int ld_cluster(uint32_t addr) {
 }
 
 // The same for longer rows, one cluster of 8 CTAs per KV head (8 heads of
-// 32768 slots: 21 us; 5 more with the moves in this kernel); each CTA owns
+// 32768 slots: 20 us; 5 more with the moves in this kernel); each CTA owns
 // a consecutive part of the slots and keeps their keys in shared memory
 // (CACHED; parts that do not fit are read again in each pass).  Four digits of
 // 8 bits: what a digit costs is reading every CTA's histogram through
@@ -471,7 +476,7 @@ __global__ void __launch_bounds__(kEvictClusterThreads) attn_cache_evict_cluster
   auto key_at = [&](int j) { return CACHED ? keys[j - j0] : evict_key(w[j], pos[j], recent_from); };
   for (int i = tid; i < 4 * BINS; i += kEvictClusterThreads) (&hist[0][0])[i] = (&first[0][0])[i] = 0;
   __syncthreads();
-  evict_load<4>(p, bh, w0, w1, j0, CACHED ? keys : nullptr, recent_from, first[lane & 3], 24);
+  evict_load<8>(p, bh, w0, w1, j0, CACHED ? keys : nullptr, recent_from, first[lane & 3], 24);
   __syncthreads();
   if (tid < BINS) hist[0][tid] = first[0][tid] + first[1][tid] + first[2][tid] + first[3][tid];
   uint32_t prefix = 0;
@@ -528,10 +533,16 @@ __global__ void __launch_bounds__(kEvictClusterThreads) attn_cache_evict_cluster
     need = s_need;
     if (d == 3 || need == s_equal) break;  // (as above; the same in every CTA)
     const uint32_t above = ~0u << shift;
-    for (int i = w0; i < w1; i += 32) {
-      const uint32_t key = i + lane < w1 ? key_at(i + lane) : ~prefix;
-      const bool on = (key & above) == prefix;
-      if (__any_sync(0xffffffffu, on)) evict_count(hist[d + 1], on ? static_cast<int>((key >> (shift - 8)) & 255u) : -1);
+    for (int i0 = w0; i0 < w1; i0 += 128) {
+      uint32_t key[4];  // four strips' loads before the first count
+#pragma unroll
+      for (int u = 0; u < 4; ++u) key[u] = i0 + 32 * u + lane < w1 ? key_at(i0 + 32 * u + lane) : ~prefix;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const bool on = (key[u] & above) == prefix;
+        if (__any_sync(0xffffffffu, on))
+          evict_count(hist[d + 1], on ? static_cast<int>((key[u] >> (shift - 8)) & 255u) : -1);
+      }
     }
   }
   const EvictKept kept{prefix, need, need < s_equal};
