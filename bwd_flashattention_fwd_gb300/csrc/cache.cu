@@ -235,9 +235,9 @@ extern "C" attn_status_t attn_cache_evict(void* k, void* v, const float* weight,
   const int heads = B * Hkv;
   if (Lk <= kEvictRowKeys) {
     // about one CTA per SM, so that the moves run at the memory's rate (4 x 8
-    // heads 8448 -> 8192: 11.7 us, by clusters 18.2; 16384 slots: 39.4 and 41.8;
-    // 2 heads of 16384: 15.1 and 15.9; past that one CTA's search takes too long:
-    // 8 heads of 32768 55 us, by clusters 20)
+    // heads 8448 -> 8192: 11.8 us, by clusters 15.8; 16384 -> 8192: 37.7 and 39.9,
+    // -> 16128: 15.6 and 16.9; 2 heads of 16384: 14.6 and 13.4; past that one CTA's
+    // search takes too long: 8 heads of 32768 55 us, by clusters 20)
     const int copies = heads < num_sms ? num_sms / heads : 1;
     static std::atomic<uint64_t> done{0};
     if (!set_smem_limit(attn_cache_evict_kernel, evict_smem(kEvictRowKeys, 1), done)) return ATTN_ERR_CUDA;
