@@ -281,12 +281,15 @@ def attn_bwd_masked(q, k, v, o, dO, lse, delta, block_mask, dq, dk, dv, scale: f
 def kv_row_pitch(k, v) -> int:
     """Row pitch of k and v for attn_fwd_ex / attn_bwd_ex: 0 when both are
     contiguous, else the capacity P of a [B, Hkv, P, D] buffer they are the
-    first Lk rows of (cache[:, :, :Lk, :]).  Any other layout is rejected."""
+    first Lk rows of (cache[:, :, :Lk, :]).  Any other layout is rejected,
+    expanded heads (stride 0) and heads that overlap among them: the calls
+    count on P >= Lk rows of storage per head, and 0 means "contiguous" to them."""
     if k.is_contiguous() and v.is_contiguous():
         return 0
     B, Hkv, Lk, D = k.shape
     st = k.stride()
-    if st[3] != 1 or st[2] != D or st[1] % D or st[0] != Hkv * st[1] or tuple(v.stride()) != tuple(st):
+    if (st[3] != 1 or st[2] != D or st[1] % D or st[1] < Lk * D or st[0] != Hkv * st[1]
+            or tuple(v.stride()) != tuple(st)):
         raise ValueError(f"k/v strides {tuple(k.stride())}, {tuple(v.stride())} are not a slice of a "
                          f"[B, Hkv, capacity, D] cache")
     return st[1] // D

@@ -1,0 +1,29 @@
+"""Layouts and arguments that the cache calls' host side has to refuse before
+a pointer crosses the C ABI (no GPU)."""
+
+import pytest
+import torch
+
+from bwd_flashattention_fwd_gb300 import gbattn
+
+
+def test_row_pitch_refuses_caches_without_a_row_per_head():
+    """An expanded cache has one head's storage behind the shape of many: its
+    strides say pitch 0, which the C ABI reads as "contiguous"."""
+    k = torch.zeros(1, 1, 30, 64, dtype=torch.bfloat16)
+    for shape in ((2, 3, 30, 64), (1, 3, 30, 64), (2, 1, 30, 64)):
+        e = k.expand(shape)
+        with pytest.raises(ValueError, match="not a slice"):
+            gbattn.kv_row_pitch(e, e)
+    # heads that overlap: fewer rows between them than each has
+    for rows in (1, 29):
+        o = torch.zeros(400 * 64, dtype=torch.bfloat16).as_strided((2, 3, 30, 64), (3 * rows * 64, rows * 64, 64, 1))
+        with pytest.raises(ValueError, match="not a slice"):
+            gbattn.kv_row_pitch(o, o)
+    # one head alone, and heads that follow one another, are contiguous
+    assert gbattn.kv_row_pitch(k, k) == 0
+    assert gbattn.kv_row_pitch(k.expand(1, 1, 30, 64), k) == 0
+    # a single row per head, and slices of one sequence or head
+    c = torch.zeros(2, 3, 40, 64, dtype=torch.bfloat16)
+    assert gbattn.kv_row_pitch(c[:, :, :1], c[:, :, :1]) == 40
+    assert gbattn.kv_row_pitch(c[1:, :, 5:30], c[1:, :, :25]) == 40
