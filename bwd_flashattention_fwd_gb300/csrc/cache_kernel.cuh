@@ -288,7 +288,8 @@ __host__ __device__ inline size_t evict_smem(int Lk, int copies) {
 __global__ void __launch_bounds__(kEvictThreads, 1) attn_cache_evict_kernel(const EvictParams p, int copies) {
   constexpr int BINS = 2048, NH = 4;
   extern __shared__ uint32_t keys[];
-  __shared__ int hist[NH][BINS];
+  __shared__ __align__(16) int hist[NH][BINS];
+  static_assert(__alignof__(hist) >= alignof(int2), "hist is read and cleared in pairs");
   __shared__ uint32_t bits[kEvictRowKeys / 32];  // kept slots
   __shared__ int warp_sum[32];
   __shared__ int2 warp_pair[32];

@@ -1,6 +1,9 @@
 """Layouts and arguments that the cache calls' host side has to refuse before
 a pointer crosses the C ABI (no GPU)."""
 
+import os
+import re
+
 import pytest
 import torch
 
@@ -27,3 +30,13 @@ def test_row_pitch_refuses_caches_without_a_row_per_head():
     c = torch.zeros(2, 3, 40, 64, dtype=torch.bfloat16)
     assert gbattn.kv_row_pitch(c[:, :, :1], c[:, :, :1]) == 40
     assert gbattn.kv_row_pitch(c[1:, :, 5:30], c[1:, :, :25]) == 40
+
+
+def test_histograms_read_in_vectors_are_aligned_for_them():
+    """Shared arrays that the eviction kernels read through int2* or as 16-byte
+    pieces declare that alignment; the layout next to other arrays is the
+    compiler's choice.  (The build has the same as a static_assert.)"""
+    path = os.path.join(os.path.dirname(gbattn.__file__), "csrc", "cache_kernel.cuh")
+    arrays = re.findall(r"__shared__ (.*?)int4? (hist|quad_sum)\[", open(path).read())
+    assert sorted(n for _, n in arrays) == ["hist", "hist", "quad_sum"]
+    assert all("__align__(16)" in how for how, _ in arrays), arrays
