@@ -411,6 +411,16 @@ def _shapes(call: str, *named) -> None:
             raise ValueError(f"{call}: {name} has shape {tuple(t.shape)}; expected {tuple(want)}")
 
 
+def _cache_pitch(call: str, k, v, p: int) -> int:
+    """A serving call's explicit kv_pitch p, where it is the layout that the
+    strides of k and v say.  A larger one would reach past the tensors; one
+    below Lk is the C ABI's to refuse."""
+    own, Lk = kv_row_pitch(k, v), k.shape[2]
+    if k.shape[0] * k.shape[1] > 1 and (p or Lk) != (own or Lk) and not (own == 0 and p < Lk):
+        raise ValueError(f"{call}: kv_pitch {p} is not the layout of k and v ({own or Lk} rows between heads)")
+    return p
+
+
 def attn_tree_workspace_bytes(B: int, Hq: int, Hkv: int, T: int, Lk: int, D: int) -> int:
     """Bytes of device workspace attn_fwd_tree needs (0: shape not served)."""
     return int(load_library().attn_tree_workspace_bytes(B, Hq, Hkv, T, Lk, D))
@@ -454,7 +464,7 @@ def attn_fwd_tree(q, k, v, k_new, v_new, cache_len, o, lse, workspace, scale: fl
         _shapes("attn_fwd_tree", (k, (B, Hkv, Lk, D), "k"), (v, (B, Hkv, Lk, D), "v"), (k_new, new, "k_new"),
                 (v_new, new, "v_new"), (o, q.shape, "o"), (lse, (B, Hq, T), "lse"), (cache_len, lens, "cache_len"),
                 (tree_len, lens, "tree_len"), (tree_mask, (B, T, T), "tree_mask"))
-    pitch = kv_row_pitch(k, v) if kv_pitch is None else int(kv_pitch)
+    pitch = kv_row_pitch(k, v) if kv_pitch is None else _cache_pitch("attn_fwd_tree", k, v, int(kv_pitch))
     st = load_library().attn_fwd_tree(q.data_ptr(), k.data_ptr(), v.data_ptr(), k_new.data_ptr(), v_new.data_ptr(),
                                       _ptr(tree_mask), cache_len.data_ptr(), _ptr(tree_len), o.data_ptr(),
                                       lse.data_ptr(), workspace.data_ptr(), workspace.numel(), pitch, B, Hq, Hkv, T,
@@ -491,7 +501,7 @@ def attn_cache_append(k_new, v_new, k, v, cache_len, accept_len, cache_len_out, 
                 (v_new, k_new.shape, "v_new"), (cache_len, lens, "cache_len"), (accept_len, lens, "accept_len"),
                 (cache_len_out, lens, "cache_len_out"), (path, (B, T), "path"), (pos, (B, Hkv, Lk), "pos"),
                 (seen, lens, "seen"), (seen_out, lens, "seen_out"), (limit, (B, T), "limit"))
-    pitch = kv_row_pitch(k, v) if kv_pitch is None else int(kv_pitch)
+    pitch = kv_row_pitch(k, v) if kv_pitch is None else _cache_pitch("attn_cache_append", k, v, int(kv_pitch))
     st = load_library().attn_cache_append(k_new.data_ptr(), v_new.data_ptr(), _ptr(path), _ptr(accept_len),
                                           cache_len.data_ptr(), _ptr(seen), k.data_ptr(), v.data_ptr(), _ptr(pos),
                                           cache_len_out.data_ptr(), _ptr(seen_out), _ptr(limit), pitch, B, Hkv, T, Lk,
@@ -531,7 +541,7 @@ def attn_key_weight(q, k, lse, weight, weight_out, workspace, scale: float, caus
                  i32=(limit,))
         _shapes("attn_key_weight", (k, (B, Hkv, Lk, D), "k"), (lse, (B, Hq, Lq), "lse"), (weight, slots, "weight"),
                 (weight_out, slots, "weight_out"), (limit, (B, Lq), "limit"))
-    pitch = kv_row_pitch(k, k) if kv_pitch is None else int(kv_pitch)
+    pitch = kv_row_pitch(k, k) if kv_pitch is None else _cache_pitch("attn_key_weight", k, k, int(kv_pitch))
     st = load_library().attn_key_weight(q.data_ptr(), k.data_ptr(), lse.data_ptr(), _ptr(limit), _ptr(weight),
                                         weight_out.data_ptr(), workspace.data_ptr(), workspace.numel(), pitch, B, Hq,
                                         Hkv, Lq, Lk, D, float(scale), int(bool(causal)),
@@ -573,7 +583,7 @@ def attn_cache_evict(k, v, weight, pos, cache_len, seen, weight_out, pos_out, ca
         _shapes("attn_cache_evict", (v, k.shape, "v"), (weight, slots, "weight"), (pos, slots, "pos"),
                 (weight_out, slots, "weight_out"), (pos_out, slots, "pos_out"), (cache_len, lens, "cache_len"),
                 (seen, lens, "seen"), (cache_len_out, lens, "cache_len_out"))
-    pitch = kv_row_pitch(k, v) if kv_pitch is None else int(kv_pitch)
+    pitch = kv_row_pitch(k, v) if kv_pitch is None else _cache_pitch("attn_cache_evict", k, v, int(kv_pitch))
     st = load_library().attn_cache_evict(k.data_ptr(), v.data_ptr(), weight.data_ptr(), pos.data_ptr(),
                                          cache_len.data_ptr(), seen.data_ptr(), weight_out.data_ptr(),
                                          pos_out.data_ptr(), cache_len_out.data_ptr(), workspace.data_ptr(),

@@ -40,3 +40,25 @@ def test_histograms_read_in_vectors_are_aligned_for_them():
     arrays = re.findall(r"__shared__ (.*?)int4? (hist|quad_sum)\[", open(path).read())
     assert sorted(n for _, n in arrays) == ["hist", "hist", "quad_sum"]
     assert all("__align__(16)" in how for how, _ in arrays), arrays
+
+
+def test_explicit_pitch_stays_inside_the_tensors():
+    """kv_pitch of the cache calls: what the strides say, or for heads that
+    follow one another Lk or 0; a larger one would reach past the tensors.  A
+    smaller one is left to the C ABI, which refuses it."""
+    pitch = gbattn._cache_pitch
+    k = torch.zeros(2, 3, 40, 64, dtype=torch.bfloat16)
+    s = k[:, :, :25]
+    assert pitch("call", k, k, 40) == 40 and pitch("call", k, k, 0) == 0 and pitch("call", s, s, 40) == 40
+    for t, bad in ((k, 41), (k, 1 << 30), (s, 41), (s, 0), (s, 25), (s, 30)):
+        with pytest.raises(ValueError, match="kv_pitch"):
+            pitch("call", t, t, bad)
+    for below in (39, 1, -1):
+        assert pitch("call", k, k, below) == below
+    one = k[:1, :1]  # nothing lies a pitch away from a single head
+    assert pitch("call", one, one, 1000) == 1000
+    with pytest.raises(ValueError):  # other layouts, whatever the pitch
+        pitch("call", k.transpose(1, 2), k.transpose(1, 2), 40)
+    e = k[:1, :1].expand(2, 3, 40, 64)
+    with pytest.raises(ValueError):
+        pitch("call", e, e, 40)
