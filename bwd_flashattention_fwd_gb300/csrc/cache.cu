@@ -67,6 +67,27 @@ attn_status_t check_key_weight(int B, int Hq, int Hkv, int Lq, int Lk, int D) {
   return ATTN_OK;
 }
 
+// An array of a call, for the checks that no output shares storage with an
+// input (blocks read the one while others write the other) or another output.
+struct Span {
+  const void* at;
+  long long bytes;
+};
+
+bool overlap(const Span& a, const Span& b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.at), y = reinterpret_cast<uintptr_t>(b.at);
+  return a.at && b.at && (x < y ? y - x < static_cast<uintptr_t>(a.bytes) : x - y < static_cast<uintptr_t>(b.bytes));
+}
+
+// Whether one of the first n_out spans overlaps any other of the n.
+template <int N>
+bool outputs_overlap(const Span (&s)[N], int n_out) {
+  for (int i = 0; i < n_out; ++i)
+    for (int j = i + 1; j < N; ++j)
+      if (overlap(s[i], s[j])) return true;
+  return false;
+}
+
 attn_status_t finish(int r) {
   return r == kLaunchOk ? ATTN_OK : r == kLaunchBadMap ? ATTN_ERR_INVALID_ARG : ATTN_ERR_CUDA;
 }
@@ -91,7 +112,7 @@ extern "C" attn_status_t attn_fwd_tree(const void* q, const void* k, const void*
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(k_new) || !aligned16(v_new) || !aligned16(o) ||
       !aligned16(lse) || !aligned16(workspace) || !aligned4(cache_len) || !aligned4(tree_len))
     return ATTN_ERR_INVALID_ARG;
-  if (o == q) return ATTN_ERR_INVALID_ARG;  // several CTAs read a row of q
+  if (o == q) return ATTN_ERR_INVALID_ARG;
   attn_status_t s = check_scale(scale);
   if (s != ATTN_OK) return s;
   s = check_tree(B, Hq, Hkv, T, Lk, D);
@@ -100,6 +121,12 @@ extern "C" attn_status_t attn_fwd_tree(const void* q, const void* k, const void*
   if (c != ATTN_OK) return c;
   if (s != ATTN_OK) return s;
   if (workspace_bytes < attn_tree_workspace_bytes(B, Hq, Hkv, T, Lk, D)) return ATTN_ERR_INVALID_ARG;
+  // several CTAs read a row of q, of the drafts, of the mask
+  const long long rows = static_cast<long long>(B) * Hq * T, drafts = static_cast<long long>(B) * Hkv * T, ints = 4LL * B;
+  const Span spans[] = {{o, rows * D * 2}, {lse, rows * 4}, {q, rows * D * 2}, {k_new, drafts * D * 2},
+                        {v_new, drafts * D * 2}, {tree_mask, static_cast<long long>(B) * T * T}, {cache_len, ints},
+                        {tree_len, ints}};
+  if (outputs_overlap(spans, 2)) return ATTN_ERR_INVALID_ARG;
   int dev, num_sms, *status;
   EncodeTiledFn enc;
   const attn_status_t ds = shared_device_state(&dev, &enc, &status, &num_sms);
@@ -148,6 +175,11 @@ extern "C" attn_status_t attn_key_weight(const void* q, const void* k, const flo
   if (s != ATTN_OK) return s;
   if (limit && (Lq > kTreeMaxT || B > kTreeMaxB)) return ATTN_ERR_UNSUPPORTED;
   if (workspace_bytes < attn_key_weight_workspace_bytes(B, Hq, Hkv, Lq, Lk, D)) return ATTN_ERR_INVALID_ARG;
+  const long long rows = static_cast<long long>(B) * Hq * Lq, slots = 4LL * B * Hkv * Lk;
+  const Span out = {weight_out, slots}, spans[] = {out, {q, rows * D * 2}, {lse, rows * 4}, {limit, 4LL * B * Lq}};
+  if (outputs_overlap(spans, 1)) return ATTN_ERR_INVALID_ARG;
+  // in place a thread reads an element before it writes it; a shifted array would be read after
+  if (weight != weight_out && overlap(out, {weight, slots})) return ATTN_ERR_INVALID_ARG;
   int dev, num_sms, *status;
   EncodeTiledFn enc;
   const attn_status_t ds = shared_device_state(&dev, &enc, &status, &num_sms);
@@ -183,12 +215,15 @@ extern "C" attn_status_t attn_cache_append(const void* k_new, const void* v_new,
       !aligned4(seen_out) || !aligned4(limit))
     return ATTN_ERR_INVALID_ARG;
   if ((pos || seen_out) && !seen) return ATTN_ERR_INVALID_ARG;
-  // other blocks read the lengths while one writes the new ones
   if (cache_len_out == cache_len || (seen_out && seen_out == seen)) return ATTN_ERR_INVALID_ARG;
   if (T < 1) return ATTN_ERR_INVALID_ARG;
   const attn_status_t s = check_cache(B, Hkv, Lk, D, kv_pitch, dtype);
   if (s != ATTN_OK) return s;
   if (path && T > kTreeMaxT) return ATTN_ERR_UNSUPPORTED;
+  const long long ints = 4LL * B;
+  const Span spans[] = {{cache_len_out, ints}, {seen_out, ints}, {limit, ints * T}, {pos, ints * Hkv * Lk}, {cache_len, ints},
+                        {seen, ints}, {accept_len, ints}, {path, ints * T}};
+  if (outputs_overlap(spans, 4)) return ATTN_ERR_INVALID_ARG;
   int dev, num_sms, *status;
   EncodeTiledFn enc;
   const attn_status_t ds = shared_device_state(&dev, &enc, &status, &num_sms);
@@ -224,6 +259,11 @@ extern "C" attn_status_t attn_cache_evict(void* k, void* v, const float* weight,
   if (s != ATTN_OK) return s;
   if (Lk > kEvictMaxLk) return ATTN_ERR_UNSUPPORTED;
   if (workspace_bytes < attn_cache_evict_workspace_bytes(B, Hkv, Lk)) return ATTN_ERR_INVALID_ARG;
+  // CTAs that share a KV head read the same weights, positions and lengths and have to choose the same slots
+  const long long ints = 4LL * B, slots = ints * Hkv * Lk;
+  const Span spans[] = {{weight_out, slots}, {pos_out, slots}, {cache_len_out, ints}, {weight, slots}, {pos, slots},
+                        {cache_len, ints}, {seen, ints}};
+  if (outputs_overlap(spans, 3)) return ATTN_ERR_INVALID_ARG;
   int dev, num_sms, *status;
   EncodeTiledFn enc;
   const attn_status_t ds = shared_device_state(&dev, &enc, &status, &num_sms);

@@ -236,9 +236,9 @@ attn_status_t attn_bwd_decode(const void* q, const void* k, const void* v, const
  *   workspace: as for the decode calls (one per call in flight), at least
  *     attn_tree_workspace_bytes(...) bytes; 0 there means the shape is rejected.
  *   Limits: T <= 1024, B <= 1024, G * T <= 65535 and Lk <= 2^30 (else
- *     ATTN_ERR_UNSUPPORTED).  o is not q (ATTN_ERR_INVALID_ARG), and no output
- *     overlaps an input.  int32 arrays are 4-byte aligned.  Other errors as
- *     for attn_fwd_ex.
+ *     ATTN_ERR_UNSUPPORTED).  No output overlaps an input or the other output
+ *     (ATTN_ERR_INVALID_ARG; the cache and the workspace are not checked).
+ *     int32 arrays are 4-byte aligned.  Other errors as for attn_fwd_ex.
  */
 size_t attn_tree_workspace_bytes(int B, int Hq, int Hkv, int T, int Lk, int D);
 attn_status_t attn_fwd_tree(const void* q, const void* k, const void* v, const void* k_new, const void* v_new,
@@ -256,18 +256,19 @@ attn_status_t attn_fwd_tree(const void* q, const void* k, const void* v, const v
  *   accept_len [B] or NULL (T for all); path [B,T] or NULL (0, 1, 2, ...: the
  *     first n drafts, a prompt for instance).  n is cut at 0, at T, at the
  *     cache's end, and at the first path entry outside 0..T-1.
- *   cache_len_out [B]: cache_len[b] + n.  Not the same array as cache_len.
+ *   cache_len_out [B]: cache_len[b] + n.
  *   seen [B] or NULL: tokens sequence b has had so far, evicted ones included,
- *     i.e. the next token's position.  seen_out [B] (with seen, not the same
- *     array) gets seen[b] + n, and pos [B,Hkv,Lk] (with seen) gets the
- *     position seen[b] + i of each new cache row.  Each may be NULL.
+ *     i.e. the next token's position.  seen_out [B] (with seen) gets
+ *     seen[b] + n, and pos [B,Hkv,Lk] (with seen) gets the position seen[b] + i
+ *     of each new cache row.  Each may be NULL.
  *   limit [B,T] or NULL: output for attn_key_weight: the number of cache rows
  *     that draft t sees once the accepted ones are appended,
  *     cache_len[b] + i + 1 for t = path[i] (the last such i), 0 for a draft
  *     that was not accepted.
  * All arrays but the 16-bit ones are int32; every pointer is a device pointer.
- * Any T >= 1, with a path T <= 1024 (else ATTN_ERR_UNSUPPORTED).  The inputs
- * may not overlap the outputs.
+ * Any T >= 1, with a path T <= 1024 (else ATTN_ERR_UNSUPPORTED).  None of the
+ * int32 outputs overlaps an int32 input or another of them
+ * (ATTN_ERR_INVALID_ARG), and k_new and v_new no row that the call writes.
  */
 attn_status_t attn_cache_append(const void* k_new, const void* v_new, const int32_t* path, const int32_t* accept_len,
                                 const int32_t* cache_len, const int32_t* seen, void* k, void* v, int32_t* pos,
@@ -288,7 +289,8 @@ attn_status_t attn_cache_append(const void* k_new, const void* v_new, const int3
  *     that range; 0: the row adds nothing).  limit needs Lq and B <= 1024.
  *   A row whose lse is +inf adds nothing.
  *   weight float32 [B,Hkv,Lk] contiguous, or NULL (zeros); weight_out
- *     [B,Hkv,Lk] may be the same array.  Sums are in a fixed order: the same
+ *     [B,Hkv,Lk] may be the same array, else it overlaps no input
+ *     (ATTN_ERR_INVALID_ARG).  Sums are in a fixed order: the same
  *     call gives the same bits.
  *   workspace: attn_key_weight_workspace_bytes(...) bytes, one per call in flight.
  */
@@ -314,7 +316,7 @@ attn_status_t attn_key_weight(const void* q, const void* k, const float* lse, co
  *   weight float32 and pos int32 [B,Hkv,Lk], cache_len and seen int32 [B]: inputs.
  *   weight_out, pos_out [B,Hkv,Lk]: the kept slots' values; 0 and -1 in every
  *     slot from the new length on.  cache_len_out [B]: min(cache_len[b], keep).
- *     None of them is the same array as its input.
+ *     None of them overlaps an input or another of them (ATTN_ERR_INVALID_ARG).
  *   1 <= keep <= Lk, 0 <= recent <= keep (else ATTN_ERR_INVALID_ARG);
  *   Lk <= 2^20 (else ATTN_ERR_UNSUPPORTED).
  *   workspace: attn_cache_evict_workspace_bytes(...) bytes, one per call in flight.

@@ -1,13 +1,14 @@
 """Layouts and arguments that the cache calls' host side has to refuse before
 a pointer crosses the C ABI (no GPU)."""
 
+import ctypes
 import os
 import re
 
 import pytest
 import torch
 
-from bwd_flashattention_fwd_gb300 import gbattn
+from bwd_flashattention_fwd_gb300 import build, gbattn
 
 
 def test_row_pitch_refuses_caches_without_a_row_per_head():
@@ -62,3 +63,87 @@ def test_explicit_pitch_stays_inside_the_tensors():
     e = k[:1, :1].expand(2, 3, 40, 64)
     with pytest.raises(ValueError):
         pitch("call", e, e, 40)
+
+
+# Addresses 16 MB apart that are never dereferenced: every call below is refused on the host.
+A = [0x1000000 * (i + 1) for i in range(16)]
+
+
+@pytest.fixture(scope="module")
+def lib():
+    build.build()
+    return gbattn.load_library()
+
+
+def append(lib, B=2, Hkv=2, T=8, Lk=100, D=128, **over):
+    a = dict(zip(("k_new", "v_new", "path", "accept_len", "cache_len", "seen", "k", "v", "pos", "cache_len_out",
+                  "seen_out", "limit"), A))
+    a.update(over)
+    return lib.attn_cache_append(*a.values(), 0, B, Hkv, T, Lk, D, 1, None)
+
+
+def evict(lib, B=2, Hkv=2, Lk=100, D=128, **over):
+    a = dict(zip(("k", "v", "weight", "pos", "cache_len", "seen", "weight_out", "pos_out", "cache_len_out", "ws"), A))
+    a.update(over)
+    return lib.attn_cache_evict(*a.values(), 1 << 40, 0, B, Hkv, Lk, D, 50, 10, 1, None)
+
+
+def tree(lib, B=2, Hq=8, Hkv=2, T=8, Lk=100, D=128, **over):
+    a = dict(zip(("q", "k", "v", "k_new", "v_new", "tree_mask", "cache_len", "tree_len", "o", "lse", "ws"), A))
+    a.update(over)
+    return lib.attn_fwd_tree(*a.values(), 1 << 40, 0, B, Hq, Hkv, T, Lk, D, ctypes.c_float(0.1), 1, None)
+
+
+def weight(lib, B=2, Hq=8, Hkv=2, Lq=8, Lk=100, D=128, **over):
+    a = dict(zip(("q", "k", "lse", "limit", "weight", "weight_out", "ws"), A))
+    a.update(over)
+    return lib.attn_key_weight(*a.values(), 1 << 40, 0, B, Hq, Hkv, Lq, Lk, D, ctypes.c_float(0.1), 0, 1, None)
+
+
+def refused(call, outputs, others, sizes):
+    """Every output over each other array, at its start, over its last element and from below."""
+    names = {n: A[i] for i, n in enumerate(call.names)}
+    for o in outputs:
+        for x in others:
+            if x == o:
+                continue
+            for at in (names[x], names[x] + sizes[x] - 16, names[x] - sizes[o] + 16):
+                assert call(**{o: at}) == gbattn.ATTN_ERR_INVALID_ARG, (o, x, at - names[x])
+
+
+def named(fn, lib, names):
+    def call(**over):
+        return fn(lib, **over)
+
+    call.names = names
+    return call
+
+
+def test_outputs_over_inputs_or_one_another_are_refused(lib):
+    """Blocks read lengths, paths and weights while others write their outputs,
+    so no output may share storage with any of them."""
+    B, Hq, Hkv, T, Lk, D = 8, 8, 2, 8, 100, 128
+    n = dict(B=B, Hkv=Hkv, Lk=Lk, D=D)
+    ints = 4 * B
+    call = named(lambda lib, **k: append(lib, T=T, **n, **k), lib,
+                 ("k_new", "v_new", "path", "accept_len", "cache_len", "seen", "k", "v", "pos", "cache_len_out",
+                  "seen_out", "limit"))
+    sizes = dict(path=ints * T, accept_len=ints, cache_len=ints, seen=ints, pos=4 * B * Hkv * Lk, cache_len_out=ints,
+                 seen_out=ints, limit=ints * T)
+    refused(call, ("pos", "cache_len_out", "seen_out", "limit"), sizes, sizes)
+    call = named(lambda lib, **k: evict(lib, **n, **k), lib,
+                 ("k", "v", "weight", "pos", "cache_len", "seen", "weight_out", "pos_out", "cache_len_out"))
+    slots = 4 * B * Hkv * Lk
+    sizes = dict(weight=slots, pos=slots, cache_len=ints, seen=ints, weight_out=slots, pos_out=slots, cache_len_out=ints)
+    refused(call, ("weight_out", "pos_out", "cache_len_out"), sizes, sizes)
+    call = named(lambda lib, **k: tree(lib, Hq=Hq, T=T, **n, **k), lib,
+                 ("q", "k", "v", "k_new", "v_new", "tree_mask", "cache_len", "tree_len", "o", "lse"))
+    sizes = dict(q=B * Hq * T * D * 2, k_new=B * Hkv * T * D * 2, v_new=B * Hkv * T * D * 2, tree_mask=B * T * T,
+                 cache_len=ints, tree_len=ints, o=B * Hq * T * D * 2, lse=B * Hq * T * 4)
+    refused(call, ("o", "lse"), sizes, sizes)
+    call = named(lambda lib, **k: weight(lib, Hq=Hq, Lq=T, **n, **k), lib,
+                 ("q", "k", "lse", "limit", "weight", "weight_out"))
+    sizes = dict(q=B * Hq * T * D * 2, lse=B * Hq * T * 4, limit=ints * T, weight=slots, weight_out=slots)
+    refused(call, ("weight_out",), ("q", "lse", "limit"), sizes)
+    for shift in (16, -16, slots - 16, 16 - slots):  # the same array is fine, a shifted one is not
+        assert call(weight_out=A[4] + shift) == gbattn.ATTN_ERR_INVALID_ARG, shift
