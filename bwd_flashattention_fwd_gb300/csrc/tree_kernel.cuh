@@ -38,6 +38,15 @@
 // raises its maximum by more than 8 (log2 units), so O is rescaled rarely;
 // O / l and m + log2 l use the same reference.
 //
+// P is rounded to 16 bits because that is what the tensor cores multiply V by;
+// l sums it unrounded.  The rounding is half a step of each p (2^-8 of it in
+// bf16, 2^-11 in fp16): against 64 bits O is 1.2 to 1.4 times as far off as with
+// P in 32 bits, whose only 16-bit rounding is O's own.  Two 16-bit parts of P
+// would take it away for twice the products.  fp16 ends at 2^-25, where bf16
+// goes on to 2^-133, and many light keys together weigh something: there P
+// and l are kept times 2^7 (p <= 2^8 by the rule above, so 2^15 at most, in
+// range), and a key counts in O down to 2^-32 of the row's reference.
+//
 // Rows of V behind the context's or the drafts' end share a stage with real
 // ones and may hold anything: P is 0 there, but 0 * NaN is not, so the softmax
 // warps clear them in shared memory before O += P V reads the stage.
@@ -272,6 +281,8 @@ __global__ void __launch_bounds__(TreeGeom<D, QS, NT>::NUM_THREADS, 1)
   using E = Elem<BF16>;
   constexpr int BK = Gm::BK, NCH = Gm::NCH, SL = Gm::SLOTS, KPW = Gm::KPW, NV = Gm::NV, NB = Gm::NB;
   constexpr int PRODUCER = Gm::SOFTMAX_WARPS;
+  // P and l are multiplied by 2^LIFT (see the head of this file)
+  constexpr float LIFT = BF16 ? 0.f : 7.f, UNLIFT = BF16 ? 1.f : 1.f / 128;
   constexpr int kWait = wait_code<94>();  // every bounded wait of this kernel
 
   extern __shared__ uint8_t smem_raw[];
@@ -591,7 +602,7 @@ __global__ void __launch_bounds__(TreeGeom<D, QS, NT>::NUM_THREADS, 1)
             }
           }
         }
-        const float mu = m == -INFINITY ? 0.f : m;
+        const float mu = m == -INFINITY ? 0.f : m - LIFT;
         const uint64_t sl2x2 = f2_pack(sl2, sl2), nm2 = f2_pack(-mu, -mu);
         uint64_t sum[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
         uint32_t pk[NB][NV / 2];
@@ -663,7 +674,7 @@ __global__ void __launch_bounds__(TreeGeom<D, QS, NT>::NUM_THREADS, 1)
       const bool mine = row < R && (whole ? dbg_in_range(grow, 1, n_rows, p.status, 64)
                                           : dbg_in_range(prow, 1, n_parts, p.status, 65));
       if (kq == 0 && mine) {
-        const float lse = m + log2f(l);
+        const float lse = m + log2f(l * UNLIFT);
         if (whole) p.lse[grow] = empty ? INFINITY : lse;
         else p.part_lse[prow] = empty ? -INFINITY : lse;
       }
