@@ -1,6 +1,8 @@
 """The cache calls where their inputs are at the edge of what they take: keys
-whose probabilities are far below the row's largest.  Bounds as in
-test_cache_ops_gpu.py, whose helpers are used."""
+whose probabilities are far below the row's largest, rows and keys that hold
+anything in the key-weight kernel for many rows, arrays that are neighbours
+in one buffer, layouts that are refused.  Bounds as in test_cache_ops_gpu.py,
+whose helpers are used."""
 
 import math
 
@@ -62,3 +64,126 @@ def test_tree_light_keys_are_not_lost(dt, B, G, T, Lk, D):
     assert err <= tol, f"O off by {err:.3g} of {ref:.3g} (tolerance {tol:.3g})"
     lref = math.log2(heavy + n_light * p)
     assert np.abs(to_f64(lse) - lref).max() <= 1.45 * (2 * d + n * X + 2.0 ** -21) + 2 * X * lref
+
+
+ROWS_OF_ALL_KINDS = [
+    # B, Hkv, G, Lq, Lk, D: G * Lq > 128 rows, several key tiles of 256
+    (4, 2, 4, 100, 900, 128),   # every step a CTA of its own: all key tiles are joined
+    (4, 8, 2, 200, 1000, 128),  # three steps a CTA, four row tiles: ranges end inside key tiles
+    (4, 2, 3, 70, 700, 256),    # steps of 64 rows
+    (4, 3, 1, 300, 520, 64),
+    (4, 2, 2, 97, 800, 96),
+    (4, 2, 2, 24, 600, 128),    # the kernel for few rows
+]
+
+
+@pytest.mark.parametrize("B,Hkv,G,Lq,Lk,D", ROWS_OF_ALL_KINDS)
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")], ids=["nan", "inf"])
+def test_key_weight_rows_that_count_for_nothing_many_rows(B, Hkv, G, Lq, Lk, D, bad):
+    """Rejected rows (limit 0, negative, or lse = +inf) hold anything, in q and
+    in lse, keys behind every limit too; limits past the end see every key."""
+    gen = torch.Generator().manual_seed(Lq + D)
+    rng = np.random.default_rng(Lq)
+    Hq = G * Hkv
+    q, k = ops.rand(gen, (B, Hq, Lq, D), BF), ops.cache(gen, B, Hkv, Lk, D, BF, pitch=Lk + 3)
+    end = [Lk - 150, Lk, Lk - 1, 300]  # keys that exist, per sequence
+    lim = np.stack([rng.integers(1, end[b] + 1, Lq) for b in range(B)]).astype(np.int32)
+    kind = rng.integers(0, 6, (B, Lq))
+    lim[kind == 0], lim[kind == 1] = 0, -7
+    lim[1][kind[1] == 2] = 10 ** 9
+    lim[2] = 0  # a sequence of which nothing is accepted
+    kind[2] = 0
+    lim[3] = np.sort(np.clip(lim[3], 0, None))  # ascending limits: whole row tiles see nothing of late key tiles
+    kind[3] = np.where(lim[3] == 0, 0, 5)
+    for b in range(B):
+        k[b, :, end[b]:] = bad
+    none = torch.from_numpy((kind == 0) | (kind == 1)).cuda()[:, None].expand(B, Hq, Lq)
+    away = torch.from_numpy(kind == 3).cuda()[:, None].expand(B, Hq, Lq)  # lse = +inf
+    qc, kc = q.clone(), torch.nan_to_num(k, nan=0.0, posinf=0.0)
+    scale = float(np.float32(1 / math.sqrt(D)))
+    seen = np.clip(lim, 0, Lk)
+    true = ops.weight_lse(qc, kc, scale, "limit", seen)
+    lse = torch.from_numpy(true).float().cuda()
+    clean = lse.clone()
+    q[none], q[away] = bad, bad
+    lse[none], clean[none] = torch.where(torch.rand(int(none.sum()), generator=gen).cuda() < 0.5, bad, -bad), 0.0
+    lse[away], clean[away] = float("inf"), float("inf")
+    w0 = torch.rand((B, Hkv, Lk), generator=gen).cuda()
+    ws = gbattn.key_weight_workspace(q, k).fill_(0xFF)
+    out = []
+    for _ in range(2):
+        out.append(torch.full_like(w0, float("nan")))
+        gbattn.attn_key_weight(q, k, lse, w0, out[-1], ws, scale, limit=torch.from_numpy(lim).cuda())
+        ops.ok()
+    assert torch.equal(out[0], out[1])
+    ops.check_weight(qc, kc, clean, w0, out[0], scale, "limit", seen)
+    for b in range(B):
+        assert torch.equal(out[0][b, :, end[b]:], w0[b, :, end[b]:])
+    assert torch.equal(out[0][2], w0[2])
+
+
+@pytest.mark.parametrize("G,Lq,D", [(1, 3, 128), (2, 70, 128), (4, 40, 256)])
+def test_key_weight_many_sequences(G, Lq, D):
+    B, Hkv, Lk = 130, 1, 300
+    gen = torch.Generator().manual_seed(Lq)
+    q, k = ops.rand(gen, (B, G, Lq, D), BF), ops.cache(gen, B, Hkv, Lk, D, BF)
+    lim = ops.row_limits(np.random.default_rng(Lq), B, Lq, Lk)
+    lim[5:60:3] = 0
+    scale = float(np.float32(1 / math.sqrt(D)))
+    lse = torch.from_numpy(ops.weight_lse(q, k, scale, "limit", lim)).float().cuda()
+    out = torch.full((B, Hkv, Lk), float("nan"), device="cuda")
+    gbattn.attn_key_weight(q, k, lse, None, out, gbattn.key_weight_workspace(q, k), scale, limit=torch.from_numpy(lim).cuda())
+    ops.ok()
+    ops.check_weight(q, k, lse, None, out, scale, "limit", lim)
+
+
+def test_arrays_side_by_side_in_one_buffer():
+    """Neighbours that do not overlap are taken, and nothing is written next to an output."""
+    B, Hkv, T, Lk, D = 8, 2, 4, 64, 64
+    gen = torch.Generator().manual_seed(3)
+    k, v = ops.cache(gen, B, Hkv, Lk, D, BF).contiguous(), ops.cache(gen, B, Hkv, Lk, D, BF).contiguous()
+    kn, vn = ops.rand(gen, (B, Hkv, T, D), BF), ops.rand(gen, (B, Hkv, T, D), BF)
+    ints = torch.arange(6 * B, dtype=torch.int32, device="cuda")
+    lens, lens_out, seen, seen_out, acc, last = ints.view(6, B)
+    lens.copy_(ops.i32([10 + b for b in range(B)])), acc.fill_(3)
+    before = ints.clone()
+    gbattn.attn_cache_append(kn, vn, k, v, lens, acc, lens_out, seen=seen, seen_out=seen_out)
+    ops.ok()
+    assert torch.equal(lens_out, before[:B] + 3) and torch.equal(seen_out, before[2 * B:3 * B] + 3)
+    assert torch.equal(lens, before[:B]) and torch.equal(seen, before[2 * B:3 * B]) and torch.equal(ints[4 * B:], before[4 * B:])
+    w = torch.rand(2, B, Hkv, Lk, generator=gen).cuda()
+    pos = torch.arange(2 * B * Hkv * Lk, dtype=torch.int32, device="cuda").view(2, B, Hkv, Lk) % Lk
+    w0, p0 = w[0].clone(), pos[0].clone()
+    gbattn.attn_cache_evict(k, v, w[0], pos[0], lens_out, seen, w[1], pos[1], last, gbattn.evict_workspace(k), 12, 0)
+    ops.ok()
+    assert torch.equal(w[0], w0) and torch.equal(pos[0], p0) and torch.equal(last, torch.clamp(lens_out, max=12))
+
+
+def test_binding_refuses_expanded_caches_and_pitches_past_the_tensors():
+    B, Hq, Hkv, T, Lk, D = 2, 4, 2, 3, 40, 64
+    z = lambda *s: torch.zeros(s, dtype=torch.int32, device="cuda")  # noqa: E731
+    f = lambda *s: torch.zeros(s, device="cuda")  # noqa: E731
+    gen = torch.Generator().manual_seed(1)
+    q, kn = ops.rand(gen, (B, Hq, T, D), BF), ops.rand(gen, (B, Hkv, T, D), BF)
+    k = ops.rand(gen, (B, Hkv, Lk, D), BF)
+    ws = torch.empty(1 << 24, dtype=torch.uint8, device="cuda")
+
+    def calls(k, **kw):
+        return (lambda: gbattn.attn_fwd_tree(q, k, k, kn, kn, z(B), torch.empty_like(q), f(B, Hq, T), ws, 0.1, **kw),
+                lambda: gbattn.attn_key_weight(q, k, f(B, Hq, T), None, f(B, Hkv, Lk), ws, 0.1, limit=z(B, T), **kw),
+                lambda: gbattn.attn_cache_append(kn, kn, k, k, z(B), None, z(B), **kw),
+                lambda: gbattn.attn_cache_evict(k, k, f(B, Hkv, Lk), z(B, Hkv, Lk), z(B), z(B), f(B, Hkv, Lk),
+                                                z(B, Hkv, Lk), z(B), ws, 10, 2, **kw))
+
+    for call in calls(k[:1, :1].expand(B, Hkv, Lk, D)):
+        with pytest.raises(ValueError, match="not a slice"):
+            call()
+    for call in calls(k, kv_pitch=Lk + 1):
+        with pytest.raises(ValueError, match="kv_pitch"):
+            call()
+    for call in calls(k, kv_pitch=Lk - 1):
+        with pytest.raises(gbattn.AttnError):
+            call()
+    for call in calls(k, kv_pitch=Lk):
+        assert call() == gbattn.ATTN_OK
+    ops.ok()
