@@ -31,6 +31,7 @@ __global__ void __launch_bounds__(kAppendThreads) attn_cache_append_kernel(const
   n = min(n, p.Lk - len);
   const int32_t* path = p.path ? p.path + static_cast<size_t>(b) * p.T : nullptr;
   if (path) {  // the path ends at its first entry that is no draft
+    if (!dbg_in_range(static_cast<size_t>(b) * p.T, n, static_cast<size_t>(p.B) * p.T, p.status, 69)) n = 0;
     if (threadIdx.x == 0) cut = n;
     __syncthreads();
     for (int i = threadIdx.x; i < n; i += kAppendThreads)
@@ -68,7 +69,7 @@ __global__ void __launch_bounds__(kAppendThreads) attn_cache_append_kernel(const
       p.cache_len_out[b] = len + n;
       if (p.seen_out) p.seen_out[b] = seen + n;
     }
-    if (p.limit) {
+    if (p.limit && dbg_in_range(static_cast<size_t>(b) * p.T, p.T, static_cast<size_t>(p.B) * p.T, p.status, 79)) {
       int32_t* limit = p.limit + static_cast<size_t>(b) * p.T;
       if (path) {
         // the last of equal entries: the largest limit, whatever the order of the maxima
@@ -404,7 +405,7 @@ __global__ void __launch_bounds__(kEvictThreads, 1) attn_cache_evict_kernel(cons
   const int m0 = min(rank * each, n), m1 = min(m0 + each, n);
   uint16_t* freed = reinterpret_cast<uint16_t*>(keys + p.Lk);
   uint16_t* moving = freed + share;
-  if (on) evict_list(tid * 32, k, m, below, above, m0, m1, freed, moving);
+  if (on && dbg_in_range(0, m1 - m0, share, p.status, 88)) evict_list(tid * 32, k, m, below, above, m0, m1, freed, moving);
   __syncthreads();
   // rows and values side by side: one's latency does not wait for the other's
   constexpr int ROW_THREADS = kEvictThreads * 3 / 4, VALUE_THREADS = kEvictThreads - ROW_THREADS;
@@ -474,7 +475,10 @@ __global__ void __launch_bounds__(kEvictClusterThreads) attn_cache_evict_cluster
   const int per_warp = ((len + NC * NW - 1) / (NC * NW) + 31) & ~31;
   const int j0 = min(rank * NW * per_warp, len), j1 = min(j0 + NW * per_warp, len);
   const int w0 = min(j0 + warp * per_warp, j1), w1 = min(w0 + per_warp, j1);
-  auto key_at = [&](int j) { return CACHED ? keys[j - j0] : evict_key(w[j], pos[j], recent_from); };
+  auto key_at = [&](int j) {
+    if constexpr (CACHED) return keys[j - j0];
+    else return evict_slot_ok(p, row + j, 89) ? evict_key(w[j], pos[j], recent_from) : 0u;
+  };
   for (int i = tid; i < 4 * BINS; i += kEvictClusterThreads) (&hist[0][0])[i] = (&first[0][0])[i] = 0;
   __syncthreads();
   evict_load<8>(p, bh, w0, w1, j0, CACHED ? keys : nullptr, recent_from, first[lane & 3], 24);
@@ -598,6 +602,7 @@ __global__ void __launch_bounds__(kEvictClusterThreads) attn_cache_evict_cluster
   const int cap = p.Lk / 2;  // min(keep, len - keep) slots at most
   int32_t* freed = p.lists + static_cast<size_t>(bh) * 2 * cap;
   int32_t* moving = freed + cap;
+  auto list_ok = [&](int i) { return dbg_in_range(i, 1, cap, p.status, 90); };  // entry i of either
   // a strip of 32 slots per lane; then the warp writes the strips one by one, so
   // that a list's entries are stored side by side (a lane for each strip took
   // 134 us at 2 x 8 heads 200000 -> 20000, where one CTA has all the freed slots, this 129)
@@ -616,8 +621,9 @@ __global__ void __launch_bounds__(kEvictClusterThreads) attn_cache_evict_cluster
       const uint32_t kt = __shfl_sync(0xffffffffu, k, t), mt = __shfl_sync(0xffffffffu, m, t);
       const int f0 = __shfl_sync(0xffffffffu, fb, t), m0 = __shfl_sync(0xffffffffu, mb, t);
       const uint32_t h = ~kt & mt, v = kt & ~mt, below_me = (1u << lane) - 1u;
-      if (((h >> lane) & 1u) && f0 + __popc(h & below_me) < n) freed[f0 + __popc(h & below_me)] = i0 + 32 * t + lane;
-      if (((v >> lane) & 1u) && m0 + __popc(v & below_me) < n) moving[m0 + __popc(v & below_me)] = i0 + 32 * t + lane;
+      const int fi = f0 + __popc(h & below_me), mi = m0 + __popc(v & below_me);
+      if (((h >> lane) & 1u) && fi < n && list_ok(fi)) freed[fi] = i0 + 32 * t + lane;
+      if (((v >> lane) & 1u) && mi < n && list_ok(mi)) moving[mi] = i0 + 32 * t + lane;
     }
     below += __shfl_sync(0xffffffffu, b0, 31), above += __shfl_sync(0xffffffffu, a0, 31);
   }
@@ -634,8 +640,10 @@ __global__ void __launch_bounds__(256) attn_cache_move_kernel(const EvictParams 
   const int bh = blockIdx.y, cap = p.Lk / 2;
   const int32_t* freed = p.lists + static_cast<size_t>(bh) * 2 * cap;
   const int all = static_cast<int>(blockIdx.x * 256 + threadIdx.x), step = static_cast<int>(gridDim.x * 256);
-  evict_move(p, bh, freed + cap, freed, p.counts[bh], all, step);
-  evict_move_values(p, bh, freed + cap, freed, p.counts[bh], all, step);
+  const int n = p.counts[bh];
+  if (!dbg_in_range(0, n, cap, p.status, 91)) return;
+  evict_move(p, bh, freed + cap, freed, n, all, step);
+  evict_move_values(p, bh, freed + cap, freed, n, all, step);
 }
 
 }  // namespace gbattn

@@ -30,7 +30,8 @@ __host__ __device__ constexpr int wait_code() {
 
 // Debug build (compiled with -DGBATTN_DEBUG_CHECKS): every plain global load
 // and store of the kernels first checks that the elements it touches,
-// [first, first + count), lie inside the tensor's extent [0, extent).  A
+// [first, first + count), lie inside the tensor's extent [0, extent) (but for
+// one element per sequence, whose number the grid or a loop to B bounds).  A
 // failed check records kDevBoundsBase + site in the status word and the
 // access is skipped -- nothing traps, and the host reads the code through
 // attn_last_device_status.  In the normal build the check is a constant

@@ -30,10 +30,16 @@
 
 namespace gbattn {
 
+// Row t's limit as given (limit calls).
+__device__ __forceinline__ int key_weight_limit(const KeyWeightParams& p, int b, int t) {
+  const size_t i = static_cast<size_t>(b) * p.Lq + t;
+  return dbg_in_range(i, 1, static_cast<size_t>(p.B) * p.Lq, p.status, 70) ? p.limit[i] : 0;
+}
+
 // Where the keys of a row end, and -lse (see above).
 __device__ __forceinline__ void key_weight_row(const KeyWeightParams& p, int b, int t, float lse, int& lim,
                                                float& nlse) {
-  lim = p.limit ? min(max(p.limit[static_cast<size_t>(b) * p.Lq + t], 0), p.Lk) : p.causal ? t + p.Lk - p.Lq + 1 : p.Lk;
+  lim = p.limit ? min(max(key_weight_limit(p, b, t), 0), p.Lk) : p.causal ? t + p.Lk - p.Lq + 1 : p.Lk;
   nlse = -lse;
   if (lse == INFINITY) lim = 0;
 }
@@ -92,9 +98,7 @@ __device__ __forceinline__ void key_weight_table(const KeyWeightParams& p, int* 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   for (int b = warp; b < p.B; b += warps) {
     int most = 0;
-    for (int t = lane; t < p.Lq; t += 32)
-      if (dbg_in_range(static_cast<size_t>(b) * p.Lq + t, 1, static_cast<size_t>(p.B) * p.Lq, p.status, 70))
-        most = max(most, p.limit[static_cast<size_t>(b) * p.Lq + t]);
+    for (int t = lane; t < p.Lq; t += 32) most = max(most, key_weight_limit(p, b, t));
     most = __reduce_max_sync(0xffffffffu, most);
     if (lane == 0) tab[b + 1] = (min(most, p.Lk) + BK - 1) / BK;
   }
@@ -644,7 +648,7 @@ __global__ void __launch_bounds__(KeyWeightGeom<D>::NUM_THREADS, 1)
             const size_t row = (p.packed ? static_cast<size_t>(z) : static_cast<size_t>(z) * p.G + at.g) * rows + in;
             const bool real = dbg_in_range(row, 1, static_cast<size_t>(p.B) * p.Hq * p.Lq, p.status, 74);
             x[u][i] = real ? p.lse[row] : INFINITY;
-            l[u][i] = p.limit ? p.limit[static_cast<size_t>(w.b) * p.Lq + t] : t;
+            l[u][i] = p.limit ? key_weight_limit(p, w.b, t) : t;
             if (r >= rows) l[u][i] = -1;
           }
           if (++fetched < w.s1) at.next(w.st);  // (the last step again, past the end)

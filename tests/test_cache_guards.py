@@ -147,3 +147,36 @@ def test_outputs_over_inputs_or_one_another_are_refused(lib):
     refused(call, ("weight_out",), ("q", "lse", "limit"), sizes)
     for shift in (16, -16, slots - 16, 16 - slots):  # the same array is fine, a shifted one is not
         assert call(weight_out=A[4] + shift) == gbattn.ATTN_ERR_INVALID_ARG, shift
+
+
+# Global arrays of the cache kernels that are indexed by something computed on
+# the device, and how far above the access its check may stand (in lines).
+CHECKED = {
+    "cache_kernel.cuh": (r"[^_]freed\[.*\] = i", r"[^_]moving\[.*\] = i", r"evict_move\(p, bh, freed", r"path\[i\] [<>]",
+                         r"limit\[t\] =", r"p\.weight\[row", r"p\.weight_out\[row", r"\(w\[j\], pos\[j\]", r"kd\[x\] =",
+                         r"p\.pos\[at", r"= w\[i"),
+    "key_weight_kernel.cuh": (r"p\.limit\[", r"p\.weight\[o\]", r"p\.weight_out\[o\] =", r"p\.part\[", r"p\.lse\["),
+    "tree_kernel.cuh": (r"p\.part_lse\[", r"p\.lse\[grow\]", r"tree_mask_bits<", r"p\.part \+ r \*"),
+}
+
+
+@pytest.mark.parametrize("name", CHECKED)
+def test_debug_build_checks_computed_indices(name):
+    lines = open(os.path.join(os.path.dirname(gbattn.__file__), "csrc", name)).read().split("\n")
+    check = re.compile(r"dbg_in_range|evict_slot_ok|list_ok\(|\bon\[u\]|\bmine\b")
+    for access in CHECKED[name]:
+        hits = [i for i, s in enumerate(lines) if re.search(access, s) and not s.lstrip().startswith("//")]
+        assert hits, f"{name}: no line matches {access}"
+        for i in hits:
+            assert any(check.search(s) for s in lines[max(0, i - 12):i + 1]), f"{name}:{i + 1}: {lines[i].strip()}"
+
+
+def test_debug_check_sites_are_unique():
+    """A recorded site names one check."""
+    sites = {}
+    for name in CHECKED:
+        text = open(os.path.join(os.path.dirname(gbattn.__file__), "csrc", name)).read()
+        for n in re.findall(r"dbg_in_range\((?:[^;{]|\n)*?status,\s*(\d+)\)", text) + re.findall(r"evict_slot_ok\(p, [^;]*?, (\d+)\)", text):
+            assert n not in sites, f"site {n}: {sites[n]} and {name}"
+            sites[n] = name
+    assert len(sites) >= 25

@@ -5,6 +5,9 @@ in one buffer, layouts that are refused.  Bounds as in test_cache_ops_gpu.py,
 whose helpers are used."""
 
 import math
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -187,3 +190,15 @@ def test_binding_refuses_expanded_caches_and_pitches_past_the_tensors():
     for call in calls(k, kv_pitch=Lk):
         assert call() == gbattn.ATTN_OK
     ops.ok()
+
+
+@pytest.mark.skipif(os.environ.get("GBATTN_DEBUG") == "1", reason="this is the child")
+def test_no_index_check_fires_here():
+    """This file's cases in the debug build, whose kernels check their indices."""
+    from bwd_flashattention_fwd_gb300 import build
+
+    build.build(debug=True)
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    run = subprocess.run([sys.executable, "-m", "pytest", "-q", "-x", "-m", "gpu", os.path.abspath(__file__)], cwd=root,
+                         env=dict(os.environ, GBATTN_DEBUG="1"), capture_output=True, text=True, timeout=600)
+    assert run.returncode == 0, run.stdout[-3000:] + run.stderr[-1000:]
