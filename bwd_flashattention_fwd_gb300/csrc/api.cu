@@ -259,6 +259,12 @@ namespace gbattn {
 attn_status_t shared_device_state(int* dev, EncodeTiledFn* enc, int** status, int* num_sms) {
   return device_state(dev, enc, status, num_sms);
 }
+bool shared_device_ready() {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return true;  // device_state's error to report
+  std::lock_guard<std::mutex> lock(g_mu);
+  return g_status[dev] != nullptr;
+}
 uint64_t shared_wait_limit_ns() { return wait_limit_ns(); }
 }  // namespace gbattn
 

@@ -88,6 +88,20 @@ bool outputs_overlap(const Span (&s)[N], int n_out) {
   return false;
 }
 
+// The device's state for a call on `stream`.  It is allocated by the first call
+// on a device, which a stream capture does not allow and would not survive: such
+// a first call is refused before it touches anything.
+attn_status_t call_state(cudaStream_t stream, int* dev, EncodeTiledFn* enc, int** status, int* num_sms) {
+  if (!shared_device_ready()) {
+    cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
+    if (cudaStreamIsCapturing(stream, &cs) != cudaSuccess || cs != cudaStreamCaptureStatusNone) {
+      cudaGetLastError();  // an implicit-capture error must not linger for later calls
+      return ATTN_ERR_INVALID_ARG;
+    }
+  }
+  return shared_device_state(dev, enc, status, num_sms);
+}
+
 attn_status_t finish(int r) {
   return r == kLaunchOk ? ATTN_OK : r == kLaunchBadMap ? ATTN_ERR_INVALID_ARG : ATTN_ERR_CUDA;
 }
@@ -129,7 +143,7 @@ extern "C" attn_status_t attn_fwd_tree(const void* q, const void* k, const void*
   if (outputs_overlap(spans, 2)) return ATTN_ERR_INVALID_ARG;
   int dev, num_sms, *status;
   EncodeTiledFn enc;
-  const attn_status_t ds = shared_device_state(&dev, &enc, &status, &num_sms);
+  const attn_status_t ds = call_state(stream, &dev, &enc, &status, &num_sms);
   if (ds != ATTN_OK) return ds;
   TreeParams p{};
   p.q = q, p.k = k, p.v = v, p.k_new = k_new, p.v_new = v_new;
@@ -182,7 +196,7 @@ extern "C" attn_status_t attn_key_weight(const void* q, const void* k, const flo
   if (weight != weight_out && overlap(out, {weight, slots})) return ATTN_ERR_INVALID_ARG;
   int dev, num_sms, *status;
   EncodeTiledFn enc;
-  const attn_status_t ds = shared_device_state(&dev, &enc, &status, &num_sms);
+  const attn_status_t ds = call_state(stream, &dev, &enc, &status, &num_sms);
   if (ds != ATTN_OK) return ds;
   KeyWeightParams p{};
   p.q = q, p.k = k, p.lse = lse, p.limit = limit, p.weight = weight, p.weight_out = weight_out;
@@ -226,7 +240,7 @@ extern "C" attn_status_t attn_cache_append(const void* k_new, const void* v_new,
   if (outputs_overlap(spans, 4)) return ATTN_ERR_INVALID_ARG;
   int dev, num_sms, *status;
   EncodeTiledFn enc;
-  const attn_status_t ds = shared_device_state(&dev, &enc, &status, &num_sms);
+  const attn_status_t ds = call_state(stream, &dev, &enc, &status, &num_sms);
   if (ds != ATTN_OK) return ds;
   AppendParams p{k_new, v_new, path, accept_len, cache_len, seen, k, v, pos, cache_len_out, seen_out, limit,
                  kv_pitch ? kv_pitch : Lk, B, Hkv, T, Lk, D / 8, status};
@@ -266,7 +280,7 @@ extern "C" attn_status_t attn_cache_evict(void* k, void* v, const float* weight,
   if (outputs_overlap(spans, 3)) return ATTN_ERR_INVALID_ARG;
   int dev, num_sms, *status;
   EncodeTiledFn enc;
-  const attn_status_t ds = shared_device_state(&dev, &enc, &status, &num_sms);
+  const attn_status_t ds = call_state(stream, &dev, &enc, &status, &num_sms);
   if (ds != ATTN_OK) return ds;
   EvictParams p{k, v, weight, pos, cache_len, seen, weight_out, pos_out, cache_len_out,
                 static_cast<int32_t*>(workspace),

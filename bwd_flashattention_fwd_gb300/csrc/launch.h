@@ -90,6 +90,8 @@ inline size_t decode_workspace_bytes(int B, int Hkv, long long rows, int Lk, int
 // Device state shared by every call of the library (api.cu): tensor-map
 // encoder, device status word, SM count; and the bounded-wait limit.
 attn_status_t shared_device_state(int* dev, EncodeTiledFn* enc, int** status, int* num_sms);
+// Whether the call above allocates nothing: the current device's state exists already (or there is no such device).
+bool shared_device_ready();
 uint64_t shared_wait_limit_ns();
 
 // Launch results: 0 = launched, 1 = tensor-map encoding rejected the

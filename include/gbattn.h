@@ -239,6 +239,11 @@ attn_status_t attn_bwd_decode(const void* q, const void* k, const void* v, const
  *     ATTN_ERR_UNSUPPORTED).  No output overlaps an input or the other output
  *     (ATTN_ERR_INVALID_ARG; the cache and the workspace are not checked).
  *     int32 arrays are 4-byte aligned.  Other errors as for attn_fwd_ex.
+ *   Stream capture: this call and the three below can be captured and replayed
+ *     (lengths, limits and paths are read on the device at each replay).  The
+ *     library's first call on a device allocates its status word; one of these
+ *     four made as that first call while `stream` is being captured is refused
+ *     with ATTN_ERR_INVALID_ARG and changes nothing.
  */
 size_t attn_tree_workspace_bytes(int B, int Hq, int Hkv, int T, int Lk, int D);
 attn_status_t attn_fwd_tree(const void* q, const void* k, const void* v, const void* k_new, const void* v_new,

@@ -192,6 +192,55 @@ def test_binding_refuses_expanded_caches_and_pitches_past_the_tensors():
     ops.ok()
 
 
+FIRST_CALL = r"""
+import torch
+from bwd_flashattention_fwd_gb300 import gbattn
+
+B, H, T, Lk, D = 1, 2, 3, 300, 64
+h = lambda n: torch.ones(B, H, n, D, dtype=torch.bfloat16, device="cuda")
+z = lambda *s: torch.zeros(s, dtype=torch.int32, device="cuda")
+f = lambda *s: torch.zeros(s, device="cuda")
+q, k, v, n, o, lens, ws = h(T), h(Lk), h(Lk), h(T), h(T), z(B), torch.empty(1 << 24, dtype=torch.uint8, device="cuda")
+lens += Lk - T
+calls = (lambda: gbattn.attn_fwd_tree(q, k, v, n, n, lens, o, lse, ws, 0.1),
+         lambda: gbattn.attn_cache_append(n, n, k, v, lens, None, out),
+         lambda: gbattn.attn_key_weight(q, k, lse, None, w, ws, 0.1),
+         lambda: gbattn.attn_cache_evict(k, v, w, pos, lens, lens, w2, pos2, out, ws, 100, 10))
+lse, w, w2, pos, pos2, out = f(B, H, T), f(B, H, Lk), f(B, H, Lk), z(B, H, Lk), z(B, H, Lk), z(B)
+torch.cuda.synchronize()
+for call in calls:
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        o.zero_()
+        try:
+            call()
+            raise SystemExit("a first call inside a capture was not refused")
+        except gbattn.AttnError as e:
+            assert e.status == gbattn.ATTN_ERR_INVALID_ARG, e
+    g.replay()  # the capture is whole
+    torch.cuda.synchronize()
+calls[0]()
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):  # the other kernels' first calls, captured
+    for call in calls:
+        call()
+g.replay()
+torch.cuda.synchronize()
+assert gbattn.attn_last_device_status() == gbattn.ATTN_OK
+assert (o == 1).all() and out.tolist() == [100]
+print("first calls refused, later ones captured")
+"""
+
+
+def test_first_call_inside_a_capture_is_refused():
+    """In a process of its own: no call has set the library up yet."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    run = subprocess.run([sys.executable, "-c", FIRST_CALL], cwd=root, env=dict(os.environ, PYTHONPATH=root),
+                         capture_output=True, text=True, timeout=300)
+    assert run.returncode == 0 and "later ones captured" in run.stdout, run.stdout[-2000:] + run.stderr[-2000:]
+
+
 @pytest.mark.skipif(os.environ.get("GBATTN_DEBUG") == "1", reason="this is the child")
 def test_no_index_check_fires_here():
     """This file's cases in the debug build, whose kernels check their indices."""
