@@ -187,6 +187,8 @@ extern "C" attn_status_t attn_key_weight(const void* q, const void* k, const flo
   if (causal && (limit || Lq > Lk)) return ATTN_ERR_INVALID_ARG;
   if (c != ATTN_OK) return c;
   if (s != ATTN_OK) return s;
+  // every CTA reads all B x Lq limits before it starts (how far each sequence's
+  // rows reach decides the division), and holds B sums
   if (limit && (Lq > kTreeMaxT || B > kTreeMaxB)) return ATTN_ERR_UNSUPPORTED;
   if (workspace_bytes < attn_key_weight_workspace_bytes(B, Hq, Hkv, Lq, Lk, D)) return ATTN_ERR_INVALID_ARG;
   const long long rows = static_cast<long long>(B) * Hq * Lq, slots = 4LL * B * Hkv * Lk;
@@ -289,9 +291,11 @@ extern "C" attn_status_t attn_cache_evict(void* k, void* v, const float* weight,
   const int heads = B * Hkv;
   if (Lk <= kEvictRowKeys) {
     // about one CTA per SM, so that the moves run at the memory's rate (4 x 8
-    // heads 8448 -> 8192: 11.8 us, by clusters 15.8; 16384 -> 8192: 37.7 and 39.9,
-    // -> 16128: 15.6 and 16.9; 2 heads of 16384: 14.6 and 13.4; past that one CTA's
-    // search takes too long: 8 heads of 32768 55 us, by clusters 20)
+    // heads 8448 -> 8192: 11.3 us, by clusters 15.6; 16384 -> 8192: 37.9 and 40.1,
+    // -> 16128: 15.2 and 16.2; 2 heads 8448 -> 8192: 9.7 and 12.2, 16384 -> 8192:
+    // 13.7 and 13.3, -> 16128: 12.0 and 12.5, so the number of heads is left out of
+    // the rule; past 16384 one CTA's search takes too long: 8 heads of 32768 55 us,
+    // by clusters 20)
     const int copies = heads < num_sms ? num_sms / heads : 1;
     static std::atomic<uint64_t> done{0};
     if (!set_smem_limit(attn_cache_evict_kernel, evict_smem(kEvictRowKeys, 1), done)) return ATTN_ERR_CUDA;

@@ -14,13 +14,18 @@ constexpr int kTreeMaxB = 1024;   // sequences (each CTA holds the lengths' pref
 // than a stage's chain of S, softmax and P V takes, so small heads take 128
 // (16384 keys D = 64: B8 T8 50.7 us, with 64 keys 67.1; T30 58.9 and 72.4).
 constexpr int tree_stage_keys(int D, int nt) { return D <= 96 && nt == 1 ? 128 : 64; }
-constexpr int kTreeExtra = 7;      // what a CTA spends on a KV head besides its stages, in stages
+// What a CTA spends on a KV head besides its stages, in stages (B16 T61 ragged
+// 70.4 us, with 4 72.5, 10 70.7, 14 70.9).
+constexpr int kTreeExtra = 7;
 // Small caches: KV heads are not divided, which saves the partials and the
 // second launch, where a CTA's stages are at most kTreeWholeMost and at most
-// kTreeWholeMore above an even share.  B2 T47 200 keys D = 64 (5 stages) 10.8
-// us, divided 15.7; B24 T4 400 keys D = 128 (2 heads of 8 stages) 18.1 and
-// 21.4; B1 T8 400 keys (8 stages) 10.0 and 9.6 on the device, with one launch
-// for the host instead of two; 700 keys (12 stages) 11.8 and 10.0.
+// kTreeWholeMore above an even share.  B2 T47 200 keys D = 64 (5 stages) 10.1
+// us, divided 12.7; B24 T4 400 keys D = 128 (2 heads of 8 stages) 18.3 and
+// 19.4; B18 T8 1400 keys (24 stages) 22.5 and 27.9; B1 T8 400 keys (8 stages) 9.9
+// and 9.1 on the device, but one launch for the host instead of two (10.9 us a
+// call and 13.7).  Beyond the rule: B1 T8 700 keys (12 stages) 11.6, divided 9.5;
+// B4 T1 1000 keys D = 256 20.0 and 10.8; the other way round B8 T8 1000 keys, 64
+// heads of 17 stages on 152 CTAs: 15.4 and 18.4.
 constexpr int kTreeWholeMost = 24, kTreeWholeMore = 8;
 constexpr int kTreeMaxCtas = 152;  // one per SM of a GB300
 constexpr int kCacheMaxLk = 1 << 30;  // rows of a KV head (row numbers are ints)

@@ -1,7 +1,7 @@
 // The two cache calls that move rows: appending accepted drafts and evicting
 // the lightest keys.  Both are bound by memory traffic and latency: a prompt of
 // 2 x 2048 tokens, 8 heads, D = 128 is appended in 7.1 us (33.6 MB, 4.7 TB/s,
-// launch included), 8 drafts in 2.5.
+// launch included), 8 drafts in 2.7.
 #pragma once
 
 #include "cache.h"
@@ -18,9 +18,9 @@ __device__ __forceinline__ size_t cache_extent(int heads, int64_t pitch, int Lk,
 
 constexpr int kAppendThreads = 256;
 
-// Accepted drafts into the cache: block (x, b * Hkv + h) copies rows x,
-// x + gridDim.x, ... of the path, 16 bytes per thread; block (0, b * Hkv)
-// writes the sequence's lengths and key limits.
+// Accepted drafts into the cache: the blocks (x, b * Hkv + h) of a KV head
+// stride over the 16-byte pieces of the path's rows, one per thread; block
+// (0, b * Hkv) writes the sequence's lengths and key limits.
 __global__ void __launch_bounds__(kAppendThreads) attn_cache_append_kernel(const AppendParams p) {
   __shared__ int cut, lims[kTreeMaxT];  // (a path has at most kTreeMaxT entries)
   grid_dependency_wait();  // the kernels before this one are complete
@@ -349,7 +349,7 @@ __global__ void __launch_bounds__(kEvictThreads, 1) attn_cache_evict_kernel(cons
     prefix |= static_cast<uint32_t>(s_digit) << shift;
     need = s_need;
     // every slot that matches so far is kept: the lower digits do not matter
-    // (the usual end, as two digits leave one slot: 11.8 us, with all three 12.7)
+    // (the usual end, as two digits leave one slot: 0.9 us less than all three)
     if (d == 2 || need == s_equal) break;
     // the next digit of the slots that match so far (few)
     const uint32_t above = ~0u << shift;
@@ -605,7 +605,7 @@ __global__ void __launch_bounds__(kEvictClusterThreads) attn_cache_evict_cluster
   auto list_ok = [&](int i) { return dbg_in_range(i, 1, cap, p.status, 90); };  // entry i of either
   // a strip of 32 slots per lane; then the warp writes the strips one by one, so
   // that a list's entries are stored side by side (a lane for each strip took
-  // 134 us at 2 x 8 heads 200000 -> 20000, where one CTA has all the freed slots, this 129)
+  // 134 us at 2 x 8 heads 200000 -> 20000, where one CTA has all the freed slots, this 123)
   for (int i0 = w0; i0 < w1; i0 += 1024) {
     const int i = i0 + 32 * lane;
     const uint32_t k = i < w1 ? bits[(i - j0) >> 5] : 0u, m = i < w1 ? evict_below(i, keep) : 0u;

@@ -40,7 +40,7 @@
 //
 // P is rounded to 16 bits because that is what the tensor cores multiply V by;
 // l sums it unrounded.  The rounding is half a step of each p (2^-8 of it in
-// bf16, 2^-11 in fp16): against 64 bits O is 1.2 to 1.4 times as far off as with
+// bf16, 2^-11 in fp16): against 64 bits O is 1.1 to 1.4 times as far off as with
 // P in 32 bits, whose only 16-bit rounding is O's own.  Two 16-bit parts of P
 // would take it away for twice the products.  fp16 ends at 2^-25, where bf16
 // goes on to 2^-133, and many light keys together weigh something: there P
@@ -52,9 +52,9 @@
 // warps clear them in shared memory before O += P V reads the stage.
 //
 // Measured (call and combine kernel, replayed): B4 32/8 heads T8 8192 keys
-// D = 128 29.9 us for 134 MB (27 stages a CTA stream in 18.6 us, at the full copy
+// D = 128 30.1 us for 134 MB (27 stages a CTA stream in 18.6 us, at the full copy
 // rate; the rest is start, quadrant merge and combine); 131072 keys D = 256 85 us,
-// 6.3 TB/s; B16 T61 ragged 70.3 us for 321 MB, which stream in 45 us, at the full rate too.
+// 6.3 TB/s; B16 T61 ragged 70.2 us for 321 MB, which stream in 45 us, at the full rate too.
 #pragma once
 
 #include "cache.h"
@@ -64,8 +64,8 @@ namespace gbattn {
 
 // What every block derives from the lengths.  The list that the CTAs divide
 // counts units: a KV head's stages, and before them `extra` units for what a
-// CTA spends on a head besides its stages (loading Q, merging and writing O:
-// about three stages' time; fewer units where the ranges are short).
+// CTA spends on a head besides its stages (loading Q, merging and writing O):
+// kTreeExtra, or a sixth of a CTA's range where that is less.
 // pre[b]: units of one KV head of the sequences before b (pre[B] the total).
 struct TreeTable {
   int extra;

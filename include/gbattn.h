@@ -291,7 +291,8 @@ attn_status_t attn_cache_append(const void* k_new, const void* v_new, const int3
  *   Which keys row i sees: limit NULL: all, or with causal = 1 j <= i + (Lk - Lq)
  *     as in attn_fwd; limit int32 [B,Lq] on the device (causal = 0): keys
  *     j < limit[b][i], for every head (values outside 0..Lk are brought into
- *     that range; 0: the row adds nothing).  limit needs Lq and B <= 1024.
+ *     that range; 0: the row adds nothing).  limit needs Lq and B <= 1024
+ *     (else ATTN_ERR_UNSUPPORTED): it is for drafts; a prompt's rows are causal.
  *   A row whose lse is +inf adds nothing.
  *   weight float32 [B,Hkv,Lk] contiguous, or NULL (zeros); weight_out
  *     [B,Hkv,Lk] may be the same array, else it overlaps no input
