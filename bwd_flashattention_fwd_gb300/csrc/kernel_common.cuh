@@ -31,7 +31,7 @@ __host__ __device__ constexpr int wait_code() {
 // Debug build (compiled with -DGBATTN_DEBUG_CHECKS): every plain global load
 // and store of the kernels first checks that the elements it touches,
 // [first, first + count), lie inside the tensor's extent [0, extent) (but for
-// one element per sequence, whose number the grid or a loop to B bounds).  A
+// one element per sequence or KV head, whose number the grid or a loop bounds).  A
 // failed check records kDevBoundsBase + site in the status word and the
 // access is skipped -- nothing traps, and the host reads the code through
 // attn_last_device_status.  In the normal build the check is a constant
