@@ -1,8 +1,9 @@
 """Build libgbattn.so in-tree with nvcc for sm_103a.
 
 The kernel instantiations compile as one translation unit per head dimension
-(inst.cu and cache_inst.cu with -DGBATTN_HEAD_DIM=<D>), in parallel, plus the C-ABI unit and
-the linear cross-entropy unit (lce.cu) and the cache unit (cache.cu); the objects link into
+(inst.cu, cache_inst.cu and paged_inst.cu with -DGBATTN_HEAD_DIM=<D>), in parallel, plus the
+C-ABI unit (api.cu), the linear cross-entropy unit (lce.cu), the cache unit (cache.cu) and the
+unit of the calls around attention (step.cu); the objects link into
 bwd_flashattention_fwd_gb300/libgbattn.so (no library besides the CUDA
 runtime).  checks.cu becomes libgbattn_checks.so, a test aid.
 """
@@ -63,10 +64,10 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), debug: boo
     flags = [*FLAGS, *extra_flags] + (["-DGBATTN_DEBUG_CHECKS"] if debug else [])
     jobs = []
     for d in HEAD_DIMS:
-        for unit in ("inst", "cache_inst"):
+        for unit in ("inst", "cache_inst", "paged_inst"):
             obj = os.path.join(bdir, f"{unit}_d{d}.o")
             jobs.append([nvcc, *ARCH, *flags, f"-DGBATTN_HEAD_DIM={d}", "-c", os.path.join(CSRC, unit + ".cu"), "-o", obj])
-    for unit in ("api", "lce", "cache"):
+    for unit in ("api", "lce", "cache", "step"):
         jobs.append([nvcc, *ARCH, *flags, "-c", os.path.join(CSRC, unit + ".cu"), "-o", os.path.join(bdir, unit + ".o")])
     checks_obj = os.path.join(bdir, "checks.o")
     if not debug:

@@ -9,8 +9,6 @@
 
 namespace gbattn {
 
-__device__ __forceinline__ int clamp_len(int n, int most) { return n < 0 ? 0 : n > most ? most : n; }
-
 // Elements of a cache buffer (16-byte pieces), for the debug build's checks.
 __device__ __forceinline__ size_t cache_extent(int heads, int64_t pitch, int Lk, int row16) {
   return (static_cast<size_t>(heads - 1) * pitch + Lk) * row16;

@@ -107,6 +107,9 @@ struct BwdParams {
   int* sched;
 };
 
+// A length, limit or count from the device, brought into 0 .. most.
+__device__ __forceinline__ int clamp_len(int n, int most) { return n < 0 ? 0 : n > most ? most : n; }
+
 // fp32 row of 32 values (128 bytes, 16-byte aligned) to global memory, scaled.
 __device__ __forceinline__ void store_row32_f32(float* dst, const uint32_t (&r)[32], float mul) {
   float4* d = reinterpret_cast<float4*>(dst);

@@ -1,0 +1,169 @@
+// The paged cache: new rows into the pages (in 16 bits or quantised to e4m3)
+// and pages back into contiguous rows.  Both are bound by memory traffic and,
+// for a decode step, by latency.
+//
+// Quantised rows.  A row of D values (one token, one KV head, K or V) has one
+// exponent e, the least with max |x| <= 448 * 2^e, and codes c = e4m3(x 2^-e),
+// so x 2^-e is exact and each value is rounded once.  A power of two costs
+// nothing against max / 448 as the scale, since the codes are floating-point
+// (their relative error is the same wherever the row's largest value falls
+// between 224 and 448), and makes reading back exact.
+#pragma once
+
+#include <cuda_fp8.h>
+
+#include "row_lanes.cuh"
+#include "step.h"
+
+namespace gbattn {
+
+// Row number (of D values) of token `at` of sequence b and head h in the pool, or -1 where its page is none.
+__device__ __forceinline__ long long paged_row(const PagedCache& c, int b, int h, int at) {
+  const int page = __ldg(c.table + static_cast<size_t>(b) * c.per_seq + (at >> c.shift));
+  if (page < 0 || page >= c.n_pages) return -1;
+  return ((static_cast<long long>(page) * c.Hkv + h) << c.shift) + (at & ((1 << c.shift) - 1));
+}
+
+// Exponent of a row whose largest finite magnitude is m.
+__device__ __forceinline__ int row_exponent(float m) {
+  // 448 = 1.75 * 2^8; m = f * 2^x with 1 <= f < 2
+  const uint32_t bits = __float_as_uint(m);
+  const int x = static_cast<int>(bits >> 23) - 127;
+  const int e = x - 8 + ((bits & 0x7fffffu) > 0x600000u);
+  return bits < 0x00800000u ? kExpMin : min(max(e, kExpMin), kExpMax);  // (below 2^-126: far under the least exponent)
+}
+
+__device__ __forceinline__ float exp2_int(int e) { return __int_as_float((e + 127) << 23); }
+
+// Two values as e4m3 codes, round to nearest even; what is not finite becomes NaN.
+__device__ __forceinline__ uint32_t e4m3_pair(float a, float b) {
+  uint32_t r = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+  if (!(fabsf(a) < INFINITY)) r |= 0x007fu;
+  if (!(fabsf(b) < INFINITY)) r |= 0x7f00u;
+  return r;
+}
+
+__device__ __forceinline__ float2 e4m3_unpack(uint32_t pair) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(pair), __NV_E4M3);
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
+constexpr int kPagedThreads = 256;
+
+// A row belongs to D / 16 lanes with 16 consecutive values each.  Units: the
+// rows of K, then those of V.
+template <int D, bool BF16, bool Q8>
+__global__ void __launch_bounds__(kPagedThreads) attn_paged_write_kernel(const PagedWriteParams p) {
+  using Gm = RowLanes<D>;
+  grid_dependency_wait();  // the kernels before this one are complete
+  if (threadIdx.x == 0) grid_launch_dependents();
+  const int lane = threadIdx.x & 31, j = lane % Gm::GROUP;
+  const long long rows = static_cast<long long>(p.B) * p.c.Hkv * p.T;
+  const int room = p.c.per_seq << p.c.shift;
+  const long long n_rows = (static_cast<long long>(p.c.n_pages) * p.c.Hkv) << p.c.shift;
+  const long long step = static_cast<long long>(gridDim.x) * (kPagedThreads / Gm::GROUP);
+  const long long first = (static_cast<long long>(blockIdx.x) * kPagedThreads + threadIdx.x) / Gm::GROUP;
+  // whole warps go round together: the shuffles below take every lane
+  for (long long base = first - lane / Gm::GROUP; base < 2 * rows; base += step) {
+    const long long unit = base + lane / Gm::GROUP;
+    const bool is_v = unit >= rows;
+    const long long r = is_v ? unit - rows : unit;  // (b, h, t)
+    const long long bh = r / p.T;
+    const int t = static_cast<int>(r - bh * p.T), b = static_cast<int>(bh / p.c.Hkv), h = static_cast<int>(bh - static_cast<long long>(b) * p.c.Hkv);
+    long long dst = -1;
+    if (unit < 2 * rows) {
+      const int len = clamp_len(__ldg(p.cache_len + b), room);
+      const int n = min(p.new_len ? clamp_len(__ldg(p.new_len + b), p.T) : p.T, room - len);
+      if (t < n) dst = paged_row(p.c, b, h, len + t);
+      if (r == bh * p.T && h == 0 && !is_v && j == 0) p.cache_len_out[b] = len + n;
+    }
+    const bool live = dst >= 0 && j < Gm::LANES && dbg_in_range(dst, 1, n_rows, p.status, 110);
+    uint4 x[2] = {};
+    if (live) {
+      const uint4* src = static_cast<const uint4*>(is_v ? p.v_new : p.k_new) + r * (D / 8) + 2 * j;
+      x[0] = src[0], x[1] = src[1];
+    }
+    if constexpr (!Q8) {
+      if (live) {
+        uint4* d = static_cast<uint4*>(is_v ? p.c.v : p.c.k) + dst * (D / 8) + 2 * j;
+        d[0] = x[0], d[1] = x[1];
+      }
+    } else {
+      float f[16], m = 0.f;
+      unpack8<BF16>(x[0], f), unpack8<BF16>(x[1], f + 8);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) m = fabsf(f[i]) < INFINITY ? fmaxf(m, fabsf(f[i])) : m;
+#pragma unroll
+      for (int k = Gm::GROUP / 2; k; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
+      const int e = row_exponent(m);
+      const float by = exp2_int(-e);
+      uint32_t w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        w[i] = e4m3_pair(f[4 * i] * by, f[4 * i + 1] * by) | e4m3_pair(f[4 * i + 2] * by, f[4 * i + 3] * by) << 16;
+      if (live) {
+        (static_cast<uint4*>(is_v ? p.c.v : p.c.k) + dst * (D / 16))[j] = make_uint4(w[0], w[1], w[2], w[3]);
+        if (j == 0) (is_v ? p.c.v_exp : p.c.k_exp)[dst] = static_cast<int8_t>(e);
+      }
+    }
+  }
+}
+
+// The codes' values in 16 bits; one that rounds past the type's largest value becomes that.
+template <bool BF16>
+__device__ __forceinline__ uint32_t dequant_pair(uint32_t pair, float by) {
+  constexpr float most = BF16 ? 3.3895313892515355e38f : 65504.f;
+  float2 v = e4m3_unpack(pair);
+  v.x *= by, v.y *= by;
+  if (fabsf(v.x) > most) v.x = copysignf(most, v.x);
+  if (fabsf(v.y) > most) v.y = copysignf(most, v.y);
+  return Elem<BF16>::pack(v.x, v.y);
+}
+
+// A block: kReadRows tokens of one sequence and head, K and V; a row belongs to D / 16 lanes.
+constexpr int kReadRows = 64;
+
+template <int D, bool BF16, bool Q8>
+__global__ void __launch_bounds__(kPagedThreads) attn_paged_read_kernel(const PagedReadParams p) {
+  constexpr int LANES = D / 16;
+  __shared__ long long src[kReadRows];
+  grid_dependency_wait();
+  if (threadIdx.x == 0) grid_launch_dependents();
+  const int b = blockIdx.y / p.c.Hkv, h = blockIdx.y - b * p.c.Hkv;
+  const int n = clamp_len(p.cache_len[b], min(p.Lk, p.c.per_seq << p.c.shift));
+  [[maybe_unused]] const long long n_rows = (static_cast<long long>(p.c.n_pages) * p.c.Hkv) << p.c.shift;
+  [[maybe_unused]] const size_t n_out = static_cast<size_t>(p.B * p.c.Hkv - 1) * p.pitch + p.Lk;
+  for (int j0 = blockIdx.x * kReadRows; j0 < n; j0 += gridDim.x * kReadRows) {
+    __syncthreads();
+    if (threadIdx.x < kReadRows) src[threadIdx.x] = j0 + threadIdx.x < n ? paged_row(p.c, b, h, j0 + threadIdx.x) : -1;
+    __syncthreads();
+#pragma unroll 4
+    for (int i = threadIdx.x; i < 2 * kReadRows * LANES; i += kPagedThreads) {
+      const bool is_v = i >= kReadRows * LANES;
+      const int x = is_v ? i - kReadRows * LANES : i, row = x / LANES, c = x - row * LANES;
+      const long long from = src[row];
+      const size_t to = static_cast<size_t>(blockIdx.y) * p.pitch + j0 + row;
+      if (from < 0 || !dbg_in_range(from, 1, n_rows, p.status, 111) || !dbg_in_range(to, 1, n_out, p.status, 112)) continue;
+      uint4* d = static_cast<uint4*>(is_v ? p.v : p.k) + to * (D / 8) + 2 * c;
+      if constexpr (Q8) {
+        const uint4 w = (static_cast<const uint4*>(is_v ? p.c.v : p.c.k) + from * (D / 16))[c];
+        const float by = exp2_int((is_v ? p.c.v_exp : p.c.k_exp)[from]);
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+        uint32_t o[8];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          o[2 * k] = dequant_pair<BF16>(u[k] & 0xffffu, by);
+          o[2 * k + 1] = dequant_pair<BF16>(u[k] >> 16, by);
+        }
+        d[0] = make_uint4(o[0], o[1], o[2], o[3]);
+        d[1] = make_uint4(o[4], o[5], o[6], o[7]);
+      } else {
+        const uint4* s = static_cast<const uint4*>(is_v ? p.c.v : p.c.k) + from * (D / 8) + 2 * c;
+        const uint4 x0 = s[0], x1 = s[1];
+        d[0] = x0, d[1] = x1;
+      }
+    }
+  }
+}
+
+}  // namespace gbattn

@@ -32,7 +32,9 @@ EXPORTED = ("attn_fwd", "attn_bwd_delta", "attn_bwd", "attn_bwd_dq", "attn_bwd_d
             "attn_fwd_decode", "attn_bwd_decode", "attn_last_device_status", "attn_wait_probe", "attn_status_string",
             "lce_workspace_bytes", "lce_fwd", "lce_bwd", "attn_tree_workspace_bytes", "attn_fwd_tree",
             "attn_cache_append", "attn_key_weight_workspace_bytes", "attn_key_weight",
-            "attn_cache_evict_workspace_bytes", "attn_cache_evict")
+            "attn_cache_evict_workspace_bytes", "attn_cache_evict", "attn_qk_norm_rope",
+            "attn_qk_norm_rope_workspace_bytes", "attn_qk_norm_rope_bwd", "attn_paged_write", "attn_paged_read",
+            "attn_paged_workspace_bytes", "attn_fwd_paged", "attn_draft_verify")
 
 _lib = None
 
@@ -106,6 +108,22 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
     lib.attn_cache_evict_workspace_bytes.restype = sz
     lib.attn_cache_evict.argtypes = [vp] * 10 + [sz, i64] + [ci] * 7 + [vp]
     lib.attn_cache_evict.restype = ci
+    lib.attn_qk_norm_rope.argtypes = [vp] * 11 + [ci] * 7 + [cf, ci, ci, vp]
+    lib.attn_qk_norm_rope.restype = ci
+    lib.attn_qk_norm_rope_workspace_bytes.argtypes = [ci]
+    lib.attn_qk_norm_rope_workspace_bytes.restype = sz
+    lib.attn_qk_norm_rope_bwd.argtypes = [vp] * 14 + [sz] + [vp] * 4 + [ci] * 7 + [cf, ci, ci, vp]
+    lib.attn_qk_norm_rope_bwd.restype = ci
+    lib.attn_paged_write.argtypes = [vp] * 10 + [ci] * 8 + [vp]
+    lib.attn_paged_write.restype = ci
+    lib.attn_paged_read.argtypes = [vp] * 8 + [i64] + [ci] * 8 + [vp]
+    lib.attn_paged_read.restype = ci
+    lib.attn_paged_workspace_bytes.argtypes = [ci] * 7
+    lib.attn_paged_workspace_bytes.restype = sz
+    lib.attn_fwd_paged.argtypes = [vp] * 10 + [sz] + [ci] * 8 + [cf, ci, vp]
+    lib.attn_fwd_paged.restype = ci
+    lib.attn_draft_verify.argtypes = [vp] * 8 + [ci] * 3 + [vp]
+    lib.attn_draft_verify.restype = ci
     lib.attn_last_device_status.argtypes = [vp]
     lib.attn_last_device_status.restype = ci
     lib.attn_wait_probe.argtypes = [vp]
@@ -121,6 +139,7 @@ def status_string(status: int) -> str:
 
 
 _F32, _U8, _I32, _BF16, _F16 = torch.float32, torch.uint8, torch.int32, torch.bfloat16, torch.float16
+_I8, _E4M3 = torch.int8, torch.float8_e4m3fn
 
 
 def _dtype_code(t: torch.Tensor) -> int:
@@ -147,17 +166,17 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _require(call: str, dense=(), sliced=(), f32=(), u8=(), i32=()):
+def _require(call: str, dense=(), sliced=(), f32=(), u8=(), i32=(), i8=(), e4m3=()):
     """Reject tensors the C ABI cannot take before any pointer crosses it.
     dense: 16-bit tensors that must be contiguous (one dtype for all of them
     and for `sliced`); sliced: 16-bit tensors whose layout the caller has
-    checked separately (k / v slices of a cache); f32 / u8 / i32: contiguous
-    float32 / uint8 / int32 tensors.  Every tensor must be on the current CUDA
+    checked separately (k / v slices of a cache); f32 / u8 / i32 / i8 / e4m3:
+    contiguous tensors of that type (e4m3: float8_e4m3fn).  Every tensor must be on the current CUDA
     device.  None entries are skipped."""
     half = None
     dev = None
     for ts, want, contig in ((dense, None, True), (sliced, None, False), (f32, _F32, True), (u8, _U8, True),
-                             (i32, _I32, True)):
+                             (i32, _I32, True), (i8, _I8, True), (e4m3, _E4M3, True)):
         for t in ts:
             if t is None:
                 continue
@@ -591,6 +610,195 @@ def attn_cache_evict(k, v, weight, pos, cache_len, seen, weight_out, pos_out, ca
                                          ATTN_DTYPE_BF16 if dt is _BF16 else ATTN_DTYPE_FP16,
                                          _raw_stream(dev) if stream is None else _stream_handle(stream))
     return _check(st, "attn_cache_evict", check)
+
+
+_Strides = ctypes.c_int64 * 3
+
+
+def _row_strides(call: str, t, name: str):
+    """Strides between sequences, heads and tokens of a [B,H,L,D] tensor whose
+    rows are contiguous (a size of 1 has none: 0)."""
+    B, H, L, D = t.shape
+    b, h, n, d = t.stride()
+    if d != 1:
+        raise ValueError(f"{call}: {name} of strides {t.stride()} has no contiguous rows")
+    return _Strides(b if B > 1 else 0, h if H > 1 else D, n if L > 1 else 0)
+
+
+def _rope_args(call, q, k, pos, freq, q_weight, k_weight, axis, dense, rows, f32=()):
+    """Checks what both directions of the rotation read; -> (axes, dtype code)."""
+    B, Hq, L, D = q.shape
+    dt, dev, Hkv, half = q.dtype, q.get_device(), k.shape[1], freq.numel()
+    axes = pos.shape[0] if pos.dim() == 3 else 1
+    at = (axes, B, L) if pos.dim() == 3 else (B, L)
+    if not (dev >= 0 and dev == _current_device() and (dt is _BF16 or dt is _F16) and k.dtype is dt and k.get_device() == dev
+            and k.shape == (B, Hkv, L, D) and _plain(pos, _I32, dev, at) and _plain(freq, _F32, dev, (half,))
+            and (axis is None or _plain(axis, _U8, dev, (half,)))
+            and all(t is None or _plain(t, dt, dev, shape) for t, shape, _ in dense)
+            and all(t.dtype is dt and t.get_device() == dev and t.shape == shape for t, shape, _ in rows)
+            and all(t is None or _plain(t, _F32, dev, (D,)) for t in f32)):
+        _require(call, dense=[t for t, _, _ in dense], sliced=(q, k, *(t for t, _, _ in rows)), f32=(freq, *f32), u8=(axis,), i32=(pos,))
+        _shapes(call, (k, (B, Hkv, L, D), "k"), (pos, at, "pos"), (freq, (half,), "freq"), (axis, (half,), "axis"), *dense, *rows,
+                *((t, (D,), "a weight's gradient") for t in f32))
+    return axes, ATTN_DTYPE_BF16 if dt is _BF16 else ATTN_DTYPE_FP16
+
+
+def attn_qk_norm_rope(q, k, q_out, k_out, pos, freq, q_weight=None, k_weight=None, axis=None, eps: float = 1e-6,
+                      interleaved: bool = False, stream=None, check: bool = True) -> int:
+    """RMS norm of every head's row of q [B,Hq,L,D] and k [B,Hkv,L,D] (with the
+    weights [D]; None: no norm) and its rotation by the token's position (writes
+    the contiguous q_out, k_out).  q and k may be views of a packed projection.
+    pos int32 [B,L] or [axes,B,L]; freq float32 [rot/2]; axis uint8 [rot/2]:
+    which axis each pair turns by (None: the first)."""
+    B, Hq, L, D = q.shape
+    Hkv = k.shape[1]
+    axes, code = _rope_args("attn_qk_norm_rope", q, k, pos, freq, q_weight, k_weight, axis,
+                            ((q_weight, (D,), "q_weight"), (k_weight, (D,), "k_weight"), (q_out, (B, Hq, L, D), "q_out"),
+                             (k_out, (B, Hkv, L, D), "k_out")), ())
+    st = load_library().attn_qk_norm_rope(
+        q.data_ptr(), k.data_ptr(), _ptr(q_weight), _ptr(k_weight), pos.data_ptr(), freq.data_ptr(), _ptr(axis),
+        q_out.data_ptr(), k_out.data_ptr(), _row_strides("attn_qk_norm_rope", q, "q"),
+        _row_strides("attn_qk_norm_rope", k, "k"), B, Hq, Hkv, L, D, 2 * freq.numel(), axes, float(eps),
+        int(bool(interleaved)), code, _raw_stream(q.get_device()) if stream is None else _stream_handle(stream))
+    return _check(st, "attn_qk_norm_rope", check)
+
+
+def attn_qk_norm_rope_workspace_bytes(D: int) -> int:
+    """Bytes of device workspace attn_qk_norm_rope_bwd needs (0: D not served)."""
+    return int(load_library().attn_qk_norm_rope_workspace_bytes(D))
+
+
+def qk_norm_rope_workspace(q, k) -> torch.Tensor:
+    """A workspace tensor for attn_qk_norm_rope_bwd on q and k [B,H,L,D]."""
+    return _workspace(attn_qk_norm_rope_workspace_bytes(q.shape[-1]), "attn_qk_norm_rope_workspace_bytes", q.device)
+
+
+def attn_qk_norm_rope_bwd(q, k, dq_out, dk_out, pos, freq, dq, dk, q_weight, k_weight, dq_weight, dk_weight, workspace,
+                          axis=None, eps: float = 1e-6, interleaved: bool = False, stream=None, check: bool = True) -> int:
+    """Gradients of attn_qk_norm_rope: from dq_out, dk_out (contiguous) writes
+    dq, dk (rows like q's and k's; views of a packed gradient will do) and, with
+    weights, dq_weight, dk_weight (float32 [D]; None without)."""
+    B, Hq, L, D = q.shape
+    Hkv = k.shape[1]
+    axes, code = _rope_args("attn_qk_norm_rope_bwd", q, k, pos, freq, q_weight, k_weight, axis,
+                            ((q_weight, (D,), "q_weight"), (k_weight, (D,), "k_weight"), (dq_out, (B, Hq, L, D), "dq_out"),
+                             (dk_out, (B, Hkv, L, D), "dk_out")),
+                            ((dq, (B, Hq, L, D), "dq"), (dk, (B, Hkv, L, D), "dk")), (dq_weight, dk_weight))
+    if not _plain(workspace, _U8, q.get_device(), workspace.shape):
+        _require("attn_qk_norm_rope_bwd", u8=(workspace,))
+    call = "attn_qk_norm_rope_bwd"
+    st = load_library().attn_qk_norm_rope_bwd(
+        q.data_ptr(), k.data_ptr(), _ptr(q_weight), _ptr(k_weight), pos.data_ptr(), freq.data_ptr(), _ptr(axis),
+        dq_out.data_ptr(), dk_out.data_ptr(), dq.data_ptr(), dk.data_ptr(), _ptr(dq_weight), _ptr(dk_weight),
+        workspace.data_ptr(), workspace.numel(), _row_strides(call, q, "q"), _row_strides(call, k, "k"),
+        _row_strides(call, dq, "dq"), _row_strides(call, dk, "dk"), B, Hq, Hkv, L, D, 2 * freq.numel(), axes, float(eps),
+        int(bool(interleaved)), code, _raw_stream(q.get_device()) if stream is None else _stream_handle(stream))
+    return _check(st, call, check)
+
+
+def _pool_args(call, k_pages, v_pages, table, k_exp, v_exp, x, lens, dense, sliced=(), i32=(), f32=(), u8=()):
+    """Checks a paged cache and what a call on it takes beside it: 16-bit
+    tensors like x (dense, sliced: (tensor, shape, name)), int32 [B] lengths."""
+    n_pages, Hkv, page, D = k_pages.shape
+    B = table.shape[0]
+    dt, dev = x.dtype, x.get_device()
+    held = dt if k_exp is None else _E4M3
+    if not (dev >= 0 and dev == _current_device() and (dt is _BF16 or dt is _F16) and _plain(k_pages, held, dev, k_pages.shape)
+            and _plain(v_pages, held, dev, k_pages.shape) and _plain(table, _I32, dev, (B, table.shape[1]))
+            and (k_exp is None or _plain(k_exp, _I8, dev, (n_pages, Hkv, page)))
+            and (v_exp is None or _plain(v_exp, _I8, dev, (n_pages, Hkv, page)))
+            and all(t is None or _plain(t, _I32, dev, (B,)) for t in lens)
+            and all(_plain(t, dt, dev, shape) for t, shape, _ in dense)
+            and all(t.dtype is dt and t.get_device() == dev and t.shape == shape for t, shape, _ in sliced)
+            and all(_plain(t, _F32, dev, shape) for t, shape, _ in f32) and all(_plain(t, _U8, dev, t.shape) for t in u8)):
+        pools = (k_pages, v_pages)
+        _require(call, dense=(*(t for t, _, _ in dense), *(pools if k_exp is None else ())), sliced=(x, *(t for t, _, _ in sliced)),
+                 f32=[t for t, _, _ in f32], u8=u8, i32=(table, *lens), i8=(k_exp, v_exp), e4m3=() if k_exp is None else pools)
+        _shapes(call, (v_pages, k_pages.shape, "v_pages"), (k_exp, (n_pages, Hkv, page), "k_exp"), (v_exp, (n_pages, Hkv, page), "v_exp"),
+                *((t, (B,), "a length") for t in lens), *dense, *sliced, *f32)
+    if (k_exp is None) != (v_exp is None):
+        raise ValueError(f"{call}: k_exp and v_exp go together")
+    return ATTN_DTYPE_BF16 if dt is _BF16 else ATTN_DTYPE_FP16
+
+
+def attn_paged_write(k_new, v_new, k_pages, v_pages, table, cache_len, cache_len_out, new_len=None, k_exp=None, v_exp=None,
+                     stream=None, check: bool = True) -> int:
+    """New rows k_new, v_new [B,Hkv,T,D] into the pages behind each sequence's
+    cache_len tokens (new_len [B]: how many; None: T); writes cache_len_out.
+    Pages [n,Hkv,page_size,D] of the same type, or float8_e4m3fn with int8
+    exponents k_exp, v_exp [n,Hkv,page_size]; table int32 [B,pages]."""
+    B, Hkv, T, D = k_new.shape
+    n_pages, _, page, _ = k_pages.shape
+    code = _pool_args("attn_paged_write", k_pages, v_pages, table, k_exp, v_exp, k_new, (cache_len, cache_len_out, new_len),
+                      ((k_new, (table.shape[0], k_pages.shape[1], T, k_pages.shape[3]), "k_new"), (v_new, k_new.shape, "v_new")))
+    st = load_library().attn_paged_write(
+        k_new.data_ptr(), v_new.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), _ptr(k_exp), _ptr(v_exp), table.data_ptr(),
+        cache_len.data_ptr(), _ptr(new_len), cache_len_out.data_ptr(), B, Hkv, T, n_pages, page, table.shape[1], D, code,
+        _raw_stream(k_new.get_device()) if stream is None else _stream_handle(stream))
+    return _check(st, "attn_paged_write", check)
+
+
+def attn_paged_read(k_pages, v_pages, table, cache_len, k, v, k_exp=None, v_exp=None, stream=None, check: bool = True) -> int:
+    """The cached tokens of each sequence into contiguous rows k, v [B,Hkv,Lk,D]
+    (or slices of a longer cache, as attn_fwd_ex takes them); rows from the
+    sequence's length on are left as they were."""
+    B, Hkv, Lk, D = k.shape
+    n_pages, _, page, _ = k_pages.shape
+    shape = (table.shape[0], k_pages.shape[1], Lk, k_pages.shape[3])
+    code = _pool_args("attn_paged_read", k_pages, v_pages, table, k_exp, v_exp, k, (cache_len,), (), ((k, shape, "k"), (v, shape, "v")))
+    st = load_library().attn_paged_read(
+        k_pages.data_ptr(), v_pages.data_ptr(), _ptr(k_exp), _ptr(v_exp), table.data_ptr(), cache_len.data_ptr(), k.data_ptr(),
+        v.data_ptr(), kv_row_pitch(k, v), B, Hkv, Lk, n_pages, page, table.shape[1], D, code,
+        _raw_stream(k.get_device()) if stream is None else _stream_handle(stream))
+    return _check(st, "attn_paged_read", check)
+
+
+def attn_paged_workspace_bytes(B: int, Hq: int, Hkv: int, T: int, page_size: int, per_seq: int, D: int) -> int:
+    """Bytes of device workspace attn_fwd_paged needs (0: shape not served)."""
+    return int(load_library().attn_paged_workspace_bytes(B, Hq, Hkv, T, page_size, per_seq, D))
+
+
+def paged_workspace(q, k_pages, table) -> torch.Tensor:
+    """A workspace tensor for attn_fwd_paged on q [B,Hq,T,D] over k_pages [n,Hkv,page_size,D] by table [B,pages]."""
+    B, Hq, T, D = q.shape
+    return _workspace(attn_paged_workspace_bytes(B, Hq, k_pages.shape[1], T, k_pages.shape[2], table.shape[1], D),
+                      "attn_paged_workspace_bytes", q.device)
+
+
+def attn_fwd_paged(q, k_pages, v_pages, table, cache_len, o, lse, workspace, scale: float, k_exp=None, v_exp=None, stream=None,
+                   check: bool = True) -> int:
+    """Attention of each sequence's T newest tokens q [B,Hq,T,D] (one, or a
+    chain) over its pages, which hold them already: cache_len [B] int32 counts
+    them (writes o, lse).  Pages as for attn_paged_write."""
+    B, Hq, T, D = q.shape
+    n_pages, Hkv, page, Dk = k_pages.shape
+    code = _pool_args("attn_fwd_paged", k_pages, v_pages, table, k_exp, v_exp, q, (cache_len,),
+                      ((q, (table.shape[0], Hq, T, Dk), "q"), (o, q.shape, "o")), f32=((lse, (B, Hq, T), "lse"),), u8=(workspace,))
+    st = load_library().attn_fwd_paged(
+        q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), _ptr(k_exp), _ptr(v_exp), table.data_ptr(), cache_len.data_ptr(),
+        o.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.numel(), B, Hq, Hkv, T, n_pages, page, table.shape[1], D,
+        float(scale), code, _raw_stream(q.get_device()) if stream is None else _stream_handle(stream))
+    return _check(st, "attn_fwd_paged", check)
+
+
+def attn_draft_verify(target, draft, tokens, u, r, accept_len, token, draft_len=None, stream=None, check: bool = True) -> int:
+    """Accepts a chain of drafts tokens int32 [B,T] against the target's
+    probabilities float32 [B,T+1,V], draft's [B,T,V] (None: deterministic
+    drafts) and uniform numbers u [B,T], and draws the next token by r [B]
+    (writes accept_len, token: int32 [B])."""
+    B, T = tokens.shape
+    V, dev, lens = target.shape[-1], target.get_device(), (B,)
+    if not (dev >= 0 and dev == _current_device() and _plain(target, _F32, dev, (B, T + 1, V))
+            and (draft is None or _plain(draft, _F32, dev, (B, T, V))) and _plain(tokens, _I32, dev, (B, T))
+            and _plain(u, _F32, dev, (B, T)) and _plain(r, _F32, dev, lens) and _plain(accept_len, _I32, dev, lens)
+            and _plain(token, _I32, dev, lens) and (draft_len is None or _plain(draft_len, _I32, dev, lens))):
+        _require("attn_draft_verify", f32=(target, draft, u, r), i32=(tokens, accept_len, token, draft_len))
+        _shapes("attn_draft_verify", (target, (B, T + 1, V), "target"), (draft, (B, T, V), "draft"), (u, (B, T), "u"), (r, lens, "r"),
+                (accept_len, lens, "accept_len"), (token, lens, "token"), (draft_len, lens, "draft_len"))
+    st = load_library().attn_draft_verify(target.data_ptr(), _ptr(draft), tokens.data_ptr(), u.data_ptr(), r.data_ptr(),
+                                          _ptr(draft_len), accept_len.data_ptr(), token.data_ptr(), B, T, V,
+                                          _raw_stream(dev) if stream is None else _stream_handle(stream))
+    return _check(st, "attn_draft_verify", check)
 
 
 def attn_last_device_status(stream=None) -> int:

@@ -334,6 +334,128 @@ attn_status_t attn_cache_evict(void* k, void* v, const float* weight, const int3
                                int D, int keep, int recent, attn_dtype_t dtype, cudaStream_t stream);
 
 /*
+ * Norm and rotation of queries and keys, in one pass: what a model does to a
+ * projection's rows before it calls attn_fwd, attn_fwd_tree or attn_fwd_paged.
+ *   n = x * w / sqrt(mean_d x_d^2 + eps)   (weights NULL: n = x, no norm),
+ *   then pair i (i < rot/2) of n turns by the angle pos[axis[i]][b][l] * freq[i]:
+ *     (a, b) -> (a cos - b sin, b cos + a sin),
+ *   pairs (i, i + rot/2), or (2i, 2i + 1) with interleaved = 1; elements from
+ *   rot on are not turned.  Everything in float32 (angles exact to far
+ *   positions), one rounding at the end.
+ *   q [B,Hq,L,D], k [B,Hkv,L,D]: inputs (dtype), D contiguous, at q_strides and
+ *     k_strides (HOST arrays of three: elements between sequences, heads and
+ *     tokens; not negative, multiples of 8), so the views of a packed
+ *     projection [B, L, heads, D] need no copy.
+ *   q_weight, k_weight [D] (dtype), both or neither.  eps: finite, >= 0.
+ *   pos int32 [axes,B,L]: positions; one axis for text, several (time, height,
+ *     width, ...) for video.  axis uint8 [rot/2]: which of them pair i turns
+ *     by (values from `axes` on count as axes - 1), NULL: the first.
+ *   freq float32 [rot/2]: radians per position, finite and below 2^22.
+ *   q_out, k_out: outputs (dtype), contiguous [B,H,L,D].  q_out may be q (and
+ *     k_out k) where q is contiguous; no other overlap (ATTN_ERR_INVALID_ARG).
+ *   rot: 16 .. D, a multiple of 16; axes 1 .. 8; B * L <= 2^30 (else ATTN_ERR_UNSUPPORTED).
+ *
+ * attn_qk_norm_rope_bwd: the gradients.  dq_out, dk_out (dtype, contiguous:
+ *   what attn_bwd wrote) are those of the outputs above, dq and dk (dtype, at
+ *   dq_strides and dk_strides, fully written; the views of one packed gradient
+ *   will do) those of q and k, dq_weight and dk_weight float32 [D] those of
+ *   the weights (with them).  No output overlaps an input, another output or
+ *   the workspace (attn_qk_norm_rope_workspace_bytes(D) bytes, one per call in
+ *   flight).  Sums are in a fixed order: the same call gives the same bits.
+ */
+attn_status_t attn_qk_norm_rope(const void* q, const void* k, const void* q_weight, const void* k_weight,
+                                const int32_t* pos, const float* freq, const uint8_t* axis, void* q_out, void* k_out,
+                                const int64_t* q_strides, const int64_t* k_strides, int B, int Hq, int Hkv, int L,
+                                int D, int rot, int axes, float eps, int interleaved, attn_dtype_t dtype,
+                                cudaStream_t stream);
+size_t attn_qk_norm_rope_workspace_bytes(int D);
+attn_status_t attn_qk_norm_rope_bwd(const void* q, const void* k, const void* q_weight, const void* k_weight,
+                                    const int32_t* pos, const float* freq, const uint8_t* axis, const void* dq_out,
+                                    const void* dk_out, void* dq, void* dk, float* dq_weight, float* dk_weight,
+                                    void* workspace, size_t workspace_bytes, const int64_t* q_strides,
+                                    const int64_t* k_strides, const int64_t* dq_strides, const int64_t* dk_strides,
+                                    int B, int Hq, int Hkv, int L, int D, int rot, int axes, float eps,
+                                    int interleaved, attn_dtype_t dtype, cudaStream_t stream);
+
+/*
+ * A paged key/value cache: k_pages, v_pages [n_pages,Hkv,page_size,D], shared
+ * by all sequences; token j of sequence b lies in page table[b][j / page_size],
+ * row j % page_size.  An entry outside 0 .. n_pages - 1 is a hole: nothing is
+ * written to it or read from it.  Two forms:
+ *   16 bits (dtype), k_exp and v_exp NULL;
+ *   8 bits: e4m3 codes and int8 exponents k_exp, v_exp [n_pages,Hkv,page_size]:
+ *     a row's values are code * 2^e, e the least exponent in -64 .. 120 with
+ *     max |x| <= 448 * 2^e, codes rounded to nearest even.  A value that is
+ *     not finite becomes NaN and does not count for e.
+ * Every page that a call writes belongs to one sequence and place only (else
+ * which value stays is undefined); reads may share pages.
+ *   table int32 [B,per_seq], cache_len int32 [B]: device memory; lengths are
+ *   brought into 0 .. per_seq * page_size.
+ *   page_size: a power of two, 8 .. 4096; per_seq * page_size <= 2^30;
+ *   B <= 1024 (else ATTN_ERR_UNSUPPORTED).
+ *
+ * attn_paged_write: rows i < n of k_new, v_new [B,Hkv,T,D] (dtype, contiguous)
+ *   become tokens cache_len[b] + i; n = new_len[b] (NULL: T), cut at 0, T and
+ *   the end of the table.  cache_len_out [B] = cache_len + n.
+ * attn_paged_read: tokens j < min(cache_len[b], Lk) into rows j of k, v
+ *   [B,Hkv,Lk,D] (dtype, kv_pitch rows between heads as in attn_fwd_ex, 0 =
+ *   Lk), as attn_fwd_ex takes them for a prompt over a cached prefix.  Other
+ *   rows, and those whose page is a hole, are left as they were.  Quantised
+ *   values are rounded to dtype (past its largest value: that value).
+ * attn_fwd_paged: attention of each sequence's T newest tokens, whose keys and
+ *   values are in the cache already (cache_len counts them): row t sees the
+ *   tokens j <= cache_len[b] - T + t that no hole hides.
+ *   q [B,Hq,T,D], o likewise (dtype), lse float32 [B,Hq,T], base 2; a row that
+ *   sees nothing gets O = 0 and lse = +inf.  Rows of pages that hold no token
+ *   of the sequence do not influence the result, whatever they hold.  A
+ *   non-finite key reaches the rows that see it, a non-finite value every row
+ *   of its sequence.  G * T <= 128 (else ATTN_ERR_UNSUPPORTED; longer prompts
+ *   take attn_paged_read and attn_fwd_ex).
+ *   workspace: attn_paged_workspace_bytes(...) bytes, one per call in flight; 0
+ *   there means the shape is rejected.
+ * No output (pages that a call writes among them) overlaps an input or another
+ * output (ATTN_ERR_INVALID_ARG).  16-byte alignment, exponents 4-byte.
+ */
+attn_status_t attn_paged_write(const void* k_new, const void* v_new, void* k_pages, void* v_pages, int8_t* k_exp,
+                               int8_t* v_exp, const int32_t* table, const int32_t* cache_len, const int32_t* new_len,
+                               int32_t* cache_len_out, int B, int Hkv, int T, int n_pages, int page_size, int per_seq,
+                               int D, attn_dtype_t dtype, cudaStream_t stream);
+attn_status_t attn_paged_read(const void* k_pages, const void* v_pages, const int8_t* k_exp, const int8_t* v_exp,
+                              const int32_t* table, const int32_t* cache_len, void* k, void* v, int64_t kv_pitch,
+                              int B, int Hkv, int Lk, int n_pages, int page_size, int per_seq, int D,
+                              attn_dtype_t dtype, cudaStream_t stream);
+size_t attn_paged_workspace_bytes(int B, int Hq, int Hkv, int T, int page_size, int per_seq, int D);
+attn_status_t attn_fwd_paged(const void* q, const void* k_pages, const void* v_pages, const int8_t* k_exp,
+                             const int8_t* v_exp, const int32_t* table, const int32_t* cache_len, void* o, float* lse,
+                             void* workspace, size_t workspace_bytes, int B, int Hq, int Hkv, int T, int n_pages,
+                             int page_size, int per_seq, int D, float scale, attn_dtype_t dtype, cudaStream_t stream);
+
+/*
+ * Verification of a chain of drafted tokens against the target model, from
+ * given uniform numbers: what decides the accept_len that attn_cache_append
+ * (or the length of a paged cache) goes by.
+ *   target float32 [B,T+1,V]: the target's probabilities after the context and
+ *     each draft; draft float32 [B,T,V]: those that draft i was drawn from, or
+ *     NULL for deterministic drafts (probability 1 at the draft).
+ *   tokens int32 [B,T]; draft_len int32 [B] or NULL (T for all; brought into 0..T).
+ *   u float32 [B,T], r float32 [B]: uniform in [0, 1).
+ *   Draft i is accepted if u_i * draft_i(x_i) < target_i(x_i) and all before
+ *   it are (a token outside 0..V-1 never is); accept_len [B] is their number n.
+ *   token [B]: the next token, drawn from w = max(target_n - draft_n, 0) where
+ *   draft n was rejected (from target_n if nothing is left of it), from
+ *   target_n where none was: the least x with sum_{y<=x} w_y > r * sum w, -1 if
+ *   all are 0.  Probabilities count in multiples of 2^-60, those below 0 and
+ *   NaN as 0, those above 1 as 1; a row's sum is below 16.  Sums are exact.
+ *   T <= 1024, B <= 65535, V <= 2^30 (else ATTN_ERR_UNSUPPORTED).  No output
+ *   overlaps an input or the other output (ATTN_ERR_INVALID_ARG).  target and
+ *   draft 16-byte aligned, the others 4-byte.
+ * These calls can be captured and replayed, as the serving calls above.
+ */
+attn_status_t attn_draft_verify(const float* target, const float* draft, const int32_t* tokens, const float* u,
+                                const float* r, const int32_t* draft_len, int32_t* accept_len, int32_t* token, int B,
+                                int T, int V, cudaStream_t stream);
+
+/*
  * attn_bwd for callers that cannot allocate device memory.  (The pages have no
  * counterpart: this is an entry point of this library only.)
  *
