@@ -9,8 +9,7 @@
 // Bound by memory traffic: 40 heads x 8192 tokens, D = 128 are 168 MB forward
 // and 252 MB backward.  A row belongs to D / 16 lanes, each with two 16-byte
 // pieces that hold both members of its eight pairs, so the rotation needs no
-// exchange and the norm's sums take log2(D / 16) shuffles.  A lane keeps its
-// token's eight sines and cosines in registers over all heads it works on.
+// exchange and the norm's sums take log2(D / 16) shuffles.
 //
 // Angles.  pos * freq of a far position loses its fraction in 32 bits (2^20
 // radians leave 4 bits behind the point), so freq is taken once per CTA as a
@@ -62,20 +61,26 @@ __device__ __forceinline__ void rotate16(float (&f)[16], const float (&c)[8], co
   }
 }
 
-// Units of work: a token and ROWS * per heads of q, then those of k.  `per` is
-// the heads a lane goes through with one set of sines.
+// A CTA takes an equal share of the tokens (and, where there are fewer tokens
+// than CTAs, of the heads) in chunks of up to kRopeChunk: the chunk's sines and
+// cosines go to shared memory once, then its rows (head by head, the chunk's
+// tokens of each) go round the CTA's groups of lanes, each row loaded while the
+// one before it is worked on.
+constexpr int kRopeChunk = 8;
+
 template <int D, bool BF16, bool INTERLEAVED, bool BWD>
-__global__ void __launch_bounds__(kRopeThreads, BWD ? 2 : 3) rope_kernel(const RopeParams p, int per) {
+__global__ void __launch_bounds__(kRopeThreads, BWD ? kRopeBwdPerSm : kRopeFwdPerSm) rope_kernel(const RopeParams p, int parts) {
   using Gm = RowLanes<D>;
+  constexpr int GROUPS = kRopeThreads / Gm::GROUP, WARPS = kRopeThreads / 32;
   __shared__ uint64_t frac[D / 2];
-  __shared__ float dw_sum[BWD ? kRopeThreads / 32 : 1][BWD ? D : 1];
+  __shared__ __align__(16) float cs[kRopeChunk][2][D / 2];  // cosines, sines
+  __shared__ float dw_sum[BWD ? WARPS : 1][BWD ? D : 1];
   grid_dependency_wait();  // the kernels before this one are complete
   if (threadIdx.x == 0) grid_launch_dependents();
   const int half = p.rot / 2;
   for (int i = threadIdx.x; i < D / 2; i += kRopeThreads) frac[i] = i < half ? turn_fraction(p.freq[i]) : 0;
-  __syncthreads();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int j = lane % Gm::GROUP, row = lane / Gm::GROUP;
+  const int j = lane % Gm::GROUP, group = threadIdx.x / Gm::GROUP;
   const bool on = j < Gm::LANES;
   // The lane's pieces (8 elements each).  Halves: both members of the pairs 8 j ..
   // 8 j + 7, and what is not turned in equal shares; interleaved: any two.
@@ -89,12 +94,19 @@ __global__ void __launch_bounds__(kRopeThreads, BWD ? 2 : 3) rope_kernel(const R
     c0 = j;
     c1 = j + turned;
   }
+  // the first of its pairs in each half of the eight; pairs that are not turned have cosine 1, sine 0
+  const int pair0 = INTERLEAVED ? 4 * c0 : 8 * j, pair1 = INTERLEAVED ? 4 * c1 : 8 * j + 4;
+  const bool turns0 = on && pair0 < half, turns1 = on && pair1 < half;
+  const bool norm = p.w[0] != nullptr;
   const long long tokens = static_cast<long long>(p.B) * p.L;
-  const long long n_warps = static_cast<long long>(gridDim.x) * (kRopeThreads / 32);
+  const int part = blockIdx.x % parts;
+  const long long block = blockIdx.x / parts, blocks = gridDim.x / parts;
+  const long long t_first = tokens * block / blocks, t_end = tokens * (block + 1) / blocks;
 #pragma unroll 1
   for (int which = 0; which < 2; ++which) {
-    const int H = p.x[which].H, step = Gm::ROWS * per, blocks = (H + step - 1) / step;
-    const bool norm = p.w[which] != nullptr;
+    const RowsView xv = p.x[which], dv = p.dx[which];
+    uint16_t* const y = static_cast<uint16_t*>(p.y[which]);
+    const int H = xv.H, h_lo = H * part / parts, h_hi = H * (part + 1) / parts;
     uint4 wp[2] = {};
     if (norm && on) {
       const uint4* w = static_cast<const uint4*>(p.w[which]);
@@ -104,42 +116,67 @@ __global__ void __launch_bounds__(kRopeThreads, BWD ? 2 : 3) rope_kernel(const R
 #pragma unroll
     for (float& x : dw) x = 0.f;
 #pragma unroll 1
-    for (long long unit = static_cast<long long>(blockIdx.x) * (kRopeThreads / 32) + warp; unit < tokens * blocks;
-         unit += n_warps) {
-      const long long token = unit / blocks;
-      const int hb = static_cast<int>(unit - token * blocks);
+    for (long long t0 = t_first; t0 < t_end; t0 += kRopeChunk) {
+      // the chunk: n tokens, rows in slots of 2^shift per head
+      const int n = static_cast<int>(t_end - t0 < kRopeChunk ? t_end - t0 : kRopeChunk);
+      const int shift = n > 4 ? 3 : n > 2 ? 2 : n > 1 ? 1 : 0;
+      const int t = group & ((1 << shift) - 1), stride = GROUPS >> shift;  // a group's rows are all of one token
+      const long long token = t0 + t;
       const int b = static_cast<int>(token / p.L), l = static_cast<int>(token - static_cast<long long>(b) * p.L);
-      const int h0 = hb * step + row;
-      const uint16_t* xrow = static_cast<const uint16_t*>(p.x[which].at) + b * p.x[which].sb + l * p.x[which].sl;
-      const size_t y0 = (static_cast<size_t>(b) * H * p.L + l) * D;
-      [[maybe_unused]] const size_t n_x = (p.B - 1) * p.x[which].sb + (H - 1) * p.x[which].sh + (p.L - 1) * p.x[which].sl + D;
-      [[maybe_unused]] const size_t n_y = static_cast<size_t>(p.B) * H * p.L * D;
-      float c[8], s[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int pair = INTERLEAVED ? (i < 4 ? 4 * c0 + i : 4 * c1 + i - 4) : 8 * j + i;
-        c[i] = 1.f, s[i] = 0.f;
-        if (on && pair < half) {
-          int a = p.axis ? p.axis[pair] : 0;
-          a = a < p.axes ? a : p.axes - 1;
-          turn(__ldg(p.pos + a * tokens + token), frac[pair], c[i], s[i]);
-          if (BWD) s[i] = -s[i];
+      const int h0 = h_lo + (group >> shift);  // the group's first head
+      const int rows = t < n && on && h0 < h_hi ? (h_hi - h0 + stride - 1) / stride : 0;  // of this lane
+      const int rounds = (h_hi - h_lo + stride - 1) / stride;  // of the CTA: the shuffles take whole warps
+      const uint16_t* xr = static_cast<const uint16_t*>(xv.at) + b * xv.sb + l * xv.sl + h0 * xv.sh;
+      uint16_t* yr = y + ((static_cast<size_t>(b) * H + h0) * p.L + l) * D;
+      uint16_t* dr = BWD ? static_cast<uint16_t*>(dv.at) + b * dv.sb + l * dv.sl + h0 * dv.sh : nullptr;
+      const int64_t step_x = stride * xv.sh, step_y = static_cast<int64_t>(stride) * p.L * D, step_d = stride * dv.sh;
+      auto inside = [&](const uint16_t* at, const RowsView& v, int site) {
+        return dbg_in_range(at - static_cast<const uint16_t*>(v.at), D, (p.B - 1) * v.sb + (v.H - 1) * v.sh + (p.L - 1) * v.sl + D, p.status, site);
+      };
+      auto inside_y = [&](const uint16_t* at, int site) {
+        return dbg_in_range(at - y, D, static_cast<size_t>(p.B) * H * p.L * D, p.status, site);
+      };
+      uint4 xn[2] = {}, gn[2] = {};
+      auto load = [&](int i) {  // row i, at xr (and yr)
+        if (i >= rows) return;
+        if ((!BWD || norm) && inside(xr, xv, 100)) {
+          const uint4* v = reinterpret_cast<const uint4*>(xr);
+          xn[0] = v[c0], xn[1] = v[c1];
         }
+        if (BWD && inside_y(yr, 101)) {
+          const uint4* v = reinterpret_cast<const uint4*>(yr);
+          gn[0] = v[c0], gn[1] = v[c1];
+        }
+      };
+      load(0);
+      __syncthreads();  // frac; the chunk before is done with cs
+      for (int i = threadIdx.x; i < n * half; i += kRopeThreads) {
+        const int ti = i / half, pair = i - ti * half;
+        int a = p.axis ? __ldg(p.axis + pair) : 0;
+        a = a < p.axes ? a : p.axes - 1;
+        float c, s;
+        turn(__ldg(p.pos + a * tokens + t0 + ti), frac[pair], c, s);
+        cs[ti][0][pair] = c, cs[ti][1][pair] = BWD ? -s : s;
       }
-#pragma unroll 2
-      for (int i = 0; i < per; ++i) {
-        const int h = h0 + i * Gm::ROWS;
-        const bool live = on && h < H;
-        const size_t xo = xrow - static_cast<const uint16_t*>(p.x[which].at) + h * p.x[which].sh;
-        const size_t yo = y0 + static_cast<size_t>(h) * p.L * D;
-        uint4 xp[2] = {}, gp[2] = {};
-        if (live && (!BWD || norm) && dbg_in_range(xo, D, n_x, p.status, 100)) {
-          const uint4* x = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.x[which].at) + xo);
-          xp[0] = x[c0], xp[1] = x[c1];
-        }
-        if (BWD && live && dbg_in_range(yo, D, n_y, p.status, 101)) {
-          const uint4* g = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.y[which]) + yo);
-          gp[0] = g[c0], gp[1] = g[c1];
+      __syncthreads();
+#pragma unroll 1
+      for (int i = 0; i < rounds; ++i) {
+        const bool live = i < rows;
+        uint4 xp[2] = {xn[0], xn[1]}, gp[2] = {gn[0], gn[1]};
+        xr += step_x;
+        uint16_t* const yi = yr;
+        yr += step_y;
+        load(i + 1);
+        float c[8], s[8];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          float4 cv = make_float4(1.f, 1.f, 1.f, 1.f), sv = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (k ? turns1 : turns0) {
+            cv = *reinterpret_cast<const float4*>(&cs[t][0][k ? pair1 : pair0]);
+            sv = *reinterpret_cast<const float4*>(&cs[t][1][k ? pair1 : pair0]);
+          }
+          c[4 * k] = cv.x, c[4 * k + 1] = cv.y, c[4 * k + 2] = cv.z, c[4 * k + 3] = cv.w;
+          s[4 * k] = sv.x, s[4 * k + 1] = sv.y, s[4 * k + 2] = sv.z, s[4 * k + 3] = sv.w;
         }
         float f[16];
         if constexpr (!BWD) {
@@ -155,33 +192,35 @@ __global__ void __launch_bounds__(kRopeThreads, BWD ? 2 : 3) rope_kernel(const R
             for (int e = 0; e < 16; ++e) f[e] *= r * w[e];
           }
           rotate16<INTERLEAVED>(f, c, s);
-          if (live && dbg_in_range(yo, D, n_y, p.status, 102)) {
-            uint4* y = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.y[which]) + yo);
-            y[c0] = pack8<BF16>(f), y[c1] = pack8<BF16>(f + 8);
+          if (live && inside_y(yi, 102)) {
+            uint4* v = reinterpret_cast<uint4*>(yi);
+            v[c0] = pack8<BF16>(f), v[c1] = pack8<BF16>(f + 8);
           }
         } else {
           unpack8<BF16>(gp[0], f), unpack8<BF16>(gp[1], f + 8);
           rotate16<INTERLEAVED>(f, c, s);
           if (norm) {
-            float x[16], w[16], ss = 0.f, gx = 0.f;
+            float x[16], ss = 0.f, gx = 0.f;
             unpack8<BF16>(xp[0], x), unpack8<BF16>(xp[1], x + 8);
+            float w[16];
             unpack8<BF16>(wp[0], w), unpack8<BF16>(wp[1], w + 8);
 #pragma unroll
             for (int e = 0; e < 16; ++e) ss = fmaf(x[e], x[e], ss), gx = fmaf(f[e] * w[e], x[e], gx);
             const float r = rsqrtf(group_sum<Gm::GROUP>(ss) * (1.f / D) + p.eps);
             const float m = group_sum<Gm::GROUP>(gx) * (1.f / D) * r * r;
+            if (live) {  // (what an idle lane's registers hold adds nothing)
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              dw[e] = fmaf(f[e] * r, x[e], dw[e]);
-              f[e] = r * (f[e] * w[e] - x[e] * m);
+              for (int e = 0; e < 16; ++e) {
+                dw[e] = fmaf(f[e] * r, x[e], dw[e]);
+                f[e] = r * (f[e] * w[e] - x[e] * m);
+              }
             }
           }
-          const size_t dxo = b * p.dx[which].sb + l * p.dx[which].sl + h * p.dx[which].sh;
-          if (live && dbg_in_range(dxo, D, (p.B - 1) * p.dx[which].sb + (H - 1) * p.dx[which].sh +
-                                               (p.L - 1) * p.dx[which].sl + D, p.status, 103)) {
-            uint4* d = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.dx[which].at) + dxo);
-            d[c0] = pack8<BF16>(f), d[c1] = pack8<BF16>(f + 8);
+          if (live && inside(dr, dv, 103)) {
+            uint4* v = reinterpret_cast<uint4*>(dr);
+            v[c0] = pack8<BF16>(f), v[c1] = pack8<BF16>(f + 8);
           }
+          dr += step_d;
         }
       }
     }
@@ -193,7 +232,7 @@ __global__ void __launch_bounds__(kRopeThreads, BWD ? 2 : 3) rope_kernel(const R
 #pragma unroll
         for (int m = Gm::GROUP; m < 32; m <<= 1) dw[e] += __shfl_xor_sync(0xffffffffu, dw[e], m);
       __syncthreads();
-      if (row == 0 && on) {
+      if (lane < Gm::GROUP && on) {
 #pragma unroll
         for (int e = 0; e < 16; ++e) dw_sum[warp][(e < 8 ? c0 : c1) * 8 + (e & 7)] = dw[e];
       }
@@ -201,7 +240,7 @@ __global__ void __launch_bounds__(kRopeThreads, BWD ? 2 : 3) rope_kernel(const R
       for (int d = threadIdx.x; d < D; d += kRopeThreads) {
         float x = 0.f;
 #pragma unroll
-        for (int w = 0; w < kRopeThreads / 32; ++w) x += dw_sum[w][d];
+        for (int w = 0; w < WARPS; ++w) x += dw_sum[w][d];
         p.part[(static_cast<size_t>(blockIdx.x) * 2 + which) * D + d] = x;
       }
     }

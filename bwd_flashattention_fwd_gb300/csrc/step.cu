@@ -13,11 +13,12 @@
 namespace gbattn {
 namespace {
 
-constexpr int kRopeFwdPerSm = 3, kRopeBwdPerSm = 2;  // CTAs of rope_kernel on an SM
-
-// Rows [B, H, L, D] at strides: none negative, each a multiple of 8 elements (16 bytes).
-attn_status_t check_strides(const int64_t* st) {
+// Rows [B, H, L, D] at strides: none negative, each a multiple of 8 elements
+// (16 bytes); a size of 1 has no stride.
+attn_status_t check_strides(const int64_t* st, int B, int H, int L) {
+  const int size[3] = {B, H, L};
   for (int i = 0; i < 3; ++i) {
+    if (size[i] == 1) continue;
     if (st[i] < 0 || st[i] % 8 != 0) return ATTN_ERR_INVALID_ARG;
     if (st[i] > (int64_t{1} << 40)) return ATTN_ERR_UNSUPPORTED;
   }
@@ -79,21 +80,19 @@ attn_status_t check_rope(const void* q, const void* k, const void* qw, const voi
   if (!supported_d(D) || rot % 16 != 0 || axes > kRopeMaxAxes) return ATTN_ERR_UNSUPPORTED;
   // units of work and rows are counted in 32 bits beside a token's number
   if (static_cast<long long>(B) * L > (1 << 30) || Hq > 65535 || Hkv > 65535) return ATTN_ERR_UNSUPPORTED;
-  const attn_status_t a = check_strides(qs), b = check_strides(ks);
+  const attn_status_t a = check_strides(qs, B, Hq, L), b = check_strides(ks, B, Hkv, L);
   return a != ATTN_OK ? a : b;
 }
 
 template <int D, bool BF16, bool INTERLEAVED, bool BWD>
 int rope_impl(const RopeParams& p, int num_sms, cudaStream_t stream) {
-  constexpr int rows = RowLanes<D>::ROWS, warps = kRopeThreads / 32;
   const int sms = num_sms < kTreeMaxCtas ? num_sms : kTreeMaxCtas;
   const long long tokens = static_cast<long long>(p.B) * p.L, most = static_cast<long long>(BWD ? kRopeBwdPerSm : kRopeFwdPerSm) * sms;
-  // heads per lane: as many as leave every warp a unit (sines are taken once per unit)
-  int per = 1;
-  while (per < 8 && per * rows < p.x[0].H && tokens * ((p.x[0].H + 2 * per * rows - 1) / (2 * per * rows)) >= most * warps) per *= 2;
-  const long long units = tokens * ((p.x[0].H + per * rows - 1) / (per * rows)), ctas = (units + warps - 1) / warps;
-  const int grid = static_cast<int>(ctas < most ? ctas : most);
-  const int r = launch_dependent(rope_kernel<D, BF16, INTERLEAVED, BWD>, dim3(grid), kRopeThreads, 0, stream, p, per);
+  // few tokens: their heads are shared out too, one round of the CTA's groups at least
+  constexpr int groups = kRopeThreads / RowLanes<D>::GROUP;
+  const int blocks = static_cast<int>(tokens < most ? tokens : most), heads = (p.x[0].H + groups - 1) / groups;
+  const int parts = most / blocks < heads ? static_cast<int>(most / blocks) : heads, grid = blocks * parts;
+  const int r = launch_dependent(rope_kernel<D, BF16, INTERLEAVED, BWD>, dim3(grid), kRopeThreads, 0, stream, p, parts);
   if (r != kLaunchOk || !BWD || !p.w[0]) return r;
   return launch_dependent(rope_dw_kernel, dim3(2 * D / 32), 256, 0, stream, p, grid);
 }
@@ -244,8 +243,8 @@ extern "C" attn_status_t attn_qk_norm_rope_bwd(const void* q, const void* k, con
   attn_status_t s = check_rope(q, k, q_weight, k_weight, pos, freq, dq_out, dk_out, q_strides, k_strides, B, Hq, Hkv, L,
                                D, rot, axes, eps, interleaved, dtype);
   if (s != ATTN_OK) return s;
-  s = check_strides(dq_strides);
-  if (s == ATTN_OK) s = check_strides(dk_strides);
+  s = check_strides(dq_strides, B, Hq, L);
+  if (s == ATTN_OK) s = check_strides(dk_strides, B, Hkv, L);
   if (s != ATTN_OK) return s;
   if (workspace_bytes < attn_qk_norm_rope_workspace_bytes(D)) return ATTN_ERR_INVALID_ARG;
   if (!disjoint_rows(B, Hq, L, D, dq_strides) || !disjoint_rows(B, Hkv, L, D, dk_strides)) return ATTN_ERR_INVALID_ARG;

@@ -15,6 +15,7 @@ struct RowsView {
 };
 
 constexpr int kRopeThreads = 256;
+constexpr int kRopeFwdPerSm = 3, kRopeBwdPerSm = 2;  // CTAs of rope_kernel on an SM
 constexpr int kRopeMaxAxes = 8;
 
 struct RopeParams {

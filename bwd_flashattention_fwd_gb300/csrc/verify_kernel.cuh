@@ -12,8 +12,8 @@
 //
 // The token is a comparison of sums of up to 10^5 terms with a threshold
 // between them, so the sums are exact: probabilities are taken as multiples of
-// 2^-60 in 64-bit integers, whose sum depends on no order.  (32-bit floating
-// sums choose another token in a few draws out of a hundred; 64-bit floating
+// 2^-45 in integers, whose sum depends on no order.  (32-bit floating sums
+// choose another token in a few draws out of a hundred; 64-bit floating
 // additions would take 25 us at 64 sequences on this GPU.)
 #pragma once
 
@@ -25,22 +25,31 @@ namespace gbattn {
 constexpr int kVerifyThreads = 512;
 constexpr int kVerifyCluster = 8;
 
-// floor(x 2^60) of a probability; what is negative or NaN counts as 0, what is above 1 as 1.
-__device__ __forceinline__ uint64_t prob_fixed(float x) {
-  if (!(x > 0.f)) return 0;
-  x = fminf(x, 1.f);
-  const uint32_t bits = __float_as_uint(x);
-  const int s = static_cast<int>(bits >> 23) - 90;
-  const uint32_t m = (bits & 0x7fffffu) | 0x800000u;
-  return s >= 0 ? static_cast<uint64_t>(m) << s : static_cast<uint64_t>(m >> min(-s, 31));
+// A probability as hi 2^-22 + lo 2^-45, both read off the bits of a float that a
+// constant pushes into a known binade (so the constants' bits belong to hi and
+// lo: differences of two are free of them).  What is negative or NaN counts as
+// 0, what is above 1 as 1; the nearest multiple of 2^-45, so a larger probability never
+// becomes the smaller one.
+struct Fixed {
+  int hi, lo;
+};
+__device__ __forceinline__ Fixed prob_fixed(float x) {
+  x = __saturatef(x);
+  const float a = __fadd_rn(x, 3.f), rest = __fsub_rn(x, __fsub_rn(a, 3.f));
+  return {__float_as_int(a), __float_as_int(__fmaf_rn(rest, 4194304.f, 1.5f))};
 }
 
-// The weight of a token: its probability, less the draft's where one was rejected (lost: the point where a
-// deterministic draft's whole probability lies, or -1).
-__device__ __forceinline__ uint64_t residual(float p, float q, bool lost) {
-  const uint64_t a = prob_fixed(p), b = prob_fixed(q);
-  return lost || a <= b ? 0 : a - b;
-}
+// A sum of a few weights max(p - q, 0), in multiples of 2^-45 (32 bits hold 256 terms).
+struct FixedSum {
+  int hi = 0, lo = 0;
+  __device__ __forceinline__ void add(float p, float q, bool lost) {
+    const Fixed a = prob_fixed(p), b = prob_fixed(q);
+    if (p > q && !lost) hi += a.hi - b.hi, lo += a.lo - b.lo;
+  }
+  __device__ __forceinline__ uint64_t value() const {
+    return static_cast<uint64_t>(static_cast<long long>(hi) * (1 << 23) + lo);
+  }
+};
 
 __device__ __forceinline__ uint64_t warp_sum(uint64_t x) {
 #pragma unroll
@@ -56,16 +65,19 @@ __device__ __forceinline__ uint64_t ld_cluster_u64(uint32_t addr) {
 
 // A cluster per sequence; warp w of CTA c holds a contiguous part of the vocabulary.  VEC: rows start on 16 bytes.
 template <bool VEC>
-__global__ void __launch_bounds__(kVerifyThreads) attn_draft_verify_kernel(const VerifyParams p) {
-  constexpr int WARPS = kVerifyThreads / 32, W = VEC ? 4 : 1;
+__global__ void __launch_bounds__(kVerifyThreads, 3) attn_draft_verify_kernel(const VerifyParams p) {
+  constexpr int WARPS = kVerifyThreads / 32, W = VEC ? 4 : 1, STEP = 32 * W;
   __shared__ int cut;
   __shared__ uint64_t part[2][WARPS];  // sums of this CTA's warps (second row: of p alone, where the residual is empty)
+  __shared__ uint64_t piece[WARPS];
+  __shared__ int chosen;  // the warp whose part holds the token, or -1
+  __shared__ uint64_t chosen_before;
   grid_dependency_wait();
   if (threadIdx.x == 0) grid_launch_dependents();
   const int b = blockIdx.x / kVerifyCluster, c = blockIdx.x % kVerifyCluster;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int most = p.draft_len ? clamp_len(p.draft_len[b], p.T) : p.T;
-  if (threadIdx.x == 0) cut = most;
+  if (threadIdx.x == 0) cut = most, chosen = -1;
   __syncthreads();
   for (int i = threadIdx.x; i < most; i += kVerifyThreads) {
     const int x = p.tokens[static_cast<size_t>(b) * p.T + i];
@@ -85,40 +97,62 @@ __global__ void __launch_bounds__(kVerifyThreads) attn_draft_verify_kernel(const
   const float* qrow = rejected && p.draft ? p.draft + (static_cast<size_t>(b) * p.T + n) * p.V : nullptr;
   const int point = rejected && !p.draft ? p.tokens[static_cast<size_t>(b) * p.T + n] : -1;
   // parts: multiples of 32 W tokens
-  const int per = ((p.V + kVerifyCluster * WARPS - 1) / (kVerifyCluster * WARPS) + 32 * W - 1) / (32 * W) * (32 * W);
-  const long long lo = static_cast<long long>(c * WARPS + warp) * per;
-  const int from = static_cast<int>(lo < p.V ? lo : p.V), to = static_cast<int>(lo + per < p.V ? lo + per : p.V);
+  const int per = ((p.V + kVerifyCluster * WARPS - 1) / (kVerifyCluster * WARPS) + STEP - 1) / STEP * STEP;
+  auto bound = [&](int w) {  // where warp w's part begins (of all warps of the cluster)
+    const long long at = static_cast<long long>(w) * per;
+    return static_cast<int>(at < p.V ? at : p.V);
+  };
 
-  auto load = [&](int x, float (&a)[W], float (&q)[W]) {  // tokens x .. x + W - 1 of this lane (zeros past the part)
+  auto load = [&](int x, int to, bool with_q, float (&a)[W], float (&q)[W]) {  // this lane's tokens x .. (zeros from `to` on)
 #pragma unroll
     for (int k = 0; k < W; ++k) a[k] = q[k] = 0.f;
     if (x >= to) return;
     if constexpr (VEC) {
       const float4 v = __ldg(reinterpret_cast<const float4*>(prow + x));
       a[0] = v.x, a[1] = v.y, a[2] = v.z, a[3] = v.w;
-      if (qrow) {
+      if (with_q) {
         const float4 w = __ldg(reinterpret_cast<const float4*>(qrow + x));
         q[0] = w.x, q[1] = w.y, q[2] = w.z, q[3] = w.w;
       }
     } else {
       a[0] = __ldg(prow + x);
-      if (qrow) q[0] = __ldg(qrow + x);
+      if (with_q) q[0] = __ldg(qrow + x);
     }
   };
-
-  uint64_t sum = 0;
-#pragma unroll 4
-  for (int x = from + lane * W; x < to; x += 32 * W) {
-    float a[W], q[W];
-    load(x, a, q);
+  auto sum_of = [&](int from, int to, bool with_q, int without) {  // this lane's share of a part
+    uint64_t sum = 0;
+    int x = from + lane * W;
+    constexpr int N = VEC ? 2 : 8;  // steps whose loads are in flight together
+    for (; x + (N - 1) * STEP < to; x += N * STEP) {
+      float a[N][W], q[N][W];
 #pragma unroll
-    for (int k = 0; k < W; ++k) sum += residual(a[k], q[k], x + k == point);
-  }
-  sum = warp_sum(sum);
+      for (int i = 0; i < N; ++i) load(x + i * STEP, to, with_q, a[i], q[i]);
+      FixedSum s;
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int k = 0; k < W; ++k) s.add(a[i][k], q[i][k], x + i * STEP + k == without);
+      sum += s.value();
+    }
+    for (; x < to; x += STEP) {
+      float a[W], q[W];
+      load(x, to, with_q, a, q);
+      FixedSum s;
+#pragma unroll
+      for (int k = 0; k < W; ++k) s.add(a[k], q[k], x + k == without);
+      sum += s.value();
+    }
+    return sum;
+  };
+
+  const int mine = c * WARPS + warp;
+  bool with_q = qrow != nullptr;
+  int without = point;
+  uint64_t sum = warp_sum(sum_of(bound(mine), bound(mine + 1), with_q, without));
   if (lane == 0) part[0][warp] = sum;
   cluster_sync_all();
   const uint32_t at = smem_u32(&part[0][0]);
-  // every warp: all parts' sums (128 of them, four a lane), their total and what lies before its own
+  // every warp: all parts' sums (a few a lane), their total and what lies before its own
   auto totals = [&](int which, uint64_t& total, uint64_t& before) {
     total = before = 0;
 #pragma unroll
@@ -126,23 +160,15 @@ __global__ void __launch_bounds__(kVerifyThreads) attn_draft_verify_kernel(const
       const int w = i * 32 + lane;
       const uint64_t v = ld_cluster_u64(cluster_map(at + (which * WARPS + w % WARPS) * 8, w / WARPS));
       total += v;
-      if (w < c * WARPS + warp) before += v;
+      if (w < mine) before += v;
     }
     total = warp_sum(total), before = warp_sum(before);
   };
   uint64_t total, before;
   totals(0, total, before);
-  bool whole = false;
   if (total == 0 && rejected) {  // nothing is left (the same for the whole cluster): p itself
-    whole = true;
-    sum = 0;
-    for (int x = from + lane * W; x < to; x += 32 * W) {
-      float a[W], q[W];
-      load(x, a, q);
-#pragma unroll
-      for (int k = 0; k < W; ++k) sum += prob_fixed(a[k]);
-    }
-    sum = warp_sum(sum);
+    with_q = false, without = -1;
+    sum = warp_sum(sum_of(bound(mine), bound(mine + 1), false, -1));
     if (lane == 0) part[1][warp] = sum;
     cluster_sync_all();
     totals(1, total, before);
@@ -163,39 +189,52 @@ __global__ void __launch_bounds__(kVerifyThreads) attn_draft_verify_kernel(const
     p.accept_len[b] = n;
     if (total == 0) p.token[b] = -1;
   }
-  if (before <= limit && limit < before + sum) {  // this warp's part holds the token
-    uint64_t run = before;
-    for (int x0 = from; x0 < to; x0 += 32 * W) {
-      const int x = x0 + lane * W;
+  if (lane == 0 && before <= limit && limit < before + sum) chosen = warp, chosen_before = before;
+  __syncthreads();
+  if (chosen >= 0) {  // this CTA holds the token: its warps look at that part's steps, WARPS at a time
+    const int from = bound(c * WARPS + chosen), to = bound(c * WARPS + chosen + 1);
+    uint64_t run = chosen_before;
+    for (int x0 = from; x0 < to; x0 += WARPS * STEP) {
+      const int x = x0 + warp * STEP + lane * W;
       float a[W], q[W];
-      load(x, a, q);
-      uint64_t v[W], mine = 0;
+      load(x, to, with_q, a, q);
+      uint64_t v[W], own = 0;
 #pragma unroll
       for (int k = 0; k < W; ++k) {
-        v[k] = x + k < to ? (whole ? prob_fixed(a[k]) : residual(a[k], q[k], x + k == point)) : 0;
-        mine += v[k];
+        FixedSum s;
+        s.add(a[k], q[k], x + k == without);
+        v[k] = s.value();
+        own += v[k];
       }
-      uint64_t upto = mine;  // inclusive sums over the lanes
+      uint64_t upto = own;  // inclusive sums over the lanes
 #pragma unroll
       for (int m = 1; m < 32; m <<= 1) {
         const uint64_t o = __shfl_up_sync(0xffffffffu, upto, m);
         if (lane >= m) upto += o;
       }
-      const uint32_t hit = __ballot_sync(0xffffffffu, run + upto > limit);
-      if (hit) {
-        if (lane == __ffs(static_cast<int>(hit)) - 1) {
-          uint64_t s = run + upto - mine;
-          int k = 0;
+      if (lane == 31) piece[warp] = upto;
+      __syncthreads();
+      uint64_t ahead = 0, all = 0;  // sums of the warps before this one, and of all
 #pragma unroll
-          for (int i = 0; i < W - 1; ++i) {
-            s += v[i];
-            if (s <= limit && k == i) k = i + 1;
-          }
-          p.token[b] = x + k;
-        }
-        break;
+      for (int w = 0; w < WARPS; ++w) {
+        const uint64_t y = piece[w];
+        if (w < warp) ahead += y;
+        all += y;
       }
-      run += __shfl_sync(0xffffffffu, upto, 31);
+      const uint64_t s0 = run + ahead + upto - own;
+      if (s0 <= limit && limit < s0 + own) {  // this lane's tokens
+        uint64_t s = s0;
+        int k = 0;
+#pragma unroll
+        for (int i = 0; i < W - 1; ++i) {
+          s += v[i];
+          if (s <= limit && k == i) k = i + 1;
+        }
+        p.token[b] = x + k;
+      }
+      run += all;
+      __syncthreads();
+      if (run > limit) break;
     }
   }
   cluster_sync_all();  // no CTA leaves while others read its sums

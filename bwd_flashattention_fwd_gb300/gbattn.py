@@ -613,34 +613,30 @@ def attn_cache_evict(k, v, weight, pos, cache_len, seen, weight_out, pos_out, ca
 
 
 _Strides = ctypes.c_int64 * 3
+_strides_of: dict = {}  # the C arrays of the strides met so far (a few per model)
 
 
 def _row_strides(call: str, t, name: str):
     """Strides between sequences, heads and tokens of a [B,H,L,D] tensor whose
-    rows are contiguous (a size of 1 has none: 0)."""
-    B, H, L, D = t.shape
-    b, h, n, d = t.stride()
-    if d != 1:
-        raise ValueError(f"{call}: {name} of strides {t.stride()} has no contiguous rows")
-    return _Strides(b if B > 1 else 0, h if H > 1 else D, n if L > 1 else 0)
+    rows are contiguous, for the C ABI."""
+    st = t.stride()
+    got = _strides_of.get(st)
+    if got is None:
+        if st[3] != 1:
+            raise ValueError(f"{call}: {name} of strides {st} has no contiguous rows")
+        if len(_strides_of) >= 256:
+            _strides_of.clear()
+        got = _strides_of[st] = _Strides(*st[:3])
+    return got
 
 
-def _rope_args(call, q, k, pos, freq, q_weight, k_weight, axis, dense, rows, f32=()):
-    """Checks what both directions of the rotation read; -> (axes, dtype code)."""
-    B, Hq, L, D = q.shape
-    dt, dev, Hkv, half = q.dtype, q.get_device(), k.shape[1], freq.numel()
-    axes = pos.shape[0] if pos.dim() == 3 else 1
-    at = (axes, B, L) if pos.dim() == 3 else (B, L)
-    if not (dev >= 0 and dev == _current_device() and (dt is _BF16 or dt is _F16) and k.dtype is dt and k.get_device() == dev
-            and k.shape == (B, Hkv, L, D) and _plain(pos, _I32, dev, at) and _plain(freq, _F32, dev, (half,))
-            and (axis is None or _plain(axis, _U8, dev, (half,)))
-            and all(t is None or _plain(t, dt, dev, shape) for t, shape, _ in dense)
-            and all(t.dtype is dt and t.get_device() == dev and t.shape == shape for t, shape, _ in rows)
-            and all(t is None or _plain(t, _F32, dev, (D,)) for t in f32)):
-        _require(call, dense=[t for t, _, _ in dense], sliced=(q, k, *(t for t, _, _ in rows)), f32=(freq, *f32), u8=(axis,), i32=(pos,))
-        _shapes(call, (k, (B, Hkv, L, D), "k"), (pos, at, "pos"), (freq, (half,), "freq"), (axis, (half,), "axis"), *dense, *rows,
-                *((t, (D,), "a weight's gradient") for t in f32))
-    return axes, ATTN_DTYPE_BF16 if dt is _BF16 else ATTN_DTYPE_FP16
+def _refuse_rope(call, q, k, pos, freq, axis, dense, rows=(), f32=(), u8=()):
+    """Names what is wrong with a rotation's arguments: (tensor, shape, name) triples besides the inputs."""
+    B, _, L, D = q.shape
+    half, at = freq.shape[0], ((pos.shape[0],) if pos.dim() == 3 else ()) + (B, L)
+    _require(call, dense=[t for t, _, _ in dense], sliced=(q, k, *(t for t, _, _ in rows)), f32=(freq, *(t for t, _, _ in f32)),
+             u8=(axis, *u8), i32=(pos,))
+    _shapes(call, (k, (B, k.shape[1], L, D), "k"), (pos, at, "pos"), (freq, (half,), "freq"), (axis, (half,), "axis"), *dense, *rows, *f32)
 
 
 def attn_qk_norm_rope(q, k, q_out, k_out, pos, freq, q_weight=None, k_weight=None, axis=None, eps: float = 1e-6,
@@ -651,15 +647,22 @@ def attn_qk_norm_rope(q, k, q_out, k_out, pos, freq, q_weight=None, k_weight=Non
     pos int32 [B,L] or [axes,B,L]; freq float32 [rot/2]; axis uint8 [rot/2]:
     which axis each pair turns by (None: the first)."""
     B, Hq, L, D = q.shape
-    Hkv = k.shape[1]
-    axes, code = _rope_args("attn_qk_norm_rope", q, k, pos, freq, q_weight, k_weight, axis,
-                            ((q_weight, (D,), "q_weight"), (k_weight, (D,), "k_weight"), (q_out, (B, Hq, L, D), "q_out"),
-                             (k_out, (B, Hkv, L, D), "k_out")), ())
+    Hkv, half, axes = k.shape[1], freq.shape[0], pos.shape[0] if pos.dim() == 3 else 1
+    dt, dev, w = q.dtype, q.get_device(), (D,)
+    if not (dev >= 0 and dev == _current_device() and (dt is _BF16 or dt is _F16) and dt is k.dtype is q_out.dtype is k_out.dtype
+            and pos.dtype is _I32 and freq.dtype is _F32
+            and dev == k.get_device() == q_out.get_device() == k_out.get_device() == pos.get_device() == freq.get_device()
+            and q_out.is_contiguous() and k_out.is_contiguous() and pos.is_contiguous() and freq.is_contiguous()
+            and (k.shape, q_out.shape, k_out.shape, pos.shape[-2:], freq.shape) == ((B, Hkv, L, D), q.shape, k.shape, (B, L), (half,))
+            and pos.dim() <= 3 and (axis is None or _plain(axis, _U8, dev, freq.shape))
+            and (q_weight is None or _plain(q_weight, dt, dev, w)) and (k_weight is None or _plain(k_weight, dt, dev, w))):
+        _refuse_rope("attn_qk_norm_rope", q, k, pos, freq, axis,
+                     ((q_weight, w, "q_weight"), (k_weight, w, "k_weight"), (q_out, (B, Hq, L, D), "q_out"), (k_out, (B, Hkv, L, D), "k_out")))
     st = load_library().attn_qk_norm_rope(
         q.data_ptr(), k.data_ptr(), _ptr(q_weight), _ptr(k_weight), pos.data_ptr(), freq.data_ptr(), _ptr(axis),
         q_out.data_ptr(), k_out.data_ptr(), _row_strides("attn_qk_norm_rope", q, "q"),
-        _row_strides("attn_qk_norm_rope", k, "k"), B, Hq, Hkv, L, D, 2 * freq.numel(), axes, float(eps),
-        int(bool(interleaved)), code, _raw_stream(q.get_device()) if stream is None else _stream_handle(stream))
+        _row_strides("attn_qk_norm_rope", k, "k"), B, Hq, Hkv, L, D, 2 * half, axes, eps, 1 if interleaved else 0,
+        ATTN_DTYPE_BF16 if dt is _BF16 else ATTN_DTYPE_FP16, _raw_stream(dev) if stream is None else _stream_handle(stream))
     return _check(st, "attn_qk_norm_rope", check)
 
 
@@ -678,47 +681,45 @@ def attn_qk_norm_rope_bwd(q, k, dq_out, dk_out, pos, freq, dq, dk, q_weight, k_w
     """Gradients of attn_qk_norm_rope: from dq_out, dk_out (contiguous) writes
     dq, dk (rows like q's and k's; views of a packed gradient will do) and, with
     weights, dq_weight, dk_weight (float32 [D]; None without)."""
-    B, Hq, L, D = q.shape
-    Hkv = k.shape[1]
-    axes, code = _rope_args("attn_qk_norm_rope_bwd", q, k, pos, freq, q_weight, k_weight, axis,
-                            ((q_weight, (D,), "q_weight"), (k_weight, (D,), "k_weight"), (dq_out, (B, Hq, L, D), "dq_out"),
-                             (dk_out, (B, Hkv, L, D), "dk_out")),
-                            ((dq, (B, Hq, L, D), "dq"), (dk, (B, Hkv, L, D), "dk")), (dq_weight, dk_weight))
-    if not _plain(workspace, _U8, q.get_device(), workspace.shape):
-        _require("attn_qk_norm_rope_bwd", u8=(workspace,))
     call = "attn_qk_norm_rope_bwd"
+    B, Hq, L, D = q.shape
+    Hkv, half, axes = k.shape[1], freq.shape[0], pos.shape[0] if pos.dim() == 3 else 1
+    dt, dev, w = q.dtype, q.get_device(), (D,)
+    if not (dev >= 0 and dev == _current_device() and (dt is _BF16 or dt is _F16)
+            and dt is k.dtype is dq_out.dtype is dk_out.dtype is dq.dtype is dk.dtype
+            and pos.dtype is _I32 and freq.dtype is _F32 and workspace.dtype is _U8
+            and dev == k.get_device() == dq_out.get_device() == dk_out.get_device() == dq.get_device() == dk.get_device()
+            == pos.get_device() == freq.get_device() == workspace.get_device()
+            and dq_out.is_contiguous() and dk_out.is_contiguous() and pos.is_contiguous() and freq.is_contiguous()
+            and workspace.is_contiguous()
+            and (k.shape, dq_out.shape, dk_out.shape, dq.shape, dk.shape, pos.shape[-2:], freq.shape)
+            == ((B, Hkv, L, D), q.shape, k.shape, q.shape, k.shape, (B, L), (half,))
+            and pos.dim() <= 3 and (axis is None or _plain(axis, _U8, dev, freq.shape))
+            and (q_weight is None or _plain(q_weight, dt, dev, w)) and (k_weight is None or _plain(k_weight, dt, dev, w))
+            and (dq_weight is None or _plain(dq_weight, _F32, dev, w)) and (dk_weight is None or _plain(dk_weight, _F32, dev, w))):
+        _refuse_rope(call, q, k, pos, freq, axis, ((q_weight, w, "q_weight"), (k_weight, w, "k_weight"), (dq_out, (B, Hq, L, D), "dq_out"),
+                                                   (dk_out, (B, Hkv, L, D), "dk_out")),
+                     ((dq, (B, Hq, L, D), "dq"), (dk, (B, Hkv, L, D), "dk")), ((dq_weight, w, "dq_weight"), (dk_weight, w, "dk_weight")),
+                     (workspace,))
     st = load_library().attn_qk_norm_rope_bwd(
         q.data_ptr(), k.data_ptr(), _ptr(q_weight), _ptr(k_weight), pos.data_ptr(), freq.data_ptr(), _ptr(axis),
         dq_out.data_ptr(), dk_out.data_ptr(), dq.data_ptr(), dk.data_ptr(), _ptr(dq_weight), _ptr(dk_weight),
         workspace.data_ptr(), workspace.numel(), _row_strides(call, q, "q"), _row_strides(call, k, "k"),
-        _row_strides(call, dq, "dq"), _row_strides(call, dk, "dk"), B, Hq, Hkv, L, D, 2 * freq.numel(), axes, float(eps),
-        int(bool(interleaved)), code, _raw_stream(q.get_device()) if stream is None else _stream_handle(stream))
+        _row_strides(call, dq, "dq"), _row_strides(call, dk, "dk"), B, Hq, Hkv, L, D, 2 * half, axes, eps, 1 if interleaved else 0,
+        ATTN_DTYPE_BF16 if dt is _BF16 else ATTN_DTYPE_FP16, _raw_stream(dev) if stream is None else _stream_handle(stream))
     return _check(st, call, check)
 
 
-def _pool_args(call, k_pages, v_pages, table, k_exp, v_exp, x, lens, dense, sliced=(), i32=(), f32=(), u8=()):
-    """Checks a paged cache and what a call on it takes beside it: 16-bit
-    tensors like x (dense, sliced: (tensor, shape, name)), int32 [B] lengths."""
-    n_pages, Hkv, page, D = k_pages.shape
-    B = table.shape[0]
-    dt, dev = x.dtype, x.get_device()
-    held = dt if k_exp is None else _E4M3
-    if not (dev >= 0 and dev == _current_device() and (dt is _BF16 or dt is _F16) and _plain(k_pages, held, dev, k_pages.shape)
-            and _plain(v_pages, held, dev, k_pages.shape) and _plain(table, _I32, dev, (B, table.shape[1]))
-            and (k_exp is None or _plain(k_exp, _I8, dev, (n_pages, Hkv, page)))
-            and (v_exp is None or _plain(v_exp, _I8, dev, (n_pages, Hkv, page)))
-            and all(t is None or _plain(t, _I32, dev, (B,)) for t in lens)
-            and all(_plain(t, dt, dev, shape) for t, shape, _ in dense)
-            and all(t.dtype is dt and t.get_device() == dev and t.shape == shape for t, shape, _ in sliced)
-            and all(_plain(t, _F32, dev, shape) for t, shape, _ in f32) and all(_plain(t, _U8, dev, t.shape) for t in u8)):
-        pools = (k_pages, v_pages)
-        _require(call, dense=(*(t for t, _, _ in dense), *(pools if k_exp is None else ())), sliced=(x, *(t for t, _, _ in sliced)),
-                 f32=[t for t, _, _ in f32], u8=u8, i32=(table, *lens), i8=(k_exp, v_exp), e4m3=() if k_exp is None else pools)
-        _shapes(call, (v_pages, k_pages.shape, "v_pages"), (k_exp, (n_pages, Hkv, page), "k_exp"), (v_exp, (n_pages, Hkv, page), "v_exp"),
-                *((t, (B,), "a length") for t in lens), *dense, *sliced, *f32)
+def _refuse_pool(call, k_pages, v_pages, table, k_exp, v_exp, lens, dense=(), sliced=(), f32=(), u8=()):
+    """Names what is wrong with a paged cache's arguments: (tensor, shape, name) triples besides the cache."""
+    n_pages, Hkv, page, _ = k_pages.shape
+    B, pools, ints = table.shape[0], (k_pages, v_pages), (n_pages, Hkv, page)
     if (k_exp is None) != (v_exp is None):
         raise ValueError(f"{call}: k_exp and v_exp go together")
-    return ATTN_DTYPE_BF16 if dt is _BF16 else ATTN_DTYPE_FP16
+    _require(call, dense=(*(t for t, _, _ in dense), *(pools if k_exp is None else ())), sliced=[t for t, _, _ in sliced],
+             f32=[t for t, _, _ in f32], u8=u8, i32=(table, *lens), i8=(k_exp, v_exp), e4m3=() if k_exp is None else pools)
+    _shapes(call, (v_pages, k_pages.shape, "v_pages"), (k_exp, ints, "k_exp"), (v_exp, ints, "v_exp"), (table, (B, *table.shape[1:2]), "table"),
+            *((t, (B,), "a length") for t in lens), *dense, *sliced, *f32)
 
 
 def attn_paged_write(k_new, v_new, k_pages, v_pages, table, cache_len, cache_len_out, new_len=None, k_exp=None, v_exp=None,
@@ -728,13 +729,25 @@ def attn_paged_write(k_new, v_new, k_pages, v_pages, table, cache_len, cache_len
     Pages [n,Hkv,page_size,D] of the same type, or float8_e4m3fn with int8
     exponents k_exp, v_exp [n,Hkv,page_size]; table int32 [B,pages]."""
     B, Hkv, T, D = k_new.shape
-    n_pages, _, page, _ = k_pages.shape
-    code = _pool_args("attn_paged_write", k_pages, v_pages, table, k_exp, v_exp, k_new, (cache_len, cache_len_out, new_len),
-                      ((k_new, (table.shape[0], k_pages.shape[1], T, k_pages.shape[3]), "k_new"), (v_new, k_new.shape, "v_new")))
+    n_pages, _, page, _ = pool = k_pages.shape
+    dt, dev, lens, per_seq = k_new.dtype, k_new.get_device(), (B,), table.shape[1]
+    held, ints = dt if k_exp is None else _E4M3, (n_pages, Hkv, page)
+    if not (dev >= 0 and dev == _current_device() and (dt is _BF16 or dt is _F16) and v_new.dtype is dt
+            and held is k_pages.dtype is v_pages.dtype and table.dtype is cache_len.dtype is cache_len_out.dtype is _I32
+            and dev == v_new.get_device() == k_pages.get_device() == v_pages.get_device() == table.get_device()
+            == cache_len.get_device() == cache_len_out.get_device()
+            and k_new.is_contiguous() and v_new.is_contiguous() and k_pages.is_contiguous() and v_pages.is_contiguous()
+            and table.is_contiguous() and cache_len.is_contiguous() and cache_len_out.is_contiguous()
+            and (pool, v_pages.shape, v_new.shape, table.shape, cache_len.shape, cache_len_out.shape)
+            == ((n_pages, Hkv, page, D), pool, k_new.shape, (B, per_seq), lens, lens)
+            and (new_len is None or _plain(new_len, _I32, dev, lens)) and (k_exp is None) == (v_exp is None)
+            and (k_exp is None or (_plain(k_exp, _I8, dev, ints) and _plain(v_exp, _I8, dev, ints)))):
+        _refuse_pool("attn_paged_write", k_pages, v_pages, table, k_exp, v_exp, (cache_len, cache_len_out, new_len),
+                     ((k_new, (table.shape[0], pool[1], T, pool[3]), "k_new"), (v_new, k_new.shape, "v_new")))
     st = load_library().attn_paged_write(
         k_new.data_ptr(), v_new.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), _ptr(k_exp), _ptr(v_exp), table.data_ptr(),
-        cache_len.data_ptr(), _ptr(new_len), cache_len_out.data_ptr(), B, Hkv, T, n_pages, page, table.shape[1], D, code,
-        _raw_stream(k_new.get_device()) if stream is None else _stream_handle(stream))
+        cache_len.data_ptr(), _ptr(new_len), cache_len_out.data_ptr(), B, Hkv, T, n_pages, page, per_seq, D,
+        ATTN_DTYPE_BF16 if dt is _BF16 else ATTN_DTYPE_FP16, _raw_stream(dev) if stream is None else _stream_handle(stream))
     return _check(st, "attn_paged_write", check)
 
 
@@ -743,13 +756,22 @@ def attn_paged_read(k_pages, v_pages, table, cache_len, k, v, k_exp=None, v_exp=
     (or slices of a longer cache, as attn_fwd_ex takes them); rows from the
     sequence's length on are left as they were."""
     B, Hkv, Lk, D = k.shape
-    n_pages, _, page, _ = k_pages.shape
-    shape = (table.shape[0], k_pages.shape[1], Lk, k_pages.shape[3])
-    code = _pool_args("attn_paged_read", k_pages, v_pages, table, k_exp, v_exp, k, (cache_len,), (), ((k, shape, "k"), (v, shape, "v")))
+    n_pages, _, page, _ = pool = k_pages.shape
+    dt, dev, lens, per_seq = k.dtype, k.get_device(), (B,), table.shape[1]
+    held, ints = dt if k_exp is None else _E4M3, (n_pages, Hkv, page)
+    if not (dev >= 0 and dev == _current_device() and (dt is _BF16 or dt is _F16) and v.dtype is dt
+            and held is k_pages.dtype is v_pages.dtype and table.dtype is cache_len.dtype is _I32
+            and dev == v.get_device() == k_pages.get_device() == v_pages.get_device() == table.get_device() == cache_len.get_device()
+            and k_pages.is_contiguous() and v_pages.is_contiguous() and table.is_contiguous() and cache_len.is_contiguous()
+            and (pool, v_pages.shape, v.shape, table.shape, cache_len.shape) == ((n_pages, Hkv, page, D), pool, k.shape, (B, per_seq), lens)
+            and (k_exp is None) == (v_exp is None)
+            and (k_exp is None or (_plain(k_exp, _I8, dev, ints) and _plain(v_exp, _I8, dev, ints)))):
+        shape = (table.shape[0], pool[1], Lk, pool[3])
+        _refuse_pool("attn_paged_read", k_pages, v_pages, table, k_exp, v_exp, (cache_len,), sliced=((k, shape, "k"), (v, shape, "v")))
     st = load_library().attn_paged_read(
         k_pages.data_ptr(), v_pages.data_ptr(), _ptr(k_exp), _ptr(v_exp), table.data_ptr(), cache_len.data_ptr(), k.data_ptr(),
-        v.data_ptr(), kv_row_pitch(k, v), B, Hkv, Lk, n_pages, page, table.shape[1], D, code,
-        _raw_stream(k.get_device()) if stream is None else _stream_handle(stream))
+        v.data_ptr(), kv_row_pitch(k, v), B, Hkv, Lk, n_pages, page, per_seq, D,
+        ATTN_DTYPE_BF16 if dt is _BF16 else ATTN_DTYPE_FP16, _raw_stream(dev) if stream is None else _stream_handle(stream))
     return _check(st, "attn_paged_read", check)
 
 
@@ -771,13 +793,25 @@ def attn_fwd_paged(q, k_pages, v_pages, table, cache_len, o, lse, workspace, sca
     chain) over its pages, which hold them already: cache_len [B] int32 counts
     them (writes o, lse).  Pages as for attn_paged_write."""
     B, Hq, T, D = q.shape
-    n_pages, Hkv, page, Dk = k_pages.shape
-    code = _pool_args("attn_fwd_paged", k_pages, v_pages, table, k_exp, v_exp, q, (cache_len,),
-                      ((q, (table.shape[0], Hq, T, Dk), "q"), (o, q.shape, "o")), f32=((lse, (B, Hq, T), "lse"),), u8=(workspace,))
+    n_pages, Hkv, page, _ = pool = k_pages.shape
+    dt, dev, per_seq = q.dtype, q.get_device(), table.shape[1]
+    held, ints = dt if k_exp is None else _E4M3, (n_pages, Hkv, page)
+    if not (dev >= 0 and dev == _current_device() and (dt is _BF16 or dt is _F16) and o.dtype is dt
+            and held is k_pages.dtype is v_pages.dtype and table.dtype is cache_len.dtype is _I32
+            and lse.dtype is _F32 and workspace.dtype is _U8
+            and dev == k_pages.get_device() == v_pages.get_device() == table.get_device() == cache_len.get_device() == o.get_device()
+            == lse.get_device() == workspace.get_device()
+            and q.is_contiguous() and k_pages.is_contiguous() and v_pages.is_contiguous() and table.is_contiguous()
+            and cache_len.is_contiguous() and o.is_contiguous() and lse.is_contiguous() and workspace.is_contiguous()
+            and (pool, v_pages.shape, table.shape, cache_len.shape, o.shape, lse.shape)
+            == ((n_pages, Hkv, page, D), pool, (B, per_seq), (B,), q.shape, (B, Hq, T)) and (k_exp is None) == (v_exp is None)
+            and (k_exp is None or (_plain(k_exp, _I8, dev, ints) and _plain(v_exp, _I8, dev, ints)))):
+        _refuse_pool("attn_fwd_paged", k_pages, v_pages, table, k_exp, v_exp, (cache_len,),
+                     ((q, (table.shape[0], Hq, T, pool[3]), "q"), (o, q.shape, "o")), f32=((lse, (B, Hq, T), "lse"),), u8=(workspace,))
     st = load_library().attn_fwd_paged(
         q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), _ptr(k_exp), _ptr(v_exp), table.data_ptr(), cache_len.data_ptr(),
-        o.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.numel(), B, Hq, Hkv, T, n_pages, page, table.shape[1], D,
-        float(scale), code, _raw_stream(q.get_device()) if stream is None else _stream_handle(stream))
+        o.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.numel(), B, Hq, Hkv, T, n_pages, page, per_seq, D, scale,
+        ATTN_DTYPE_BF16 if dt is _BF16 else ATTN_DTYPE_FP16, _raw_stream(dev) if stream is None else _stream_handle(stream))
     return _check(st, "attn_fwd_paged", check)
 
 
@@ -788,10 +822,13 @@ def attn_draft_verify(target, draft, tokens, u, r, accept_len, token, draft_len=
     (writes accept_len, token: int32 [B])."""
     B, T = tokens.shape
     V, dev, lens = target.shape[-1], target.get_device(), (B,)
-    if not (dev >= 0 and dev == _current_device() and _plain(target, _F32, dev, (B, T + 1, V))
-            and (draft is None or _plain(draft, _F32, dev, (B, T, V))) and _plain(tokens, _I32, dev, (B, T))
-            and _plain(u, _F32, dev, (B, T)) and _plain(r, _F32, dev, lens) and _plain(accept_len, _I32, dev, lens)
-            and _plain(token, _I32, dev, lens) and (draft_len is None or _plain(draft_len, _I32, dev, lens))):
+    if not (dev >= 0 and dev == _current_device() and target.dtype is u.dtype is r.dtype is _F32
+            and tokens.dtype is accept_len.dtype is token.dtype is _I32
+            and dev == tokens.get_device() == u.get_device() == r.get_device() == accept_len.get_device() == token.get_device()
+            and target.is_contiguous() and tokens.is_contiguous() and u.is_contiguous() and r.is_contiguous()
+            and accept_len.is_contiguous() and token.is_contiguous()
+            and (target.shape, u.shape, r.shape, accept_len.shape, token.shape) == ((B, T + 1, V), tokens.shape, lens, lens, lens)
+            and (draft is None or _plain(draft, _F32, dev, (B, T, V))) and (draft_len is None or _plain(draft_len, _I32, dev, lens))):
         _require("attn_draft_verify", f32=(target, draft, u, r), i32=(tokens, accept_len, token, draft_len))
         _shapes("attn_draft_verify", (target, (B, T + 1, V), "target"), (draft, (B, T, V), "draft"), (u, (B, T), "u"), (r, lens, "r"),
                 (accept_len, lens, "accept_len"), (token, lens, "token"), (draft_len, lens, "draft_len"))

@@ -444,8 +444,8 @@ attn_status_t attn_fwd_paged(const void* q, const void* k_pages, const void* v_p
  *   token [B]: the next token, drawn from w = max(target_n - draft_n, 0) where
  *   draft n was rejected (from target_n if nothing is left of it), from
  *   target_n where none was: the least x with sum_{y<=x} w_y > r * sum w, -1 if
- *   all are 0.  Probabilities count in multiples of 2^-60, those below 0 and
- *   NaN as 0, those above 1 as 1; a row's sum is below 16.  Sums are exact.
+ *   all are 0.  Probabilities count in multiples of 2^-45 (the
+ *   nearest), those below 0 and NaN as 0, those above 1 as 1.  Sums are exact.
  *   T <= 1024, B <= 65535, V <= 2^30 (else ATTN_ERR_UNSUPPORTED).  No output
  *   overlaps an input or the other output (ATTN_ERR_INVALID_ARG).  target and
  *   draft 16-byte aligned, the others 4-byte.

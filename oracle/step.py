@@ -131,9 +131,9 @@ def paged_attention(q, k, v, ke, ve, table, page_size, cache_len, scale):
 
 
 def fixed(x):
-    """Probabilities as integers, multiples of 2^-60."""
+    """Probabilities as integers, the nearest multiples of 2^-45."""
     x = np.minimum(np.where(np.isnan(x) | (x < 0), 0.0, np.asarray(x, dtype=np.float64)), 1.0)
-    return [int(v) for v in np.floor(x * 2.0 ** 60)]
+    return [int(v) for v in np.rint(x * 2.0 ** 45)]
 
 
 def verify(target, draft, tokens, u, r, draft_len=None):
