@@ -14,6 +14,38 @@ namespace GBATTN_CAT(paged_d, GBATTN_HEAD_DIM) {
 
 constexpr int kD = GBATTN_HEAD_DIM;
 
+// A cluster of CTAs per head, in one launch, or equal pieces and a second one.
+// A cluster saves the join (b4 x 8 heads, 8000 keys, D = 128: 26.2 us, 28.8 by
+// pieces; 1000 keys of one sequence 5.4 and 6.7), but its CTAs get what their
+// head has: a CTA alone takes kPagedAlone % of the time per step that it takes
+// when all share the bandwidth at half the room's length, so it pays where the
+// clusters fill enough of the GPU for the steps each has (one sequence: 2000
+// keys 6.8 and 7.1, 4000 keys 9.5 and 8.6; 16 quantised sequences of 500 to 4000 keys 26.3
+// and 25.2, 1000 to 8192 43.5 and 35.7).  Past kPagedShort steps a single long
+// sequence among short ones would be waited for too long.
+constexpr int kPagedShort = 32;
+template <bool Q8>
+constexpr float kPagedAlone = Q8 ? 120.f : 93.f;
+
+template <typename... Params, typename... Args>
+int launch_cluster(void (*kern)(Params...), unsigned grid, int size, int threads, size_t smem, cudaStream_t stream, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = size;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess ? kLaunchOk : kLaunchCudaError;
+}
+
 template <bool BF16, bool Q8, int NT>
 int impl(const PagedAttnParams& p0, int num_sms, cudaStream_t stream) {
   using Gm = PagedGeom<kD, Q8>;
@@ -23,17 +55,33 @@ int impl(const PagedAttnParams& p0, int num_sms, cudaStream_t stream) {
   const int smem = Gm::smem(rows) + (p.B + 1) * 4;
   // two CTAs per SM where their shared memory (1 KB more each, 228 KB in all) and static arrays allow it
   constexpr int fixed = 1024 + 256 + Gm::NW * (rows * 8 + Gm::ST * 4) + rows * 4;
-  const int per_sm = 2 * (smem + fixed) <= 233472 ? 2 : 1;
+  const int per_sm = Gm::per_sm(NT) == 2 && 2 * (smem + fixed) <= 233472 ? 2 : 1;
   p.n_groups = per_sm * (num_sms < kTreeMaxCtas ? num_sms : kTreeMaxCtas);
+  const long long all = static_cast<long long>(p.B) * p.c.Hkv * p.n_rb, room = static_cast<long long>(p.c.per_seq) << p.c.shift;
+  const long long steps = (room + Gm::KS - 1) / Gm::KS;
+  int size = 1;
+  while (size < kPagedCluster && 2 * size * all <= p.n_groups && size < steps) size *= 2;
+  const long long per = (steps + size - 1) / size;
+  if (per <= kPagedShort && per * (kPagedAlone<Q8> - 100.f * size * all / p.n_groups) <= 400.f) {
+    auto kern = attn_paged_cluster_kernel<kD, BF16, Q8, NT>;
+    static std::atomic<uint64_t> done{0};
+    if (!set_smem_limit(kern, Gm::smem(rows), done)) return kLaunchCudaError;
+    return launch_cluster(kern, static_cast<unsigned>(all) * size, size, Gm::THREADS, Gm::smem(rows), stream, p, size);
+  }
   p.part_ml = p.part + static_cast<size_t>(kPagedMaxCtas) * 2 * rows * kD;
   auto kern = attn_paged_kernel<kD, BF16, Q8, NT>;
   static std::atomic<uint64_t> done{0};
   if (!set_smem_limit(kern, Gm::smem(rows) + (kPagedMaxB + 1) * 4, done)) return kLaunchCudaError;
   const int r = launch_dependent(kern, dim3(p.n_groups), Gm::THREADS, smem, stream, p);
   if (r != kLaunchOk || p.n_groups == 1) return r;
-  const long long tasks = static_cast<long long>(p.B) * p.c.Hkv * p.R, most = 8LL * kTreeMaxCtas;
-  return launch_dependent(attn_paged_join_kernel<kD, BF16, Q8, NT>, dim3(static_cast<unsigned>(tasks < most ? tasks : most)),
-                          kPagedJoinThreads, 0, stream, p);
+  // a block's warps share a row's partial results where there are many
+  const long long tasks = static_cast<long long>(p.B) * p.c.Hkv * p.R;
+  auto join = [&](auto kern_j, int per) {
+    const long long blocks = (tasks + per - 1) / per, most = 8LL * kTreeMaxCtas;
+    return launch_dependent(kern_j, dim3(static_cast<unsigned>(blocks < most ? blocks : most)), kPagedJoinThreads, 0, stream, p);
+  };
+  if (p.n_groups > 8 * all) return join(attn_paged_join_kernel<kD, BF16, Q8, NT, 8>, 1);
+  return join(attn_paged_join_kernel<kD, BF16, Q8, NT, 1>, kPagedJoinThreads / 32);
 }
 
 template <bool BF16, bool Q8>

@@ -50,8 +50,8 @@ __device__ __forceinline__ float2 e4m3_unpack(uint32_t pair) {
 
 constexpr int kPagedThreads = 256;
 
-// A row belongs to D / 16 lanes with 16 consecutive values each.  Units: the
-// rows of K, then those of V.
+// A token's row of K and its row of V belong to D / 16 lanes, 16 consecutive
+// values each; both are loaded before the page is looked up.
 template <int D, bool BF16, bool Q8>
 __global__ void __launch_bounds__(kPagedThreads) attn_paged_write_kernel(const PagedWriteParams p) {
   using Gm = RowLanes<D>;
@@ -62,48 +62,52 @@ __global__ void __launch_bounds__(kPagedThreads) attn_paged_write_kernel(const P
   const int room = p.c.per_seq << p.c.shift;
   const long long n_rows = (static_cast<long long>(p.c.n_pages) * p.c.Hkv) << p.c.shift;
   const long long step = static_cast<long long>(gridDim.x) * (kPagedThreads / Gm::GROUP);
-  const long long first = (static_cast<long long>(blockIdx.x) * kPagedThreads + threadIdx.x) / Gm::GROUP;
   // whole warps go round together: the shuffles below take every lane
-  for (long long base = first - lane / Gm::GROUP; base < 2 * rows; base += step) {
-    const long long unit = base + lane / Gm::GROUP;
-    const bool is_v = unit >= rows;
-    const long long r = is_v ? unit - rows : unit;  // (b, h, t)
-    const long long bh = r / p.T;
-    const int t = static_cast<int>(r - bh * p.T), b = static_cast<int>(bh / p.c.Hkv), h = static_cast<int>(bh - static_cast<long long>(b) * p.c.Hkv);
+  const long long first = (static_cast<long long>(blockIdx.x) * kPagedThreads + (threadIdx.x & ~31)) / Gm::GROUP;
+  for (long long base = first; base < rows; base += step) {
+    const long long r = base + lane / Gm::GROUP;  // (b, h, t)
+    const bool in = r < rows;
+    uint4 x[2][2] = {};
+    if (in && j < Gm::LANES) {
+      const uint4* ks = static_cast<const uint4*>(p.k_new) + r * (D / 8) + 2 * j;
+      const uint4* vs = static_cast<const uint4*>(p.v_new) + r * (D / 8) + 2 * j;
+      x[0][0] = ks[0], x[0][1] = ks[1], x[1][0] = vs[0], x[1][1] = vs[1];
+    }
     long long dst = -1;
-    if (unit < 2 * rows) {
+    if (in) {
+      const long long bh = r / p.T;
+      const int t = static_cast<int>(r - bh * p.T), b = static_cast<int>(bh / p.c.Hkv);
+      const int h = static_cast<int>(bh - static_cast<long long>(b) * p.c.Hkv);
       const int len = clamp_len(__ldg(p.cache_len + b), room);
       const int n = min(p.new_len ? clamp_len(__ldg(p.new_len + b), p.T) : p.T, room - len);
       if (t < n) dst = paged_row(p.c, b, h, len + t);
-      if (r == bh * p.T && h == 0 && !is_v && j == 0) p.cache_len_out[b] = len + n;
+      if (t == 0 && h == 0 && j == 0) p.cache_len_out[b] = len + n;
     }
     const bool live = dst >= 0 && j < Gm::LANES && dbg_in_range(dst, 1, n_rows, p.status, 110);
-    uint4 x[2] = {};
-    if (live) {
-      const uint4* src = static_cast<const uint4*>(is_v ? p.v_new : p.k_new) + r * (D / 8) + 2 * j;
-      x[0] = src[0], x[1] = src[1];
-    }
-    if constexpr (!Q8) {
-      if (live) {
-        uint4* d = static_cast<uint4*>(is_v ? p.c.v : p.c.k) + dst * (D / 8) + 2 * j;
-        d[0] = x[0], d[1] = x[1];
-      }
-    } else {
-      float f[16], m = 0.f;
-      unpack8<BF16>(x[0], f), unpack8<BF16>(x[1], f + 8);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) m = fabsf(f[i]) < INFINITY ? fmaxf(m, fabsf(f[i])) : m;
+    for (int v = 0; v < 2; ++v) {
+      if constexpr (!Q8) {
+        if (live) {
+          uint4* d = static_cast<uint4*>(v ? p.c.v : p.c.k) + dst * (D / 8) + 2 * j;
+          d[0] = x[v][0], d[1] = x[v][1];
+        }
+      } else {
+        float f[16], m = 0.f;
+        unpack8<BF16>(x[v][0], f), unpack8<BF16>(x[v][1], f + 8);
 #pragma unroll
-      for (int k = Gm::GROUP / 2; k; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
-      const int e = row_exponent(m);
-      const float by = exp2_int(-e);
-      uint32_t w[4];
+        for (int i = 0; i < 16; ++i) m = fabsf(f[i]) < INFINITY ? fmaxf(m, fabsf(f[i])) : m;
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        w[i] = e4m3_pair(f[4 * i] * by, f[4 * i + 1] * by) | e4m3_pair(f[4 * i + 2] * by, f[4 * i + 3] * by) << 16;
-      if (live) {
-        (static_cast<uint4*>(is_v ? p.c.v : p.c.k) + dst * (D / 16))[j] = make_uint4(w[0], w[1], w[2], w[3]);
-        if (j == 0) (is_v ? p.c.v_exp : p.c.k_exp)[dst] = static_cast<int8_t>(e);
+        for (int k = Gm::GROUP / 2; k; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
+        const int e = row_exponent(m);
+        const float by = exp2_int(-e);
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          w[i] = e4m3_pair(f[4 * i] * by, f[4 * i + 1] * by) | e4m3_pair(f[4 * i + 2] * by, f[4 * i + 3] * by) << 16;
+        if (live) {
+          (static_cast<uint4*>(v ? p.c.v : p.c.k) + dst * (D / 16))[j] = make_uint4(w[0], w[1], w[2], w[3]);
+          if (j == 0) (v ? p.c.v_exp : p.c.k_exp)[dst] = static_cast<int8_t>(e);
+        }
       }
     }
   }
@@ -120,48 +124,76 @@ __device__ __forceinline__ uint32_t dequant_pair(uint32_t pair, float by) {
   return Elem<BF16>::pack(v.x, v.y);
 }
 
-// A block: kReadRows tokens of one sequence and head, K and V; a row belongs to D / 16 lanes.
-constexpr int kReadRows = 64;
+// A block: read_rows tokens of one sequence and head.  A thread holds the same
+// 16 values of several tokens' K and V, whose pages it looks up first, so that
+// all its loads are in flight together.
+constexpr int kReadTokens = 4;  // of a thread
+constexpr int read_rows(int D) { return kReadTokens * (kPagedThreads / (D / 16)); }
 
 template <int D, bool BF16, bool Q8>
 __global__ void __launch_bounds__(kPagedThreads) attn_paged_read_kernel(const PagedReadParams p) {
-  constexpr int LANES = D / 16;
-  __shared__ long long src[kReadRows];
+  constexpr int LANES = D / 16, GROUPS = kPagedThreads / LANES, N = kReadTokens, ROWS = N * GROUPS;
   grid_dependency_wait();
   if (threadIdx.x == 0) grid_launch_dependents();
   const int b = blockIdx.y / p.c.Hkv, h = blockIdx.y - b * p.c.Hkv;
   const int n = clamp_len(p.cache_len[b], min(p.Lk, p.c.per_seq << p.c.shift));
   [[maybe_unused]] const long long n_rows = (static_cast<long long>(p.c.n_pages) * p.c.Hkv) << p.c.shift;
   [[maybe_unused]] const size_t n_out = static_cast<size_t>(p.B * p.c.Hkv - 1) * p.pitch + p.Lk;
-  for (int j0 = blockIdx.x * kReadRows; j0 < n; j0 += gridDim.x * kReadRows) {
-    __syncthreads();
-    if (threadIdx.x < kReadRows) src[threadIdx.x] = j0 + threadIdx.x < n ? paged_row(p.c, b, h, j0 + threadIdx.x) : -1;
-    __syncthreads();
-#pragma unroll 4
-    for (int i = threadIdx.x; i < 2 * kReadRows * LANES; i += kPagedThreads) {
-      const bool is_v = i >= kReadRows * LANES;
-      const int x = is_v ? i - kReadRows * LANES : i, row = x / LANES, c = x - row * LANES;
-      const long long from = src[row];
-      const size_t to = static_cast<size_t>(blockIdx.y) * p.pitch + j0 + row;
-      if (from < 0 || !dbg_in_range(from, 1, n_rows, p.status, 111) || !dbg_in_range(to, 1, n_out, p.status, 112)) continue;
-      uint4* d = static_cast<uint4*>(is_v ? p.v : p.k) + to * (D / 8) + 2 * c;
-      if constexpr (Q8) {
-        const uint4 w = (static_cast<const uint4*>(is_v ? p.c.v : p.c.k) + from * (D / 16))[c];
-        const float by = exp2_int((is_v ? p.c.v_exp : p.c.k_exp)[from]);
-        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-        uint32_t o[8];
+  const int group = threadIdx.x / LANES, c = threadIdx.x - group * LANES;
+  const size_t out0 = static_cast<size_t>(blockIdx.y) * p.pitch;
+  for (long long j0 = static_cast<long long>(blockIdx.x) * ROWS; j0 < n; j0 += static_cast<long long>(gridDim.x) * ROWS) {
+    long long from[N];
+    int row[N];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          o[2 * k] = dequant_pair<BF16>(u[k] & 0xffffu, by);
-          o[2 * k + 1] = dequant_pair<BF16>(u[k] >> 16, by);
+    for (int i = 0; i < N; ++i) {
+      const int x = i * GROUPS + group;
+      row[i] = static_cast<int>(j0) + x;
+      from[i] = group < GROUPS && row[i] < n ? paged_row(p.c, b, h, row[i]) : -1;
+      if (from[i] >= 0 && !(dbg_in_range(from[i], 1, n_rows, p.status, 111) && dbg_in_range(out0 + row[i], 1, n_out, p.status, 112))) from[i] = -1;
+    }
+    if constexpr (Q8) {
+      uint4 w[2][N];
+      int e[2][N];
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (from[i] >= 0) {
+          w[0][i] = (static_cast<const uint4*>(p.c.k) + from[i] * LANES)[c], e[0][i] = p.c.k_exp[from[i]];
+          w[1][i] = (static_cast<const uint4*>(p.c.v) + from[i] * LANES)[c], e[1][i] = p.c.v_exp[from[i]];
         }
-        d[0] = make_uint4(o[0], o[1], o[2], o[3]);
-        d[1] = make_uint4(o[4], o[5], o[6], o[7]);
-      } else {
-        const uint4* s = static_cast<const uint4*>(is_v ? p.c.v : p.c.k) + from * (D / 8) + 2 * c;
-        const uint4 x0 = s[0], x1 = s[1];
-        d[0] = x0, d[1] = x1;
-      }
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+          if (from[i] < 0) continue;
+          const float by = exp2_int(e[v][i]);
+          const uint32_t u[4] = {w[v][i].x, w[v][i].y, w[v][i].z, w[v][i].w};
+          uint32_t o[8];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            o[2 * k] = dequant_pair<BF16>(u[k] & 0xffffu, by);
+            o[2 * k + 1] = dequant_pair<BF16>(u[k] >> 16, by);
+          }
+          uint4* d = static_cast<uint4*>(v ? p.v : p.k) + (out0 + row[i]) * (D / 8) + 2 * c;
+          d[0] = make_uint4(o[0], o[1], o[2], o[3]);
+          d[1] = make_uint4(o[4], o[5], o[6], o[7]);
+        }
+    } else {
+      uint4 w[2][N][2];
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (from[i] >= 0) {
+          const uint4* ks = static_cast<const uint4*>(p.c.k) + from[i] * (D / 8) + 2 * c;
+          const uint4* vs = static_cast<const uint4*>(p.c.v) + from[i] * (D / 8) + 2 * c;
+          w[0][i][0] = ks[0], w[0][i][1] = ks[1], w[1][i][0] = vs[0], w[1][i][1] = vs[1];
+        }
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+          if (from[i] < 0) continue;
+          uint4* d = static_cast<uint4*>(v ? p.v : p.k) + (out0 + row[i]) * (D / 8) + 2 * c;
+          d[0] = w[v][i][0], d[1] = w[v][i][1];
+        }
     }
   }
 }

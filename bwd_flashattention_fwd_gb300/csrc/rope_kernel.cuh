@@ -49,39 +49,99 @@ __device__ __forceinline__ void turn(int pos, uint64_t F, float& c, float& s) {
   sincospif(static_cast<float>(static_cast<int32_t>(t)) * 4.656612873077393e-10f, &s, &c);  // 2^-31: half turns
 }
 
-// Turn the eight pairs of a lane's two pieces f[0..7], f[8..15] by (c, sgn * s).
-template <bool INTERLEAVED>
-__device__ __forceinline__ void rotate16(float (&f)[16], const float (&c)[8], const float (&s)[8]) {
+// A lane's sixteen values as eight pairs of neighbours (two lanes of a 64-bit
+// register, which one instruction multiplies or adds).
+template <bool BF16>
+__device__ __forceinline__ void unpack16(const uint4 (&u)[2], uint64_t (&f)[8]) {
+  const uint32_t w[8] = {u[0].x, u[0].y, u[0].z, u[0].w, u[1].x, u[1].y, u[1].z, u[1].w};
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const int a = INTERLEAVED ? 2 * i : i, b = INTERLEAVED ? 2 * i + 1 : 8 + i;
-    const float x = f[a], y = f[b];
-    f[a] = x * c[i] - y * s[i];
-    f[b] = y * c[i] + x * s[i];
+    const float2 v = Elem<BF16>::unpack(w[i]);
+    f[i] = f2_pack(v.x, v.y);
   }
 }
 
+template <bool BF16>
+__device__ __forceinline__ void store16(uint16_t* row, int c0, int c1, const uint64_t (&f)[8]) {
+  uint32_t w[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float a, b;
+    f2_unpack(f[i], a, b);
+    w[i] = Elem<BF16>::pack(a, b);
+  }
+  uint4* v = reinterpret_cast<uint4*>(row);
+  v[c0] = make_uint4(w[0], w[1], w[2], w[3]);
+  v[c1] = make_uint4(w[4], w[5], w[6], w[7]);
+}
+
+// Turn the eight pairs of a lane's two pieces.  Halves: neighbours f[i] turn with
+// f[i + 4], c[i] and s[i] (i < 4) hold two pairs' cosines and sines, ns[i] = -s[i].
+// Interleaved: f[i] is one pair, c[i] = (cos, cos), s[i] = (-sin, sin) (i < 8).
+template <bool INTERLEAVED>
+__device__ __forceinline__ void rotate16(uint64_t (&f)[8], const uint64_t (&c)[INTERLEAVED ? 8 : 4], const uint64_t (&s)[INTERLEAVED ? 8 : 4],
+                                         const uint64_t (&ns)[INTERLEAVED ? 1 : 4]) {
+  if constexpr (INTERLEAVED) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float a, b;
+      f2_unpack(f[i], a, b);
+      f[i] = f2_fma(f[i], c[i], f2_mul(f2_pack(b, a), s[i]));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint64_t a = f[i], b = f[i + 4];
+      f[i] = f2_fma(a, c[i], f2_mul(b, ns[i]));
+      f[i + 4] = f2_fma(b, c[i], f2_mul(a, s[i]));
+    }
+  }
+}
+
+__device__ __forceinline__ float f2_total(const uint64_t (&f)[2]) {
+  float a, b;
+  f2_unpack(f2_add(f[0], f[1]), a, b);
+  return a + b;
+}
+
 // A CTA takes an equal share of the tokens (and, where there are fewer tokens
-// than CTAs, of the heads) in chunks of up to kRopeChunk: the chunk's sines and
-// cosines go to shared memory once, then its rows (head by head, the chunk's
-// tokens of each) go round the CTA's groups of lanes, each row loaded while the
-// one before it is worked on.
-constexpr int kRopeChunk = 8;
+// than CTAs, of the heads), up to TOKENS of them at a time: their sines and
+// cosines and the offsets of their rows go to shared memory, then their rows
+// (head by head, every token of each) go round the CTA's groups of lanes.  A
+// lane copies its pieces of the rows to come into a ring of its own (cp.async),
+// DEPTH rows ahead: that many bytes in flight are more than the registers
+// would hold (video prompt: 42 us with one row ahead in registers).
+template <int D, bool BWD>
+struct RopeGeom {
+  static constexpr int GROUPS = kRopeThreads / RowLanes<D>::GROUP;
+  static constexpr int PER_SM = BWD ? kRopeBwdPerSm : kRopeFwdPerSm;
+  static constexpr int TOKENS = 2048 / D;                       // 8 KB of sines and cosines
+  static constexpr int DEPTH = 4;
+  static constexpr int PIECES = BWD ? 4 : 2;                    // 16-byte pieces of a row: x (and dy)
+  static constexpr int RING = DEPTH * PIECES * kRopeThreads * 16;
+  static constexpr int CS = TOKENS * D * 4;                     // [TOKENS][2][D / 2] floats
+  static constexpr int OFFSETS = TOKENS * 3 * 8;                // of x, y and dx
+  static constexpr int SUMS = BWD ? kRopeThreads / 32 * D * 4 : 0;
+  static constexpr int SMEM = RING + CS + OFFSETS + SUMS;
+};
 
 template <int D, bool BF16, bool INTERLEAVED, bool BWD>
-__global__ void __launch_bounds__(kRopeThreads, BWD ? kRopeBwdPerSm : kRopeFwdPerSm) rope_kernel(const RopeParams p, int parts) {
-  using Gm = RowLanes<D>;
-  constexpr int GROUPS = kRopeThreads / Gm::GROUP, WARPS = kRopeThreads / 32;
+__global__ void __launch_bounds__(kRopeThreads, RopeGeom<D, BWD>::PER_SM) rope_kernel(const RopeParams p, int parts) {
+  using Gm = RopeGeom<D, BWD>;
+  using Ln = RowLanes<D>;
+  constexpr int WARPS = kRopeThreads / 32, DEPTH = Gm::DEPTH;
+  extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t frac[D / 2];
-  __shared__ __align__(16) float cs[kRopeChunk][2][D / 2];  // cosines, sines
-  __shared__ float dw_sum[BWD ? WARPS : 1][BWD ? D : 1];
+  float* const cs = reinterpret_cast<float*>(smem + Gm::RING);                                  // [TOKENS][2][D / 2]
+  long long* const offsets = reinterpret_cast<long long*>(smem + Gm::RING + Gm::CS);            // [3][TOKENS]
+  float* const dw_sum = reinterpret_cast<float*>(smem + Gm::RING + Gm::CS + Gm::OFFSETS);       // [WARPS][D]
   grid_dependency_wait();  // the kernels before this one are complete
   if (threadIdx.x == 0) grid_launch_dependents();
   const int half = p.rot / 2;
   for (int i = threadIdx.x; i < D / 2; i += kRopeThreads) frac[i] = i < half ? turn_fraction(p.freq[i]) : 0;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int j = lane % Gm::GROUP, group = threadIdx.x / Gm::GROUP;
-  const bool on = j < Gm::LANES;
+  const int j = lane % Ln::GROUP, group = threadIdx.x / Ln::GROUP;
+  const bool on = j < Ln::LANES;
   // The lane's pieces (8 elements each).  Halves: both members of the pairs 8 j ..
   // 8 j + 7, and what is not turned in equal shares; interleaved: any two.
   const int turned = p.rot / 16;
@@ -98,6 +158,7 @@ __global__ void __launch_bounds__(kRopeThreads, BWD ? kRopeBwdPerSm : kRopeFwdPe
   const int pair0 = INTERLEAVED ? 4 * c0 : 8 * j, pair1 = INTERLEAVED ? 4 * c1 : 8 * j + 4;
   const bool turns0 = on && pair0 < half, turns1 = on && pair1 < half;
   const bool norm = p.w[0] != nullptr;
+  const uint32_t ring = smem_u32(smem) + threadIdx.x * 16;  // piece k of slot s: + (s * PIECES + k) * kRopeThreads * 16
   const long long tokens = static_cast<long long>(p.B) * p.L;
   const int part = blockIdx.x % parts;
   const long long block = blockIdx.x / parts, blocks = gridDim.x / parts;
@@ -107,140 +168,164 @@ __global__ void __launch_bounds__(kRopeThreads, BWD ? kRopeBwdPerSm : kRopeFwdPe
     const RowsView xv = p.x[which], dv = p.dx[which];
     uint16_t* const y = static_cast<uint16_t*>(p.y[which]);
     const int H = xv.H, h_lo = H * part / parts, h_hi = H * (part + 1) / parts;
-    uint4 wp[2] = {};
-    if (norm && on) {
-      const uint4* w = static_cast<const uint4*>(p.w[which]);
-      wp[0] = __ldg(w + c0), wp[1] = __ldg(w + c1);
+    uint64_t w[8], dw[BWD ? 8 : 1];
+    {
+      uint4 wp[2] = {};
+      if (norm && on) {
+        const uint4* v = static_cast<const uint4*>(p.w[which]);
+        wp[0] = __ldg(v + c0), wp[1] = __ldg(v + c1);
+      }
+      unpack16<BF16>(wp, w);
     }
-    float dw[BWD ? 16 : 1];
 #pragma unroll
-    for (float& x : dw) x = 0.f;
+    for (uint64_t& x : dw) x = 0;
 #pragma unroll 1
-    for (long long t0 = t_first; t0 < t_end; t0 += kRopeChunk) {
-      // the chunk: n tokens, rows in slots of 2^shift per head
-      const int n = static_cast<int>(t_end - t0 < kRopeChunk ? t_end - t0 : kRopeChunk);
-      const int shift = n > 4 ? 3 : n > 2 ? 2 : n > 1 ? 1 : 0;
-      const int t = group & ((1 << shift) - 1), stride = GROUPS >> shift;  // a group's rows are all of one token
-      const long long token = t0 + t;
-      const int b = static_cast<int>(token / p.L), l = static_cast<int>(token - static_cast<long long>(b) * p.L);
-      const int h0 = h_lo + (group >> shift);  // the group's first head
-      const int rows = t < n && on && h0 < h_hi ? (h_hi - h0 + stride - 1) / stride : 0;  // of this lane
-      const int rounds = (h_hi - h_lo + stride - 1) / stride;  // of the CTA: the shuffles take whole warps
-      const uint16_t* xr = static_cast<const uint16_t*>(xv.at) + b * xv.sb + l * xv.sl + h0 * xv.sh;
-      uint16_t* yr = y + ((static_cast<size_t>(b) * H + h0) * p.L + l) * D;
-      uint16_t* dr = BWD ? static_cast<uint16_t*>(dv.at) + b * dv.sb + l * dv.sl + h0 * dv.sh : nullptr;
-      const int64_t step_x = stride * xv.sh, step_y = static_cast<int64_t>(stride) * p.L * D, step_d = stride * dv.sh;
-      auto inside = [&](const uint16_t* at, const RowsView& v, int site) {
-        return dbg_in_range(at - static_cast<const uint16_t*>(v.at), D, (p.B - 1) * v.sb + (v.H - 1) * v.sh + (p.L - 1) * v.sl + D, p.status, site);
-      };
-      auto inside_y = [&](const uint16_t* at, int site) {
-        return dbg_in_range(at - y, D, static_cast<size_t>(p.B) * H * p.L * D, p.status, site);
-      };
-      uint4 xn[2] = {}, gn[2] = {};
-      auto load = [&](int i) {  // row i, at xr (and yr)
-        if (i >= rows) return;
-        if ((!BWD || norm) && inside(xr, xv, 100)) {
-          const uint4* v = reinterpret_cast<const uint4*>(xr);
-          xn[0] = v[c0], xn[1] = v[c1];
-        }
-        if (BWD && inside_y(yr, 101)) {
-          const uint4* v = reinterpret_cast<const uint4*>(yr);
-          gn[0] = v[c0], gn[1] = v[c1];
-        }
-      };
-      load(0);
-      __syncthreads();  // frac; the chunk before is done with cs
+    for (long long t0 = t_first; t0 < t_end; t0 += Gm::TOKENS) {
+      const int n = static_cast<int>(t_end - t0 < Gm::TOKENS ? t_end - t0 : Gm::TOKENS);
+      __syncthreads();  // frac; the tokens before are done with
+      if (threadIdx.x < n) {
+        const long long token = t0 + threadIdx.x, b = token / p.L, l = token - b * p.L;
+        offsets[threadIdx.x] = b * xv.sb + l * xv.sl;
+        offsets[Gm::TOKENS + threadIdx.x] = (b * H * p.L + l) * D;
+        if (BWD) offsets[2 * Gm::TOKENS + threadIdx.x] = b * dv.sb + l * dv.sl;
+      }
       for (int i = threadIdx.x; i < n * half; i += kRopeThreads) {
-        const int ti = i / half, pair = i - ti * half;
+        const int t = i / half, pair = i - t * half;
         int a = p.axis ? __ldg(p.axis + pair) : 0;
         a = a < p.axes ? a : p.axes - 1;
         float c, s;
-        turn(__ldg(p.pos + a * tokens + t0 + ti), frac[pair], c, s);
-        cs[ti][0][pair] = c, cs[ti][1][pair] = BWD ? -s : s;
+        turn(__ldg(p.pos + a * tokens + t0 + t), frac[pair], c, s);
+        cs[t * D + pair] = c, cs[t * D + D / 2 + pair] = BWD ? -s : s;
       }
       __syncthreads();
+      // rows head by head: this group's are group, group + GROUPS, ... of (h_hi - h_lo) * n
+      const int rows = (h_hi - h_lo) * n, rounds = (rows + Gm::GROUPS - 1) / Gm::GROUPS;  // (the shuffles take whole warps)
+      const int step_h = Gm::GROUPS / n, step_t = Gm::GROUPS - step_h * n;
+      auto inside = [&](long long at, const RowsView& v, int site) {
+        return dbg_in_range(at, D, (p.B - 1) * v.sb + (v.H - 1) * v.sh + (p.L - 1) * v.sl + D, p.status, site);
+      };
+      auto inside_y = [&](long long at, int site) { return dbg_in_range(at, D, static_cast<size_t>(p.B) * H * p.L * D, p.status, site); };
+      int ahead_h = h_lo + group / n, ahead_t = group % n, ahead = 0;  // the row that is fetched next
+      auto fetch = [&]() {
+        if (on && ahead * Gm::GROUPS + group < rows) {
+          const uint32_t slot = ring + (ahead % DEPTH) * (Gm::PIECES * kRopeThreads * 16);
+          const long long xo = offsets[ahead_t] + ahead_h * xv.sh;
+          if ((!BWD || norm) && inside(xo, xv, 100)) {
+            const uint4* v = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(xv.at) + xo);
+            cp_async16(slot, v + c0, true), cp_async16(slot + kRopeThreads * 16, v + c1, true);
+          }
+          if constexpr (BWD) {
+            const long long yo = offsets[Gm::TOKENS + ahead_t] + static_cast<long long>(ahead_h) * p.L * D;
+            if (inside_y(yo, 101)) {
+              const uint4* v = reinterpret_cast<const uint4*>(y + yo);
+              cp_async16(slot + 2 * kRopeThreads * 16, v + c0, true), cp_async16(slot + 3 * kRopeThreads * 16, v + c1, true);
+            }
+          }
+        }
+        cp_async_commit();
+        ++ahead, ahead_h += step_h, ahead_t += step_t;
+        if (ahead_t >= n) ahead_t -= n, ++ahead_h;
+      };
+#pragma unroll
+      for (int i = 0; i < DEPTH - 1; ++i) fetch();
+      int h = h_lo + group / n, t = group % n;
 #pragma unroll 1
       for (int i = 0; i < rounds; ++i) {
-        const bool live = i < rows;
-        uint4 xp[2] = {xn[0], xn[1]}, gp[2] = {gn[0], gn[1]};
-        xr += step_x;
-        uint16_t* const yi = yr;
-        yr += step_y;
-        load(i + 1);
-        float c[8], s[8];
+        const bool live = on && i * Gm::GROUPS + group < rows;
+        fetch();
+        cp_async_wait<DEPTH - 1>();
+        const uint32_t slot = ring + (i % DEPTH) * (Gm::PIECES * kRopeThreads * 16);
+        // this token's cosines and sines, as rotate16 takes them
+        constexpr int NC = INTERLEAVED ? 8 : 4;
+        uint64_t c[NC], s[NC], ns[INTERLEAVED ? 1 : 4];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           float4 cv = make_float4(1.f, 1.f, 1.f, 1.f), sv = make_float4(0.f, 0.f, 0.f, 0.f);
           if (k ? turns1 : turns0) {
-            cv = *reinterpret_cast<const float4*>(&cs[t][0][k ? pair1 : pair0]);
-            sv = *reinterpret_cast<const float4*>(&cs[t][1][k ? pair1 : pair0]);
+            cv = *reinterpret_cast<const float4*>(cs + t * D + (k ? pair1 : pair0));
+            sv = *reinterpret_cast<const float4*>(cs + t * D + D / 2 + (k ? pair1 : pair0));
           }
-          c[4 * k] = cv.x, c[4 * k + 1] = cv.y, c[4 * k + 2] = cv.z, c[4 * k + 3] = cv.w;
-          s[4 * k] = sv.x, s[4 * k + 1] = sv.y, s[4 * k + 2] = sv.z, s[4 * k + 3] = sv.w;
+          if constexpr (INTERLEAVED) {
+            c[4 * k] = f2_pack(cv.x, cv.x), c[4 * k + 1] = f2_pack(cv.y, cv.y), c[4 * k + 2] = f2_pack(cv.z, cv.z), c[4 * k + 3] = f2_pack(cv.w, cv.w);
+            s[4 * k] = f2_pack(-sv.x, sv.x), s[4 * k + 1] = f2_pack(-sv.y, sv.y), s[4 * k + 2] = f2_pack(-sv.z, sv.z), s[4 * k + 3] = f2_pack(-sv.w, sv.w);
+          } else {
+            c[2 * k] = f2_pack(cv.x, cv.y), c[2 * k + 1] = f2_pack(cv.z, cv.w);
+            s[2 * k] = f2_pack(sv.x, sv.y), s[2 * k + 1] = f2_pack(sv.z, sv.w);
+            ns[2 * k] = f2_pack(-sv.x, -sv.y), ns[2 * k + 1] = f2_pack(-sv.z, -sv.w);
+          }
         }
-        float f[16];
+        uint64_t f[8];
         if constexpr (!BWD) {
-          unpack8<BF16>(xp[0], f), unpack8<BF16>(xp[1], f + 8);
+          const uint4 xp[2] = {ld_shared_v4(slot), ld_shared_v4(slot + kRopeThreads * 16)};
+          unpack16<BF16>(xp, f);
           if (norm) {
-            float ss = 0.f;
+            uint64_t ss[2] = {f2_mul(f[0], f[0]), f2_mul(f[1], f[1])};
 #pragma unroll
-            for (int e = 0; e < 16; ++e) ss = fmaf(f[e], f[e], ss);
-            const float r = rsqrtf(group_sum<Gm::GROUP>(ss) * (1.f / D) + p.eps);
-            float w[16];
-            unpack8<BF16>(wp[0], w), unpack8<BF16>(wp[1], w + 8);
+            for (int e = 2; e < 8; ++e) ss[e & 1] = f2_fma(f[e], f[e], ss[e & 1]);
+            const float r = rsqrtf(group_sum<Ln::GROUP>(on ? f2_total(ss) : 0.f) * (1.f / D) + p.eps);
+            const uint64_t rr = f2_pack(r, r);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) f[e] *= r * w[e];
+            for (int e = 0; e < 8; ++e) f[e] = f2_mul(f2_mul(f[e], rr), w[e]);
           }
-          rotate16<INTERLEAVED>(f, c, s);
-          if (live && inside_y(yi, 102)) {
-            uint4* v = reinterpret_cast<uint4*>(yi);
-            v[c0] = pack8<BF16>(f), v[c1] = pack8<BF16>(f + 8);
+          rotate16<INTERLEAVED>(f, c, s, ns);
+          if (live) {
+            const long long yo = offsets[Gm::TOKENS + t] + static_cast<long long>(h) * p.L * D;
+            if (inside_y(yo, 102)) store16<BF16>(y + yo, c0, c1, f);
           }
         } else {
-          unpack8<BF16>(gp[0], f), unpack8<BF16>(gp[1], f + 8);
-          rotate16<INTERLEAVED>(f, c, s);
+          const uint4 gp[2] = {ld_shared_v4(slot + 2 * kRopeThreads * 16), ld_shared_v4(slot + 3 * kRopeThreads * 16)};
+          unpack16<BF16>(gp, f);
+          rotate16<INTERLEAVED>(f, c, s, ns);
           if (norm) {
-            float x[16], ss = 0.f, gx = 0.f;
-            unpack8<BF16>(xp[0], x), unpack8<BF16>(xp[1], x + 8);
-            float w[16];
-            unpack8<BF16>(wp[0], w), unpack8<BF16>(wp[1], w + 8);
+            const uint4 xp[2] = {ld_shared_v4(slot), ld_shared_v4(slot + kRopeThreads * 16)};
+            uint64_t x[8], ss[2] = {0, 0}, gx[2] = {0, 0};
+            unpack16<BF16>(xp, x);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) ss = fmaf(x[e], x[e], ss), gx = fmaf(f[e] * w[e], x[e], gx);
-            const float r = rsqrtf(group_sum<Gm::GROUP>(ss) * (1.f / D) + p.eps);
-            const float m = group_sum<Gm::GROUP>(gx) * (1.f / D) * r * r;
-            if (live) {  // (what an idle lane's registers hold adds nothing)
+            for (int e = 0; e < 8; ++e) {
+              ss[e & 1] = f2_fma(x[e], x[e], ss[e & 1]);
+              gx[e & 1] = f2_fma(f2_mul(f[e], w[e]), x[e], gx[e & 1]);
+            }
+            const float r = rsqrtf(group_sum<Ln::GROUP>(on ? f2_total(ss) : 0.f) * (1.f / D) + p.eps);
+            const float m = -group_sum<Ln::GROUP>(on ? f2_total(gx) : 0.f) * (1.f / D) * r * r;
+            const uint64_t rr = f2_pack(r, r), mm = f2_pack(m, m);
+            if (live) {  // (what an idle lane's ring holds adds nothing)
 #pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                dw[e] = fmaf(f[e] * r, x[e], dw[e]);
-                f[e] = r * (f[e] * w[e] - x[e] * m);
+              for (int e = 0; e < 8; ++e) {
+                dw[e] = f2_fma(f2_mul(f[e], rr), x[e], dw[e]);
+                f[e] = f2_mul(rr, f2_fma(x[e], mm, f2_mul(f[e], w[e])));
               }
             }
           }
-          if (live && inside(dr, dv, 103)) {
-            uint4* v = reinterpret_cast<uint4*>(dr);
-            v[c0] = pack8<BF16>(f), v[c1] = pack8<BF16>(f + 8);
+          if (live) {
+            const long long dxo = offsets[2 * Gm::TOKENS + t] + h * dv.sh;
+            if (inside(dxo, dv, 103)) store16<BF16>(static_cast<uint16_t*>(dv.at) + dxo, c0, c1, f);
           }
-          dr += step_d;
         }
+        h += step_h, t += step_t;
+        if (t >= n) t -= n, ++h;
       }
+      cp_async_wait<0>();
     }
     if constexpr (BWD) {
       if (!norm) continue;
       // rows of the warp, then its CTA's warps, in a fixed order
 #pragma unroll
-      for (int e = 0; e < 16; ++e)
+      for (int e = 0; e < 8; ++e)
 #pragma unroll
-        for (int m = Gm::GROUP; m < 32; m <<= 1) dw[e] += __shfl_xor_sync(0xffffffffu, dw[e], m);
+        for (int m = Ln::GROUP; m < 32; m <<= 1) dw[e] = f2_add(dw[e], __shfl_xor_sync(0xffffffffu, dw[e], m));
       __syncthreads();
-      if (lane < Gm::GROUP && on) {
+      if (lane < Ln::GROUP && on) {
 #pragma unroll
-        for (int e = 0; e < 16; ++e) dw_sum[warp][(e < 8 ? c0 : c1) * 8 + (e & 7)] = dw[e];
+        for (int e = 0; e < 8; ++e) {
+          float* at = dw_sum + warp * D + (e < 4 ? c0 : c1) * 8 + 2 * (e & 3);
+          f2_unpack(dw[e], at[0], at[1]);
+        }
       }
       __syncthreads();
       for (int d = threadIdx.x; d < D; d += kRopeThreads) {
         float x = 0.f;
 #pragma unroll
-        for (int w = 0; w < WARPS; ++w) x += dw_sum[w][d];
+        for (int k = 0; k < WARPS; ++k) x += dw_sum[k * D + d];
         p.part[(static_cast<size_t>(blockIdx.x) * 2 + which) * D + d] = x;
       }
     }

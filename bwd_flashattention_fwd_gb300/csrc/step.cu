@@ -86,13 +86,16 @@ attn_status_t check_rope(const void* q, const void* k, const void* qw, const voi
 
 template <int D, bool BF16, bool INTERLEAVED, bool BWD>
 int rope_impl(const RopeParams& p, int num_sms, cudaStream_t stream) {
+  using Gm = RopeGeom<D, BWD>;
   const int sms = num_sms < kTreeMaxCtas ? num_sms : kTreeMaxCtas;
-  const long long tokens = static_cast<long long>(p.B) * p.L, most = static_cast<long long>(BWD ? kRopeBwdPerSm : kRopeFwdPerSm) * sms;
+  const long long tokens = static_cast<long long>(p.B) * p.L, most = static_cast<long long>(Gm::PER_SM) * sms;
   // few tokens: their heads are shared out too, one round of the CTA's groups at least
-  constexpr int groups = kRopeThreads / RowLanes<D>::GROUP;
-  const int blocks = static_cast<int>(tokens < most ? tokens : most), heads = (p.x[0].H + groups - 1) / groups;
+  const int blocks = static_cast<int>(tokens < most ? tokens : most), heads = (p.x[0].H + Gm::GROUPS - 1) / Gm::GROUPS;
   const int parts = most / blocks < heads ? static_cast<int>(most / blocks) : heads, grid = blocks * parts;
-  const int r = launch_dependent(rope_kernel<D, BF16, INTERLEAVED, BWD>, dim3(grid), kRopeThreads, 0, stream, p, parts);
+  const auto kern = rope_kernel<D, BF16, INTERLEAVED, BWD>;
+  static std::atomic<uint64_t> done{0};
+  if (!set_smem_limit(kern, Gm::SMEM, done)) return kLaunchCudaError;
+  const int r = launch_dependent(kern, dim3(grid), kRopeThreads, Gm::SMEM, stream, p, parts);
   if (r != kLaunchOk || !BWD || !p.w[0]) return r;
   return launch_dependent(rope_dw_kernel, dim3(2 * D / 32), 256, 0, stream, p, grid);
 }
@@ -140,7 +143,7 @@ long long pool_rows(int Hkv, int n_pages, int page_size) { return static_cast<lo
 template <int D, bool BF16>
 int write_impl(const PagedWriteParams& p, int num_sms, cudaStream_t stream) {
   constexpr int per_cta = kPagedThreads / RowLanes<D>::GROUP;
-  const long long ctas = (2LL * p.B * p.c.Hkv * p.T + per_cta - 1) / per_cta, most = 8LL * num_sms;
+  const long long ctas = (static_cast<long long>(p.B) * p.c.Hkv * p.T + per_cta - 1) / per_cta, most = 8LL * num_sms;
   const dim3 grid(static_cast<unsigned>(ctas < most ? ctas : most));
   return p.c.k_exp ? launch_dependent(attn_paged_write_kernel<D, BF16, true>, grid, kPagedThreads, 0, stream, p)
                    : launch_dependent(attn_paged_write_kernel<D, BF16, false>, grid, kPagedThreads, 0, stream, p);
@@ -149,7 +152,7 @@ int write_impl(const PagedWriteParams& p, int num_sms, cudaStream_t stream) {
 template <int D, bool BF16>
 int read_impl(const PagedReadParams& p, int num_sms, cudaStream_t stream) {
   const int room = p.c.per_seq << p.c.shift, heads = p.B * p.c.Hkv;
-  const long long blocks = (static_cast<long long>(p.Lk < room ? p.Lk : room) + kReadRows - 1) / kReadRows, most = 8LL * num_sms / heads + 1;
+  const long long blocks = (static_cast<long long>(p.Lk < room ? p.Lk : room) + read_rows(D) - 1) / read_rows(D), most = 8LL * num_sms / heads + 1;
   const dim3 grid(static_cast<unsigned>(blocks < most ? blocks : most), heads);
   return p.c.k_exp ? launch_dependent(attn_paged_read_kernel<D, BF16, true>, grid, kPagedThreads, 0, stream, p)
                    : launch_dependent(attn_paged_read_kernel<D, BF16, false>, grid, kPagedThreads, 0, stream, p);
@@ -178,9 +181,9 @@ attn_status_t check_paged_attn(int B, int Hq, int Hkv, int T, int page_size, int
   if (!supported_d(D) || B > kPagedMaxB) return ATTN_ERR_UNSUPPORTED;
   const long long rows = static_cast<long long>(Hq / Hkv) * T, room = static_cast<long long>(per_seq) * page_size;
   if (rows > kPagedMaxRows || room > kPagedMaxTokens) return ATTN_ERR_UNSUPPORTED;
-  // the units of work of the whole call are ints (steps of 64 keys at least)
+  // the units of work of the whole call are ints (steps of 32 keys at least)
   const long long blocks = (rows + paged_rows(static_cast<int>(rows), D) - 1) / paged_rows(static_cast<int>(rows), D);
-  if ((room / 64 + 4) * B * Hkv * blocks > 0x7fff0000LL) return ATTN_ERR_UNSUPPORTED;
+  if ((room / 32 + 4) * B * Hkv * blocks > 0x7fff0000LL) return ATTN_ERR_UNSUPPORTED;
   return ATTN_OK;
 }
 

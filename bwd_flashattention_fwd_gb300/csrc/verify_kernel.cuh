@@ -22,7 +22,7 @@
 
 namespace gbattn {
 
-constexpr int kVerifyThreads = 512;
+constexpr int kVerifyThreads = 256;
 constexpr int kVerifyCluster = 8;
 
 // A probability as hi 2^-22 + lo 2^-45, both read off the bits of a float that a
@@ -42,9 +42,9 @@ __device__ __forceinline__ Fixed prob_fixed(float x) {
 // A sum of a few weights max(p - q, 0), in multiples of 2^-45 (32 bits hold 256 terms).
 struct FixedSum {
   int hi = 0, lo = 0;
-  __device__ __forceinline__ void add(float p, float q, bool lost) {
+  __device__ __forceinline__ void add(float p, float q) {
     const Fixed a = prob_fixed(p), b = prob_fixed(q);
-    if (p > q && !lost) hi += a.hi - b.hi, lo += a.lo - b.lo;
+    if (p > q) hi += a.hi - b.hi, lo += a.lo - b.lo;
   }
   __device__ __forceinline__ uint64_t value() const {
     return static_cast<uint64_t>(static_cast<long long>(hi) * (1 << 23) + lo);
@@ -65,7 +65,7 @@ __device__ __forceinline__ uint64_t ld_cluster_u64(uint32_t addr) {
 
 // A cluster per sequence; warp w of CTA c holds a contiguous part of the vocabulary.  VEC: rows start on 16 bytes.
 template <bool VEC>
-__global__ void __launch_bounds__(kVerifyThreads, 3) attn_draft_verify_kernel(const VerifyParams p) {
+__global__ void __launch_bounds__(kVerifyThreads, 6) attn_draft_verify_kernel(const VerifyParams p) {
   constexpr int WARPS = kVerifyThreads / 32, W = VEC ? 4 : 1, STEP = 32 * W;
   __shared__ int cut;
   __shared__ uint64_t part[2][WARPS];  // sums of this CTA's warps (second row: of p alone, where the residual is empty)
@@ -103,10 +103,9 @@ __global__ void __launch_bounds__(kVerifyThreads, 3) attn_draft_verify_kernel(co
     return static_cast<int>(at < p.V ? at : p.V);
   };
 
-  auto load = [&](int x, int to, bool with_q, float (&a)[W], float (&q)[W]) {  // this lane's tokens x .. (zeros from `to` on)
+  auto load = [&](int x, bool with_q, float (&a)[W], float (&q)[W]) {  // tokens x .. x + W - 1
 #pragma unroll
-    for (int k = 0; k < W; ++k) a[k] = q[k] = 0.f;
-    if (x >= to) return;
+    for (int k = 0; k < W; ++k) q[k] = 0.f;
     if constexpr (VEC) {
       const float4 v = __ldg(reinterpret_cast<const float4*>(prow + x));
       a[0] = v.x, a[1] = v.y, a[2] = v.z, a[3] = v.w;
@@ -126,21 +125,26 @@ __global__ void __launch_bounds__(kVerifyThreads, 3) attn_draft_verify_kernel(co
     for (; x + (N - 1) * STEP < to; x += N * STEP) {
       float a[N][W], q[N][W];
 #pragma unroll
-      for (int i = 0; i < N; ++i) load(x + i * STEP, to, with_q, a[i], q[i]);
+      for (int i = 0; i < N; ++i) load(x + i * STEP, with_q, a[i], q[i]);
       FixedSum s;
 #pragma unroll
       for (int i = 0; i < N; ++i)
 #pragma unroll
-        for (int k = 0; k < W; ++k) s.add(a[i][k], q[i][k], x + i * STEP + k == without);
+        for (int k = 0; k < W; ++k) s.add(a[i][k], q[i][k]);
       sum += s.value();
     }
     for (; x < to; x += STEP) {
       float a[W], q[W];
-      load(x, to, with_q, a, q);
+      load(x, with_q, a, q);
       FixedSum s;
 #pragma unroll
-      for (int k = 0; k < W; ++k) s.add(a[k], q[k], x + k == without);
+      for (int k = 0; k < W; ++k) s.add(a[k], q[k]);
       sum += s.value();
+    }
+    if (lane == 0 && without >= from && without < to) {  // a deterministic draft's token has no weight
+      FixedSum s;
+      s.add(__ldg(prow + without), 0.f);
+      sum -= s.value();
     }
     return sum;
   };
@@ -197,13 +201,15 @@ __global__ void __launch_bounds__(kVerifyThreads, 3) attn_draft_verify_kernel(co
     for (int x0 = from; x0 < to; x0 += WARPS * STEP) {
       const int x = x0 + warp * STEP + lane * W;
       float a[W], q[W];
-      load(x, to, with_q, a, q);
+#pragma unroll
+      for (int k = 0; k < W; ++k) a[k] = q[k] = 0.f;
+      if (x < to) load(x, with_q, a, q);
       uint64_t v[W], own = 0;
 #pragma unroll
       for (int k = 0; k < W; ++k) {
         FixedSum s;
-        s.add(a[k], q[k], x + k == without);
-        v[k] = s.value();
+        s.add(a[k], q[k]);
+        v[k] = x + k == without ? 0 : s.value();
         own += v[k];
       }
       uint64_t upto = own;  // inclusive sums over the lanes
