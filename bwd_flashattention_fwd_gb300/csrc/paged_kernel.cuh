@@ -113,21 +113,36 @@ __global__ void __launch_bounds__(kPagedThreads) attn_paged_write_kernel(const P
   }
 }
 
-// The codes' values in 16 bits; one that rounds past the type's largest value becomes that.
-template <bool BF16>
+// The codes' values in 16 bits; EDGE: one that rounds past the type's largest value becomes that.
+template <bool BF16, bool EDGE>
 __device__ __forceinline__ uint32_t dequant_pair(uint32_t pair, float by) {
-  constexpr float most = BF16 ? 3.3895313892515355e38f : 65504.f;
   float2 v = e4m3_unpack(pair);
   v.x *= by, v.y *= by;
-  if (fabsf(v.x) > most) v.x = copysignf(most, v.x);
-  if (fabsf(v.y) > most) v.y = copysignf(most, v.y);
+  if constexpr (EDGE) {
+    constexpr float most = BF16 ? 3.3895313892515355e38f : 65504.f;
+    if (fabsf(v.x) > most) v.x = copysignf(most, v.x);
+    if (fabsf(v.y) > most) v.y = copysignf(most, v.y);
+  }
   return Elem<BF16>::pack(v.x, v.y);
+}
+
+template <bool BF16, bool EDGE>
+__device__ __forceinline__ void dequant16(const uint4& w, float by, uint4* d) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+  uint32_t o[8];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    o[2 * k] = dequant_pair<BF16, EDGE>(u[k] & 0xffffu, by);
+    o[2 * k + 1] = dequant_pair<BF16, EDGE>(u[k] >> 16, by);
+  }
+  d[0] = make_uint4(o[0], o[1], o[2], o[3]);
+  d[1] = make_uint4(o[4], o[5], o[6], o[7]);
 }
 
 // A block: read_rows tokens of one sequence and head.  A thread holds the same
 // 16 values of several tokens' K and V, whose pages it looks up first, so that
 // all its loads are in flight together.
-constexpr int kReadTokens = 4;  // of a thread
+constexpr int kReadTokens = 2;  // of a thread
 constexpr int read_rows(int D) { return kReadTokens * (kPagedThreads / (D / 16)); }
 
 template <int D, bool BF16, bool Q8>
@@ -165,17 +180,12 @@ __global__ void __launch_bounds__(kPagedThreads) attn_paged_read_kernel(const Pa
 #pragma unroll
         for (int v = 0; v < 2; ++v) {
           if (from[i] < 0) continue;
-          const float by = exp2_int(e[v][i]);
-          const uint32_t u[4] = {w[v][i].x, w[v][i].y, w[v][i].z, w[v][i].w};
-          uint32_t o[8];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            o[2 * k] = dequant_pair<BF16>(u[k] & 0xffffu, by);
-            o[2 * k + 1] = dequant_pair<BF16>(u[k] >> 16, by);
-          }
           uint4* d = static_cast<uint4*>(v ? p.v : p.k) + (out0 + row[i]) * (D / 8) + 2 * c;
-          d[0] = make_uint4(o[0], o[1], o[2], o[3]);
-          d[1] = make_uint4(o[4], o[5], o[6], o[7]);
+          // 448 * 2^e is within the type up to these
+          if (e[v][i] <= (BF16 ? 118 : 7))
+            dequant16<BF16, false>(w[v][i], exp2_int(e[v][i]), d);
+          else
+            dequant16<BF16, true>(w[v][i], exp2_int(e[v][i]), d);
         }
     } else {
       uint4 w[2][N][2];

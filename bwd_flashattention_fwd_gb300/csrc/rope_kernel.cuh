@@ -115,13 +115,13 @@ template <int D, bool BWD>
 struct RopeGeom {
   static constexpr int GROUPS = kRopeThreads / RowLanes<D>::GROUP;
   static constexpr int PER_SM = BWD ? kRopeBwdPerSm : kRopeFwdPerSm;
-  static constexpr int TOKENS = 2048 / D;                       // 8 KB of sines and cosines
+  static constexpr int TOKENS = 4096 / D;                       // 16 KB of sines and cosines
   static constexpr int DEPTH = 4;
   static constexpr int PIECES = BWD ? 4 : 2;                    // 16-byte pieces of a row: x (and dy)
   static constexpr int RING = DEPTH * PIECES * kRopeThreads * 16;
   static constexpr int CS = TOKENS * D * 4;                     // [TOKENS][2][D / 2] floats
-  static constexpr int OFFSETS = TOKENS * 3 * 8;                // of x, y and dx
-  static constexpr int SUMS = BWD ? kRopeThreads / 32 * D * 4 : 0;
+  static constexpr int OFFSETS = TOKENS * 6 * 8;                // of x, y and dx, of q and k
+  static constexpr int SUMS = BWD ? 2 * kRopeThreads / 32 * D * 4 : 0;
   static constexpr int SMEM = RING + CS + OFFSETS + SUMS;
 };
 
@@ -133,12 +133,11 @@ __global__ void __launch_bounds__(kRopeThreads, RopeGeom<D, BWD>::PER_SM) rope_k
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t frac[D / 2];
   float* const cs = reinterpret_cast<float*>(smem + Gm::RING);                                  // [TOKENS][2][D / 2]
-  long long* const offsets = reinterpret_cast<long long*>(smem + Gm::RING + Gm::CS);            // [3][TOKENS]
-  float* const dw_sum = reinterpret_cast<float*>(smem + Gm::RING + Gm::CS + Gm::OFFSETS);       // [WARPS][D]
+  long long* const offsets = reinterpret_cast<long long*>(smem + Gm::RING + Gm::CS);            // [2][3][TOKENS]
+  float* const dw_sum = reinterpret_cast<float*>(smem + Gm::RING + Gm::CS + Gm::OFFSETS);       // [2][WARPS][D]
   grid_dependency_wait();  // the kernels before this one are complete
   if (threadIdx.x == 0) grid_launch_dependents();
   const int half = p.rot / 2;
-  for (int i = threadIdx.x; i < D / 2; i += kRopeThreads) frac[i] = i < half ? turn_fraction(p.freq[i]) : 0;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int j = lane % Ln::GROUP, group = threadIdx.x / Ln::GROUP;
   const bool on = j < Ln::LANES;
@@ -159,82 +158,103 @@ __global__ void __launch_bounds__(kRopeThreads, RopeGeom<D, BWD>::PER_SM) rope_k
   const bool turns0 = on && pair0 < half, turns1 = on && pair1 < half;
   const bool norm = p.w[0] != nullptr;
   const uint32_t ring = smem_u32(smem) + threadIdx.x * 16;  // piece k of slot s: + (s * PIECES + k) * kRopeThreads * 16
-  const long long tokens = static_cast<long long>(p.B) * p.L;
-  const int part = blockIdx.x % parts;
-  const long long block = blockIdx.x / parts, blocks = gridDim.x / parts;
-  const long long t_first = tokens * block / blocks, t_end = tokens * (block + 1) / blocks;
+  const int tokens = p.B * p.L;  // (at most 2^30)
+  const int part = blockIdx.x % parts, block = blockIdx.x / parts, blocks = gridDim.x / parts;
+  const int t_first = static_cast<int>(static_cast<long long>(tokens) * block / blocks);
+  const int t_end = static_cast<int>(static_cast<long long>(tokens) * (block + 1) / blocks);
+  const int q_lo = p.x[0].H * part / parts, q_n = p.x[0].H * (part + 1) / parts - q_lo;  // heads of q and of k
+  const int k_lo = p.x[1].H * part / parts, k_n = p.x[1].H * (part + 1) / parts - k_lo;
 #pragma unroll 1
-  for (int which = 0; which < 2; ++which) {
-    const RowsView xv = p.x[which], dv = p.dx[which];
-    uint16_t* const y = static_cast<uint16_t*>(p.y[which]);
-    const int H = xv.H, h_lo = H * part / parts, h_hi = H * (part + 1) / parts;
-    uint64_t w[8], dw[BWD ? 8 : 1];
-    {
-      uint4 wp[2] = {};
-      if (norm && on) {
-        const uint4* v = static_cast<const uint4*>(p.w[which]);
-        wp[0] = __ldg(v + c0), wp[1] = __ldg(v + c1);
-      }
-      unpack16<BF16>(wp, w);
+  for (int t0 = t_first; t0 < t_end; t0 += Gm::TOKENS) {
+    const int n = min(t_end - t0, Gm::TOKENS);
+    if (t0 == t_first) {
+      for (int i = threadIdx.x; i < half; i += kRopeThreads) frac[i] = turn_fraction(p.freq[i]);
+    } else {
+      __syncthreads();  // the tokens before are done with
     }
+    if (threadIdx.x < n) {
+      const int token = t0 + threadIdx.x, b = token / p.L, l = token - b * p.L;
 #pragma unroll
-    for (uint64_t& x : dw) x = 0;
-#pragma unroll 1
-    for (long long t0 = t_first; t0 < t_end; t0 += Gm::TOKENS) {
-      const int n = static_cast<int>(t_end - t0 < Gm::TOKENS ? t_end - t0 : Gm::TOKENS);
-      __syncthreads();  // frac; the tokens before are done with
-      if (threadIdx.x < n) {
-        const long long token = t0 + threadIdx.x, b = token / p.L, l = token - b * p.L;
-        offsets[threadIdx.x] = b * xv.sb + l * xv.sl;
-        offsets[Gm::TOKENS + threadIdx.x] = (b * H * p.L + l) * D;
-        if (BWD) offsets[2 * Gm::TOKENS + threadIdx.x] = b * dv.sb + l * dv.sl;
+      for (int which = 0; which < 2; ++which) {
+        long long* const at = offsets + which * 3 * Gm::TOKENS + threadIdx.x;
+        at[0] = b * p.x[which].sb + l * p.x[which].sl;
+        at[Gm::TOKENS] = (static_cast<long long>(b) * p.x[which].H * p.L + l) * D;
+        if (BWD) at[2 * Gm::TOKENS] = b * p.dx[which].sb + l * p.dx[which].sl;
       }
-      for (int i = threadIdx.x; i < n * half; i += kRopeThreads) {
-        const int t = i / half, pair = i - t * half;
-        int a = p.axis ? __ldg(p.axis + pair) : 0;
-        a = a < p.axes ? a : p.axes - 1;
-        float c, s;
-        turn(__ldg(p.pos + a * tokens + t0 + t), frac[pair], c, s);
-        cs[t * D + pair] = c, cs[t * D + D / 2 + pair] = BWD ? -s : s;
-      }
-      __syncthreads();
-      // rows head by head: this group's are group, group + GROUPS, ... of (h_hi - h_lo) * n
-      const int rows = (h_hi - h_lo) * n, rounds = (rows + Gm::GROUPS - 1) / Gm::GROUPS;  // (the shuffles take whole warps)
-      const int step_h = Gm::GROUPS / n, step_t = Gm::GROUPS - step_h * n;
-      auto inside = [&](long long at, const RowsView& v, int site) {
-        return dbg_in_range(at, D, (p.B - 1) * v.sb + (v.H - 1) * v.sh + (p.L - 1) * v.sl + D, p.status, site);
-      };
-      auto inside_y = [&](long long at, int site) { return dbg_in_range(at, D, static_cast<size_t>(p.B) * H * p.L * D, p.status, site); };
-      int ahead_h = h_lo + group / n, ahead_t = group % n, ahead = 0;  // the row that is fetched next
-      auto fetch = [&]() {
-        if (on && ahead * Gm::GROUPS + group < rows) {
-          const uint32_t slot = ring + (ahead % DEPTH) * (Gm::PIECES * kRopeThreads * 16);
-          const long long xo = offsets[ahead_t] + ahead_h * xv.sh;
-          if ((!BWD || norm) && inside(xo, xv, 100)) {
-            const uint4* v = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(xv.at) + xo);
-            cp_async16(slot, v + c0, true), cp_async16(slot + kRopeThreads * 16, v + c1, true);
-          }
-          if constexpr (BWD) {
-            const long long yo = offsets[Gm::TOKENS + ahead_t] + static_cast<long long>(ahead_h) * p.L * D;
-            if (inside_y(yo, 101)) {
-              const uint4* v = reinterpret_cast<const uint4*>(y + yo);
-              cp_async16(slot + 2 * kRopeThreads * 16, v + c0, true), cp_async16(slot + 3 * kRopeThreads * 16, v + c1, true);
-            }
+    }
+    __syncthreads();
+    // Rows head by head, a round of GROUPS of them at a time (whole rounds of q, then of k): this group's row of round
+    // r of q is row r * GROUPS + group of q_n * n.  (The shuffles take whole warps.)
+    const int q_rounds = (q_n * n + Gm::GROUPS - 1) / Gm::GROUPS, k_rounds = (k_n * n + Gm::GROUPS - 1) / Gm::GROUPS;
+    const int step_h = Gm::GROUPS / n, step_t = Gm::GROUPS - step_h * n;
+    const int first_h = group / n, first_t = group - first_h * n;
+    auto inside = [&](long long at, const RowsView& v, int site) {
+      return dbg_in_range(at, D, (p.B - 1) * v.sb + (v.H - 1) * v.sh + (p.L - 1) * v.sl + D, p.status, site);
+    };
+    auto inside_y = [&](long long at, int which, int site) {
+      return dbg_in_range(at, D, static_cast<size_t>(p.B) * p.x[which].H * p.L * D, p.status, site);
+    };
+    int ahead = 0, ahead_h = first_h, ahead_t = first_t;  // the round that is fetched next, and its row
+    auto fetch = [&]() {
+      const bool is_k = ahead >= q_rounds;
+      if (on && ahead < q_rounds + k_rounds && ahead_h < (is_k ? k_n : q_n)) {
+        const uint32_t slot = ring + (ahead % DEPTH) * (Gm::PIECES * kRopeThreads * 16);
+        const int which = is_k ? 1 : 0, h = (is_k ? k_lo : q_lo) + ahead_h;
+        const long long* const at = offsets + which * 3 * Gm::TOKENS + ahead_t;
+        const long long xo = at[0] + h * (is_k ? p.x[1].sh : p.x[0].sh);
+        if ((!BWD || norm) && inside(xo, p.x[which], 100)) {
+          const uint4* v = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(is_k ? p.x[1].at : p.x[0].at) + xo);
+          cp_async16(slot, v + c0, true), cp_async16(slot + kRopeThreads * 16, v + c1, true);
+        }
+        if constexpr (BWD) {
+          const long long yo = at[Gm::TOKENS] + static_cast<long long>(h) * p.L * D;
+          if (inside_y(yo, which, 101)) {
+            const uint4* v = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(is_k ? p.y[1] : p.y[0]) + yo);
+            cp_async16(slot + 2 * kRopeThreads * 16, v + c0, true), cp_async16(slot + 3 * kRopeThreads * 16, v + c1, true);
           }
         }
-        cp_async_commit();
-        ++ahead, ahead_h += step_h, ahead_t += step_t;
-        if (ahead_t >= n) ahead_t -= n, ++ahead_h;
-      };
+      }
+      cp_async_commit();
+      ++ahead, ahead_h += step_h, ahead_t += step_t;
+      if (ahead_t >= n) ahead_t -= n, ++ahead_h;
+      if (ahead == q_rounds) ahead_h = first_h, ahead_t = first_t;
+    };
 #pragma unroll
-      for (int i = 0; i < DEPTH - 1; ++i) fetch();
-      int h = h_lo + group / n, t = group % n;
+    for (int i = 0; i < DEPTH - 1; ++i) fetch();
+    for (int i = threadIdx.x; i < n * half; i += kRopeThreads) {  // (while the first rows are on their way)
+      const int t = i / half, pair = i - t * half;
+      int a = p.axis ? __ldg(p.axis + pair) : 0;
+      a = a < p.axes ? a : p.axes - 1;
+      float c, s;
+      turn(__ldg(p.pos + static_cast<long long>(a) * tokens + t0 + t), frac[pair], c, s);
+      cs[t * D + pair] = c, cs[t * D + D / 2 + pair] = BWD ? -s : s;
+    }
+    __syncthreads();
+    int round = 0;
 #pragma unroll 1
-      for (int i = 0; i < rounds; ++i) {
-        const bool live = on && i * Gm::GROUPS + group < rows;
+    for (int which = 0; which < 2; ++which) {
+      const int rounds = which ? k_rounds : q_rounds, h_n = which ? k_n : q_n, h_lo = which ? k_lo : q_lo;
+      const RowsView dv = p.dx[which];
+      uint16_t* const y = static_cast<uint16_t*>(p.y[which]);
+      const long long* const at = offsets + which * 3 * Gm::TOKENS;
+      uint64_t w[8], dw[BWD ? 8 : 1];
+      {
+        uint4 wp[2] = {};
+        if (norm && on) {
+          const uint4* v = static_cast<const uint4*>(p.w[which]);
+          wp[0] = __ldg(v + c0), wp[1] = __ldg(v + c1);
+        }
+        unpack16<BF16>(wp, w);
+      }
+#pragma unroll
+      for (uint64_t& x : dw) x = 0;
+      int h = first_h, t = first_t;
+#pragma unroll 1
+      for (int i = 0; i < rounds; ++i, ++round) {
+        const bool live = on && h < h_n;
         fetch();
         cp_async_wait<DEPTH - 1>();
-        const uint32_t slot = ring + (i % DEPTH) * (Gm::PIECES * kRopeThreads * 16);
+        const uint32_t slot = ring + (round % DEPTH) * (Gm::PIECES * kRopeThreads * 16);
         // this token's cosines and sines, as rotate16 takes them
         constexpr int NC = INTERLEAVED ? 8 : 4;
         uint64_t c[NC], s[NC], ns[INTERLEAVED ? 1 : 4];
@@ -269,8 +289,8 @@ __global__ void __launch_bounds__(kRopeThreads, RopeGeom<D, BWD>::PER_SM) rope_k
           }
           rotate16<INTERLEAVED>(f, c, s, ns);
           if (live) {
-            const long long yo = offsets[Gm::TOKENS + t] + static_cast<long long>(h) * p.L * D;
-            if (inside_y(yo, 102)) store16<BF16>(y + yo, c0, c1, f);
+            const long long yo = at[Gm::TOKENS + t] + static_cast<long long>(h_lo + h) * p.L * D;
+            if (inside_y(yo, which, 102)) store16<BF16>(y + yo, c0, c1, f);
           }
         } else {
           const uint4 gp[2] = {ld_shared_v4(slot + 2 * kRopeThreads * 16), ld_shared_v4(slot + 3 * kRopeThreads * 16)};
@@ -297,56 +317,59 @@ __global__ void __launch_bounds__(kRopeThreads, RopeGeom<D, BWD>::PER_SM) rope_k
             }
           }
           if (live) {
-            const long long dxo = offsets[2 * Gm::TOKENS + t] + h * dv.sh;
+            const long long dxo = at[2 * Gm::TOKENS + t] + (h_lo + h) * dv.sh;
             if (inside(dxo, dv, 103)) store16<BF16>(static_cast<uint16_t*>(dv.at) + dxo, c0, c1, f);
           }
         }
         h += step_h, t += step_t;
         if (t >= n) t -= n, ++h;
       }
-      cp_async_wait<0>();
-    }
-    if constexpr (BWD) {
-      if (!norm) continue;
-      // rows of the warp, then its CTA's warps, in a fixed order
+      if constexpr (BWD) {
+        if (!norm) continue;
+        // the warp's rows, added to those of the tokens before, in a fixed order
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
+        for (int e = 0; e < 8; ++e)
 #pragma unroll
-        for (int m = Ln::GROUP; m < 32; m <<= 1) dw[e] = f2_add(dw[e], __shfl_xor_sync(0xffffffffu, dw[e], m));
-      __syncthreads();
-      if (lane < Ln::GROUP && on) {
+          for (int m = Ln::GROUP; m < 32; m <<= 1) dw[e] = f2_add(dw[e], __shfl_xor_sync(0xffffffffu, dw[e], m));
+        if (lane < Ln::GROUP && on) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          float* at = dw_sum + warp * D + (e < 4 ? c0 : c1) * 8 + 2 * (e & 3);
-          f2_unpack(dw[e], at[0], at[1]);
+          for (int e = 0; e < 8; ++e) {
+            uint64_t* sum = reinterpret_cast<uint64_t*>(dw_sum + (which * WARPS + warp) * D + (e < 4 ? c0 : c1) * 8) + (e & 3);
+            *sum = t0 == t_first ? dw[e] : f2_add(*sum, dw[e]);
+          }
         }
       }
-      __syncthreads();
-      for (int d = threadIdx.x; d < D; d += kRopeThreads) {
-        float x = 0.f;
+    }
+    cp_async_wait<0>();
+  }
+  if constexpr (BWD) {
+    if (!norm) return;
+    __syncthreads();
+    for (int i = threadIdx.x; i < 2 * D; i += kRopeThreads) {  // the CTA's warps
+      const int which = i / D, d = i - which * D;
+      float x = 0.f;
 #pragma unroll
-        for (int k = 0; k < WARPS; ++k) x += dw_sum[k * D + d];
-        p.part[(static_cast<size_t>(blockIdx.x) * 2 + which) * D + d] = x;
-      }
+      for (int k = 0; k < WARPS; ++k) x += dw_sum[(which * WARPS + k) * D + d];
+      p.part[static_cast<size_t>(blockIdx.x) * 2 * D + i] = x;
     }
   }
 }
 
-// dw = the CTAs' partial sums, in a fixed order: a block per 32 columns, a warp per eighth of the CTAs.
-__global__ void __launch_bounds__(256) rope_dw_kernel(const RopeParams p, int n) {
-  __shared__ float sum[8][32];
+// dw = the CTAs' partial sums, in a fixed order: a block per 32 columns, a warp per 32nd of the CTAs.
+__global__ void __launch_bounds__(1024) rope_dw_kernel(const RopeParams p, int n) {
+  __shared__ float sum[32][32];
   grid_dependency_wait();
-  const int col = blockIdx.x * 32 + (threadIdx.x & 31), warp = threadIdx.x >> 5;
-  const int which = col / p.D, d = col - which * p.D;
+  const int lane = threadIdx.x & 31, col = blockIdx.x * 32 + lane, warp = threadIdx.x >> 5;
   float x = 0.f;
-#pragma unroll 8
-  for (int i = warp; i < n; i += 8) x += p.part[(static_cast<size_t>(i) * 2 + which) * p.D + d];
-  sum[warp][threadIdx.x & 31] = x;
+#pragma unroll 10
+  for (int i = warp; i < n; i += 32) x += p.part[static_cast<size_t>(i) * 2 * p.D + col];
+  sum[warp][lane] = x;
   __syncthreads();
   if (warp == 0) {
 #pragma unroll
-    for (int w = 1; w < 8; ++w) x += sum[w][threadIdx.x & 31];
-    p.dw[which][d] = x;
+    for (int w = 1; w < 32; ++w) x += sum[w][lane];
+    const int which = col / p.D;
+    p.dw[which][col - which * p.D] = x;
   }
 }
 

@@ -97,7 +97,7 @@ int rope_impl(const RopeParams& p, int num_sms, cudaStream_t stream) {
   if (!set_smem_limit(kern, Gm::SMEM, done)) return kLaunchCudaError;
   const int r = launch_dependent(kern, dim3(grid), kRopeThreads, Gm::SMEM, stream, p, parts);
   if (r != kLaunchOk || !BWD || !p.w[0]) return r;
-  return launch_dependent(rope_dw_kernel, dim3(2 * D / 32), 256, 0, stream, p, grid);
+  return launch_dependent(rope_dw_kernel, dim3(2 * D / 32), 1024, 0, stream, p, grid);
 }
 
 template <int D, bool BF16>
@@ -152,7 +152,7 @@ int write_impl(const PagedWriteParams& p, int num_sms, cudaStream_t stream) {
 template <int D, bool BF16>
 int read_impl(const PagedReadParams& p, int num_sms, cudaStream_t stream) {
   const int room = p.c.per_seq << p.c.shift, heads = p.B * p.c.Hkv;
-  const long long blocks = (static_cast<long long>(p.Lk < room ? p.Lk : room) + read_rows(D) - 1) / read_rows(D), most = 8LL * num_sms / heads + 1;
+  const long long blocks = (static_cast<long long>(p.Lk < room ? p.Lk : room) + read_rows(D) - 1) / read_rows(D), most = 64LL * num_sms / heads + 1;  // (blocks past a sequence's end leave at once)
   const dim3 grid(static_cast<unsigned>(blocks < most ? blocks : most), heads);
   return p.c.k_exp ? launch_dependent(attn_paged_read_kernel<D, BF16, true>, grid, kPagedThreads, 0, stream, p)
                    : launch_dependent(attn_paged_read_kernel<D, BF16, false>, grid, kPagedThreads, 0, stream, p);

@@ -65,7 +65,7 @@ __device__ __forceinline__ uint64_t ld_cluster_u64(uint32_t addr) {
 
 // A cluster per sequence; warp w of CTA c holds a contiguous part of the vocabulary.  VEC: rows start on 16 bytes.
 template <bool VEC>
-__global__ void __launch_bounds__(kVerifyThreads, 6) attn_draft_verify_kernel(const VerifyParams p) {
+__global__ void __launch_bounds__(kVerifyThreads, 4) attn_draft_verify_kernel(const VerifyParams p) {
   constexpr int WARPS = kVerifyThreads / 32, W = VEC ? 4 : 1, STEP = 32 * W;
   __shared__ int cut;
   __shared__ uint64_t part[2][WARPS];  // sums of this CTA's warps (second row: of p alone, where the residual is empty)
@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 6) attn_draft_verify_kernel(co
   auto sum_of = [&](int from, int to, bool with_q, int without) {  // this lane's share of a part
     uint64_t sum = 0;
     int x = from + lane * W;
-    constexpr int N = VEC ? 2 : 8;  // steps whose loads are in flight together
+    constexpr int N = VEC ? 4 : 8;  // steps whose loads are in flight together
     for (; x + (N - 1) * STEP < to; x += N * STEP) {
       float a[N][W], q[N][W];
 #pragma unroll
