@@ -108,21 +108,22 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
     lib.attn_cache_evict_workspace_bytes.restype = sz
     lib.attn_cache_evict.argtypes = [vp] * 10 + [sz, i64] + [ci] * 7 + [vp]
     lib.attn_cache_evict.restype = ci
-    lib.attn_qk_norm_rope.argtypes = [vp] * 11 + [ci] * 7 + [cf, ci, ci, vp]
+    at = ctypes.c_long  # an address as an integer (0: none): converted faster than c_void_p, which counts in the calls below
+    lib.attn_qk_norm_rope.argtypes = [at] * 11 + [ci] * 7 + [cf, ci, ci, vp]
     lib.attn_qk_norm_rope.restype = ci
     lib.attn_qk_norm_rope_workspace_bytes.argtypes = [ci]
     lib.attn_qk_norm_rope_workspace_bytes.restype = sz
-    lib.attn_qk_norm_rope_bwd.argtypes = [vp] * 14 + [sz] + [vp] * 4 + [ci] * 7 + [cf, ci, ci, vp]
+    lib.attn_qk_norm_rope_bwd.argtypes = [at] * 14 + [sz] + [at] * 4 + [ci] * 7 + [cf, ci, ci, vp]
     lib.attn_qk_norm_rope_bwd.restype = ci
-    lib.attn_paged_write.argtypes = [vp] * 10 + [ci] * 8 + [vp]
+    lib.attn_paged_write.argtypes = [at] * 10 + [ci] * 8 + [at]
     lib.attn_paged_write.restype = ci
-    lib.attn_paged_read.argtypes = [vp] * 8 + [i64] + [ci] * 8 + [vp]
+    lib.attn_paged_read.argtypes = [at] * 8 + [i64] + [ci] * 8 + [at]
     lib.attn_paged_read.restype = ci
     lib.attn_paged_workspace_bytes.argtypes = [ci] * 7
     lib.attn_paged_workspace_bytes.restype = sz
-    lib.attn_fwd_paged.argtypes = [vp] * 10 + [sz] + [ci] * 8 + [cf, ci, vp]
+    lib.attn_fwd_paged.argtypes = [at] * 10 + [sz] + [ci] * 8 + [cf, ci, vp]
     lib.attn_fwd_paged.restype = ci
-    lib.attn_draft_verify.argtypes = [vp] * 8 + [ci] * 3 + [vp]
+    lib.attn_draft_verify.argtypes = [at] * 8 + [ci] * 3 + [at]
     lib.attn_draft_verify.restype = ci
     lib.attn_last_device_status.argtypes = [vp]
     lib.attn_last_device_status.restype = ci
@@ -613,21 +614,22 @@ def attn_cache_evict(k, v, weight, pos, cache_len, seen, weight_out, pos_out, ca
 
 
 _Strides = ctypes.c_int64 * 3
-_strides_of: dict = {}  # the C arrays of the strides met so far (a few per model)
+_strides_of: dict = {}  # the C arrays of the strides met so far (a few per model), and their addresses
 
 
-def _row_strides(call: str, t, name: str):
-    """Strides between sequences, heads and tokens of a [B,H,L,D] tensor whose
-    rows are contiguous, for the C ABI."""
+def _row_strides(call: str, t, name: str) -> int:
+    """Address of the strides between sequences, heads and tokens of a [B,H,L,D]
+    tensor whose rows are contiguous, for the C ABI."""
     st = t.stride()
     got = _strides_of.get(st)
     if got is None:
         if st[3] != 1:
             raise ValueError(f"{call}: {name} of strides {st} has no contiguous rows")
-        if len(_strides_of) >= 256:
-            _strides_of.clear()
-        got = _strides_of[st] = _Strides(*st[:3])
-    return got
+        if len(_strides_of) >= 4096:
+            _strides_of.pop(next(iter(_strides_of)))  # (the oldest: a call in progress holds at most four)
+        arr = _Strides(*st[:3])
+        got = _strides_of[st] = (ctypes.addressof(arr), arr)
+    return got[0]
 
 
 def _refuse_rope(call, q, k, pos, freq, axis, dense, rows=(), f32=(), u8=()):
@@ -655,15 +657,17 @@ def attn_qk_norm_rope(q, k, q_out, k_out, pos, freq, q_weight=None, k_weight=Non
             and q_out.is_contiguous() and k_out.is_contiguous() and pos.is_contiguous() and freq.is_contiguous()
             and (k.shape, q_out.shape, k_out.shape, pos.shape[-2:], freq.shape) == ((B, Hkv, L, D), q.shape, k.shape, (B, L), (half,))
             and pos.dim() <= 3 and (axis is None or _plain(axis, _U8, dev, freq.shape))
-            and (q_weight is None or _plain(q_weight, dt, dev, w)) and (k_weight is None or _plain(k_weight, dt, dev, w))):
+            and (q_weight is k_weight is None or (q_weight is not None and k_weight is not None and q_weight.dtype is k_weight.dtype is dt
+                 and dev == q_weight.get_device() == k_weight.get_device() and q_weight.is_contiguous() and k_weight.is_contiguous()
+                 and q_weight.shape == w == k_weight.shape))):
         _refuse_rope("attn_qk_norm_rope", q, k, pos, freq, axis,
                      ((q_weight, w, "q_weight"), (k_weight, w, "k_weight"), (q_out, (B, Hq, L, D), "q_out"), (k_out, (B, Hkv, L, D), "k_out")))
-    st = load_library().attn_qk_norm_rope(
-        q.data_ptr(), k.data_ptr(), _ptr(q_weight), _ptr(k_weight), pos.data_ptr(), freq.data_ptr(), _ptr(axis),
+    st = (_lib or load_library()).attn_qk_norm_rope(
+        q.data_ptr(), k.data_ptr(), 0 if q_weight is None else q_weight.data_ptr(), 0 if k_weight is None else k_weight.data_ptr(), pos.data_ptr(), freq.data_ptr(), 0 if axis is None else axis.data_ptr(),
         q_out.data_ptr(), k_out.data_ptr(), _row_strides("attn_qk_norm_rope", q, "q"),
         _row_strides("attn_qk_norm_rope", k, "k"), B, Hq, Hkv, L, D, 2 * half, axes, eps, 1 if interleaved else 0,
         ATTN_DTYPE_BF16 if dt is _BF16 else ATTN_DTYPE_FP16, _raw_stream(dev) if stream is None else _stream_handle(stream))
-    return _check(st, "attn_qk_norm_rope", check)
+    return st if st == ATTN_OK else _check(st, "attn_qk_norm_rope", check)
 
 
 def attn_qk_norm_rope_workspace_bytes(D: int) -> int:
@@ -695,19 +699,21 @@ def attn_qk_norm_rope_bwd(q, k, dq_out, dk_out, pos, freq, dq, dk, q_weight, k_w
             and (k.shape, dq_out.shape, dk_out.shape, dq.shape, dk.shape, pos.shape[-2:], freq.shape)
             == ((B, Hkv, L, D), q.shape, k.shape, q.shape, k.shape, (B, L), (half,))
             and pos.dim() <= 3 and (axis is None or _plain(axis, _U8, dev, freq.shape))
-            and (q_weight is None or _plain(q_weight, dt, dev, w)) and (k_weight is None or _plain(k_weight, dt, dev, w))
+            and (q_weight is k_weight is None or (q_weight is not None and k_weight is not None and q_weight.dtype is k_weight.dtype is dt
+                 and dev == q_weight.get_device() == k_weight.get_device() and q_weight.is_contiguous() and k_weight.is_contiguous()
+                 and q_weight.shape == w == k_weight.shape))
             and (dq_weight is None or _plain(dq_weight, _F32, dev, w)) and (dk_weight is None or _plain(dk_weight, _F32, dev, w))):
         _refuse_rope(call, q, k, pos, freq, axis, ((q_weight, w, "q_weight"), (k_weight, w, "k_weight"), (dq_out, (B, Hq, L, D), "dq_out"),
                                                    (dk_out, (B, Hkv, L, D), "dk_out")),
                      ((dq, (B, Hq, L, D), "dq"), (dk, (B, Hkv, L, D), "dk")), ((dq_weight, w, "dq_weight"), (dk_weight, w, "dk_weight")),
                      (workspace,))
-    st = load_library().attn_qk_norm_rope_bwd(
-        q.data_ptr(), k.data_ptr(), _ptr(q_weight), _ptr(k_weight), pos.data_ptr(), freq.data_ptr(), _ptr(axis),
-        dq_out.data_ptr(), dk_out.data_ptr(), dq.data_ptr(), dk.data_ptr(), _ptr(dq_weight), _ptr(dk_weight),
+    st = (_lib or load_library()).attn_qk_norm_rope_bwd(
+        q.data_ptr(), k.data_ptr(), 0 if q_weight is None else q_weight.data_ptr(), 0 if k_weight is None else k_weight.data_ptr(), pos.data_ptr(), freq.data_ptr(), 0 if axis is None else axis.data_ptr(),
+        dq_out.data_ptr(), dk_out.data_ptr(), dq.data_ptr(), dk.data_ptr(), 0 if dq_weight is None else dq_weight.data_ptr(), 0 if dk_weight is None else dk_weight.data_ptr(),
         workspace.data_ptr(), workspace.numel(), _row_strides(call, q, "q"), _row_strides(call, k, "k"),
         _row_strides(call, dq, "dq"), _row_strides(call, dk, "dk"), B, Hq, Hkv, L, D, 2 * half, axes, eps, 1 if interleaved else 0,
         ATTN_DTYPE_BF16 if dt is _BF16 else ATTN_DTYPE_FP16, _raw_stream(dev) if stream is None else _stream_handle(stream))
-    return _check(st, call, check)
+    return st if st == ATTN_OK else _check(st, call, check)
 
 
 def _refuse_pool(call, k_pages, v_pages, table, k_exp, v_exp, lens, dense=(), sliced=(), f32=(), u8=()):
@@ -741,14 +747,15 @@ def attn_paged_write(k_new, v_new, k_pages, v_pages, table, cache_len, cache_len
             and (pool, v_pages.shape, v_new.shape, table.shape, cache_len.shape, cache_len_out.shape)
             == ((n_pages, Hkv, page, D), pool, k_new.shape, (B, per_seq), lens, lens)
             and (new_len is None or _plain(new_len, _I32, dev, lens)) and (k_exp is None) == (v_exp is None)
-            and (k_exp is None or (_plain(k_exp, _I8, dev, ints) and _plain(v_exp, _I8, dev, ints)))):
+            and (k_exp is None or (k_exp.dtype is v_exp.dtype is _I8 and dev == k_exp.get_device() == v_exp.get_device()
+                                  and k_exp.is_contiguous() and v_exp.is_contiguous() and k_exp.shape == ints == v_exp.shape))):
         _refuse_pool("attn_paged_write", k_pages, v_pages, table, k_exp, v_exp, (cache_len, cache_len_out, new_len),
                      ((k_new, (table.shape[0], pool[1], T, pool[3]), "k_new"), (v_new, k_new.shape, "v_new")))
-    st = load_library().attn_paged_write(
-        k_new.data_ptr(), v_new.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), _ptr(k_exp), _ptr(v_exp), table.data_ptr(),
-        cache_len.data_ptr(), _ptr(new_len), cache_len_out.data_ptr(), B, Hkv, T, n_pages, page, per_seq, D,
+    st = (_lib or load_library()).attn_paged_write(
+        k_new.data_ptr(), v_new.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), 0 if k_exp is None else k_exp.data_ptr(), 0 if v_exp is None else v_exp.data_ptr(), table.data_ptr(),
+        cache_len.data_ptr(), 0 if new_len is None else new_len.data_ptr(), cache_len_out.data_ptr(), B, Hkv, T, n_pages, page, per_seq, D,
         ATTN_DTYPE_BF16 if dt is _BF16 else ATTN_DTYPE_FP16, _raw_stream(dev) if stream is None else _stream_handle(stream))
-    return _check(st, "attn_paged_write", check)
+    return st if st == ATTN_OK else _check(st, "attn_paged_write", check)
 
 
 def attn_paged_read(k_pages, v_pages, table, cache_len, k, v, k_exp=None, v_exp=None, stream=None, check: bool = True) -> int:
@@ -765,14 +772,15 @@ def attn_paged_read(k_pages, v_pages, table, cache_len, k, v, k_exp=None, v_exp=
             and k_pages.is_contiguous() and v_pages.is_contiguous() and table.is_contiguous() and cache_len.is_contiguous()
             and (pool, v_pages.shape, v.shape, table.shape, cache_len.shape) == ((n_pages, Hkv, page, D), pool, k.shape, (B, per_seq), lens)
             and (k_exp is None) == (v_exp is None)
-            and (k_exp is None or (_plain(k_exp, _I8, dev, ints) and _plain(v_exp, _I8, dev, ints)))):
+            and (k_exp is None or (k_exp.dtype is v_exp.dtype is _I8 and dev == k_exp.get_device() == v_exp.get_device()
+                                  and k_exp.is_contiguous() and v_exp.is_contiguous() and k_exp.shape == ints == v_exp.shape))):
         shape = (table.shape[0], pool[1], Lk, pool[3])
         _refuse_pool("attn_paged_read", k_pages, v_pages, table, k_exp, v_exp, (cache_len,), sliced=((k, shape, "k"), (v, shape, "v")))
-    st = load_library().attn_paged_read(
-        k_pages.data_ptr(), v_pages.data_ptr(), _ptr(k_exp), _ptr(v_exp), table.data_ptr(), cache_len.data_ptr(), k.data_ptr(),
+    st = (_lib or load_library()).attn_paged_read(
+        k_pages.data_ptr(), v_pages.data_ptr(), 0 if k_exp is None else k_exp.data_ptr(), 0 if v_exp is None else v_exp.data_ptr(), table.data_ptr(), cache_len.data_ptr(), k.data_ptr(),
         v.data_ptr(), kv_row_pitch(k, v), B, Hkv, Lk, n_pages, page, per_seq, D,
         ATTN_DTYPE_BF16 if dt is _BF16 else ATTN_DTYPE_FP16, _raw_stream(dev) if stream is None else _stream_handle(stream))
-    return _check(st, "attn_paged_read", check)
+    return st if st == ATTN_OK else _check(st, "attn_paged_read", check)
 
 
 def attn_paged_workspace_bytes(B: int, Hq: int, Hkv: int, T: int, page_size: int, per_seq: int, D: int) -> int:
@@ -805,14 +813,15 @@ def attn_fwd_paged(q, k_pages, v_pages, table, cache_len, o, lse, workspace, sca
             and cache_len.is_contiguous() and o.is_contiguous() and lse.is_contiguous() and workspace.is_contiguous()
             and (pool, v_pages.shape, table.shape, cache_len.shape, o.shape, lse.shape)
             == ((n_pages, Hkv, page, D), pool, (B, per_seq), (B,), q.shape, (B, Hq, T)) and (k_exp is None) == (v_exp is None)
-            and (k_exp is None or (_plain(k_exp, _I8, dev, ints) and _plain(v_exp, _I8, dev, ints)))):
+            and (k_exp is None or (k_exp.dtype is v_exp.dtype is _I8 and dev == k_exp.get_device() == v_exp.get_device()
+                                  and k_exp.is_contiguous() and v_exp.is_contiguous() and k_exp.shape == ints == v_exp.shape))):
         _refuse_pool("attn_fwd_paged", k_pages, v_pages, table, k_exp, v_exp, (cache_len,),
                      ((q, (table.shape[0], Hq, T, pool[3]), "q"), (o, q.shape, "o")), f32=((lse, (B, Hq, T), "lse"),), u8=(workspace,))
-    st = load_library().attn_fwd_paged(
-        q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), _ptr(k_exp), _ptr(v_exp), table.data_ptr(), cache_len.data_ptr(),
+    st = (_lib or load_library()).attn_fwd_paged(
+        q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), 0 if k_exp is None else k_exp.data_ptr(), 0 if v_exp is None else v_exp.data_ptr(), table.data_ptr(), cache_len.data_ptr(),
         o.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.numel(), B, Hq, Hkv, T, n_pages, page, per_seq, D, scale,
         ATTN_DTYPE_BF16 if dt is _BF16 else ATTN_DTYPE_FP16, _raw_stream(dev) if stream is None else _stream_handle(stream))
-    return _check(st, "attn_fwd_paged", check)
+    return st if st == ATTN_OK else _check(st, "attn_fwd_paged", check)
 
 
 def attn_draft_verify(target, draft, tokens, u, r, accept_len, token, draft_len=None, stream=None, check: bool = True) -> int:
@@ -832,10 +841,10 @@ def attn_draft_verify(target, draft, tokens, u, r, accept_len, token, draft_len=
         _require("attn_draft_verify", f32=(target, draft, u, r), i32=(tokens, accept_len, token, draft_len))
         _shapes("attn_draft_verify", (target, (B, T + 1, V), "target"), (draft, (B, T, V), "draft"), (u, (B, T), "u"), (r, lens, "r"),
                 (accept_len, lens, "accept_len"), (token, lens, "token"), (draft_len, lens, "draft_len"))
-    st = load_library().attn_draft_verify(target.data_ptr(), _ptr(draft), tokens.data_ptr(), u.data_ptr(), r.data_ptr(),
-                                          _ptr(draft_len), accept_len.data_ptr(), token.data_ptr(), B, T, V,
+    st = (_lib or load_library()).attn_draft_verify(target.data_ptr(), 0 if draft is None else draft.data_ptr(), tokens.data_ptr(), u.data_ptr(), r.data_ptr(),
+                                          0 if draft_len is None else draft_len.data_ptr(), accept_len.data_ptr(), token.data_ptr(), B, T, V,
                                           _raw_stream(dev) if stream is None else _stream_handle(stream))
-    return _check(st, "attn_draft_verify", check)
+    return st if st == ATTN_OK else _check(st, "attn_draft_verify", check)
 
 
 def attn_last_device_status(stream=None) -> int:

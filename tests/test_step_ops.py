@@ -81,26 +81,30 @@ def test_oracle_verify_keeps_the_targets_distribution():
 # --- refusals ----------------------------------------------------------------
 
 
+KEEP = []  # the stride arrays whose addresses the calls get
+
+
 def st(*s):
-    return (ctypes.c_int64 * 3)(*s)
+    KEEP.append((ctypes.c_int64 * 3)(*s))
+    return ctypes.addressof(KEEP[-1])
 
 
 def rope(lib, B=2, Hq=8, Hkv=2, L=16, D=128, rot=128, axes=1, eps=1e-6, inter=0, dtype=1, **over):
     a = dict(zip(("q", "k", "qw", "kw", "pos", "freq", "axis", "q_out", "k_out"), A))
     a["qs"], a["ks"] = st(Hq * L * D, L * D, D), st(Hkv * L * D, L * D, D)
-    a.update(over)
+    a.update({k: v or 0 for k, v in over.items()})  # (None: a null pointer)
     return lib.attn_qk_norm_rope(a["q"], a["k"], a["qw"], a["kw"], a["pos"], a["freq"], a["axis"], a["q_out"], a["k_out"], a["qs"],
-                                 a["ks"], B, Hq, Hkv, L, D, rot, axes, ctypes.c_float(eps), inter, dtype, None)
+                                 a["ks"], B, Hq, Hkv, L, D, rot, axes, ctypes.c_float(eps), inter, dtype, 0)
 
 
 def rope_bwd(lib, B=2, Hq=8, Hkv=2, L=16, D=128, rot=128, axes=1, eps=1e-6, inter=0, dtype=1, nbytes=1 << 20, **over):
     a = dict(zip(("q", "k", "qw", "kw", "pos", "freq", "axis", "dq_out", "dk_out", "dq", "dk", "dqw", "dkw", "ws"), A))
     a["qs"], a["ks"] = st(Hq * L * D, L * D, D), st(Hkv * L * D, L * D, D)
     a["dqs"], a["dks"] = a["qs"], a["ks"]
-    a.update(over)
+    a.update({k: v or 0 for k, v in over.items()})  # (None: a null pointer)
     return lib.attn_qk_norm_rope_bwd(a["q"], a["k"], a["qw"], a["kw"], a["pos"], a["freq"], a["axis"], a["dq_out"], a["dk_out"], a["dq"],
                                      a["dk"], a["dqw"], a["dkw"], a["ws"], nbytes, a["qs"], a["ks"], a["dqs"], a["dks"], B, Hq, Hkv, L, D,
-                                     rot, axes, ctypes.c_float(eps), inter, dtype, None)
+                                     rot, axes, ctypes.c_float(eps), inter, dtype, 0)
 
 
 @pytest.mark.parametrize("call", [rope, rope_bwd])
@@ -148,23 +152,23 @@ def test_rope_refuses_shared_storage(lib):
 
 def write(lib, B=2, Hkv=2, T=4, n_pages=10, page=16, per_seq=5, D=128, dtype=1, **over):
     a = dict(zip(("k_new", "v_new", "k", "v", "ke", "ve", "table", "len", "new", "out"), A))
-    a.update(over)
+    a.update({k: v or 0 for k, v in over.items()})  # (None: a null pointer)
     return lib.attn_paged_write(a["k_new"], a["v_new"], a["k"], a["v"], a["ke"], a["ve"], a["table"], a["len"], a["new"], a["out"], B, Hkv,
-                                T, n_pages, page, per_seq, D, dtype, None)
+                                T, n_pages, page, per_seq, D, dtype, 0)
 
 
 def read(lib, B=2, Hkv=2, Lk=70, n_pages=10, page=16, per_seq=5, D=128, dtype=1, pitch=0, **over):
     a = dict(zip(("k", "v", "ke", "ve", "table", "len", "ko", "vo"), A))
-    a.update(over)
+    a.update({k: v or 0 for k, v in over.items()})  # (None: a null pointer)
     return lib.attn_paged_read(a["k"], a["v"], a["ke"], a["ve"], a["table"], a["len"], a["ko"], a["vo"], pitch, B, Hkv, Lk, n_pages, page,
-                               per_seq, D, dtype, None)
+                               per_seq, D, dtype, 0)
 
 
 def paged(lib, B=2, Hq=8, Hkv=2, T=1, n_pages=10, page=16, per_seq=5, D=128, scale=0.1, dtype=1, nbytes=1 << 26, **over):
     a = dict(zip(("q", "k", "v", "ke", "ve", "table", "len", "o", "lse", "ws"), A))
-    a.update(over)
+    a.update({k: v or 0 for k, v in over.items()})  # (None: a null pointer)
     return lib.attn_fwd_paged(a["q"], a["k"], a["v"], a["ke"], a["ve"], a["table"], a["len"], a["o"], a["lse"], a["ws"], nbytes, B, Hq, Hkv,
-                              T, n_pages, page, per_seq, D, ctypes.c_float(scale), dtype, None)
+                              T, n_pages, page, per_seq, D, ctypes.c_float(scale), dtype, 0)
 
 
 @pytest.mark.parametrize("call", [write, read, paged])
@@ -213,8 +217,8 @@ def test_paged_attention_rejects(lib):
 
 def verify(lib, B=2, T=3, V=100, **over):
     a = dict(zip(("target", "draft", "tokens", "u", "r", "len", "accept", "token"), A))
-    a.update(over)
-    return lib.attn_draft_verify(a["target"], a["draft"], a["tokens"], a["u"], a["r"], a["len"], a["accept"], a["token"], B, T, V, None)
+    a.update({k: v or 0 for k, v in over.items()})  # (None: a null pointer)
+    return lib.attn_draft_verify(a["target"], a["draft"], a["tokens"], a["u"], a["r"], a["len"], a["accept"], a["token"], B, T, V, 0)
 
 
 def test_verify_rejects(lib):
