@@ -108,22 +108,21 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
     lib.attn_cache_evict_workspace_bytes.restype = sz
     lib.attn_cache_evict.argtypes = [vp] * 10 + [sz, i64] + [ci] * 7 + [vp]
     lib.attn_cache_evict.restype = ci
-    at = ctypes.c_long  # an address as an integer (0: none): converted faster than c_void_p, which counts in the calls below
-    lib.attn_qk_norm_rope.argtypes = [at] * 11 + [ci] * 7 + [cf, ci, ci, vp]
+    lib.attn_qk_norm_rope.argtypes = [vp] * 11 + [ci] * 7 + [cf, ci, ci, vp]
     lib.attn_qk_norm_rope.restype = ci
     lib.attn_qk_norm_rope_workspace_bytes.argtypes = [ci]
     lib.attn_qk_norm_rope_workspace_bytes.restype = sz
-    lib.attn_qk_norm_rope_bwd.argtypes = [at] * 14 + [sz] + [at] * 4 + [ci] * 7 + [cf, ci, ci, vp]
+    lib.attn_qk_norm_rope_bwd.argtypes = [vp] * 14 + [sz] + [vp] * 4 + [ci] * 7 + [cf, ci, ci, vp]
     lib.attn_qk_norm_rope_bwd.restype = ci
-    lib.attn_paged_write.argtypes = [at] * 10 + [ci] * 8 + [at]
+    lib.attn_paged_write.argtypes = [vp] * 10 + [ci] * 8 + [vp]
     lib.attn_paged_write.restype = ci
-    lib.attn_paged_read.argtypes = [at] * 8 + [i64] + [ci] * 8 + [at]
+    lib.attn_paged_read.argtypes = [vp] * 8 + [i64] + [ci] * 8 + [vp]
     lib.attn_paged_read.restype = ci
     lib.attn_paged_workspace_bytes.argtypes = [ci] * 7
     lib.attn_paged_workspace_bytes.restype = sz
-    lib.attn_fwd_paged.argtypes = [at] * 10 + [sz] + [ci] * 8 + [cf, ci, vp]
+    lib.attn_fwd_paged.argtypes = [vp] * 10 + [sz] + [ci] * 8 + [cf, ci, vp]
     lib.attn_fwd_paged.restype = ci
-    lib.attn_draft_verify.argtypes = [at] * 8 + [ci] * 3 + [at]
+    lib.attn_draft_verify.argtypes = [vp] * 8 + [ci] * 3 + [vp]
     lib.attn_draft_verify.restype = ci
     lib.attn_last_device_status.argtypes = [vp]
     lib.attn_last_device_status.restype = ci
