@@ -5,7 +5,8 @@ The kernel instantiations compile as one translation unit per head dimension
 C-ABI unit (api.cu), the linear cross-entropy unit (lce.cu), the cache unit (cache.cu) and the
 unit of the calls around attention (step.cu); the objects link into
 bwd_flashattention_fwd_gb300/libgbattn.so (no library besides the CUDA
-runtime).  checks.cu becomes libgbattn_checks.so, a test aid.
+runtime).  checks.cu becomes libgbattn_checks.so, a test aid, and binding.cpp
+_binding.so, the Python binding's fast path (against torch's headers).
 """
 
 from __future__ import annotations
@@ -23,6 +24,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libgbattn.so")
 CHECKS_LIB = os.path.join(PKG, "libgbattn_checks.so")  # device checks of the kernels' math helpers (tests only)
 DEBUG_LIB = os.path.join(PKG, "libgbattn_debug.so")  # index checks compiled in (GBATTN_DEBUG_CHECKS)
+BINDING = os.path.join(PKG, "_binding.so")  # fast path of the Python binding: tensors checked in C++
 HEAD_DIMS = (64, 96, 128, 256)
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -34,6 +36,23 @@ def _nvcc() -> str:
         if cand and os.path.exists(cand):
             return cand
     raise RuntimeError("nvcc not found")
+
+
+def _binding_cmd(out: str):
+    """Compile and link the Python extension against the installed torch."""
+    import sysconfig
+
+    import torch
+
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(_nvcc()))
+    inc = [sysconfig.get_paths()["include"], os.path.join(root, "include"),
+           os.path.join(root, "include", "torch", "csrc", "api", "include"), os.path.join(cuda, "include")]
+    cxx = os.environ.get("CXX") or shutil.which("g++") or "g++"
+    return [cxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *(f"-I{d}" for d in inc),
+            os.path.join(CSRC, "binding.cpp"), "-o", out, "-L" + os.path.join(root, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu",
+            "-ltorch_python"]
 
 
 def _sources_mtime() -> float:
@@ -55,7 +74,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), debug: boo
     """Compile (if stale) and return the path of libgbattn.so (with debug:
     libgbattn_debug.so, the kernels' index checks compiled in)."""
     lib = DEBUG_LIB if debug else LIB
-    outs_needed = (lib,) if debug else (LIB, CHECKS_LIB)
+    outs_needed = (lib,) if debug else (LIB, CHECKS_LIB, BINDING)
     if not force and all(os.path.exists(p) and os.path.getmtime(p) >= _sources_mtime() for p in outs_needed):
         return lib
     nvcc = _nvcc()
@@ -70,14 +89,16 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), debug: boo
     for unit in ("api", "lce", "cache", "step"):
         jobs.append([nvcc, *ARCH, *flags, "-c", os.path.join(CSRC, unit + ".cu"), "-o", os.path.join(bdir, unit + ".o")])
     checks_obj = os.path.join(bdir, "checks.o")
+    tmp_binding = BINDING + ".tmp"
     if not debug:
         jobs.append([nvcc, *ARCH, *flags, "-c", os.path.join(CSRC, "checks.cu"), "-o", checks_obj])
+        jobs.append(_binding_cmd(tmp_binding))
     with ThreadPoolExecutor(max_workers=len(jobs)) as ex:
         outs = list(ex.map(_run, jobs))
     if verbose:
         for o in outs:
             sys.stdout.write(o)
-    objs = [j[-1] for j in jobs if j[-1] != checks_obj]
+    objs = [j[-1] for j in jobs if j[-1].endswith(".o") and j[-1] != checks_obj]
     tmp = lib + ".tmp"
     _run([nvcc, *ARCH, "-shared", "-o", tmp, *objs])
     os.replace(tmp, lib)
@@ -85,6 +106,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), debug: boo
         tmp = CHECKS_LIB + ".tmp"
         _run([nvcc, *ARCH, "-shared", "-o", tmp, checks_obj])
         os.replace(tmp, CHECKS_LIB)
+        os.replace(tmp_binding, BINDING)
     return lib
 
 

@@ -56,7 +56,7 @@ struct PagedGeom {
   // CTAs on an SM, as far as registers allow
   __host__ __device__ static constexpr int per_sm(int nt) { return NW <= 4 || D * nt <= 128 ? 2 : 1; }
   static constexpr int join_pitch = D + 4;  // floats of a row where the warps meet
-  __host__ __device__ static constexpr int smem(int rows) {  // (and the B + 1 starts behind)
+  __host__ __device__ static constexpr int smem(int rows) {  // (and the B + 1 starts and B lengths behind)
     const int join = NW * rows * join_pitch * 4;
     return (RING > join ? RING : join) + (D / 16) * (rows / 8) * 256;
   }
@@ -87,8 +87,8 @@ struct PagedHead {
 };
 
 // Prefix sums of the sequences' units (fewer than 2^31 in all: the host sees to
-// it) into starts[0..B] (shared memory); every thread calls it.
-__device__ __forceinline__ void paged_starts(const PagedAttnParams& p, int ks, int* starts) {
+// it) into starts[0..B], and their lengths into lens (shared memory; may be null); every thread calls it.
+__device__ __forceinline__ void paged_starts(const PagedAttnParams& p, int ks, int* starts, int* lens) {
   __shared__ int warp_total[32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n_warps = blockDim.x >> 5;
   const int room = p.c.per_seq << p.c.shift;
@@ -96,7 +96,9 @@ __device__ __forceinline__ void paged_starts(const PagedAttnParams& p, int ks, i
   int base = 0;
   for (int b0 = 0; b0 < p.B; b0 += blockDim.x) {
     const int b = b0 + threadIdx.x;
-    int x = b < p.B ? ((clamp_len(p.cache_len[b], room) + ks - 1) / ks + kPagedExtra) * heads : 0;
+    const int len = b < p.B ? clamp_len(p.cache_len[b], room) : 0;
+    if (lens && b < p.B) lens[b] = len;
+    int x = b < p.B ? ((len + ks - 1) / ks + kPagedExtra) * heads : 0;
     const int own = x;
 #pragma unroll
     for (int m = 1; m < 32; m <<= 1) {
@@ -192,8 +194,8 @@ struct PagedShared {
   float ml[NW][ROWS][2];
 };
 
-// Steps s0 .. s1 - 1 of a head's keys, n in all, for one block of its rows: leaves the warps' results in smem
-// (rows of join_pitch floats) and sh.ml.
+// Steps s0 .. s1 - 1 of a head's keys, n in all, for one block of its rows: leaves the warps' results in
+// smem (rows of join_pitch floats) and sh.ml.
 template <int D, bool BF16, bool Q8, int NT>
 __device__ __forceinline__ void paged_part(const PagedAttnParams& p, const PagedHead& hd, int s0, int s1, int n, uint8_t* smem,
                                            PagedShared<PagedGeom<D, Q8>::NW, PagedGeom<D, Q8>::ST, 8 * NT>& sh) {
@@ -213,12 +215,15 @@ __device__ __forceinline__ void paged_part(const PagedAttnParams& p, const Paged
   const int row0 = hd.rb * ROWS;  // first packed row
 
   // ---- the warp's ring of tiles ----
-  int page = -1;  // of this lane's key in the tile that is issued next
-  auto look_up = [&](int s) {
+  auto look_up = [&](int s) {  // page of this lane's key in the tile of step s
     const int key = (s * NW + warp) * KT + (lane & (KT - 1));
-    page = s < s1 && key < n ? __ldg(p.c.table + static_cast<size_t>(hd.b) * p.c.per_seq + (key >> p.c.shift)) : -1;
-    if (page >= p.c.n_pages) page = -1;
+    if (s >= s1 || key >= n) return -1;
+    const int pg = __ldg(p.c.table + static_cast<size_t>(hd.b) * p.c.per_seq + (key >> p.c.shift));
+    return pg < p.c.n_pages ? pg : -1;
   };
+  int page[ST];  // of the tiles that are issued next: the first ones' are looked up together, then one at a time
+#pragma unroll
+  for (int i = 0; i < ST; ++i) page[i] = look_up(s0 + i);
   // Where the tile's rows lie in the pool, by eights (a page has at least eight), and which of them are there.
   long long src[KT / 8];
   uint32_t there_next = 0;
@@ -243,13 +248,13 @@ __device__ __forceinline__ void paged_part(const PagedAttnParams& p, const Paged
       }
     }
   };
-  auto issue_k = [&](int s) {
+  auto issue_k = [&](int s, int slot, int pages) {
     if (s < s1) {
-      const int slot = (s - s0) % ST, key0 = (s * NW + warp) * KT;
-      there_next = __ballot_sync(0xffffffffu, page >= 0);
+      const int key0 = (s * NW + warp) * KT;
+      there_next = __ballot_sync(0xffffffffu, pages >= 0);
 #pragma unroll
       for (int e = 0; e < KT / 8; ++e) {
-        const int pg = __shfl_sync(0xffffffffu, page, 8 * e);
+        const int pg = __shfl_sync(0xffffffffu, pages, 8 * e);
         const long long r = ((static_cast<long long>(pg) * p.c.Hkv + hd.h) << p.c.shift) + ((key0 + 8 * e) & ((1 << p.c.shift) - 1));
         src[e] = r;
         if (pg < 0 || !dbg_in_range(r, 8, n_rows, p.status, 120)) {  // (a hole, or past the end)
@@ -270,20 +275,19 @@ __device__ __forceinline__ void paged_part(const PagedAttnParams& p, const Paged
           cp_async4(dst + 2 * KT * Gm::PITCH + (is_v ? KT : 0) + 4 * i, (is_v ? p.c.v_exp : p.c.k_exp) + at + 4 * (i & 1),
                     there_next >> (4 * i) & 1u);
       }
-      look_up(s + 1);
     }
     cp_async_commit();
   };
-  auto issue_v = [&](int s) {  // (behind issue_k of the same tile)
-    if (s < s1) copy_rows(ring + (s - s0) % ST * Gm::TILE + KT * Gm::PITCH, p.c.v);
+  auto issue_v = [&](int s, int slot) {  // (behind issue_k of the same tile)
+    if (s < s1) copy_rows(ring + slot * Gm::TILE + KT * Gm::PITCH, p.c.v);
     cp_async_commit();
   };
-  look_up(s0);
 #pragma unroll
   for (int i = 0; i < ST; ++i) {
-    issue_k(s0 + i);
-    issue_v(s0 + i);
+    issue_k(s0 + i, i, page[i]);
+    issue_v(s0 + i, i);
   }
+  int next_page = look_up(s0 + ST);
 
   // ---- Q as B fragments, the same for every warp ----
   const uint16_t* q = static_cast<const uint16_t*>(p.q) + (static_cast<size_t>(hd.b) * p.c.Hkv + hd.h) * p.R * D;
@@ -335,17 +339,18 @@ __device__ __forceinline__ void paged_part(const PagedAttnParams& p, const Paged
 #pragma unroll
     for (int d = 0; d < KK; ++d) acc[d][i][0] = acc[d][i][1] = acc[d][i][2] = acc[d][i][3] = 0.f;
   }
-  for (int s = s0; s < s1; ++s) {
+  for (int s = s0, slot = 0; s < s1; ++s, slot = slot + 1 == ST ? 0 : slot + 1) {
     cp_async_wait<2 * ST - 1>();  // K of this tile
     __syncwarp();
-    const int slot = (s - s0) % ST, key0 = (s * NW + warp) * KT;
+    const int key0 = (s * NW + warp) * KT;
     const uint32_t tile = ring + slot * Gm::TILE;
     const uint32_t there = key_mask[warp][slot];
     if (there == 0) {  // past the end, or all holes
       __syncwarp();
-      issue_k(s + ST);
+      issue_k(s + ST, slot, next_page);
+      next_page = look_up(s + ST + 1);
       cp_async_wait<2 * ST - 1>();
-      issue_v(s + ST);
+      issue_v(s + ST, slot);
       continue;
     }
     // S^T = K Q^T
@@ -450,7 +455,8 @@ __device__ __forceinline__ void paged_part(const PagedAttnParams& p, const Paged
       }
     }
     __syncwarp();  // every lane has read K and the exponents
-    issue_k(s + ST);
+    issue_k(s + ST, slot, next_page);
+    next_page = look_up(s + ST + 1);
     cp_async_wait<2 * ST - 1>();  // V of this tile
     __syncwarp();
     // P^T, and O^T += V^T P^T
@@ -494,7 +500,7 @@ __device__ __forceinline__ void paged_part(const PagedAttnParams& p, const Paged
       }
     }
     __syncwarp();  // every lane has read V
-    issue_v(s + ST);
+    issue_v(s + ST, slot);
   }
   cp_async_wait<0>();
   __syncthreads();  // every warp is done with its ring: the warps' results go there
@@ -560,10 +566,10 @@ __global__ void __launch_bounds__(PagedGeom<D, Q8>::THREADS, PagedGeom<D, Q8>::p
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ PagedShared<Gm::NW, Gm::ST, ROWS> sh;
   const float* join = reinterpret_cast<const float*>(smem);
-  int* starts = reinterpret_cast<int*>(smem + Gm::smem(ROWS));  // [B + 1]
+  int* starts = reinterpret_cast<int*>(smem + Gm::smem(ROWS));  // [B + 1], then lengths [B]
   grid_dependency_wait();  // the kernels before this one are complete
   if (threadIdx.x == 0) grid_launch_dependents();
-  paged_starts(p, Gm::KS, starts);
+  paged_starts(p, Gm::KS, starts, starts + p.B + 1);
   const PagedPieces pieces(starts[p.B], p.n_groups);
   if (blockIdx.x >= pieces.n) return;
   int u = pieces.first(blockIdx.x);
@@ -574,9 +580,8 @@ __global__ void __launch_bounds__(PagedGeom<D, Q8>::THREADS, PagedGeom<D, Q8>::p
     const int s1 = min(hd.steps, s0 + min(left, u_end - u));
     u += left;  // the next head, if any
     if (s0 >= s1 && !(hd.steps == 0 && s0 == 0)) continue;  // only the head's extra units
-    const int n = clamp_len(p.cache_len[hd.b], p.c.per_seq << p.c.shift);
     __syncthreads();  // the results of the head before are read
-    paged_part<D, BF16, Q8, NT>(p, hd, s0, s1, n, smem, sh);
+    paged_part<D, BF16, Q8, NT>(p, hd, s0, s1, starts[p.B + 1 + hd.b], smem, sh);
     const bool whole = s0 == 0 && s1 == hd.steps;
     const size_t part0 = (static_cast<size_t>(blockIdx.x) * 2 + (s0 == 0 ? 1 : 0)) * ROWS;
     const size_t out0 = (static_cast<size_t>(hd.b) * p.c.Hkv + hd.h) * p.R + hd.rb * ROWS;
@@ -666,7 +671,7 @@ __global__ void __launch_bounds__(kPagedJoinThreads) attn_paged_join_kernel(cons
   __shared__ int starts[kPagedMaxB + 1];
   __shared__ float4 sum[WARPS > 1 ? WARPS : 1][QUADS];
   __shared__ float2 stat[WARPS];
-  paged_starts(p, Gm::KS, starts);  // (lengths: nothing that the kernel before writes)
+  paged_starts(p, Gm::KS, starts, nullptr);  // (lengths: nothing that the kernel before writes)
   grid_dependency_wait();
   const PagedPieces pieces(starts[p.B], p.n_groups);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;

@@ -52,7 +52,7 @@ int impl(const PagedAttnParams& p0, int num_sms, cudaStream_t stream) {
   PagedAttnParams p = p0;
   constexpr int rows = 8 * NT;
   p.n_rb = (p.R + rows - 1) / rows;
-  const int smem = Gm::smem(rows) + (p.B + 1) * 4;
+  const int smem = Gm::smem(rows) + (2 * p.B + 1) * 4;
   // two CTAs per SM where their shared memory (1 KB more each, 228 KB in all) and static arrays allow it
   constexpr int fixed = 1024 + 256 + Gm::NW * (rows * 8 + Gm::ST * 4) + rows * 4;
   const int per_sm = Gm::per_sm(NT) == 2 && 2 * (smem + fixed) <= 233472 ? 2 : 1;
@@ -71,7 +71,7 @@ int impl(const PagedAttnParams& p0, int num_sms, cudaStream_t stream) {
   p.part_ml = p.part + static_cast<size_t>(kPagedMaxCtas) * 2 * rows * kD;
   auto kern = attn_paged_kernel<kD, BF16, Q8, NT>;
   static std::atomic<uint64_t> done{0};
-  if (!set_smem_limit(kern, Gm::smem(rows) + (kPagedMaxB + 1) * 4, done)) return kLaunchCudaError;
+  if (!set_smem_limit(kern, Gm::smem(rows) + (2 * kPagedMaxB + 1) * 4, done)) return kLaunchCudaError;
   const int r = launch_dependent(kern, dim3(p.n_groups), Gm::THREADS, smem, stream, p);
   if (r != kLaunchOk || p.n_groups == 1) return r;
   // a block's warps share a row's partial results where there are many

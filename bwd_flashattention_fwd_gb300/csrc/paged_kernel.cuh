@@ -151,19 +151,21 @@ __global__ void __launch_bounds__(kPagedThreads) attn_paged_read_kernel(const Pa
   grid_dependency_wait();
   if (threadIdx.x == 0) grid_launch_dependents();
   const int b = blockIdx.y / p.c.Hkv, h = blockIdx.y - b * p.c.Hkv;
-  const int n = clamp_len(p.cache_len[b], min(p.Lk, p.c.per_seq << p.c.shift));
+  const int most = min(p.Lk, p.c.per_seq << p.c.shift), n = clamp_len(p.cache_len[b], most);
   [[maybe_unused]] const long long n_rows = (static_cast<long long>(p.c.n_pages) * p.c.Hkv) << p.c.shift;
   [[maybe_unused]] const size_t n_out = static_cast<size_t>(p.B * p.c.Hkv - 1) * p.pitch + p.Lk;
   const int group = threadIdx.x / LANES, c = threadIdx.x - group * LANES;
   const size_t out0 = static_cast<size_t>(blockIdx.y) * p.pitch;
-  for (long long j0 = static_cast<long long>(blockIdx.x) * ROWS; j0 < n; j0 += static_cast<long long>(gridDim.x) * ROWS) {
+  for (long long j0 = static_cast<long long>(blockIdx.x) * ROWS; j0 < most; j0 += static_cast<long long>(gridDim.x) * ROWS) {
+    if (j0 != static_cast<long long>(blockIdx.x) * ROWS && j0 >= n) break;
     long long from[N];
     int row[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int x = i * GROUPS + group;
       row[i] = static_cast<int>(j0) + x;
-      from[i] = group < GROUPS && row[i] < n ? paged_row(p.c, b, h, row[i]) : -1;
+      from[i] = group < GROUPS && row[i] < most ? paged_row(p.c, b, h, row[i]) : -1;  // (not waiting for n)
+      if (row[i] >= n) from[i] = -1;
       if (from[i] >= 0 && !(dbg_in_range(from[i], 1, n_rows, p.status, 111) && dbg_in_range(out0 + row[i], 1, n_out, p.status, 112))) from[i] = -1;
     }
     if constexpr (Q8) {

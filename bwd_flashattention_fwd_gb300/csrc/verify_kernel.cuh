@@ -77,9 +77,10 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) attn_draft_verify_kernel(co
   const int b = blockIdx.x / kVerifyCluster, c = blockIdx.x % kVerifyCluster;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int most = p.draft_len ? clamp_len(p.draft_len[b], p.T) : p.T;
-  if (threadIdx.x == 0) cut = most, chosen = -1;
+  const float r = p.r[b];
+  if (threadIdx.x == 0) cut = p.T, chosen = -1;
   __syncthreads();
-  for (int i = threadIdx.x; i < most; i += kVerifyThreads) {
+  for (int i = threadIdx.x; i < p.T; i += kVerifyThreads) {  // (all of them: nothing waits for draft_len)
     const int x = p.tokens[static_cast<size_t>(b) * p.T + i];
     bool good = x >= 0 && x < p.V;
     if (good) {
@@ -91,7 +92,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) attn_draft_verify_kernel(co
     if (!good) atomicMin(&cut, i);
   }
   __syncthreads();
-  const int n = cut;
+  const int n = min(cut, most);
   const bool rejected = n < most;
   const float* prow = p.target + (static_cast<size_t>(b) * (p.T + 1) + n) * p.V;
   const float* qrow = rejected && p.draft ? p.draft + (static_cast<size_t>(b) * p.T + n) * p.V : nullptr;
@@ -178,7 +179,6 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) attn_draft_verify_kernel(co
     totals(1, total, before);
   }
   // r as a multiple of 2^-64 (a float below 1 has 24 bits, so this is exact from 2^-40 up)
-  const float r = p.r[b];
   uint64_t rf = 0;
   if (r >= 1.f) {
     rf = ~0ull;

@@ -37,6 +37,7 @@ EXPORTED = ("attn_fwd", "attn_bwd_delta", "attn_bwd", "attn_bwd_dq", "attn_bwd_d
             "attn_paged_workspace_bytes", "attn_fwd_paged", "attn_draft_verify")
 
 _lib = None
+_fast = None  # the compiled fast path (csrc/binding.cpp) of the calls around attention, on _lib's functions
 
 
 class AttnError(RuntimeError):
@@ -49,7 +50,7 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
     """Load libgbattn.so once and declare its C signatures.  With
     GBATTN_DEBUG=1 in the environment the process uses the debug build
     (libgbattn_debug.so) instead."""
-    global _lib
+    global _lib, _fast
     if _lib is not None:
         return _lib
     if path is None:
@@ -130,8 +131,24 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
     lib.attn_wait_probe.restype = ci
     lib.attn_status_string.argtypes = [ci]
     lib.attn_status_string.restype = ctypes.c_char_p
-    _lib = lib
+    try:
+        from . import _binding
+    except ImportError as e:
+        raise RuntimeError(f"{os.path.join(_HERE, '_binding.so')} is not built for this Python and torch ({e}); run "
+                           "bwd_flashattention_fwd_gb300.build.build() (or __graft_entry__.build())") from e
+    _binding.init({n: ctypes.cast(getattr(lib, n), vp).value for n in
+                   ("attn_qk_norm_rope", "attn_qk_norm_rope_bwd", "attn_paged_write", "attn_paged_read", "attn_fwd_paged",
+                    "attn_draft_verify")})
+    _lib, _fast = lib, _binding
     return lib
+
+
+def _fast_path():
+    """The compiled fast path: each of its functions checks its tensors and makes
+    one call, or returns -1 where one is not what the call takes; the wrapper's
+    own checks then name it and raise."""
+    load_library()
+    return _fast
 
 
 def status_string(status: int) -> str:
@@ -612,23 +629,17 @@ def attn_cache_evict(k, v, weight, pos, cache_len, seen, weight_out, pos_out, ca
     return _check(st, "attn_cache_evict", check)
 
 
-_Strides = ctypes.c_int64 * 3
-_strides_of: dict = {}  # the C arrays of the strides met so far (a few per model), and their addresses
+def _handle(stream):
+    """A stream argument as the fast path takes it: None (the current one) or a handle."""
+    return None if stream is None else _stream_handle(stream)
 
 
-def _row_strides(call: str, t, name: str) -> int:
-    """Address of the strides between sequences, heads and tokens of a [B,H,L,D]
-    tensor whose rows are contiguous, for the C ABI."""
-    st = t.stride()
-    got = _strides_of.get(st)
-    if got is None:
-        if st[3] != 1:
-            raise ValueError(f"{call}: {name} of strides {st} has no contiguous rows")
-        if len(_strides_of) >= 4096:
-            _strides_of.pop(next(iter(_strides_of)))  # (the oldest: a call in progress holds at most four)
-        arr = _Strides(*st[:3])
-        got = _strides_of[st] = (ctypes.addressof(arr), arr)
-    return got[0]
+def _refuse(call: str, *rows):
+    """Behind a fast path that refused, and checks that named nothing."""
+    for t, name in rows:
+        if t.dim() == 4 and t.shape[3] > 1 and t.stride(3) != 1:
+            raise ValueError(f"{call}: {name} of strides {t.stride()} has no contiguous rows")
+    raise ValueError(f"{call}: the arguments do not fit together")
 
 
 def _refuse_rope(call, q, k, pos, freq, axis, dense, rows=(), f32=(), u8=()):
@@ -638,6 +649,7 @@ def _refuse_rope(call, q, k, pos, freq, axis, dense, rows=(), f32=(), u8=()):
     _require(call, dense=[t for t, _, _ in dense], sliced=(q, k, *(t for t, _, _ in rows)), f32=(freq, *(t for t, _, _ in f32)),
              u8=(axis, *u8), i32=(pos,))
     _shapes(call, (k, (B, k.shape[1], L, D), "k"), (pos, at, "pos"), (freq, (half,), "freq"), (axis, (half,), "axis"), *dense, *rows, *f32)
+    _refuse(call, (q, "q"), (k, "k"), *((t, n) for t, _, n in rows))
 
 
 def attn_qk_norm_rope(q, k, q_out, k_out, pos, freq, q_weight=None, k_weight=None, axis=None, eps: float = 1e-6,
@@ -647,25 +659,11 @@ def attn_qk_norm_rope(q, k, q_out, k_out, pos, freq, q_weight=None, k_weight=Non
     the contiguous q_out, k_out).  q and k may be views of a packed projection.
     pos int32 [B,L] or [axes,B,L]; freq float32 [rot/2]; axis uint8 [rot/2]:
     which axis each pair turns by (None: the first)."""
-    B, Hq, L, D = q.shape
-    Hkv, half, axes = k.shape[1], freq.shape[0], pos.shape[0] if pos.dim() == 3 else 1
-    dt, dev, w = q.dtype, q.get_device(), (D,)
-    if not (dev >= 0 and dev == _current_device() and (dt is _BF16 or dt is _F16) and dt is k.dtype is q_out.dtype is k_out.dtype
-            and pos.dtype is _I32 and freq.dtype is _F32
-            and dev == k.get_device() == q_out.get_device() == k_out.get_device() == pos.get_device() == freq.get_device()
-            and q_out.is_contiguous() and k_out.is_contiguous() and pos.is_contiguous() and freq.is_contiguous()
-            and (k.shape, q_out.shape, k_out.shape, pos.shape[-2:], freq.shape) == ((B, Hkv, L, D), q.shape, k.shape, (B, L), (half,))
-            and pos.dim() <= 3 and (axis is None or _plain(axis, _U8, dev, freq.shape))
-            and (q_weight is k_weight is None or (q_weight is not None and k_weight is not None and q_weight.dtype is k_weight.dtype is dt
-                 and dev == q_weight.get_device() == k_weight.get_device() and q_weight.is_contiguous() and k_weight.is_contiguous()
-                 and q_weight.shape == w == k_weight.shape))):
+    st = (_fast or _fast_path()).qk_norm_rope(q, k, q_out, k_out, pos, freq, q_weight, k_weight, axis, eps, interleaved, _handle(stream))
+    if st < 0:
+        w = q.shape[-1:]
         _refuse_rope("attn_qk_norm_rope", q, k, pos, freq, axis,
-                     ((q_weight, w, "q_weight"), (k_weight, w, "k_weight"), (q_out, (B, Hq, L, D), "q_out"), (k_out, (B, Hkv, L, D), "k_out")))
-    st = (_lib or load_library()).attn_qk_norm_rope(
-        q.data_ptr(), k.data_ptr(), 0 if q_weight is None else q_weight.data_ptr(), 0 if k_weight is None else k_weight.data_ptr(), pos.data_ptr(), freq.data_ptr(), 0 if axis is None else axis.data_ptr(),
-        q_out.data_ptr(), k_out.data_ptr(), _row_strides("attn_qk_norm_rope", q, "q"),
-        _row_strides("attn_qk_norm_rope", k, "k"), B, Hq, Hkv, L, D, 2 * half, axes, eps, 1 if interleaved else 0,
-        ATTN_DTYPE_BF16 if dt is _BF16 else ATTN_DTYPE_FP16, _raw_stream(dev) if stream is None else _stream_handle(stream))
+                     ((q_weight, w, "q_weight"), (k_weight, w, "k_weight"), (q_out, q.shape, "q_out"), (k_out, k.shape, "k_out")))
     return st if st == ATTN_OK else _check(st, "attn_qk_norm_rope", check)
 
 
@@ -684,35 +682,14 @@ def attn_qk_norm_rope_bwd(q, k, dq_out, dk_out, pos, freq, dq, dk, q_weight, k_w
     """Gradients of attn_qk_norm_rope: from dq_out, dk_out (contiguous) writes
     dq, dk (rows like q's and k's; views of a packed gradient will do) and, with
     weights, dq_weight, dk_weight (float32 [D]; None without)."""
-    call = "attn_qk_norm_rope_bwd"
-    B, Hq, L, D = q.shape
-    Hkv, half, axes = k.shape[1], freq.shape[0], pos.shape[0] if pos.dim() == 3 else 1
-    dt, dev, w = q.dtype, q.get_device(), (D,)
-    if not (dev >= 0 and dev == _current_device() and (dt is _BF16 or dt is _F16)
-            and dt is k.dtype is dq_out.dtype is dk_out.dtype is dq.dtype is dk.dtype
-            and pos.dtype is _I32 and freq.dtype is _F32 and workspace.dtype is _U8
-            and dev == k.get_device() == dq_out.get_device() == dk_out.get_device() == dq.get_device() == dk.get_device()
-            == pos.get_device() == freq.get_device() == workspace.get_device()
-            and dq_out.is_contiguous() and dk_out.is_contiguous() and pos.is_contiguous() and freq.is_contiguous()
-            and workspace.is_contiguous()
-            and (k.shape, dq_out.shape, dk_out.shape, dq.shape, dk.shape, pos.shape[-2:], freq.shape)
-            == ((B, Hkv, L, D), q.shape, k.shape, q.shape, k.shape, (B, L), (half,))
-            and pos.dim() <= 3 and (axis is None or _plain(axis, _U8, dev, freq.shape))
-            and (q_weight is k_weight is None or (q_weight is not None and k_weight is not None and q_weight.dtype is k_weight.dtype is dt
-                 and dev == q_weight.get_device() == k_weight.get_device() and q_weight.is_contiguous() and k_weight.is_contiguous()
-                 and q_weight.shape == w == k_weight.shape))
-            and (dq_weight is None or _plain(dq_weight, _F32, dev, w)) and (dk_weight is None or _plain(dk_weight, _F32, dev, w))):
-        _refuse_rope(call, q, k, pos, freq, axis, ((q_weight, w, "q_weight"), (k_weight, w, "k_weight"), (dq_out, (B, Hq, L, D), "dq_out"),
-                                                   (dk_out, (B, Hkv, L, D), "dk_out")),
-                     ((dq, (B, Hq, L, D), "dq"), (dk, (B, Hkv, L, D), "dk")), ((dq_weight, w, "dq_weight"), (dk_weight, w, "dk_weight")),
-                     (workspace,))
-    st = (_lib or load_library()).attn_qk_norm_rope_bwd(
-        q.data_ptr(), k.data_ptr(), 0 if q_weight is None else q_weight.data_ptr(), 0 if k_weight is None else k_weight.data_ptr(), pos.data_ptr(), freq.data_ptr(), 0 if axis is None else axis.data_ptr(),
-        dq_out.data_ptr(), dk_out.data_ptr(), dq.data_ptr(), dk.data_ptr(), 0 if dq_weight is None else dq_weight.data_ptr(), 0 if dk_weight is None else dk_weight.data_ptr(),
-        workspace.data_ptr(), workspace.numel(), _row_strides(call, q, "q"), _row_strides(call, k, "k"),
-        _row_strides(call, dq, "dq"), _row_strides(call, dk, "dk"), B, Hq, Hkv, L, D, 2 * half, axes, eps, 1 if interleaved else 0,
-        ATTN_DTYPE_BF16 if dt is _BF16 else ATTN_DTYPE_FP16, _raw_stream(dev) if stream is None else _stream_handle(stream))
-    return st if st == ATTN_OK else _check(st, call, check)
+    st = (_fast or _fast_path()).qk_norm_rope_bwd(q, k, dq_out, dk_out, pos, freq, dq, dk, q_weight, k_weight, dq_weight, dk_weight,
+                                                  workspace, axis, eps, interleaved, _handle(stream))
+    if st < 0:
+        w = q.shape[-1:]
+        _refuse_rope("attn_qk_norm_rope_bwd", q, k, pos, freq, axis,
+                     ((q_weight, w, "q_weight"), (k_weight, w, "k_weight"), (dq_out, q.shape, "dq_out"), (dk_out, k.shape, "dk_out")),
+                     ((dq, q.shape, "dq"), (dk, k.shape, "dk")), ((dq_weight, w, "dq_weight"), (dk_weight, w, "dk_weight")), (workspace,))
+    return st if st == ATTN_OK else _check(st, "attn_qk_norm_rope_bwd", check)
 
 
 def _refuse_pool(call, k_pages, v_pages, table, k_exp, v_exp, lens, dense=(), sliced=(), f32=(), u8=()):
@@ -725,6 +702,9 @@ def _refuse_pool(call, k_pages, v_pages, table, k_exp, v_exp, lens, dense=(), sl
              f32=[t for t, _, _ in f32], u8=u8, i32=(table, *lens), i8=(k_exp, v_exp), e4m3=() if k_exp is None else pools)
     _shapes(call, (v_pages, k_pages.shape, "v_pages"), (k_exp, ints, "k_exp"), (v_exp, ints, "v_exp"), (table, (B, *table.shape[1:2]), "table"),
             *((t, (B,), "a length") for t in lens), *dense, *sliced, *f32)
+    if sliced:
+        kv_row_pitch(sliced[0][0], sliced[1][0])
+    _refuse(call)
 
 
 def attn_paged_write(k_new, v_new, k_pages, v_pages, table, cache_len, cache_len_out, new_len=None, k_exp=None, v_exp=None,
@@ -733,27 +713,12 @@ def attn_paged_write(k_new, v_new, k_pages, v_pages, table, cache_len, cache_len
     cache_len tokens (new_len [B]: how many; None: T); writes cache_len_out.
     Pages [n,Hkv,page_size,D] of the same type, or float8_e4m3fn with int8
     exponents k_exp, v_exp [n,Hkv,page_size]; table int32 [B,pages]."""
-    B, Hkv, T, D = k_new.shape
-    n_pages, _, page, _ = pool = k_pages.shape
-    dt, dev, lens, per_seq = k_new.dtype, k_new.get_device(), (B,), table.shape[1]
-    held, ints = dt if k_exp is None else _E4M3, (n_pages, Hkv, page)
-    if not (dev >= 0 and dev == _current_device() and (dt is _BF16 or dt is _F16) and v_new.dtype is dt
-            and held is k_pages.dtype is v_pages.dtype and table.dtype is cache_len.dtype is cache_len_out.dtype is _I32
-            and dev == v_new.get_device() == k_pages.get_device() == v_pages.get_device() == table.get_device()
-            == cache_len.get_device() == cache_len_out.get_device()
-            and k_new.is_contiguous() and v_new.is_contiguous() and k_pages.is_contiguous() and v_pages.is_contiguous()
-            and table.is_contiguous() and cache_len.is_contiguous() and cache_len_out.is_contiguous()
-            and (pool, v_pages.shape, v_new.shape, table.shape, cache_len.shape, cache_len_out.shape)
-            == ((n_pages, Hkv, page, D), pool, k_new.shape, (B, per_seq), lens, lens)
-            and (new_len is None or _plain(new_len, _I32, dev, lens)) and (k_exp is None) == (v_exp is None)
-            and (k_exp is None or (k_exp.dtype is v_exp.dtype is _I8 and dev == k_exp.get_device() == v_exp.get_device()
-                                  and k_exp.is_contiguous() and v_exp.is_contiguous() and k_exp.shape == ints == v_exp.shape))):
+    st = (_fast or _fast_path()).paged_write(k_new, v_new, k_pages, v_pages, table, cache_len, cache_len_out, new_len, k_exp, v_exp,
+                                             _handle(stream))
+    if st < 0:
+        rows = (table.shape[0], k_pages.shape[1], k_new.shape[2], k_pages.shape[3])
         _refuse_pool("attn_paged_write", k_pages, v_pages, table, k_exp, v_exp, (cache_len, cache_len_out, new_len),
-                     ((k_new, (table.shape[0], pool[1], T, pool[3]), "k_new"), (v_new, k_new.shape, "v_new")))
-    st = (_lib or load_library()).attn_paged_write(
-        k_new.data_ptr(), v_new.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), 0 if k_exp is None else k_exp.data_ptr(), 0 if v_exp is None else v_exp.data_ptr(), table.data_ptr(),
-        cache_len.data_ptr(), 0 if new_len is None else new_len.data_ptr(), cache_len_out.data_ptr(), B, Hkv, T, n_pages, page, per_seq, D,
-        ATTN_DTYPE_BF16 if dt is _BF16 else ATTN_DTYPE_FP16, _raw_stream(dev) if stream is None else _stream_handle(stream))
+                     ((k_new, rows, "k_new"), (v_new, rows, "v_new")))
     return st if st == ATTN_OK else _check(st, "attn_paged_write", check)
 
 
@@ -761,24 +726,10 @@ def attn_paged_read(k_pages, v_pages, table, cache_len, k, v, k_exp=None, v_exp=
     """The cached tokens of each sequence into contiguous rows k, v [B,Hkv,Lk,D]
     (or slices of a longer cache, as attn_fwd_ex takes them); rows from the
     sequence's length on are left as they were."""
-    B, Hkv, Lk, D = k.shape
-    n_pages, _, page, _ = pool = k_pages.shape
-    dt, dev, lens, per_seq = k.dtype, k.get_device(), (B,), table.shape[1]
-    held, ints = dt if k_exp is None else _E4M3, (n_pages, Hkv, page)
-    if not (dev >= 0 and dev == _current_device() and (dt is _BF16 or dt is _F16) and v.dtype is dt
-            and held is k_pages.dtype is v_pages.dtype and table.dtype is cache_len.dtype is _I32
-            and dev == v.get_device() == k_pages.get_device() == v_pages.get_device() == table.get_device() == cache_len.get_device()
-            and k_pages.is_contiguous() and v_pages.is_contiguous() and table.is_contiguous() and cache_len.is_contiguous()
-            and (pool, v_pages.shape, v.shape, table.shape, cache_len.shape) == ((n_pages, Hkv, page, D), pool, k.shape, (B, per_seq), lens)
-            and (k_exp is None) == (v_exp is None)
-            and (k_exp is None or (k_exp.dtype is v_exp.dtype is _I8 and dev == k_exp.get_device() == v_exp.get_device()
-                                  and k_exp.is_contiguous() and v_exp.is_contiguous() and k_exp.shape == ints == v_exp.shape))):
-        shape = (table.shape[0], pool[1], Lk, pool[3])
-        _refuse_pool("attn_paged_read", k_pages, v_pages, table, k_exp, v_exp, (cache_len,), sliced=((k, shape, "k"), (v, shape, "v")))
-    st = (_lib or load_library()).attn_paged_read(
-        k_pages.data_ptr(), v_pages.data_ptr(), 0 if k_exp is None else k_exp.data_ptr(), 0 if v_exp is None else v_exp.data_ptr(), table.data_ptr(), cache_len.data_ptr(), k.data_ptr(),
-        v.data_ptr(), kv_row_pitch(k, v), B, Hkv, Lk, n_pages, page, per_seq, D,
-        ATTN_DTYPE_BF16 if dt is _BF16 else ATTN_DTYPE_FP16, _raw_stream(dev) if stream is None else _stream_handle(stream))
+    st = (_fast or _fast_path()).paged_read(k_pages, v_pages, table, cache_len, k, v, k_exp, v_exp, _handle(stream))
+    if st < 0:
+        rows = (table.shape[0], k_pages.shape[1], k.shape[2], k_pages.shape[3])
+        _refuse_pool("attn_paged_read", k_pages, v_pages, table, k_exp, v_exp, (cache_len,), sliced=((k, rows, "k"), (v, rows, "v")))
     return st if st == ATTN_OK else _check(st, "attn_paged_read", check)
 
 
@@ -799,27 +750,11 @@ def attn_fwd_paged(q, k_pages, v_pages, table, cache_len, o, lse, workspace, sca
     """Attention of each sequence's T newest tokens q [B,Hq,T,D] (one, or a
     chain) over its pages, which hold them already: cache_len [B] int32 counts
     them (writes o, lse).  Pages as for attn_paged_write."""
-    B, Hq, T, D = q.shape
-    n_pages, Hkv, page, _ = pool = k_pages.shape
-    dt, dev, per_seq = q.dtype, q.get_device(), table.shape[1]
-    held, ints = dt if k_exp is None else _E4M3, (n_pages, Hkv, page)
-    if not (dev >= 0 and dev == _current_device() and (dt is _BF16 or dt is _F16) and o.dtype is dt
-            and held is k_pages.dtype is v_pages.dtype and table.dtype is cache_len.dtype is _I32
-            and lse.dtype is _F32 and workspace.dtype is _U8
-            and dev == k_pages.get_device() == v_pages.get_device() == table.get_device() == cache_len.get_device() == o.get_device()
-            == lse.get_device() == workspace.get_device()
-            and q.is_contiguous() and k_pages.is_contiguous() and v_pages.is_contiguous() and table.is_contiguous()
-            and cache_len.is_contiguous() and o.is_contiguous() and lse.is_contiguous() and workspace.is_contiguous()
-            and (pool, v_pages.shape, table.shape, cache_len.shape, o.shape, lse.shape)
-            == ((n_pages, Hkv, page, D), pool, (B, per_seq), (B,), q.shape, (B, Hq, T)) and (k_exp is None) == (v_exp is None)
-            and (k_exp is None or (k_exp.dtype is v_exp.dtype is _I8 and dev == k_exp.get_device() == v_exp.get_device()
-                                  and k_exp.is_contiguous() and v_exp.is_contiguous() and k_exp.shape == ints == v_exp.shape))):
-        _refuse_pool("attn_fwd_paged", k_pages, v_pages, table, k_exp, v_exp, (cache_len,),
-                     ((q, (table.shape[0], Hq, T, pool[3]), "q"), (o, q.shape, "o")), f32=((lse, (B, Hq, T), "lse"),), u8=(workspace,))
-    st = (_lib or load_library()).attn_fwd_paged(
-        q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), 0 if k_exp is None else k_exp.data_ptr(), 0 if v_exp is None else v_exp.data_ptr(), table.data_ptr(), cache_len.data_ptr(),
-        o.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.numel(), B, Hq, Hkv, T, n_pages, page, per_seq, D, scale,
-        ATTN_DTYPE_BF16 if dt is _BF16 else ATTN_DTYPE_FP16, _raw_stream(dev) if stream is None else _stream_handle(stream))
+    st = (_fast or _fast_path()).fwd_paged(q, k_pages, v_pages, table, cache_len, o, lse, workspace, scale, k_exp, v_exp, _handle(stream))
+    if st < 0:
+        B, Hq, T, D = table.shape[0], q.shape[1], q.shape[2], k_pages.shape[3]
+        _refuse_pool("attn_fwd_paged", k_pages, v_pages, table, k_exp, v_exp, (cache_len,), ((q, (B, Hq, T, D), "q"), (o, q.shape, "o")),
+                     f32=((lse, (B, Hq, T), "lse"),), u8=(workspace,))
     return st if st == ATTN_OK else _check(st, "attn_fwd_paged", check)
 
 
@@ -828,21 +763,13 @@ def attn_draft_verify(target, draft, tokens, u, r, accept_len, token, draft_len=
     probabilities float32 [B,T+1,V], draft's [B,T,V] (None: deterministic
     drafts) and uniform numbers u [B,T], and draws the next token by r [B]
     (writes accept_len, token: int32 [B])."""
-    B, T = tokens.shape
-    V, dev, lens = target.shape[-1], target.get_device(), (B,)
-    if not (dev >= 0 and dev == _current_device() and target.dtype is u.dtype is r.dtype is _F32
-            and tokens.dtype is accept_len.dtype is token.dtype is _I32
-            and dev == tokens.get_device() == u.get_device() == r.get_device() == accept_len.get_device() == token.get_device()
-            and target.is_contiguous() and tokens.is_contiguous() and u.is_contiguous() and r.is_contiguous()
-            and accept_len.is_contiguous() and token.is_contiguous()
-            and (target.shape, u.shape, r.shape, accept_len.shape, token.shape) == ((B, T + 1, V), tokens.shape, lens, lens, lens)
-            and (draft is None or _plain(draft, _F32, dev, (B, T, V))) and (draft_len is None or _plain(draft_len, _I32, dev, lens))):
+    st = (_fast or _fast_path()).draft_verify(target, draft, tokens, u, r, accept_len, token, draft_len, _handle(stream))
+    if st < 0:
+        (B, T), V = tokens.shape, target.shape[-1]
         _require("attn_draft_verify", f32=(target, draft, u, r), i32=(tokens, accept_len, token, draft_len))
-        _shapes("attn_draft_verify", (target, (B, T + 1, V), "target"), (draft, (B, T, V), "draft"), (u, (B, T), "u"), (r, lens, "r"),
-                (accept_len, lens, "accept_len"), (token, lens, "token"), (draft_len, lens, "draft_len"))
-    st = (_lib or load_library()).attn_draft_verify(target.data_ptr(), 0 if draft is None else draft.data_ptr(), tokens.data_ptr(), u.data_ptr(), r.data_ptr(),
-                                          0 if draft_len is None else draft_len.data_ptr(), accept_len.data_ptr(), token.data_ptr(), B, T, V,
-                                          _raw_stream(dev) if stream is None else _stream_handle(stream))
+        _shapes("attn_draft_verify", (target, (B, T + 1, V), "target"), (draft, (B, T, V), "draft"), (u, (B, T), "u"), (r, (B,), "r"),
+                (accept_len, (B,), "accept_len"), (token, (B,), "token"), (draft_len, (B,), "draft_len"))
+        _refuse("attn_draft_verify")
     return st if st == ATTN_OK else _check(st, "attn_draft_verify", check)
 
 

@@ -233,6 +233,23 @@ def test_verify_rejects(lib):
         assert verify(lib, **{name: at}) == INV, name
 
 
+def test_fast_path_refuses_what_it_cannot_take(lib):
+    """The compiled binding answers -1 (and leaves no error behind) for host tensors, other objects and wrong counts."""
+    from bwd_flashattention_fwd_gb300 import _binding
+
+    x = torch.zeros(2, 4, 3, 64, dtype=torch.bfloat16)
+    for name, n in (("qk_norm_rope", 12), ("qk_norm_rope_bwd", 17), ("paged_write", 11), ("paged_read", 9), ("fwd_paged", 12),
+                    ("draft_verify", 9)):
+        f = getattr(_binding, name)
+        for args in ((x,) * n, (None,) * n, ("x",) * n, (x,) * (n - 1), (x,) * (n + 1), ()):
+            assert f(*args) == -1, name
+    with pytest.raises(KeyError):
+        _binding.init({"attn_paged_read": 1})
+    gbattn._lib, keep = None, gbattn._lib
+    assert gbattn.load_library() is not None  # (the addresses are set again)
+    gbattn._lib = keep
+
+
 def test_binding_rejects_host_tensors():
     q = torch.zeros(1, 2, 8, 64, dtype=torch.bfloat16)
     pages = torch.zeros(4, 2, 8, 64, dtype=torch.bfloat16)

@@ -797,6 +797,28 @@ def test_two_streams_and_shared_pages():
             assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
+def test_streams_given_and_current():
+    """A stream as an object, as a handle and as the current one: the same results, in that stream's order."""
+    gen = torch.Generator().manual_seed(24)
+    c = rope_case(8, 2, 40, 4, 2, 64, 64, 1, BF, True, False, True)
+    want = run_rope(c)
+    ok()
+    st = torch.cuda.Stream()
+    for how in (st, st.cuda_stream, "current"):
+        got = [torch.full_like(t, float("nan")) for t in want]
+        torch.cuda.synchronize()
+        with torch.cuda.stream(st):
+            big = torch.randn(3000, 3000, device="cuda")
+            for _ in range(20):
+                big = big @ big * 1e-4
+            c["q"].mul_(1), c["k"].mul_(1)  # on st, behind the products
+            gbattn.attn_qk_norm_rope(c["q"], c["k"], *got, c["pos"], c["freq"], c["qw"], c["kw"], eps=c["eps"],
+                                     **({} if how == "current" else {"stream": how}))
+        st.synchronize()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    ok()
+
+
 def test_binding_refuses_shapes_and_types():
     z = torch.zeros
     q, k = z(2, 4, 3, 64, dtype=BF, device="cuda"), z(2, 2, 3, 64, dtype=BF, device="cuda")
