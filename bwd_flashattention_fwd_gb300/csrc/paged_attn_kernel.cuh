@@ -58,7 +58,7 @@ struct PagedGeom {
   static constexpr int join_pitch = D + 4;  // floats of a row where the warps meet
   __host__ __device__ static constexpr int smem(int rows) {  // (and the B + 1 starts and B lengths behind)
     const int join = NW * rows * join_pitch * 4;
-    return (RING > join ? RING : join) + (D / 16) * (rows / 8) * 256;
+    return (RING > join ? RING : join) + rows * D * 2;  // ring, Q
   }
 };
 
@@ -207,12 +207,21 @@ __device__ __forceinline__ void paged_part(const PagedAttnParams& p, const Paged
   auto& q_exp = sh.q_exp;
   auto& key_mask = sh.key_mask;
   auto& ml = sh.ml;
-  uint2* qf = reinterpret_cast<uint2*>(smem + (Gm::smem(ROWS) - KK * NT * 256));
+  uint16_t* const q_rows = reinterpret_cast<uint16_t*>(smem + (Gm::smem(ROWS) - ROWS * D * 2));  // [ROWS][D], then
+  uint2* const qf = reinterpret_cast<uint2*>(q_rows);                                            // as fragments
   float* join = reinterpret_cast<float*>(smem);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t4 = lane & 3;
   const uint32_t ring = smem_u32(smem) + warp * ST * Gm::TILE;
   [[maybe_unused]] const long long n_rows = (static_cast<long long>(p.c.n_pages) * p.c.Hkv) << p.c.shift;
   const int row0 = hd.rb * ROWS;  // first packed row
+
+  // ---- Q, ahead of everything ----
+  const uint8_t* q = static_cast<const uint8_t*>(p.q) + ((static_cast<size_t>(hd.b) * p.c.Hkv + hd.h) * p.R + row0) * (D * 2);
+  for (int x = threadIdx.x; x < ROWS * (D / 8); x += Gm::THREADS) {
+    const bool in = row0 + x / (D / 8) < p.R;
+    cp_async16(smem_u32(q_rows) + x * 16, in ? q + static_cast<size_t>(x) * 16 : static_cast<const uint8_t*>(p.q), in);
+  }
+  cp_async_commit();
 
   // ---- the warp's ring of tiles ----
   auto look_up = [&](int s) {  // page of this lane's key in the tile of step s
@@ -290,15 +299,15 @@ __device__ __forceinline__ void paged_part(const PagedAttnParams& p, const Paged
   int next_page = look_up(s0 + ST);
 
   // ---- Q as B fragments, the same for every warp ----
-  const uint16_t* q = static_cast<const uint16_t*>(p.q) + (static_cast<size_t>(hd.b) * p.c.Hkv + hd.h) * p.R * D;
+  cp_async_wait<2 * ST>();
+  __syncthreads();
   if constexpr (Q8) {
     for (int r = warp; r < ROWS; r += NW) {
       float m = 0.f;
-      if (row0 + r < p.R)
-        for (int d = lane; d < D / 2; d += 32) {
-          const float2 v = Elem<BF16>::unpack(reinterpret_cast<const uint32_t*>(q + static_cast<size_t>(row0 + r) * D)[d]);
-          m = fmaxf(m, fmaxf(fabsf(v.x), fabsf(v.y)));
-        }
+      for (int d = lane; d < D / 2; d += 32) {
+        const float2 v = Elem<BF16>::unpack(reinterpret_cast<const uint32_t*>(q_rows + r * D)[d]);
+        m = fmaxf(m, fmaxf(fabsf(v.x), fabsf(v.y)));
+      }
 #pragma unroll
       for (int x = 16; x; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
       // to a largest value in 2^14 .. 2^15 (a row of zeros or with an infinity as it is)
@@ -307,12 +316,18 @@ __device__ __forceinline__ void paged_part(const PagedAttnParams& p, const Paged
     }
     __syncthreads();
   }
-  for (int x = threadIdx.x; x < KK * NT * 32; x += Gm::THREADS) {
-    const int kk = x / (NT * 32), r = (x / 32 % NT) * 8 + (x % 32) / 4;
-    uint2 w = make_uint2(0u, 0u);
-    if (row0 + r < p.R)
-      w = q_fragment<D, BF16, Q8>(q + static_cast<size_t>(row0 + r) * D, kk, x & 3, Q8 ? exp2_int(static_cast<int>(q_exp[r])) : 1.f);
-    qf[x] = w;
+  constexpr int FRAGMENTS = (KK * NT * 32 + Gm::THREADS - 1) / Gm::THREADS;  // of a thread
+  {
+    uint2 w[FRAGMENTS];
+#pragma unroll
+    for (int i = 0; i < FRAGMENTS; ++i) {
+      const int x = i * Gm::THREADS + threadIdx.x, kk = x / (NT * 32), r = (x / 32 % NT) * 8 + (x % 32) / 4;
+      if (x < KK * NT * 32) w[i] = q_fragment<D, BF16, Q8>(q_rows + r * D, kk, x & 3, Q8 ? exp2_int(static_cast<int>(q_exp[r])) : 1.f);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < FRAGMENTS; ++i)
+      if (i * Gm::THREADS + threadIdx.x < KK * NT * 32) qf[i * Gm::THREADS + threadIdx.x] = w[i];
   }
   __syncthreads();
   uint2 qr[Q_REGS ? KK * NT : 1];

@@ -12,7 +12,7 @@
 // exchange and the norm's sums take log2(D / 16) shuffles.
 //
 // Angles.  pos * freq of a far position loses its fraction in 32 bits (2^20
-// radians leave 4 bits behind the point), so freq is taken once per CTA as a
+// radians leave 4 bits behind the point), so freq is taken once per thread as a
 // 64-bit fraction of a turn, F = freq / 2 pi mod 1, and pos * F mod 1 is an
 // integer product that wraps: exact to pos * 2^-63 turns.
 #pragma once
@@ -131,13 +131,22 @@ __global__ void __launch_bounds__(kRopeThreads, RopeGeom<D, BWD>::PER_SM) rope_k
   using Ln = RowLanes<D>;
   constexpr int WARPS = kRopeThreads / 32, DEPTH = Gm::DEPTH;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ uint64_t frac[D / 2];
   float* const cs = reinterpret_cast<float*>(smem + Gm::RING);                                  // [TOKENS][2][D / 2]
   long long* const offsets = reinterpret_cast<long long*>(smem + Gm::RING + Gm::CS);            // [2][3][TOKENS]
   float* const dw_sum = reinterpret_cast<float*>(smem + Gm::RING + Gm::CS + Gm::OFFSETS);       // [2][WARPS][D]
   grid_dependency_wait();  // the kernels before this one are complete
   if (threadIdx.x == 0) grid_launch_dependents();
   const int half = p.rot / 2;
+  // This thread's part of the sines: one pair, of every `abreast`-th token.
+  const int abreast = kRopeThreads / half, my_t = threadIdx.x / half, pair = threadIdx.x - my_t * half;
+  uint64_t my_frac = 0;
+  const int32_t* my_pos = p.pos;
+  if (my_t < abreast) {
+    my_frac = turn_fraction(__ldg(p.freq + pair));
+    int a = p.axis ? __ldg(p.axis + pair) : 0;
+    a = a < p.axes ? a : p.axes - 1;
+    my_pos += static_cast<long long>(a) * p.B * p.L;
+  }
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int j = lane % Ln::GROUP, group = threadIdx.x / Ln::GROUP;
   const bool on = j < Ln::LANES;
@@ -167,11 +176,7 @@ __global__ void __launch_bounds__(kRopeThreads, RopeGeom<D, BWD>::PER_SM) rope_k
 #pragma unroll 1
   for (int t0 = t_first; t0 < t_end; t0 += Gm::TOKENS) {
     const int n = min(t_end - t0, Gm::TOKENS);
-    if (t0 == t_first) {
-      for (int i = threadIdx.x; i < half; i += kRopeThreads) frac[i] = turn_fraction(p.freq[i]);
-    } else {
-      __syncthreads();  // the tokens before are done with
-    }
+    if (t0 != t_first) __syncthreads();  // the tokens before are done with
     if (threadIdx.x < n) {
       const int token = t0 + threadIdx.x, b = token / p.L, l = token - b * p.L;
 #pragma unroll
@@ -221,14 +226,12 @@ __global__ void __launch_bounds__(kRopeThreads, RopeGeom<D, BWD>::PER_SM) rope_k
     };
 #pragma unroll
     for (int i = 0; i < DEPTH - 1; ++i) fetch();
-    for (int i = threadIdx.x; i < n * half; i += kRopeThreads) {  // (while the first rows are on their way)
-      const int t = i / half, pair = i - t * half;
-      int a = p.axis ? __ldg(p.axis + pair) : 0;
-      a = a < p.axes ? a : p.axes - 1;
-      float c, s;
-      turn(__ldg(p.pos + static_cast<long long>(a) * tokens + t0 + t), frac[pair], c, s);
-      cs[t * D + pair] = c, cs[t * D + D / 2 + pair] = BWD ? -s : s;
-    }
+    if (my_t < abreast)  // (while the first rows are on their way)
+      for (int t = my_t; t < n; t += abreast) {
+        float c, s;
+        turn(__ldg(my_pos + t0 + t), my_frac, c, s);
+        cs[t * D + pair] = c, cs[t * D + D / 2 + pair] = BWD ? -s : s;
+      }
     __syncthreads();
     int round = 0;
 #pragma unroll 1
