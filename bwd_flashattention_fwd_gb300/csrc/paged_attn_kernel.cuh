@@ -40,26 +40,28 @@
 
 namespace gbattn {
 
-template <int D, bool Q8>
+// Warps: as many as hide the latency of a tile's chain (look-up, copy, products,
+// exponentials), which registers limit: 8 rows over quantised pages take 126
+// registers, 16 warps on an SM (8192 keys, 4 sequences: 18.2 us; 8 warps of 32-key tiles 21.7).
+template <int D, bool Q8, int NT>
 struct PagedGeom {
-  static constexpr int NW = D == 256 && !Q8 ? 2 : Q8 && D < 256 ? 8 : 4;  // warps of a CTA
+  static constexpr int NW = D == 256 && !Q8 ? 2 : Q8 && D * NT <= 128 ? 8 : 4;  // warps of a CTA
+  static constexpr int PER_SM = Q8 && NT == 2 && NW == 4 && D <= 128 ? 3 : 2;              // CTAs on an SM, as far as registers allow
   static constexpr int THREADS = NW * 32;
+  static constexpr int ROWS = 8 * NT;
   static constexpr int ROWB = D * (Q8 ? 1 : 2);            // bytes of a row
   static constexpr int CH = ROWB / 16;                     // its 16-byte pieces
   static constexpr int PITCH = (CH | 1) * 16;              // and its pitch in shared memory
-  static constexpr int KT = ROWB <= 64 ? 32 : 16;          // keys of a warp's tile
+  static constexpr int KT = 16;                            // keys of a warp's tile
   static constexpr int ST = 3;                             // tiles in flight
   static constexpr int KS = NW * KT;                       // keys of a CTA's step
   static constexpr int EXP = Q8 ? 2 * KT : 0;              // exponents of K, then of V
   static constexpr int TILE = 2 * KT * PITCH + EXP;        // K, V, exponents
   static constexpr int RING = NW * ST * TILE;
-  // CTAs on an SM, as far as registers allow
-  __host__ __device__ static constexpr int per_sm(int nt) { return NW <= 4 || D * nt <= 128 ? 2 : 1; }
-  static constexpr int join_pitch = D + 4;  // floats of a row where the warps meet
-  __host__ __device__ static constexpr int smem(int rows) {  // (and the B + 1 starts and B lengths behind)
-    const int join = NW * rows * join_pitch * 4;
-    return (RING > join ? RING : join) + rows * D * 2;  // ring, Q
-  }
+  static constexpr int JOIN_PITCH = D + 4;                 // floats of a row where the warps meet
+  static constexpr int JOIN = NW * ROWS * JOIN_PITCH * 4;
+  static constexpr int Q_AT = RING > JOIN ? RING : JOIN;   // Q's rows, then fragments
+  static constexpr int SMEM = Q_AT + ROWS * D * 2;         // (and the B + 1 starts and B lengths behind)
 };
 
 // The division of the work: the heads (b, h, row block) one after the other,
@@ -195,11 +197,11 @@ struct PagedShared {
 };
 
 // Steps s0 .. s1 - 1 of a head's keys, n in all, for one block of its rows: leaves the warps' results in
-// smem (rows of join_pitch floats) and sh.ml.
+// smem (rows of JOIN_PITCH floats) and sh.ml.
 template <int D, bool BF16, bool Q8, int NT>
 __device__ __forceinline__ void paged_part(const PagedAttnParams& p, const PagedHead& hd, int s0, int s1, int n, uint8_t* smem,
-                                           PagedShared<PagedGeom<D, Q8>::NW, PagedGeom<D, Q8>::ST, 8 * NT>& sh) {
-  using Gm = PagedGeom<D, Q8>;
+                                           PagedShared<PagedGeom<D, Q8, NT>::NW, PagedGeom<D, Q8, NT>::ST, 8 * NT>& sh) {
+  using Gm = PagedGeom<D, Q8, NT>;
   constexpr int NW = Gm::NW, KT = Gm::KT, ST = Gm::ST, MB = KT / 16, ROWS = 8 * NT, KK = D / 16;
   constexpr bool MMA_BF16 = BF16 && !Q8;          // type of the products' operands
   constexpr float kPShift = MMA_BF16 ? 0.f : 15.f;  // P is kept times 2^kPShift
@@ -207,8 +209,8 @@ __device__ __forceinline__ void paged_part(const PagedAttnParams& p, const Paged
   auto& q_exp = sh.q_exp;
   auto& key_mask = sh.key_mask;
   auto& ml = sh.ml;
-  uint16_t* const q_rows = reinterpret_cast<uint16_t*>(smem + (Gm::smem(ROWS) - ROWS * D * 2));  // [ROWS][D], then
-  uint2* const qf = reinterpret_cast<uint2*>(q_rows);                                            // as fragments
+  uint16_t* const q_rows = reinterpret_cast<uint16_t*>(smem + Gm::Q_AT);  // [ROWS][D], then
+  uint2* const qf = reinterpret_cast<uint2*>(q_rows);                         // as fragments
   float* join = reinterpret_cast<float*>(smem);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t4 = lane & 3;
   const uint32_t ring = smem_u32(smem) + warp * ST * Gm::TILE;
@@ -529,7 +531,7 @@ __device__ __forceinline__ void paged_part(const PagedAttnParams& p, const Paged
       for (int x = 4; x < 32; x <<= 1) l[i][e] += __shfl_xor_sync(0xffffffffu, l[i][e], x);
       const int r = i * 8 + 2 * t4 + e;
       if (g == 0) ml[warp][r][0] = m[i][e], ml[warp][r][1] = l[i][e];
-      float* dst = join + (warp * ROWS + r) * Gm::join_pitch;
+      float* dst = join + (warp * ROWS + r) * Gm::JOIN_PITCH;
 #pragma unroll
       for (int d = 0; d < KK; ++d) {
         if constexpr (Q8) {
@@ -544,9 +546,9 @@ __device__ __forceinline__ void paged_part(const PagedAttnParams& p, const Paged
 }
 
 // Row r, column quad c of a CTA's warps' results joined: O (unnormalised) and its maximum and sum.
-template <int D, bool Q8, int ROWS, class Shared>
+template <int D, bool Q8, int NT, class Shared>
 __device__ __forceinline__ float4 paged_join_warps(const float* join, const Shared& sh, int r, int c, float& mx, float& lsum) {
-  using Gm = PagedGeom<D, Q8>;
+  using Gm = PagedGeom<D, Q8, NT>;
   mx = sh.ml[0][r][0];
 #pragma unroll
   for (int w = 1; w < Gm::NW; ++w) mx = fmaxf(mx, sh.ml[w][r][0]);
@@ -556,7 +558,7 @@ __device__ __forceinline__ float4 paged_join_warps(const float* join, const Shar
 #pragma unroll
   for (int w = 0; w < Gm::NW; ++w) {
     const float f = ex2_approx(sh.ml[w][r][0] - ref);
-    const float4 a = *reinterpret_cast<const float4*>(join + (w * ROWS + r) * Gm::join_pitch + 4 * c);
+    const float4 a = *reinterpret_cast<const float4*>(join + (w * Gm::ROWS + r) * Gm::JOIN_PITCH + 4 * c);
     lsum = fmaf(sh.ml[w][r][1], f, lsum);
     o.x = fmaf(a.x, f, o.x), o.y = fmaf(a.y, f, o.y), o.z = fmaf(a.z, f, o.z), o.w = fmaf(a.w, f, o.w);
   }
@@ -574,14 +576,14 @@ __device__ __forceinline__ void paged_store(const PagedAttnParams& p, size_t row
 
 // A piece of the work per CTA; heads that several pieces share leave partial results.
 template <int D, bool BF16, bool Q8, int NT>
-__global__ void __launch_bounds__(PagedGeom<D, Q8>::THREADS, PagedGeom<D, Q8>::per_sm(NT)) attn_paged_kernel(const PagedAttnParams p) {
-  using Gm = PagedGeom<D, Q8>;
+__global__ void __launch_bounds__(PagedGeom<D, Q8, NT>::THREADS, PagedGeom<D, Q8, NT>::PER_SM) attn_paged_kernel(const PagedAttnParams p) {
+  using Gm = PagedGeom<D, Q8, NT>;
   constexpr int ROWS = 8 * NT;
   constexpr float kPShift = BF16 && !Q8 ? 0.f : 15.f;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ PagedShared<Gm::NW, Gm::ST, ROWS> sh;
   const float* join = reinterpret_cast<const float*>(smem);
-  int* starts = reinterpret_cast<int*>(smem + Gm::smem(ROWS));  // [B + 1], then lengths [B]
+  int* starts = reinterpret_cast<int*>(smem + Gm::SMEM);  // [B + 1], then lengths [B]
   grid_dependency_wait();  // the kernels before this one are complete
   if (threadIdx.x == 0) grid_launch_dependents();
   paged_starts(p, Gm::KS, starts, starts + p.B + 1);
@@ -604,7 +606,7 @@ __global__ void __launch_bounds__(PagedGeom<D, Q8>::THREADS, PagedGeom<D, Q8>::p
       const int r = x / (D / 4), c = x - r * (D / 4);
       if (hd.rb * ROWS + r >= p.R) continue;
       float mx, lsum;
-      const float4 o = paged_join_warps<D, Q8, ROWS>(join, sh, r, c, mx, lsum);
+      const float4 o = paged_join_warps<D, Q8, NT>(join, sh, r, c, mx, lsum);
       if (whole) {
         paged_store<D, BF16>(p, out0 + r, c, o, mx, lsum, kPShift);
       } else if (dbg_in_range(part0 + r, 1, static_cast<size_t>(p.n_groups) * 2 * ROWS, p.status, 123)) {
@@ -618,8 +620,8 @@ __global__ void __launch_bounds__(PagedGeom<D, Q8>::THREADS, PagedGeom<D, Q8>::p
 // Short caches: a cluster of `size` CTAs per head shares its steps out and joins their results through distributed
 // shared memory, in one launch.
 template <int D, bool BF16, bool Q8, int NT>
-__global__ void __launch_bounds__(PagedGeom<D, Q8>::THREADS, PagedGeom<D, Q8>::per_sm(NT)) attn_paged_cluster_kernel(const PagedAttnParams p, int size) {
-  using Gm = PagedGeom<D, Q8>;
+__global__ void __launch_bounds__(PagedGeom<D, Q8, NT>::THREADS, PagedGeom<D, Q8, NT>::PER_SM) attn_paged_cluster_kernel(const PagedAttnParams p, int size) {
+  using Gm = PagedGeom<D, Q8, NT>;
   constexpr int ROWS = 8 * NT;
   constexpr float kPShift = BF16 && !Q8 ? 0.f : 15.f;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -639,11 +641,11 @@ __global__ void __launch_bounds__(PagedGeom<D, Q8>::THREADS, PagedGeom<D, Q8>::p
   for (int x = threadIdx.x; x < rows * (D / 4); x += Gm::THREADS) {
     const int r = x / (D / 4), c = x - r * (D / 4);
     float mx, lsum;
-    const float4 o = paged_join_warps<D, Q8, ROWS>(join, sh, r, c, mx, lsum);
+    const float4 o = paged_join_warps<D, Q8, NT>(join, sh, r, c, mx, lsum);
     if (size == 1) {
       paged_store<D, BF16>(p, out0 + r, c, o, mx, lsum, kPShift);
     } else {  // over the first warp's, which no other thread reads here
-      *reinterpret_cast<float4*>(join + r * Gm::join_pitch + 4 * c) = o;
+      *reinterpret_cast<float4*>(join + r * Gm::JOIN_PITCH + 4 * c) = o;
       if (c == 0) stat[r] = make_float2(mx, lsum);
     }
   }
@@ -665,7 +667,7 @@ __global__ void __launch_bounds__(PagedGeom<D, Q8>::THREADS, PagedGeom<D, Q8>::p
     for (int k = 0; k < kPagedCluster; ++k) {
       if (k >= size) continue;
       const float f = ex2_approx(ml[k].x - ref);
-      const float4 a = ld_cluster_f4(cluster_map(join_at + (r * Gm::join_pitch + 4 * c) * 4, k));
+      const float4 a = ld_cluster_f4(cluster_map(join_at + (r * Gm::JOIN_PITCH + 4 * c) * 4, k));
       lsum = fmaf(ml[k].y, f, lsum);
       o.x = fmaf(a.x, f, o.x), o.y = fmaf(a.y, f, o.y), o.z = fmaf(a.z, f, o.z), o.w = fmaf(a.w, f, o.w);
     }
@@ -680,7 +682,7 @@ constexpr int kPagedJoinThreads = 256;
 
 template <int D, bool BF16, bool Q8, int NT, int WARPS>
 __global__ void __launch_bounds__(kPagedJoinThreads) attn_paged_join_kernel(const PagedAttnParams p) {
-  using Gm = PagedGeom<D, Q8>;
+  using Gm = PagedGeom<D, Q8, NT>;
   constexpr int ROWS = 8 * NT, QUADS = D / 4, Q = (QUADS + 31) / 32;  // column quads, and a lane's
   constexpr float kPShift = BF16 && !Q8 ? 0.f : 15.f;
   __shared__ int starts[kPagedMaxB + 1];

@@ -48,14 +48,15 @@ int launch_cluster(void (*kern)(Params...), unsigned grid, int size, int threads
 
 template <bool BF16, bool Q8, int NT>
 int impl(const PagedAttnParams& p0, int num_sms, cudaStream_t stream) {
-  using Gm = PagedGeom<kD, Q8>;
+  using Gm = PagedGeom<kD, Q8, NT>;
   PagedAttnParams p = p0;
   constexpr int rows = 8 * NT;
   p.n_rb = (p.R + rows - 1) / rows;
-  const int smem = Gm::smem(rows) + (2 * p.B + 1) * 4;
-  // two CTAs per SM where their shared memory (1 KB more each, 228 KB in all) and static arrays allow it
-  constexpr int fixed = 1024 + 256 + Gm::NW * (rows * 8 + Gm::ST * 4) + rows * 4;
-  const int per_sm = Gm::per_sm(NT) == 2 && 2 * (smem + fixed) <= 233472 ? 2 : 1;
+  const int smem = Gm::SMEM + (2 * p.B + 1) * 4;
+  // CTAs per SM: shared memory (1 KB more each, 228 KB in all) and static arrays
+  constexpr int fixed = 1024 + 256 + Gm::NW * (rows * 8 + Gm::ST * 4) + rows * 12;
+  int per_sm = Gm::PER_SM;
+  while (per_sm > 1 && per_sm * (smem + fixed) > 233472) --per_sm;
   p.n_groups = per_sm * (num_sms < kTreeMaxCtas ? num_sms : kTreeMaxCtas);
   const long long all = static_cast<long long>(p.B) * p.c.Hkv * p.n_rb, room = static_cast<long long>(p.c.per_seq) << p.c.shift;
   const long long steps = (room + Gm::KS - 1) / Gm::KS;
@@ -65,13 +66,13 @@ int impl(const PagedAttnParams& p0, int num_sms, cudaStream_t stream) {
   if (per <= kPagedShort && per * (kPagedAlone<Q8> - 100.f * size * all / p.n_groups) <= 400.f) {
     auto kern = attn_paged_cluster_kernel<kD, BF16, Q8, NT>;
     static std::atomic<uint64_t> done{0};
-    if (!set_smem_limit(kern, Gm::smem(rows), done)) return kLaunchCudaError;
-    return launch_cluster(kern, static_cast<unsigned>(all) * size, size, Gm::THREADS, Gm::smem(rows), stream, p, size);
+    if (!set_smem_limit(kern, Gm::SMEM, done)) return kLaunchCudaError;
+    return launch_cluster(kern, static_cast<unsigned>(all) * size, size, Gm::THREADS, Gm::SMEM, stream, p, size);
   }
   p.part_ml = p.part + static_cast<size_t>(kPagedMaxCtas) * 2 * rows * kD;
   auto kern = attn_paged_kernel<kD, BF16, Q8, NT>;
   static std::atomic<uint64_t> done{0};
-  if (!set_smem_limit(kern, Gm::smem(rows) + (2 * kPagedMaxB + 1) * 4, done)) return kLaunchCudaError;
+  if (!set_smem_limit(kern, Gm::SMEM + (2 * kPagedMaxB + 1) * 4, done)) return kLaunchCudaError;
   const int r = launch_dependent(kern, dim3(p.n_groups), Gm::THREADS, smem, stream, p);
   if (r != kLaunchOk || p.n_groups == 1) return r;
   // a block's warps share a row's partial results where there are many

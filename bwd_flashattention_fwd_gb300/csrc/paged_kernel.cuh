@@ -35,12 +35,27 @@ __device__ __forceinline__ int row_exponent(float m) {
 
 __device__ __forceinline__ float exp2_int(int e) { return __int_as_float((e + 127) << 23); }
 
-// Two values as e4m3 codes, round to nearest even; what is not finite becomes NaN.
+// Two values as e4m3 codes, round to nearest even; CHECK: what is not finite becomes NaN.
+template <bool CHECK>
 __device__ __forceinline__ uint32_t e4m3_pair(float a, float b) {
   uint32_t r = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-  if (!(fabsf(a) < INFINITY)) r |= 0x007fu;
-  if (!(fabsf(b) < INFINITY)) r |= 0x7f00u;
+  if constexpr (CHECK) {
+    if (!(fabsf(a) < INFINITY)) r |= 0x007fu;
+    if (!(fabsf(b) < INFINITY)) r |= 0x7f00u;
+  }
   return r;
+}
+
+// Sixteen values times `by` as codes.
+template <bool BF16, bool CHECK>
+__device__ __forceinline__ uint4 e4m3_16(const uint4 (&x)[2], float by) {
+  float f[16];
+  uint32_t w[4];
+  unpack8<BF16>(x[0], f), unpack8<BF16>(x[1], f + 8);
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    w[i] = e4m3_pair<CHECK>(f[4 * i] * by, f[4 * i + 1] * by) | e4m3_pair<CHECK>(f[4 * i + 2] * by, f[4 * i + 3] * by) << 16;
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 __device__ __forceinline__ float2 e4m3_unpack(uint32_t pair) {
@@ -50,9 +65,28 @@ __device__ __forceinline__ float2 e4m3_unpack(uint32_t pair) {
 
 constexpr int kPagedThreads = 256;
 
+// A lane's 16 values of a row, 32 bytes: in one access where the arrays start on 32 bytes (WIDE), else in two.  (Two
+// leave half a sector each: quantised prefixes read back in 27.9 us by halves, 22.3 by wholes.)
+template <bool WIDE>
+__device__ __forceinline__ void load32(const void* p, uint4 (&x)[2]) {
+  if constexpr (WIDE) {
+    ld_global_v8(p, x[0], x[1]);
+  } else {
+    x[0] = static_cast<const uint4*>(p)[0], x[1] = static_cast<const uint4*>(p)[1];
+  }
+}
+template <bool WIDE>
+__device__ __forceinline__ void store32(void* p, const uint4& a, const uint4& b) {
+  if constexpr (WIDE) {
+    st_global_v8(p, a, b);
+  } else {
+    static_cast<uint4*>(p)[0] = a, static_cast<uint4*>(p)[1] = b;
+  }
+}
+
 // A token's row of K and its row of V belong to D / 16 lanes, 16 consecutive
 // values each; both are loaded before the page is looked up.
-template <int D, bool BF16, bool Q8>
+template <int D, bool BF16, bool Q8, bool WIDE>
 __global__ void __launch_bounds__(kPagedThreads) attn_paged_write_kernel(const PagedWriteParams p) {
   using Gm = RowLanes<D>;
   grid_dependency_wait();  // the kernels before this one are complete
@@ -69,9 +103,8 @@ __global__ void __launch_bounds__(kPagedThreads) attn_paged_write_kernel(const P
     const bool in = r < rows;
     uint4 x[2][2] = {};
     if (in && j < Gm::LANES) {
-      const uint4* ks = static_cast<const uint4*>(p.k_new) + r * (D / 8) + 2 * j;
-      const uint4* vs = static_cast<const uint4*>(p.v_new) + r * (D / 8) + 2 * j;
-      x[0][0] = ks[0], x[0][1] = ks[1], x[1][0] = vs[0], x[1][1] = vs[1];
+      load32<WIDE>(static_cast<const uint4*>(p.k_new) + r * (D / 8) + 2 * j, x[0]);
+      load32<WIDE>(static_cast<const uint4*>(p.v_new) + r * (D / 8) + 2 * j, x[1]);
     }
     long long dst = -1;
     if (in) {
@@ -87,25 +120,35 @@ __global__ void __launch_bounds__(kPagedThreads) attn_paged_write_kernel(const P
 #pragma unroll
     for (int v = 0; v < 2; ++v) {
       if constexpr (!Q8) {
-        if (live) {
-          uint4* d = static_cast<uint4*>(v ? p.c.v : p.c.k) + dst * (D / 8) + 2 * j;
-          d[0] = x[v][0], d[1] = x[v][1];
-        }
+        if (live) store32<WIDE>(static_cast<uint4*>(v ? p.c.v : p.c.k) + dst * (D / 8) + 2 * j, x[v][0], x[v][1]);
       } else {
-        float f[16], m = 0.f;
-        unpack8<BF16>(x[v][0], f), unpack8<BF16>(x[v][1], f + 8);
+        // the row's largest magnitude, from the 16-bit patterns (which order as the values do)
+        const uint32_t u[8] = {x[v][0].x, x[v][0].y, x[v][0].z, x[v][0].w, x[v][1].x, x[v][1].y, x[v][1].z, x[v][1].w};
+        constexpr uint32_t kInf = BF16 ? 0x7f80u : 0x7c00u;
+        uint32_t m = 0;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) m = fabsf(f[i]) < INFINITY ? fmaxf(m, fabsf(f[i])) : m;
+        for (int i = 0; i < 8; ++i) m = __vmaxu2(m, u[i] & 0x7fff7fffu);
+        m = max(m & 0xffffu, m >> 16);
 #pragma unroll
-        for (int k = Gm::GROUP / 2; k; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
-        const int e = row_exponent(m);
-        const float by = exp2_int(-e);
-        uint32_t w[4];
+        for (int k = Gm::GROUP / 2; k; k >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, k));
+        const bool fine = m < kInf;
+        if (__any_sync(0xffffffffu, !fine)) {  // the largest finite one, for rows with others
+          uint32_t f = 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          w[i] = e4m3_pair(f[4 * i] * by, f[4 * i + 1] * by) | e4m3_pair(f[4 * i + 2] * by, f[4 * i + 3] * by) << 16;
+          for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const uint32_t y = u[i] >> (16 * k) & 0x7fffu;
+              if (y < kInf) f = max(f, y);
+            }
+#pragma unroll
+          for (int k = Gm::GROUP / 2; k; k >>= 1) f = max(f, __shfl_xor_sync(0xffffffffu, f, k));
+          m = f;
+        }
+        const int e = row_exponent(Elem<BF16>::unpack(m).x);
+        const uint4 w = fine ? e4m3_16<BF16, false>(x[v], exp2_int(-e)) : e4m3_16<BF16, true>(x[v], exp2_int(-e));
         if (live) {
-          (static_cast<uint4*>(v ? p.c.v : p.c.k) + dst * (D / 16))[j] = make_uint4(w[0], w[1], w[2], w[3]);
+          (static_cast<uint4*>(v ? p.c.v : p.c.k) + dst * (D / 16))[j] = w;
           if (j == 0) (v ? p.c.v_exp : p.c.k_exp)[dst] = static_cast<int8_t>(e);
         }
       }
@@ -126,7 +169,7 @@ __device__ __forceinline__ uint32_t dequant_pair(uint32_t pair, float by) {
   return Elem<BF16>::pack(v.x, v.y);
 }
 
-template <bool BF16, bool EDGE>
+template <bool BF16, bool EDGE, bool WIDE>
 __device__ __forceinline__ void dequant16(const uint4& w, float by, uint4* d) {
   const uint32_t u[4] = {w.x, w.y, w.z, w.w};
   uint32_t o[8];
@@ -135,8 +178,7 @@ __device__ __forceinline__ void dequant16(const uint4& w, float by, uint4* d) {
     o[2 * k] = dequant_pair<BF16, EDGE>(u[k] & 0xffffu, by);
     o[2 * k + 1] = dequant_pair<BF16, EDGE>(u[k] >> 16, by);
   }
-  d[0] = make_uint4(o[0], o[1], o[2], o[3]);
-  d[1] = make_uint4(o[4], o[5], o[6], o[7]);
+  store32<WIDE>(d, make_uint4(o[0], o[1], o[2], o[3]), make_uint4(o[4], o[5], o[6], o[7]));
 }
 
 // A block: read_rows tokens of one sequence and head.  A thread holds the same
@@ -145,7 +187,7 @@ __device__ __forceinline__ void dequant16(const uint4& w, float by, uint4* d) {
 constexpr int kReadTokens = 2;  // of a thread
 constexpr int read_rows(int D) { return kReadTokens * (kPagedThreads / (D / 16)); }
 
-template <int D, bool BF16, bool Q8>
+template <int D, bool BF16, bool Q8, bool WIDE>
 __global__ void __launch_bounds__(kPagedThreads) attn_paged_read_kernel(const PagedReadParams p) {
   constexpr int LANES = D / 16, GROUPS = kPagedThreads / LANES, N = kReadTokens, ROWS = N * GROUPS;
   grid_dependency_wait();
@@ -185,26 +227,24 @@ __global__ void __launch_bounds__(kPagedThreads) attn_paged_read_kernel(const Pa
           uint4* d = static_cast<uint4*>(v ? p.v : p.k) + (out0 + row[i]) * (D / 8) + 2 * c;
           // 448 * 2^e is within the type up to these
           if (e[v][i] <= (BF16 ? 118 : 7))
-            dequant16<BF16, false>(w[v][i], exp2_int(e[v][i]), d);
+            dequant16<BF16, false, WIDE>(w[v][i], exp2_int(e[v][i]), d);
           else
-            dequant16<BF16, true>(w[v][i], exp2_int(e[v][i]), d);
+            dequant16<BF16, true, WIDE>(w[v][i], exp2_int(e[v][i]), d);
         }
     } else {
       uint4 w[2][N][2];
 #pragma unroll
       for (int i = 0; i < N; ++i)
         if (from[i] >= 0) {
-          const uint4* ks = static_cast<const uint4*>(p.c.k) + from[i] * (D / 8) + 2 * c;
-          const uint4* vs = static_cast<const uint4*>(p.c.v) + from[i] * (D / 8) + 2 * c;
-          w[0][i][0] = ks[0], w[0][i][1] = ks[1], w[1][i][0] = vs[0], w[1][i][1] = vs[1];
+          load32<WIDE>(static_cast<const uint4*>(p.c.k) + from[i] * (D / 8) + 2 * c, w[0][i]);
+          load32<WIDE>(static_cast<const uint4*>(p.c.v) + from[i] * (D / 8) + 2 * c, w[1][i]);
         }
 #pragma unroll
       for (int i = 0; i < N; ++i)
 #pragma unroll
         for (int v = 0; v < 2; ++v) {
           if (from[i] < 0) continue;
-          uint4* d = static_cast<uint4*>(v ? p.v : p.k) + (out0 + row[i]) * (D / 8) + 2 * c;
-          d[0] = w[v][i][0], d[1] = w[v][i][1];
+          store32<WIDE>(static_cast<uint4*>(v ? p.v : p.k) + (out0 + row[i]) * (D / 8) + 2 * c, w[v][i][0], w[v][i][1]);
         }
     }
   }

@@ -140,22 +140,25 @@ PagedCache paged_cache(const void* k, const void* v, const int8_t* ke, const int
 
 long long pool_rows(int Hkv, int n_pages, int page_size) { return static_cast<long long>(n_pages) * Hkv * page_size; }
 
-template <int D, bool BF16>
+bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
+
+template <int D, bool BF16, bool WIDE>
 int write_impl(const PagedWriteParams& p, int num_sms, cudaStream_t stream) {
   constexpr int per_cta = kPagedThreads / RowLanes<D>::GROUP;
   const long long ctas = (static_cast<long long>(p.B) * p.c.Hkv * p.T + per_cta - 1) / per_cta, most = 8LL * num_sms;
   const dim3 grid(static_cast<unsigned>(ctas < most ? ctas : most));
-  return p.c.k_exp ? launch_dependent(attn_paged_write_kernel<D, BF16, true>, grid, kPagedThreads, 0, stream, p)
-                   : launch_dependent(attn_paged_write_kernel<D, BF16, false>, grid, kPagedThreads, 0, stream, p);
+  return p.c.k_exp ? launch_dependent(attn_paged_write_kernel<D, BF16, true, WIDE>, grid, kPagedThreads, 0, stream, p)
+                   : launch_dependent(attn_paged_write_kernel<D, BF16, false, WIDE>, grid, kPagedThreads, 0, stream, p);
 }
 
-template <int D, bool BF16>
+template <int D, bool BF16, bool WIDE>
 int read_impl(const PagedReadParams& p, int num_sms, cudaStream_t stream) {
   const int room = p.c.per_seq << p.c.shift, heads = p.B * p.c.Hkv;
-  const long long blocks = (static_cast<long long>(p.Lk < room ? p.Lk : room) + read_rows(D) - 1) / read_rows(D), most = 64LL * num_sms / heads + 1;  // (blocks past a sequence's end leave at once)
+  const long long blocks = (static_cast<long long>(p.Lk < room ? p.Lk : room) + read_rows(D) - 1) / read_rows(D);
+  const long long most = 64LL * num_sms / heads + 1;  // (blocks past a sequence's end leave at once)
   const dim3 grid(static_cast<unsigned>(blocks < most ? blocks : most), heads);
-  return p.c.k_exp ? launch_dependent(attn_paged_read_kernel<D, BF16, true>, grid, kPagedThreads, 0, stream, p)
-                   : launch_dependent(attn_paged_read_kernel<D, BF16, false>, grid, kPagedThreads, 0, stream, p);
+  return p.c.k_exp ? launch_dependent(attn_paged_read_kernel<D, BF16, true, WIDE>, grid, kPagedThreads, 0, stream, p)
+                   : launch_dependent(attn_paged_read_kernel<D, BF16, false, WIDE>, grid, kPagedThreads, 0, stream, p);
 }
 
 template <template <int, bool> class F, typename P>
@@ -169,11 +172,17 @@ int by_type(const P& p, int D, bool bf16, int num_sms, cudaStream_t stream) {
 }
 template <int D, bool BF16>
 struct Write {
-  static int run(const PagedWriteParams& p, int n, cudaStream_t s) { return write_impl<D, BF16>(p, n, s); }
+  static int run(const PagedWriteParams& p, int n, cudaStream_t s) {
+    const bool wide = aligned32(p.k_new) && aligned32(p.v_new) && (p.c.k_exp || (aligned32(p.c.k) && aligned32(p.c.v)));
+    return wide ? write_impl<D, BF16, true>(p, n, s) : write_impl<D, BF16, false>(p, n, s);
+  }
 };
 template <int D, bool BF16>
 struct Read {
-  static int run(const PagedReadParams& p, int n, cudaStream_t s) { return read_impl<D, BF16>(p, n, s); }
+  static int run(const PagedReadParams& p, int n, cudaStream_t s) {
+    const bool wide = aligned32(p.k) && aligned32(p.v) && (p.c.k_exp || (aligned32(p.c.k) && aligned32(p.c.v)));
+    return wide ? read_impl<D, BF16, true>(p, n, s) : read_impl<D, BF16, false>(p, n, s);
+  }
 };
 
 attn_status_t check_paged_attn(int B, int Hq, int Hkv, int T, int page_size, int per_seq, int D) {

@@ -36,7 +36,7 @@ struct RopeParams {
 constexpr int kPagedMaxB = 1024;        // sequences (each CTA holds the lengths' prefix sums in shared memory)
 constexpr int kPagedMaxRows = 128;      // G * T
 constexpr int kPagedMaxTokens = 1 << 30;  // a sequence's room (token numbers are ints)
-constexpr int kPagedMaxCtas = 2 * kTreeMaxCtas;
+constexpr int kPagedMaxCtas = 3 * kTreeMaxCtas;
 constexpr int kPagedCluster = 8;  // CTAs that share a head of a short cache, at most
 // A quantised row's exponent: scores and sums that carry 2^e and 2^-e stay inside fp32.
 constexpr int kExpMin = -64, kExpMax = 120;

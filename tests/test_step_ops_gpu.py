@@ -389,6 +389,38 @@ def test_paged_read(case, q8):
         assert torch.equal(got.cpu(), want)
 
 
+@pytest.mark.parametrize("q8", [False, True])
+def test_pages_on_16_bytes(q8):
+    """Arrays that start on 16 bytes, not on 32: the same bits as aligned ones."""
+    gen = torch.Generator().manual_seed(25)
+    B, H, T, D, page, per_seq = 2, 3, 40, 96, 16, 4
+
+    def shifted(t):
+        n = t.numel() * t.element_size()
+        buf = torch.empty(n + 64, dtype=torch.uint8, device="cuda")
+        out = buf[16: 16 + n].view(t.dtype).view(t.shape)
+        assert out.data_ptr() % 32 == 16
+        return out.copy_(t) if t.dtype != F8 else out.view(torch.uint8).copy_(t.view(torch.uint8)).view(F8)
+
+    pool = make_pool(gen, 8, H, page, D, HF, q8)
+    kn, vn = rand(gen, (B, H, T, D), HF), rand(gen, (B, H, T, D), HF)
+    table, lens = torch.randperm(8, generator=gen).view(B, per_seq).to(torch.int32).cuda(), i32([3, 17])
+    results = []
+    for move in (lambda t: t.clone(), shifted):
+        k, v = move(pool[0]), move(pool[1])
+        ke, ve = (None, None) if not q8 else (pool[2].clone(), pool[3].clone())
+        out = i32([0, 0])
+        gbattn.attn_paged_write(move(kn), move(vn), k, v, table, lens, out, k_exp=ke, v_exp=ve)
+        ko, vo = move(torch.zeros(B, H, 60, D, dtype=HF, device="cuda")), move(torch.zeros(B, H, 60, D, dtype=HF, device="cuda"))
+        gbattn.attn_paged_read(k, v, table, out, ko, vo, k_exp=ke, v_exp=ve)
+        q = move(rand(torch.Generator().manual_seed(1), (B, 6, 1, D), HF))
+        o = run_paged(q, (k, v, ke, ve), table, out, 0.1)
+        ok()
+        results.append([out, pool64(k), pool64(v), ko.clone(), vo.clone(), *o])
+    for x, y in zip(*results):
+        assert np.array_equal(x, y) if isinstance(x, np.ndarray) else torch.equal(x, y)
+
+
 PAGED = [
     # B, Hq, Hkv, T, D, page, per_seq, dtype, lengths
     (1, 1, 1, 1, 64, 8, 1, BF, [1]),
