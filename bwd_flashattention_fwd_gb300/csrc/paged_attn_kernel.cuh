@@ -220,7 +220,8 @@ __device__ __forceinline__ void paged_part(const PagedAttnParams& p, const Paged
   // ---- Q, ahead of everything ----
   const uint8_t* q = static_cast<const uint8_t*>(p.q) + ((static_cast<size_t>(hd.b) * p.c.Hkv + hd.h) * p.R + row0) * (D * 2);
   for (int x = threadIdx.x; x < ROWS * (D / 8); x += Gm::THREADS) {
-    const bool in = row0 + x / (D / 8) < p.R;
+    const bool in = row0 + x / (D / 8) < p.R &&
+                    dbg_in_range(static_cast<size_t>(q - static_cast<const uint8_t*>(p.q)) + x * 16, 16, static_cast<size_t>(p.B) * p.Hq * p.T * D * 2, p.status, 126);
     cp_async16(smem_u32(q_rows) + x * 16, in ? q + static_cast<size_t>(x) * 16 : static_cast<const uint8_t*>(p.q), in);
   }
   cp_async_commit();
@@ -229,6 +230,7 @@ __device__ __forceinline__ void paged_part(const PagedAttnParams& p, const Paged
   auto look_up = [&](int s) {  // page of this lane's key in the tile of step s
     const int key = (s * NW + warp) * KT + (lane & (KT - 1));
     if (s >= s1 || key >= n) return -1;
+    if (!dbg_in_range(static_cast<size_t>(hd.b) * p.c.per_seq + (key >> p.c.shift), 1, static_cast<size_t>(p.B) * p.c.per_seq, p.status, 125)) return -1;
     const int pg = __ldg(p.c.table + static_cast<size_t>(hd.b) * p.c.per_seq + (key >> p.c.shift));
     return pg < p.c.n_pages ? pg : -1;
   };
@@ -688,8 +690,10 @@ __global__ void __launch_bounds__(kPagedJoinThreads) attn_paged_join_kernel(cons
   __shared__ int starts[kPagedMaxB + 1];
   __shared__ float4 sum[WARPS > 1 ? WARPS : 1][QUADS];
   __shared__ float2 stat[WARPS];
-  paged_starts(p, Gm::KS, starts, nullptr);  // (lengths: nothing that the kernel before writes)
-  grid_dependency_wait();
+  // (lengths: nothing that the kernel before writes; it has waited for what did.  So the first row's part of the plan is
+  // worked out before the wait.)
+  paged_starts(p, Gm::KS, starts, nullptr);
+  bool waited = false;
   const PagedPieces pieces(starts[p.B], p.n_groups);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const long long tasks = static_cast<long long>(p.B) * p.c.Hkv * p.R;
@@ -705,6 +709,8 @@ __global__ void __launch_bounds__(kPagedJoinThreads) attn_paged_join_kernel(cons
     if (steps == 0) continue;
     const int c0 = pieces.of(s), c1 = pieces.of(s + steps - 1);
     if (c0 == c1) continue;  // one CTA had it all
+    if (!waited) grid_dependency_wait();
+    waited = true;
     const int n = c1 - c0 + 1, first = WARPS > 1 ? n * warp / WARPS : 0, last = WARPS > 1 ? n * (warp + 1) / WARPS : n;
     auto at = [&](int i) { return (static_cast<size_t>(c0 + i) * 2 + (i == 0 ? 1 : 0)) * ROWS + r; };
     // this warp's partial results: running maximum and sums, 32 of them at a time
@@ -797,6 +803,8 @@ __global__ void __launch_bounds__(kPagedJoinThreads) attn_paged_join_kernel(cons
       if (lane == 0) p.lse[task] = mx == -INFINITY ? INFINITY : mx - kPShift + log2f(l);
     }
   }
+  // (a grid that ended before the one ahead of it would let the next one in early)
+  if (!waited) grid_dependency_wait();
 }
 
 }  // namespace gbattn

@@ -18,7 +18,8 @@
 namespace gbattn {
 
 // Row number (of D values) of token `at` of sequence b and head h in the pool, or -1 where its page is none.
-__device__ __forceinline__ long long paged_row(const PagedCache& c, int b, int h, int at) {
+__device__ __forceinline__ long long paged_row(const PagedCache& c, int b, int h, int at, [[maybe_unused]] int B, [[maybe_unused]] int* status) {
+  if (!dbg_in_range(static_cast<size_t>(b) * c.per_seq + (at >> c.shift), 1, static_cast<size_t>(B) * c.per_seq, status, 113)) return -1;
   const int page = __ldg(c.table + static_cast<size_t>(b) * c.per_seq + (at >> c.shift));
   if (page < 0 || page >= c.n_pages) return -1;
   return ((static_cast<long long>(page) * c.Hkv + h) << c.shift) + (at & ((1 << c.shift) - 1));
@@ -113,7 +114,7 @@ __global__ void __launch_bounds__(kPagedThreads) attn_paged_write_kernel(const P
       const int h = static_cast<int>(bh - static_cast<long long>(b) * p.c.Hkv);
       const int len = clamp_len(__ldg(p.cache_len + b), room);
       const int n = min(p.new_len ? clamp_len(__ldg(p.new_len + b), p.T) : p.T, room - len);
-      if (t < n) dst = paged_row(p.c, b, h, len + t);
+      if (t < n) dst = paged_row(p.c, b, h, len + t, p.B, p.status);
       if (t == 0 && h == 0 && j == 0) p.cache_len_out[b] = len + n;
     }
     const bool live = dst >= 0 && j < Gm::LANES && dbg_in_range(dst, 1, n_rows, p.status, 110);
@@ -206,7 +207,7 @@ __global__ void __launch_bounds__(kPagedThreads) attn_paged_read_kernel(const Pa
     for (int i = 0; i < N; ++i) {
       const int x = i * GROUPS + group;
       row[i] = static_cast<int>(j0) + x;
-      from[i] = group < GROUPS && row[i] < most ? paged_row(p.c, b, h, row[i]) : -1;  // (not waiting for n)
+      from[i] = group < GROUPS && row[i] < most ? paged_row(p.c, b, h, row[i], p.B, p.status) : -1;  // (not waiting for n)
       if (row[i] >= n) from[i] = -1;
       if (from[i] >= 0 && !(dbg_in_range(from[i], 1, n_rows, p.status, 111) && dbg_in_range(out0 + row[i], 1, n_out, p.status, 112))) from[i] = -1;
     }

@@ -137,12 +137,13 @@ __global__ void __launch_bounds__(kRopeThreads, RopeGeom<D, BWD>::PER_SM) rope_k
   grid_dependency_wait();  // the kernels before this one are complete
   if (threadIdx.x == 0) grid_launch_dependents();
   const int half = p.rot / 2;
-  // This thread's part of the sines: one pair, of every `abreast`-th token.
+  // This thread's part of the sines: one pair, of every `abreast`-th token.  What
+  // they need is on its way long before they are worked out.
   const int abreast = kRopeThreads / half, my_t = threadIdx.x / half, pair = threadIdx.x - my_t * half;
-  uint64_t my_frac = 0;
+  float my_freq = 0.f;
   const int32_t* my_pos = p.pos;
   if (my_t < abreast) {
-    my_frac = turn_fraction(__ldg(p.freq + pair));
+    my_freq = __ldg(p.freq + pair);
     int a = p.axis ? __ldg(p.axis + pair) : 0;
     a = a < p.axes ? a : p.axes - 1;
     my_pos += static_cast<long long>(a) * p.B * p.L;
@@ -173,10 +174,20 @@ __global__ void __launch_bounds__(kRopeThreads, RopeGeom<D, BWD>::PER_SM) rope_k
   const int t_end = static_cast<int>(static_cast<long long>(tokens) * (block + 1) / blocks);
   const int q_lo = p.x[0].H * part / parts, q_n = p.x[0].H * (part + 1) / parts - q_lo;  // heads of q and of k
   const int k_lo = p.x[1].H * part / parts, k_n = p.x[1].H * (part + 1) / parts - k_lo;
+  const int chunks = max(1, (t_end - t_first + Gm::TOKENS - 1) / Gm::TOKENS), each = (t_end - t_first + chunks - 1) / chunks;  // (equal ones)
 #pragma unroll 1
-  for (int t0 = t_first; t0 < t_end; t0 += Gm::TOKENS) {
-    const int n = min(t_end - t0, Gm::TOKENS);
+  for (int t0 = t_first; t0 < t_end; t0 += each) {
+    const int n = min(t_end - t0, each);
     if (t0 != t_first) __syncthreads();  // the tokens before are done with
+    constexpr int POS = (Gm::TOKENS + kRopeThreads / (D / 2) - 1) / (kRopeThreads / (D / 2));  // tokens of a thread, at most
+    int pos[POS];
+#pragma unroll
+    for (int i = 0; i < POS; ++i) {
+      const int t = my_t + i * abreast;
+      const bool in = my_t < abreast && t < n &&
+                      dbg_in_range(my_pos + t0 + t - p.pos, 1, static_cast<size_t>(p.axes) * tokens, p.status, 104);
+      pos[i] = in ? __ldg(my_pos + t0 + t) : 0;
+    }
     if (threadIdx.x < n) {
       const int token = t0 + threadIdx.x, b = token / p.L, l = token - b * p.L;
 #pragma unroll
@@ -226,12 +237,18 @@ __global__ void __launch_bounds__(kRopeThreads, RopeGeom<D, BWD>::PER_SM) rope_k
     };
 #pragma unroll
     for (int i = 0; i < DEPTH - 1; ++i) fetch();
-    if (my_t < abreast)  // (while the first rows are on their way)
-      for (int t = my_t; t < n; t += abreast) {
-        float c, s;
-        turn(__ldg(my_pos + t0 + t), my_frac, c, s);
-        cs[t * D + pair] = c, cs[t * D + D / 2 + pair] = BWD ? -s : s;
+    {  // (while the first rows are on their way)
+      const uint64_t my_frac = turn_fraction(my_freq);
+#pragma unroll
+      for (int i = 0; i < POS; ++i) {
+        const int t = my_t + i * abreast;
+        if (my_t < abreast && t < n) {
+          float c, s;
+          turn(pos[i], my_frac, c, s);
+          cs[t * D + pair] = c, cs[t * D + D / 2 + pair] = BWD ? -s : s;
+        }
       }
+    }
     __syncthreads();
     int round = 0;
 #pragma unroll 1

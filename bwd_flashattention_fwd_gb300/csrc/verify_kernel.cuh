@@ -107,6 +107,13 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) attn_draft_verify_kernel(co
   auto load = [&](int x, bool with_q, float (&a)[W], float (&q)[W]) {  // tokens x .. x + W - 1
 #pragma unroll
     for (int k = 0; k < W; ++k) q[k] = 0.f;
+    if constexpr (kDebugChecks) {
+#pragma unroll
+      for (int k = 0; k < W; ++k) a[k] = 0.f;
+      const size_t row = static_cast<size_t>(b) * p.T + n;
+      if (!dbg_in_range((row + b) * p.V + x, W, static_cast<size_t>(p.B) * (p.T + 1) * p.V, p.status, 130)) return;
+      if (with_q && !dbg_in_range(row * p.V + x, W, static_cast<size_t>(p.B) * p.T * p.V, p.status, 131)) return;
+    }
     if constexpr (VEC) {
       const float4 v = __ldg(reinterpret_cast<const float4*>(prow + x));
       a[0] = v.x, a[1] = v.y, a[2] = v.z, a[3] = v.w;
