@@ -74,11 +74,12 @@ struct PagedGeom {
 constexpr int kPagedExtra = 2;
 
 struct PagedPieces {
-  int total, n;  // units, pieces of them
-  __device__ __forceinline__ PagedPieces(int total_, int ctas) : total(total_), n(total_ < ctas ? total_ : ctas) {}
-  __device__ __forceinline__ int first(int c) const { return static_cast<int>(static_cast<long long>(total) * c / n); }  // unit of piece c
+  int n, each, more;  // pieces; units of each, and how many (the first ones) have one more
+  __device__ __forceinline__ PagedPieces(int total, int ctas) : n(total < ctas ? total : ctas), each(total / n), more(total - each * n) {}
+  __device__ __forceinline__ int first(int c) const { return c * each + min(c, more); }  // unit of piece c
   __device__ __forceinline__ int of(int u) const {  // the piece that unit u belongs to
-    return static_cast<int>((static_cast<long long>(u + 1) * n - 1) / total);
+    const int longer = more * (each + 1);
+    return u < longer ? u / (each + 1) : more + (u - longer) / each;
   }
 };
 

@@ -93,25 +93,23 @@ __global__ void __launch_bounds__(kPagedThreads) attn_paged_write_kernel(const P
   grid_dependency_wait();  // the kernels before this one are complete
   if (threadIdx.x == 0) grid_launch_dependents();
   const int lane = threadIdx.x & 31, j = lane % Gm::GROUP;
-  const long long rows = static_cast<long long>(p.B) * p.c.Hkv * p.T;
+  const uint32_t rows = static_cast<uint32_t>(p.B) * p.c.Hkv * p.T;  // below 2^31
   const int room = p.c.per_seq << p.c.shift;
-  const long long n_rows = (static_cast<long long>(p.c.n_pages) * p.c.Hkv) << p.c.shift;
-  const long long step = static_cast<long long>(gridDim.x) * (kPagedThreads / Gm::GROUP);
+  [[maybe_unused]] const long long n_rows = (static_cast<long long>(p.c.n_pages) * p.c.Hkv) << p.c.shift;
+  const uint32_t step = gridDim.x * (kPagedThreads / Gm::GROUP);
   // whole warps go round together: the shuffles below take every lane
-  const long long first = (static_cast<long long>(blockIdx.x) * kPagedThreads + (threadIdx.x & ~31)) / Gm::GROUP;
-  for (long long base = first; base < rows; base += step) {
-    const long long r = base + lane / Gm::GROUP;  // (b, h, t)
+  for (uint32_t base = (blockIdx.x * kPagedThreads + (threadIdx.x & ~31u)) / Gm::GROUP; base < rows; base += step) {
+    const uint32_t r = base + lane / Gm::GROUP;  // (b, h, t)
     const bool in = r < rows;
     uint4 x[2][2] = {};
     if (in && j < Gm::LANES) {
-      load32<WIDE>(static_cast<const uint4*>(p.k_new) + r * (D / 8) + 2 * j, x[0]);
-      load32<WIDE>(static_cast<const uint4*>(p.v_new) + r * (D / 8) + 2 * j, x[1]);
+      load32<WIDE>(static_cast<const uint4*>(p.k_new) + static_cast<size_t>(r) * (D / 8) + 2 * j, x[0]);
+      load32<WIDE>(static_cast<const uint4*>(p.v_new) + static_cast<size_t>(r) * (D / 8) + 2 * j, x[1]);
     }
     long long dst = -1;
     if (in) {
-      const long long bh = r / p.T;
-      const int t = static_cast<int>(r - bh * p.T), b = static_cast<int>(bh / p.c.Hkv);
-      const int h = static_cast<int>(bh - static_cast<long long>(b) * p.c.Hkv);
+      const uint32_t bh = p.T == 1 ? r : r / p.T;
+      const int t = r - bh * p.T, b = bh / p.c.Hkv, h = bh - b * p.c.Hkv;
       const int len = clamp_len(__ldg(p.cache_len + b), room);
       const int n = min(p.new_len ? clamp_len(__ldg(p.new_len + b), p.T) : p.T, room - len);
       if (t < n) dst = paged_row(p.c, b, h, len + t, p.B, p.status);

@@ -126,7 +126,7 @@ struct RopeGeom {
 };
 
 template <int D, bool BF16, bool INTERLEAVED, bool BWD>
-__global__ void __launch_bounds__(kRopeThreads, RopeGeom<D, BWD>::PER_SM) rope_kernel(const RopeParams p, int parts) {
+__global__ void __launch_bounds__(kRopeThreads, RopeGeom<D, BWD>::PER_SM) rope_kernel(const RopeParams p, int parts, int per, int more, int inv_half) {
   using Gm = RopeGeom<D, BWD>;
   using Ln = RowLanes<D>;
   constexpr int WARPS = kRopeThreads / 32, DEPTH = Gm::DEPTH;
@@ -139,7 +139,8 @@ __global__ void __launch_bounds__(kRopeThreads, RopeGeom<D, BWD>::PER_SM) rope_k
   const int half = p.rot / 2;
   // This thread's part of the sines: one pair, of every `abreast`-th token.  What
   // they need is on its way long before they are worked out.
-  const int abreast = kRopeThreads / half, my_t = threadIdx.x / half, pair = threadIdx.x - my_t * half;
+  // (Divisions cost a decode step as much as its loads: what the host can divide it passes, or passes as a factor of 2^-16.)
+  const int abreast = kRopeThreads * inv_half >> 16, my_t = static_cast<int>(threadIdx.x) * inv_half >> 16, pair = threadIdx.x - my_t * half;
   float my_freq = 0.f;
   const int32_t* my_pos = p.pos;
   if (my_t < abreast) {
@@ -169,9 +170,9 @@ __global__ void __launch_bounds__(kRopeThreads, RopeGeom<D, BWD>::PER_SM) rope_k
   const bool norm = p.w[0] != nullptr;
   const uint32_t ring = smem_u32(smem) + threadIdx.x * 16;  // piece k of slot s: + (s * PIECES + k) * kRopeThreads * 16
   const int tokens = p.B * p.L;  // (at most 2^30)
-  const int part = blockIdx.x % parts, block = blockIdx.x / parts, blocks = gridDim.x / parts;
-  const int t_first = static_cast<int>(static_cast<long long>(tokens) * block / blocks);
-  const int t_end = static_cast<int>(static_cast<long long>(tokens) * (block + 1) / blocks);
+  // blocks of `per` tokens, the first `more` of them one more
+  const int part = blockIdx.y, block = blockIdx.x;
+  const int t_first = block * per + min(block, more), t_end = t_first + per + (block < more ? 1 : 0);
   const int q_lo = p.x[0].H * part / parts, q_n = p.x[0].H * (part + 1) / parts - q_lo;  // heads of q and of k
   const int k_lo = p.x[1].H * part / parts, k_n = p.x[1].H * (part + 1) / parts - k_lo;
   const int chunks = max(1, (t_end - t_first + Gm::TOKENS - 1) / Gm::TOKENS), each = (t_end - t_first + chunks - 1) / chunks;  // (equal ones)
@@ -202,8 +203,9 @@ __global__ void __launch_bounds__(kRopeThreads, RopeGeom<D, BWD>::PER_SM) rope_k
     // Rows head by head, a round of GROUPS of them at a time (whole rounds of q, then of k): this group's row of round
     // r of q is row r * GROUPS + group of q_n * n.  (The shuffles take whole warps.)
     const int q_rounds = (q_n * n + Gm::GROUPS - 1) / Gm::GROUPS, k_rounds = (k_n * n + Gm::GROUPS - 1) / Gm::GROUPS;
-    const int step_h = Gm::GROUPS / n, step_t = Gm::GROUPS - step_h * n;
-    const int first_h = group / n, first_t = group - first_h * n;
+    const int inv_n = 65536 / n + 1;  // (exact for what is below 65536 / n)
+    const int step_h = Gm::GROUPS * inv_n >> 16, step_t = Gm::GROUPS - step_h * n;
+    const int first_h = group * inv_n >> 16, first_t = group - first_h * n;
     auto inside = [&](long long at, const RowsView& v, int site) {
       return dbg_in_range(at, D, (p.B - 1) * v.sb + (v.H - 1) * v.sh + (p.L - 1) * v.sl + D, p.status, site);
     };
@@ -370,7 +372,7 @@ __global__ void __launch_bounds__(kRopeThreads, RopeGeom<D, BWD>::PER_SM) rope_k
       float x = 0.f;
 #pragma unroll
       for (int k = 0; k < WARPS; ++k) x += dw_sum[(which * WARPS + k) * D + d];
-      p.part[static_cast<size_t>(blockIdx.x) * 2 * D + i] = x;
+      p.part[(static_cast<size_t>(blockIdx.y) * gridDim.x + blockIdx.x) * 2 * D + i] = x;
     }
   }
 }

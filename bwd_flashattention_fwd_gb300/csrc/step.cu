@@ -97,10 +97,11 @@ int rope_impl(const RopeParams& p, int num_sms, cudaStream_t stream) {
   // few tokens: their heads are shared out too, one round of the CTA's groups at least
   const int blocks = static_cast<int>(tokens < most ? tokens : most), heads = (p.x[0].H + Gm::GROUPS - 1) / Gm::GROUPS;
   const int parts = most / blocks < heads ? static_cast<int>(most / blocks) : heads, grid = blocks * parts;
+  const int per = static_cast<int>(tokens / blocks), more = static_cast<int>(tokens % blocks), half = p.rot / 2;
   const auto kern = rope_kernel<D, BF16, INTERLEAVED, BWD>;
   static std::atomic<uint64_t> done{0};
   if (!set_smem_limit(kern, Gm::SMEM, done)) return kLaunchCudaError;
-  const int r = launch_dependent(kern, dim3(grid), kRopeThreads, Gm::SMEM, stream, p, parts);
+  const int r = launch_dependent(kern, dim3(blocks, parts), kRopeThreads, Gm::SMEM, stream, p, parts, per, more, (65536 + half - 1) / half);
   if (r != kLaunchOk || !BWD || !p.w[0]) return r;
   return launch_dependent(rope_dw_kernel, dim3(2 * D / 32), 1024, 0, stream, p, grid);
 }
@@ -307,7 +308,8 @@ extern "C" attn_status_t attn_paged_write(const void* k_new, const void* v_new, 
     return ATTN_ERR_INVALID_ARG;
   const attn_status_t s = check_paged(k_pages, v_pages, k_exp, v_exp, table, B, Hkv, n_pages, page_size, per_seq, D, dtype);
   if (s != ATTN_OK) return s;
-  if (T > kPagedMaxTokens) return ATTN_ERR_UNSUPPORTED;
+  // rows are counted in 32 bits (a row has 128 bytes at least)
+  if (T > kPagedMaxTokens || static_cast<long long>(B) * Hkv * T > 0x7fffffffLL) return ATTN_ERR_UNSUPPORTED;
   const long long pool = pool_rows(Hkv, n_pages, page_size), ints = 4LL * B, fresh = 2LL * B * Hkv * T * D;
   const long long bytes = pool * D * (k_exp ? 1 : 2);
   const Span spans[] = {{cache_len_out, ints}, {k_pages, bytes}, {v_pages, bytes}, {k_exp, pool}, {v_exp, pool}, {k_new, fresh},
