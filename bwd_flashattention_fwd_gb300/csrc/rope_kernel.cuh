@@ -76,11 +76,10 @@ __device__ __forceinline__ void store16(uint16_t* row, int c0, int c1, const uin
 }
 
 // Turn the eight pairs of a lane's two pieces.  Halves: neighbours f[i] turn with
-// f[i + 4], c[i] and s[i] (i < 4) hold two pairs' cosines and sines, ns[i] = -s[i].
+// f[i + 4], c[i] and s[i] (i < 4) hold two pairs' cosines and sines.
 // Interleaved: f[i] is one pair, c[i] = (cos, cos), s[i] = (-sin, sin) (i < 8).
 template <bool INTERLEAVED>
-__device__ __forceinline__ void rotate16(uint64_t (&f)[8], const uint64_t (&c)[INTERLEAVED ? 8 : 4], const uint64_t (&s)[INTERLEAVED ? 8 : 4],
-                                         const uint64_t (&ns)[INTERLEAVED ? 1 : 4]) {
+__device__ __forceinline__ void rotate16(uint64_t (&f)[8], const uint64_t (&c)[INTERLEAVED ? 8 : 4], const uint64_t (&s)[INTERLEAVED ? 8 : 4]) {
   if constexpr (INTERLEAVED) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -92,7 +91,7 @@ __device__ __forceinline__ void rotate16(uint64_t (&f)[8], const uint64_t (&c)[I
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const uint64_t a = f[i], b = f[i + 4];
-      f[i] = f2_fma(a, c[i], f2_mul(b, ns[i]));
+      f[i] = f2_sub(f2_mul(a, c[i]), f2_mul(b, s[i]));
       f[i + 4] = f2_fma(b, c[i], f2_mul(a, s[i]));
     }
   }
@@ -106,7 +105,7 @@ __device__ __forceinline__ float f2_total(const uint64_t (&f)[2]) {
 
 // A CTA takes an equal share of the tokens (and, where there are fewer tokens
 // than CTAs, of the heads), up to TOKENS of them at a time: their sines and
-// cosines and the offsets of their rows go to shared memory, then their rows
+// cosines and the addresses of their rows go to shared memory, then their rows
 // (head by head, every token of each) go round the CTA's groups of lanes.  A
 // lane copies its pieces of the rows to come into a ring of its own (cp.async),
 // DEPTH rows ahead: that many bytes in flight are more than the registers
@@ -120,9 +119,9 @@ struct RopeGeom {
   static constexpr int PIECES = BWD ? 4 : 2;                    // 16-byte pieces of a row: x (and dy)
   static constexpr int RING = DEPTH * PIECES * kRopeThreads * 16;
   static constexpr int CS = TOKENS * D * 4;                     // [TOKENS][2][D / 2] floats
-  static constexpr int OFFSETS = TOKENS * 6 * 8;                // of x, y and dx, of q and k
+  static constexpr int ROWS_AT = TOKENS * 6 * 8;                // addresses in x, y and dx, of q and k
   static constexpr int SUMS = BWD ? 2 * kRopeThreads / 32 * D * 4 : 0;
-  static constexpr int SMEM = RING + CS + OFFSETS + SUMS;
+  static constexpr int SMEM = RING + CS + ROWS_AT + SUMS;
 };
 
 template <int D, bool BF16, bool INTERLEAVED, bool BWD>
@@ -132,8 +131,8 @@ __global__ void __launch_bounds__(kRopeThreads, RopeGeom<D, BWD>::PER_SM) rope_k
   constexpr int WARPS = kRopeThreads / 32, DEPTH = Gm::DEPTH;
   extern __shared__ __align__(128) uint8_t smem[];
   float* const cs = reinterpret_cast<float*>(smem + Gm::RING);                                  // [TOKENS][2][D / 2]
-  long long* const offsets = reinterpret_cast<long long*>(smem + Gm::RING + Gm::CS);            // [2][3][TOKENS]
-  float* const dw_sum = reinterpret_cast<float*>(smem + Gm::RING + Gm::CS + Gm::OFFSETS);       // [2][WARPS][D]
+  uint64_t* const rows_at = reinterpret_cast<uint64_t*>(smem + Gm::RING + Gm::CS);              // [2][3][TOKENS]
+  float* const dw_sum = reinterpret_cast<float*>(smem + Gm::RING + Gm::CS + Gm::ROWS_AT);       // [2][WARPS][D]
   grid_dependency_wait();  // the kernels before this one are complete
   if (threadIdx.x == 0) grid_launch_dependents();
   const int half = p.rot / 2;
@@ -164,9 +163,10 @@ __global__ void __launch_bounds__(kRopeThreads, RopeGeom<D, BWD>::PER_SM) rope_k
     c0 = j;
     c1 = j + turned;
   }
-  // the first of its pairs in each half of the eight; pairs that are not turned have cosine 1, sine 0
-  const int pair0 = INTERLEAVED ? 4 * c0 : 8 * j, pair1 = INTERLEAVED ? 4 * c1 : 8 * j + 4;
-  const bool turns0 = on && pair0 < half, turns1 = on && pair1 < half;
+  // Where the cosines (and, D / 2 floats on, sines) of its pairs lie in a token's part of cs, in fours: neighbouring
+  // lanes' fours side by side.  Pairs that are not turned have cosine 1 and sine 0.
+  const int four0 = 4 * (INTERLEAVED ? c0 : j), four1 = 4 * (INTERLEAVED ? c1 : D / 16 + j);
+  auto place = [](int pair) { return INTERLEAVED ? pair : ((pair >> 2 & 1) * (D / 16) + (pair >> 3)) * 4 + (pair & 3); };
   const bool norm = p.w[0] != nullptr;
   const uint32_t ring = smem_u32(smem) + threadIdx.x * 16;  // piece k of slot s: + (s * PIECES + k) * kRopeThreads * 16
   const int tokens = p.B * p.L;  // (at most 2^30)
@@ -175,6 +175,14 @@ __global__ void __launch_bounds__(kRopeThreads, RopeGeom<D, BWD>::PER_SM) rope_k
   const int t_first = block * per + min(block, more), t_end = t_first + per + (block < more ? 1 : 0);
   const int q_lo = p.x[0].H * part / parts, q_n = p.x[0].H * (part + 1) / parts - q_lo;  // heads of q and of k
   const int k_lo = p.x[1].H * part / parts, k_n = p.x[1].H * (part + 1) / parts - k_lo;
+  if (p.rot < D)
+    for (int i = threadIdx.x; i < Gm::TOKENS * (D / 2); i += kRopeThreads) {
+      const int ti = i / (D / 2), pi = i - ti * (D / 2);
+      if (pi >= half) cs[ti * D + place(pi)] = 1.f, cs[ti * D + D / 2 + place(pi)] = 0.f;
+    }
+  // bytes between heads
+  const uint32_t x_head[2] = {static_cast<uint32_t>(p.x[0].sh * 2), static_cast<uint32_t>(p.x[1].sh * 2)};
+  const uint32_t d_head[2] = {static_cast<uint32_t>(p.dx[0].sh * 2), static_cast<uint32_t>(p.dx[1].sh * 2)}, y_head = p.L * (D * 2);
   const int chunks = max(1, (t_end - t_first + Gm::TOKENS - 1) / Gm::TOKENS), each = (t_end - t_first + chunks - 1) / chunks;  // (equal ones)
 #pragma unroll 1
   for (int t0 = t_first; t0 < t_end; t0 += each) {
@@ -193,10 +201,12 @@ __global__ void __launch_bounds__(kRopeThreads, RopeGeom<D, BWD>::PER_SM) rope_k
       const int token = t0 + threadIdx.x, b = token / p.L, l = token - b * p.L;
 #pragma unroll
       for (int which = 0; which < 2; ++which) {
-        long long* const at = offsets + which * 3 * Gm::TOKENS + threadIdx.x;
-        at[0] = b * p.x[which].sb + l * p.x[which].sl;
-        at[Gm::TOKENS] = (static_cast<long long>(b) * p.x[which].H * p.L + l) * D;
-        if (BWD) at[2 * Gm::TOKENS] = b * p.dx[which].sb + l * p.dx[which].sl;
+        uint64_t* const at = rows_at + which * 3 * Gm::TOKENS + threadIdx.x;
+        const int lo = which ? k_lo : q_lo;
+        const RowsView &xv = p.x[which], &dv = p.dx[which];
+        at[0] = reinterpret_cast<uint64_t>(static_cast<uint16_t*>(xv.at) + (b * xv.sb + l * xv.sl + lo * xv.sh));
+        at[Gm::TOKENS] = reinterpret_cast<uint64_t>(static_cast<uint16_t*>(p.y[which]) + ((static_cast<long long>(b) * xv.H + lo) * p.L + l) * D);
+        if (BWD) at[2 * Gm::TOKENS] = reinterpret_cast<uint64_t>(static_cast<uint16_t*>(dv.at) + (b * dv.sb + l * dv.sl + lo * dv.sh));
       }
     }
     __syncthreads();
@@ -206,28 +216,28 @@ __global__ void __launch_bounds__(kRopeThreads, RopeGeom<D, BWD>::PER_SM) rope_k
     const int inv_n = 65536 / n + 1;  // (exact for what is below 65536 / n)
     const int step_h = Gm::GROUPS * inv_n >> 16, step_t = Gm::GROUPS - step_h * n;
     const int first_h = group * inv_n >> 16, first_t = group - first_h * n;
-    auto inside = [&](long long at, const RowsView& v, int site) {
-      return dbg_in_range(at, D, (p.B - 1) * v.sb + (v.H - 1) * v.sh + (p.L - 1) * v.sl + D, p.status, site);
+    auto inside = [&](uint64_t at, const RowsView& v, int site) {
+      return dbg_in_range((at - reinterpret_cast<uint64_t>(v.at)) / 2, D, (p.B - 1) * v.sb + (v.H - 1) * v.sh + (p.L - 1) * v.sl + D, p.status, site);
     };
-    auto inside_y = [&](long long at, int which, int site) {
-      return dbg_in_range(at, D, static_cast<size_t>(p.B) * p.x[which].H * p.L * D, p.status, site);
+    auto inside_y = [&](uint64_t at, int which, int site) {
+      return dbg_in_range((at - reinterpret_cast<uint64_t>(p.y[which])) / 2, D, static_cast<size_t>(p.B) * p.x[which].H * p.L * D, p.status, site);
     };
     int ahead = 0, ahead_h = first_h, ahead_t = first_t;  // the round that is fetched next, and its row
     auto fetch = [&]() {
       const bool is_k = ahead >= q_rounds;
       if (on && ahead < q_rounds + k_rounds && ahead_h < (is_k ? k_n : q_n)) {
         const uint32_t slot = ring + (ahead % DEPTH) * (Gm::PIECES * kRopeThreads * 16);
-        const int which = is_k ? 1 : 0, h = (is_k ? k_lo : q_lo) + ahead_h;
-        const long long* const at = offsets + which * 3 * Gm::TOKENS + ahead_t;
-        const long long xo = at[0] + h * (is_k ? p.x[1].sh : p.x[0].sh);
+        const int which = is_k ? 1 : 0;
+        const uint64_t* const at = rows_at + which * 3 * Gm::TOKENS + ahead_t;
+        const uint64_t xo = at[0] + static_cast<uint64_t>(static_cast<uint32_t>(ahead_h)) * (is_k ? x_head[1] : x_head[0]);
         if ((!BWD || norm) && inside(xo, p.x[which], 100)) {
-          const uint4* v = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(is_k ? p.x[1].at : p.x[0].at) + xo);
+          const uint4* v = reinterpret_cast<const uint4*>(xo);
           cp_async16(slot, v + c0, true), cp_async16(slot + kRopeThreads * 16, v + c1, true);
         }
         if constexpr (BWD) {
-          const long long yo = at[Gm::TOKENS] + static_cast<long long>(h) * p.L * D;
+          const uint64_t yo = at[Gm::TOKENS] + static_cast<uint64_t>(static_cast<uint32_t>(ahead_h)) * y_head;
           if (inside_y(yo, which, 101)) {
-            const uint4* v = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(is_k ? p.y[1] : p.y[0]) + yo);
+            const uint4* v = reinterpret_cast<const uint4*>(yo);
             cp_async16(slot + 2 * kRopeThreads * 16, v + c0, true), cp_async16(slot + 3 * kRopeThreads * 16, v + c1, true);
           }
         }
@@ -241,13 +251,14 @@ __global__ void __launch_bounds__(kRopeThreads, RopeGeom<D, BWD>::PER_SM) rope_k
     for (int i = 0; i < DEPTH - 1; ++i) fetch();
     {  // (while the first rows are on their way)
       const uint64_t my_frac = turn_fraction(my_freq);
+      const int at = place(pair);
 #pragma unroll
       for (int i = 0; i < POS; ++i) {
         const int t = my_t + i * abreast;
         if (my_t < abreast && t < n) {
           float c, s;
           turn(pos[i], my_frac, c, s);
-          cs[t * D + pair] = c, cs[t * D + D / 2 + pair] = BWD ? -s : s;
+          cs[t * D + at] = c, cs[t * D + D / 2 + at] = BWD ? -s : s;
         }
       }
     }
@@ -255,10 +266,8 @@ __global__ void __launch_bounds__(kRopeThreads, RopeGeom<D, BWD>::PER_SM) rope_k
     int round = 0;
 #pragma unroll 1
     for (int which = 0; which < 2; ++which) {
-      const int rounds = which ? k_rounds : q_rounds, h_n = which ? k_n : q_n, h_lo = which ? k_lo : q_lo;
-      const RowsView dv = p.dx[which];
-      uint16_t* const y = static_cast<uint16_t*>(p.y[which]);
-      const long long* const at = offsets + which * 3 * Gm::TOKENS;
+      const int rounds = which ? k_rounds : q_rounds, h_n = which ? k_n : q_n;
+      const uint64_t* const at = rows_at + which * 3 * Gm::TOKENS;
       uint64_t w[8], dw[BWD ? 8 : 1];
       {
         uint4 wp[2] = {};
@@ -279,21 +288,17 @@ __global__ void __launch_bounds__(kRopeThreads, RopeGeom<D, BWD>::PER_SM) rope_k
         const uint32_t slot = ring + (round % DEPTH) * (Gm::PIECES * kRopeThreads * 16);
         // this token's cosines and sines, as rotate16 takes them
         constexpr int NC = INTERLEAVED ? 8 : 4;
-        uint64_t c[NC], s[NC], ns[INTERLEAVED ? 1 : 4];
+        uint64_t c[NC], s[NC];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          float4 cv = make_float4(1.f, 1.f, 1.f, 1.f), sv = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (k ? turns1 : turns0) {
-            cv = *reinterpret_cast<const float4*>(cs + t * D + (k ? pair1 : pair0));
-            sv = *reinterpret_cast<const float4*>(cs + t * D + D / 2 + (k ? pair1 : pair0));
-          }
+          const float4 cv = *reinterpret_cast<const float4*>(cs + t * D + (k ? four1 : four0));
+          const float4 sv = *reinterpret_cast<const float4*>(cs + t * D + D / 2 + (k ? four1 : four0));
           if constexpr (INTERLEAVED) {
             c[4 * k] = f2_pack(cv.x, cv.x), c[4 * k + 1] = f2_pack(cv.y, cv.y), c[4 * k + 2] = f2_pack(cv.z, cv.z), c[4 * k + 3] = f2_pack(cv.w, cv.w);
             s[4 * k] = f2_pack(-sv.x, sv.x), s[4 * k + 1] = f2_pack(-sv.y, sv.y), s[4 * k + 2] = f2_pack(-sv.z, sv.z), s[4 * k + 3] = f2_pack(-sv.w, sv.w);
           } else {
             c[2 * k] = f2_pack(cv.x, cv.y), c[2 * k + 1] = f2_pack(cv.z, cv.w);
             s[2 * k] = f2_pack(sv.x, sv.y), s[2 * k + 1] = f2_pack(sv.z, sv.w);
-            ns[2 * k] = f2_pack(-sv.x, -sv.y), ns[2 * k + 1] = f2_pack(-sv.z, -sv.w);
           }
         }
         uint64_t f[8];
@@ -309,15 +314,15 @@ __global__ void __launch_bounds__(kRopeThreads, RopeGeom<D, BWD>::PER_SM) rope_k
 #pragma unroll
             for (int e = 0; e < 8; ++e) f[e] = f2_mul(f2_mul(f[e], rr), w[e]);
           }
-          rotate16<INTERLEAVED>(f, c, s, ns);
+          rotate16<INTERLEAVED>(f, c, s);
           if (live) {
-            const long long yo = at[Gm::TOKENS + t] + static_cast<long long>(h_lo + h) * p.L * D;
-            if (inside_y(yo, which, 102)) store16<BF16>(y + yo, c0, c1, f);
+            const uint64_t yo = at[Gm::TOKENS + t] + static_cast<uint64_t>(static_cast<uint32_t>(h)) * y_head;
+            if (inside_y(yo, which, 102)) store16<BF16>(reinterpret_cast<uint16_t*>(yo), c0, c1, f);
           }
         } else {
           const uint4 gp[2] = {ld_shared_v4(slot + 2 * kRopeThreads * 16), ld_shared_v4(slot + 3 * kRopeThreads * 16)};
           unpack16<BF16>(gp, f);
-          rotate16<INTERLEAVED>(f, c, s, ns);
+          rotate16<INTERLEAVED>(f, c, s);
           if (norm) {
             const uint4 xp[2] = {ld_shared_v4(slot), ld_shared_v4(slot + kRopeThreads * 16)};
             uint64_t x[8], ss[2] = {0, 0}, gx[2] = {0, 0};
@@ -339,8 +344,8 @@ __global__ void __launch_bounds__(kRopeThreads, RopeGeom<D, BWD>::PER_SM) rope_k
             }
           }
           if (live) {
-            const long long dxo = at[2 * Gm::TOKENS + t] + (h_lo + h) * dv.sh;
-            if (inside(dxo, dv, 103)) store16<BF16>(static_cast<uint16_t*>(dv.at) + dxo, c0, c1, f);
+            const uint64_t dxo = at[2 * Gm::TOKENS + t] + static_cast<uint64_t>(static_cast<uint32_t>(h)) * (which ? d_head[1] : d_head[0]);
+            if (inside(dxo, p.dx[which], 103)) store16<BF16>(reinterpret_cast<uint16_t*>(dxo), c0, c1, f);
           }
         }
         h += step_h, t += step_t;

@@ -20,7 +20,8 @@ attn_status_t check_strides(const int64_t* st, int B, int H, int L) {
   for (int i = 0; i < 3; ++i) {
     if (size[i] == 1) continue;
     if (st[i] < 0 || st[i] % 8 != 0) return ATTN_ERR_INVALID_ARG;
-    if (st[i] > (int64_t{1} << 40)) return ATTN_ERR_UNSUPPORTED;
+    // (bytes between heads are counted in 32 bits)
+    if (st[i] > (int64_t{1} << 40) || (i == 1 && st[i] > 0x7fffffffLL)) return ATTN_ERR_UNSUPPORTED;
   }
   return ATTN_OK;
 }
@@ -79,7 +80,8 @@ attn_status_t check_rope(const void* q, const void* k, const void* qw, const voi
   if (dtype != ATTN_DTYPE_FP16 && dtype != ATTN_DTYPE_BF16) return ATTN_ERR_INVALID_ARG;
   if (!supported_d(D) || rot % 16 != 0 || axes > kRopeMaxAxes) return ATTN_ERR_UNSUPPORTED;
   // units of work and rows are counted in 32 bits beside a token's number
-  if (static_cast<long long>(B) * L > (1 << 30) || Hq > 65535 || Hkv > 65535) return ATTN_ERR_UNSUPPORTED;
+  if (static_cast<long long>(B) * L > (1 << 30) || Hq > 65535 || Hkv > 65535 || static_cast<long long>(L) * D > 0x7fffffffLL)
+    return ATTN_ERR_UNSUPPORTED;
   const attn_status_t a = check_strides(qs, B, Hq, L), b = check_strides(ks, B, Hkv, L);
   return a != ATTN_OK ? a : b;
 }

@@ -353,7 +353,8 @@ attn_status_t attn_cache_evict(void* k, void* v, const float* weight, const int3
  *   freq float32 [rot/2]: radians per position, finite and below 2^22.
  *   q_out, k_out: outputs (dtype), contiguous [B,H,L,D].  q_out may be q (and
  *     k_out k) where q is contiguous; no other overlap (ATTN_ERR_INVALID_ARG).
- *   rot: 16 .. D, a multiple of 16; axes 1 .. 8; B * L <= 2^30 (else ATTN_ERR_UNSUPPORTED).
+ *   rot: 16 .. D, a multiple of 16; axes 1 .. 8; B * L <= 2^30; L * D and the
+ *   strides between heads below 2^31 (else ATTN_ERR_UNSUPPORTED).
  *
  * attn_qk_norm_rope_bwd: the gradients.  dq_out, dk_out (dtype, contiguous:
  *   what attn_bwd wrote) are those of the outputs above, dq and dk (dtype, at

@@ -118,12 +118,12 @@ def test_rope_rejects(lib, call):
     for kw in (dict(B=0), dict(Hq=0), dict(Hkv=0), dict(L=0), dict(rot=0), dict(rot=136), dict(axes=0), dict(eps=-1.0), dict(eps=math.nan),
                dict(eps=math.inf), dict(inter=2), dict(dtype=5)):
         assert call(lib, **kw) == INV, kw
-    for kw in (dict(D=80, rot=16), dict(rot=24), dict(rot=8), dict(axes=9), dict(B=1 << 16, L=1 << 16), dict(Hq=70000)):
+    for kw in (dict(D=80, rot=16), dict(rot=24), dict(rot=8), dict(axes=9), dict(B=1 << 16, L=1 << 16), dict(B=1, L=1 << 24), dict(Hq=70000)):
         assert call(lib, **kw) == UNS, kw
     for name in ("qs", "ks"):
         assert call(lib, **{name: st(16384, 2048, 124)}) == INV  # rows not 16 bytes apart
         assert call(lib, **{name: st(16384, -2048, 128)}) == INV
-        assert call(lib, **{name: st(1 << 41, 2048, 128)}) == UNS
+        assert call(lib, **{name: st(1 << 41, 2048, 128)}) == UNS and call(lib, **{name: st(1 << 40, 1 << 31, 128)}) == UNS
 
 
 def test_rope_refuses_shared_storage(lib):
