@@ -158,6 +158,9 @@ __device__ __forceinline__ uint32_t cluster_map(uint32_t local_addr, uint32_t ra
 __device__ __forceinline__ void cluster_sync_all() {
   asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
+// Its two halves, for work between them that needs no other CTA.
+__device__ __forceinline__ void cluster_arrive_all() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait_all() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 // Bulk copy of `bytes` from this CTA's shared memory to another CTA's
 // (cluster address), completing on that CTA's mbarrier `cluster_bar`; one
 // elected lane of the calling warp issues it.  Both addresses 16-byte

@@ -128,25 +128,26 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) attn_draft_verify_kernel(co
   };
   auto sum_of = [&](int from, int to, bool with_q, int without) {  // this lane's share of a part
     uint64_t sum = 0;
-    int x = from + lane * W;
     constexpr int N = VEC ? 4 : 8;  // steps whose loads are in flight together
-    for (; x + (N - 1) * STEP < to; x += N * STEP) {
+    for (int x0 = from; x0 < to; x0 += N * STEP) {
+      const int x = x0 + lane * W;
       float a[N][W], q[N][W];
+      if (x0 + N * STEP <= to) {
 #pragma unroll
-      for (int i = 0; i < N; ++i) load(x + i * STEP, with_q, a[i], q[i]);
+        for (int i = 0; i < N; ++i) load(x + i * STEP, with_q, a[i], q[i]);
+      } else {  // the last ones: together too
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+#pragma unroll
+          for (int k = 0; k < W; ++k) a[i][k] = q[i][k] = 0.f;
+          if (x + i * STEP < to) load(x + i * STEP, with_q, a[i], q[i]);
+        }
+      }
       FixedSum s;
 #pragma unroll
       for (int i = 0; i < N; ++i)
 #pragma unroll
         for (int k = 0; k < W; ++k) s.add(a[i][k], q[i][k]);
-      sum += s.value();
-    }
-    for (; x < to; x += STEP) {
-      float a[W], q[W];
-      load(x, with_q, a, q);
-      FixedSum s;
-#pragma unroll
-      for (int k = 0; k < W; ++k) s.add(a[k], q[k]);
       sum += s.value();
     }
     if (lane == 0 && without >= from && without < to) {  // a deterministic draft's token has no weight
@@ -160,31 +161,27 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) attn_draft_verify_kernel(co
   const int mine = c * WARPS + warp;
   bool with_q = qrow != nullptr;
   int without = point;
-  uint64_t sum = warp_sum(sum_of(bound(mine), bound(mine + 1), with_q, without));
-  if (lane == 0) part[0][warp] = sum;
-  cluster_sync_all();
-  const uint32_t at = smem_u32(&part[0][0]);
-  // every warp: all parts' sums (a few a lane), their total and what lies before its own
-  auto totals = [&](int which, uint64_t& total, uint64_t& before) {
+  uint64_t sum, total, before;  // of this warp's part, of all, of what lies before the part
+  auto add_up = [&](int which) {
+    sum = warp_sum(sum_of(bound(mine), bound(mine + 1), with_q, without));
+    if (lane == 0) part[which][warp] = sum;
+    cluster_sync_all();
     total = before = 0;
 #pragma unroll
-    for (int i = 0; i < kVerifyCluster * WARPS / 32; ++i) {
+    for (int i = 0; i < kVerifyCluster * WARPS / 32; ++i) {  // all warps' sums, a few a lane
       const int w = i * 32 + lane;
-      const uint64_t v = ld_cluster_u64(cluster_map(at + (which * WARPS + w % WARPS) * 8, w / WARPS));
+      const uint64_t v = ld_cluster_u64(cluster_map(smem_u32(&part[which][w % WARPS]), w / WARPS));
       total += v;
       if (w < mine) before += v;
     }
     total = warp_sum(total), before = warp_sum(before);
   };
-  uint64_t total, before;
-  totals(0, total, before);
+  add_up(0);
   if (total == 0 && rejected) {  // nothing is left (the same for the whole cluster): p itself
     with_q = false, without = -1;
-    sum = warp_sum(sum_of(bound(mine), bound(mine + 1), false, -1));
-    if (lane == 0) part[1][warp] = sum;
-    cluster_sync_all();
-    totals(1, total, before);
+    add_up(1);
   }
+  cluster_arrive_all();  // (this CTA has read the others' sums)
   // r as a multiple of 2^-64 (a float below 1 has 24 bits, so this is exact from 2^-40 up)
   uint64_t rf = 0;
   if (r >= 1.f) {
@@ -250,7 +247,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) attn_draft_verify_kernel(co
       if (run > limit) break;
     }
   }
-  cluster_sync_all();  // no CTA leaves while others read its sums
+  cluster_wait_all();  // no CTA leaves while others read its sums
 }
 
 }  // namespace gbattn
