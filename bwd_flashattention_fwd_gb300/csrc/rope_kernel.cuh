@@ -115,7 +115,7 @@ struct RopeGeom {
   static constexpr int GROUPS = kRopeThreads / RowLanes<D>::GROUP;
   static constexpr int PER_SM = BWD ? kRopeBwdPerSm : kRopeFwdPerSm;
   static constexpr int TOKENS = 4096 / D;                       // 16 KB of sines and cosines
-  static constexpr int DEPTH = 4;
+  static constexpr int DEPTH = BWD ? 3 : 4;  // (gradient, 8192 tokens: 46.4 us, with 4 47.7, with 5 48.4; video prompt 30.9, with 3 31.1, with 6 31.1)
   static constexpr int PIECES = BWD ? 4 : 2;                    // 16-byte pieces of a row: x (and dy)
   static constexpr int RING = DEPTH * PIECES * kRopeThreads * 16;
   static constexpr int CS = TOKENS * D * 4;                     // [TOKENS][2][D / 2] floats
@@ -382,21 +382,23 @@ __global__ void __launch_bounds__(kRopeThreads, RopeGeom<D, BWD>::PER_SM) rope_k
   }
 }
 
-// dw = the CTAs' partial sums, in a fixed order: a block per 32 columns, a warp per 32nd of the CTAs.
+// dw = the CTAs' partial sums, in a fixed order: a block per 8 columns, 128 threads for each.
 __global__ void __launch_bounds__(1024) rope_dw_kernel(const RopeParams p, int n) {
-  __shared__ float sum[32][32];
+  __shared__ float sum[128][9];
   grid_dependency_wait();
-  const int lane = threadIdx.x & 31, col = blockIdx.x * 32 + lane, warp = threadIdx.x >> 5;
+  const int c = threadIdx.x & 7, row = threadIdx.x >> 3, col = blockIdx.x * 8 + c;
   float x = 0.f;
-#pragma unroll 10
-  for (int i = warp; i < n; i += 32) x += p.part[static_cast<size_t>(i) * 2 * p.D + col];
-  sum[warp][lane] = x;
+#pragma unroll 4
+  for (int i = row; i < n; i += 128) x += p.part[static_cast<size_t>(i) * 2 * p.D + col];
+  sum[row][c] = x;
   __syncthreads();
-  if (warp == 0) {
+  if (threadIdx.x < 256) {  // a warp per column
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    float y = (sum[lane][w] + sum[lane + 32][w]) + (sum[lane + 64][w] + sum[lane + 96][w]);
 #pragma unroll
-    for (int w = 1; w < 32; ++w) x += sum[w][lane];
-    const int which = col / p.D;
-    p.dw[which][col - which * p.D] = x;
+    for (int m = 16; m; m >>= 1) y += __shfl_xor_sync(0xffffffffu, y, m);
+    const int at = blockIdx.x * 8 + w, which = at / p.D;
+    if (lane == 0) p.dw[which][at - which * p.D] = y;
   }
 }
 

@@ -105,7 +105,7 @@ int rope_impl(const RopeParams& p, int num_sms, cudaStream_t stream) {
   if (!set_smem_limit(kern, Gm::SMEM, done)) return kLaunchCudaError;
   const int r = launch_dependent(kern, dim3(blocks, parts), kRopeThreads, Gm::SMEM, stream, p, parts, per, more, (65536 + half - 1) / half);
   if (r != kLaunchOk || !BWD || !p.w[0]) return r;
-  return launch_dependent(rope_dw_kernel, dim3(2 * D / 32), 1024, 0, stream, p, grid);
+  return launch_dependent(rope_dw_kernel, dim3(2 * D / 8), 1024, 0, stream, p, grid);
 }
 
 template <int D, bool BF16>
