@@ -15,17 +15,18 @@ namespace GBATTN_CAT(paged_d, GBATTN_HEAD_DIM) {
 constexpr int kD = GBATTN_HEAD_DIM;
 
 // A cluster of CTAs per head, in one launch, or equal pieces and a second one.
-// A cluster saves the join (b4 x 8 heads, 8000 keys, D = 128: 26.2 us, 28.8 by
-// pieces; 1000 keys of one sequence 5.4 and 6.7), but its CTAs get what their
-// head has: a CTA alone takes kPagedAlone % of the time per step that it takes
-// when all share the bandwidth at half the room's length, so it pays where the
-// clusters fill enough of the GPU for the steps each has (one sequence: 2000
-// keys 6.8 and 7.1, 4000 keys 9.5 and 8.6; 16 quantised sequences of 500 to 4000 keys 26.3
-// and 25.2, 1000 to 8192 43.5 and 35.7).  Past kPagedShort steps a single long
-// sequence among short ones would be waited for too long.
+// A cluster saves the join, but its CTAs get what their head has.  A step alone
+// takes kPagedAlone us; where clusters fill the GPU, their steps take what the
+// memory gives (6.6 TB/s), with rooms half full on average half as long.  A
+// cluster is taken where the longest possible sequence would so be late by
+// kPagedLate us at most (32 heads of 8192 keys 25.4 us, by pieces 28.8; 1000 keys
+// of one sequence 5.0 and 6.7, 4000 keys 9.5 and 8.6; D = 64, 128 heads of 250 to
+// 2000 keys 14.4 and 13.3, of 125 to 1000 7.8 and 8.2; 1024 to 8192 keys quantised 43.5 and 35.7).
+// Past kPagedShort steps a single long sequence among short ones would be waited for too long.
 constexpr int kPagedShort = 32;
+constexpr float kPagedLate = 4.f;
 template <bool Q8>
-constexpr float kPagedAlone = Q8 ? 120.f : 93.f;
+constexpr float kPagedAlone = Q8 ? 0.9f : 0.7f;
 
 template <typename... Params, typename... Args>
 int launch_cluster(void (*kern)(Params...), unsigned grid, int size, int threads, size_t smem, cudaStream_t stream, Args... args) {
@@ -63,7 +64,8 @@ int impl(const PagedAttnParams& p0, int num_sms, cudaStream_t stream) {
   int size = 1;
   while (size < kPagedCluster && 2 * size * all <= p.n_groups && size < steps) size *= 2;
   const long long per = (steps + size - 1) / size;
-  if (per <= kPagedShort && per * (kPagedAlone<Q8> - 100.f * size * all / p.n_groups) <= 400.f) {
+  const float half_full = static_cast<float>(size * all) * Gm::KS * Gm::ROWB / 6.6e6f;  // us of a step
+  if (per <= kPagedShort && per * (kPagedAlone<Q8> - half_full) <= kPagedLate) {
     auto kern = attn_paged_cluster_kernel<kD, BF16, Q8, NT>;
     static std::atomic<uint64_t> done{0};
     if (!set_smem_limit(kern, Gm::SMEM, done)) return kLaunchCudaError;
