@@ -18,7 +18,7 @@
 // column of lanes and its B fragment along a row: movmatrix turns one into the
 // other without shared memory.
 //
-// Every warp works on tiles of its own (16 or 32 keys) out of a ring of its
+// Every warp works on tiles of its own (16 keys) out of a ring of its
 // own that cp.async fills, so the loop has no CTA barrier; row pitches are an odd
 // number of 16-byte pieces, so ldmatrix meets no bank twice.  Pages only change
 // the address of a row: a lane looks a key's page up one tile ahead.
@@ -436,7 +436,8 @@ __device__ __forceinline__ void paged_part(const PagedAttnParams& p, const Paged
         if constexpr (Q8) {
           const int8_t* ex = reinterpret_cast<const int8_t*>(smem) + (tile - smem_u32(smem)) + 2 * KT * Gm::PITCH;
           fk = exp2_int(ex[at]);
-          ev[mb][k] = static_cast<float>(ex[KT + at]);
+          // (a row that is not there may hold any exponent: 2^128 times its weight 0 would not be 0)
+          ev[mb][k] = there >> at & 1u ? static_cast<float>(ex[KT + at]) : 0.f;
         }
 #pragma unroll
         for (int i = 0; i < NT; ++i)

@@ -472,8 +472,8 @@ def check_paged(q, pool, table, page, lens, scale, got):
     within(lse[~inf], lref[~inf], 1.45 * (2 * d + n * X + 2.0 ** -21) + 2 * X * np.abs(lref[~inf]), "lse")
 
 
-def stale(pool, table, page, lens):
-    """Rows that hold no token filled with what must not matter: NaN and infinities (NaN codes, large exponents)."""
+def stale(pool, table, page, lens, exponent=120):
+    """Rows that hold no token filled with what must not matter: NaN and infinities (NaN codes, extreme exponents)."""
     k, v, ke, ve = pool
     live = torch.zeros(k.shape[0], page, dtype=torch.bool)
     for b in range(len(lens)):
@@ -487,7 +487,7 @@ def stale(pool, table, page, lens):
     else:
         for t, e in ((k, ke), (v, ve)):
             t.view(torch.uint8).masked_fill_(dead, 0x7F)
-            e.masked_fill_(dead[..., 0], 120)
+            e.masked_fill_(dead[..., 0], exponent)
 
 
 @pytest.mark.parametrize("q8", [False, True])
@@ -503,6 +503,22 @@ def test_paged_attention(case, q8):
     got = run_paged(q, pool, table.cuda(), i32(lens), scale)
     ok()
     check_paged(q, pool, table, page, lens, scale, got)
+
+
+@pytest.mark.parametrize("D", [64, 96, 128, 256])
+@pytest.mark.parametrize("exponent", [-128, -127, 127])
+def test_paged_attention_any_exponent_in_unused_rows(D, exponent):
+    """Rows behind the last token, in the same four whose exponents are fetched together: any byte may stand there."""
+    gen = torch.Generator().manual_seed(26)
+    B, Hq, Hkv, page, per_seq = 4, 4, 2, 16, 3
+    pool = make_pool(gen, B * per_seq, Hkv, page, D, BF, True)
+    table = torch.randperm(B * per_seq, generator=gen).view(B, per_seq).to(torch.int32)
+    lens = [1, 18, 35, 45]
+    stale(pool, table, page, lens, exponent)
+    q = rand(gen, (B, Hq, 1, D), BF)
+    got = run_paged(q, pool, table.cuda(), i32(lens), 0.1)
+    ok()
+    check_paged(q, pool, table, page, lens, 0.1, got)
 
 
 @pytest.mark.parametrize("q8", [False, True])
