@@ -34,7 +34,15 @@
 //
 // fp16 P: times 2^15, so that what counts as nothing is 2^-40 of the row's
 // largest (2^-25 otherwise, and 10^5 such keys add up).
+//
+// Past a few rows, or with codes to widen, the instructions of a tile bound it (64
+// to 55% of the issue slots): scores and sums in packed pairs, masks only in tiles that need
+// one, the rows' references moved only by scores well above them, offsets of copies in the
+// instructions: 32 rows over 4 sequences of 65536 quantised keys 150 us (166 without), D = 64 105 (120).
 #pragma once
+
+#include <cfloat>
+#include <utility>
 
 #include "paged_kernel.cuh"
 
@@ -189,6 +197,16 @@ __device__ __forceinline__ uint2 q_fragment(const uint16_t* qrow, int kk, int t,
   }
 }
 
+// 16 bytes each from src, src + SRC, ..., whose offsets go into the instructions.
+template <int DST, int SRC>
+__device__ __forceinline__ void cp_async16_at(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0 + %2], [%1 + %3], 16;" ::"r"(dst), "l"(src), "n"(DST), "n"(SRC) : "memory");
+}
+template <int DST, int SRC, int... I>
+__device__ __forceinline__ void cp_async16_rows(uint32_t dst, const void* src, std::integer_sequence<int, I...>) {
+  (..., cp_async16_at<I * DST, I * SRC>(dst, src));
+}
+
 // What the warps of a CTA share besides the ring.
 template <int NW, int ST, int ROWS>
 struct PagedShared {
@@ -205,7 +223,8 @@ __device__ __forceinline__ void paged_part(const PagedAttnParams& p, const Paged
   using Gm = PagedGeom<D, Q8, NT>;
   constexpr int NW = Gm::NW, KT = Gm::KT, ST = Gm::ST, MB = KT / 16, ROWS = 8 * NT, KK = D / 16;
   constexpr bool MMA_BF16 = BF16 && !Q8;          // type of the products' operands
-  constexpr float kPShift = MMA_BF16 ? 0.f : 15.f;  // P is kept times 2^kPShift
+  constexpr float kPShift = MMA_BF16 ? 0.f : 15.f;  // P is kept times 2^kPShift,
+  constexpr float kPMost = kPShift + 0.9f;          // and no larger than 2^kPMost (fp16 ends at 2^16)
   constexpr bool Q_REGS = KK * NT * 2 <= 32;
   auto& q_exp = sh.q_exp;
   auto& key_mask = sh.key_mask;
@@ -246,11 +265,17 @@ __device__ __forceinline__ void paged_part(const PagedAttnParams& p, const Paged
     if constexpr (32 % Gm::CH == 0) {
       constexpr int RPI = 32 / Gm::CH;  // rows per instruction: whole ones, all in one eight
       const int row = lane / Gm::CH, c = lane % Gm::CH;
-      const uint32_t in = there_next >> row;
 #pragma unroll
-      for (int i = 0; i < KT / RPI; ++i)
-        cp_async16(dst + (i * RPI + row) * Gm::PITCH + c * 16,
-                   base + (src[i * RPI / 8] + (i * RPI % 8 + row)) * Gm::ROWB + c * 16, in >> (i * RPI) & 1u);
+      for (int e = 0; e < KT / 8; ++e) {
+        const uint32_t to = dst + (e * 8 + row) * Gm::PITCH + c * 16;
+        const uint8_t* from = base + src[e] * Gm::ROWB + (row * Gm::ROWB + c * 16);
+        if (there_next == 0xffffffffu) {
+          cp_async16_rows<RPI * Gm::PITCH, RPI * Gm::ROWB>(to, from, std::make_integer_sequence<int, 8 / RPI>());
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; j += RPI) cp_async16(to + j * Gm::PITCH, from + j * Gm::ROWB, there_next >> (e * 8 + j + row) & 1u);
+        }
+      }
     } else {
 #pragma unroll
       for (int i = 0; i < KT * Gm::CH / 32; ++i) {
@@ -340,22 +365,23 @@ __device__ __forceinline__ void paged_part(const PagedAttnParams& p, const Paged
 #pragma unroll
     for (int i = 0; i < KK * NT; ++i) qr[i] = qf[i * 32 + lane];
   }
-  float mul[NT][2];  // of the scores of rows 2 t4, 2 t4 + 1
+  uint64_t mul[NT];  // of the scores of rows 2 t4, 2 t4 + 1
   int lim[NT][2];    // and how many keys they see
 #pragma unroll
-  for (int i = 0; i < NT; ++i)
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int r = i * 8 + 2 * t4 + k;
-      mul[i][k] = p.scale_log2 * (Q8 ? exp2_int(-static_cast<int>(q_exp[r])) : 1.f);
-      lim[i][k] = n - p.T + 1 + (row0 + r) % p.T;
-    }
+  for (int i = 0; i < NT; ++i) {
+    const int r = i * 8 + 2 * t4;
+    mul[i] = Q8 ? f2_pack(p.scale_log2 * exp2_int(-static_cast<int>(q_exp[r])), p.scale_log2 * exp2_int(-static_cast<int>(q_exp[r + 1])))
+                : f2_pack(p.scale_log2, p.scale_log2);
+    lim[i][0] = n - p.T + 1 + (row0 + r) % p.T, lim[i][1] = n - p.T + 1 + (row0 + r + 1) % p.T;
+  }
 
   // ---- the keys ----
-  float acc[KK][NT][4], m[NT][2], l[NT][2];
+  // (m: a row's reference, 2^kPShift below a score that was its largest; see below)
+  float acc[KK][NT][4];
+  uint64_t m[NT], l[NT];
 #pragma unroll
   for (int i = 0; i < NT; ++i) {
-    m[i][0] = m[i][1] = -INFINITY, l[i][0] = l[i][1] = 0.f;
+    m[i] = f2_pack(-FLT_MAX, -FLT_MAX), l[i] = 0;
 #pragma unroll
     for (int d = 0; d < KK; ++d) acc[d][i][0] = acc[d][i][1] = acc[d][i][2] = acc[d][i][3] = 0.f;
   }
@@ -420,58 +446,72 @@ __device__ __forceinline__ void paged_part(const PagedAttnParams& p, const Paged
         for (int x = 0; x < 4; ++x) sc[0][0][x] += sc2[1][0][0][x];
       }
     }
-    // scores, masked, and their running maxima
-    float ev[MB][2];  // exponents of this lane's keys' values
-    const bool edge = there != 0xffffffffu || key0 + KT > n - p.T + 1;
-    float top[NT][2];
-#pragma unroll
-    for (int i = 0; i < NT; ++i) top[i][0] = m[i][0], top[i][1] = m[i][1];
+    // scores, masked
+    int ev[MB][2];  // exponents of this lane's keys' values
 #pragma unroll
     for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
       for (int k = 0; k < 2; ++k) {  // key mb * 16 + g + 8 k
-        const int at = mb * 16 + g + 8 * k;
-        float fk = 1.f;
-        ev[mb][k] = 0.f;
+        uint64_t fk = 0, fe = 0;
         if constexpr (Q8) {
-          const int8_t* ex = reinterpret_cast<const int8_t*>(smem) + (tile - smem_u32(smem)) + 2 * KT * Gm::PITCH;
-          fk = exp2_int(ex[at]);
-          // (a row that is not there may hold any exponent: 2^128 times its weight 0 would not be 0)
-          ev[mb][k] = there >> at & 1u ? static_cast<float>(ex[KT + at]) : 0.f;
+          const int8_t* ex = reinterpret_cast<const int8_t*>(smem) + (tile - smem_u32(smem)) + 2 * KT * Gm::PITCH + mb * 16 + g + 8 * k;
+          ev[mb][k] = ex[KT];
+          const float f = exp2_int(ex[0]), e = static_cast<float>(ev[mb][k]);
+          fk = f2_pack(f, f), fe = f2_pack(e, e);
         }
 #pragma unroll
-        for (int i = 0; i < NT; ++i)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float x = sc[mb][i][2 * k + e] * mul[i][e];
-            if constexpr (Q8) x = fmaf(x, fk, ev[mb][k]);
-            if (edge && (!(there >> at & 1u) || key0 + at >= lim[i][e])) x = -INFINITY;
-            sc[mb][i][2 * k + e] = x;
-            top[i][e] = fmaxf(top[i][e], x);
-          }
+        for (int i = 0; i < NT; ++i) {
+          uint64_t x = f2_mul(f2_pack(sc[mb][i][2 * k], sc[mb][i][2 * k + 1]), mul[i]);
+          if constexpr (Q8) x = f2_fma(x, fk, fe);
+          f2_unpack(x, sc[mb][i][2 * k], sc[mb][i][2 * k + 1]);
+        }
       }
-    bool same = true;
-    float fix[NT][2];
+    if (there != 0xffffffffu || key0 + KT > n - p.T + 1) {
 #pragma unroll
-    for (int i = 0; i < NT; ++i)
+      for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
+        for (int k = 0; k < 2; ++k) {
+          const int at = mb * 16 + g + 8 * k;
+          const bool in = there >> at & 1u;
+          if (!in) ev[mb][k] = 0;  // (such a row may hold any exponent: 2^128 times its weight 0 would not be 0)
 #pragma unroll
-        for (int x = 4; x < 32; x <<= 1) top[i][e] = fmaxf(top[i][e], __shfl_xor_sync(0xffffffffu, top[i][e], x));
-        const float ref = top[i][e] == -INFINITY ? 0.f : top[i][e];
-        fix[i][e] = ex2_approx(m[i][e] - ref);
-        same = same && top[i][e] == m[i][e];
-        m[i][e] = top[i][e];
-        top[i][e] = ref - kPShift;
-      }
-    if (!__all_sync(0xffffffffu, same)) {
+          for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              if (!in || key0 + at >= lim[i][e]) sc[mb][i][2 * k + e] = -INFINITY;
+        }
+    }
+    // The rows' references.  A score may be 0.9 above the one that set its row's before it moves, which
+    // saves the lanes' common maximum and the sums' rescaling in nearly every tile.
+    bool up = false;
+    float top[NT][2];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      top[i][0] = sc[0][i][0], top[i][1] = sc[0][i][1];
+#pragma unroll
+      for (int x = 2; x < 4 * MB; ++x) top[i][x & 1] = fmaxf(top[i][x & 1], sc[x / 4][i][x & 3]);
+      float b0, b1;
+      f2_unpack(f2_add(m[i], f2_pack(kPMost, kPMost)), b0, b1);
+      up = up || top[i][0] > b0 || top[i][1] > b1;
+    }
+    if (__any_sync(0xffffffffu, up)) {
 #pragma unroll
       for (int i = 0; i < NT; ++i) {
-        l[i][0] *= fix[i][0], l[i][1] *= fix[i][1];
+        float old[2], fix[2];
+        f2_unpack(m[i], old[0], old[1]);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+#pragma unroll
+          for (int x = 4; x < 32; x <<= 1) top[i][e] = fmaxf(top[i][e], __shfl_xor_sync(0xffffffffu, top[i][e], x));
+          top[i][e] = top[i][e] > old[e] + kPMost ? top[i][e] - kPShift : old[e];  // (no row's result depends on another's scores)
+          fix[e] = ex2_approx(old[e] - top[i][e]);
+        }
+        m[i] = f2_pack(top[i][0], top[i][1]);
+        l[i] = f2_mul(l[i], f2_pack(fix[0], fix[1]));
 #pragma unroll
         for (int d = 0; d < KK; ++d) {
-          acc[d][i][0] *= fix[i][0], acc[d][i][1] *= fix[i][1];
-          acc[d][i][2] *= fix[i][0], acc[d][i][3] *= fix[i][1];
+          acc[d][i][0] *= fix[0], acc[d][i][1] *= fix[1];
+          acc[d][i][2] *= fix[0], acc[d][i][3] *= fix[1];
         }
       }
     }
@@ -488,9 +528,15 @@ __device__ __forceinline__ void paged_part(const PagedAttnParams& p, const Paged
       for (int i = 0; i < NT; ++i)
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          const float p0 = ex2_approx(sc[mb][i][2 * k] - top[i][0]), p1 = ex2_approx(sc[mb][i][2 * k + 1] - top[i][1]);
-          const float w = Q8 ? exp2_int(-static_cast<int>(ev[mb][k])) : 1.f;
-          l[i][0] = fmaf(p0, w, l[i][0]), l[i][1] = fmaf(p1, w, l[i][1]);
+          float p0, p1;
+          f2_unpack(f2_sub(f2_pack(sc[mb][i][2 * k], sc[mb][i][2 * k + 1]), m[i]), p0, p1);
+          p0 = ex2_approx(p0), p1 = ex2_approx(p1);
+          if constexpr (Q8) {
+            const float w = exp2_int(-ev[mb][k]);
+            l[i] = f2_fma(f2_pack(p0, p1), f2_pack(w, w), l[i]);
+          } else {
+            l[i] = f2_add(l[i], f2_pack(p0, p1));
+          }
           b[i][k] = mat_trans(Elem<MMA_BF16>::pack(p0, p1));
         }
       const uint32_t vt = tile + (KT + mb * 16) * Gm::PITCH;
@@ -528,13 +574,16 @@ __device__ __forceinline__ void paged_part(const PagedAttnParams& p, const Paged
 
   // ---- the warps' results ----
 #pragma unroll
-  for (int i = 0; i < NT; ++i)
+  for (int i = 0; i < NT; ++i) {
+    float mi[2], li[2];
+    f2_unpack(m[i], mi[0], mi[1]);
+    f2_unpack(l[i], li[0], li[1]);
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
 #pragma unroll
-      for (int x = 4; x < 32; x <<= 1) l[i][e] += __shfl_xor_sync(0xffffffffu, l[i][e], x);
+      for (int x = 4; x < 32; x <<= 1) li[e] += __shfl_xor_sync(0xffffffffu, li[e], x);
       const int r = i * 8 + 2 * t4 + e;
-      if (g == 0) ml[warp][r][0] = m[i][e], ml[warp][r][1] = l[i][e];
+      if (g == 0) ml[warp][r][0] = mi[e], ml[warp][r][1] = li[e];
       float* dst = join + (warp * ROWS + r) * Gm::JOIN_PITCH;
 #pragma unroll
       for (int d = 0; d < KK; ++d) {
@@ -546,6 +595,7 @@ __device__ __forceinline__ void paged_part(const PagedAttnParams& p, const Paged
         }
       }
     }
+  }
   __syncthreads();
 }
 
@@ -556,12 +606,11 @@ __device__ __forceinline__ float4 paged_join_warps(const float* join, const Shar
   mx = sh.ml[0][r][0];
 #pragma unroll
   for (int w = 1; w < Gm::NW; ++w) mx = fmaxf(mx, sh.ml[w][r][0]);
-  const float ref = mx == -INFINITY ? 0.f : mx;
   lsum = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
   for (int w = 0; w < Gm::NW; ++w) {
-    const float f = ex2_approx(sh.ml[w][r][0] - ref);
+    const float f = ex2_approx(sh.ml[w][r][0] - mx);
     const float4 a = *reinterpret_cast<const float4*>(join + (w * Gm::ROWS + r) * Gm::JOIN_PITCH + 4 * c);
     lsum = fmaf(sh.ml[w][r][1], f, lsum);
     o.x = fmaf(a.x, f, o.x), o.y = fmaf(a.y, f, o.y), o.z = fmaf(a.z, f, o.z), o.w = fmaf(a.w, f, o.w);
@@ -569,13 +618,13 @@ __device__ __forceinline__ float4 paged_join_warps(const float* join, const Shar
   return o;
 }
 
-// A finished row's column quad (and, with the first, its lse): mx and lsum its maximum and sum, P times 2^shift.
+// A finished row's column quad (and, with the first, its lse): mx and lsum its reference and sum (0: it saw no key).
 template <int D, bool BF16>
-__device__ __forceinline__ void paged_store(const PagedAttnParams& p, size_t row, int c, const float4& o, float mx, float lsum, float shift) {
-  const float by = mx == -INFINITY ? 0.f : 1.f / lsum;
+__device__ __forceinline__ void paged_store(const PagedAttnParams& p, size_t row, int c, const float4& o, float mx, float lsum) {
+  const float by = lsum == 0.f ? 0.f : 1.f / lsum;
   if (!dbg_in_range(row, 1, static_cast<size_t>(p.B) * p.Hq * p.T, p.status, 122)) return;
   reinterpret_cast<uint2*>(p.o)[row * (D / 4) + c] = make_uint2(Elem<BF16>::pack(o.x * by, o.y * by), Elem<BF16>::pack(o.z * by, o.w * by));
-  if (c == 0) p.lse[row] = mx == -INFINITY ? INFINITY : mx - shift + log2f(lsum);
+  if (c == 0) p.lse[row] = lsum == 0.f ? INFINITY : mx + log2f(lsum);
 }
 
 // A piece of the work per CTA; heads that several pieces share leave partial results.
@@ -583,7 +632,6 @@ template <int D, bool BF16, bool Q8, int NT>
 __global__ void __launch_bounds__(PagedGeom<D, Q8, NT>::THREADS, PagedGeom<D, Q8, NT>::PER_SM) attn_paged_kernel(const PagedAttnParams p) {
   using Gm = PagedGeom<D, Q8, NT>;
   constexpr int ROWS = 8 * NT;
-  constexpr float kPShift = BF16 && !Q8 ? 0.f : 15.f;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ PagedShared<Gm::NW, Gm::ST, ROWS> sh;
   const float* join = reinterpret_cast<const float*>(smem);
@@ -612,7 +660,7 @@ __global__ void __launch_bounds__(PagedGeom<D, Q8, NT>::THREADS, PagedGeom<D, Q8
       float mx, lsum;
       const float4 o = paged_join_warps<D, Q8, NT>(join, sh, r, c, mx, lsum);
       if (whole) {
-        paged_store<D, BF16>(p, out0 + r, c, o, mx, lsum, kPShift);
+        paged_store<D, BF16>(p, out0 + r, c, o, mx, lsum);
       } else if (dbg_in_range(part0 + r, 1, static_cast<size_t>(p.n_groups) * 2 * ROWS, p.status, 123)) {
         reinterpret_cast<float4*>(p.part)[(part0 + r) * (D / 4) + c] = o;
         if (c == 0) reinterpret_cast<float2*>(p.part_ml)[part0 + r] = make_float2(mx, lsum);
@@ -627,7 +675,6 @@ template <int D, bool BF16, bool Q8, int NT>
 __global__ void __launch_bounds__(PagedGeom<D, Q8, NT>::THREADS, PagedGeom<D, Q8, NT>::PER_SM) attn_paged_cluster_kernel(const PagedAttnParams p, int size) {
   using Gm = PagedGeom<D, Q8, NT>;
   constexpr int ROWS = 8 * NT;
-  constexpr float kPShift = BF16 && !Q8 ? 0.f : 15.f;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ PagedShared<Gm::NW, Gm::ST, ROWS> sh;
   __shared__ float2 stat[ROWS];  // the CTA's maxima and sums
@@ -647,7 +694,7 @@ __global__ void __launch_bounds__(PagedGeom<D, Q8, NT>::THREADS, PagedGeom<D, Q8
     float mx, lsum;
     const float4 o = paged_join_warps<D, Q8, NT>(join, sh, r, c, mx, lsum);
     if (size == 1) {
-      paged_store<D, BF16>(p, out0 + r, c, o, mx, lsum, kPShift);
+      paged_store<D, BF16>(p, out0 + r, c, o, mx, lsum);
     } else {  // over the first warp's, which no other thread reads here
       *reinterpret_cast<float4*>(join + r * Gm::JOIN_PITCH + 4 * c) = o;
       if (c == 0) stat[r] = make_float2(mx, lsum);
@@ -666,16 +713,15 @@ __global__ void __launch_bounds__(PagedGeom<D, Q8, NT>::THREADS, PagedGeom<D, Q8
       ml[k] = k < size ? ld_cluster_f2(cluster_map(stat_at + r * 8, k)) : make_float2(-INFINITY, 0.f);
       mx = fmaxf(mx, ml[k].x);
     }
-    const float ref = mx == -INFINITY ? 0.f : mx;
 #pragma unroll
     for (int k = 0; k < kPagedCluster; ++k) {
       if (k >= size) continue;
-      const float f = ex2_approx(ml[k].x - ref);
+      const float f = ex2_approx(ml[k].x - mx);
       const float4 a = ld_cluster_f4(cluster_map(join_at + (r * Gm::JOIN_PITCH + 4 * c) * 4, k));
       lsum = fmaf(ml[k].y, f, lsum);
       o.x = fmaf(a.x, f, o.x), o.y = fmaf(a.y, f, o.y), o.z = fmaf(a.z, f, o.z), o.w = fmaf(a.w, f, o.w);
     }
-    paged_store<D, BF16>(p, out0 + r, c, o, mx, lsum, kPShift);
+    paged_store<D, BF16>(p, out0 + r, c, o, mx, lsum);
   }
   cluster_sync_all();  // no CTA leaves while others read its results
 }
@@ -688,7 +734,6 @@ template <int D, bool BF16, bool Q8, int NT, int WARPS>
 __global__ void __launch_bounds__(kPagedJoinThreads) attn_paged_join_kernel(const PagedAttnParams p) {
   using Gm = PagedGeom<D, Q8, NT>;
   constexpr int ROWS = 8 * NT, QUADS = D / 4, Q = (QUADS + 31) / 32;  // column quads, and a lane's
-  constexpr float kPShift = BF16 && !Q8 ? 0.f : 15.f;
   __shared__ int starts[kPagedMaxB + 1];
   __shared__ float4 sum[WARPS > 1 ? WARPS : 1][QUADS];
   __shared__ float2 stat[WARPS];
@@ -737,7 +782,7 @@ __global__ void __launch_bounds__(kPagedJoinThreads) attn_paged_join_kernel(cons
 #pragma unroll
       for (int x = 16; x; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
       top = fmaxf(top, mx);
-      const float ref = top == -INFINITY ? 0.f : top, w = ex2_approx(ml.x - ref), fix = ex2_approx(mx - ref);
+      const float w = ex2_approx(ml.x - top), fix = ex2_approx(mx - top);
       float add = ml.y * w;
 #pragma unroll
       for (int x = 16; x; x >>= 1) add += __shfl_xor_sync(0xffffffffu, add, x);
@@ -778,13 +823,12 @@ __global__ void __launch_bounds__(kPagedJoinThreads) attn_paged_join_kernel(cons
       float top = mx;
 #pragma unroll
       for (int w = 1; w < WARPS; ++w) top = fmaxf(top, stat[w].x);
-      const float ref = top == -INFINITY ? 0.f : top;
       l = 0.f;
 #pragma unroll
       for (int x = 0; x < Q; ++x) o[x] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < WARPS; ++w) {
-        const float f = ex2_approx(stat[w].x - ref);
+        const float f = ex2_approx(stat[w].x - top);
         l = fmaf(stat[w].y, f, l);
 #pragma unroll
         for (int x = 0; x < Q; ++x) {
@@ -795,14 +839,14 @@ __global__ void __launch_bounds__(kPagedJoinThreads) attn_paged_join_kernel(cons
       }
       mx = top;
     }
-    const float by = mx == -INFINITY ? 0.f : 1.f / l;
+    const float by = l == 0.f ? 0.f : 1.f / l;
     if (dbg_in_range(task, 1, static_cast<size_t>(tasks), p.status, 124)) {
 #pragma unroll
       for (int x = 0; x < Q; ++x)
         if (QUADS % 32 == 0 || x * 32 + lane < QUADS)
           reinterpret_cast<uint2*>(p.o)[static_cast<size_t>(task) * QUADS + x * 32 + lane] =
               make_uint2(Elem<BF16>::pack(o[x].x * by, o[x].y * by), Elem<BF16>::pack(o[x].z * by, o[x].w * by));
-      if (lane == 0) p.lse[task] = mx == -INFINITY ? INFINITY : mx - kPShift + log2f(l);
+      if (lane == 0) p.lse[task] = l == 0.f ? INFINITY : mx + log2f(l);
     }
   }
   // (a grid that ended before the one ahead of it would let the next one in early)

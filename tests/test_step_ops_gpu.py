@@ -522,6 +522,53 @@ def test_paged_attention_any_exponent_in_unused_rows(D, exponent):
 
 
 @pytest.mark.parametrize("q8", [False, True])
+@pytest.mark.parametrize("dt", [BF, HF])
+@pytest.mark.parametrize("rise", [0.01, 0.05, 0.056, 0.12, 0.9, 3.0])
+def test_paged_attention_rising_scores(rise, dt, q8):
+    """Scores that rise (and fall, for every other query head) by a little from key to key: the largest is always new."""
+    gen = torch.Generator().manual_seed(27)
+    D, Hkv, G, page, n = 128, 1, 8, 16, 500
+    pool = make_pool(gen, 32, Hkv, page, D, dt, q8)
+    table = torch.randperm(32, generator=gen).view(1, 32).to(torch.int32)
+    k = pool[0]
+    j = torch.empty(32, page)
+    j[table[0].long()] = torch.arange(32 * page, dtype=torch.float32).view(32, page)
+    full = torch.zeros(32, Hkv, page, D)
+    full[:, 0, :, 0], full[:, 0, :, 1] = torch.floor(j / 16), j / 16 % 1  # exact as codes but for wholes above 16
+    k.copy_(full.to(k.dtype))
+    if q8:
+        pool[2].zero_()
+    q = torch.zeros(1, G, 1, D)
+    for g in range(G):
+        q[0, g, 0, :2] = (g + 1) * (1 if g % 2 == 0 else -1)
+    q = q.to(dt).cuda()
+    got = run_paged(q, pool, table.cuda(), i32([n]), 16 * rise)
+    ok()
+    check_paged(q, pool, table, page, [n], 16 * rise, got)
+
+
+@pytest.mark.parametrize("q8", [False, True])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("n", [40, 3000, 11000])
+def test_paged_attention_nan_query(D, q8, n):
+    """A row of Q with a NaN has a NaN result and a NaN lse, not those of a row that sees no key; its neighbours' stand."""
+    gen = torch.Generator().manual_seed(28)
+    page, per_seq = 16, 700
+    pool = make_pool(gen, 2 * per_seq, 2, page, D, BF, q8)
+    table = torch.randperm(2 * per_seq, generator=gen).view(2, per_seq).to(torch.int32)
+    q = rand(gen, (2, 4, 1, D), BF)
+    ref = run_paged(q, pool, table.cuda(), i32([n, 17]), 0.1)
+    bad = q.clone()
+    bad[0, 1, 0, 3] = float("nan")
+    o, lse = run_paged(bad, pool, table.cuda(), i32([n, 17]), 0.1)
+    ok()
+    assert o[0, 1].isnan().all() and lse[0, 1].isnan().all()
+    keep = torch.ones(2, 4, dtype=torch.bool)
+    keep[0, 1] = False
+    assert torch.equal(o[keep.cuda()], ref[0][keep.cuda()]) and torch.equal(lse[keep.cuda()], ref[1][keep.cuda()])
+
+
+@pytest.mark.parametrize("q8", [False, True])
 @pytest.mark.parametrize("D", [64, 128, 256])
 def test_paged_attention_holes_and_lengths_out_of_range(D, q8):
     gen = torch.Generator().manual_seed(14)
