@@ -20,7 +20,7 @@ namespace gbattn {
 // Row number (of D values) of token `at` of sequence b and head h in the pool, or -1 where its page is none.
 __device__ __forceinline__ long long paged_row(const PagedCache& c, int b, int h, int at, [[maybe_unused]] int B, [[maybe_unused]] int* status) {
   if (!dbg_in_range(static_cast<size_t>(b) * c.per_seq + (at >> c.shift), 1, static_cast<size_t>(B) * c.per_seq, status, 113)) return -1;
-  const int page = __ldg(c.table + static_cast<size_t>(b) * c.per_seq + (at >> c.shift));
+  const int page = c.table[static_cast<size_t>(b) * c.per_seq + (at >> c.shift)];
   if (page < 0 || page >= c.n_pages) return -1;
   return ((static_cast<long long>(page) * c.Hkv + h) << c.shift) + (at & ((1 << c.shift) - 1));
 }
@@ -110,8 +110,8 @@ __global__ void __launch_bounds__(kPagedThreads) attn_paged_write_kernel(const P
     if (in) {
       const uint32_t bh = p.T == 1 ? r : r / p.T;
       const int t = r - bh * p.T, b = bh / p.c.Hkv, h = bh - b * p.c.Hkv;
-      const int len = clamp_len(__ldg(p.cache_len + b), room);
-      const int n = min(p.new_len ? clamp_len(__ldg(p.new_len + b), p.T) : p.T, room - len);
+      const int len = clamp_len(p.cache_len[b], room);
+      const int n = min(p.new_len ? clamp_len(p.new_len[b], p.T) : p.T, room - len);
       if (t < n) dst = paged_row(p.c, b, h, len + t, p.B, p.status);
       if (t == 0 && h == 0 && j == 0) p.cache_len_out[b] = len + n;
     }

@@ -143,8 +143,8 @@ __global__ void __launch_bounds__(kRopeThreads, RopeGeom<D, BWD>::PER_SM) rope_k
   float my_freq = 0.f;
   const int32_t* my_pos = p.pos;
   if (my_t < abreast) {
-    my_freq = __ldg(p.freq + pair);
-    int a = p.axis ? __ldg(p.axis + pair) : 0;
+    my_freq = p.freq[pair];
+    int a = p.axis ? p.axis[pair] : 0;
     a = a < p.axes ? a : p.axes - 1;
     my_pos += static_cast<long long>(a) * p.B * p.L;
   }
@@ -195,7 +195,7 @@ __global__ void __launch_bounds__(kRopeThreads, RopeGeom<D, BWD>::PER_SM) rope_k
       const int t = my_t + i * abreast;
       const bool in = my_t < abreast && t < n &&
                       dbg_in_range(my_pos + t0 + t - p.pos, 1, static_cast<size_t>(p.axes) * tokens, p.status, 104);
-      pos[i] = in ? __ldg(my_pos + t0 + t) : 0;
+      pos[i] = in ? my_pos[t0 + t] : 0;
     }
     if (threadIdx.x < n) {
       const int token = t0 + threadIdx.x, b = token / p.L, l = token - b * p.L;
@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(kRopeThreads, RopeGeom<D, BWD>::PER_SM) rope_k
         uint4 wp[2] = {};
         if (norm && on) {
           const uint4* v = static_cast<const uint4*>(p.w[which]);
-          wp[0] = __ldg(v + c0), wp[1] = __ldg(v + c1);
+          wp[0] = v[c0], wp[1] = v[c1];
         }
         unpack16<BF16>(wp, w);
       }

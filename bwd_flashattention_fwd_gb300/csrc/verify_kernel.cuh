@@ -115,15 +115,15 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) attn_draft_verify_kernel(co
       if (with_q && !dbg_in_range(row * p.V + x, W, static_cast<size_t>(p.B) * p.T * p.V, p.status, 131)) return;
     }
     if constexpr (VEC) {
-      const float4 v = __ldg(reinterpret_cast<const float4*>(prow + x));
+      const float4 v = *reinterpret_cast<const float4*>(prow + x);
       a[0] = v.x, a[1] = v.y, a[2] = v.z, a[3] = v.w;
       if (with_q) {
-        const float4 w = __ldg(reinterpret_cast<const float4*>(qrow + x));
+        const float4 w = *reinterpret_cast<const float4*>(qrow + x);
         q[0] = w.x, q[1] = w.y, q[2] = w.z, q[3] = w.w;
       }
     } else {
-      a[0] = __ldg(prow + x);
-      if (with_q) q[0] = __ldg(qrow + x);
+      a[0] = prow[x];
+      if (with_q) q[0] = qrow[x];
     }
   };
   auto sum_of = [&](int from, int to, bool with_q, int without) {  // this lane's share of a part
@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) attn_draft_verify_kernel(co
     }
     if (lane == 0 && without >= from && without < to) {  // a deterministic draft's token has no weight
       FixedSum s;
-      s.add(__ldg(prow + without), 0.f);
+      s.add(prow[without], 0.f);
       sum -= s.value();
     }
     return sum;
