@@ -19,12 +19,12 @@ constexpr int kD = GBATTN_HEAD_DIM;
 // takes kPagedAlone us; where clusters fill the GPU, their steps take what the
 // memory gives (6.6 TB/s), with rooms half full on average half as long.  A
 // cluster is taken where the longest possible sequence would so be late by
-// kPagedLate us at most (32 heads of 8192 keys 25.4 us, by pieces 28.8; 1000 keys
-// of one sequence 5.0 and 6.7, 4000 keys 9.5 and 8.6; D = 64, 128 heads of 250 to
-// 2000 keys 14.4 and 13.3, of 125 to 1000 7.8 and 8.2; 1024 to 8192 keys quantised 43.5 and 35.7).
+// kPagedLate us at most (32 heads of 8192 keys 25.8 us, by pieces 27.3, quantised 16.3 and 19.0; 1000 keys
+// of one sequence 5.5 and 6.2, 4000 keys 8.7 and 8.3; D = 64, 128 heads of 250 to
+// 2000 keys 13.3 and 13.1, of 125 to 1000 7.5 and 8.3; 1024 to 8192 keys quantised 38.0 and 31.6).
 // Past kPagedShort steps a single long sequence among short ones would be waited for too long.
 constexpr int kPagedShort = 32;
-constexpr float kPagedLate = 4.f;
+constexpr float kPagedLate = 3.f;
 template <bool Q8>
 constexpr float kPagedAlone = Q8 ? 0.9f : 0.7f;
 
