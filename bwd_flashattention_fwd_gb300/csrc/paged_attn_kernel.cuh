@@ -50,7 +50,7 @@ namespace gbattn {
 
 // Warps: as many as hide the latency of a tile's chain (look-up, copy, products,
 // exponentials), which registers limit: 8 rows over quantised pages take 126
-// registers, 16 warps on an SM (8192 keys, 4 sequences: 18.2 us; 8 warps of 32-key tiles 21.7).
+// registers, 16 warps on an SM (8192 keys, 4 sequences: 16.3 us; 8 warps of 32-key tiles 3.5 more).
 template <int D, bool Q8, int NT>
 struct PagedGeom {
   static constexpr int NW = D == 256 && !Q8 ? 2 : Q8 && D * NT <= 128 ? 8 : 4;  // warps of a CTA
