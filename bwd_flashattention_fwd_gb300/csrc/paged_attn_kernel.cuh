@@ -490,9 +490,9 @@ __device__ __forceinline__ void paged_part(const PagedAttnParams& p, const Paged
       top[i][0] = sc[0][i][0], top[i][1] = sc[0][i][1];
 #pragma unroll
       for (int x = 2; x < 4 * MB; ++x) top[i][x & 1] = fmaxf(top[i][x & 1], sc[x / 4][i][x & 3]);
-      float b0, b1;
-      f2_unpack(f2_add(m[i], f2_pack(kPMost, kPMost)), b0, b1);
-      up = up || top[i][0] > b0 || top[i][1] > b1;
+      float d0, d1;  // (the difference that P is the power of, not a rounded bound on the score: P may not pass 2^kPMost)
+      f2_unpack(f2_sub(f2_pack(top[i][0], top[i][1]), m[i]), d0, d1);
+      up = up || d0 > kPMost || d1 > kPMost;
     }
     if (__any_sync(0xffffffffu, up)) {
 #pragma unroll
@@ -503,7 +503,8 @@ __device__ __forceinline__ void paged_part(const PagedAttnParams& p, const Paged
         for (int e = 0; e < 2; ++e) {
 #pragma unroll
           for (int x = 4; x < 32; x <<= 1) top[i][e] = fmaxf(top[i][e], __shfl_xor_sync(0xffffffffu, top[i][e], x));
-          top[i][e] = top[i][e] > old[e] + kPMost ? top[i][e] - kPShift : old[e];  // (no row's result depends on another's scores)
+          // (no row's result depends on another's scores; upwards, so that large scores too give at most 2^kPShift)
+          top[i][e] = top[i][e] - old[e] > kPMost ? __fadd_ru(top[i][e], -kPShift) : old[e];
           fix[e] = ex2_approx(old[e] - top[i][e]);
         }
         m[i] = f2_pack(top[i][0], top[i][1]);

@@ -548,6 +548,28 @@ def test_paged_attention_rising_scores(rise, dt, q8):
 
 
 @pytest.mark.parametrize("q8", [False, True])
+@pytest.mark.parametrize("dt", [BF, HF])
+@pytest.mark.parametrize("log2_scale", [0, 8, 14, 17, 18, 19, 20, 21, 22, 23, 24, 26, 30, 60])
+def test_paged_attention_large_scores(log2_scale, dt, q8):
+    """Scores of any size: values of one average to one, |dO| <= u_p + n x + 2^-20 + u, whatever the weights are."""
+    gen = torch.Generator().manual_seed(29)
+    D, Hkv, G, page, n = 64, 2, 4, 16, 1600
+    pool = make_pool(gen, 100, Hkv, page, D, dt, q8)
+    if q8:
+        pool[1].copy_(torch.ones(pool[1].shape).to(F8))
+        pool[3].zero_()
+    else:
+        pool[1].fill_(1)
+    table = torch.randperm(100, generator=gen).view(1, 100).to(torch.int32)
+    q = rand(gen, (1, G * Hkv, 1, D), dt)
+    o, lse = run_paged(q, pool, table.cuda(), i32([n]), 2.0 ** log2_scale)
+    ok()
+    up = 2.0 ** -8 if dt == BF and not q8 else 2.0 ** -11
+    within(to_f64(o), np.ones(o.shape), up + n * X + 2.0 ** -20 + U[dt], "O")
+    assert torch.isfinite(lse).all()
+
+
+@pytest.mark.parametrize("q8", [False, True])
 @pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("n", [40, 3000, 11000])
 def test_paged_attention_nan_query(D, q8, n):
