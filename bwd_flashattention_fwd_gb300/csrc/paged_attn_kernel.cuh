@@ -29,11 +29,16 @@
 // D, and V's come out as two rows of V^T after one byte permutation.  A
 // key's 2^e multiplies its score; a value's goes into the exponent, p'_j =
 // 2^(s_j + e_j - m') with m' the running maximum of s_j + e_j, so p' <= 1 whatever
-// the exponents, and l sums p'_j 2^-e_j in 32 bits: O = sum p' c / l.  Rows of Q
+// the exponents, and l sums the weights 2^(s_j - m') in 32 bits: O = sum p' c / l.
+// The largest weight of l is between 2^-120 and 2^64 (e is -64 .. 120), and l is kept
+// times 2^kPLift, so that a weight counts down to 2^-37 of it.  (p' comes from the weight and not
+// the other way round, which would be one instruction less for two: p' of a row of zeros, e = -64, beside
+// one of 2^100 is nothing where its weight is not.  32 rows over 4 sequences of 32768 quantised
+// keys 85.6 us, 83.8 so; D = 64 59.0 and 56.4; 4 x 8192 keys, 4 rows 16.6 and 16.4.)  Rows of Q
 // are scaled by a power of two to use fp16's range.
 //
 // fp16 P: times 2^15, so that what counts as nothing is 2^-40 of the row's
-// largest (2^-25 otherwise, and 10^5 such keys add up).
+// largest (2^-25 otherwise, and 10^5 such keys add up; beside exponents above 117 2^-37).
 //
 // Past a few rows, or with codes to widen, the instructions of a tile bound it (64
 // to 55% of the issue slots): scores and sums in packed pairs, masks only in tiles that need
@@ -206,6 +211,23 @@ template <int DST, int SRC, int... I>
 __device__ __forceinline__ void cp_async16_rows(uint32_t dst, const void* src, std::integer_sequence<int, I...>) {
   (..., cp_async16_at<I * DST, I * SRC>(dst, src));
 }
+
+constexpr int kPLift = 16;  // l is at most 2^(64 + 16 + kPLift) times the number of keys, 2^30
+
+// What results of reference `from` are multiplied by beside ones of reference `to`, d = from - to: O by o, l by l0 and then by l1.
+// Over quantised pages l 2^d may be of ordinary size where 2^d is below what 32 bits hold: by halves.
+template <bool Q8>
+struct PagedRescale {
+  float o, l0, l1;
+  __device__ __forceinline__ explicit PagedRescale(float d) {
+    if constexpr (Q8) {
+      l0 = l1 = ex2_approx(0.5f * d);
+      o = l0 * l1;
+    } else {
+      l0 = 1.f, o = l1 = ex2_approx(d);
+    }
+  }
+};
 
 // What the warps of a CTA share besides the ring.
 template <int NW, int ST, int ROWS>
@@ -497,7 +519,7 @@ __device__ __forceinline__ void paged_part(const PagedAttnParams& p, const Paged
     if (__any_sync(0xffffffffu, up)) {
 #pragma unroll
       for (int i = 0; i < NT; ++i) {
-        float old[2], fix[2];
+        float old[2], fix[2], l0[2], l1[2];
         f2_unpack(m[i], old[0], old[1]);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
@@ -505,10 +527,12 @@ __device__ __forceinline__ void paged_part(const PagedAttnParams& p, const Paged
           for (int x = 4; x < 32; x <<= 1) top[i][e] = fmaxf(top[i][e], __shfl_xor_sync(0xffffffffu, top[i][e], x));
           // (no row's result depends on another's scores; upwards, so that large scores too give at most 2^kPShift)
           top[i][e] = top[i][e] - old[e] > kPMost ? __fadd_ru(top[i][e], -kPShift) : old[e];
-          fix[e] = ex2_approx(old[e] - top[i][e]);
+          const PagedRescale<Q8> by(old[e] - top[i][e]);
+          fix[e] = by.o, l0[e] = by.l0, l1[e] = by.l1;
         }
         m[i] = f2_pack(top[i][0], top[i][1]);
-        l[i] = f2_mul(l[i], f2_pack(fix[0], fix[1]));
+        if constexpr (Q8) l[i] = f2_mul(l[i], f2_pack(l0[0], l0[1]));
+        l[i] = f2_mul(l[i], f2_pack(l1[0], l1[1]));
 #pragma unroll
         for (int d = 0; d < KK; ++d) {
           acc[d][i][0] *= fix[0], acc[d][i][1] *= fix[1];
@@ -529,14 +553,18 @@ __device__ __forceinline__ void paged_part(const PagedAttnParams& p, const Paged
       for (int i = 0; i < NT; ++i)
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          float p0, p1;
-          f2_unpack(f2_sub(f2_pack(sc[mb][i][2 * k], sc[mb][i][2 * k + 1]), m[i]), p0, p1);
-          p0 = ex2_approx(p0), p1 = ex2_approx(p1);
+          uint64_t x = f2_sub(f2_pack(sc[mb][i][2 * k], sc[mb][i][2 * k + 1]), m[i]);
           if constexpr (Q8) {
-            const float w = exp2_int(-ev[mb][k]);
-            l[i] = f2_fma(f2_pack(p0, p1), f2_pack(w, w), l[i]);
-          } else {
-            l[i] = f2_add(l[i], f2_pack(p0, p1));
+            const float e = static_cast<float>(ev[mb][k] - kPLift);
+            x = f2_sub(x, f2_pack(e, e));
+          }
+          float p0, p1;
+          f2_unpack(x, p0, p1);
+          p0 = ex2_approx(p0), p1 = ex2_approx(p1);
+          l[i] = f2_add(l[i], f2_pack(p0, p1));
+          if constexpr (Q8) {
+            const float e = exp2_int(ev[mb][k] - kPLift);
+            f2_unpack(f2_mul(f2_pack(p0, p1), f2_pack(e, e)), p0, p1);
           }
           b[i][k] = mat_trans(Elem<MMA_BF16>::pack(p0, p1));
         }
@@ -611,17 +639,18 @@ __device__ __forceinline__ float4 paged_join_warps(const float* join, const Shar
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
   for (int w = 0; w < Gm::NW; ++w) {
-    const float f = ex2_approx(sh.ml[w][r][0] - mx);
+    const PagedRescale<Q8> f(sh.ml[w][r][0] - mx);
     const float4 a = *reinterpret_cast<const float4*>(join + (w * Gm::ROWS + r) * Gm::JOIN_PITCH + 4 * c);
-    lsum = fmaf(sh.ml[w][r][1], f, lsum);
-    o.x = fmaf(a.x, f, o.x), o.y = fmaf(a.y, f, o.y), o.z = fmaf(a.z, f, o.z), o.w = fmaf(a.w, f, o.w);
+    lsum = fmaf(sh.ml[w][r][1] * f.l0, f.l1, lsum);
+    o.x = fmaf(a.x, f.o, o.x), o.y = fmaf(a.y, f.o, o.y), o.z = fmaf(a.z, f.o, o.z), o.w = fmaf(a.w, f.o, o.w);
   }
   return o;
 }
 
 // A finished row's column quad (and, with the first, its lse): mx and lsum its reference and sum (0: it saw no key).
-template <int D, bool BF16>
+template <int D, bool BF16, bool Q8>
 __device__ __forceinline__ void paged_store(const PagedAttnParams& p, size_t row, int c, const float4& o, float mx, float lsum) {
+  if constexpr (Q8) lsum *= exp2_int(-kPLift);
   const float by = lsum == 0.f ? 0.f : 1.f / lsum;
   if (!dbg_in_range(row, 1, static_cast<size_t>(p.B) * p.Hq * p.T, p.status, 122)) return;
   reinterpret_cast<uint2*>(p.o)[row * (D / 4) + c] = make_uint2(Elem<BF16>::pack(o.x * by, o.y * by), Elem<BF16>::pack(o.z * by, o.w * by));
@@ -661,7 +690,7 @@ __global__ void __launch_bounds__(PagedGeom<D, Q8, NT>::THREADS, PagedGeom<D, Q8
       float mx, lsum;
       const float4 o = paged_join_warps<D, Q8, NT>(join, sh, r, c, mx, lsum);
       if (whole) {
-        paged_store<D, BF16>(p, out0 + r, c, o, mx, lsum);
+        paged_store<D, BF16, Q8>(p, out0 + r, c, o, mx, lsum);
       } else if (dbg_in_range(part0 + r, 1, static_cast<size_t>(p.n_groups) * 2 * ROWS, p.status, 123)) {
         reinterpret_cast<float4*>(p.part)[(part0 + r) * (D / 4) + c] = o;
         if (c == 0) reinterpret_cast<float2*>(p.part_ml)[part0 + r] = make_float2(mx, lsum);
@@ -695,7 +724,7 @@ __global__ void __launch_bounds__(PagedGeom<D, Q8, NT>::THREADS, PagedGeom<D, Q8
     float mx, lsum;
     const float4 o = paged_join_warps<D, Q8, NT>(join, sh, r, c, mx, lsum);
     if (size == 1) {
-      paged_store<D, BF16>(p, out0 + r, c, o, mx, lsum);
+      paged_store<D, BF16, Q8>(p, out0 + r, c, o, mx, lsum);
     } else {  // over the first warp's, which no other thread reads here
       *reinterpret_cast<float4*>(join + r * Gm::JOIN_PITCH + 4 * c) = o;
       if (c == 0) stat[r] = make_float2(mx, lsum);
@@ -717,12 +746,12 @@ __global__ void __launch_bounds__(PagedGeom<D, Q8, NT>::THREADS, PagedGeom<D, Q8
 #pragma unroll
     for (int k = 0; k < kPagedCluster; ++k) {
       if (k >= size) continue;
-      const float f = ex2_approx(ml[k].x - mx);
+      const PagedRescale<Q8> f(ml[k].x - mx);
       const float4 a = ld_cluster_f4(cluster_map(join_at + (r * Gm::JOIN_PITCH + 4 * c) * 4, k));
-      lsum = fmaf(ml[k].y, f, lsum);
-      o.x = fmaf(a.x, f, o.x), o.y = fmaf(a.y, f, o.y), o.z = fmaf(a.z, f, o.z), o.w = fmaf(a.w, f, o.w);
+      lsum = fmaf(ml[k].y * f.l0, f.l1, lsum);
+      o.x = fmaf(a.x, f.o, o.x), o.y = fmaf(a.y, f.o, o.y), o.z = fmaf(a.z, f.o, o.z), o.w = fmaf(a.w, f.o, o.w);
     }
-    paged_store<D, BF16>(p, out0 + r, c, o, mx, lsum);
+    paged_store<D, BF16, Q8>(p, out0 + r, c, o, mx, lsum);
   }
   cluster_sync_all();  // no CTA leaves while others read its results
 }
@@ -785,11 +814,12 @@ __global__ void __launch_bounds__(kPagedJoinThreads) attn_paged_join_kernel(cons
 #pragma unroll
       for (int x = 16; x; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
       top = fmaxf(top, mx);
-      const float w = ex2_approx(ml.x - top), fix = ex2_approx(mx - top);
-      float add = ml.y * w;
+      const PagedRescale<Q8> part_by(ml.x - top), by(mx - top);
+      const float w = part_by.o, fix = by.o;
+      float add = ml.y * part_by.l0 * part_by.l1;
 #pragma unroll
       for (int x = 16; x; x >>= 1) add += __shfl_xor_sync(0xffffffffu, add, x);
-      l = fmaf(l, fix, add);
+      l = fmaf(l * by.l0, by.l1, add);
       mx = top;
 #pragma unroll
       for (int x = 0; x < Q; ++x) o[x].x *= fix, o[x].y *= fix, o[x].z *= fix, o[x].w *= fix;
@@ -837,8 +867,9 @@ __global__ void __launch_bounds__(kPagedJoinThreads) attn_paged_join_kernel(cons
       for (int x = 0; x < Q; ++x) o[x] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < WARPS; ++w) {
-        const float f = ex2_approx(stat[w].x - top);
-        l = fmaf(stat[w].y, f, l);
+        const PagedRescale<Q8> by(stat[w].x - top);
+        const float f = by.o;
+        l = fmaf(stat[w].y * by.l0, by.l1, l);
 #pragma unroll
         for (int x = 0; x < Q; ++x) {
           if (QUADS % 32 != 0 && x * 32 + lane >= QUADS) continue;
@@ -848,6 +879,7 @@ __global__ void __launch_bounds__(kPagedJoinThreads) attn_paged_join_kernel(cons
       }
       mx = top;
     }
+    if constexpr (Q8) l *= exp2_int(-kPLift);
     const float by = l == 0.f ? 0.f : 1.f / l;
     if (dbg_in_range(task, 1, static_cast<size_t>(tasks), p.status, 124)) {
 #pragma unroll

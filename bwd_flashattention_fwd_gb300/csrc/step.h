@@ -38,7 +38,7 @@ constexpr int kPagedMaxRows = 128;      // G * T
 constexpr int kPagedMaxTokens = 1 << 30;  // a sequence's room (token numbers are ints)
 constexpr int kPagedMaxCtas = 3 * kTreeMaxCtas;
 constexpr int kPagedCluster = 8;  // CTAs that share a head of a short cache, at most
-// A quantised row's exponent: scores and sums that carry 2^e and 2^-e stay inside fp32.
+// A quantised row's exponent.  (The largest is what bf16's values need; below the least lie 2^-73 and less.)
 constexpr int kExpMin = -64, kExpMax = 120;
 
 // The cache: pages [n_pages][Hkv][2^shift][D], 16-bit or e4m3 with an exponent per row.

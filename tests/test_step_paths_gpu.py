@@ -1,0 +1,135 @@
+"""GPU parity of the calls around attention on the paths that only larger
+inputs reach, and at values that only some rows see: equal pieces of the paged
+attention with both joins and several blocks of rows, exponents of quantised
+values at both ends of their range, several tables of sines in a CTA of the
+rotation, elements that are not turned, probabilities that are none, streams.
+
+Tolerances as in test_step_ops_gpu.py, but for what a test says itself.
+Launch shapes are those of a GPU with 152 SMs (the launcher's rules are in
+sizes, so another count moves a case to another path, not to another result)."""
+
+import os
+import subprocess
+import sys
+
+import numpy as np
+import pytest
+import torch
+
+import oracle.step as S
+import test_step_ops_gpu as ops
+from bwd_flashattention_fwd_gb300 import gbattn
+from bwd_flashattention_fwd_gb300.inputs import to_f64
+from test_step_ops_gpu import BF, F8, HF, U, X, i32, make_pool, ok, pool64, rand, run_paged, within
+
+pytestmark = pytest.mark.gpu
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _library():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from bwd_flashattention_fwd_gb300 import build
+
+    build.build()
+    gbattn.load_library()
+
+
+def roomy(gen, B, page, lens, room, order="random"):
+    """A table with `room` tokens for each sequence whose pages past the lengths are holes, and the pool's size."""
+    need = [-(-max(n, 0) // page) for n in lens]
+    total = sum(need)
+    pages = torch.randperm(total, generator=gen) if order == "random" else torch.arange(total)
+    table, at = torch.full((B, room // page), -1, dtype=torch.int32), 0
+    for b, n in enumerate(need):
+        table[b, :n] = pages[at:at + n].to(torch.int32)
+        at += n
+    return table, total + 1
+
+
+# --- exponents of quantised values at both ends of their range ------------------
+
+
+def check_wide(q, pool, table, page, lens, scale, got):
+    """As check_paged, with one more term: a score s carries its value's exponent through three sums (s + e, less the
+    row's reference, less e), each rounded to 2^-24 of at most E = 2 (max |e| + max |s| log2e + 32): a probability is off by a
+    factor within 1 +- 3 ln2 E x more.  What P's type rounds to nothing is 2^-40 of the row's largest product of probability and
+    scale, 448 2^e of which some element has half (a row of zeros: 2^-55)."""
+    k, v, ke, ve = pool
+    D, dt, n = q.shape[-1], q.dtype, max(lens)
+    e = [t.cpu().numpy() for t in (ke, ve)]
+    ref, lref, mag = S.paged_attention(to_f64(q), pool64(k), pool64(v), *e, table.numpy(), page, lens, scale)
+    used = np.unique(table.numpy())
+    used = used[used >= 0]
+    kk = pool64(k)[used] * 2.0 ** e[0][used][..., None].astype(float)
+    s = scale * np.sqrt((to_f64(q) ** 2).sum(-1).max()) * np.sqrt((kk ** 2).sum(-1).max())
+    d = (D + 16) * X * s + 3 * np.log(2) * X * 2 * (np.abs(e[1][used].astype(int)).max() + 1.45 * s + 32)
+    o, lse = to_f64(got[0]), to_f64(got[1])
+    tol = (2.0 ** -11 + 4 * d + n * X + 2.0 ** -20) * mag + U[dt] * np.abs(ref) + 2.0 ** -38 * n * (2 * mag.max(-1, keepdims=True) + 2.0 ** -55)
+    within(o, ref, tol, "O")
+    inf = np.isposinf(lref)
+    assert np.array_equal(inf, np.isposinf(lse)) and (o[inf] == 0).all()
+    within(lse[~inf], lref[~inf], 1.45 * (2 * d + n * X + 2.0 ** -21) + 2 * X * np.abs(lref[~inf]), "lse")
+
+
+# which tokens (of n) hold large values, the others being zero or tiny: in one tile, by warps' tiles, by clusters' and pieces' parts
+SPLITS = {
+    "alternate": lambda j, n: j % 2 == 0,
+    "one": lambda j, n: j == n // 3,
+    "tiles": lambda j, n: j // 16 % 2 == 1,
+    "steps": lambda j, n: j // 128 % 2 == 1,
+    "first half": lambda j, n: j < n // 2,
+    "last half": lambda j, n: j >= n // 2,
+}
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("high", [40, 60, 92, 119])
+@pytest.mark.parametrize("split", list(SPLITS))
+def test_exponents_far_apart(split, high, D):
+    """Rows of V that are zero (exponent -64) or tiny beside rows with exponents up to `high`: every key keeps its weight in
+    the sum of the softmax, whatever its value's exponent."""
+    gen = torch.Generator().manual_seed(45)
+    n, page, G = 600, 16, {64: 12, 128: 20, 256: 8}[D]
+    rng = np.random.default_rng(46)
+    large = SPLITS[split](np.arange(n), n)
+    for room, low in ((608, -64), (608, -30), (40000, -64)):  # a cluster per head; pieces and a join
+        table, n_pages = roomy(gen, 1, page, [n], room, order="sorted")
+        pool = make_pool(gen, n_pages, 1, page, D, BF, True)
+        k, v, ke, ve = pool
+        e = np.full(n_pages * page, low)
+        e[:n][large] = high - rng.integers(0, 3, large.sum())
+        ve.copy_(torch.from_numpy(e).to(torch.int8).view(n_pages, 1, page))
+        if low == -64:  # zero rows
+            v.view(torch.uint8).masked_fill_((ve == -64)[..., None], 0)
+        q = rand(gen, (1, G, 1, D), BF, 0.5)
+        q[0, 0] = 0  # equal scores
+        got = run_paged(q, pool, table.cuda(), i32([n]), 0.1)
+        ok()
+        check_wide(q, pool, table[:, :38], page, [n], 0.1, got)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_exponents_of_every_size(D):
+    """Sequences whose values' exponents run through the whole range, with scores that favour the small ones."""
+    gen = torch.Generator().manual_seed(47)
+    page, lens = 16, [500, 400, 1]
+    for room in (512, 40000):
+        table, n_pages = roomy(gen, 3, page, lens, room, order="sorted")
+        pool = make_pool(gen, n_pages, 2, page, D, BF, True, std=0.3)
+        k, v, ke, ve = pool
+        ve.copy_(torch.randint(-64, 120, ve.shape, generator=gen).to(torch.int8))
+        # (the product with q below is the exponent's share of the score: -0.7 of it)
+        first = (-ve.float() / 16).cpu().numpy()
+        c, _ = S.quantise(np.repeat(first[..., None].astype(np.float64), D, -1))
+        k64 = pool64(k) * 2.0 ** ke.cpu().numpy()[..., None].astype(float)
+        k64[..., 0] = first
+        c, e = S.quantise(k64)
+        k.copy_(torch.from_numpy(c).float().to(F8)), ke.copy_(torch.from_numpy(e).to(torch.int8))
+        q = rand(gen, (3, 4, 1, D), BF, 0.3)
+        q[..., 0] = 80
+        got = run_paged(q, pool, table.cuda(), i32(lens), 0.1)
+        ok()
+        check_wide(q, pool, table[:, :32], page, lens, 0.1, got)
