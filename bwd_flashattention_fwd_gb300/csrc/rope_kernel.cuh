@@ -78,16 +78,20 @@ __device__ __forceinline__ void store16(uint16_t* row, int c0, int c1, const uin
 // Turn the eight pairs of a lane's two pieces.  Halves: neighbours f[i] turn with
 // f[i + 4], c[i] and s[i] (i < 4) hold two pairs' cosines and sines.
 // Interleaved: f[i] is one pair, c[i] = (cos, cos), s[i] = (-sin, sin) (i < 8).
+// turn0, turn1: whether the first and the second piece hold pairs (halves: both or neither); what
+// is not turned is left alone (turned by nothing, an infinite one would reach its neighbours).
 template <bool INTERLEAVED>
-__device__ __forceinline__ void rotate16(uint64_t (&f)[8], const uint64_t (&c)[INTERLEAVED ? 8 : 4], const uint64_t (&s)[INTERLEAVED ? 8 : 4]) {
+__device__ __forceinline__ void rotate16(uint64_t (&f)[8], const uint64_t (&c)[INTERLEAVED ? 8 : 4], const uint64_t (&s)[INTERLEAVED ? 8 : 4],
+                                         bool turn0, bool turn1) {
   if constexpr (INTERLEAVED) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
+      if (!(i < 4 ? turn0 : turn1)) continue;
       float a, b;
       f2_unpack(f[i], a, b);
       f[i] = f2_fma(f[i], c[i], f2_mul(f2_pack(b, a), s[i]));
     }
-  } else {
+  } else if (turn0) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const uint64_t a = f[i], b = f[i + 4];
@@ -163,8 +167,9 @@ __global__ void __launch_bounds__(kRopeThreads, RopeGeom<D, BWD>::PER_SM) rope_k
     c0 = j;
     c1 = j + turned;
   }
+  const bool turn0 = INTERLEAVED ? c0 < 2 * turned : j < turned, turn1 = INTERLEAVED ? c1 < 2 * turned : turn0;
   // Where the cosines (and, D / 2 floats on, sines) of its pairs lie in a token's part of cs, in fours: neighbouring
-  // lanes' fours side by side.  Pairs that are not turned have cosine 1 and sine 0.
+  // lanes' fours side by side.  (What lies there for elements that are not turned is not used.)
   const int four0 = 4 * (INTERLEAVED ? c0 : j), four1 = 4 * (INTERLEAVED ? c1 : D / 16 + j);
   auto place = [](int pair) { return INTERLEAVED ? pair : ((pair >> 2 & 1) * (D / 16) + (pair >> 3)) * 4 + (pair & 3); };
   const bool norm = p.w[0] != nullptr;
@@ -175,11 +180,6 @@ __global__ void __launch_bounds__(kRopeThreads, RopeGeom<D, BWD>::PER_SM) rope_k
   const int t_first = block * per + min(block, more), t_end = t_first + per + (block < more ? 1 : 0);
   const int q_lo = p.x[0].H * part / parts, q_n = p.x[0].H * (part + 1) / parts - q_lo;  // heads of q and of k
   const int k_lo = p.x[1].H * part / parts, k_n = p.x[1].H * (part + 1) / parts - k_lo;
-  if (p.rot < D)
-    for (int i = threadIdx.x; i < Gm::TOKENS * (D / 2); i += kRopeThreads) {
-      const int ti = i / (D / 2), pi = i - ti * (D / 2);
-      if (pi >= half) cs[ti * D + place(pi)] = 1.f, cs[ti * D + D / 2 + place(pi)] = 0.f;
-    }
   // bytes between heads
   const uint32_t x_head[2] = {static_cast<uint32_t>(p.x[0].sh * 2), static_cast<uint32_t>(p.x[1].sh * 2)};
   const uint32_t d_head[2] = {static_cast<uint32_t>(p.dx[0].sh * 2), static_cast<uint32_t>(p.dx[1].sh * 2)}, y_head = p.L * (D * 2);
@@ -314,7 +314,7 @@ __global__ void __launch_bounds__(kRopeThreads, RopeGeom<D, BWD>::PER_SM) rope_k
 #pragma unroll
             for (int e = 0; e < 8; ++e) f[e] = f2_mul(f2_mul(f[e], rr), w[e]);
           }
-          rotate16<INTERLEAVED>(f, c, s);
+          rotate16<INTERLEAVED>(f, c, s, turn0, turn1);
           if (live) {
             const uint64_t yo = at[Gm::TOKENS + t] + static_cast<uint64_t>(static_cast<uint32_t>(h)) * y_head;
             if (inside_y(yo, which, 102)) store16<BF16>(reinterpret_cast<uint16_t*>(yo), c0, c1, f);
@@ -322,7 +322,7 @@ __global__ void __launch_bounds__(kRopeThreads, RopeGeom<D, BWD>::PER_SM) rope_k
         } else {
           const uint4 gp[2] = {ld_shared_v4(slot + 2 * kRopeThreads * 16), ld_shared_v4(slot + 3 * kRopeThreads * 16)};
           unpack16<BF16>(gp, f);
-          rotate16<INTERLEAVED>(f, c, s);
+          rotate16<INTERLEAVED>(f, c, s, turn0, turn1);
           if (norm) {
             const uint4 xp[2] = {ld_shared_v4(slot), ld_shared_v4(slot + kRopeThreads * 16)};
             uint64_t x[8], ss[2] = {0, 0}, gx[2] = {0, 0};

@@ -133,3 +133,45 @@ def test_exponents_of_every_size(D):
         got = run_paged(q, pool, table.cuda(), i32(lens), 0.1)
         ok()
         check_wide(q, pool, table[:, :32], page, lens, 0.1, got)
+
+
+# --- the rotation: elements that are not turned --------------------
+
+
+@pytest.mark.parametrize("value", [float("inf"), float("-inf"), float("nan")])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("D,rot", [(64, 16), (64, 48), (96, 32), (96, 80), (128, 64), (256, 16), (256, 192)])
+def test_rope_unturned_elements_are_their_own(D, rot, interleaved, value):
+    """One element that is not turned is infinite or no number: every other element of the row is as without it, and it
+    comes out as it went in (no norm; forward, and the gradient)."""
+    gen = torch.Generator().manual_seed(53)
+    L = D - rot  # token t has it at element rot + t
+    pos = torch.arange(L, dtype=torch.int32, device="cuda")[None] * 7
+    freq = torch.rand(rot // 2, generator=gen).cuda()
+    clean = [rand(gen, (1, h, L, D), BF) for h in (3, 2)]
+    dirty = [x.clone() for x in clean]
+    at = torch.arange(L, device="cuda")
+    for x, y in zip(clean, dirty):
+        x[:, :, at, rot + at] = 0
+        y[:, :, at, rot + at] = value
+    mark = torch.zeros(L, D, dtype=torch.bool, device="cuda")
+    mark[at, rot + at] = True
+
+    def forward(x):
+        out = [torch.empty_like(t) for t in x]
+        gbattn.attn_qk_norm_rope(*x, *out, pos, freq, interleaved=interleaved)
+        return out
+
+    def backward(x):
+        out = [torch.empty_like(t) for t in x]
+        gbattn.attn_qk_norm_rope_bwd(*clean, *x, pos, freq, *out, None, None, None, None, gbattn.qk_norm_rope_workspace(*x), interleaved=interleaved)
+        return out
+
+    for f in (forward, backward):
+        want, got = f(clean), f(dirty)
+        ok()
+        for w, g, x in zip(want, got, dirty):
+            assert torch.equal(torch.where(mark, torch.zeros_like(g), g), w)
+            assert torch.equal(g[..., rot:].view(torch.int16), x[..., rot:].view(torch.int16)) or value != value
+            if value != value:
+                assert g[:, :, at, rot + at].isnan().all()
