@@ -27,14 +27,12 @@ constexpr int kVerifyCluster = 8;
 
 // A probability as hi 2^-22 + lo 2^-45, both read off the bits of a float that a
 // constant pushes into a known binade (so the constants' bits belong to hi and
-// lo: differences of two are free of them).  What is negative or NaN counts as
-// 0, what is above 1 as 1; the nearest multiple of 2^-45, so a larger probability never
-// becomes the smaller one.
+// lo: differences of two are free of them); the nearest multiple of 2^-45, so a larger
+// probability never becomes the smaller one.
 struct Fixed {
   int hi, lo;
 };
-__device__ __forceinline__ Fixed prob_fixed(float x) {
-  x = __saturatef(x);
+__device__ __forceinline__ Fixed prob_fixed(float x) {  // (0 <= x <= 1)
   const float a = __fadd_rn(x, 3.f), rest = __fsub_rn(x, __fsub_rn(a, 3.f));
   return {__float_as_int(a), __float_as_int(__fmaf_rn(rest, 4194304.f, 1.5f))};
 }
@@ -43,6 +41,7 @@ __device__ __forceinline__ Fixed prob_fixed(float x) {
 struct FixedSum {
   int hi = 0, lo = 0;
   __device__ __forceinline__ void add(float p, float q) {
+    p = __saturatef(p), q = __saturatef(q);  // what is negative or NaN counts as 0, what is above 1 as 1, in the comparison as well
     const Fixed a = prob_fixed(p), b = prob_fixed(q);
     if (p > q) hi += a.hi - b.hi, lo += a.lo - b.lo;
   }

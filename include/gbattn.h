@@ -441,7 +441,8 @@ attn_status_t attn_fwd_paged(const void* q, const void* k_pages, const void* v_p
  *   tokens int32 [B,T]; draft_len int32 [B] or NULL (T for all; brought into 0..T).
  *   u float32 [B,T], r float32 [B]: uniform in [0, 1).
  *   Draft i is accepted if u_i * draft_i(x_i) < target_i(x_i) and all before
- *   it are (a token outside 0..V-1 never is); accept_len [B] is their number n.
+ *   it are (a token outside 0..V-1 never is, nor where one of the three is NaN);
+ *   accept_len [B] is their number n.
  *   token [B]: the next token, drawn from w = max(target_n - draft_n, 0) where
  *   draft n was rejected (from target_n if nothing is left of it), from
  *   target_n where none was: the least x with sum_{y<=x} w_y > r * sum w, -1 if

@@ -175,3 +175,33 @@ def test_rope_unturned_elements_are_their_own(D, rot, interleaved, value):
             assert torch.equal(g[..., rot:].view(torch.int16), x[..., rot:].view(torch.int16)) or value != value
             if value != value:
                 assert g[:, :, at, rot + at].isnan().all()
+
+
+# --- verification -----------------------------------------------------------------
+
+
+@pytest.mark.parametrize("V", [70, 72, 5003, 5004])
+def test_verify_draft_that_is_no_probability(V):
+    """NaN, negative, infinite and large entries of the draft: NaN and what is negative count as 0, what is above 1 as 1."""
+    nan, inf = float("nan"), float("inf")
+    p = torch.zeros(10, 2, V)
+    q = torch.zeros(10, 1, V)
+    p[:, 0, 0], p[:, 0, 1], p[:, 0, V - 1] = 0.25, 0.25, 0.5
+    p[:, 1, 2] = 1
+    q[:, 0, 1], q[:, 0, V - 1] = 0.9, 0.1
+    q[0, 0, 0] = q[1, 0, 0] = nan
+    q[2, 0, 0] = -3.0
+    q[3, 0, 0] = -inf
+    q[4, 0, 0] = inf
+    q[5, 0, 0] = 7.0
+    q[6, 0] = nan          # at the token as well: rejected, and p is left
+    q[7, 0, V - 1] = nan
+    p[8, 0, 0] = nan       # both
+    q[8, 0, 0] = nan
+    p[9, 0, 0], q[9, 0, 0] = 2.5, 1.5
+    tokens = torch.ones(10, 1, dtype=torch.int32)
+    u, r = torch.full((10, 1), 0.9), torch.full((10,), 0.1)
+    r[1] = 0.9
+    a, t = ops.verify(*(x.cuda() for x in (p, q, tokens, u, r)))
+    assert a.tolist() == [0] * 10
+    assert t.tolist() == [0, V - 1, 0, 0, V - 1, V - 1, 0, 0, V - 1, V - 1]
