@@ -425,6 +425,7 @@ extern "C" attn_status_t attn_draft_verify(const float* target, const float* dra
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  const auto kern = V % 4 == 0 ? attn_draft_verify_kernel<true> : attn_draft_verify_kernel<false>;
+  const auto kern = V < kVerifyLong ? (V % 4 == 0 ? attn_draft_verify_kernel<true, false> : attn_draft_verify_kernel<false, false>)
+                                    : (V % 4 == 0 ? attn_draft_verify_kernel<true, true> : attn_draft_verify_kernel<false, true>);
   return cudaLaunchKernelEx(&cfg, kern, p) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }

@@ -50,9 +50,19 @@ struct FixedSum {
   }
 };
 
+// Sums of weights.  Past 2^19 tokens entries of 1 could add up to 2^64 and more (probabilities come nowhere near): there
+// (LONG) sums stop at 2^64 - 1, which is the same in any order, so that a token is still found where
+// they first pass r times that.  (At 64 x 151936 tokens 19.0 us with such sums, 18.3 without.)
+constexpr int kVerifyLong = 1 << 19;
+template <bool LONG>
+__device__ __forceinline__ uint64_t plus(uint64_t a, uint64_t b) {
+  const uint64_t s = a + b;
+  return LONG && s < a ? ~0ull : s;
+}
+template <bool LONG>
 __device__ __forceinline__ uint64_t warp_sum(uint64_t x) {
 #pragma unroll
-  for (int m = 16; m; m >>= 1) x += __shfl_xor_sync(0xffffffffu, x, m);
+  for (int m = 16; m; m >>= 1) x = plus<LONG>(x, __shfl_xor_sync(0xffffffffu, x, m));
   return x;
 }
 
@@ -63,7 +73,7 @@ __device__ __forceinline__ uint64_t ld_cluster_u64(uint32_t addr) {
 }
 
 // A cluster per sequence; warp w of CTA c holds a contiguous part of the vocabulary.  VEC: rows start on 16 bytes.
-template <bool VEC>
+template <bool VEC, bool LONG>
 __global__ void __launch_bounds__(kVerifyThreads, 4) attn_draft_verify_kernel(const VerifyParams p) {
   constexpr int WARPS = kVerifyThreads / 32, W = VEC ? 4 : 1, STEP = 32 * W;
   __shared__ int cut;
@@ -147,9 +157,9 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) attn_draft_verify_kernel(co
       for (int i = 0; i < N; ++i)
 #pragma unroll
         for (int k = 0; k < W; ++k) s.add(a[i][k], q[i][k]);
-      sum += s.value();
+      sum = plus<LONG>(sum, s.value());
     }
-    if (lane == 0 && without >= from && without < to) {  // a deterministic draft's token has no weight
+    if (without >= from && without < to && (without - from) / W % 32 == lane) {  // a deterministic draft's token has no weight
       FixedSum s;
       s.add(prow[without], 0.f);
       sum -= s.value();
@@ -162,7 +172,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) attn_draft_verify_kernel(co
   int without = point;
   uint64_t sum, total, before;  // of this warp's part, of all, of what lies before the part
   auto add_up = [&](int which) {
-    sum = warp_sum(sum_of(bound(mine), bound(mine + 1), with_q, without));
+    sum = warp_sum<LONG>(sum_of(bound(mine), bound(mine + 1), with_q, without));
     if (lane == 0) part[which][warp] = sum;
     cluster_sync_all();
     total = before = 0;
@@ -170,10 +180,10 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) attn_draft_verify_kernel(co
     for (int i = 0; i < kVerifyCluster * WARPS / 32; ++i) {  // all warps' sums, a few a lane
       const int w = i * 32 + lane;
       const uint64_t v = ld_cluster_u64(cluster_map(smem_u32(&part[which][w % WARPS]), w / WARPS));
-      total += v;
-      if (w < mine) before += v;
+      total = plus<LONG>(total, v);
+      if (w < mine) before = plus<LONG>(before, v);
     }
-    total = warp_sum(total), before = warp_sum(before);
+    total = warp_sum<LONG>(total), before = warp_sum<LONG>(before);
   };
   add_up(0);
   if (total == 0 && rejected) {  // nothing is left (the same for the whole cluster): p itself
@@ -196,7 +206,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) attn_draft_verify_kernel(co
     p.accept_len[b] = n;
     if (total == 0) p.token[b] = -1;
   }
-  if (lane == 0 && before <= limit && limit < before + sum) chosen = warp, chosen_before = before;
+  if (lane == 0 && before <= limit && limit < plus<LONG>(before, sum)) chosen = warp, chosen_before = before;
   __syncthreads();
   if (chosen >= 0) {  // this CTA holds the token: its warps look at that part's steps, WARPS at a time
     const int from = bound(c * WARPS + chosen), to = bound(c * WARPS + chosen + 1);
@@ -230,18 +240,18 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) attn_draft_verify_kernel(co
         if (w < warp) ahead += y;
         all += y;
       }
-      const uint64_t s0 = run + ahead + upto - own;
-      if (s0 <= limit && limit < s0 + own) {  // this lane's tokens
+      const uint64_t s0 = plus<LONG>(run, ahead + (upto - own));
+      if (s0 <= limit && limit < plus<LONG>(s0, own)) {  // this lane's tokens
         uint64_t s = s0;
         int k = 0;
 #pragma unroll
         for (int i = 0; i < W - 1; ++i) {
-          s += v[i];
+          s = plus<LONG>(s, v[i]);
           if (s <= limit && k == i) k = i + 1;
         }
         p.token[b] = x + k;
       }
-      run += all;
+      run = plus<LONG>(run, all);
       __syncthreads();
       if (run > limit) break;
     }

@@ -447,7 +447,8 @@ attn_status_t attn_fwd_paged(const void* q, const void* k_pages, const void* v_p
  *   draft n was rejected (from target_n if nothing is left of it), from
  *   target_n where none was: the least x with sum_{y<=x} w_y > r * sum w, -1 if
  *   all are 0.  Probabilities count in multiples of 2^-45 (the
- *   nearest), those below 0 and NaN as 0, those above 1 as 1.  Sums are exact.
+ *   nearest), those below 0 and NaN as 0, those above 1 as 1.  Sums are exact (and stop at
+ *   2^19, which rows that are no probabilities can pass).
  *   T <= 1024, B <= 65535, V <= 2^30 (else ATTN_ERR_UNSUPPORTED).  No output
  *   overlaps an input or the other output (ATTN_ERR_INVALID_ARG).  target and
  *   draft 16-byte aligned, the others 4-byte.

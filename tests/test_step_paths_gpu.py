@@ -205,3 +205,27 @@ def test_verify_draft_that_is_no_probability(V):
     a, t = ops.verify(*(x.cuda() for x in (p, q, tokens, u, r)))
     assert a.tolist() == [0] * 10
     assert t.tolist() == [0, V - 1, 0, 0, V - 1, V - 1, 0, 0, V - 1, V - 1]
+
+
+@pytest.mark.parametrize("V", [(1 << 19) - 4, 1 << 19, (1 << 19) + 8, 1 << 20, (1 << 20) + 3])
+def test_verify_sums_past_64_bits(V):
+    """Rows whose entries add up to 2^19 and more (no probabilities, then): sums stop at 2^64 - 1 multiples of 2^-45, so the
+    token is still the one that the definition gives."""
+    most, one = 2 ** 64 - 1, 2 ** 45
+    p = torch.ones(4, 2, V, device="cuda")
+    r = torch.tensor([0.0, 0.25, 0.5, 1 - 2.0 ** -24])
+    total = min(V * one, most)
+    want = [(int(float(x) * 2.0 ** 64) * total >> 64) // one for x in r]  # the least x with (x + 1) one > limit
+    for draft, skip in ((None, None), (torch.zeros(4, 1, V, device="cuda"), None)):
+        accept, token = i32([-9] * 4), i32([-9] * 4)
+        # draft_len 0: the token is drawn from the whole row
+        gbattn.attn_draft_verify(p, draft, i32([[5]] * 4), torch.full((4, 1), 0.5, device="cuda"), r.cuda(), accept, token, draft_len=i32([0] * 4))
+        ok()
+        assert accept.tolist() == [0] * 4 and token.tolist() == want
+    # a rejected deterministic draft (u q < p does not hold): its token has no weight
+    accept, token = i32([-9] * 4), i32([-9] * 4)
+    gbattn.attn_draft_verify(p, None, i32([[5]] * 4), torch.full((4, 1), 1.0, device="cuda"), r.cuda(), accept, token)
+    ok()
+    total = min((V - 1) * one, most)
+    least = [(int(float(x) * 2.0 ** 64) * total >> 64) // one for x in r]
+    assert accept.tolist() == [0] * 4 and token.tolist() == [x if x < 5 else x + 1 for x in least]
