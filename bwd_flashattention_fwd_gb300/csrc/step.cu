@@ -47,20 +47,32 @@ Span rows_span(const void* at, int B, int H, int L, int D, const int64_t* st) {
   return {at, 2 * ((B - 1) * st[0] + (H - 1) * st[1] + (L - 1) * st[2] + D)};
 }
 
-// Whether two sets of rows that interleave (heads of one packed [B, L, heads, D]
-// array) have an element in common, as far as their strides tell.
+// Whether off + sum n_i s_i, lo_i <= n_i <= hi_i, comes within D of 0 for the dimensions order[i] on, the widest stride
+// first.  What the narrower ones span is at most a stride, so each n_i is one of the two that bring the sum across 0.
+bool rows_meet(int64_t off, const int64_t (&s)[3], const int (&lo)[3], const int (&hi)[3], const int (&order)[3], int i, int D) {
+  if (i == 3) return off > -D && off < D;
+  const int k = order[i];
+  if (lo[k] == 0 && hi[k] == 0) return rows_meet(off, s, lo, hi, order, i + 1, D);
+  const int64_t n = off <= 0 ? -off / s[k] : -((off + s[k] - 1) / s[k]);  // floor(-off / s)
+  for (int64_t x = n; x <= n + 1; ++x)
+    if (x >= lo[k] && x <= hi[k] && rows_meet(off + x * s[k], s, lo, hi, order, i + 1, D)) return true;
+  return false;
+}
+
+// Whether two sets of rows (each with no element twice) have an element in common, exact for views of one packed array:
+// strides alike wherever a size has them, starts a whole number of rows apart.  Others are taken to, where what they span overlaps.
 bool rows_overlap(const void* a, int Ha, const int64_t* sa, const void* b, int Hb, const int64_t* sb, int B, int L, int D) {
   if (!overlap(rows_span(a, B, Ha, L, D, sa), rows_span(b, B, Hb, L, D, sb))) return false;
-  if (sa[0] != sb[0] || sa[1] != sb[1] || sa[2] != sb[2] || sa[1] == 0) return true;
-  const bool a_first = reinterpret_cast<uintptr_t>(a) <= reinterpret_cast<uintptr_t>(b);
-  const int64_t off = static_cast<int64_t>(a_first ? reinterpret_cast<uintptr_t>(b) - reinterpret_cast<uintptr_t>(a)
-                                                   : reinterpret_cast<uintptr_t>(a) - reinterpret_cast<uintptr_t>(b));
-  // the later one begins `off` behind the earlier: a whole number of heads, past
-  // its last, and the two together are one array of rows that do not overlap
-  if (off % (2 * sa[1]) != 0) return true;
-  const int64_t heads = off / (2 * sa[1]);
-  const int first = a_first ? Ha : Hb, second = a_first ? Hb : Ha;
-  return heads < first || heads + second > (1 << 30) || !disjoint_rows(B, static_cast<int>(heads) + second, L, D, sa);
+  if ((B > 1 && sa[0] != sb[0]) || (Ha > 1 && Hb > 1 && sa[1] != sb[1]) || (L > 1 && sa[2] != sb[2])) return true;
+  const int64_t off = static_cast<int64_t>(reinterpret_cast<uintptr_t>(b) - reinterpret_cast<uintptr_t>(a));
+  if (off % (2 * D) != 0) return true;
+  const int64_t s[3] = {sa[0], Ha > 1 ? sa[1] : sb[1], sa[2]};
+  const int lo[3] = {1 - B, 1 - Ha, 1 - L}, hi[3] = {B - 1, Hb - 1, L - 1};
+  int order[3] = {0, 1, 2};
+  for (int i = 0; i < 3; ++i)
+    for (int j = i + 1; j < 3; ++j)
+      if (s[order[j]] > s[order[i]]) { const int t = order[i]; order[i] = order[j], order[j] = t; }
+  return rows_meet(off / 2, s, lo, hi, order, 0, D);
 }
 
 void dense(int64_t* st, int H, int L, int D) {

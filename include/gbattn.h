@@ -359,7 +359,8 @@ attn_status_t attn_cache_evict(void* k, void* v, const float* weight, const int3
  * attn_qk_norm_rope_bwd: the gradients.  dq_out, dk_out (dtype, contiguous:
  *   what attn_bwd wrote) are those of the outputs above, dq and dk (dtype, at
  *   dq_strides and dk_strides, fully written; the views of one packed gradient
- *   will do) those of q and k, dq_weight and dk_weight float32 [D] those of
+ *   will do, in any order of its dimensions, where their strides are alike and
+ *   they start whole rows apart) those of q and k, dq_weight and dk_weight float32 [D] those of
  *   the weights (with them).  No output overlaps an input, another output or
  *   the workspace (attn_qk_norm_rope_workspace_bytes(D) bytes, one per call in
  *   flight).  Sums are in a fixed order: the same call gives the same bits.

@@ -266,3 +266,59 @@ def test_binding_rejects_host_tensors():
         gbattn.attn_fwd_paged(q, pages, pages, i, i[0], q, f, f, 0.1)
     with pytest.raises(ValueError, match="CUDA tensor"):
         gbattn.attn_draft_verify(f.view(1, 2, 16), None, i[:, :1], f, f, i, i)
+
+
+# --- gradients that share an array ---------------------------------------------
+
+
+def rows_of(at, B, H, L, D, s):
+    """Every element (in units of 8) of rows [B, H, L, D] at strides s from address `at`."""
+    i = np.arange(B)[:, None, None, None] * s[0] + np.arange(H)[None, :, None, None] * s[1] + np.arange(L)[None, None, :, None] * s[2]
+    return set(((at - A[9]) // 16 + (i + np.arange(0, D, 8)) // 8).reshape(-1).tolist())
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="an accepted call would run on these addresses")
+def test_rope_takes_any_packed_gradient(lib):
+    """Layouts of one packed gradient that the header allows: one KV head under any stride, q and k of each head side by
+    side, sizes of one whose strides say nothing.  (Without a GPU an accepted call ends at the device.)"""
+    D, L = 64, 16
+    at = A[9]
+    ok = lambda **kw: rope_bwd(lib, D=D, rot=D, L=L, **kw) not in (INV, UNS)
+    # [B, L, Hq + 2, D], one KV head taken by an index and unsqueezed
+    packed = (L * 10 * D, D, 10 * D)
+    assert ok(Hkv=1, dqs=st(*packed), dks=st(packed[0], L * 10 * D, 10 * D), dk=at + 2 * 8 * D)
+    assert ok(Hkv=1, dqs=st(*packed), dks=st(packed[0], 0, 10 * D), dk=at + 2 * 9 * D)
+    assert ok(Hq=1, Hkv=1, dqs=st(L * 3 * D, 8, 3 * D), dks=st(L * 3 * D, 1 << 20, 3 * D), dk=at + 2 * D)
+    # [B, L, H, 3, D]: q, k and v of a head side by side
+    side = (L * 4 * 3 * D, 3 * D, 4 * 3 * D)
+    assert ok(Hq=4, Hkv=4, dqs=st(*side), dks=st(*side), dk=at + 2 * D)
+    assert ok(Hq=4, Hkv=4, dqs=st(*side), dks=st(*side), dk=at + 2 * 2 * D, dq=at)
+    # one sequence, one token
+    assert ok(B=1, dqs=st(7, D, 12 * D), dks=st(1 << 30, D, 12 * D), dk=at + 2 * 8 * D)
+    assert rope_bwd(lib, D=D, rot=D, L=1, dqs=st(12 * D, D, 1), dks=st(12 * D, D, 5), dk=at + 2 * 8 * D) not in (INV, UNS)
+    # heads outermost, tokens of both beside one another
+    assert ok(Hq=4, Hkv=2, dqs=st(2 * D * L, 4 * D * L, 2 * D), dks=st(2 * D * L, 4 * D * L, 2 * D), dk=at + 2 * D)
+    # and the same where they do meet
+    for kw in (dict(Hkv=1, dqs=st(*packed), dks=st(packed[0], L * 10 * D, 10 * D), dk=at + 2 * 7 * D),
+               dict(Hq=4, Hkv=4, dqs=st(*side), dks=st(*side), dk=at + 2 * 3 * D), dict(Hq=4, Hkv=4, dqs=st(*side), dks=st(*side), dk=at + D),
+               dict(Hq=4, Hkv=2, dqs=st(2 * D * L, 4 * D * L, 2 * D), dks=st(2 * D * L, 4 * D * L, 2 * D), dk=at + 2 * 4 * D * L)):
+        assert rope_bwd(lib, **dict(dict(D=D, rot=D, L=L), **kw)) == INV
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="an accepted call would run on these addresses")
+def test_rope_overlap_of_gradients_is_exact(lib):
+    """Random layouts of two gradients with common strides, whole rows apart: refused exactly where an element belongs to both."""
+    rng = np.random.default_rng(9)
+    D, seen = 64, {True: 0, False: 0}
+    for _ in range(4000):
+        B, L, Hq, Hkv = (int(rng.integers(1, 4)) for _ in range(4))
+        sizes, s, span = {0: B, 1: max(Hq, Hkv), 2: L}, [0, 0, 0], D
+        for i in rng.permutation(3):  # each stride past what the smaller ones span
+            s[i] = span + 8 * int(rng.integers(0, 30))
+            span += (sizes[i] - 1) * s[i]
+        at = A[9] + 2 * D * int(rng.integers(-span // D, span // D + 1))
+        meet = bool(rows_of(A[9], B, Hq, L, D, s) & rows_of(at, B, Hkv, L, D, s))
+        got = rope_bwd(lib, B=B, Hq=Hq, Hkv=Hkv, L=L, D=D, rot=D, dqs=st(*s), dks=st(*s), dk=at)
+        assert (got == INV) == meet, (B, Hq, Hkv, L, s, at - A[9], meet)
+        seen[meet] += 1
+    assert min(seen.values()) > 500

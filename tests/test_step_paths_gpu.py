@@ -177,6 +177,28 @@ def test_rope_unturned_elements_are_their_own(D, rot, interleaved, value):
                 assert g[:, :, at, rot + at].isnan().all()
 
 
+@pytest.mark.parametrize("layout", ["one KV head", "side by side", "heads outermost"])
+def test_rope_backward_into_any_packed_gradient(layout):
+    """One array for the gradients of q, k (and v, left as it was), in other orders than heads one after the other: the same
+    bits as into arrays of their own."""
+    B, L, Hq, Hkv, D = 2, 45, 4, 1 if layout == "one KV head" else 4, 64
+    c = ops.rope_case(54, B, L, Hq, Hkv, D, D, 1, BF, True, False, False)
+    want = ops.run_rope_bwd(c)
+    if layout == "one KV head":
+        packed = torch.full((B, L, Hq + 2, D), 7.0, dtype=BF, device="cuda")
+        dq, dk, rest = packed[:, :, :Hq].transpose(1, 2), packed[:, :, Hq].unsqueeze(1), packed[:, :, Hq + 1]
+    elif layout == "side by side":
+        packed = torch.full((B, L, Hq, 3, D), 7.0, dtype=BF, device="cuda")
+        dq, dk, rest = (packed[:, :, :, i].transpose(1, 2) for i in range(3))
+    else:
+        packed = torch.full((B, Hq, 2, L, D), 7.0, dtype=BF, device="cuda")
+        dq, dk, rest = packed[:, :, 0], packed[:, :, 1], None
+    gbattn.attn_qk_norm_rope_bwd(c["q"], c["k"], want[0], want[1], c["pos"], c["freq"], dq, dk, c["qw"], c["kw"], want[4].clone(), want[5].clone(),
+                                 gbattn.qk_norm_rope_workspace(c["q"], c["k"]), eps=c["eps"])
+    ok()
+    assert torch.equal(dq, want[2]) and torch.equal(dk, want[3]) and (rest is None or bool((rest == 7).all()))
+
+
 # --- verification -----------------------------------------------------------------
 
 
