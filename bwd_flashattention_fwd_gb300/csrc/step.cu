@@ -136,6 +136,13 @@ int rope_by_d(const RopeParams& p, bool interleaved, bool bwd, int num_sms, cuda
   }
 }
 
+// Whether a paged cache of these (positive) sizes is served.
+bool paged_sizes(int B, int Hkv, int page_size, int per_seq) {
+  // a page's rows are found by shifts, and hold a multiple of four exponents
+  if (page_size < 8 || page_size > 4096 || (page_size & (page_size - 1)) != 0) return false;
+  return static_cast<long long>(per_seq) * page_size <= kPagedMaxTokens && B <= kPagedMaxB && static_cast<long long>(B) * Hkv <= 65535;
+}
+
 // Sizes, types and alignment of a paged cache.
 attn_status_t check_paged(const void* k, const void* v, const int8_t* ke, const int8_t* ve, const int32_t* table, int B,
                           int Hkv, int n_pages, int page_size, int per_seq, int D, attn_dtype_t dtype) {
@@ -144,11 +151,7 @@ attn_status_t check_paged(const void* k, const void* v, const int8_t* ke, const 
   if (B < 1 || Hkv < 1 || n_pages < 1 || page_size < 1 || per_seq < 1) return ATTN_ERR_INVALID_ARG;
   if (dtype != ATTN_DTYPE_FP16 && dtype != ATTN_DTYPE_BF16) return ATTN_ERR_INVALID_ARG;
   if (!supported_d(D)) return ATTN_ERR_UNSUPPORTED;
-  // a page's rows are found by shifts, and hold a multiple of four exponents
-  if (page_size < 8 || page_size > 4096 || (page_size & (page_size - 1)) != 0) return ATTN_ERR_UNSUPPORTED;
-  if (static_cast<long long>(per_seq) * page_size > kPagedMaxTokens) return ATTN_ERR_UNSUPPORTED;
-  if (B > kPagedMaxB || static_cast<long long>(B) * Hkv > 65535) return ATTN_ERR_UNSUPPORTED;
-  return ATTN_OK;
+  return paged_sizes(B, Hkv, page_size, per_seq) ? ATTN_OK : ATTN_ERR_UNSUPPORTED;
 }
 
 PagedCache paged_cache(const void* k, const void* v, const int8_t* ke, const int8_t* ve, const int32_t* table, int Hkv,
@@ -207,9 +210,9 @@ struct Read {
 
 attn_status_t check_paged_attn(int B, int Hq, int Hkv, int T, int page_size, int per_seq, int D) {
   if (B < 1 || Hq < 1 || Hkv < 1 || T < 1 || page_size < 1 || per_seq < 1 || Hq % Hkv != 0) return ATTN_ERR_INVALID_ARG;
-  if (!supported_d(D) || B > kPagedMaxB) return ATTN_ERR_UNSUPPORTED;
+  if (!supported_d(D) || !paged_sizes(B, Hkv, page_size, per_seq)) return ATTN_ERR_UNSUPPORTED;
   const long long rows = static_cast<long long>(Hq / Hkv) * T, room = static_cast<long long>(per_seq) * page_size;
-  if (rows > kPagedMaxRows || room > kPagedMaxTokens) return ATTN_ERR_UNSUPPORTED;
+  if (rows > kPagedMaxRows) return ATTN_ERR_UNSUPPORTED;
   // the units of work of the whole call are ints (steps of 32 keys at least)
   const long long blocks = (rows + paged_rows(static_cast<int>(rows), D) - 1) / paged_rows(static_cast<int>(rows), D);
   if ((room / 32 + 4) * B * Hkv * blocks > 0x7fff0000LL) return ATTN_ERR_UNSUPPORTED;

@@ -322,3 +322,14 @@ def test_rope_overlap_of_gradients_is_exact(lib):
         assert (got == INV) == meet, (B, Hq, Hkv, L, s, at - A[9], meet)
         seen[meet] += 1
     assert min(seen.values()) > 500
+
+
+def test_paged_workspace_is_0_for_what_the_call_refuses(lib):
+    """A size that attn_fwd_paged refuses has no workspace (and one that it takes has)."""
+    for kw in (dict(page=4), dict(page=24), dict(page=8192), dict(page=7), dict(B=1025), dict(B=1000, Hkv=66, Hq=66), dict(per_seq=(1 << 26) + 1)):
+        a = dict(dict(B=2, Hq=8, Hkv=2, T=1, page=16, per_seq=5, D=128), **kw)
+        assert paged(lib, **kw) == UNS, kw
+        assert lib.attn_paged_workspace_bytes(a["B"], a["Hq"], a["Hkv"], a["T"], a["page"], a["per_seq"], a["D"]) == 0, kw
+    for kw in (dict(page=8), dict(page=4096), dict(B=1024), dict(B=1000, Hkv=65, Hq=65), dict(per_seq=1 << 26)):
+        a = dict(dict(B=2, Hq=8, Hkv=2, T=1, page=16, per_seq=5, D=128), **kw)
+        assert lib.attn_paged_workspace_bytes(a["B"], a["Hq"], a["Hkv"], a["T"], a["page"], a["per_seq"], a["D"]) > 0, kw
