@@ -293,4 +293,9 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, n
 
 }  // namespace
 
-extern "C" __attribute__((visibility("default"))) PyObject* PyInit__binding() { return PyModule_Create(&module); }
+// (what the wrapper compares with the Python and torch that it runs under)
+extern "C" __attribute__((visibility("default"))) PyObject* PyInit__binding() {
+  PyObject* m = PyModule_Create(&module);
+  if (m && PyModule_AddStringConstant(m, "built_for", GBATTN_BUILT_FOR) < 0) Py_CLEAR(m);
+  return m;
+}

@@ -13,6 +13,8 @@ import os
 
 import torch
 
+from .build import built_for
+
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libgbattn.so")
 # the debug build: the same kernels with index checks (GBATTN_DEBUG_CHECKS)
@@ -131,23 +133,30 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
     lib.attn_wait_probe.restype = ci
     lib.attn_status_string.argtypes = [ci]
     lib.attn_status_string.restype = ctypes.c_char_p
-    try:
-        from . import _binding
-    except ImportError as e:
-        raise RuntimeError(f"{os.path.join(_HERE, '_binding.so')} is not built for this Python and torch ({e}); run "
-                           "bwd_flashattention_fwd_gb300.build.build() (or __graft_entry__.build())") from e
-    _binding.init({n: ctypes.cast(getattr(lib, n), vp).value for n in
-                   ("attn_qk_norm_rope", "attn_qk_norm_rope_bwd", "attn_paged_write", "attn_paged_read", "attn_fwd_paged",
-                    "attn_draft_verify")})
-    _lib, _fast = lib, _binding
+    _lib, _fast = lib, None
     return lib
 
 
 def _fast_path():
     """The compiled fast path: each of its functions checks its tensors and makes
     one call, or returns -1 where one is not what the call takes; the wrapper's
-    own checks then name it and raise."""
-    load_library()
+    own checks then name it and raise.  Only the calls around attention need it."""
+    global _fast
+    lib = load_library()
+    if _fast is None:
+        try:
+            from . import _binding
+            its = getattr(_binding, "built_for", "another source")
+            why = "" if its == built_for() else f"it was built for {its}"
+        except ImportError as e:
+            why = str(e)
+        if why:
+            raise RuntimeError(f"the extension module _binding does not fit {built_for()} ({why}); run "
+                               "bwd_flashattention_fwd_gb300.build.build() (or __graft_entry__.build())")
+        _binding.init({n: ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in
+                       ("attn_qk_norm_rope", "attn_qk_norm_rope_bwd", "attn_paged_write", "attn_paged_read", "attn_fwd_paged",
+                        "attn_draft_verify")})
+        _fast = _binding
     return _fast
 
 

@@ -333,3 +333,81 @@ def test_paged_workspace_is_0_for_what_the_call_refuses(lib):
     for kw in (dict(page=8), dict(page=4096), dict(B=1024), dict(B=1000, Hkv=65, Hq=65), dict(per_seq=1 << 26)):
         a = dict(dict(B=2, Hq=8, Hkv=2, T=1, page=16, per_seq=5, D=128), **kw)
         assert lib.attn_paged_workspace_bytes(a["B"], a["Hq"], a["Hkv"], a["T"], a["page"], a["per_seq"], a["D"]) > 0, kw
+
+
+# --- the compiled fast path of the binding --------------------------------------
+
+WITHOUT = r"""
+import ctypes, sys, types
+import torch
+import bwd_flashattention_fwd_gb300 as package
+from bwd_flashattention_fwd_gb300 import gbattn
+
+name = "bwd_flashattention_fwd_gb300._binding"
+x = torch.zeros(1, 2, 8, 64, dtype=torch.bfloat16)
+for module in (None, types.SimpleNamespace(), types.SimpleNamespace(built_for="Python 3.1, torch 0.1")):
+    sys.modules[name] = module
+    if module is not None:
+        package._binding = module
+    lib = gbattn.load_library()
+    # every other call works without it
+    assert lib.attn_fwd(0, 0, 0, 0, 0, 1, 1, 1, 1, 1, 64, ctypes.c_float(1.0), 0, 1, 0) == gbattn.ATTN_ERR_INVALID_ARG
+    assert gbattn.status_string(gbattn.ATTN_OK) and gbattn.attn_paged_workspace_bytes(1, 1, 1, 1, 16, 1, 64) > 0
+    for call in (lambda: gbattn.attn_qk_norm_rope(x, x, x, x, x, x), lambda: gbattn.attn_paged_read(x, x, x, x, x, x)):
+        try:
+            call()
+        except RuntimeError as e:
+            assert "build" in str(e) and "torch " + torch.__version__ in str(e), e
+        else:
+            raise SystemExit("no error")
+print("older calls work")
+"""
+
+
+def test_library_works_without_the_fast_path(lib):
+    """No extension module, one of another source, one built for another Python and torch: the calls that need it say so,
+    the others run."""
+    import os
+    import subprocess
+    import sys
+
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    run = subprocess.run([sys.executable, "-c", WITHOUT], cwd=root, env=dict(os.environ, PYTHONPATH=root), capture_output=True, text=True, timeout=300)
+    assert run.returncode == 0 and "older calls work" in run.stdout, run.stdout + run.stderr
+
+
+def test_extension_module_is_built_for_this_python_and_torch(lib, tmp_path, monkeypatch):
+    """A change of Python or torch makes the extension module stale, and nothing else; the debug build brings it as well."""
+    import sysconfig
+
+    from bwd_flashattention_fwd_gb300 import _binding
+
+    assert _binding.built_for == build.built_for() and torch.__version__ in build.built_for()
+    assert build.BINDING.endswith(sysconfig.get_config_var("EXT_SUFFIX"))
+    assert build._stale() == (False, False)
+    ran = []
+
+    def run(cmd):
+        ran.append(cmd)
+        (tmp_path / cmd[cmd.index("-o") + 1].rsplit("/", 1)[-1]).write_text("")
+        return ""
+
+    monkeypatch.setattr(build, "_run", run)
+    for name in ("BINDING", "BINDING_STAMP"):
+        path = tmp_path / getattr(build, name).rsplit("/", 1)[-1]
+        path.write_text(build._read(build.BINDING_STAMP) if name == "BINDING_STAMP" else "")
+        monkeypatch.setattr(build, name, str(path))
+    assert build._stale() == (False, False)
+    build.build()
+    assert ran == []
+    monkeypatch.setattr(build, "built_for", lambda: "Python 3.99, torch 9.9")
+    assert build._stale() == (False, True)
+    build.build()
+    assert len(ran) == 1 and any(a.endswith("binding.cpp") for a in ran[0])
+    assert '-DGBATTN_BUILT_FOR="Python 3.99, torch 9.9"' in ran[0] and build._stale() == (False, False)
+    (tmp_path / "libgbattn_debug.so").write_text("")  # (a debug library that is there, without the module)
+    monkeypatch.setattr(build, "DEBUG_LIB", str(tmp_path / "libgbattn_debug.so"))
+    (tmp_path / build.BINDING.rsplit("/", 1)[-1]).unlink()
+    assert build._stale(debug=True) == (False, True)
+    build.build(debug=True)
+    assert len(ran) == 2 and build._stale(debug=True) == (False, False)
