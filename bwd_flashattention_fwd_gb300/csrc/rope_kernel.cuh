@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(kRopeThreads, RopeGeom<D, BWD>::PER_SM) rope_k
   const int k_lo = p.x[1].H * part / parts, k_n = p.x[1].H * (part + 1) / parts - k_lo;
   // bytes between heads
   const uint32_t x_head[2] = {static_cast<uint32_t>(p.x[0].sh * 2), static_cast<uint32_t>(p.x[1].sh * 2)};
-  const uint32_t d_head[2] = {static_cast<uint32_t>(p.dx[0].sh * 2), static_cast<uint32_t>(p.dx[1].sh * 2)}, y_head = p.L * (D * 2);
+  const uint32_t d_head[2] = {static_cast<uint32_t>(p.dx[0].sh * 2), static_cast<uint32_t>(p.dx[1].sh * 2)}, y_head = static_cast<uint32_t>(p.L) * (D * 2);
   const int chunks = max(1, (t_end - t_first + Gm::TOKENS - 1) / Gm::TOKENS), each = (t_end - t_first + chunks - 1) / chunks;  // (equal ones)
 #pragma unroll 1
   for (int t0 = t_first; t0 < t_end; t0 += each) {
