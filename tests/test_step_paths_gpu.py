@@ -49,6 +49,121 @@ def roomy(gen, B, page, lens, room, order="random"):
     return table, total + 1
 
 
+def lengths(kind, B, top):
+    if kind == "ragged":  # from nothing to `top`
+        return [(i * 97 + 31) * top // 1009 % (top + 1) for i in range(B)]
+    if kind == "short":  # long ones with runs of short and empty ones between them: pieces that hold whole heads
+        return [top if i % 7 == 0 else (0, 1, 5, 70)[i % 4] for i in range(B)]
+    return [top - 13 * i for i in range(B)]
+
+
+# --- the paged attention's pieces ---------------------------------------------
+
+
+PIECES = [
+    # B, Hq, Hkv, T, D, page, top, lengths, dtype: with room for 40 times top, so pieces; the join's warps a row and the blocks of rows
+    (16, 16, 4, 1, 64, 16, 400, "ragged", BF),    # 4 rows; 1 warp
+    (16, 16, 4, 1, 128, 16, 400, "ragged", HF),   # 4 rows; 1 warp
+    (16, 12, 4, 4, 96, 8, 300, "ragged", BF),     # 12 rows; 1 warp
+    (16, 16, 4, 3, 128, 32, 300, "ragged", BF),   # 12 rows; 1 warp
+    (16, 32, 4, 4, 128, 16, 300, "ragged", BF),   # 32 rows; 1 warp
+    (16, 32, 4, 4, 64, 16, 300, "ragged", HF),    # 32 rows; 1 warp
+    (48, 16, 8, 1, 128, 16, 500, "short", BF),    # several heads in a piece
+    (48, 8, 8, 1, 64, 64, 500, "short", HF),
+    (40, 24, 8, 4, 96, 16, 300, "short", BF),     # the same with 12 rows
+    (30, 20, 10, 1, 256, 32, 300, "short", BF),
+    (3, 32, 4, 5, 64, 16, 700, "near", BF),       # 40 rows in 2 blocks; 1 warp
+    (2, 16, 2, 16, 128, 16, 500, "near", BF),     # 128 rows in 4 blocks; 1 warp
+    (2, 12, 2, 11, 96, 16, 500, "near", HF),      # 66 rows in 3 blocks; 8 warps from here on
+    (5, 16, 2, 3, 256, 32, 300, "near", BF),      # 24 rows in 2 blocks of 16
+    (2, 16, 2, 8, 256, 8, 300, "near", HF),       # 64 rows in 4 blocks of 16
+    (2, 8, 2, 1, 256, 64, 2500, "near", HF),      # few heads
+    (1, 32, 1, 1, 128, 16, 2500, "near", BF),     # one head of 32 rows
+    (1, 10, 1, 1, 64, 16, 3000, "near", BF),
+]
+
+
+@pytest.mark.parametrize("q8", [False, True])
+@pytest.mark.parametrize("case", PIECES)
+def test_pieces(case, q8):
+    B, Hq, Hkv, T, D, page, top, kind, dt = case
+    gen = torch.Generator().manual_seed(41)
+    lens = lengths(kind, B, top)
+    table, n_pages = roomy(gen, B, page, lens, 40 * top // page * page)
+    pool = make_pool(gen, n_pages, Hkv, page, D, dt, q8)
+    ops.stale(pool, table, page, lens)
+    q, scale = rand(gen, (B, Hq, T, D), dt), float(np.float32(1 / np.sqrt(D)))
+    got = run_paged(q, pool, table.cuda(), i32(lens), scale)
+    again = run_paged(q, pool, table.cuda(), i32(lens), scale)
+    ok()
+    assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])
+    ops.check_paged(q, pool, table[:, :-(-max(lens) // page)], page, lens, scale, got)
+
+
+@pytest.mark.parametrize("q8", [False, True])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_room_within_each_elements_bound(D, q8):
+    """The same tokens in a small table (a cluster per head) and in a large one (pieces and a join): both within their
+    elements' bounds."""
+    gen = torch.Generator().manual_seed(42)
+    B, Hq, Hkv, page, lens = 2, 8, 2, 16, [300, 7]
+    table, n_pages = roomy(gen, B, page, lens, 304)
+    wide = torch.full((B, 20000), -1, dtype=torch.int32)
+    wide[:, :19] = table
+    pool, q = make_pool(gen, n_pages, Hkv, page, D, BF, q8), rand(gen, (B, Hq, 1, D), BF)
+    for t in (table, wide):
+        got = run_paged(q, pool, t.cuda(), i32(lens), 0.09)
+        ok()
+        ops.check_paged(q, pool, table, page, lens, 0.09, got)
+
+
+def test_cached_prefix_within_each_elements_bound():
+    """One new token over pages, and by attn_fwd_ex over the same pages read back: both within the elements' bounds of the
+    same definition (attn_fwd_ex rounds P to bf16, over quantised pages attn_fwd_paged to fp16)."""
+    gen = torch.Generator().manual_seed(43)
+    B, Hq, Hkv, D, page, per_seq, n = 2, 8, 2, 128, 16, 12, 180
+    pool = make_pool(gen, B * per_seq, Hkv, page, D, BF, True)
+    table = torch.randperm(B * per_seq, generator=gen).view(B, per_seq).to(torch.int32)
+    q = rand(gen, (B, Hq, 1, D), BF)
+    o, lse = run_paged(q, pool, table.cuda(), i32([n, n]), 0.09)
+    k, v = (torch.zeros(B, Hkv, per_seq * page, D, dtype=BF, device="cuda")[:, :, :n] for _ in range(2))
+    gbattn.attn_paged_read(pool[0], pool[1], table.cuda(), i32([n, n]), k, v, k_exp=pool[2], v_exp=pool[3])
+    o2, lse2 = torch.empty_like(o), torch.empty_like(lse)
+    gbattn.attn_fwd_ex(q, k, v, o2, lse2, 0.09, True)
+    ok()
+    ops.check_paged(q, pool, table, page, [n, n], 0.09, (o, lse))
+    ref, lref, mag = S.paged_attention(to_f64(q), *(pool64(t) for t in pool[:2]), *(t.cpu().numpy() for t in pool[2:]), table.numpy(), page, [n, n], 0.09)
+    # test_parity_gpu.py's roundings for one row: P's 2^-8, and O's
+    within(to_f64(o2), ref, (2.0 ** -8 + 2.0 ** -12) * mag + U[BF] * np.abs(ref), "O of attn_fwd_ex")
+    within(to_f64(lse2), lref, 1e-4, "lse of attn_fwd_ex")
+
+
+@pytest.mark.parametrize("q8", [False, True])
+def test_two_streams_over_pieces(q8):
+    """Two calls at once that both need their workspaces, with different queries: the same bits as alone."""
+    gen = torch.Generator().manual_seed(44)
+    B, Hq, Hkv, D, page = 12, 16, 4, 128, 16
+    lens = [2000 - 150 * i for i in range(B)]
+    table, n_pages = roomy(gen, B, page, lens, 20000)
+    pool, table = make_pool(gen, n_pages, Hkv, page, D, BF, q8), table.cuda()
+    q = [rand(gen, (B, Hq, 1, D), BF) for _ in range(2)]
+    ws = [gbattn.paged_workspace(q[0], pool[0], table) for _ in range(2)]
+    want = [run_paged(x, pool, table, i32(lens), 0.1, w) for x, w in zip(q, ws)]
+    ok()
+    assert not torch.equal(want[0][0], want[1][0])
+    streams, n = [torch.cuda.Stream() for _ in range(2)], i32(lens)
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                got[i].append(run_paged(q[i], pool, table, n, 0.1, ws[i]))
+    ok()
+    for runs, w in zip(got, want):
+        for a in runs:
+            assert torch.equal(a[0], w[0]) and torch.equal(a[1], w[1])
+
+
 # --- exponents of quantised values at both ends of their range ------------------
 
 
@@ -115,9 +230,9 @@ def test_exponents_far_apart(split, high, D):
 def test_exponents_of_every_size(D):
     """Sequences whose values' exponents run through the whole range, with scores that favour the small ones."""
     gen = torch.Generator().manual_seed(47)
-    page, lens = 16, [500, 400, 1]
-    for room in (512, 40000):
-        table, n_pages = roomy(gen, 3, page, lens, room, order="sorted")
+    page = 16
+    for room, lens in ((512, [500, 400, 1]), (40000, [500, 400, 1]), (40000, lengths("ragged", 40, 300))):  # a cluster; 8 and 1 warps in the join
+        table, n_pages = roomy(gen, len(lens), page, lens, room, order="sorted")
         pool = make_pool(gen, n_pages, 2, page, D, BF, True, std=0.3)
         k, v, ke, ve = pool
         ve.copy_(torch.randint(-64, 120, ve.shape, generator=gen).to(torch.int8))
@@ -128,14 +243,49 @@ def test_exponents_of_every_size(D):
         k64[..., 0] = first
         c, e = S.quantise(k64)
         k.copy_(torch.from_numpy(c).float().to(F8)), ke.copy_(torch.from_numpy(e).to(torch.int8))
-        q = rand(gen, (3, 4, 1, D), BF, 0.3)
+        q = rand(gen, (len(lens), 4, 1, D), BF, 0.3)
         q[..., 0] = 80
         got = run_paged(q, pool, table.cuda(), i32(lens), 0.1)
         ok()
         check_wide(q, pool, table[:, :32], page, lens, 0.1, got)
 
 
-# --- the rotation: elements that are not turned --------------------
+# --- the rotation: long prompts, elements that are not turned --------------------
+
+
+LONG = [
+    # B, L, Hq, Hkv, D, rot, axes, dtype, norm, interleaved, packed
+    (1, 7400, 1, 1, 256, 256, 2, BF, True, False, False),    # two tables of sines in a CTA
+    (2, 11000, 2, 1, 256, 64, 1, HF, False, True, True),     # three CTAs after one another, two tables in each
+    (1, 14700, 2, 1, 128, 128, 1, BF, True, False, True),    # three CTAs after one another
+    (1, 44000, 1, 1, 128, 128, 1, BF, True, False, False),   # both
+    (1, 15001, 1, 2, 96, 48, 3, BF, True, True, True),
+]
+
+
+@pytest.mark.parametrize("case", LONG)
+def test_rope_long(case):
+    c = ops.rope_case(51, *case)
+    got = ops.run_rope(c)
+    ok()
+    ops.check_rope(c, got)
+
+
+LONG_BWD = [
+    (1, 5000, 1, 1, 256, 256, 2, BF, True, False, False),    # two tables of sines in a CTA
+    (1, 9900, 2, 1, 128, 128, 1, BF, True, False, True),
+    (1, 15001, 1, 2, 96, 48, 3, HF, True, True, True),
+    (2, 10000, 1, 1, 64, 64, 1, BF, True, False, True),
+    (1, 12000, 1, 1, 256, 64, 1, BF, False, True, False),    # three tables
+]
+
+
+@pytest.mark.parametrize("case", LONG_BWD)
+def test_rope_backward_long(case):
+    c = ops.rope_case(52, *case)
+    got = ops.run_rope_bwd(c)
+    ok()
+    ops.check_rope_bwd(c, got)
 
 
 @pytest.mark.parametrize("value", [float("inf"), float("-inf"), float("nan")])
@@ -251,3 +401,80 @@ def test_verify_sums_past_64_bits(V):
     total = min((V - 1) * one, most)
     least = [(int(float(x) * 2.0 ** 64) * total >> 64) // one for x in r]
     assert accept.tolist() == [0] * 4 and token.tolist() == [x if x < 5 else x + 1 for x in least]
+
+
+# --- streams ------------------------------------------------------------------------
+
+
+def stream_calls():
+    """Six calls as (inputs whose values matter, outputs, the call)."""
+    gen = torch.Generator().manual_seed(61)
+    c = ops.rope_case(62, 2, 40, 4, 2, 64, 64, 1, BF, True, False, True)
+    q, k = c["q"].contiguous(), c["k"].contiguous()
+    qo, ko, dq, dk = torch.empty_like(q), torch.empty_like(k), torch.empty_like(q), torch.empty_like(k)
+    gq, gk = rand(gen, tuple(q.shape), BF), rand(gen, tuple(k.shape), BF)
+    dqw, dkw, ws = torch.empty(64, device="cuda"), torch.empty(64, device="cuda"), gbattn.qk_norm_rope_workspace(q, k)
+    tail = (c["pos"], c["freq"])
+    yield "rope", (q, k), (qo, ko), lambda **s: gbattn.attn_qk_norm_rope(q, k, qo, ko, *tail, c["qw"], c["kw"], **s)
+    yield "rope_bwd", (gq, gk), (dq, dk, dqw, dkw), lambda **s: gbattn.attn_qk_norm_rope_bwd(q, k, gq, gk, *tail, dq, dk, c["qw"], c["kw"], dqw, dkw,
+                                                                                            ws, **s)
+    pk, pv, _, _ = make_pool(gen, 40, 2, 16, 64, BF, False)
+    table, n = torch.randperm(40, generator=gen).view(2, 20).to(torch.int32).cuda(), i32([300, 200])
+    kn, vn, kp, vp, after = rand(gen, (2, 2, 5, 64), BF), rand(gen, (2, 2, 5, 64), BF), torch.zeros_like(pk), torch.zeros_like(pv), i32([0, 0])
+    yield "write", (kn, vn), (kp, vp, after), lambda **s: gbattn.attn_paged_write(kn, vn, kp, vp, table, n, after, **s)
+    kr, vr = torch.zeros(2, 2, 320, 64, dtype=BF, device="cuda"), torch.zeros(2, 2, 320, 64, dtype=BF, device="cuda")
+    yield "read", (pk, pv), (kr, vr), lambda **s: gbattn.attn_paged_read(pk, pv, table, n, kr, vr, **s)
+    x = rand(gen, (2, 8, 1, 64), BF)
+    o, lse, ws2 = torch.empty_like(x), torch.empty(2, 8, 1, device="cuda"), gbattn.paged_workspace(x, pk, table)
+    yield "paged", (x,), (o, lse), lambda **s: gbattn.attn_fwd_paged(x, pk, pv, table, n, o, lse, ws2, 0.3, **s)
+    target, draft = (torch.softmax(torch.randn(2, t, 500, generator=gen), -1).cuda() for t in (4, 3))
+    tokens, u, r, acc, tok = i32([[1, 2, 3]] * 2), torch.rand(2, 3, generator=gen).cuda(), torch.rand(2, generator=gen).cuda(), i32([0, 0]), i32([0, 0])
+    yield "verify", (target, u), (acc, tok), lambda **s: gbattn.attn_draft_verify(target, draft, tokens, u, r, acc, tok, **s)
+
+
+def test_calls_run_in_their_streams_order():
+    """Each call's inputs hold wrong values until a copy on its stream, behind long products, puts the right ones there: a
+    call that ran on another stream would read the wrong ones.  With a stream given, another one is current."""
+    st, other = torch.cuda.Stream(), torch.cuda.Stream()
+    for name, inputs, outputs, call in stream_calls():
+        call()
+        ok()
+        want, right = [t.clone() for t in outputs], [t.clone() for t in inputs]
+        wrong = [torch.zeros_like(t) if t.dtype != torch.float32 else torch.ones_like(t) for t in inputs]
+        for t, w in zip(inputs, wrong):
+            t.copy_(w)
+        call()
+        ok()
+        assert not all(torch.equal(a, b) for a, b in zip(outputs, want)), name  # (what reading the wrong ones would give)
+        for how in (st, st.cuda_stream, None):
+            for t, w in zip(inputs, wrong):
+                t.copy_(w)
+            for t in outputs:
+                t.zero_()
+            torch.cuda.synchronize()
+            with torch.cuda.stream(st):
+                big = torch.randn(3000, 3000, device="cuda")
+                for _ in range(20):
+                    big = big @ big * 1e-4
+                for t, w in zip(inputs, right):
+                    t.copy_(w)
+                if how is None:
+                    call()
+            if how is not None:
+                with torch.cuda.stream(other):
+                    call(stream=how)
+            torch.cuda.synchronize()
+            for a, b in zip(outputs, want):
+                assert torch.equal(a, b), (name, how)
+    ok()
+
+
+@pytest.mark.skipif(os.environ.get("GBATTN_DEBUG") == "1", reason="this is the child")
+def test_no_index_check_fires_on_these_paths():
+    """The pieces, the long prompts and the extreme exponents in the debug build, whose kernels check their indices."""
+    from bwd_flashattention_fwd_gb300 import build
+
+    build.build(debug=True)
+    run = subprocess.run([sys.executable, "-m", "pytest", "-q", "-x", "-m", "gpu", "-k", "pieces or long or every_size or unturned or verify",
+                          os.path.abspath(__file__)], cwd=ROOT, env=dict(os.environ, GBATTN_DEBUG="1"), capture_output=True, text=True, timeout=900)
+    assert run.returncode == 0, run.stdout[-3000:] + run.stderr[-1000:]
