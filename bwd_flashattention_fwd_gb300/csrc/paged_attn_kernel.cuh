@@ -8,13 +8,16 @@
 // with running m and l per warp, joined over the warps of a CTA and then over
 // the CTAs that share a KV head.
 //
-// Bound by HBM: every key and value is read once, 4 G T products an element.
+// Bound by HBM: every key and value is read once for each block of rows (32 at
+// most, 16 at D = 256), 4 G T products an element.  (The blocks of a head follow one another in the order of
+// the work: with two of them at D = 256 the second finds the keys in L2, 134.3 MB read for 134.2 of
+// keys; with four of 32 rows at D = 128, 4 x 8192 keys, memory gives them 2.9 times.)
 // A KV head has few rows, so the products are taken transposed, S^T = K Q^T and
 // O^T = V^T P^T, with the keys (or the columns of V) on the 16 rows of a
 // warp-level matrix instruction and the rows on its 8 columns: eight rows fill
-// it.  (tcgen05's smallest tile has 64 rows of which 4 to 8 would be used, and
-// it takes no 8-bit operand beside a 16-bit one, so quantised tiles would have
-// to go through shared memory twice more.)  Its C fragment holds keys down a
+// it.  (tcgen05 would take 64 or 128 keys on its rows the same way, widened codes by way of tensor
+// memory.  With 8 rows that has little to win, the tensor pipe being 8 to 16% busy; for
+// more rows over quantised pages it was not tried.)  Its C fragment holds keys down a
 // column of lanes and its B fragment along a row: movmatrix turns one into the
 // other without shared memory.
 //
@@ -40,10 +43,10 @@
 // fp16 P: times 2^15, so that what counts as nothing is 2^-40 of the row's
 // largest (2^-25 otherwise, and 10^5 such keys add up; beside exponents above 117 2^-37).
 //
-// Past a few rows, or with codes to widen, the instructions of a tile bound it (64
-// to 55% of the issue slots): scores and sums in packed pairs, masks only in tiles that need
+// Past a few rows, or with codes to widen, the instructions of a tile bound it (46
+// to 62% of the issue slots): scores and sums in packed pairs, masks only in tiles that need
 // one, the rows' references moved only by scores well above them, offsets of copies in the
-// instructions: 32 rows over 4 sequences of 65536 quantised keys 150 us (166 without), D = 64 105 (120).
+// instructions: 32 rows over 4 sequences of 65536 quantised keys 150 us (166 without), D = 64 102 (120).
 #pragma once
 
 #include <cfloat>
@@ -54,8 +57,8 @@
 namespace gbattn {
 
 // Warps: as many as hide the latency of a tile's chain (look-up, copy, products,
-// exponentials), which registers limit: 8 rows over quantised pages take 126
-// registers, 16 warps on an SM (8192 keys, 4 sequences: 16.3 us; 8 warps of 32-key tiles 3.5 more).
+// exponentials), which registers limit: 8 rows over quantised pages take 128
+// registers, 16 warps on an SM (8192 keys, 4 sequences: 16.4 us; 8 warps of 32-key tiles 3.5 more).
 template <int D, bool Q8, int NT>
 struct PagedGeom {
   static constexpr int NW = D == 256 && !Q8 ? 2 : Q8 && D * NT <= 128 ? 8 : 4;  // warps of a CTA
@@ -802,7 +805,7 @@ __global__ void __launch_bounds__(kPagedJoinThreads) attn_paged_join_kernel(cons
       float2 ml = make_float2(-INFINITY, 0.f);
       if (lane < k) ml = reinterpret_cast<const float2*>(p.part_ml)[at(i0 + lane)];
       // The first rows are on their way while the weights are worked out, the others loaded so many at a time, all before the
-      // first is used (one head of 24137 quantised keys, 12 rows: 11.4 us; 21.6 where the sums and loads took turns).
+      // first is used (one head of 24137 quantised keys, 12 rows: 11.7 us; 21.6 where the sums and loads took turns).
       constexpr int AHEAD = 6, AT_ONCE = WARPS > 1 ? 13 : 8;
       float4 early[AHEAD][Q];
 #pragma unroll

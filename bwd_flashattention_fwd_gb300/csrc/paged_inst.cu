@@ -19,9 +19,10 @@ constexpr int kD = GBATTN_HEAD_DIM;
 // takes kPagedAlone us; where clusters fill the GPU, their steps take what the
 // memory gives (6.6 TB/s), with rooms half full on average half as long.  A
 // cluster is taken where the longest possible sequence would so be late by
-// kPagedLate us at most (32 heads of 8192 keys 25.8 us, by pieces 27.3, quantised 16.3 and 19.0; 1000 keys
-// of one sequence 5.5 and 6.2, 4000 keys 8.7 and 8.3; D = 64, 128 heads of 250 to
-// 2000 keys 13.3 and 13.1, of 125 to 1000 7.5 and 8.3; 1024 to 8192 keys quantised 38.0 and 31.6).
+// kPagedLate us at most (32 heads of 8192 keys 25.9 us, by pieces 27.4, quantised 16.4 and 19.0; 1000 keys
+// of one sequence 5.4 and 6.0, 4000 keys 8.7 and 8.3; D = 64, 128 heads of 250 to
+// 2000 keys 13.3 and 13.1, of 125 to 1000 7.5 and 8.3; 1024 to 8192 keys quantised 28.2 and 22.6).
+// The longest possible sequence is the table's room: 1000 keys in room for 32768 go by pieces, 5.9 us for 5.2.
 // Past kPagedShort steps a single long sequence among short ones would be waited for too long.
 constexpr int kPagedShort = 32;
 constexpr float kPagedLate = 3.f;
@@ -78,7 +79,7 @@ int impl(const PagedAttnParams& p0, int num_sms, cudaStream_t stream) {
   const int r = launch_dependent(kern, dim3(p.n_groups), Gm::THREADS, smem, stream, p);
   if (r != kLaunchOk || p.n_groups == 1) return r;
   // a block's warps share a row's partial results where there are many, and few rows: past two blocks on an SM a warp
-  // per row is faster (7 x 8 heads of 8943 keys, D = 96, 12 rows: 27.9 us, 32.3)
+  // per row is faster (7 x 8 heads of 8943 quantised keys, D = 96, 12 rows: 30.6 us, 35.4)
   const long long tasks = static_cast<long long>(p.B) * p.c.Hkv * p.R;
   auto join = [&](auto kern_j, int per) {
     const long long blocks = (tasks + per - 1) / per, most = 8LL * kTreeMaxCtas;
