@@ -76,7 +76,7 @@ def _sources_mtime() -> float:
 def _run(cmd):
     r = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
     if r.returncode != 0:
-        raise RuntimeError("nvcc failed:\n" + " ".join(cmd) + "\n" + r.stdout)
+        raise RuntimeError(f"{os.path.basename(cmd[0])} failed:\n" + " ".join(cmd) + "\n" + r.stdout)
     return r.stdout
 
 
@@ -101,7 +101,9 @@ def _stale(debug: bool = False) -> tuple:
 
 def build(force: bool = False, verbose: bool = False, extra_flags=(), debug: bool = False) -> str:
     """Compile what is stale and return the path of libgbattn.so (with debug:
-    libgbattn_debug.so, the kernels' index checks compiled in)."""
+    libgbattn_debug.so, the kernels' index checks compiled in).  Where the
+    extension module cannot be compiled the libraries are there all the same
+    when this raises."""
     lib = DEBUG_LIB if debug else LIB
     libs, binding = (True, True) if force else _stale(debug)
     if not libs and not binding:
@@ -122,17 +124,18 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), debug: boo
             jobs.append([nvcc, *ARCH, *flags, "-c", os.path.join(CSRC, unit + ".cu"), "-o", objs[-1]])
         if not debug:
             jobs.append([nvcc, *ARCH, *flags, "-c", os.path.join(CSRC, "checks.cu"), "-o", checks_obj])
-    if binding:
-        jobs.append(_binding_cmd(tmp_binding))
-    with ThreadPoolExecutor(max_workers=len(jobs)) as ex:
+    with ThreadPoolExecutor(max_workers=len(jobs) + 1) as ex:
+        module = ex.submit(lambda: _run(_binding_cmd(tmp_binding))) if binding else None
         outs = list(ex.map(_run, jobs))
+        if libs:
+            for out, parts in ((lib, objs), *(() if debug else ((CHECKS_LIB, [checks_obj]),))):
+                _run([nvcc, *ARCH, "-shared", "-o", out + ".tmp", *parts])
+                os.replace(out + ".tmp", out)
+    if module:
+        outs.append(module.result())
     if verbose:
         for o in outs:
             sys.stdout.write(o)
-    if libs:
-        for out, parts in ((lib, objs), *(() if debug else ((CHECKS_LIB, [checks_obj]),))):
-            _run([nvcc, *ARCH, "-shared", "-o", out + ".tmp", *parts])
-            os.replace(out + ".tmp", out)
     if binding:
         os.replace(tmp_binding, BINDING)
         with open(BINDING_STAMP, "w") as f:

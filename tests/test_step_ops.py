@@ -411,3 +411,20 @@ def test_extension_module_is_built_for_this_python_and_torch(lib, tmp_path, monk
     assert build._stale(debug=True) == (False, True)
     build.build(debug=True)
     assert len(ran) == 2 and build._stale(debug=True) == (False, False)
+
+
+def test_libraries_are_built_where_the_extension_module_cannot_be(lib, tmp_path, monkeypatch):
+    """No compiler or headers for the extension module: the build says so, after it has linked the libraries."""
+    def run(cmd):
+        if any(a.endswith("binding.cpp") for a in cmd):
+            raise RuntimeError("no Python.h")
+        (tmp_path / cmd[cmd.index("-o") + 1].rsplit("/", 1)[-1]).write_text("")
+        return ""
+
+    monkeypatch.setattr(build, "_run", run)
+    for name in ("LIB", "CHECKS_LIB", "BINDING", "BINDING_STAMP"):
+        monkeypatch.setattr(build, name, str(tmp_path / getattr(build, name).rsplit("/", 1)[-1]))
+    with pytest.raises(RuntimeError, match="no Python.h"):
+        build.build()
+    assert (tmp_path / "libgbattn.so").exists() and (tmp_path / "libgbattn_checks.so").exists()
+    assert build._stale() == (False, True)
