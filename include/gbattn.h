@@ -388,7 +388,8 @@ attn_status_t attn_qk_norm_rope_bwd(const void* q, const void* k, const void* q_
  *   8 bits: e4m3 codes and int8 exponents k_exp, v_exp [n_pages,Hkv,page_size]:
  *     a row's values are code * 2^e, e the least exponent in -64 .. 120 with
  *     max |x| <= 448 * 2^e, codes rounded to nearest even.  A value that is
- *     not finite becomes NaN and does not count for e.
+ *     not finite becomes NaN and does not count for e.  (Rows written by other
+ *     means: any e in -64 .. 120.)
  * Every page that a call writes belongs to one sequence and place only (else
  * which value stays is undefined); reads may share pages.
  *   table int32 [B,per_seq], cache_len int32 [B]: device memory; lengths are
